@@ -2,7 +2,9 @@
  * os_softmax.h -- C ABI of libos_softmax.so: row-wise online-normalizer
  * softmax and fused softmax+TopK on one NVIDIA GB300 GPU (sm_103a), with the
  * attention forward that the same (m, d) recurrence carries onto the tensor
- * cores (os_attention_fwd).
+ * cores (os_attention_fwd) and its gradient (os_attention_bwd), the router
+ * over experts (os_route_topk, os_route_bwd) and the sampler over whole rows
+ * of logits (os_sample).
  *
  * Operations (statement of the problem):
  *   softmax : for each row r of x[rows, cols], y[r, i] = e^(x[r,i] - m_r) / d_r
@@ -68,13 +70,13 @@ typedef enum {
     OS_ERR_NULL = 1,    /* a required pointer is NULL (with rows > 0) */
     OS_ERR_SHAPE = 2,   /* rows < 0, cols outside [1, 2^31 - 1] */
     OS_ERR_DTYPE = 3,   /* dtype value not in os_dtype */
-    OS_ERR_K = 4,       /* K outside [1, min(cols, 256)] */
+    OS_ERR_K = 4,       /* K outside [1, min(cols, 256)] (its range in os_route_topk) */
     OS_ERR_ALIAS = 5,   /* an output overlaps an input or another output */
     OS_ERR_CUDA = 6,    /* the CUDA runtime reported an error (launch or device query) */
     OS_ERR_TIMEOUT = 7, /* a device-side bounded wait gave up (os_device_status) */
     OS_ERR_PATH = 8,    /* the requested kernel family cannot run this shape */
     OS_ERR_ALIGN = 9,   /* a pointer is not aligned to its element size */
-    OS_ERR_VALUE = 10   /* a scalar argument outside its range (attention scale, causal flag) */
+    OS_ERR_VALUE = 10   /* a scalar argument outside its range (scale, flags, sampling settings) */
 } os_status;
 
 /* Kernel families (see os_softmax_fwd_path). */
@@ -232,6 +234,130 @@ os_status os_topk_sample(const float *vals, const int32_t *idx, const float *u, 
 os_status os_attention_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
                            int64_t bh, int64_t n, int32_t head_dim, float scale, int32_t causal,
                            os_stream_t stream);
+
+/*
+ * Gradient of os_attention_fwd.  With P = e^(scale Q K^T - L) over the keys
+ * that a query sees, and delta_i = dO_i . O_i - dL_i:
+ *   dV = P^T dO,  dS = P o (dO V^T - delta),  dQ = scale dS K,  dK = scale dS^T Q.
+ *   q, k, v, o, dout  [bh][n][head_dim] bf16, 16-byte aligned: the forward's
+ *              inputs, its output and the gradient that reaches that output.
+ *   lse        [bh][n] fp32: the forward's logsumexp L.  A row with L = -inf
+ *              has no keys and takes no part.
+ *   dlse       [bh][n] fp32: the gradient that reaches L, or NULL (none).
+ *   dq, dk, dv [bh][n][head_dim] bf16 outputs, 16-byte aligned.
+ *   delta      [bh][n] fp32 workspace, overwritten.
+ *   No output (delta among them) may overlap an input or another output
+ *   (OS_ERR_ALIAS).
+ *   bh, n, head_dim, scale, causal  as os_attention_fwd; bh == 0 or n == 0 is
+ *              a no-op.
+ * Arithmetic: scores and dO V^T in fp32 on the tensor cores from bf16
+ * operands; P and dS in fp32, rounded to bf16 as operands of the last three
+ * products, which accumulate in fp32; results rounded to bf16.  Every sum runs
+ * in a fixed order: the same inputs give the same bits.  q, k, v and dout must
+ * be finite.
+ */
+os_status os_attention_bwd(const void *q, const void *k, const void *v, const void *o,
+                           const float *lse, const void *dout, const float *dlse, void *dq,
+                           void *dk, void *dv, float *delta, int64_t bh, int64_t n,
+                           int32_t head_dim, float scale, int32_t causal, os_stream_t stream);
+
+/*
+ * Routing of tokens to experts: for each row of `experts` logits x the scores
+ *   s = softmax(x)  or  s_e = 1 / (1 + e^-x_e),
+ * the choice value c_e = s_e + bias_e, and the K experts of largest c, best
+ * first, ties to the lower expert.  With groups > 1 the experts are `groups`
+ * runs of equal length, a group's value is the sum of its group_top largest c,
+ * and only experts of the topk_groups groups of largest value take part (ties
+ * to the lower group).
+ *   x        [rows][experts] of in_dtype, read only.
+ *   bias     [experts] fp32, finite, or NULL (none).  It steers the choice
+ *            only; the weights are made of s.
+ *   weights  [rows][K] fp32: scale s_z, or with renorm scale s_z / (sum of the
+ *            K chosen s), of the k-th expert z.
+ *   idx      [rows][K] int32: the experts z.
+ *   experts  1..1024; groups 1..32, a divisor of experts; 1 <= topk_groups <=
+ *            groups; group_top 1 or 2, at most the group's length
+ *            (OS_ERR_SHAPE).
+ *   K        1..32 and at most the topk_groups groups' experts (OS_ERR_K).
+ *   score, renorm (0 or 1), scale (finite)  else OS_ERR_VALUE.
+ * A logit of -inf marks an expert that is not there: its score is 0 and its
+ * choice value -inf, so it is chosen only after every other (and then has
+ * weight 0).  A row of only -inf gets weights 0.  Choices are those of exact
+ * arithmetic: without a bias the logits themselves are compared (s rises with
+ * x); with one, and for sums of two scores, values that fp32 cannot tell apart
+ * are compared in 64 bits.  Outputs may not overlap inputs or each other.
+ */
+typedef enum {
+    OS_SCORE_SOFTMAX = 0,
+    OS_SCORE_SIGMOID = 1
+} os_score;
+
+os_status os_route_topk(const void *x, const float *bias, float *weights, int32_t *idx,
+                        int64_t rows, int64_t experts, int32_t K, int32_t groups,
+                        int32_t topk_groups, int32_t group_top, os_score score, int32_t renorm,
+                        float scale, os_dtype in_dtype, os_stream_t stream);
+
+/*
+ * Gradient of os_route_topk's weights with respect to the logits, the chosen
+ * experts held fixed (neither the choice nor the bias has a gradient):
+ *   x         [rows][experts] of in_dtype: the logits.
+ *   idx       [rows][K] int32: the chosen experts, in any order.  An entry
+ *             outside [0, experts) takes no part; an expert named twice counts
+ *             twice.
+ *   dweights  [rows][K] fp32: the gradient that reaches the weights.
+ *   dx        [rows][experts] of in_dtype, written whole (zero where a logit
+ *             has no gradient); may not overlap the inputs (OS_ERR_ALIAS).
+ *   Other arguments and checks as os_route_topk.
+ */
+os_status os_route_bwd(const void *x, const int32_t *idx, const float *dweights, void *dx,
+                       int64_t rows, int64_t experts, int32_t K, os_score score, int32_t renorm,
+                       float scale, os_dtype in_dtype, os_stream_t stream);
+
+/*
+ * Sampling from rows of logits: for each row one column, drawn with a given
+ * uniform number from softmax(x / temperature) cut down by top-k, top-p and
+ * min-p.  With m the row's maximum and w_c = e^((x_c - m) / temperature), the
+ * columns sorted by (logit descending, column ascending):
+ *   top_k   keeps the first top_k of them;
+ *   top_p   keeps, of those, the shortest prefix whose weight is at least
+ *           top_p times theirs;
+ *   min_p   keeps, of those, the columns with w_c >= min_p.
+ * The best column always stays.  out[r] is the lowest kept column whose
+ * running sum of w over the kept columns, in column order, exceeds u[r] times
+ * their sum; prob[r] is its share of that sum.
+ *   x      [rows][cols] of in_dtype, read only.
+ *   u      [rows] fp32 in [0, 1) (values outside are taken as the nearest
+ *          inside, NaN as 0).
+ *   out    [rows] int32;  prob  [rows] fp32 or NULL.  They may not overlap the
+ *          inputs or each other (OS_ERR_ALIAS).
+ *   s      the settings: per row (device pointers to `rows` values), or where
+ *          the pointer is NULL one value for all rows.  temperature 0: the
+ *          row's lowest best column, with probability 1 and u unused.
+ *          Off: top_k 0, top_p 1, min_p 0.  The values for all rows must be
+ *          finite, temperature >= 0, top_k >= 0, top_p and min_p in [0, 1]
+ *          (OS_ERR_VALUE); per-row values outside are taken as the nearest
+ *          inside, a NaN as 0 (temperature) or as off, and top_k past the
+ *          row's length is off.  Temperatures below 1.5e-30 act as that.
+ * Entries of -inf are never drawn, NaN entries count as -inf, and a row
+ * without any other entry gives column -1 and probability 0.  Cuts and draws
+ * fall where real arithmetic has them, up to 2^-38 relative in the sums: the
+ * weights are summed as integers, so a result depends on the row and the
+ * settings alone.
+ */
+typedef struct {
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+    float temperature_all;
+    int32_t top_k_all;
+    float top_p_all;
+    float min_p_all;
+} os_sampling;
+
+os_status os_sample(const void *x, const float *u, const os_sampling *s, int32_t *out,
+                    float *prob, int64_t rows, int64_t cols, os_dtype in_dtype,
+                    os_stream_t stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *os_status_string(os_status status);

@@ -2,16 +2,17 @@
 
 The C ABI (include/os_softmax.h) is wrapped with ctypes under the same names:
 ``os_softmax_fwd``, ``os_softmax_topk``, ``os_topk``, ``os_softmax_causal_fwd``,
-``os_softmax_stats``, ``os_topk_sample``, ``os_attention_fwd``, ``os_softmax_fwd_path``,
+``os_softmax_stats``, ``os_topk_sample``, ``os_attention_fwd``, ``os_attention_bwd``,
+``os_route_topk``, ``os_route_bwd``, ``os_sample``, ``os_softmax_fwd_path``,
 ``os_softmax_plan``, ``os_topk_plan``, ``os_exp_f32``, ``os_exp_pairs_f32``,
 ``os_exp_pairs_coarse_f32``, ``os_device_status``,
 ``os_set_wait_timeout_ns``, ``os_set_fault_injection``, ``os_status_string``.  They take raw
 device pointers (ints) and a raw stream handle, exactly like the C functions,
 and raise ``OsError`` on a non-OK status.
 
-``softmax``, ``softmax_topk``, ``topk``, ``softmax_causal``, ``softmax_stats`` and
-``attention`` are the
-tensor-level conveniences: they take
+``softmax``, ``softmax_topk``, ``topk``, ``softmax_causal``, ``softmax_stats``,
+``attention``, ``attention_backward``, ``route``, ``route_backward`` and ``sample``
+are the tensor-level conveniences: they take
 torch CUDA tensors, allocate outputs with torch, pass the current torch
 stream, and call the same C entry points.  PyTorch only provides memory and
 streams; every step of the computation runs in the library's CUDA kernels.
@@ -34,6 +35,8 @@ PATHS = {"auto": OS_PATH_AUTO, "warp": OS_PATH_WARP, "onchip": OS_PATH_ONCHIP,
 STATUS = ["OS_OK", "OS_ERR_NULL", "OS_ERR_SHAPE", "OS_ERR_DTYPE", "OS_ERR_K", "OS_ERR_ALIAS",
           "OS_ERR_CUDA", "OS_ERR_TIMEOUT", "OS_ERR_PATH", "OS_ERR_ALIGN", "OS_ERR_VALUE"]
 KMAX = 256
+OS_SCORE_SOFTMAX, OS_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": OS_SCORE_SOFTMAX, "sigmoid": OS_SCORE_SIGMOID}
 
 
 class OsError(RuntimeError):
@@ -55,6 +58,15 @@ class Plan(ctypes.Structure):
         return {f: getattr(self, f) for f, _ in self._fields_}
 
 
+class Sampling(ctypes.Structure):
+    """The settings of os_sample: device pointers to one value per row, or (pointer 0)
+    the value for all rows."""
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p),
+                ("temperature_all", ctypes.c_float), ("top_k_all", ctypes.c_int32),
+                ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -71,6 +83,11 @@ def _load() -> ctypes.CDLL:
     lib.os_softmax_stats.argtypes = [vp, vp, vp, vp, i64, i64, st, vp]
     lib.os_topk_sample.argtypes = [vp, vp, vp, vp, i64, i32, vp]
     lib.os_attention_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, ctypes.c_float, i32, vp]
+    lib.os_attention_bwd.argtypes = [vp] * 11 + [i64, i64, i32, ctypes.c_float, i32, vp]
+    lib.os_route_topk.argtypes = [vp, vp, vp, vp, i64, i64, i32, i32, i32, i32, st, i32,
+                                  ctypes.c_float, st, vp]
+    lib.os_route_bwd.argtypes = [vp, vp, vp, vp, i64, i64, i32, st, i32, ctypes.c_float, st, vp]
+    lib.os_sample.argtypes = [vp, vp, ctypes.POINTER(Sampling), vp, vp, i64, i64, st, vp]
     lib.os_softmax_plan.argtypes = [i64, i64, st, st, st, ctypes.POINTER(Plan)]
     lib.os_topk_plan.argtypes = [i64, i64, i32, ctypes.POINTER(Plan)]
     lib.os_exp_f32.argtypes = [vp, vp, i64, vp]
@@ -83,6 +100,7 @@ def _load() -> ctypes.CDLL:
     lib.os_status_string.restype = ctypes.c_char_p
     for name in ("os_softmax_fwd", "os_softmax_fwd_path", "os_softmax_topk", "os_topk",
                  "os_softmax_causal_fwd", "os_softmax_stats", "os_topk_sample", "os_attention_fwd",
+                 "os_attention_bwd", "os_route_topk", "os_route_bwd", "os_sample",
                  "os_softmax_plan",
                  "os_topk_plan", "os_exp_f32", "os_exp_pairs_f32", "os_exp_pairs_coarse_f32",
                  "os_device_status",
@@ -146,6 +164,33 @@ def os_attention_fwd(q: int, k: int, v: int, o: int, lse: int | None, bh: int, n
                      head_dim: int, scale: float, causal: int, stream: int | None) -> None:
     _check(_lib.os_attention_fwd(q, k, v, o, lse, bh, n, head_dim, scale, causal, stream),
            "os_attention_fwd")
+
+
+def os_attention_bwd(q: int, k: int, v: int, o: int, lse: int, dout: int, dlse: int | None,
+                     dq: int, dk: int, dv: int, delta: int, bh: int, n: int, head_dim: int,
+                     scale: float, causal: int, stream: int | None) -> None:
+    _check(_lib.os_attention_bwd(q, k, v, o, lse, dout, dlse, dq, dk, dv, delta, bh, n, head_dim,
+                                 scale, causal, stream), "os_attention_bwd")
+
+
+def os_route_topk(x: int, bias: int | None, weights: int, idx: int, rows: int, experts: int,
+                  K: int, groups: int, topk_groups: int, group_top: int, score: int, renorm: int,
+                  scale: float, in_dtype: int, stream: int | None) -> None:
+    _check(_lib.os_route_topk(x, bias, weights, idx, rows, experts, K, groups, topk_groups,
+                              group_top, score, renorm, scale, in_dtype, stream), "os_route_topk")
+
+
+def os_route_bwd(x: int, idx: int, dweights: int, dx: int, rows: int, experts: int, K: int,
+                 score: int, renorm: int, scale: float, in_dtype: int,
+                 stream: int | None) -> None:
+    _check(_lib.os_route_bwd(x, idx, dweights, dx, rows, experts, K, score, renorm, scale,
+                             in_dtype, stream), "os_route_bwd")
+
+
+def os_sample(x: int, u: int, settings: Sampling, out: int, prob: int | None, rows: int,
+              cols: int, in_dtype: int, stream: int | None) -> None:
+    _check(_lib.os_sample(x, u, ctypes.byref(settings), out, prob, rows, cols, in_dtype, stream),
+           "os_sample")
 
 
 def os_exp_f32(z: int, out: int, n: int, stream: int | None) -> None:
@@ -349,6 +394,129 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, out=Non
                          lse.data_ptr() if lse is not None else None, bh, n, hd, s, int(causal),
                          _stream_handle(q))
     return out, lse
+
+
+def _like(name, t, shape, dtype, device):
+    """An output or optional input: `t` when it fits, a new tensor when it is None."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                         f"on {device}")
+    return t
+
+
+def attention_backward(q, k, v, out, lse, dout, causal: bool = False, scale: float | None = None,
+                       dlse=None, dq=None, dk=None, dv=None, delta=None):
+    """(dq, dk, dv) bf16 of ``attention``: q, k, v and its results ``out`` and ``lse`` with
+    the gradients that reach them, ``dout`` (bf16, q's shape) and ``dlse`` (fp32, lse's shape,
+    or None).  ``causal`` and ``scale`` as in the forward call.  ``delta`` is an fp32
+    workspace of lse's shape (allocated when not given)."""
+    import torch
+    if not q.is_cuda or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.dim() < 2:
+        raise ValueError("q must be a contiguous bf16 CUDA tensor [..., n, head_dim]")
+    shape, dev, bf16 = q.shape, q.device, torch.bfloat16
+    for name, t in (("k", k), ("v", v), ("out", out), ("dout", dout)):
+        if t is None:
+            raise ValueError(f"{name} is required")
+        _like(name, t, shape, bf16, dev)
+    if lse is None:
+        raise ValueError("lse is required: call attention with want_lse=True")
+    _like("lse", lse, shape[:-1], torch.float32, dev)
+    if dlse is not None:
+        _like("dlse", dlse, shape[:-1], torch.float32, dev)
+    n, hd = shape[-2], shape[-1]
+    bh = q.numel() // max(n * hd, 1)
+    dq = _like("dq", dq, shape, bf16, dev)
+    dk = _like("dk", dk, shape, bf16, dev)
+    dv = _like("dv", dv, shape, bf16, dev)
+    delta = _like("delta", delta, shape[:-1], torch.float32, dev)
+    s = (1.0 / hd ** 0.5) if scale is None else float(scale)
+    with _OnDevice(dev):
+        os_attention_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                         dout.data_ptr(), dlse.data_ptr() if dlse is not None else None,
+                         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), delta.data_ptr(), bh, n, hd,
+                         s, int(causal), _stream_handle(q))
+    return dq, dk, dv
+
+
+def route(x, K: int, score: str | int = "softmax", bias=None, groups: int = 1,
+          topk_groups: int | None = None, group_top: int = 1, renorm: bool = True,
+          scale: float = 1.0, weights=None, idx=None):
+    """Routing of tokens to experts: (weights fp32 [rows, K], experts int32 [rows, K]) of the
+    K experts of largest score (plus ``bias``, fp32 [experts], for the choice only), best first.
+    ``score`` is "softmax" or "sigmoid" of the logits x (fp32 or bf16 [rows, experts]).  With
+    ``groups`` the experts are that many runs of equal length, of which the ``topk_groups`` of
+    largest value (the sum of a group's ``group_top`` largest) take part."""
+    import torch
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous 2-D CUDA tensor")
+    rows, experts = x.shape
+    if bias is not None:
+        _like("bias", bias, (experts,), torch.float32, x.device)
+    weights = _like("weights", weights, (rows, K), torch.float32, x.device)
+    idx = _like("idx", idx, (rows, K), torch.int32, x.device)
+    code = SCORES[score] if isinstance(score, str) else int(score)
+    with _OnDevice(x.device):
+        os_route_topk(x.data_ptr(), bias.data_ptr() if bias is not None else None,
+                      weights.data_ptr(), idx.data_ptr(), rows, experts, K, groups,
+                      groups if topk_groups is None else topk_groups, group_top, code,
+                      int(renorm), scale, _dtype_code(x.dtype), _stream_handle(x))
+    return weights, idx
+
+
+def route_backward(x, idx, dweights, score: str | int = "softmax", renorm: bool = True,
+                   scale: float = 1.0, dx=None):
+    """Gradient of ``route``'s weights with respect to the logits x (x's dtype and shape), for
+    the experts ``idx`` that it chose and the gradient ``dweights`` (fp32 [rows, K]) that
+    reaches the weights; ``score``, ``renorm`` and ``scale`` as in the forward call."""
+    import torch
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous 2-D CUDA tensor")
+    if idx.dim() != 2:
+        raise ValueError("idx must be int32 [rows, K]")
+    rows, experts = x.shape
+    K = idx.shape[1]
+    _like("idx", idx, (rows, K), torch.int32, x.device)
+    _like("dweights", dweights, (rows, K), torch.float32, x.device)
+    dx = _like("dx", dx, x.shape, x.dtype, x.device)
+    code = SCORES[score] if isinstance(score, str) else int(score)
+    with _OnDevice(x.device):
+        os_route_bwd(x.data_ptr(), idx.data_ptr(), dweights.data_ptr(), dx.data_ptr(), rows,
+                     experts, K, code, int(renorm), scale, _dtype_code(x.dtype),
+                     _stream_handle(x))
+    return dx
+
+
+def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, prob=None):
+    """One column per row of the logits x (fp32 or bf16 [rows, cols]), drawn with the uniform
+    numbers u (fp32 [rows], in [0, 1)) from softmax(x / temperature) cut down by top-k, then
+    top-p, then min-p: (columns int32 [rows], their probabilities fp32 [rows]).  Each setting
+    is one number for all rows or a tensor of one value per row (fp32, top_k int32);
+    temperature 0 takes the best column, and 0, 1 and 0 turn top_k, top_p and min_p off."""
+    import torch
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous 2-D CUDA tensor")
+    rows = x.shape[0]
+    settings = Sampling()
+    for name, value, dtype in (("temperature", temperature, torch.float32),
+                               ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32),
+                               ("min_p", min_p, torch.float32)):
+        if isinstance(value, torch.Tensor):
+            setattr(settings, name, _like(name, value, (rows,), dtype, x.device).data_ptr())
+        else:
+            setattr(settings, name + "_all", value)
+    if u is None:
+        raise ValueError("u is required: one uniform number per row")
+    _like("u", u, (rows,), torch.float32, x.device)
+    out = _like("out", out, (rows,), torch.int32, x.device)
+    prob = _like("prob", prob, (rows,), torch.float32, x.device)
+    with _OnDevice(x.device):
+        os_sample(x.data_ptr(), u.data_ptr(), settings, out.data_ptr(), prob.data_ptr(), rows,
+                  x.shape[1], _dtype_code(x.dtype), _stream_handle(x))
+    return out, prob
 
 
 def exp(z, pairs: bool = False, coarse: bool = False):

@@ -295,6 +295,148 @@ os_status os_attention_fwd(const void* q, const void* k, const void* v, void* o,
     return e == cudaSuccess ? OS_OK : OS_ERR_CUDA;
 }
 
+os_status os_attention_bwd(const void* q, const void* k, const void* v, const void* o,
+                           const float* lse, const void* dout, const float* dlse, void* dq,
+                           void* dk, void* dv, float* delta, int64_t bh, int64_t n,
+                           int32_t head_dim, float scale, int32_t causal, os_stream_t stream) {
+    if (bh < 0 || n < 0 || n > INT32_MAX || (head_dim != 64 && head_dim != 128))
+        return OS_ERR_SHAPE;
+    if (!(scale > 0.f) || !(scale < INFINITY) || (causal != 0 && causal != 1)) return OS_ERR_VALUE;
+    if (bh == 0 || n == 0) return OS_OK;
+    const int64_t nt = (n + 127) / 128;
+    if (bh > INT32_MAX / nt || bh > INT64_MAX / 2 / head_dim / n) return OS_ERR_SHAPE;
+    if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !delta) return OS_ERR_NULL;
+    const int64_t tb = bh * n * head_dim * 2, lb = bh * n * 4;
+    const struct {
+        const void* p;
+        int64_t bytes;
+        int align;
+    } in[] = {{q, tb, 16}, {k, tb, 16}, {v, tb, 16}, {o, tb, 16}, {dout, tb, 16}, {lse, lb, 4},
+              {dlse, lb, 4}},
+      out[] = {{dq, tb, 16}, {dk, tb, 16}, {dv, tb, 16}, {delta, lb, 4}};
+    for (const auto& a : in)
+        if (reinterpret_cast<uintptr_t>(a.p) % a.align) return OS_ERR_ALIGN;
+    for (const auto& a : out)
+        if (reinterpret_cast<uintptr_t>(a.p) % a.align) return OS_ERR_ALIGN;
+    for (int i = 0; i < 4; ++i) {
+        for (const auto& a : in)
+            if (a.p && overlaps(out[i].p, out[i].bytes, a.p, a.bytes)) return OS_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return OS_ERR_ALIAS;
+    }
+    os::KernelCtl ctl;
+    if (!make_ctl(&ctl)) return OS_ERR_CUDA;
+    os::AttentionBwdArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.o = o;
+    a.dout = dout;
+    a.lse = lse;
+    a.dlse = dlse;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.delta = delta;
+    a.bh = bh;
+    a.n = static_cast<int>(n);
+    a.scale = scale;
+    a.causal = causal != 0;
+    const cudaError_t e = os::launch_attention_bwd(a, head_dim, ctl,
+                                                   reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? OS_OK : OS_ERR_CUDA;
+}
+
+// Checks that the router and its gradient share.
+static os_status route_checks(int64_t rows, int64_t experts, int32_t K, int64_t most_k,
+                              os_score score, int32_t renorm, float scale, os_dtype in) {
+    if (!valid_dtype(in)) return OS_ERR_DTYPE;
+    if (rows < 0 || experts < 1 || experts > 1024 || rows > INT64_MAX / 8 / experts)
+        return OS_ERR_SHAPE;
+    if (K < 1 || K > 32 || K > most_k) return OS_ERR_K;
+    if ((score != OS_SCORE_SOFTMAX && score != OS_SCORE_SIGMOID) || (renorm != 0 && renorm != 1) ||
+        !(scale > -INFINITY) || !(scale < INFINITY))
+        return OS_ERR_VALUE;
+    return OS_OK;
+}
+
+os_status os_route_topk(const void* x, const float* bias, float* weights, int32_t* idx,
+                        int64_t rows, int64_t experts, int32_t K, int32_t groups,
+                        int32_t topk_groups, int32_t group_top, os_score score, int32_t renorm,
+                        float scale, os_dtype in, os_stream_t stream) {
+    if (experts < 1 || groups < 1 || groups > 32 || experts % groups || topk_groups < 1 ||
+        topk_groups > groups || group_top < 1 || group_top > 2 || group_top > experts / groups)
+        return OS_ERR_SHAPE;
+    const os_status st = route_checks(rows, experts, K, experts / groups * topk_groups, score,
+                                      renorm, scale, in);
+    if (st != OS_OK) return st;
+    if (rows == 0) return OS_OK;
+    if (!x || !weights || !idx) return OS_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(x) % elem_bytes(in) || reinterpret_cast<uintptr_t>(bias) % 4 ||
+        reinterpret_cast<uintptr_t>(weights) % 4 || reinterpret_cast<uintptr_t>(idx) % 4)
+        return OS_ERR_ALIGN;
+    const int64_t xb = rows * experts * elem_bytes(in), kb = rows * int64_t(K) * 4;
+    if (overlaps(weights, kb, x, xb) || overlaps(idx, kb, x, xb) || overlaps(weights, kb, idx, kb) ||
+        (bias && (overlaps(weights, kb, bias, experts * 4) || overlaps(idx, kb, bias, experts * 4))))
+        return OS_ERR_ALIAS;
+    os::RouteArgs a = {x, in, bias, rows, static_cast<int>(experts), K, groups, topk_groups,
+                       group_top, score, renorm != 0, scale};
+    const cudaError_t e = os::launch_route(a, weights, idx, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? OS_OK : OS_ERR_CUDA;
+}
+
+os_status os_route_bwd(const void* x, const int32_t* idx, const float* dweights, void* dx,
+                       int64_t rows, int64_t experts, int32_t K, os_score score, int32_t renorm,
+                       float scale, os_dtype in, os_stream_t stream) {
+    const os_status st = route_checks(rows, experts, K, experts, score, renorm, scale, in);
+    if (st != OS_OK) return st;
+    if (rows == 0) return OS_OK;
+    if (!x || !idx || !dweights || !dx) return OS_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(x) % elem_bytes(in) ||
+        reinterpret_cast<uintptr_t>(dx) % elem_bytes(in) || reinterpret_cast<uintptr_t>(idx) % 4 ||
+        reinterpret_cast<uintptr_t>(dweights) % 4)
+        return OS_ERR_ALIGN;
+    const int64_t xb = rows * experts * elem_bytes(in), kb = rows * int64_t(K) * 4;
+    if (overlaps(dx, xb, x, xb) || overlaps(dx, xb, idx, kb) || overlaps(dx, xb, dweights, kb))
+        return OS_ERR_ALIAS;
+    os::RouteArgs a = {x, in, nullptr, rows, static_cast<int>(experts), K, 1, 1, 1, score,
+                       renorm != 0, scale};
+    const cudaError_t e = os::launch_route_bwd(a, idx, dweights, dx,
+                                               reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? OS_OK : OS_ERR_CUDA;
+}
+
+os_status os_sample(const void* x, const float* u, const os_sampling* s, int32_t* out, float* prob,
+                    int64_t rows, int64_t cols, os_dtype in, os_stream_t stream) {
+    if (!valid_dtype(in)) return OS_ERR_DTYPE;
+    if (!shape_ok(rows, cols)) return OS_ERR_SHAPE;
+    if (!s) return OS_ERR_NULL;
+    if ((!s->temperature && !(s->temperature_all >= 0.f && s->temperature_all < INFINITY)) ||
+        (!s->top_k && s->top_k_all < 0) ||
+        (!s->top_p && !(s->top_p_all >= 0.f && s->top_p_all <= 1.f)) ||
+        (!s->min_p && !(s->min_p_all >= 0.f && s->min_p_all <= 1.f)))
+        return OS_ERR_VALUE;
+    if (rows == 0) return OS_OK;
+    if (!x || !u || !out) return OS_ERR_NULL;
+    const void* words[] = {u, s->temperature, s->top_k, s->top_p, s->min_p};
+    if (reinterpret_cast<uintptr_t>(x) % elem_bytes(in) || reinterpret_cast<uintptr_t>(out) % 4 ||
+        reinterpret_cast<uintptr_t>(prob) % 4)
+        return OS_ERR_ALIGN;
+    for (const void* p : words)
+        if (reinterpret_cast<uintptr_t>(p) % 4) return OS_ERR_ALIGN;
+    const int64_t xb = rows * cols * elem_bytes(in), rb = rows * 4;
+    if (prob && overlaps(out, rb, prob, rb)) return OS_ERR_ALIAS;
+    for (const void* o : {static_cast<const void*>(out), static_cast<const void*>(prob)}) {
+        if (!o) continue;
+        if (overlaps(o, rb, x, xb)) return OS_ERR_ALIAS;
+        for (const void* p : words)
+            if (p && overlaps(o, rb, p, rb)) return OS_ERR_ALIAS;
+    }
+    const cudaError_t e = os::launch_sample(x, in, u, out, prob, rows, static_cast<int>(cols), *s,
+                                            reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? OS_OK : OS_ERR_CUDA;
+}
+
 os_status os_exp_f32(const float* z, float* out, int64_t n, os_stream_t stream) {
     if (n < 0) return OS_ERR_SHAPE;
     if (n == 0) return OS_OK;

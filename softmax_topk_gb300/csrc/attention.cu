@@ -7,50 +7,14 @@
 // zero-filled by the copy engine and never read from the next slice.
 #include <cuda.h>
 
-#include <mutex>
-
 #include "host_common.h"
 #include "internal.h"
 #include "kernels/attention_kernel.cuh"
+#include "tensor_map.h"
 
 namespace os {
 
 namespace {
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder, looked up through the runtime once.
-EncodeTiled encoder() {
-    static EncodeTiled fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiled>(p);
-        else
-            cudaGetLastError();
-    });
-    return fn;
-}
-
-bool make_map(CUtensorMap* map, const void* base, int64_t bh, int n, int d) {
-    EncodeTiled enc = encoder();
-    if (!enc) return false;
-    const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(n), cuuint64_t(bh)};
-    const cuuint64_t strides[2] = {cuuint64_t(d) * 2, cuuint64_t(n) * cuuint64_t(d) * 2};
-    const cuuint32_t box[3] = {64, cuuint32_t(attn::kBN), 1};
-    const cuuint32_t elem[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-               elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
-}
 
 template <int D>
 cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, void* o,
@@ -77,7 +41,8 @@ cudaError_t launch_attention(const void* q, const void* k, const void* v, void* 
                              int64_t bh, int n, int d, float scale, bool causal,
                              const KernelCtl& ctl, cudaStream_t stream) {
     CUtensorMap mq, mk, mv;
-    if (!make_map(&mq, q, bh, n, d) || !make_map(&mk, k, bh, n, d) || !make_map(&mv, v, bh, n, d))
+    if (!make_tile_map(&mq, q, bh, n, d) || !make_tile_map(&mk, k, bh, n, d) ||
+        !make_tile_map(&mv, v, bh, n, d))
         return cudaErrorInvalidValue;
     const float scale_log2 = scale * 1.442695041f;
     if (d == 64) return launch_d<64>(mq, mk, mv, o, lse, bh, n, scale_log2, causal, ctl, stream);

@@ -44,6 +44,40 @@ cudaError_t launch_attention(const void* q, const void* k, const void* v, void* 
                              int64_t bh, int n, int d, float scale, bool causal,
                              const KernelCtl& ctl, cudaStream_t stream);
 
+// gradient of the attention forward; delta is a workspace of bh * n floats,
+// dlse (the gradient that reaches the logsumexp) may be NULL
+struct AttentionBwdArgs {
+    const void *q, *k, *v, *o, *dout;
+    const float *lse, *dlse;
+    void *dq, *dk, *dv;
+    float* delta;
+    int64_t bh;
+    int n;
+    float scale;
+    bool causal;
+};
+cudaError_t launch_attention_bwd(const AttentionBwdArgs& a, int d, const KernelCtl& ctl,
+                                 cudaStream_t stream);
+
+// router over experts (see os_route_topk, os_route_bwd)
+struct RouteArgs {
+    const void* x;
+    os_dtype in;
+    const float* bias;  // or NULL
+    int64_t rows;
+    int experts, K, groups, topk_groups, group_top;
+    os_score score;
+    bool renorm;
+    float scale;
+};
+cudaError_t launch_route(const RouteArgs& a, float* weights, int32_t* idx, cudaStream_t stream);
+cudaError_t launch_route_bwd(const RouteArgs& a, const int32_t* idx, const float* dweights,
+                             void* dx, cudaStream_t stream);
+
+// one column per row under the sampling settings (see os_sample)
+cudaError_t launch_sample(const void* x, os_dtype in, const float* u, int32_t* out, float* prob,
+                          int64_t rows, int cols, const os_sampling& s, cudaStream_t stream);
+
 // (m, d, lse) of every row; any output may be NULL
 cudaError_t launch_stats(const void* x, os_dtype in, float* m, float* d, float* lse, int64_t rows,
                          int cols, bool aligned, cudaStream_t stream);

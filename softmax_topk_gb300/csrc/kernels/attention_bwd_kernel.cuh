@@ -1,0 +1,500 @@
+// attention_bwd_kernel.cuh -- gradient of the attention forward on the
+// fifth-generation tensor cores.
+//
+// With S = scale Q K^T, P = e^(S - L) (L the forward's logsumexp, so P is the
+// softmax itself, recomputed instead of stored), and the row constants
+// delta_i = dO_i . O_i - dL_i:
+//   dV = P^T dO,   dP = dO V^T,   dS = P o (dP - delta),
+//   dQ = scale dS K,   dK = scale dS^T Q.
+// Two kernels, one per side that a sum runs over, so that every output row is
+// summed by one CTA in a fixed order (no atomics, results do not depend on
+// scheduling):
+//   KV = true:  one item is a tile of 128 keys; it keeps K and V of those rows
+//               and streams the tiles of (Q, dO), accumulating dK and dV;
+//   KV = false: one item is a tile of 128 queries; it keeps Q and dO and
+//               streams the tiles of (K, V), accumulating dQ.
+// Both are the same program on swapped operands: with (X, Y) the resident pair
+// and (U, W) the streamed one, per tile
+//   A1 = X U^T  (S or its transpose),  A2 = Y W^T  (dP or its transpose),
+//   P and dS from A1 and A2 element by element,
+//   acc1 += dS U  (dK or dQ),  acc2 += P W  (dV, KV only).
+// The price of the split is that S and dP are formed twice: seven products
+// instead of five.
+//
+// GB300 mapping (persistent CTAs, one per SM, warp-specialised):
+//   * load warp: TMA tiled loads of the resident pair once per item and of the
+//     streamed pairs through a ring of stages;
+//   * MMA warp (one lane): the products, accumulators in tensor memory.  A
+//     product that overwrites what an earlier one reads (A1 lies over P, A2
+//     over dS) is issued after that one's completion was seen;
+//   * stat warp (KV only): the streamed rows' (L log2e, delta) into shared
+//     memory, L = +inf for rows past the end so that their P is 0;
+//   * eight compute warps: thread (r, h) owns tile row r (one tensor-memory
+//     lane) and half h of its columns: P = 2^(A1 scale log2e - L log2e) to
+//     bf16 for the dV product, dS = P (A2 - delta) to bf16 for the dK / dQ
+//     product (both read from tensor memory as the A operand), fp32 in between.
+//     The two roundings to bf16 are the price of the bf16 tensor cores, as P's
+//     is in the forward; sums are fp32.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "../ctl.h"
+#include "attention_kernel.cuh"
+#include "ops.cuh"
+#include "umma.cuh"
+
+namespace os {
+namespace attn_bwd {
+
+constexpr int kRows = 128;          // rows of a tile, resident or streamed
+constexpr int kComputeWarps = 8;
+constexpr int kCompute = kComputeWarps * 32;
+constexpr int kLoadWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kStatWarp = 10;
+constexpr int kThreads = 352;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kA1 = 0;         // A1 (fp32, 128 columns); P in its columns 0-31 and 64-95
+constexpr uint32_t kA2 = 128;       // A2 (fp32, 128 columns); dS likewise
+constexpr uint32_t kAcc1 = 256;     // dK or dQ, D columns
+constexpr uint32_t kAcc2 = 384;     // dV, D columns
+constexpr float kLog2e = 1.442695041f;
+
+template <int D>
+struct Layout {
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kBlock = kRows * 64 * 2;  // 16 KB: 128 rows of 64 bf16
+    static constexpr int kTile = kRows * D * 2;
+    static constexpr int kX = 0;
+    static constexpr int kY = kX + kTile;
+    static constexpr int kU = kY + kTile;               // kStages buffers
+    static constexpr int kW = kU + kStages * kTile;     // kStages buffers
+    static constexpr int kStat = kW + kStages * kTile;  // 2 x (128 L log2e, 128 delta)
+    static constexpr int kBytes = kStat + 2 * 2 * kRows * 4;
+    static constexpr int kDynBytes = kBytes + 1024;
+};
+
+template <int STAGES>
+struct Barriers {
+    uint64_t x_full, x_empty;                      // resident pair landed / its products done
+    uint64_t u_full[STAGES], w_full[STAGES];       // streamed tile landed
+    uint64_t uw_empty[STAGES];                     // every product reading the stage done
+    uint64_t a1_full, a2_full;                     // A1 / A2 of a tile in tensor memory
+    uint64_t p_full, ds_full;                      // P / dS in tensor memory (all compute threads)
+    uint64_t pw_done, acc_done;                    // acc2 += P W / acc1 += dS U completed
+    uint64_t acc_empty;                            // an item's sums are in registers
+    uint64_t stat_full[2], stat_empty[2];          // the streamed rows' statistics there / read
+    uint64_t drain;
+    uint32_t tmem;
+};
+
+// Bounded waits of one role: once one gave up, the rest return at once, so a
+// kernel whose data never comes ends after one timeout per role.
+struct Waiter {
+    const KernelCtl& ctl;
+    bool ok;
+    __device__ __forceinline__ explicit Waiter(const KernelCtl& c) : ctl(c), ok(true) {}
+    __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+        if (ok) ok = umma::mbar_wait(bar, parity, ctl);
+    }
+};
+
+// Tiles that item `tile` walks: all of them, or under the mask the queries at
+// or after a key tile (KV) and the keys at or before a query tile.
+template <bool KV>
+__device__ __forceinline__ void tile_range(int tile, int nt, bool causal, int& first, int& count) {
+    first = KV && causal ? tile : 0;
+    count = !causal ? nt : (KV ? nt - tile : tile + 1);
+}
+
+// delta[i] = dO_i . O_i - dL_i, one group of D / 8 lanes per row, 16 bytes a lane.
+template <int D>
+__global__ void __launch_bounds__(256)
+delta_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
+             const float* __restrict__ dlse, float* __restrict__ delta, int64_t rows) {
+    constexpr int G = D / 8;
+    const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / G;
+    const int part = threadIdx.x % G;
+    float s = 0.f;
+    if (row < rows) {
+        const uint4 a = *reinterpret_cast<const uint4*>(o + row * D + part * 8);
+        const uint4 b = *reinterpret_cast<const uint4*>(dout + row * D + part * 8);
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = unpack_bf16x2(aw[i]), y = unpack_bf16x2(bw[i]);
+            s = fmaf(x.x, y.x, s);
+            s = fmaf(x.y, y.y, s);
+        }
+    }
+#pragma unroll
+    for (int k = G / 2; k > 0; k >>= 1) s += __shfl_xor_sync(kFullMask, s, k);
+    if (row < rows && part == 0) delta[row] = s - (dlse ? dlse[row] : 0.f);
+}
+
+template <int D, bool KV>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
+                     const __grid_constant__ CUtensorMap map_y,
+                     const __grid_constant__ CUtensorMap map_u,
+                     const __grid_constant__ CUtensorMap map_w, const float* __restrict__ lse,
+                     const float* __restrict__ delta, __nv_bfloat16* __restrict__ out1,
+                     __nv_bfloat16* __restrict__ out2, int n, int nt, int units, float scale,
+                     int causal_flag, KernelCtl ctl) {
+    using L = Layout<D>;
+    constexpr int STAGES = L::kStages;
+    extern __shared__ unsigned char dyn_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ Barriers<STAGES> bars;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool causal = causal_flag != 0;
+
+    if (tid == 0) {
+        mbar_init(&bars.x_full, 1);
+        mbar_init(&bars.x_empty, 1);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&bars.u_full[s], 1);
+            mbar_init(&bars.w_full[s], 1);
+            mbar_init(&bars.uw_empty[s], 1);
+        }
+        mbar_init(&bars.a1_full, 1);
+        mbar_init(&bars.a2_full, 1);
+        mbar_init(&bars.p_full, kCompute);
+        mbar_init(&bars.ds_full, kCompute);
+        mbar_init(&bars.pw_done, 1);
+        mbar_init(&bars.acc_done, 1);
+        mbar_init(&bars.acc_empty, kCompute);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars.stat_full[s], 32);
+            mbar_init(&bars.stat_empty[s], kComputeWarps);
+        }
+        mbar_init(&bars.drain, 1);
+        mbar_init_fence();
+    }
+    if (warp == 0) umma::tmem_alloc(&bars.tmem, kTmemCols);
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = bars.tmem;
+
+    // Every role walks the same items in the same order (work units as in the
+    // forward: single tiles, or balanced pairs under the mask); g counts the
+    // streamed tiles and it the items across the whole walk, and give the
+    // barriers' phases.
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            umma::prefetch_tensormap(&map_x);
+            umma::prefetch_tensormap(&map_y);
+            umma::prefetch_tensormap(&map_u);
+            umma::prefetch_tensormap(&map_w);
+            Waiter wait(ctl);
+            int g = 0, it = 0;
+            for (int u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
+                int bh, ta, tb;
+                const int cnt = attn::work_unit(u, nt, causal, bh, ta, tb);
+                for (int e = 0; e < cnt && wait.ok; ++e) {
+                    const int tile = e == 0 ? ta : tb;
+                    int first, count;
+                    tile_range<KV>(tile, nt, causal, first, count);
+                    if (it > 0) wait(&bars.x_empty, (it - 1) & 1);
+                    if (!wait.ok) break;
+                    mbar_arrive_expect_tx(&bars.x_full, 2 * L::kTile);
+                    ++it;
+#pragma unroll
+                    for (int blk = 0; blk < D / 64; ++blk) {
+                        umma::tma_load_3d(smem + L::kX + blk * L::kBlock, &map_x, 64 * blk,
+                                          tile * kRows, bh, &bars.x_full);
+                        umma::tma_load_3d(smem + L::kY + blk * L::kBlock, &map_y, 64 * blk,
+                                          tile * kRows, bh, &bars.x_full);
+                    }
+                    for (int j = 0; j < count; ++j) {
+                        const int st = g % STAGES;
+                        if (g >= STAGES) wait(&bars.uw_empty[st], (g / STAGES - 1) & 1);
+                        if (!wait.ok) break;
+                        ++g;
+                        mbar_arrive_expect_tx(&bars.u_full[st], L::kTile);
+#pragma unroll
+                        for (int blk = 0; blk < D / 64; ++blk)
+                            umma::tma_load_3d(smem + L::kU + st * L::kTile + blk * L::kBlock,
+                                              &map_u, 64 * blk, (first + j) * kRows, bh,
+                                              &bars.u_full[st]);
+                        mbar_arrive_expect_tx(&bars.w_full[st], L::kTile);
+#pragma unroll
+                        for (int blk = 0; blk < D / 64; ++blk)
+                            umma::tma_load_3d(smem + L::kW + st * L::kTile + blk * L::kBlock,
+                                              &map_w, 64 * blk, (first + j) * kRows, bh,
+                                              &bars.w_full[st]);
+                    }
+                }
+            }
+            // no copy may land after this CTA has gone
+            if (it > 0)
+                mbar_wait_bounded_ns(&bars.x_full, (it - 1) & 1, kDrainTimeoutNs, ctl.err);
+            for (int k = g > STAGES ? g - STAGES : 0; k < g; ++k) {
+                mbar_wait_bounded_ns(&bars.u_full[k % STAGES], (k / STAGES) & 1, kDrainTimeoutNs,
+                                     ctl.err);
+                mbar_wait_bounded_ns(&bars.w_full[k % STAGES], (k / STAGES) & 1, kDrainTimeoutNs,
+                                     ctl.err);
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            constexpr uint32_t id_a = umma::idesc_bf16(kRows, kRows, false);
+            constexpr uint32_t id_acc = umma::idesc_bf16(kRows, D, true);
+            const uint32_t x_addr = smem_addr(smem + L::kX), y_addr = smem_addr(smem + L::kY);
+            Waiter wait(ctl);
+            // A (128 x 128 fp32) = resident tile times streamed tile transposed
+            auto product = [&](uint32_t dst, uint32_t a_addr, uint32_t b_addr) {
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t koff = (s >> 2) * L::kBlock + (s & 3) * 32;
+                    umma::mma_bf16(tmem + dst, umma::desc_sw128(a_addr + koff, 16, 1024),
+                                   umma::desc_sw128(b_addr + koff, 16, 1024), id_a, s > 0);
+                }
+            };
+            // acc (128 x D) += P or dS (tensor memory, columns 0-63 of the
+            // tile at `src`, 64-127 at src + 64) times a streamed tile
+            auto accumulate = [&](uint32_t dst, uint32_t src, uint32_t b_addr, bool keep) {
+#pragma unroll
+                for (int s = 0; s < kRows / 16; ++s)
+                    umma::mma_bf16_tmem_a(tmem + dst, tmem + src + (s < 4 ? 8 * s : 32 + 8 * s),
+                                          umma::desc_sw128(b_addr + s * 2048, L::kBlock, 1024),
+                                          id_acc, keep || s > 0);
+            };
+            auto issue_a1 = [&](int g) {
+                const int st = g % STAGES;
+                wait(&bars.u_full[st], (g / STAGES) & 1);
+                // A1 lies over P of tile g - 1: its product must have read it
+                if (KV && g > 0) wait(&bars.pw_done, (g - 1) & 1);
+                if (!wait.ok) return;
+                umma::fence_after_sync();
+                product(kA1, x_addr, smem_addr(smem + L::kU + st * L::kTile));
+                umma::commit(&bars.a1_full);
+            };
+            auto issue_a2 = [&](int g) {
+                const int st = g % STAGES;
+                wait(&bars.w_full[st], (g / STAGES) & 1);
+                // A2 lies over dS of tile g - 1
+                if (g > 0) wait(&bars.acc_done, (g - 1) & 1);
+                if (!wait.ok) return;
+                umma::fence_after_sync();
+                product(kA2, y_addr, smem_addr(smem + L::kW + st * L::kTile));
+                umma::commit(&bars.a2_full);
+            };
+            int g = 0, it = 0;
+            for (int u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
+                int bh, ta, tb;
+                const int cnt = attn::work_unit(u, nt, causal, bh, ta, tb);
+                for (int e = 0; e < cnt && wait.ok; ++e, ++it) {
+                    int first, count;
+                    tile_range<KV>(e == 0 ? ta : tb, nt, causal, first, count);
+                    wait(&bars.x_full, it & 1);
+                    issue_a1(g);
+                    issue_a2(g);
+                    for (int j = 0; j < count && wait.ok; ++j, ++g) {
+                        const int st = g % STAGES;
+                        wait(&bars.p_full, g & 1);
+                        // the first products of an item overwrite the sums
+                        if (j == 0 && it > 0) wait(&bars.acc_empty, (it - 1) & 1);
+                        if (!wait.ok) break;
+                        if (KV) {
+                            umma::fence_after_sync();
+                            accumulate(kAcc2, kA1, smem_addr(smem + L::kW + st * L::kTile), j > 0);
+                            umma::commit(&bars.pw_done);
+                        }
+                        if (j + 1 < count) issue_a1(g + 1);
+                        wait(&bars.ds_full, g & 1);
+                        if (!wait.ok) break;
+                        umma::fence_after_sync();
+                        accumulate(kAcc1, kA2, smem_addr(smem + L::kU + st * L::kTile), j > 0);
+                        umma::commit(&bars.acc_done);
+                        umma::commit(&bars.uw_empty[st]);
+                        if (j + 1 < count) issue_a2(g + 1);
+                    }
+                    if (wait.ok) umma::commit(&bars.x_empty);
+                }
+            }
+            // no product may be in flight when tensor memory is given back
+            umma::commit(&bars.drain);
+            mbar_wait_bounded_ns(&bars.drain, 0, kDrainTimeoutNs, ctl.err);
+        }
+    } else if (warp == kStatWarp) {
+        if (KV) {
+            Waiter wait(ctl);
+            int g = 0;
+            for (int u = blockIdx.x; u < units; u += gridDim.x) {
+                int bh, ta, tb;
+                const int cnt = attn::work_unit(u, nt, causal, bh, ta, tb);
+                for (int e = 0; e < cnt; ++e) {
+                    int first, count;
+                    tile_range<KV>(e == 0 ? ta : tb, nt, causal, first, count);
+                    const float* lrow = lse + int64_t(bh) * n;
+                    const float* drow = delta + int64_t(bh) * n;
+                    for (int j = 0; j < count; ++j, ++g) {
+                        const int base = (first + j) * kRows;
+                        float lv[4], dv[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int q = base + lane + 32 * i;
+                            lv[i] = q < n ? lrow[q] * kLog2e : INFINITY;
+                            dv[i] = q < n ? drow[q] : 0.f;
+                            if (lv[i] == -INFINITY) lv[i] = INFINITY;
+                        }
+                        // buffer g & 1 was last read for tile g - 2
+                        if (g >= 2) wait(&bars.stat_empty[g & 1], ((g - 2) >> 1) & 1);
+                        float* stat = reinterpret_cast<float*>(smem + L::kStat) + (g & 1) * 2 * kRows;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            stat[lane + 32 * i] = lv[i];
+                            stat[kRows + lane + 32 * i] = dv[i];
+                        }
+                        umma::mbar_arrive(&bars.stat_full[g & 1]);
+                    }
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- compute
+        const int r = tid & 127, half = tid >> 7;  // tile row, column half
+        const uint32_t lane_addr = tmem + (uint32_t((warp & 3) * 32) << 16);
+        const uint32_t a1 = lane_addr + kA1 + 64 * half, a2 = lane_addr + kA2 + 64 * half;
+        const float scale_log2 = scale * kLog2e;
+        Waiter wait(ctl);
+        int g = 0;
+        for (int u = blockIdx.x; u < units; u += gridDim.x) {
+            int bh, ta, tb;
+            const int cnt = attn::work_unit(u, nt, causal, bh, ta, tb);
+            for (int e = 0; e < cnt; ++e) {
+                const int tile = e == 0 ? ta : tb;
+                int first, count;
+                tile_range<KV>(tile, nt, causal, first, count);
+                const int row = tile * kRows + r;
+                float row_l = INFINITY, row_delta = 0.f;
+                if (!KV && row < n) {
+                    row_l = lse[int64_t(bh) * n + row] * kLog2e;
+                    if (row_l == -INFINITY) row_l = INFINITY;
+                    row_delta = delta[int64_t(bh) * n + row];
+                }
+                for (int j = 0; j < count; ++j, ++g) {
+                    const int col0 = (first + j) * kRows + 64 * half;
+                    const float* stat =
+                        reinterpret_cast<const float*>(smem + L::kStat) + (g & 1) * 2 * kRows + 64 * half;
+                    float p[64];
+                    uint32_t pk[32];
+                    wait(&bars.a1_full, g & 1);
+                    umma::fence_after_sync();
+                    umma::tmem_ld32(a1, p);
+                    umma::tmem_ld32(a1 + 32, p + 32);
+                    if (KV) wait(&bars.stat_full[g & 1], (g >> 1) & 1);
+                    umma::tmem_wait_ld();
+                    // columns [lo, hi) of this half take part: keys up to the
+                    // end and the query (KV = false), queries from the key on
+                    // (KV = true; queries past the end have L = +inf)
+                    int lo = 0, hi = 64;
+                    if (KV) {
+                        if (causal) lo = row - col0;
+                    } else {
+                        hi = n - col0;
+                        if (causal) hi = min(hi, row - col0 + 1);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 64; c += 4) {
+                        float4 l4;
+                        if (KV) l4 = *reinterpret_cast<const float4*>(stat + c);
+                        else l4 = make_float4(row_l, row_l, row_l, row_l);
+                        p[c] = ex2_sfu(fmaf(p[c], scale_log2, -l4.x));
+                        p[c + 1] = ex2_sfu(fmaf(p[c + 1], scale_log2, -l4.y));
+                        p[c + 2] = ex2_sfu(fmaf(p[c + 2], scale_log2, -l4.z));
+                        p[c + 3] = ex2_sfu(fmaf(p[c + 3], scale_log2, -l4.w));
+                    }
+                    if (lo > 0 || hi < 64) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (c < lo || c >= hi) p[c] = 0.f;
+                    }
+                    if (KV) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+                        umma::tmem_st32(a1, reinterpret_cast<const float*>(pk));
+                        umma::tmem_wait_st();
+                    }
+                    umma::fence_before_sync();
+                    umma::mbar_arrive(&bars.p_full);
+
+                    float dp[64];
+                    wait(&bars.a2_full, g & 1);
+                    umma::fence_after_sync();
+                    umma::tmem_ld32(a2, dp);
+                    umma::tmem_ld32(a2 + 32, dp + 32);
+                    umma::tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 64; c += 4) {
+                        float4 d4;
+                        if (KV) d4 = *reinterpret_cast<const float4*>(stat + kRows + c);
+                        else d4 = make_float4(row_delta, row_delta, row_delta, row_delta);
+                        pk[c / 2] = pack_bf16x2(p[c] * (dp[c] - d4.x), p[c + 1] * (dp[c + 1] - d4.y));
+                        pk[c / 2 + 1] =
+                            pack_bf16x2(p[c + 2] * (dp[c + 2] - d4.z), p[c + 3] * (dp[c + 3] - d4.w));
+                    }
+                    umma::tmem_st32(a2, reinterpret_cast<const float*>(pk));
+                    umma::tmem_wait_st();
+                    umma::fence_before_sync();
+                    umma::mbar_arrive(&bars.ds_full);
+                    if (KV) {
+                        __syncwarp();
+                        if (lane == 0) umma::mbar_arrive(&bars.stat_empty[g & 1]);
+                    }
+                }
+                // the item's sums: acc1 is complete after its last product, and
+                // acc2's last product was seen before that one was issued
+                wait(&bars.acc_done, (g - 1) & 1);
+                umma::fence_after_sync();
+                constexpr int H = D / 2;  // columns per thread
+                float o1[H], o2[KV ? H : 1];
+#pragma unroll
+                for (int c = 0; c < H / 32; ++c) {
+                    umma::tmem_ld32(lane_addr + kAcc1 + half * H + 32 * c, o1 + 32 * c);
+                    if constexpr (KV)
+                        umma::tmem_ld32(lane_addr + kAcc2 + half * H + 32 * c, o2 + 32 * c);
+                }
+                umma::tmem_wait_ld();
+                umma::fence_before_sync();
+                umma::mbar_arrive(&bars.acc_empty);
+                if (row < n && wait.ok) {
+                    const int64_t at = (int64_t(bh) * n + row) * D + half * H;
+#pragma unroll
+                    for (int v = 0; v < H / 8; ++v) {
+                        uint4 w;
+                        w.x = pack_bf16x2(o1[8 * v + 0] * scale, o1[8 * v + 1] * scale);
+                        w.y = pack_bf16x2(o1[8 * v + 2] * scale, o1[8 * v + 3] * scale);
+                        w.z = pack_bf16x2(o1[8 * v + 4] * scale, o1[8 * v + 5] * scale);
+                        w.w = pack_bf16x2(o1[8 * v + 6] * scale, o1[8 * v + 7] * scale);
+                        *reinterpret_cast<uint4*>(out1 + at + 8 * v) = w;
+                        if constexpr (KV) {
+                            w.x = pack_bf16x2(o2[8 * v + 0], o2[8 * v + 1]);
+                            w.y = pack_bf16x2(o2[8 * v + 2], o2[8 * v + 3]);
+                            w.z = pack_bf16x2(o2[8 * v + 4], o2[8 * v + 5]);
+                            w.w = pack_bf16x2(o2[8 * v + 6], o2[8 * v + 7]);
+                            *reinterpret_cast<uint4*>(out2 + at + 8 * v) = w;
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    umma::fence_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        umma::fence_after_sync();
+        umma::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+}  // namespace attn_bwd
+}  // namespace os

@@ -1,0 +1,499 @@
+// route_kernel.cuh -- routing of tokens to experts and its gradient, one warp
+// per token.
+//
+// A row of E logits x gives scores s = softmax(x) or s_e = 1 / (1 + e^-x_e).
+// The choice is made on c_e = s_e + bias_e (bias only steers the choice): with
+// groups, the E experts are `groups` runs of equal length, a group is worth the
+// sum of its `group_top` largest c, and only experts of the topk_groups best
+// groups take part; then the K largest c, ties to the lower expert.  The
+// weights are s of the chosen experts, divided by their sum when renormalised,
+// times a scale.
+//
+// What bounds it: E logits are read and K pairs written per token, a few
+// instructions per logit, so memory for large batches and one launch for small
+// ones.  A token's row lives in the registers of one warp: lane l holds a run
+// of consecutive experts, runs in lane order inside a group and groups in lane
+// order, so the lowest expert among ties is the lowest lane's lowest element
+// and a maximum over the warp is one redux instruction.
+//
+// Exact choices.  Without a bias s rises with x, so logits are compared and
+// the choice is exact.  With a bias (and for sums of two scores) c is computed
+// in fp32 and the choice could turn on its rounding.  Its error is bounded:
+// s carries at most (|x - m| + 12) 2^-24 relative, which is at most
+// 2^-20 s_max absolute (|z| e^-|z| is small where s is), and the sum one
+// rounding.  A token in which two compared values lie closer than the bounds
+// allow (about 1 in 500 for 256 experts and 8 choices), and are not of equal
+// logit and bias, is chosen again with s and c in 64 bits.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "ops.cuh"
+
+namespace os {
+namespace route {
+
+constexpr int kWarps = 4;      // tokens per CTA at a time
+constexpr int kMaxK = 32;      // one lane per chosen expert
+constexpr int kMaxExperts = 1024;
+
+struct Shape {
+    int experts, K, groups, topk_groups, group_top;
+    int lanes;     // lanes per group (a power of two)
+    int per_lane;  // experts per lane
+    int sigmoid, renorm;
+    float scale;
+};
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Order-preserving 32-bit key of a float (-0 must be +0); 0 is below every key.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kFullMask, v); }
+__device__ __forceinline__ uint32_t warp_min(uint32_t v) { return __reduce_min_sync(kFullMask, v); }
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float sigmoid(float x) {
+    const float e = exp1(-fabsf(x));
+    return __fdiv_rn(x < 0.f ? e : 1.f, 1.f + e);
+}
+
+// This lane's run of a row: N consecutive values from p, `count` of them real
+// (the rest -inf).  VEC: count is N or (a lane without experts) 0, and p
+// aligned to min(16, N * sizeof(T)).
+template <typename T, int N, bool VEC>
+__device__ __forceinline__ void load_run(const T* p, int count, float (&v)[N]) {
+    if constexpr (VEC) {
+        if (count == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = -INFINITY;
+            return;
+        }
+        constexpr int bytes = N * int(sizeof(T));
+        uint32_t w[(bytes + 3) / 4];
+        if constexpr (bytes >= 16) {
+#pragma unroll
+            for (int i = 0; i < bytes / 16; ++i)
+                *reinterpret_cast<uint4*>(w + 4 * i) = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+        } else if constexpr (bytes == 8) {
+            *reinterpret_cast<uint2*>(w) = __ldcs(reinterpret_cast<const uint2*>(p));
+        } else if constexpr (bytes == 4) {
+            w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
+        } else {
+            w[0] = *reinterpret_cast<const uint16_t*>(p);
+        }
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float2 f = unpack_bf16x2(w[i / 2]);
+                v[i] = f.x;
+                if (i + 1 < N) v[i + 1] = f.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = i < count ? widen(p[i]) : -INFINITY;
+    }
+}
+
+// The choice of one token with s and c in 64 bits (bias given or sums of two
+// scores): rare, so written for size.  Every lane returns the expert of slot
+// `lane` (lane < K).  xrow is the token's row, lanes hold its logits as in
+// the caller.
+template <typename T>
+__device__ __noinline__ int choose_wide(const T* xrow, const float* bias, const Shape sh, float mf) {
+    const int lane = threadIdx.x & 31, E = sh.experts, gsize = E / sh.groups;
+    const double m = mf;
+    double d = 1.0;
+    if (!sh.sigmoid) {
+        d = 0.0;
+        for (int e = lane; e < E; e += 32) {
+            const float x = widen(xrow[e]);
+            if (x > -INFINITY) d += exp(double(x) - m);
+        }
+        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFullMask, d, o);
+    }
+    auto choice = [&](int e) -> double {
+        const float x = widen(xrow[e]);
+        if (!(x > -INFINITY)) return -INFINITY;
+        const double s = sh.sigmoid ? 1.0 / (1.0 + exp(-double(x))) : exp(double(x) - m) / d;
+        return bias ? s + double(bias[e]) : s;
+    };
+    // groups: lane g holds group g's value; bit g of `kept` is set when it takes part
+    uint32_t kept = 0xffffffffu;
+    if (sh.groups > 1) {
+        double score = -INFINITY;
+        if (lane < sh.groups) {
+            double a = -INFINITY, b = -INFINITY;
+            for (int i = 0; i < gsize; ++i) {
+                const double c = choice(lane * gsize + i);
+                if (c > a) {
+                    b = a;
+                    a = c;
+                } else if (c > b) {
+                    b = c;
+                }
+            }
+            score = sh.group_top == 2 ? a + b : a;
+        }
+        int rank = 0;
+        for (int g = 0; g < sh.groups; ++g) {
+            const double o = __shfl_sync(kFullMask, score, g);
+            rank += o > score || (o == score && g < lane);
+        }
+        kept = __ballot_sync(kFullMask, lane < sh.groups && rank < sh.topk_groups);
+    }
+    // slot by slot: the best expert after the previous slot's in (c, expert) order
+    int mine = 0, last = -1;
+    double bound = INFINITY;
+    for (int k = 0; k < sh.K; ++k) {
+        double best = -INFINITY;
+        int at = kMaxExperts;
+        for (int e = lane; e < E; e += 32) {
+            if (!(kept >> (e / gsize) & 1)) continue;
+            const double c = bias ? choice(e) : double(widen(xrow[e]));  // s rises with x
+            const bool after = last < 0 || c < bound || (c == bound && e > last);
+            if (after && (at == kMaxExperts || c > best)) {
+                best = c;
+                at = e;
+            }
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            const double ob = __shfl_xor_sync(kFullMask, best, o);
+            const int oa = __shfl_xor_sync(kFullMask, at, o);
+            if (oa < kMaxExperts && (at == kMaxExperts || ob > best || (ob == best && oa < at))) {
+                best = ob;
+                at = oa;
+            }
+        }
+        last = at;
+        bound = best;
+        if (lane == k) mine = min(at, E - 1);  // in range whatever the inputs (NaN)
+    }
+    return mine;
+}
+
+// N: experts per lane, rounded up to a power of two.
+template <typename T, int N, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32)
+route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __restrict__ weights,
+             int* __restrict__ idx, int64_t rows, const Shape sh) {
+    const int lane = threadIdx.x & 31;
+    const int E = sh.experts, gsize = E / sh.groups;
+    const int group = lane / sh.lanes;
+    const int first = (lane % sh.lanes) * sh.per_lane;  // within the group
+    const int base = group * gsize + first;
+    const int count = group < sh.groups ? max(0, min(sh.per_lane, gsize - first)) : 0;
+    const bool by_score = bias != nullptr;  // else logits give the order
+    // the softmax's maximum and sum are needed for its scores themselves
+    const bool pair_sum = sh.groups > 1 && sh.group_top == 2;
+    const bool need_sum = !sh.sigmoid && (by_score || pair_sum || !sh.renorm);
+
+    for (int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < rows;
+         row += int64_t(gridDim.x) * kWarps) {
+        const T* xrow = x + row * E;
+        float v[N];
+        load_run<T, N, VEC>(xrow + base, count, v);
+        float m = 0.f, inv_d = 1.f;
+        if (!sh.sigmoid) {
+            m = v[0];
+#pragma unroll
+            for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+            m = key_value(warp_max(order_key(m + 0.f)));
+            if (need_sum) {
+                const float ref = m == -INFINITY ? 0.f : m;
+                float d = 0.f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) d += v[i] == -INFINITY ? 0.f : exp1(v[i] - ref);
+                d = warp_sum(d);
+                inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
+            }
+        }
+        auto score = [&](float xv) {
+            if (xv == -INFINITY) return 0.f;
+            return sh.sigmoid ? sigmoid(xv) : exp1(xv - m) * inv_d;
+        };
+        const float s_max = sh.sigmoid ? 1.f : inv_d;
+        const float err = s_max * 0x1p-19f;  // twice the bound of a score
+
+        // ---- the value that is compared, as an order key; 0 = takes no part
+        uint32_t key[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float c = v[i];
+            if (by_score && v[i] != -INFINITY) c = score(v[i]) + bias[i < count ? base + i : 0];
+            key[i] = i < count ? order_key(c + 0.f) : 0u;
+        }
+        bool wide = false;
+        if (sh.groups > 1) {
+            float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (i < count) {
+                    float c = key_value(key[i]);
+                    if (pair_sum && !by_score) c = v[i] == -INFINITY ? -INFINITY : score(v[i]);
+                    b = fmaxf(b, fminf(a, c));
+                    a = fmaxf(a, c);
+                }
+            }
+            for (int o = sh.lanes / 2; o > 0; o >>= 1) {
+                const float oa = __shfl_xor_sync(kFullMask, a, o), ob = __shfl_xor_sync(kFullMask, b, o);
+                b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+                a = fmaxf(a, oa);
+            }
+            const float value = pair_sum ? a + b : a;
+            const uint32_t gkey = group < sh.groups ? order_key(value + 0.f) : 0u;
+            int rank = 0;
+            for (int g = 0; g < sh.groups; ++g) {
+                const uint32_t o = __shfl_sync(kFullMask, gkey, g * sh.lanes);
+                rank += o > gkey || (o == gkey && g < group);
+            }
+            const bool keep = group < sh.groups && rank < sh.topk_groups;
+            if (!keep) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) key[i] = 0u;
+            }
+            if (by_score || pair_sum) {
+                const float low = key_value(warp_min(keep ? gkey : 0xffffffffu));
+                const uint32_t out = warp_max(keep ? 0u : gkey);
+                if (out != 0u) {
+                    const float high = key_value(out);
+                    if (high != -INFINITY && !(low - high > 2.f * err + fabsf(low) * 0x1p-21f))
+                        wide = true;
+                }
+            }
+        }
+
+        // ---- K rounds: this lane's best, then the warp's
+        uint32_t best = 0u;
+        int at = 0;
+        auto local_best = [&]() {
+            best = 0u;
+            at = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (key[i] > best) {
+                    best = key[i];
+                    at = i;
+                }
+        };
+        local_best();
+        int mine = 0;
+        float xm = -INFINITY, prev_c = 0.f, prev_x = 0.f, prev_b = 0.f;
+        for (int k = 0; k < sh.K; ++k) {
+            const uint32_t top = warp_max(best);
+            const int src = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
+            float xv = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i == at) xv = v[i];
+            xv = __shfl_sync(kFullMask, xv, src);
+            const int e = min(__shfl_sync(kFullMask, base + at, src), E - 1);
+            if (lane == k) {
+                mine = e;
+                xm = xv;
+            }
+            if (by_score) {
+                const float c = key_value(top), be = bias[e];
+                if (k > 0 && c != -INFINITY && !(prev_c - c > err + fabsf(prev_c) * 0x1p-22f) &&
+                    !(xv == prev_x && be == prev_b))
+                    wide = true;
+                prev_c = c;
+                prev_x = xv;
+                prev_b = be;
+            }
+            if (lane == src) {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (i == at) key[i] = 0u;
+                local_best();
+            }
+        }
+        if (by_score && prev_c != -INFINITY) {
+            // experts left out that are too near the last one taken
+            const float border = prev_c - (err + fabsf(prev_c) * 0x1p-22f);
+            bool near = false;
+            if (best != 0u && !(key_value(best) < border)) {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (key[i] != 0u && !(key_value(key[i]) < border) &&
+                        !(v[i] == prev_x && bias[base + i] == prev_b))
+                        near = true;
+            }
+            wide = wide || __any_sync(kFullMask, near);
+        }
+        if (wide) {
+            float mw = m;
+            mine = choose_wide<T>(xrow, bias, sh, mw);
+            xm = lane < sh.K ? widen(xrow[mine]) : -INFINITY;
+        }
+
+        // ---- weights: lane k holds slot k
+        const bool live = lane < sh.K && xm != -INFINITY;
+        float w;
+        if (!sh.renorm) {
+            w = live ? score(xm) : 0.f;
+        } else {
+            // relative to the largest chosen logit, so that no sum underflows
+            float top = key_value(warp_max(order_key((live ? xm : -INFINITY) + 0.f)));
+            if (sh.sigmoid) top = fminf(top, 0.f);
+            if (sh.sigmoid && xm > 0.f) {
+                w = sigmoid(xm);
+            } else {
+                w = exp1(xm - top);
+                if (sh.sigmoid) w = __fdiv_rn(w, 1.f + exp1(xm));
+            }
+            if (!live) w = 0.f;
+            const float sum = warp_sum(w);
+            w = sum > 0.f ? __fdiv_rn(w, sum) : 0.f;
+        }
+        if (lane < sh.K) {
+            weights[row * sh.K + lane] = w * sh.scale;
+            idx[row * sh.K + lane] = mine;
+        }
+    }
+}
+
+// Gradient of the weights with respect to the logits, for given experts.  With
+// g_k = scale dw_k, s the scores, S = sum of the chosen scores, w = s / S:
+//   sigmoid:              dx_e = sum over slots of e of g_k s (1 - s)
+//   sigmoid, renormalised:       sum of w_k (g_k - D) (1 - s_k),  D = sum g w
+//   softmax:              dx_e = s_e (sum over slots of e of g_k - D),  D = sum g_k s_k
+//   softmax, renormalised: sum over slots of e of w_k (g_k - D),  D = sum g w
+// Only the plain softmax gives every logit a gradient; the others are zero
+// outside the chosen experts, whose logits alone are read.  One read of what
+// is needed and one write of the dense row: memory bound.
+template <typename T, int N, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32)
+route_bwd_kernel(const T* __restrict__ x, const int* __restrict__ idx,
+                 const float* __restrict__ dweights, T* __restrict__ dx, int64_t rows,
+                 const Shape sh) {
+    const int lane = threadIdx.x & 31;
+    const int E = sh.experts;
+    const int base = lane * sh.per_lane;
+    const int count = max(0, min(sh.per_lane, E - base));
+    const bool all = !sh.sigmoid && !sh.renorm;
+    for (int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < rows;
+         row += int64_t(gridDim.x) * kWarps) {
+        const T* xrow = x + row * E;
+        // lane k: slot k's expert, logit and gradient; an expert outside the
+        // row takes no part
+        int e = -1;
+        float xk = -INFINITY, g = 0.f;
+        if (lane < sh.K) {
+            e = idx[row * sh.K + lane];
+            if (e < 0 || e >= E) e = -1;
+            if (e >= 0) {
+                xk = widen(xrow[e]);
+                g = dweights[row * sh.K + lane] * sh.scale;
+            }
+        }
+        const bool live = xk != -INFINITY;
+        float v[N];
+        float slot;  // what slot k adds to its expert's logit
+        if (all) {
+            load_run<T, N, VEC>(xrow + base, count, v);
+            float m = v[0];
+#pragma unroll
+            for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+            m = key_value(warp_max(order_key(m + 0.f)));
+            const float ref = m == -INFINITY ? 0.f : m;
+            float d = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                v[i] = v[i] == -INFINITY ? 0.f : exp1(v[i] - ref);
+                d += v[i];
+            }
+            d = warp_sum(d);
+            const float inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
+            const float sk = live ? exp1(xk - ref) * inv_d : 0.f;
+            const float D = warp_sum(g * sk);
+            slot = live ? g * sk : 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] *= -inv_d * D;
+        } else {
+            float top = 0.f, w;
+            if (sh.renorm) {
+                top = key_value(warp_max(order_key((live ? xk : -INFINITY) + 0.f)));
+                if (sh.sigmoid) top = fminf(top, 0.f);
+            }
+            const float s = sh.sigmoid ? sigmoid(xk) : 0.f;
+            if (!sh.renorm || (sh.sigmoid && xk > 0.f)) {
+                w = s;
+            } else {
+                w = exp1(xk - top);
+                if (sh.sigmoid) w = __fdiv_rn(w, 1.f + exp1(xk));
+            }
+            if (!live) w = 0.f;
+            float D = 0.f;
+            if (sh.renorm) {
+                const float sum = warp_sum(w);
+                w = sum > 0.f ? __fdiv_rn(w, sum) : 0.f;
+                D = warp_sum(g * w);
+            }
+            slot = w * (g - D);
+            if (sh.sigmoid) slot *= sigmoid(-xk);
+            if (!live) slot = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = 0.f;
+        }
+        for (int k = 0; k < sh.K; ++k) {
+            const int ek = __shfl_sync(kFullMask, e, k) - base;
+            const float add = __shfl_sync(kFullMask, slot, k);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i == ek) v[i] += add;
+        }
+        T* drow = dx + row * E + base;
+        if constexpr (VEC) {
+            constexpr int bytes = N * int(sizeof(T));
+            uint32_t w[(bytes + 3) / 4];
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) w[i] = __float_as_uint(v[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; i += 2) w[i / 2] = pack_bf16x2(v[i], i + 1 < N ? v[i + 1] : 0.f);
+            }
+            if constexpr (bytes >= 16) {
+#pragma unroll
+                for (int i = 0; i < bytes / 16; ++i)
+                    __stcs(reinterpret_cast<uint4*>(drow) + i,
+                           make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+            } else if constexpr (bytes == 8) {
+                *reinterpret_cast<uint2*>(drow) = make_uint2(w[0], w[1]);
+            } else if constexpr (bytes == 4) {
+                *reinterpret_cast<uint32_t*>(drow) = w[0];
+            } else {
+                *reinterpret_cast<uint16_t*>(drow) = uint16_t(w[0]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i < count) {
+                    if constexpr (sizeof(T) == 4) drow[i] = v[i];
+                    else drow[i] = __float2bfloat16_rn(v[i]);
+                }
+        }
+    }
+}
+
+}  // namespace route
+}  // namespace os

@@ -1,0 +1,97 @@
+// Router over experts: the choice of kernel variant and the launches.
+#include "host_common.h"
+#include "internal.h"
+#include "kernels/route_kernel.cuh"
+
+namespace os {
+
+namespace {
+
+using route::Shape;
+
+// Lanes per group: the largest power of two that still gives every group its
+// own lanes; experts per lane follow.
+Shape make_shape(const RouteArgs& a, int groups) {
+    Shape s = {};
+    s.experts = a.experts;
+    s.K = a.K;
+    s.groups = groups;
+    s.topk_groups = a.topk_groups;
+    s.group_top = a.group_top;
+    s.lanes = 1;
+    while (s.lanes * 2 * groups <= 32) s.lanes *= 2;
+    s.per_lane = (a.experts / groups + s.lanes - 1) / s.lanes;
+    s.sigmoid = a.score == OS_SCORE_SIGMOID;
+    s.renorm = a.renorm;
+    s.scale = a.scale;
+    return s;
+}
+
+// Whole vectors: every lane that has experts has a full run, which starts on a
+// boundary of its own size (at most 16 bytes).
+bool whole_runs(const Shape& s, int N, int size, const void* p, const void* q) {
+    const int bytes = N * size < 16 ? N * size : 16;
+    return s.per_lane == N && s.experts == s.groups * s.lanes * N &&
+           reinterpret_cast<uintptr_t>(p) % bytes == 0 && reinterpret_cast<uintptr_t>(q) % bytes == 0;
+}
+
+int64_t grid_for(int64_t rows) { return min64(ceil_div(rows, route::kWarps), int64_t(1) << 22); }
+
+template <typename T, int N>
+cudaError_t launch_fwd(const RouteArgs& a, const Shape& s, float* weights, int32_t* idx,
+                       cudaStream_t stream) {
+    auto k = whole_runs(s, N, sizeof(T), a.x, a.x) ? route::route_kernel<T, N, true>
+                                                   : route::route_kernel<T, N, false>;
+    return launch_kernel(k, grid_for(a.rows), route::kWarps * 32, 1, 0, stream,
+                         static_cast<const T*>(a.x), a.bias, weights, reinterpret_cast<int*>(idx),
+                         a.rows, s);
+}
+
+template <typename T, int N>
+cudaError_t launch_bwd(const RouteArgs& a, const Shape& s, const int32_t* idx,
+                       const float* dweights, void* dx, cudaStream_t stream) {
+    auto k = whole_runs(s, N, sizeof(T), a.x, dx) ? route::route_bwd_kernel<T, N, true>
+                                                  : route::route_bwd_kernel<T, N, false>;
+    return launch_kernel(k, grid_for(a.rows), route::kWarps * 32, 1, 0, stream,
+                         static_cast<const T*>(a.x), reinterpret_cast<const int*>(idx), dweights,
+                         static_cast<T*>(dx), a.rows, s);
+}
+
+template <typename T>
+cudaError_t fwd(const RouteArgs& a, float* w, int32_t* idx, cudaStream_t stream) {
+    const Shape s = make_shape(a, a.groups);
+    if (s.per_lane <= 1) return launch_fwd<T, 1>(a, s, w, idx, stream);
+    if (s.per_lane <= 2) return launch_fwd<T, 2>(a, s, w, idx, stream);
+    if (s.per_lane <= 4) return launch_fwd<T, 4>(a, s, w, idx, stream);
+    if (s.per_lane <= 8) return launch_fwd<T, 8>(a, s, w, idx, stream);
+    if (s.per_lane <= 16) return launch_fwd<T, 16>(a, s, w, idx, stream);
+    if (s.per_lane <= 32) return launch_fwd<T, 32>(a, s, w, idx, stream);
+    return launch_fwd<T, 64>(a, s, w, idx, stream);  // 3, 5-7, 9-15 or 17-31 groups
+}
+
+template <typename T>
+cudaError_t bwd(const RouteArgs& a, const int32_t* idx, const float* dw, void* dx,
+                cudaStream_t stream) {
+    const Shape s = make_shape(a, 1);
+    if (s.per_lane <= 1) return launch_bwd<T, 1>(a, s, idx, dw, dx, stream);
+    if (s.per_lane <= 2) return launch_bwd<T, 2>(a, s, idx, dw, dx, stream);
+    if (s.per_lane <= 4) return launch_bwd<T, 4>(a, s, idx, dw, dx, stream);
+    if (s.per_lane <= 8) return launch_bwd<T, 8>(a, s, idx, dw, dx, stream);
+    if (s.per_lane <= 16) return launch_bwd<T, 16>(a, s, idx, dw, dx, stream);
+    return launch_bwd<T, 32>(a, s, idx, dw, dx, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouteArgs& a, float* weights, int32_t* idx, cudaStream_t stream) {
+    return a.in == OS_F32 ? fwd<float>(a, weights, idx, stream)
+                          : fwd<__nv_bfloat16>(a, weights, idx, stream);
+}
+
+cudaError_t launch_route_bwd(const RouteArgs& a, const int32_t* idx, const float* dweights,
+                             void* dx, cudaStream_t stream) {
+    return a.in == OS_F32 ? bwd<float>(a, idx, dweights, dx, stream)
+                          : bwd<__nv_bfloat16>(a, idx, dweights, dx, stream);
+}
+
+}  // namespace os
