@@ -4,8 +4,10 @@
 // With m the row's maximum, weights w_c = e^((x_c - m) / T).  Sorted by (logit
 // descending, column ascending) the filters each keep a prefix: top-k the
 // first k; top-p the shortest prefix of those whose weight reaches p times
-// theirs; min-p the columns with w >= min_p.  The draw is the lowest kept column
-// whose running sum, in column order, exceeds u times the kept weight.
+// theirs; min-p the columns with w >= min_p.  So what stays is the columns
+// with x > cut, and those with x == cut up to a last column.  The draw is the
+// lowest kept column whose running sum, in column order, exceeds u times the
+// kept weight.
 //
 // Exact draws.  Where a cut or a draw falls depends on sums of up to 2^31
 // weights compared with a border, so the sums are kept as integers: a weight
@@ -14,10 +16,31 @@
 // then do not depend on how the row was split or in which order atomics came,
 // and a draw that differs from the one in real arithmetic needs u within about
 // 2^-38 of a border.
+//
+// Passes.  The row is read from memory once (maximum, and bounds for the
+// cuts); what else is needed is read again from L2, where a batch's rows in
+// flight stay:
+//   no filter, min-p:  the kept columns' weights are summed per warp, the
+//                      border's warp is found, its run summed again in pieces,
+//                      and the border's piece element by element;
+//   top-k (<= 1024):   the columns at or above a bound that k of them reach
+//                      are listed in shared memory (a few times k), sorted,
+//                      and everything else happens on the list;
+//   top-p alone:       total weight; a histogram of weight over 2048 equal
+//                      steps of the logit down to where the rest could not
+//                      matter; the columns of the border's step are listed and
+//                      sorted, which gives the cut; then as without a filter;
+//   else (k larger, too many equal logits for the lists): the cut is found
+//                      digit by digit of the logits' order keys over the row.
+//
+// One row is shared by a cluster of S CTAs (1 to 8, by the number of rows),
+// each with a run of columns, which exchange through distributed shared memory.
 #pragma once
 
 #include <cuda_bf16.h>
 
+#include <cfloat>
+#include <climits>
 #include <cstdint>
 
 #include "ops.cuh"
@@ -27,6 +50,10 @@ namespace sample {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kList = 2048;   // columns that a list holds
+constexpr int kBins = 2048;   // steps of the top-p histogram
+constexpr int kTopK = 1024;   // top-k up to here is settled on a list
 using u64 = unsigned long long;
 
 // 2^(j/64) in two fp32 parts, j = 0..63
@@ -132,16 +159,125 @@ __device__ __forceinline__ u64 warp_prefix64(u64 v, int lane) {  // inclusive
     return v;
 }
 
+// What stays of a row: x > value, and x == value up to column `last`.
+struct alignas(8) Cut {
+    float value;
+    int last;
+    __device__ __forceinline__ bool keeps(float x, int64_t col) const {
+        return x > value || (x == value && col <= last);
+    }
+};
+
 struct Shared {
     float2 table[64];
-    u64 mass[256];
-    uint32_t count[256];
+    // exchanged over the cluster, one value per warp
+    uint32_t top[kWarps], bound[kWarps];
+    u64 sum[kWarps];    // weights of a warp's run
+    u64 draw[kWarps];   // kept weights of a warp's run
+    u64 piece[kWarps];  // kept weights of a piece of the border's run
+    // rank 0's findings, read by the others
+    uint32_t listed;    // columns put on the list (it may be more than fit)
+    uint32_t bin;       // the border's step of the histogram
+    Cut cut;
+    u64 above;
+    // scratch of one CTA
     u64 warp[kWarps];
     u64 result[2];
     uint32_t found[2];
+    uint32_t count[256];
+    u64 list[kList];    // (order key << 32) | ~column
+    union {
+        u64 mass[kBins];
+        u64 sorted[kList];
+    };
 };
 
-// Sum of v over the CTA (all threads get it).
+// This CTA's address of the shared object `local` in CTA `rank` of the cluster.
+template <int S, typename V>
+__device__ __forceinline__ V remote(const V* local, int rank) {
+    if constexpr (S == 1) {
+        return *local;
+    } else {
+        const uint32_t a = map_to_rank(local, rank);
+        V v;
+        if constexpr (sizeof(V) == 8) {
+            u64 t;
+            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(t) : "r"(a) : "memory");
+            memcpy(&v, &t, 8);
+        } else {
+            uint32_t t;
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(t) : "r"(a) : "memory");
+            memcpy(&v, &t, 4);
+        }
+        return v;
+    }
+}
+template <int S>
+__device__ __forceinline__ void row_sync() {
+    if constexpr (S == 1) __syncthreads();
+    else cluster_sync();
+}
+
+// Puts (x, col) on rank 0's list.
+template <int S>
+__device__ __forceinline__ void list_push(Shared& sh, float x, uint32_t col) {
+    const u64 e = (u64(order_key(x)) << 32) | (0xffffffffu - col);
+    if constexpr (S == 1) {
+        const uint32_t at = atomicAdd(&sh.listed, 1u);
+        if (at < kList) sh.list[at] = e;
+    } else {
+        uint32_t at;
+        asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;"
+                     : "=r"(at) : "r"(map_to_rank(&sh.listed, 0)) : "memory");
+        if (at < kList)
+            asm volatile("st.shared::cluster.u64 [%0], %1;"
+                         :: "r"(map_to_rank(&sh.list[at], 0)), "l"(e) : "memory");
+    }
+}
+
+// Sorts list[0, n) into sorted[0, n), best (key, lower column) first.  Up to
+// 512 entries are ranked by counting (one thread per entry, no barriers); more
+// by a bitonic network.  All threads of the CTA.
+__device__ __forceinline__ void sort_list(Shared& sh, int n) {
+    const int tid = threadIdx.x;
+    if (n <= kThreads) {
+        if (tid < n) {
+            const u64 mine = sh.list[tid];
+            int rank = 0;
+            for (int i = 0; i < n; ++i) rank += sh.list[i] > mine;
+            sh.sorted[rank] = mine;  // entries differ: each has a column of its own
+        }
+        __syncthreads();
+        return;
+    }
+    int size = 1024;
+    while (size < n) size *= 2;
+    for (int i = tid; i < size; i += kThreads) sh.sorted[i] = i < n ? sh.list[i] : 0ull;
+    for (int width = 2; width <= size; width *= 2)
+        for (int step = width / 2; step > 0; step /= 2) {
+            __syncthreads();
+            for (int i = tid; i < size / 2; i += kThreads) {
+                const int a = 2 * i - (i & (step - 1)), b = a + step;
+                const u64 p = sh.sorted[a], q = sh.sorted[b];
+                if ((p < q) == ((a & width) == 0)) {
+                    sh.sorted[a] = q;
+                    sh.sorted[b] = p;
+                }
+            }
+        }
+    __syncthreads();
+}
+
+// Inclusive prefix sum of one value per thread over the CTA.
+__device__ __forceinline__ u64 cta_prefix(Shared& sh, u64 v) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    v = warp_prefix64(v, lane);
+    __syncthreads();
+    if (lane == 31) sh.warp[warp] = v;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) v += sh.warp[i];
+    return v;
+}
 __device__ __forceinline__ u64 cta_sum(Shared& sh, u64 v) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     v = warp_sum64(v);
@@ -154,11 +290,20 @@ __device__ __forceinline__ u64 cta_sum(Shared& sh, u64 v) {
     return t;
 }
 
+// p (in [0, 1]) times `total`, rounded up: the least integer that is at least
+// the product.
+__device__ __forceinline__ u64 share_of(float p, u64 total) {
+    const u64 frac = __double2ull_rz(double(p) * 18446744073709551616.0);  // p < 1
+    const u64 want = __umul64hi(frac, total) + (frac * total != 0);
+    return want > 0 ? want : 1;
+}
+
+// ------------------------------------------------------------------ the general cut
 // Digit by digit from the top, the largest key T such that the elements with
 // key >= T amount to at least `want`, an element amounting to amount(key) (its
 // count or its weight).  On return `above` is what the keys > T amount to and
-// `ties` the number of elements with key T.  each(f) calls f(key) for every
-// element of the calling thread's share.
+// `ties` the number of elements with key T.  each(f) calls f(key, times) for
+// every element of the calling thread's share.
 template <typename Each, typename Amount>
 __device__ uint32_t select_key(Shared& sh, u64 want, Each each, Amount amount, u64& above,
                                uint32_t& ties) {
@@ -204,187 +349,478 @@ __device__ uint32_t select_key(Shared& sh, u64 want, Each each, Amount amount, u
     return prefix;
 }
 
+// The cut of top-k and top-p by one CTA over the whole row.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restrict__ out,
-              float* __restrict__ prob, int64_t rows, int cols, const Settings s, int bits) {
-    __shared__ Shared sh;
+__device__ __noinline__ Cut general_cut(Shared& sh, const T* p, int cols, const Weight w, int k,
+                                        float tp) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid < 64) sh.table[tid] = kPow2[tid];
-    // columns of a warp: a run of whole 32-column pieces
-    const int pieces = (cols + 31) / 32;
-    const int64_t per_warp = int64_t(pieces + kWarps - 1) / kWarps * 32;
+    uint32_t cut = kKeyNegInf, room = 0;  // keys > cut stay, and `room` columns at it
+    bool some = false;                    // only the first `room`, there are more
+    auto each_all = [&](auto f) {
+        for (int64_t i = tid; i < cols; i += kThreads) f(order_key(widen(p[i])), 1u);
+    };
+    if (k > 0 && k < cols) {
+        u64 above;
+        uint32_t ties;
+        cut = select_key(sh, u64(k), each_all, [](uint32_t) { return 1ull; }, above, ties);
+        room = uint32_t(k - above);
+        some = room < ties;
+        if (cut <= kKeyNegInf) {
+            cut = kKeyNegInf;
+            some = false;
+            room = 0;
+        }
+    }
+    if (tp < 1.f) {
+        u64 total = 0;
+        for (int64_t i = tid; i < cols; i += kThreads) {
+            const float v = widen(p[i]);
+            if (order_key(v) > cut) total += w(v);
+        }
+        const u64 w_cut = cut > kKeyNegInf ? w(key_value(cut)) : 0;
+        total = cta_sum(sh, total) + w_cut * room;
+        const u64 want = share_of(fmaxf(tp, 0.f), total);
+        const uint32_t cut_k = cut, room_k = room;
+        u64 above;
+        uint32_t ties;
+        auto each_kept = [&](auto f) {
+            each_all([&](uint32_t key, uint32_t) {
+                if (key > cut_k) f(key, 1u);
+            });
+            if (tid == 0 && room_k > 0) f(cut_k, room_k);
+        };
+        cut = select_key(sh, want, each_kept, [&](uint32_t key) { return w(key_value(key)); },
+                         above, ties);
+        const u64 wt = w(key_value(cut));
+        room = wt > 0 ? uint32_t((want - above + wt - 1) / wt) : ties;
+        if (room > ties) room = ties;
+        some = cut == cut_k ? (some || room < room_k) : room < ties;
+    }
+    if (cut <= kKeyNegInf) return {-FLT_MAX, INT_MAX};
+    if (!some) return {key_value(cut), INT_MAX};
+    // the last of the first `room` columns at the cut: runs of columns per warp
+    const int64_t per_warp = (int64_t(cols) + kThreads - 1) / kThreads * 32;
     const int64_t lo = min(int64_t(cols), warp * per_warp);
     const int64_t hi = min(int64_t(cols), (warp + 1) * per_warp);
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-        const T* p = x + row * cols;
-        // ---- maximum and its lowest column
-        u64 top = 0;
-        for (int64_t c = tid; c < cols; c += kThreads) {
-            const u64 k = (u64(order_key(widen(p[c]))) << 32) | (0xffffffffu - uint32_t(c));
-            top = k > top ? k : top;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const u64 t = __shfl_xor_sync(kFullMask, top, o);
-            top = t > top ? t : top;
-        }
-        __syncthreads();
-        if (lane == 0) sh.warp[warp] = top;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) top = sh.warp[i] > top ? sh.warp[i] : top;
-        const uint32_t top_key = uint32_t(top >> 32);
-        const float T_ = s.temperature ? s.temperature[row] : s.temperature_all;
-        if (top_key <= kKeyNegInf || !(T_ > 0.f)) {
-            if (tid == 0) {
-                out[row] = top_key <= kKeyNegInf ? -1 : int(0xffffffffu - uint32_t(top));
-                if (prob) prob[row] = top_key <= kKeyNegInf ? 0.f : 1.f;
+    uint32_t mine = 0;
+    for (int64_t i = lo + lane; i < hi; i += 32) mine += order_key(widen(p[i])) == cut;
+    mine = __reduce_add_sync(kFullMask, mine);
+    __syncthreads();
+    if (lane == 0) sh.warp[warp] = mine;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int i = 0; i < warp; ++i) before += uint32_t(sh.warp[i]);
+    if (before < room && room <= before + mine) {
+        for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+            const bool tie = i0 + lane < hi && order_key(widen(p[i0 + lane])) == cut;
+            const uint32_t b = __ballot_sync(kFullMask, tie);
+            if (before + __popc(b) >= room) {
+                const uint32_t upto = before + __popc(b & (0xffffffffu >> (31 - lane)));
+                if (tie && upto == room) sh.found[0] = uint32_t(i0 + lane);
+                break;
             }
-            continue;
+            before += __popc(b);
         }
-        Weight w;
-        w.m = key_value(top_key);
-        const double c = fmin(1.4426950408889634074 / double(T_), 1e30);
-        w.c_hi = float(c);
-        w.c_lo = float(c - double(w.c_hi));
-        w.bits = bits;
-        w.table = sh.table;
+    }
+    __syncthreads();
+    return {key_value(cut), int(sh.found[0])};
+}
+
+// ------------------------------------------------------------------ the kernel
+// The 16-byte blocks of memory that a row covers: block b holds columns
+// b * EPV - head .. b * EPV - head + EPV - 1, those outside the row read as -inf.
+template <typename T>
+struct Blocks {
+    static constexpr int EPV = VecTraits<T>::EPV;
+    const T* base;  // 16-byte aligned, `head` elements before the row
+    int head, cols;
+    int64_t count;
+    __device__ __forceinline__ Blocks(const T* row, int cols_) : cols(cols_) {
+        head = int((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+        base = row - head;
+        count = (int64_t(head) + cols + EPV - 1) / EPV;
+    }
+    __device__ __forceinline__ int64_t col(int64_t b) const { return b * EPV - head; }
+    __device__ __forceinline__ void load(int64_t b, float (&v)[EPV]) const {
+        const int64_t c = col(b);
+        if (c >= 0 && c + EPV <= cols) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(base) + b);
+            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = fmaxf(__uint_as_float(a[i]), -INFINITY);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack_bf16x2(a[i]);
+                    v[2 * i] = fmaxf(f.x, -INFINITY);
+                    v[2 * i + 1] = fmaxf(f.y, -INFINITY);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPV; ++i)
+                v[i] = c + i >= 0 && c + i < cols ? widen(base[b * EPV + i]) : -INFINITY;
+        }
+    }
+};
+
+template <typename T, int S>
+__global__ void __launch_bounds__(kThreads, 2)
+sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restrict__ out,
+              float* __restrict__ prob, int64_t rows, int cols, const Settings s, int bits) {
+    constexpr int EPV = VecTraits<T>::EPV;
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = S == 1 ? 0 : int(cluster_rank());
+    if (tid < 64) sh.table[tid] = kPow2[tid];
+    for (int64_t row = blockIdx.x / S; row < rows; row += gridDim.x / S) {
+        const Blocks<T> blocks(x + row * cols, cols);
+        // runs of blocks, in column order: CTA by CTA, warp by warp
+        const int64_t per_warp = (blocks.count + S * kThreads - 1) / (S * kThreads) * 32;
+        const int64_t lo = min(blocks.count, (rank * kWarps + warp) * per_warp);
+        const int64_t hi = min(blocks.count, lo + per_warp);
+        const float t_row = s.temperature ? s.temperature[row] : s.temperature_all;
         const int k = s.top_k ? s.top_k[row] : s.top_k_all;
         const float tp = s.top_p ? s.top_p[row] : s.top_p_all;
         const float mp = s.min_p ? s.min_p[row] : s.min_p_all;
+        float uu = u[row] > 0.f ? fminf(u[row], 0x1.fffffep-1f) : 0.f;
+        const bool by_k = k > 0 && k < cols;
+        const bool list_k = by_k && k <= kTopK && k <= S * kThreads;
 
-        // ---- the kept prefix: keys > cut, and the first `room` columns with key == cut
-        uint32_t cut = kKeyNegInf, room = 0;
-        bool some = false;  // of the columns at the cut, only the first `room`
-        auto each_all = [&](auto f) {
-            for (int64_t i = tid; i < cols; i += kThreads) f(order_key(widen(p[i])), 1u);
-        };
-        if (k > 0 && k < cols) {
-            u64 above;
-            uint32_t ties;
-            cut = select_key(sh, u64(k), each_all, [](uint32_t) { return 1ull; }, above, ties);
-            room = uint32_t(k - above);
-            some = room < ties;
-            if (cut <= kKeyNegInf) {
-                cut = kKeyNegInf;
-                some = false;
-                room = 0;
-            } else if (!some) {
-                room = ties;
-            }
+        // ---- the only pass over memory: maxima per thread
+        float top = -INFINITY;
+#pragma unroll 4
+        for (int64_t b = lo + lane; b < hi; b += 32) {
+            float v[EPV];
+            blocks.load(b, v);
+#pragma unroll
+            for (int i = 0; i < EPV; ++i) top = fmaxf(top, v[i]);
         }
-        if (tp < 1.f) {
-            const float pc = fmaxf(tp, 0.f);
-            u64 total = 0;
-            for (int64_t i = tid; i < cols; i += kThreads) {
-                const float v = widen(p[i]);
-                if (order_key(v) > cut) total += w(v);
-            }
-            const u64 w_cut = cut > kKeyNegInf ? w(key_value(cut)) : 0;
-            total = cta_sum(sh, total) + w_cut * room;
-            const u64 frac = __double2ull_rz(double(pc) * 18446744073709551616.0);
-            u64 want = __umul64hi(frac, total) + (frac * total != 0);
-            if (want == 0) want = 1;
-            const uint32_t cut_k = cut, room_k = room;
-            u64 above;
-            uint32_t ties;
-            auto each_kept = [&](auto f) {
-                each_all([&](uint32_t key, uint32_t) {
-                    if (key > cut_k) f(key, 1u);
-                });
-                if (tid == 0 && room_k > 0) f(cut_k, room_k);
-            };
-            cut = select_key(sh, want, each_kept, [&](uint32_t key) { return w(key_value(key)); },
-                             above, ties);
-            const u64 wt = w(key_value(cut));
-            room = wt > 0 ? uint32_t((want - above + wt - 1) / wt) : ties;
-            if (room > ties) room = ties;
-            some = cut == cut_k ? (some || room < room_k) : room < ties;
-        }
-        if (mp > 0.f) {
-            const float q = fminf(mp, 1.f);
-            const double thr = q < 1.f ? double(w.m) + double(T_) * log(double(q)) : double(w.m);
-            uint32_t key = order_key(__double2float_ru(thr));
-            if (key <= kKeyNegInf) key = kKeyNegInf + 1;
-            if (key > top_key) key = top_key;
-            if (key > cut) {  // everything from this key on
-                cut = key - 1;
-                some = false;
-                room = 0;
-            }
-        }
-        if (cut > kKeyNegInf && !some && room > 0) --cut;  // all columns at the cut stay: keys > cut - 1
-
-        // ---- the last column that stays among those at the cut
-        int last = -1;
-        if (some) {
-            uint32_t mine = 0;
-            for (int64_t i = lo + lane; i < hi; i += 32) mine += order_key(widen(p[i])) == cut;
-            mine = __reduce_add_sync(kFullMask, mine);
-            __syncthreads();
-            if (lane == 0) sh.warp[warp] = mine;
-            __syncthreads();
-            uint32_t before = 0;
-            for (int i = 0; i < warp; ++i) before += uint32_t(sh.warp[i]);
-            if (before < room && room <= before + mine) {
-                for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-                    const bool tie = i0 + lane < hi && order_key(widen(p[i0 + lane])) == cut;
-                    const uint32_t b = __ballot_sync(kFullMask, tie);
-                    if (before + __popc(b) >= room) {
-                        const uint32_t upto = before + __popc(b & (0xffffffffu >> (31 - lane)));
-                        if (tie && upto == room) sh.found[0] = uint32_t(i0 + lane);
-                        break;
-                    }
-                    before += __popc(b);
+        uint32_t key = order_key(top);
+        const uint32_t warp_top = __reduce_max_sync(kFullMask, key);
+        uint32_t bound = 0;
+        if (list_k) {
+            // every warp's j-th best thread maximum, j = ceil(k / warps): the
+            // smallest of them is reached by j threads in every warp, so by k
+            // elements.  The lanes' keys are sorted descending to find it.
+            const int j = (k + S * kWarps - 1) / (S * kWarps);
+#pragma unroll
+            for (int width = 2; width <= 32; width *= 2)
+#pragma unroll
+                for (int step = width / 2; step > 0; step /= 2) {
+                    const uint32_t o = __shfl_xor_sync(kFullMask, key, step);
+                    const bool first = (lane & step) == 0, down = (lane & width) == 0;
+                    key = first == down ? max(key, o) : min(key, o);
                 }
-            }
-            __syncthreads();
-            last = int(sh.found[0]);
+            bound = __shfl_sync(kFullMask, key, j - 1);
         }
+        if (lane == 0) {
+            sh.top[warp] = warp_top;
+            sh.bound[warp] = bound;
+        }
+        if (tid == 0) sh.listed = 0;
+        row_sync<S>();
+        uint32_t top_key = 0;
+        bound = 0xffffffffu;
+        for (int i = lane; i < S * kWarps; i += 32) {
+            top_key = max(top_key, remote<S>(&sh.top[i % kWarps], i / kWarps));
+            bound = min(bound, remote<S>(&sh.bound[i % kWarps], i / kWarps));
+        }
+        top_key = __reduce_max_sync(kFullMask, top_key);
+        bound = __reduce_min_sync(kFullMask, bound);
 
-        // ---- the draw, in column order
-        const float uu = u[row] > 0.f ? fminf(u[row], 0x1.fffffep-1f) : 0.f;
-        auto kept_weight = [&](int64_t i) -> u64 {
-            const float v = widen(p[i]);
-            const uint32_t key = order_key(v);
-            if (!(key > cut || (key == cut && i <= last))) return 0;
-            const u64 a = w(v);
-            return uu == 0.f && a == 0 ? 1ull : a;  // u = 0: the first kept column, however small
-        };
-        u64 mine = 0;
-        for (int64_t i = lo + lane; i < hi; i += 32) mine += kept_weight(i);
-        mine = warp_sum64(mine);
-        __syncthreads();
-        if (lane == 0) sh.warp[warp] = mine;
-        __syncthreads();
-        u64 before = 0, total = 0;
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) before += sh.warp[i];
-            total += sh.warp[i];
+        Weight w;
+        w.m = key_value(top_key);
+        w.bits = bits;
+        w.table = sh.table;
+        const bool greedy = !(t_row > 0.f);
+        {
+            const double c = greedy ? 1.0 : fmin(1.4426950408889634074 / double(t_row), 1e30);
+            w.c_hi = float(c);
+            w.c_lo = float(c - double(w.c_hi));
         }
-        const u64 target = __umul64hi(__double2ull_rz(double(uu) * 18446744073709551616.0), total);
-        if (before <= target && target < before + mine) {
-            u64 run = before;
-            for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-                const u64 a = i0 + lane < hi ? kept_weight(i0 + lane) : 0;
-                const u64 upto = run + warp_prefix64(a, lane);
-                const uint32_t hit = __ballot_sync(kFullMask, upto > target);
-                if (hit) {
-                    if (lane == __ffs(hit) - 1) {
-                        out[row] = int(i0 + lane);
-                        // the weight itself, not its integer: a small one keeps its digits
-                        if (prob) {
-                            const float v = widen(p[i0 + lane]);
-                            const double e = v == w.m ? 1.0 : exp((double(v) - double(w.m)) / double(T_));
-                            prob[row] = float(ldexp(e, bits) / double(total));
+        // the lowest logit that min-p keeps; compared in fp32 it decides as in
+        // real arithmetic, since it is rounded up
+        float floor_p = -FLT_MAX;
+        if (mp > 0.f && !greedy) {
+            const float q = fminf(mp, 1.f);
+            floor_p = q < 1.f ? __double2float_ru(double(w.m) + double(t_row) * log(double(q))) : w.m;
+        }
+        auto write = [&](int64_t c, float v, u64 total) {
+            out[row] = int(c);
+            // the weight itself, not its integer: a small one keeps its digits
+            const double e = v == w.m ? 1.0 : exp((double(v) - double(w.m)) / double(t_row));
+            if (prob) prob[row] = greedy ? 1.f : float(ldexp(e, bits) / double(total));
+        };
+        auto target_of = [&](u64 total) {
+            return __umul64hi(__double2ull_rz(double(uu) * 18446744073709551616.0), total);
+        };
+
+        bool done = false;
+        Cut cut = {-FLT_MAX, INT_MAX};
+        if (top_key <= kKeyNegInf) {
+            if (rank == 0 && tid == 0) {
+                out[row] = -1;
+                if (prob) prob[row] = 0.f;
+            }
+            done = true;
+        } else if (greedy) {
+            cut.value = w.m;
+            uu = 0.f;  // the first kept column
+        } else {
+            bool settled = !by_k && !(tp < 1.f);
+            if (list_k && bound > kKeyNegInf) {
+                // ---- top-k on a list
+                const float least = key_value(bound);
+#pragma unroll 2
+                for (int64_t b = lo + lane; b < hi; b += 32) {
+                    float v[EPV];
+                    blocks.load(b, v);
+#pragma unroll
+                    for (int i = 0; i < EPV; ++i)
+                        if (v[i] >= least) list_push<S>(sh, v[i], uint32_t(blocks.col(b) + i));
+                }
+                row_sync<S>();
+                const uint32_t n = remote<S>(&sh.listed, 0);
+                if (n <= kList) {
+                    settled = done = true;
+                    if (rank == 0) {
+                        sort_list(sh, int(n));
+                        // thread t: sorted entries 2t, 2t + 1 (k <= 1024)
+                        u64 e[2], a[2];
+                        float v[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            e[i] = 2 * tid + i < k ? sh.sorted[2 * tid + i] : 0;
+                            v[i] = e[i] ? key_value(uint32_t(e[i] >> 32)) : -INFINITY;
+                            a[i] = e[i] ? w(v[i]) : 0;
+                        }
+                        const u64 upto1 = cta_prefix(sh, a[0] + a[1]), upto0 = upto1 - a[1];
+                        __syncthreads();
+                        if (tid == kThreads - 1) sh.result[0] = upto1;
+                        __syncthreads();
+                        if (tp < 1.f) {
+                            const u64 want = share_of(fmaxf(tp, 0.f), sh.result[0]);
+                            if (upto0 - a[0] >= want) a[0] = 0, v[0] = -INFINITY;
+                            if (upto0 >= want) a[1] = 0, v[1] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (!(v[i] >= floor_p)) a[i] = 0, v[i] = -INFINITY;
+                        // what stays, as (column, weight): list and sorted hold them
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (uu == 0.f && v[i] > -INFINITY && a[i] == 0) a[i] = 1;
+                            sh.list[2 * tid + i] = 0xffffffffu - uint32_t(e[i]);
+                        }
+                        const u64 total = cta_sum(sh, a[0] + a[1]);
+                        sh.sorted[2 * tid] = a[0];
+                        sh.sorted[2 * tid + 1] = a[1];
+                        __syncthreads();
+                        const u64 target = target_of(total);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (a[i] == 0) continue;
+                            const u64 col = 0xffffffffu - uint32_t(e[i]);
+                            u64 before = 0;
+                            for (int j = 0; j < k; ++j) before += sh.list[j] < col ? sh.sorted[j] : 0;
+                            if (before <= target && target < before + a[i])
+                                write(int64_t(col), v[i], total);
                         }
                     }
-                    break;
                 }
-                run = __shfl_sync(kFullMask, upto, 31);
+            } else if (!by_k && tp < 1.f) {
+                // ---- top-p: the border by a histogram of weight
+                u64 mine = 0;
+                for (int64_t b = lo + lane; b < hi; b += 32) {
+                    float v[EPV];
+                    blocks.load(b, v);
+#pragma unroll
+                    for (int i = 0; i < EPV; ++i) mine += w(v[i]);
+                }
+                mine = warp_sum64(mine);
+                if (lane == 0) sh.sum[warp] = mine;
+                for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0;
+                row_sync<S>();
+                u64 total = 0;
+                for (int i = lane; i < S * kWarps; i += 32)
+                    total += remote<S>(&sh.sum[i % kWarps], i / kWarps);
+                total = warp_sum64(total);
+                const u64 want = share_of(fmaxf(tp, 0.f), total);
+                // columns of at most this weight cannot reach the border even
+                // together; `low` is at or below their logits
+                const u64 small = (total - want) / u64(cols);
+                double low = -FLT_MAX;
+                if (small > 0)
+                    low = double(w.m) +
+                          double(t_row) * (log(double(small)) - double(bits) * 0.69314718055994530942);
+                low -= 1e-6 * (fabs(low) + fabs(double(w.m)) + double(t_row));
+                const float least = fmaxf(float(low), -FLT_MAX);
+                const float steps = float(kBins) / (w.m - least);
+                if (w.m < INFINITY && steps > 0.f && steps < INFINITY) {
+                    auto step_of = [&](float v) { return min(kBins - 1, int((w.m - v) * steps)); };
+                    for (int64_t b = lo + lane; b < hi; b += 32) {
+                        float v[EPV];
+                        blocks.load(b, v);
+#pragma unroll
+                        for (int i = 0; i < EPV; ++i)
+                            if (v[i] >= least) atomicAdd(&sh.mass[step_of(v[i])], w(v[i]));
+                    }
+                    row_sync<S>();
+                    if (rank == 0) {
+                        u64 part[kBins / kThreads], own = 0;
+#pragma unroll
+                        for (int i = 0; i < kBins / kThreads; ++i) {
+                            part[i] = 0;
+                            for (int r = 0; r < S; ++r)
+                                part[i] += remote<S>(&sh.mass[kBins / kThreads * tid + i], r);
+                            own += part[i];
+                        }
+                        const u64 upto = cta_prefix(sh, own);
+                        u64 run = upto - own;
+                        if (run < want && want <= upto) {
+                            int i = 0;
+                            while (i < kBins / kThreads - 1 && run + part[i] < want) run += part[i++];
+                            sh.bin = kBins / kThreads * tid + i;
+                            sh.above = run;
+                        }
+                    }
+                    row_sync<S>();
+                    const int bin = int(remote<S>(&sh.bin, 0));
+                    for (int64_t b = lo + lane; b < hi; b += 32) {
+                        float v[EPV];
+                        blocks.load(b, v);
+#pragma unroll
+                        for (int i = 0; i < EPV; ++i)
+                            if (v[i] >= least && step_of(v[i]) == bin)
+                                list_push<S>(sh, v[i], uint32_t(blocks.col(b) + i));
+                    }
+                    row_sync<S>();
+                    const uint32_t n = remote<S>(&sh.listed, 0);
+                    if (n <= kList) {
+                        settled = true;
+                        if (rank == 0) {
+                            sort_list(sh, int(n));
+                            constexpr int P = kList / kThreads;
+                            u64 a[P], own = 0;
+#pragma unroll
+                            for (int i = 0; i < P; ++i) {
+                                const int at = P * tid + i;
+                                a[i] = at < int(n) ? w(key_value(uint32_t(sh.sorted[at] >> 32))) : 0;
+                                own += a[i];
+                            }
+                            const u64 upto = cta_prefix(sh, own) + sh.above;
+                            u64 run = upto - own;
+                            if (run < want && want <= upto) {
+                                int i = 0;
+                                while (i < P - 1 && run + a[i] < want) run += a[i++];
+                                const u64 e = sh.sorted[P * tid + i];
+                                sh.cut = {key_value(uint32_t(e >> 32)),
+                                          int(0xffffffffu - uint32_t(e))};
+                            }
+                        }
+                        row_sync<S>();
+                        cut = remote<S>(&sh.cut, 0);
+                    }
+                }
+            }
+            if (!settled) {
+                row_sync<S>();
+                if (rank == 0) {
+                    const Cut c = general_cut<T>(sh, x + row * cols, cols, w, k, tp);
+                    __syncthreads();
+                    if (tid == 0) sh.cut = c;
+                }
+                row_sync<S>();
+                cut = remote<S>(&sh.cut, 0);
+            }
+            if (floor_p > cut.value) cut = {floor_p, INT_MAX};
+        }
+
+        if (!done) {
+            // ---- the draw, in column order
+            auto kept_weight = [&](float v, int64_t c) -> u64 {
+                if (!cut.keeps(v, c)) return 0;
+                const u64 a = w(v);
+                return uu == 0.f && a == 0 ? 1ull : a;  // u = 0: the first column, however small
+            };
+            auto block_weight = [&](int64_t b) {
+                float v[EPV];
+                blocks.load(b, v);
+                u64 a = 0;
+#pragma unroll
+                for (int i = 0; i < EPV; ++i) a += kept_weight(v[i], blocks.col(b) + i);
+                return a;
+            };
+            u64 mine = 0;
+            for (int64_t b = lo + lane; b < hi; b += 32) mine += block_weight(b);
+            mine = warp_sum64(mine);
+            if (lane == 0) sh.draw[warp] = mine;
+            row_sync<S>();
+            // the run that holds the border: before <= target < before + its sum
+            constexpr int R = (S * kWarps + 31) / 32;  // runs per lane, in order
+            u64 part[R], own = 0;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int g = R * lane + i;
+                part[i] = g < S * kWarps ? remote<S>(&sh.draw[g % kWarps], g / kWarps) : 0;
+                own += part[i];
+            }
+            const u64 upto = warp_prefix64(own, lane);
+            const u64 total = __shfl_sync(kFullMask, upto, 31), target = target_of(total);
+            const int src = __ffs(__ballot_sync(kFullMask, upto > target)) - 1;
+            int run_id = R * lane;
+            u64 before = upto - own;
+#pragma unroll
+            for (int i = 0; i < R - 1; ++i)
+                if (before + part[i] <= target && run_id == R * lane + i) {
+                    before += part[i];
+                    ++run_id;
+                }
+            run_id = __shfl_sync(kFullMask, run_id, src);
+            before = __shfl_sync(kFullMask, before, src);
+            if (run_id / kWarps == rank) {
+                // its columns again, a piece per warp
+                const int64_t from = run_id * per_warp;
+                const int64_t to = min(blocks.count, from + per_warp);
+                const int64_t per_piece = (per_warp / 32 + kWarps - 1) / kWarps * 32;
+                const int64_t plo = min(to, from + warp * per_piece), phi = min(to, plo + per_piece);
+                u64 piece = 0;
+                for (int64_t b = plo + lane; b < phi; b += 32) piece += block_weight(b);
+                piece = warp_sum64(piece);
+                if (lane == 0) sh.piece[warp] = piece;
+                __syncthreads();
+                for (int i = 0; i < warp; ++i) before += sh.piece[i];
+                if (before <= target && target < before + piece) {
+                    for (int64_t b0 = plo; b0 < phi; b0 += 32) {
+                        const u64 a = b0 + lane < phi ? block_weight(b0 + lane) : 0;
+                        const u64 end = before + warp_prefix64(a, lane);
+                        const uint32_t hit = __ballot_sync(kFullMask, end > target);
+                        if (hit) {
+                            if (lane == __ffs(hit) - 1) {
+                                float v[EPV];
+                                blocks.load(b0 + lane, v);
+                                u64 run = end - a;
+                                bool open = true;
+#pragma unroll
+                                for (int i = 0; i < EPV; ++i) {
+                                    const int64_t c = blocks.col(b0 + lane) + i;
+                                    run += kept_weight(v[i], c);
+                                    if (open && run > target) {
+                                        write(c, v[i], total);
+                                        open = false;
+                                    }
+                                }
+                            }
+                            break;
+                        }
+                        before = __shfl_sync(kFullMask, end, 31);
+                    }
+                }
             }
         }
+        row_sync<S>();  // the next row's values may be written; peers may leave
     }
 }
 

@@ -7,16 +7,33 @@ namespace os {
 
 namespace {
 
+template <typename T, int S>
+cudaError_t launch_s(const void* x, const float* u, int32_t* out, float* prob, int64_t rows,
+                     int cols, const sample::Settings& s, int bits, cudaStream_t stream) {
+    return launch_kernel(sample::sample_kernel<T, S>, S * min64(rows, int64_t(1) << 22),
+                         sample::kThreads, S, 0, stream, static_cast<const T*>(x), u,
+                         reinterpret_cast<int*>(out), prob, rows, cols, s, bits);
+}
+
 template <typename T>
 cudaError_t launch_t(const void* x, const float* u, int32_t* out, float* prob, int64_t rows,
                      int cols, const sample::Settings& s, cudaStream_t stream) {
+    const DeviceInfo* dev = device_info();
+    if (!dev) return cudaErrorInvalidDevice;
     // weights are multiples of 2^-bits, at most 1: cols of them fit in 62 bits
     int log2_cols = 0;
     while ((int64_t(1) << log2_cols) < cols) ++log2_cols;
     const int bits = 62 - log2_cols < 44 ? 62 - log2_cols : 44;
-    return launch_kernel(sample::sample_kernel<T>, min64(rows, int64_t(1) << 22),
-                         sample::kThreads, 1, 0, stream, static_cast<const T*>(x), u,
-                         reinterpret_cast<int*>(out), prob, rows, cols, s, bits);
+    // CTAs per row: as many as fit beside each other (two per SM), while each
+    // keeps 32 blocks of 16 bytes per warp or more
+    const int64_t slots = 2 * int64_t(dev->sms);
+    const int64_t useful = ceil_div(int64_t(cols) * int64_t(sizeof(T)), 16 * sample::kThreads);
+    int S = 1;
+    while (S < sample::kMaxCluster && 2 * S * rows <= slots && 2 * S <= useful) S *= 2;
+    if (S == 8) return launch_s<T, 8>(x, u, out, prob, rows, cols, s, bits, stream);
+    if (S == 4) return launch_s<T, 4>(x, u, out, prob, rows, cols, s, bits, stream);
+    if (S == 2) return launch_s<T, 2>(x, u, out, prob, rows, cols, s, bits, stream);
+    return launch_s<T, 1>(x, u, out, prob, rows, cols, s, bits, stream);
 }
 
 }  // namespace
