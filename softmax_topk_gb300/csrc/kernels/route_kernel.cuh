@@ -18,7 +18,6 @@
 //
 // Exact choices.  Without a bias s rises with x, so logits are compared and
 // the choice is exact.  With a bias (and for sums of two scores) c is computed
-// in fp32 and the choice could turn on its rounding.  Its error is bounded:
 // s carries at most (|x - m| + 12) 2^-24 relative, which is at most
 // 2^-20 s_max absolute (|z| e^-|z| is small where s is), and the sum one
 // rounding.  A token in which two compared values lie closer than the bounds
@@ -28,6 +27,7 @@
 
 #include <cuda_bf16.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "ops.cuh"
@@ -43,6 +43,7 @@ struct Shape {
     int experts, K, groups, topk_groups, group_top;
     int lanes;     // lanes per group (a power of two)
     int per_lane;  // experts per lane
+    int index_mask;  // experts up to a power of two, less one
     int sigmoid, renorm;
     float scale;
 };
@@ -65,6 +66,12 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
     return v;
+}
+
+__device__ __forceinline__ float rcp_sfu(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 __device__ __forceinline__ float sigmoid(float x) {
@@ -115,8 +122,8 @@ __device__ __forceinline__ void load_run(const T* p, int count, float (&v)[N]) {
 
 // The choice of one token with s and c in 64 bits (bias given or sums of two
 // scores): rare, so written for size.  Every lane returns the expert of slot
-// `lane` (lane < K).  xrow is the token's row, lanes hold its logits as in
-// the caller.
+// `lane` (lane < K); m is the row's maximum.  Lane l looks after experts l,
+// l + 32, ...
 template <typename T>
 __device__ __noinline__ int choose_wide(const T* xrow, const float* bias, const Shape sh, float mf) {
     const int lane = threadIdx.x & 31, E = sh.experts, gsize = E / sh.groups;
@@ -130,28 +137,34 @@ __device__ __noinline__ int choose_wide(const T* xrow, const float* bias, const 
         }
         for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFullMask, d, o);
     }
-    auto choice = [&](int e) -> double {
+    double c[kMaxExperts / 32];
+    for (int e = lane; e < E; e += 32) {
         const float x = widen(xrow[e]);
-        if (!(x > -INFINITY)) return -INFINITY;
-        const double s = sh.sigmoid ? 1.0 / (1.0 + exp(-double(x))) : exp(double(x) - m) / d;
-        return bias ? s + double(bias[e]) : s;
-    };
-    // groups: lane g holds group g's value; bit g of `kept` is set when it takes part
+        double v = -INFINITY;
+        if (x > -INFINITY) {
+            v = sh.sigmoid ? 1.0 / (1.0 + exp(-double(x))) : exp(double(x) - m) / d;
+            if (bias) v += double(bias[e]);
+        }
+        c[e >> 5] = v;
+    }
+    // the groups that take part, one bit each
     uint32_t kept = 0xffffffffu;
     if (sh.groups > 1) {
-        double score = -INFINITY;
-        if (lane < sh.groups) {
+        double score = -INFINITY;  // lane g: group g's value
+        for (int g = 0; g < sh.groups; ++g) {
             double a = -INFINITY, b = -INFINITY;
-            for (int i = 0; i < gsize; ++i) {
-                const double c = choice(lane * gsize + i);
-                if (c > a) {
-                    b = a;
-                    a = c;
-                } else if (c > b) {
-                    b = c;
+            for (int e = lane; e < (g + 1) * gsize; e += 32)
+                if (e >= g * gsize) {
+                    b = fmax(b, fmin(a, c[e >> 5]));
+                    a = fmax(a, c[e >> 5]);
                 }
+            for (int o = 16; o > 0; o >>= 1) {
+                const double oa = __shfl_xor_sync(kFullMask, a, o);
+                const double ob = __shfl_xor_sync(kFullMask, b, o);
+                b = fmax(fmin(a, oa), fmax(b, ob));
+                a = fmax(a, oa);
             }
-            score = sh.group_top == 2 ? a + b : a;
+            if (lane == g) score = sh.group_top == 2 ? a + b : a;
         }
         int rank = 0;
         for (int g = 0; g < sh.groups; ++g) {
@@ -167,11 +180,11 @@ __device__ __noinline__ int choose_wide(const T* xrow, const float* bias, const 
         double best = -INFINITY;
         int at = kMaxExperts;
         for (int e = lane; e < E; e += 32) {
-            if (!(kept >> (e / gsize) & 1)) continue;
-            const double c = bias ? choice(e) : double(widen(xrow[e]));  // s rises with x
-            const bool after = last < 0 || c < bound || (c == bound && e > last);
-            if (after && (at == kMaxExperts || c > best)) {
-                best = c;
+            if (!((kept >> (e / gsize)) & 1)) continue;
+            const double v = bias ? c[e >> 5] : double(widen(xrow[e]));  // s rises with x
+            const bool after = last < 0 || v < bound || (v == bound && e > last);
+            if (after && (at == kMaxExperts || v > best)) {
+                best = v;
                 at = e;
             }
         }
@@ -190,21 +203,204 @@ __device__ __noinline__ int choose_wide(const T* xrow, const float* bias, const 
     return mine;
 }
 
+// A lane's place: its group, its experts base .. base + count - 1.
+struct Place {
+    int group, base, count;
+    __device__ __forceinline__ explicit Place(const Shape& sh) {
+        const int lane = threadIdx.x & 31, gsize = sh.experts / sh.groups;
+        group = lane / sh.lanes;
+        const int first = (lane % sh.lanes) * sh.per_lane;  // within the group
+        base = group * gsize + first;
+        count = group < sh.groups ? max(0, min(sh.per_lane, gsize - first)) : 0;
+    }
+};
+
+// Largest two values over the lanes of a group.
+__device__ __forceinline__ void group_top2(const Shape& sh, float& a, float& b) {
+    for (int o = sh.lanes / 2; o > 0; o >>= 1) {
+        const float oa = __shfl_xor_sync(kFullMask, a, o), ob = __shfl_xor_sync(kFullMask, b, o);
+        b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+        a = fmaxf(a, oa);
+    }
+}
+
+// Whether this lane's group, of the given value, takes part; `near` is set when
+// values at the border are closer than `slack` + |value| 2^-21.
+__device__ __forceinline__ bool group_keep(const Shape& sh, int group, float value, float slack,
+                                           bool exact, bool& near) {
+    const uint32_t gkey = group < sh.groups ? order_key(value + 0.f) : 0u;
+    int rank = 0;
+    for (int g = 0; g < sh.groups; ++g) {
+        const uint32_t o = __shfl_sync(kFullMask, gkey, g * sh.lanes);
+        rank += o > gkey || (o == gkey && g < group);
+    }
+    const bool keep = group < sh.groups && rank < sh.topk_groups;
+    if (!exact) {
+        const float low = key_value(warp_min(keep ? gkey : 0xffffffffu));
+        const uint32_t out = warp_max(keep ? 0u : gkey);
+        if (out != 0u) {
+            const float high = key_value(out);
+            if (high != -INFINITY && !(low - high > slack + fabsf(low) * 0x1p-21f)) near = true;
+        }
+    }
+    return keep;
+}
+
+// The choice with c in fp32; returns and arguments as choose_wide.
+template <typename T, int N>
+__device__ __noinline__ int choose_exact(const T* xrow, const float* bias, const Shape sh) {
+    const int lane = threadIdx.x & 31, E = sh.experts;
+    const Place at_(sh);
+    const int base = at_.base, count = at_.count;
+    const bool by_score = bias != nullptr;
+    const bool pair_sum = sh.groups > 1 && sh.group_top == 2;
+    float v[N];
+    load_run<T, N, false>(xrow + base, count, v);
+    float m = 0.f, inv_d = 1.f;
+    if (!sh.sigmoid) {
+        m = v[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+        m = key_value(warp_max(order_key(m + 0.f)));
+        const float ref = m == -INFINITY ? 0.f : m;
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) d += v[i] == -INFINITY ? 0.f : exp1(v[i] - ref);
+        d = warp_sum(d);
+        inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
+    }
+    auto score = [&](float xv) {
+        if (xv == -INFINITY) return 0.f;
+        return sh.sigmoid ? sigmoid(xv) : exp1(xv - m) * inv_d;
+    };
+    const float err = (sh.sigmoid ? 1.f : inv_d) * 0x1p-19f;  // twice the bound of a score
+
+    // the value that is compared, as an order key; 0 = takes no part
+    uint32_t key[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float c = v[i];
+        if (by_score && v[i] != -INFINITY) c = score(v[i]) + bias[i < count ? base + i : 0];
+        key[i] = i < count ? order_key(c + 0.f) : 0u;
+    }
+    bool wide = false;
+    if (sh.groups > 1) {
+        float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i < count) {
+                float c = key_value(key[i]);
+                if (pair_sum && !by_score) c = v[i] == -INFINITY ? -INFINITY : score(v[i]);
+                b = fmaxf(b, fminf(a, c));
+                a = fmaxf(a, c);
+            }
+        }
+        group_top2(sh, a, b);
+        if (!group_keep(sh, at_.group, pair_sum ? a + b : a, 2.f * err, !(by_score || pair_sum), wide)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) key[i] = 0u;
+        }
+    }
+
+    // K rounds: this lane's best, then the warp's
+    uint32_t best = 0u;
+    int at = 0;
+    auto local_best = [&]() {
+        best = 0u;
+        at = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+    };
+    local_best();
+    int mine = 0;
+    float prev_c = 0.f, prev_x = 0.f, prev_b = 0.f;
+    for (int k = 0; k < sh.K; ++k) {
+        const uint32_t top = warp_max(best);
+        const int src = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
+        const int e = min(__shfl_sync(kFullMask, base + at, src), E - 1);
+        if (lane == k) mine = e;
+        if (by_score) {
+            const float c = key_value(top), be = bias[e], xv = widen(xrow[e]);
+            if (k > 0 && c != -INFINITY && !(prev_c - c > err + fabsf(prev_c) * 0x1p-22f) &&
+                !(xv == prev_x && be == prev_b))
+                wide = true;
+            prev_c = c;
+            prev_x = xv;
+            prev_b = be;
+        }
+        if (lane == src) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i == at) key[i] = 0u;
+            local_best();
+        }
+    }
+    if (by_score && prev_c != -INFINITY) {
+        // experts left out that are too near the last one taken
+        const float border = prev_c - (err + fabsf(prev_c) * 0x1p-22f);
+        bool near = false;
+        if (best != 0u && !(key_value(best) < border)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (key[i] != 0u && !(key_value(key[i]) < border) &&
+                    !(v[i] == prev_x && bias[base + i] == prev_b))
+                    near = true;
+        }
+        wide = wide || __any_sync(kFullMask, near);
+    }
+    return wide ? choose_wide<T>(xrow, bias, sh, m) : mine;
+}
+
+// Descending order of N (a power of two, at most 8) values by a network.
+template <int N>
+__device__ __forceinline__ void sort_run(int (&k)[N]) {
+#pragma unroll
+    for (int width = 2; width <= N; width *= 2)
+#pragma unroll
+        for (int step = width / 2; step > 0; step /= 2)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if ((i & step) == 0) {
+                    const int a = k[i], b = k[i + step];
+                    const bool down = (i & width) == 0;
+                    k[i] = down ? max(a, b) : min(a, b);
+                    k[i + step] = down ? min(a, b) : max(a, b);
+                }
+}
+
+// Signed order key of a float, and back.
+__device__ __forceinline__ int signed_key(float v) {
+    const int b = __float_as_int(v);
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float signed_value(int k) {
+    return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
+constexpr int kNone = INT_MIN;             // takes no part; below every key
+constexpr int kMissing = int(0x80800000u);  // keys of -inf are below this
+
 // N: experts per lane, rounded up to a power of two.
 template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32)
 route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __restrict__ weights,
              int* __restrict__ idx, int64_t rows, const Shape sh) {
     const int lane = threadIdx.x & 31;
-    const int E = sh.experts, gsize = E / sh.groups;
-    const int group = lane / sh.lanes;
-    const int first = (lane % sh.lanes) * sh.per_lane;  // within the group
-    const int base = group * gsize + first;
-    const int count = group < sh.groups ? max(0, min(sh.per_lane, gsize - first)) : 0;
+    const int E = sh.experts;
+    const Place at(sh);
+    const int base = at.base, count = at.count;
     const bool by_score = bias != nullptr;  // else logits give the order
     // the softmax's maximum and sum are needed for its scores themselves
     const bool pair_sum = sh.groups > 1 && sh.group_top == 2;
-    const bool need_sum = !sh.sigmoid && (by_score || pair_sum || !sh.renorm);
+    const bool need_scores = by_score || pair_sum;
+    const bool need_sum = !sh.sigmoid && (need_scores || !sh.renorm);
+    const int low_bits = sh.index_mask;  // of a key: the expert, counted down
+    float be[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) be[i] = by_score && i < count ? bias[base + i] : 0.f;
 
     for (int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < rows;
          row += int64_t(gridDim.x) * kWarps) {
@@ -217,139 +413,118 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
 #pragma unroll
             for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
             m = key_value(warp_max(order_key(m + 0.f)));
-            if (need_sum) {
-                const float ref = m == -INFINITY ? 0.f : m;
-                float d = 0.f;
+        }
+        float s[N];  // scores, where they are compared
+        if (need_sum) {
+            const float ref = m == -INFINITY ? 0.f : m;
+            float d = 0.f;
 #pragma unroll
-                for (int i = 0; i < N; ++i) d += v[i] == -INFINITY ? 0.f : exp1(v[i] - ref);
-                d = warp_sum(d);
-                inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
+            for (int i = 0; i < N; i += 2) {
+                const float2 e = exp_pair<false>(
+                    make_float2(v[i] - ref, i + 1 < N ? v[i + 1] - ref : -INFINITY));
+                s[i] = e.x;
+                if (i + 1 < N) s[i + 1] = e.y;
+                d += e.x + e.y;
             }
-        }
-        auto score = [&](float xv) {
-            if (xv == -INFINITY) return 0.f;
-            return sh.sigmoid ? sigmoid(xv) : exp1(xv - m) * inv_d;
-        };
-        const float s_max = sh.sigmoid ? 1.f : inv_d;
-        const float err = s_max * 0x1p-19f;  // twice the bound of a score
-
-        // ---- the value that is compared, as an order key; 0 = takes no part
-        uint32_t key[N];
+            d = warp_sum(d);
+            inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float c = v[i];
-            if (by_score && v[i] != -INFINITY) c = score(v[i]) + bias[i < count ? base + i : 0];
-            key[i] = i < count ? order_key(c + 0.f) : 0u;
+            for (int i = 0; i < N; ++i) s[i] *= inv_d;
+        } else if (need_scores) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                s[i] = rcp_sfu(1.f + ex2_sfu(-expc::kLog2e * v[i]));
         }
-        bool wide = false;
+        const float err = (sh.sigmoid ? 1.f : inv_d) * 0x1p-19f;  // twice the bound of a score
+
+        float c[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            c[i] = by_score && v[i] != -INFINITY ? s[i] + be[i] : v[i];
+        bool unsure = false, keep = true;
         if (sh.groups > 1) {
             float a = -INFINITY, b = -INFINITY;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 if (i < count) {
-                    float c = key_value(key[i]);
-                    if (pair_sum && !by_score) c = v[i] == -INFINITY ? -INFINITY : score(v[i]);
-                    b = fmaxf(b, fminf(a, c));
-                    a = fmaxf(a, c);
+                    const float g = pair_sum && !by_score && v[i] != -INFINITY ? s[i] : c[i];
+                    b = fmaxf(b, fminf(a, g));
+                    a = fmaxf(a, g);
                 }
             }
-            for (int o = sh.lanes / 2; o > 0; o >>= 1) {
-                const float oa = __shfl_xor_sync(kFullMask, a, o), ob = __shfl_xor_sync(kFullMask, b, o);
-                b = fmaxf(fminf(a, oa), fmaxf(b, ob));
-                a = fmaxf(a, oa);
-            }
-            const float value = pair_sum ? a + b : a;
-            const uint32_t gkey = group < sh.groups ? order_key(value + 0.f) : 0u;
-            int rank = 0;
-            for (int g = 0; g < sh.groups; ++g) {
-                const uint32_t o = __shfl_sync(kFullMask, gkey, g * sh.lanes);
-                rank += o > gkey || (o == gkey && g < group);
-            }
-            const bool keep = group < sh.groups && rank < sh.topk_groups;
-            if (!keep) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) key[i] = 0u;
-            }
-            if (by_score || pair_sum) {
-                const float low = key_value(warp_min(keep ? gkey : 0xffffffffu));
-                const uint32_t out = warp_max(keep ? 0u : gkey);
-                if (out != 0u) {
-                    const float high = key_value(out);
-                    if (high != -INFINITY && !(low - high > 2.f * err + fabsf(low) * 0x1p-21f))
-                        wide = true;
-                }
-            }
+            group_top2(sh, a, b);
+            keep = group_keep(sh, at.group, pair_sum ? a + b : a, 2.f * err, !need_scores, unsure);
         }
-
-        // ---- K rounds: this lane's best, then the warp's
-        uint32_t best = 0u;
-        int at = 0;
-        auto local_best = [&]() {
-            best = 0u;
-            at = 0;
+        int key[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at = i;
-                }
+        for (int i = 0; i < N; ++i)
+            key[i] = keep && i < count
+                         ? ((signed_key(c[i] + 0.f) & ~low_bits) | (low_bits - (base + i)))
+                         : kNone;
+
+        // ---- K rounds: lane k takes slot k's key; `next` is the best left out
+        if constexpr (N <= 8) sort_run<N>(key);
+        auto lane_best = [&]() {
+            int best = key[0];
+            if constexpr (N > 8) {
+#pragma unroll
+                for (int i = 1; i < N; ++i) best = max(best, key[i]);
+            }
+            return best;
         };
-        local_best();
-        int mine = 0;
-        float xm = -INFINITY, prev_c = 0.f, prev_x = 0.f, prev_b = 0.f;
+        int mine = kNone;
         for (int k = 0; k < sh.K; ++k) {
-            const uint32_t top = warp_max(best);
-            const int src = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
-            float xv = 0.f;
+            const int best = lane_best();
+            const int top = __reduce_max_sync(kFullMask, best);
+            if (lane == k) mine = top;
+            if (best == top) {  // one lane: keys differ in their experts
+                if constexpr (N <= 8) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i == at) xv = v[i];
-            xv = __shfl_sync(kFullMask, xv, src);
-            const int e = min(__shfl_sync(kFullMask, base + at, src), E - 1);
-            if (lane == k) {
-                mine = e;
-                xm = xv;
+                    for (int i = 0; i + 1 < N; ++i) key[i] = key[i + 1];
+                    key[N - 1] = kNone;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        if (key[i] == top) key[i] = kNone;
+                }
             }
+        }
+        const int next = __reduce_max_sync(kFullMask, lane_best());
+
+        // ---- is the order certain?  lane k compares slots k and k + 1, lane
+        // K - 1 its slot with what is left out
+        int e = min(low_bits - (mine & low_bits), E - 1);
+        float xm = lane < sh.K ? widen(xrow[e]) : -INFINITY;
+        if (by_score || sizeof(T) == 4) {
+            int after = __shfl_down_sync(kFullMask, mine, 1);
+            if (lane == sh.K - 1) after = next;
+            bool near;
             if (by_score) {
-                const float c = key_value(top), be = bias[e];
-                if (k > 0 && c != -INFINITY && !(prev_c - c > err + fabsf(prev_c) * 0x1p-22f) &&
-                    !(xv == prev_x && be == prev_b))
-                    wide = true;
-                prev_c = c;
-                prev_x = xv;
-                prev_b = be;
+                const float va = signed_value(mine & ~low_bits), vb = signed_value(after & ~low_bits);
+                near = !(va - vb > err + (fabsf(va) + fabsf(vb)) * float(low_bits + 2) * 0x1p-23f);
+            } else {
+                near = (mine & ~low_bits) == (after & ~low_bits);
             }
-            if (lane == src) {
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (i == at) key[i] = 0u;
-                local_best();
+            near = near && lane < sh.K && after >= kMissing;
+            if (__any_sync(kFullMask, near)) {
+                // equal logits of equal bias stand in the order of their experts
+                const float b = by_score ? bias[e] : 0.f;
+                const float xa = __shfl_down_sync(kFullMask, xm, 1);
+                const float ba = __shfl_down_sync(kFullMask, b, 1);
+                if (near && (lane == sh.K - 1 || xa != xm || ba != b)) unsure = true;
             }
         }
-        if (by_score && prev_c != -INFINITY) {
-            // experts left out that are too near the last one taken
-            const float border = prev_c - (err + fabsf(prev_c) * 0x1p-22f);
-            bool near = false;
-            if (best != 0u && !(key_value(best) < border)) {
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (key[i] != 0u && !(key_value(key[i]) < border) &&
-                        !(v[i] == prev_x && bias[base + i] == prev_b))
-                        near = true;
-            }
-            wide = wide || __any_sync(kFullMask, near);
-        }
-        if (wide) {
-            float mw = m;
-            mine = choose_wide<T>(xrow, bias, sh, mw);
-            xm = lane < sh.K ? widen(xrow[mine]) : -INFINITY;
+        if (__any_sync(kFullMask, unsure)) {
+            e = choose_exact<T, N>(xrow, bias, sh);
+            xm = lane < sh.K ? widen(xrow[e]) : -INFINITY;
         }
 
-        // ---- weights: lane k holds slot k
+        // ---- weights
         const bool live = lane < sh.K && xm != -INFINITY;
         float w;
         if (!sh.renorm) {
-            w = live ? score(xm) : 0.f;
+            w = sh.sigmoid ? sigmoid(xm) : exp1(xm - m) * inv_d;
+            if (!live) w = 0.f;
         } else {
             // relative to the largest chosen logit, so that no sum underflows
             float top = key_value(warp_max(order_key((live ? xm : -INFINITY) + 0.f)));
@@ -366,7 +541,7 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
         }
         if (lane < sh.K) {
             weights[row * sh.K + lane] = w * sh.scale;
-            idx[row * sh.K + lane] = mine;
+            idx[row * sh.K + lane] = e;
         }
     }
 }
@@ -385,6 +560,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 route_bwd_kernel(const T* __restrict__ x, const int* __restrict__ idx,
                  const float* __restrict__ dweights, T* __restrict__ dx, int64_t rows,
                  const Shape sh) {
+    __shared__ alignas(16) float buffer[N <= 2 ? 1 : kWarps][N <= 2 ? 1 : 32 * N];
     const int lane = threadIdx.x & 31;
     const int E = sh.experts;
     const int base = lane * sh.per_lane;
@@ -454,12 +630,52 @@ route_bwd_kernel(const T* __restrict__ x, const int* __restrict__ idx,
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] = 0.f;
         }
-        for (int k = 0; k < sh.K; ++k) {
-            const int ek = __shfl_sync(kFullMask, e, k) - base;
-            const float add = __shfl_sync(kFullMask, slot, k);
+        if constexpr (N <= 2) {
+            for (int k = 0; k < sh.K; ++k) {
+                const int ek = __shfl_sync(kFullMask, e, k) - base;
+                const float add = __shfl_sync(kFullMask, slot, k);
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i == ek) v[i] += add;
+                for (int i = 0; i < N; ++i)
+                    if (i == ek) v[i] += add;
+            }
+        } else {
+            // every lane's run into shared memory, the slots' parts added there
+            // (one by one where an expert is named twice, so that the order of
+            // the sum is fixed), and the runs back
+            float* mine = buffer[threadIdx.x >> 5];
+            if constexpr (VEC) {
+#pragma unroll
+                for (int i = 0; i < N; i += 4)
+                    *reinterpret_cast<float4*>(mine + base + i) =
+                        make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (i < count) mine[base + i] = v[i];
+            }
+            __syncwarp();
+            const uint32_t same = __match_any_sync(kFullMask, e >= 0 ? e : -1 - lane);
+            if (!__any_sync(kFullMask, __popc(same) > 1)) {
+                if (e >= 0) mine[e] += slot;
+            } else {
+                for (int k = 0; k < sh.K; ++k) {
+                    if (lane == k && e >= 0) mine[e] += slot;
+                    __syncwarp();
+                }
+            }
+            __syncwarp();
+            if constexpr (VEC) {
+#pragma unroll
+                for (int i = 0; i < N; i += 4) {
+                    const float4 t = *reinterpret_cast<const float4*>(mine + base + i);
+                    v[i] = t.x, v[i + 1] = t.y, v[i + 2] = t.z, v[i + 3] = t.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (i < count) v[i] = mine[base + i];
+            }
+            __syncwarp();
         }
         T* drow = dx + row * E + base;
         if constexpr (VEC) {

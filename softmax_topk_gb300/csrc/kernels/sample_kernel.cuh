@@ -56,31 +56,20 @@ constexpr int kBins = 2048;   // steps of the top-p histogram
 constexpr int kTopK = 1024;   // top-k up to here is settled on a list
 using u64 = unsigned long long;
 
-// 2^(j/64) in two fp32 parts, j = 0..63
-__device__ const float2 kPow2[64] = {
-    {1.f, 0.f}, {0x1.02c9a4p+0f, -0x1.887fap-28f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f},
-    {0x1.087452p+0f, -0x1.e2990ep-26f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f}, {0x1.0e3ec4p+0f, -0x1.a585ccp-25f},
-    {0x1.11301ep+0f, -0x1.fdb496p-25f}, {0x1.1429aap+0f, 0x1.d525bcp-25f}, {0x1.172b84p+0f, -0x1.c15742p-27f},
-    {0x1.1a35bep+0f, 0x1.6df96ep-25f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f}, {0x1.2063b8p+0f, 0x1.0c519ap-25f},
-    {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.26b456p+0f, 0x1.789f38p-26f}, {0x1.29e9ep+0f, -0x1.5c0424p-25f},
-    {0x1.2d285ap+0f, 0x1.b900c2p-26f}, {0x1.306fep+0f, 0x1.4636e2p-25f}, {0x1.33c08cp+0f, -0x1.b37d2p-25f},
-    {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.3a7db4p+0f, -0x1.634c02p-25f}, {0x1.3dea64p+0f, 0x1.824684p-25f},
-    {0x1.4160a2p+0f, 0x1.f72e2ap-28f}, {0x1.44e086p+0f, 0x1.8624b4p-30f}, {0x1.486a2cp+0f, -0x1.47d866p-25f},
-    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.4f9b28p+0f, -0x1.2c5a6cp-25f}, {0x1.5342b6p+0f, -0x1.2c561p-25f},
-    {0x1.56f474p+0f, -0x1.295b04p-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f}, {0x1.5e76f2p+0f, -0x1.4a5bd6p-25f},
-    {0x1.6247ecp+0f, -0x1.f8b55p-25f}, {0x1.662388p+0f, 0x1.2a9112p-27f}, {0x1.6a09e6p+0f, 0x1.9fcef4p-26f},
-    {0x1.6dfb24p+0f, -0x1.cd72e8p-27f}, {0x1.71f75ep+0f, 0x1.1d8beep-25f}, {0x1.75feb6p+0f, -0x1.37b306p-25f},
-    {0x1.7a1148p+0f, -0x1.829fdp-25f}, {0x1.7e2f34p+0f, -0x1.261634p-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f},
-    {0x1.868d9ap+0f, -0x1.2edb44p-26f}, {0x1.8ace54p+0f, 0x1.15506ep-27f}, {0x1.8f1aeap+0f, -0x1.baa232p-26f},
-    {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.97d82ap+0f, -0x1.0d8d84p-31f}, {0x1.9c4918p+0f, 0x1.51f848p-27f},
-    {0x1.a0c668p+0f, -0x1.2886a6p-26f}, {0x1.a5503cp+0f, -0x1.b83b54p-25f}, {0x1.a9e6b6p+0f, -0x1.50c048p-25f},
-    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b33a2cp+0f, -0x1.ec3a82p-26f}, {0x1.b7f77p+0f, -0x1.a09438p-25f},
-    {0x1.bcc1eap+0f, -0x1.f687c6p-25f}, {0x1.c199bep+0f, -0x1.3d56b2p-27f}, {0x1.c67f12p+0f, 0x1.cafa2ap-25f},
-    {0x1.cb720ep+0f, -0x1.8837ccp-27f}, {0x1.d072d4p+0f, 0x1.40f13p-25f}, {0x1.d5818ep+0f, -0x1.822dbcp-27f},
-    {0x1.da9e6p+0f, 0x1.ed9942p-27f}, {0x1.dfc974p+0f, -0x1.908c94p-25f}, {0x1.e502eep+0f, 0x1.e2cffep-26f},
-    {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.efa1bep+0f, 0x1.cc2b44p-25f}, {0x1.f50766p+0f, -0x1.246ebp-26f},
-    {0x1.fa7c18p+0f, 0x1.9e90d8p-28f},
-};
+// 2^(j/32) in two fp32 parts, j = 0..31: the high parts, then the low ones
+__device__ const float kPow2[64] = {
+    0x1p+0f, 0x1.059b0ep+0f, 0x1.0b5586p+0f, 0x1.11301ep+0f, 0x1.172b84p+0f, 0x1.1d4874p+0f,
+    0x1.2387a6p+0f, 0x1.29e9ep+0f, 0x1.306fep+0f, 0x1.371a74p+0f, 0x1.3dea64p+0f, 0x1.44e086p+0f,
+    0x1.4bfdaep+0f, 0x1.5342b6p+0f, 0x1.5ab07ep+0f, 0x1.6247ecp+0f, 0x1.6a09e6p+0f, 0x1.71f75ep+0f,
+    0x1.7a1148p+0f, 0x1.82589ap+0f, 0x1.8ace54p+0f, 0x1.93737cp+0f, 0x1.9c4918p+0f, 0x1.a5503cp+0f,
+    0x1.ae89fap+0f, 0x1.b7f77p+0f, 0x1.c199bep+0f, 0x1.cb720ep+0f, 0x1.d5818ep+0f, 0x1.dfc974p+0f,
+    0x1.ea4afap+0f, 0x1.f50766p+0f,
+    0.f, -0x1.9d4f52p-25f, 0x1.9f3122p-25f, -0x1.fdb496p-25f, -0x1.c15742p-27f, -0x1.d2e8cap-25f,
+    0x1.ceac48p-25f, -0x1.5c0424p-25f, 0x1.4636e2p-25f, -0x1.18aac6p-25f, 0x1.824684p-25f, 0x1.8624b4p-30f,
+    -0x1.593abcp-25f, -0x1.2c561p-25f, -0x1.5bd5ecp-27f, -0x1.f8b55p-25f, 0x1.9fcef4p-26f, 0x1.1d8beep-25f,
+    -0x1.829fdp-25f, -0x1.accc7cp-26f, 0x1.15506ep-27f, -0x1.e64744p-25f, 0x1.51f848p-27f, -0x1.b83b54p-25f,
+    -0x1.a94b14p-26f, -0x1.a09438p-25f, -0x1.3d56b2p-27f, -0x1.8837ccp-27f, -0x1.822dbcp-27f, -0x1.908c94p-25f,
+    0x1.52486cp-27f, -0x1.246ebp-26f};
 
 struct Settings {
     const float* temperature;
@@ -107,41 +96,82 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 constexpr uint32_t kKeyNegInf = 0x007fffffu;  // order_key(-inf)
 
 // A row's weight function: w(x) = e^((x - m) / T) as a multiple of 2^-bits.
+//
+// (x - m) 32 log2 e / T = 32 n + j + g, |g| <= 1/2 and 2^(g/32) = e^y with
+// y = g ln 2 / 32; w = 2^n 2^(j/32) (1 + (e^y - 1)).  Every product whose
+// rounding would show at 2^-38 carries its residual, and the two parts of w are
+// turned into integers by adding a constant whose last bit is their unit (all
+// on the FMA and integer pipes: the conversion instructions run at an eighth
+// of their rate, 256 rows of 128256 columns took 141 us with them).
 struct Weight {
-    float m, c_hi, c_lo;  // maximum; log2 e / T in two parts
+    float m, c_hi, c_lo;  // maximum; 32 log2 e / T in two parts
+    float unit;           // 1.5 * 2^(23 - bits): its last bit is 2^-bits
     int bits;             // 31..44
-    const float2* table;  // kPow2 in shared memory
+    const float* table;   // kPow2 in shared memory
 
-    // (x - m) log2 e / T = n + j/64 + g, |g| <= 1/128; 2^g - 1 = e^y - 1 with
-    // y = g ln 2 = y_h + y_l; every product whose rounding would show at 2^-38
-    // carries its residual.
-    __device__ __forceinline__ u64 operator()(float x) const {
-        if (x == m) return 1ull << bits;
+    __device__ __forceinline__ void set(float m_, double temperature, int bits_, const float* t) {
+        m = m_;
+        const double c = fmin(46.166241308446829036 / temperature, 1e30);
+        c_hi = float(c);
+        c_lo = float(c - double(c_hi));
+        bits = bits_;
+        unit = 1.5f * __int_as_float((23 - bits + 127) << 23);
+        table = t;
+    }
+
+    // w = hi 2^-22 + lo 2^-bits
+    __device__ __forceinline__ void parts(float x, uint32_t& hi, int& lo) const {
         const float dh = x - m;
         const float bb = dh - x;
         const float dl = (x - (dh - bb)) + (-m - bb);  // x - m = dh + dl exactly
-        const float th = dh * c_hi;
-        if (!(th > -60.f)) return 0;  // below 2^-60, -inf
+        const float th = __fmul_rn(dh, c_hi);  // its residual is added below
         const float tl = fmaf(dh, c_hi, -th) + fmaf(dh, c_lo, dl * c_hi);
-        const float uf = fmaf(th, 64.f, expc::kRound);
-        const float un = uf - expc::kRound;
-        const float gh = fmaf(un, -0x1p-6f, th);
+        const float uf = th + expc::kRound;
+        const float gh = th - (uf - expc::kRound);
         const float g = gh + tl;
         const float gl = tl - (g - gh);
-        const float yh = g * 0x1.62e43p-1f;
-        const float yl = fmaf(g, 0x1.62e43p-1f, -yh) + fmaf(g, -0x1.05c61p-29f, gl * 0x1.62e43p-1f);
+        constexpr float kL = 0x1.62e43p-6f, kLLo = -0x1.05c61p-34f;  // ln 2 / 32
+        const float yh = __fmul_rn(g, kL);
+        const float yl = fmaf(g, kL, -yh) + fmaf(gl, kL, g * kLLo);
         const float poly = fmaf(yh, fmaf(yh, 0x1.555556p-5f, 0x1.555556p-3f), 0.5f);
-        const float r = fmaf(yh * yh, poly, yl);
-        const int i = __float_as_int(uf) - __float_as_int(expc::kRound);
-        const float2 t = table[i & 63];
-        const float wh = fmaf(t.x, yh, t.x);
-        const float wl = fmaf(t.x, r, fmaf(t.x, yh, t.x - wh) + fmaf(t.y, yh, t.y));
-        const float s = __int_as_float(((i >> 6) + 24 + 127) << 23);  // 2^(n + 24)
-        const float i1 = rintf(wh * s);
-        const float rest = fmaf(wh, s, -i1) + wl * s;
-        const float i2 = rintf(rest * __int_as_float((bits - 24 + 127) << 23));
-        const long long w = (static_cast<long long>(__float2int_rn(i1)) << (bits - 24)) + __float2int_rn(i2);
-        return w > 0 ? static_cast<u64>(w) : 0ull;
+        const float q = __fmul_rn(yh * yh, poly);
+        const float eh = yh + q, el = (q - (eh - yh)) + yl;  // e^y - 1
+        const int i = __float_as_int(uf);  // the constant's bits are a multiple of 32
+        const float t = table[i & 31], t_lo = table[32 + (i & 31)];
+        const float wh = fmaf(t, eh, t);
+        const float wl = fmaf(t, el, fmaf(t, eh, t - wh) + fmaf(t_lo, eh, t_lo));
+        // 2^n: n is the constant's distance, moved to the exponent field
+        const float s = __int_as_float(((i & ~31) << 18) + 0x3f800000);
+        const float big = fmaf(wh, s, 3.f);  // last bit 2^-22
+        const float rest = fmaf(wl, s, fmaf(wh, s, -(big - 3.f)));
+        hi = __float_as_uint(big) - __float_as_uint(3.f);
+        lo = __float_as_int(rest + unit) - __float_as_int(unit);
+        if (!(th > -1920.f)) hi = 0, lo = 0;           // below 2^-60, -inf
+        if (x == m) hi = 1u << 22, lo = 0;             // also m = +inf
+    }
+    __device__ __forceinline__ u64 join(uint32_t hi, int lo) const {
+        const long long w = static_cast<long long>(u64(hi) << (bits - 22)) + lo;
+        return w > 0 ? u64(w) : 0;
+    }
+    __device__ __forceinline__ u64 operator()(float x) const {
+        uint32_t hi;
+        int lo;
+        parts(x, hi, lo);
+        return join(hi, lo);
+    }
+    // the weights of N columns, those with keep[i] alone
+    template <int N>
+    __device__ __forceinline__ u64 sum(const float (&v)[N], const bool (&keep)[N]) const {
+        uint32_t hi = 0;
+        int lo = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint32_t h;
+            int l;
+            parts(v[i], h, l);
+            if (keep[i]) hi += h, lo += l;
+        }
+        return static_cast<u64>(static_cast<long long>(u64(hi) << (bits - 22)) + lo);
     }
 };
 
@@ -169,7 +199,7 @@ struct alignas(8) Cut {
 };
 
 struct Shared {
-    float2 table[64];
+    float table[64];
     // exchanged over the cluster, one value per warp
     uint32_t top[kWarps], bound[kWarps];
     u64 sum[kWarps];    // weights of a warp's run
@@ -531,15 +561,8 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
         bound = __reduce_min_sync(kFullMask, bound);
 
         Weight w;
-        w.m = key_value(top_key);
-        w.bits = bits;
-        w.table = sh.table;
         const bool greedy = !(t_row > 0.f);
-        {
-            const double c = greedy ? 1.0 : fmin(1.4426950408889634074 / double(t_row), 1e30);
-            w.c_hi = float(c);
-            w.c_lo = float(c - double(w.c_hi));
-        }
+        w.set(key_value(top_key), greedy ? 1.0 : double(t_row), bits, sh.table);
         // the lowest logit that min-p keeps; compared in fp32 it decides as in
         // real arithmetic, since it is rounded up
         float floor_p = -FLT_MAX;
@@ -636,8 +659,10 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                 for (int64_t b = lo + lane; b < hi; b += 32) {
                     float v[EPV];
                     blocks.load(b, v);
+                    bool all[EPV];
 #pragma unroll
-                    for (int i = 0; i < EPV; ++i) mine += w(v[i]);
+                    for (int i = 0; i < EPV; ++i) all[i] = true;
+                    mine += w.sum(v, all);
                 }
                 mine = warp_sum64(mine);
                 if (lane == 0) sh.sum[warp] = mine;
@@ -748,12 +773,20 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
             auto block_weight = [&](int64_t b) {
                 float v[EPV];
                 blocks.load(b, v);
-                u64 a = 0;
+                bool keep[EPV], any = false;
 #pragma unroll
-                for (int i = 0; i < EPV; ++i) a += kept_weight(v[i], blocks.col(b) + i);
+                for (int i = 0; i < EPV; ++i) any |= keep[i] = cut.keeps(v[i], blocks.col(b) + i);
+                if (!any) return u64(0);
+                u64 a = w.sum(v, keep);
+                if (uu == 0.f) {
+                    a = 0;
+#pragma unroll
+                    for (int i = 0; i < EPV; ++i) a += kept_weight(v[i], blocks.col(b) + i);
+                }
                 return a;
             };
             u64 mine = 0;
+#pragma unroll 2
             for (int64_t b = lo + lane; b < hi; b += 32) mine += block_weight(b);
             mine = warp_sum64(mine);
             if (lane == 0) sh.draw[warp] = mine;

@@ -21,6 +21,7 @@ Shape make_shape(const RouteArgs& a, int groups) {
     s.lanes = 1;
     while (s.lanes * 2 * groups <= 32) s.lanes *= 2;
     s.per_lane = (a.experts / groups + s.lanes - 1) / s.lanes;
+    s.index_mask = pow2_at_least(a.experts) - 1;
     s.sigmoid = a.score == OS_SCORE_SIGMOID;
     s.renorm = a.renorm;
     s.scale = a.scale;
@@ -40,8 +41,9 @@ int64_t grid_for(int64_t rows) { return min64(ceil_div(rows, route::kWarps), int
 template <typename T, int N>
 cudaError_t launch_fwd(const RouteArgs& a, const Shape& s, float* weights, int32_t* idx,
                        cudaStream_t stream) {
-    auto k = whole_runs(s, N, sizeof(T), a.x, a.x) ? route::route_kernel<T, N, true>
-                                                   : route::route_kernel<T, N, false>;
+    auto k = route::route_kernel<T, N, false>;
+    if constexpr (N <= 32)  // groups of 33 to 64 experts to a lane never fill it
+        if (whole_runs(s, N, sizeof(T), a.x, a.x)) k = route::route_kernel<T, N, true>;
     return launch_kernel(k, grid_for(a.rows), route::kWarps * 32, 1, 0, stream,
                          static_cast<const T*>(a.x), a.bias, weights, reinterpret_cast<int*>(idx),
                          a.rows, s);
