@@ -159,17 +159,82 @@ struct Weight {
         parts(x, hi, lo);
         return join(hi, lo);
     }
-    // the weights of N columns, those with keep[i] alone
+    // Whether parts2 holds: the row's values clamped at least() are finite and
+    // the clamp, as rounded, is still far below every weight that counts.
+    __device__ __forceinline__ bool plain() const {
+        return c_hi > 1e-30f && fabsf(m) < 1e30f && fabsf(least()) < 1e30f &&
+               (m - least()) * c_hi > 1600.f;
+    }
+    // weights below this are 0 (2^-60); a lower x may stand in for any lower one
+    __device__ __forceinline__ float least() const { return m - 1920.f / c_hi; }
+
+    // parts() of two values at a time on packed fp32 pairs, for x in [least(), m]
+    // and plain() rows; negated values save the sign changes that the packed
+    // forms lack.
+    __device__ __forceinline__ void parts2(float2 x, uint32_t (&hi)[2], int (&lo)[2]) const {
+        const float2 minus = splat2(-1.f), nm = splat2(-m), ch = splat2(c_hi), K = splat2(expc::kRound);
+        const float2 dh = add2(x, nm);
+        const float2 bb = fma2(x, minus, dh);
+        const float2 d1 = fma2(bb, minus, dh);
+        const float2 d2 = fma2(d1, minus, x);
+        const float2 dl = add2(d2, fma2(bb, minus, nm));
+        const float2 nth = mul2(dh, splat2(-c_hi));
+        const float2 tl = add2(fma2(dh, ch, nth), fma2(dh, splat2(c_lo), mul2(dl, ch)));
+        const float2 uf = fma2(nth, minus, K);
+        const float2 ngh = add2(nth, fma2(K, minus, uf));
+        const float2 g = fma2(ngh, minus, tl);
+        const float2 gl = fma2(add2(g, ngh), minus, tl);
+        constexpr float kL = 0x1.62e43p-6f, kLLo = -0x1.05c61p-34f;  // ln 2 / 32
+        const float2 nyh = mul2(g, splat2(-kL));
+        const float2 yl = add2(fma2(g, splat2(kL), nyh), fma2(gl, splat2(kL), mul2(g, splat2(kLLo))));
+        float2 poly = fma2(nyh, splat2(-0x1.555556p-5f), splat2(0x1.555556p-3f));
+        poly = fma2(nyh, mul2(poly, minus), splat2(0.5f));
+        const float2 q = mul2(mul2(nyh, nyh), poly);
+        const float2 eh = fma2(nyh, minus, q);
+        const float2 el = add2(fma2(add2(eh, nyh), minus, q), yl);
+        const int i0 = __float_as_int(uf.x), i1 = __float_as_int(uf.y);
+        const float2 t = make_float2(table[i0 & 31], table[i1 & 31]);
+        const float2 t_lo = make_float2(table[32 + (i0 & 31)], table[32 + (i1 & 31)]);
+        const float2 wh = fma2(t, eh, t);
+        const float2 wl = fma2(t, el, add2(fma2(t, eh, fma2(wh, minus, t)), fma2(t_lo, eh, t_lo)));
+        const float2 s = make_float2(__int_as_float(((i0 & ~31) << 18) + 0x3f800000),
+                                     __int_as_float(((i1 & ~31) << 18) + 0x3f800000));
+        const float2 big = fma2(wh, s, splat2(3.f));
+        const float2 rest = fma2(wl, s, fma2(wh, s, fma2(big, minus, splat2(3.f))));
+        const float2 end = add2(rest, splat2(unit));
+        hi[0] = __float_as_uint(big.x) - __float_as_uint(3.f);
+        hi[1] = __float_as_uint(big.y) - __float_as_uint(3.f);
+        lo[0] = __float_as_int(end.x) - __float_as_int(unit);
+        lo[1] = __float_as_int(end.y) - __float_as_int(unit);
+    }
+
+    // The summed weights of N values of at least `from` (finite); `fast` rows
+    // are plain() ones.
     template <int N>
-    __device__ __forceinline__ u64 sum(const float (&v)[N], const bool (&keep)[N]) const {
+    __device__ __forceinline__ u64 sum_from(const float (&v)[N], float from, bool fast) const {
         uint32_t hi = 0;
         int lo = 0;
+        if (fast) {
+            const float clamp = least();
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            uint32_t h;
-            int l;
-            parts(v[i], h, l);
-            if (keep[i]) hi += h, lo += l;
+            for (int i = 0; i < N; i += 2) {
+                uint32_t h[2];
+                int l[2];
+                parts2(make_float2(fmaxf(v[i], clamp), fmaxf(v[i + 1], clamp)), h, l);
+                if (v[i] >= from) hi += h[0], lo += l[0];
+                if (v[i + 1] >= from) hi += h[1], lo += l[1];
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) {
+                float x = v[0];
+#pragma unroll
+                for (int j = 1; j < N; ++j) x = j == i ? v[j] : x;
+                uint32_t h;
+                int l;
+                parts(x, h, l);
+                if (x >= from) hi += h, lo += l;
+            }
         }
         return static_cast<u64>(static_cast<long long>(u64(hi) << (bits - 22)) + lo);
     }
@@ -549,7 +614,12 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
             sh.top[warp] = warp_top;
             sh.bound[warp] = bound;
         }
-        if (tid == 0) sh.listed = 0;
+        if (tid == 0) {
+            sh.listed = 0;
+            sh.bin = kBins - 1;
+            sh.above = 0;
+            sh.cut = {-FLT_MAX, INT_MAX};
+        }
         row_sync<S>();
         uint32_t top_key = 0;
         bound = 0xffffffffu;
@@ -563,6 +633,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
         Weight w;
         const bool greedy = !(t_row > 0.f);
         w.set(key_value(top_key), greedy ? 1.0 : double(t_row), bits, sh.table);
+        const bool fast = w.plain();
         // the lowest logit that min-p keeps; compared in fp32 it decides as in
         // real arithmetic, since it is rounded up
         float floor_p = -FLT_MAX;
@@ -659,10 +730,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                 for (int64_t b = lo + lane; b < hi; b += 32) {
                     float v[EPV];
                     blocks.load(b, v);
-                    bool all[EPV];
-#pragma unroll
-                    for (int i = 0; i < EPV; ++i) all[i] = true;
-                    mine += w.sum(v, all);
+                    mine += w.sum_from(v, -FLT_MAX, fast);
                 }
                 mine = warp_sum64(mine);
                 if (lane == 0) sh.sum[warp] = mine;
@@ -764,7 +832,9 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
         }
 
         if (!done) {
-            // ---- the draw, in column order
+            // ---- the draw, in column order; column by column where the cut goes
+            // through equal logits or every kept column counts (u = 0)
+            const bool by_column = cut.last != INT_MAX || uu == 0.f;
             auto kept_weight = [&](float v, int64_t c) -> u64 {
                 if (!cut.keeps(v, c)) return 0;
                 const u64 a = w(v);
@@ -773,15 +843,19 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
             auto block_weight = [&](int64_t b) {
                 float v[EPV];
                 blocks.load(b, v);
-                bool keep[EPV], any = false;
+                if (!by_column) return w.sum_from(v, cut.value, fast);
+                u64 a = 0;
+                bool any = false;
 #pragma unroll
-                for (int i = 0; i < EPV; ++i) any |= keep[i] = cut.keeps(v[i], blocks.col(b) + i);
-                if (!any) return u64(0);
-                u64 a = w.sum(v, keep);
-                if (uu == 0.f) {
-                    a = 0;
+                for (int i = 0; i < EPV; ++i) any |= v[i] >= cut.value;
+                if (any) {
+#pragma unroll 1
+                    for (int j = 0; j < EPV; ++j) {
+                        float y = v[0];
 #pragma unroll
-                    for (int i = 0; i < EPV; ++i) a += kept_weight(v[i], blocks.col(b) + i);
+                        for (int i = 1; i < EPV; ++i) y = i == j ? v[i] : y;
+                        a += kept_weight(y, blocks.col(b) + j);
+                    }
                 }
                 return a;
             };
@@ -835,16 +909,21 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                                 float v[EPV];
                                 blocks.load(b0 + lane, v);
                                 u64 run = end - a;
+                                int64_t pick = 0;
+                                float x_pick = w.m;
                                 bool open = true;
 #pragma unroll
                                 for (int i = 0; i < EPV; ++i) {
                                     const int64_t c = blocks.col(b0 + lane) + i;
-                                    run += kept_weight(v[i], c);
-                                    if (open && run > target) {
-                                        write(c, v[i], total);
-                                        open = false;
+                                    const u64 a_i = kept_weight(v[i], c);
+                                    if (open && a_i > 0) {
+                                        pick = c;
+                                        x_pick = v[i];
+                                        run += a_i;
+                                        open = run <= target;
                                     }
                                 }
+                                write(pick, x_pick, total);
                             }
                             break;
                         }
