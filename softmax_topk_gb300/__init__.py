@@ -243,12 +243,15 @@ def _dtype_code(t) -> int:
 
 
 def _stream_handle(x) -> int:
+    """The handle of torch's current stream on x's device (without building a Stream object,
+    which costs the host 2 us a call)."""
     import torch
-    return torch.cuda.current_stream(x.device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(x.device.index)
 
 
 class _OnDevice:
     """Make x's device current for the call (a no-op when it already is)."""
+    __slots__ = ("index", "prev")
 
     def __init__(self, device):
         self.index = device.index
@@ -398,11 +401,10 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, out=Non
 
 def _like(name, t, shape, dtype, device):
     """An output or optional input: `t` when it fits, a new tensor when it is None."""
-    import torch
     if t is None:
+        import torch
         return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device \
-            or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
                          f"on {device}")
     return t

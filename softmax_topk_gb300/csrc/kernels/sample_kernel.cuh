@@ -208,6 +208,32 @@ struct Weight {
         lo[1] = __float_as_int(end.y) - __float_as_int(unit);
     }
 
+    // add(v, weight) for each of N values of at least `least_in`, and the summed
+    // weights of the others.
+    template <int N, typename Add>
+    __device__ __forceinline__ u64 hist(const float (&v)[N], float least_in, bool fast, Add add) const {
+        uint32_t hi = 0;
+        int lo = 0;
+        const float clamp = fast ? least() : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            uint32_t h[2];
+            int l[2];
+            if (fast) {
+                parts2(make_float2(fmaxf(v[i], clamp), fmaxf(v[i + 1], clamp)), h, l);
+            } else {
+                parts(fmaxf(v[i], clamp), h[0], l[0]);
+                parts(fmaxf(v[i + 1], clamp), h[1], l[1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (v[i + j] >= least_in) add(v[i + j], join(h[j], l[j]));
+                else hi += h[j], lo += l[j];
+            }
+        }
+        return static_cast<u64>(static_cast<long long>(u64(hi) << (bits - 22)) + lo);
+    }
+
     // The summed weights of N values of at least `from` (finite); `fast` rows
     // are plain() ones.
     template <int N>
@@ -267,14 +293,15 @@ struct Shared {
     float table[64];
     // exchanged over the cluster, one value per warp
     uint32_t top[kWarps], bound[kWarps];
-    u64 sum[kWarps];    // weights of a warp's run
+    float near[kWarps];  // weights of a warp's run, in fp32
+    u64 sum[kWarps];     // weights of a warp's run outside the histogram
     u64 draw[kWarps];   // kept weights of a warp's run
     u64 piece[kWarps];  // kept weights of a piece of the border's run
     // rank 0's findings, read by the others
     uint32_t listed;    // columns put on the list (it may be more than fit)
     uint32_t bin;       // the border's step of the histogram
     Cut cut;
-    u64 above;
+    u64 above, want;
     // scratch of one CTA
     u64 warp[kWarps];
     u64 result[2];
@@ -536,20 +563,27 @@ struct Blocks {
         count = (int64_t(head) + cols + EPV - 1) / EPV;
     }
     __device__ __forceinline__ int64_t col(int64_t b) const { return b * EPV - head; }
+    __device__ __forceinline__ bool whole(int64_t b) const {
+        return col(b) >= 0 && col(b) + EPV <= cols;
+    }
+    __device__ __forceinline__ uint4 words(int64_t b) const {
+        return __ldg(reinterpret_cast<const uint4*>(base) + b);
+    }
+    // a NaN stays one: it fails every comparison and is passed over by maxima
     __device__ __forceinline__ void load(int64_t b, float (&v)[EPV]) const {
         const int64_t c = col(b);
-        if (c >= 0 && c + EPV <= cols) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(base) + b);
+        if (whole(b)) {
+            const uint4 w = words(b);
             const uint32_t a[4] = {w.x, w.y, w.z, w.w};
             if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = fmaxf(__uint_as_float(a[i]), -INFINITY);
+                for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(a[i]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 f = unpack_bf16x2(a[i]);
-                    v[2 * i] = fmaxf(f.x, -INFINITY);
-                    v[2 * i + 1] = fmaxf(f.y, -INFINITY);
+                    v[2 * i] = f.x;
+                    v[2 * i + 1] = f.y;
                 }
             }
         } else {
@@ -557,6 +591,37 @@ struct Blocks {
             for (int i = 0; i < EPV; ++i)
                 v[i] = c + i >= 0 && c + i < cols ? widen(base[b * EPV + i]) : -INFINITY;
         }
+    }
+    // The largest value of the blocks b, b + 32, ... below `end`.
+    __device__ __forceinline__ float maximum(int64_t b, int64_t end) const {
+        float top = -INFINITY;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll 4
+            for (; b < end; b += 32) {
+                float v[EPV];
+                load(b, v);
+                top = fmaxf(max3(top, v[0], v[1]), fmaxf(v[2], v[3]));
+            }
+        } else {
+            __nv_bfloat162 best = __float2bfloat162_rn(-INFINITY);
+#pragma unroll 4
+            for (; b < end; b += 32) {
+                if (whole(b)) {
+                    const uint4 w = words(b);
+                    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        best = __hmax2(best, *reinterpret_cast<const __nv_bfloat162*>(&a[i]));
+                } else {
+                    float v[EPV];
+                    load(b, v);
+#pragma unroll
+                    for (int i = 0; i < EPV; ++i) top = fmaxf(top, v[i]);
+                }
+            }
+            top = fmaxf(top, fmaxf(__low2float(best), __high2float(best)));
+        }
+        return top;
     }
 };
 
@@ -581,25 +646,19 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
         const float mp = s.min_p ? s.min_p[row] : s.min_p_all;
         float uu = u[row] > 0.f ? fminf(u[row], 0x1.fffffep-1f) : 0.f;
         const bool by_k = k > 0 && k < cols;
-        const bool list_k = by_k && k <= kTopK && k <= S * kThreads;
+        // warps with a whole run: those whose thread maxima bound the k-th best
+        const int full = int(blocks.count / per_warp);
+        const bool list_k = by_k && k <= kTopK && k <= 32 * full;
 
         // ---- the only pass over memory: maxima per thread
-        float top = -INFINITY;
-#pragma unroll 4
-        for (int64_t b = lo + lane; b < hi; b += 32) {
-            float v[EPV];
-            blocks.load(b, v);
-#pragma unroll
-            for (int i = 0; i < EPV; ++i) top = fmaxf(top, v[i]);
-        }
-        uint32_t key = order_key(top);
+        uint32_t key = order_key(blocks.maximum(lo + lane, hi));
         const uint32_t warp_top = __reduce_max_sync(kFullMask, key);
-        uint32_t bound = 0;
-        if (list_k) {
-            // every warp's j-th best thread maximum, j = ceil(k / warps): the
-            // smallest of them is reached by j threads in every warp, so by k
-            // elements.  The lanes' keys are sorted descending to find it.
-            const int j = (k + S * kWarps - 1) / (S * kWarps);
+        uint32_t bound = 0xffffffffu;
+        if (list_k && rank * kWarps + warp < full) {
+            // every such warp's j-th best thread maximum, j = ceil(k / warps):
+            // the smallest of them is reached by j threads in every warp, so by
+            // k elements.  The lanes' keys are sorted descending to find it.
+            const int j = (k + full - 1) / full;
 #pragma unroll
             for (int width = 2; width <= 32; width *= 2)
 #pragma unroll
@@ -616,9 +675,8 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
         }
         if (tid == 0) {
             sh.listed = 0;
-            sh.bin = kBins - 1;
-            sh.above = 0;
-            sh.cut = {-FLT_MAX, INT_MAX};
+            sh.bin = kBins;  // none
+            sh.cut = {NAN, 0};
         }
         row_sync<S>();
         uint32_t top_key = 0;
@@ -725,43 +783,58 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                     }
                 }
             } else if (!by_k && tp < 1.f) {
-                // ---- top-p: the border by a histogram of weight
-                u64 mine = 0;
-                for (int64_t b = lo + lane; b < hi; b += 32) {
-                    float v[EPV];
-                    blocks.load(b, v);
-                    mine += w.sum_from(v, -FLT_MAX, fast);
+                // ---- top-p: the border by a histogram of weight.  A total in
+                // fp32 (to 1e-4, the slack below) says how far down it may lie:
+                // columns of at most (1 - p) total / cols cannot reach it even
+                // together.
+                float near = 0.f;
+                {
+                    const float c = w.c_hi * 0.03125f;
+#pragma unroll 2
+                    for (int64_t b = lo + lane; b < hi; b += 32) {
+                        float v[EPV];
+                        blocks.load(b, v);
+                        float part = 0.f;
+#pragma unroll
+                        for (int i = 0; i < EPV; ++i)
+                            part += v[i] >= -FLT_MAX ? ex2_sfu((v[i] - w.m) * c) : 0.f;
+                        near += part;
+                    }
                 }
-                mine = warp_sum64(mine);
-                if (lane == 0) sh.sum[warp] = mine;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) near += __shfl_xor_sync(kFullMask, near, o);
+                if (lane == 0) sh.near[warp] = near;
                 for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0;
                 row_sync<S>();
-                u64 total = 0;
+                near = 0.f;
                 for (int i = lane; i < S * kWarps; i += 32)
-                    total += remote<S>(&sh.sum[i % kWarps], i / kWarps);
-                total = warp_sum64(total);
-                const u64 want = share_of(fmaxf(tp, 0.f), total);
-                // columns of at most this weight cannot reach the border even
-                // together; `low` is at or below their logits
-                const u64 small = (total - want) / u64(cols);
-                double low = -FLT_MAX;
-                if (small > 0)
-                    low = double(w.m) +
-                          double(t_row) * (log(double(small)) - double(bits) * 0.69314718055994530942);
+                    near += remote<S>(&sh.near[i % kWarps], i / kWarps);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) near += __shfl_xor_sync(kFullMask, near, o);
+                const float pc = fmaxf(tp, 0.f);
+                const double small = (1.0 - double(pc)) * double(near) * 0.999 / double(cols);
+                double low = double(w.m) + double(t_row) * log(small);
                 low -= 1e-6 * (fabs(low) + fabs(double(w.m)) + double(t_row));
                 const float least = fmaxf(float(low), -FLT_MAX);
                 const float steps = float(kBins) / (w.m - least);
                 if (w.m < INFINITY && steps > 0.f && steps < INFINITY) {
                     auto step_of = [&](float v) { return min(kBins - 1, int((w.m - v) * steps)); };
+                    u64 rest = 0;
                     for (int64_t b = lo + lane; b < hi; b += 32) {
                         float v[EPV];
                         blocks.load(b, v);
-#pragma unroll
-                        for (int i = 0; i < EPV; ++i)
-                            if (v[i] >= least) atomicAdd(&sh.mass[step_of(v[i])], w(v[i]));
+                        rest += w.hist(v, least, fast, [&](float y, u64 a) {
+                            atomicAdd(&sh.mass[step_of(y)], a);
+                        });
                     }
+                    rest = warp_sum64(rest);
+                    if (lane == 0) sh.sum[warp] = rest;
                     row_sync<S>();
                     if (rank == 0) {
+                        u64 total = 0;
+                        for (int i = lane; i < S * kWarps; i += 32)
+                            total += remote<S>(&sh.sum[i % kWarps], i / kWarps);
+                        total = warp_sum64(total);
                         u64 part[kBins / kThreads], own = 0;
 #pragma unroll
                         for (int i = 0; i < kBins / kThreads; ++i) {
@@ -771,6 +844,9 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                             own += part[i];
                         }
                         const u64 upto = cta_prefix(sh, own);
+                        if (tid == kThreads - 1) sh.result[0] = upto;
+                        __syncthreads();
+                        const u64 want = share_of(pc, total + sh.result[0]);
                         u64 run = upto - own;
                         if (run < want && want <= upto) {
                             int i = 0;
@@ -778,10 +854,11 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                             sh.bin = kBins / kThreads * tid + i;
                             sh.above = run;
                         }
+                        if (tid == 0) sh.want = want;
                     }
                     row_sync<S>();
                     const int bin = int(remote<S>(&sh.bin, 0));
-                    for (int64_t b = lo + lane; b < hi; b += 32) {
+                    for (int64_t b = bin < kBins ? lo + lane : hi; b < hi; b += 32) {
                         float v[EPV];
                         blocks.load(b, v);
 #pragma unroll
@@ -791,8 +868,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                     }
                     row_sync<S>();
                     const uint32_t n = remote<S>(&sh.listed, 0);
-                    if (n <= kList) {
-                        settled = true;
+                    if (n > 0 && n <= kList) {
                         if (rank == 0) {
                             sort_list(sh, int(n));
                             constexpr int P = kList / kThreads;
@@ -803,7 +879,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                                 a[i] = at < int(n) ? w(key_value(uint32_t(sh.sorted[at] >> 32))) : 0;
                                 own += a[i];
                             }
-                            const u64 upto = cta_prefix(sh, own) + sh.above;
+                            const u64 upto = cta_prefix(sh, own) + sh.above, want = sh.want;
                             u64 run = upto - own;
                             if (run < want && want <= upto) {
                                 int i = 0;
@@ -815,6 +891,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                         }
                         row_sync<S>();
                         cut = remote<S>(&sh.cut, 0);
+                        settled = cut.value == cut.value;  // found
                     }
                 }
             }
@@ -832,9 +909,11 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
         }
 
         if (!done) {
-            // ---- the draw, in column order; column by column where the cut goes
-            // through equal logits or every kept column counts (u = 0)
-            const bool by_column = cut.last != INT_MAX || uu == 0.f;
+            // ---- the draw, in column order; column by column where every kept
+            // column counts (u = 0).  Columns at the cut and past its last one
+            // are summed with the rest and taken off again.
+            const bool by_column = uu == 0.f;
+            const u64 w_cut = cut.last != INT_MAX ? w(cut.value) : 0;
             auto kept_weight = [&](float v, int64_t c) -> u64 {
                 if (!cut.keeps(v, c)) return 0;
                 const u64 a = w(v);
@@ -843,8 +922,16 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
             auto block_weight = [&](int64_t b) {
                 float v[EPV];
                 blocks.load(b, v);
-                if (!by_column) return w.sum_from(v, cut.value, fast);
                 u64 a = 0;
+                if (!by_column) {
+                    a = w.sum_from(v, cut.value, fast);
+                    if (cut.last != INT_MAX) {
+#pragma unroll
+                        for (int i = 0; i < EPV; ++i)
+                            if (v[i] == cut.value && blocks.col(b) + i > cut.last) a -= w_cut;
+                    }
+                    return a;
+                }
                 bool any = false;
 #pragma unroll
                 for (int i = 0; i < EPV; ++i) any |= v[i] >= cut.value;
