@@ -17,7 +17,7 @@ cudaError_t launch_side(const CUtensorMap& mx, const CUtensorMap& my, const CUte
                         void* out2, int64_t bh, int n, float scale, bool causal,
                         const KernelCtl& ctl, cudaStream_t stream) {
     auto k = attn_bwd::attention_bwd_kernel<D, KV>;
-    constexpr int smem = attn_bwd::Layout<D>::kDynBytes;
+    constexpr int smem = attn_bwd::Layout<D>::kBytes;
     if (!prepare_kernel(k, 1, smem)) return cudaErrorInvalidConfiguration;
     const DeviceInfo* dev = device_info();
     if (!dev) return cudaErrorInvalidDevice;

@@ -25,9 +25,9 @@
 //   * load warp: TMA tiled loads of the resident pair once per item and of the
 //     streamed pairs through a ring of stages;
 //   * MMA warp (one lane): the products, accumulators in tensor memory.  A
-//     product that overwrites what an earlier one reads (A1 lies over P, A2
-//     over dS) is issued after that one's completion was seen;
-//   * stat warp (KV only): the streamed rows' (L log2e, delta) into shared
+//     product that overwrites what an earlier one reads is issued after that
+//     one's completion was seen;
+//   * stat warp (KV only): the streamed rows' -L log2e and -delta into shared
 //     memory, L = +inf for rows past the end so that their P is 0;
 //   * eight compute warps: thread (r, h) owns tile row r (one tensor-memory
 //     lane) and half h of its columns: P = 2^(A1 scale log2e - L log2e) to
@@ -35,6 +35,15 @@
 //     product (both read from tensor memory as the A operand), fp32 in between.
 //     The two roundings to bf16 are the price of the bf16 tensor cores, as P's
 //     is in the forward; sums are fp32.
+//
+// Tensor memory (512 columns): A1, A2 and, with KV and D = 128, two sums of
+// 128 columns each leave no room for P and dS of their own.  A1 is read into
+// registers at once and so is free for the next tile's scores while this
+// tile's exponentials run; P and dS are written over A2, half by half, after
+// the thread has read its part.  So only A2 of the next tile has to wait for
+// this tile's two sums, and that wait passes under the next exponentials.
+// Without KV dS alternates between two buffers where the second sum would be,
+// and A2 waits for its readers only.
 #pragma once
 
 #include <cuda.h>
@@ -58,34 +67,44 @@ constexpr int kMmaWarp = 9;
 constexpr int kStatWarp = 10;
 constexpr int kThreads = 352;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kA1 = 0;         // A1 (fp32, 128 columns); P in its columns 0-31 and 64-95
-constexpr uint32_t kA2 = 128;       // A2 (fp32, 128 columns); dS likewise
+constexpr uint32_t kA1 = 0;         // A1 (fp32, 128 columns)
+constexpr uint32_t kA2 = 128;       // A2 (fp32, 128 columns)
 constexpr uint32_t kAcc1 = 256;     // dK or dQ, D columns
 constexpr uint32_t kAcc2 = 384;     // dV, D columns
+// bf16 operands, 32 columns for tile columns 0-63 and 32 for 64-127, 64 apart
+constexpr uint32_t kP = kA2;        // KV: over A2
+constexpr uint32_t kDs = kA2 + 32;  // KV: over A2
+constexpr uint32_t kDs2 = 384;      // without KV: tile g at kDs2 + 32 (g & 1)
 constexpr float kLog2e = 1.442695041f;
 
+// One stage more for U than for W: U of a tile is read twice, by its first and
+// its last product, W is done with earlier.  At D = 128 that fills the SM's
+// shared memory to the last kilobyte, so the barriers live in it too.
 template <int D>
 struct Layout {
-    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kUStages = D == 128 ? 3 : 4;
+    static constexpr int kWStages = D == 128 ? 2 : 4;
     static constexpr int kBlock = kRows * 64 * 2;  // 16 KB: 128 rows of 64 bf16
     static constexpr int kTile = kRows * D * 2;
     static constexpr int kX = 0;
     static constexpr int kY = kX + kTile;
-    static constexpr int kU = kY + kTile;               // kStages buffers
-    static constexpr int kW = kU + kStages * kTile;     // kStages buffers
-    static constexpr int kStat = kW + kStages * kTile;  // 2 x (128 L log2e, 128 delta)
-    static constexpr int kBytes = kStat + 2 * 2 * kRows * 4;
-    static constexpr int kDynBytes = kBytes + 1024;
+    static constexpr int kU = kY + kTile;               // kUStages buffers
+    static constexpr int kW = kU + kUStages * kTile;    // kWStages buffers
+    static constexpr int kStat = kW + kWStages * kTile;  // 2 x (128 -L log2e, 128 -delta)
+    static constexpr int kBars = kStat + 2 * 2 * kRows * 4;
+    static constexpr int kBytes = kBars + 512;
 };
 
-template <int STAGES>
+template <int D>
 struct Barriers {
+    using L = Layout<D>;
     uint64_t x_full, x_empty;                      // resident pair landed / its products done
-    uint64_t u_full[STAGES], w_full[STAGES];       // streamed tile landed
-    uint64_t uw_empty[STAGES];                     // every product reading the stage done
+    uint64_t u_full[L::kUStages], u_empty[L::kUStages];  // streamed tile landed / read
+    uint64_t w_full[L::kWStages], w_empty[L::kWStages];
     uint64_t a1_full, a2_full;                     // A1 / A2 of a tile in tensor memory
+    uint64_t a1_free;                              // A1 is in registers (all compute threads)
     uint64_t p_full, ds_full;                      // P / dS in tensor memory (all compute threads)
-    uint64_t pw_done, acc_done;                    // acc2 += P W / acc1 += dS U completed
+    uint64_t acc_done[2];                          // sums of tile g (at g & 1) completed
     uint64_t acc_empty;                            // an item's sums are in registers
     uint64_t stat_full[2], stat_empty[2];          // the streamed rows' statistics there / read
     uint64_t drain;
@@ -146,28 +165,32 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                      __nv_bfloat16* __restrict__ out2, int n, int nt, int units, float scale,
                      int causal_flag, KernelCtl ctl) {
     using L = Layout<D>;
-    constexpr int STAGES = L::kStages;
-    extern __shared__ unsigned char dyn_raw[];
-    unsigned char* smem = reinterpret_cast<unsigned char*>(
-        (reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ Barriers<STAGES> bars;
+    constexpr int US = L::kUStages, WS = L::kWStages;
+    static_assert(sizeof(Barriers<D>) <= L::kBytes - L::kBars, "barriers");
+    // no static shared memory: the dynamic part starts on a 1024-byte boundary
+    extern __shared__ __align__(1024) unsigned char smem[];
+    Barriers<D>& bars = *reinterpret_cast<Barriers<D>*>(smem + L::kBars);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool causal = causal_flag != 0;
 
     if (tid == 0) {
         mbar_init(&bars.x_full, 1);
         mbar_init(&bars.x_empty, 1);
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < US; ++s) {
             mbar_init(&bars.u_full[s], 1);
+            mbar_init(&bars.u_empty[s], 1);
+        }
+        for (int s = 0; s < WS; ++s) {
             mbar_init(&bars.w_full[s], 1);
-            mbar_init(&bars.uw_empty[s], 1);
+            mbar_init(&bars.w_empty[s], 1);
         }
         mbar_init(&bars.a1_full, 1);
         mbar_init(&bars.a2_full, 1);
         mbar_init(&bars.p_full, kCompute);
         mbar_init(&bars.ds_full, kCompute);
-        mbar_init(&bars.pw_done, 1);
-        mbar_init(&bars.acc_done, 1);
+        mbar_init(&bars.a1_free, kCompute);
+        mbar_init(&bars.acc_done[0], 1);
+        mbar_init(&bars.acc_done[1], 1);
         mbar_init(&bars.acc_empty, kCompute);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars.stat_full[s], 32);
@@ -193,7 +216,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
             umma::prefetch_tensormap(&map_u);
             umma::prefetch_tensormap(&map_w);
             Waiter wait(ctl);
-            int g = 0, it = 0;
+            int g = 0, nu = 0, it = 0;  // tiles of W and of U, items so far
             for (int u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
                 int bh, ta, tb;
                 const int cnt = attn::work_unit(u, nt, causal, bh, ta, tb);
@@ -213,34 +236,35 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                                           tile * kRows, bh, &bars.x_full);
                     }
                     for (int j = 0; j < count; ++j) {
-                        const int st = g % STAGES;
-                        if (g >= STAGES) wait(&bars.uw_empty[st], (g / STAGES - 1) & 1);
+                        const int us = g % US, ws = g % WS;
+                        if (g >= US) wait(&bars.u_empty[us], (g / US - 1) & 1);
                         if (!wait.ok) break;
-                        ++g;
-                        mbar_arrive_expect_tx(&bars.u_full[st], L::kTile);
+                        mbar_arrive_expect_tx(&bars.u_full[us], L::kTile);
 #pragma unroll
                         for (int blk = 0; blk < D / 64; ++blk)
-                            umma::tma_load_3d(smem + L::kU + st * L::kTile + blk * L::kBlock,
+                            umma::tma_load_3d(smem + L::kU + us * L::kTile + blk * L::kBlock,
                                               &map_u, 64 * blk, (first + j) * kRows, bh,
-                                              &bars.u_full[st]);
-                        mbar_arrive_expect_tx(&bars.w_full[st], L::kTile);
+                                              &bars.u_full[us]);
+                        ++nu;
+                        if (g >= WS) wait(&bars.w_empty[ws], (g / WS - 1) & 1);
+                        if (!wait.ok) break;
+                        mbar_arrive_expect_tx(&bars.w_full[ws], L::kTile);
 #pragma unroll
                         for (int blk = 0; blk < D / 64; ++blk)
-                            umma::tma_load_3d(smem + L::kW + st * L::kTile + blk * L::kBlock,
+                            umma::tma_load_3d(smem + L::kW + ws * L::kTile + blk * L::kBlock,
                                               &map_w, 64 * blk, (first + j) * kRows, bh,
-                                              &bars.w_full[st]);
+                                              &bars.w_full[ws]);
+                        ++g;
                     }
                 }
             }
             // no copy may land after this CTA has gone
             if (it > 0)
                 mbar_wait_bounded_ns(&bars.x_full, (it - 1) & 1, kDrainTimeoutNs, ctl.err);
-            for (int k = g > STAGES ? g - STAGES : 0; k < g; ++k) {
-                mbar_wait_bounded_ns(&bars.u_full[k % STAGES], (k / STAGES) & 1, kDrainTimeoutNs,
-                                     ctl.err);
-                mbar_wait_bounded_ns(&bars.w_full[k % STAGES], (k / STAGES) & 1, kDrainTimeoutNs,
-                                     ctl.err);
-            }
+            for (int k = nu > US ? nu - US : 0; k < nu; ++k)
+                mbar_wait_bounded_ns(&bars.u_full[k % US], (k / US) & 1, kDrainTimeoutNs, ctl.err);
+            for (int k = g > WS ? g - WS : 0; k < g; ++k)
+                mbar_wait_bounded_ns(&bars.w_full[k % WS], (k / WS) & 1, kDrainTimeoutNs, ctl.err);
         }
     } else if (warp == kMmaWarp) {
         if (lane == 0) {
@@ -257,8 +281,8 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                                    umma::desc_sw128(b_addr + koff, 16, 1024), id_a, s > 0);
                 }
             };
-            // acc (128 x D) += P or dS (tensor memory, columns 0-63 of the
-            // tile at `src`, 64-127 at src + 64) times a streamed tile
+            // acc (128 x D) += P or dS (tensor memory, tile columns 0-63 at
+            // `src`, 64-127 at src + 64) times a streamed tile
             auto accumulate = [&](uint32_t dst, uint32_t src, uint32_t b_addr, bool keep) {
 #pragma unroll
                 for (int s = 0; s < kRows / 16; ++s)
@@ -267,24 +291,26 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                                           id_acc, keep || s > 0);
             };
             auto issue_a1 = [&](int g) {
-                const int st = g % STAGES;
-                wait(&bars.u_full[st], (g / STAGES) & 1);
-                // A1 lies over P of tile g - 1: its product must have read it
-                if (KV && g > 0) wait(&bars.pw_done, (g - 1) & 1);
+                const int us = g % US;
+                wait(&bars.u_full[us], (g / US) & 1);
+                if (g > 0) wait(&bars.a1_free, (g - 1) & 1);
                 if (!wait.ok) return;
                 umma::fence_after_sync();
-                product(kA1, x_addr, smem_addr(smem + L::kU + st * L::kTile));
+                product(kA1, x_addr, smem_addr(smem + L::kU + us * L::kTile));
                 umma::commit(&bars.a1_full);
             };
-            auto issue_a2 = [&](int g) {
-                const int st = g % STAGES;
-                wait(&bars.w_full[st], (g / STAGES) & 1);
-                // A2 lies over dS of tile g - 1
-                if (g > 0) wait(&bars.acc_done, (g - 1) & 1);
+            auto issue_a2 = [&](int g, bool last) {
+                const int ws = g % WS;
+                wait(&bars.w_full[ws], (g / WS) & 1);
+                // over P and dS of tile g - 1 (without KV its readers are done:
+                // they have arrived on ds_full)
+                if (KV && g > 0) wait(&bars.acc_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
                 if (!wait.ok) return;
                 umma::fence_after_sync();
-                product(kA2, y_addr, smem_addr(smem + L::kW + st * L::kTile));
+                product(kA2, y_addr, smem_addr(smem + L::kW + ws * L::kTile));
                 umma::commit(&bars.a2_full);
+                if (!KV) umma::commit(&bars.w_empty[ws]);
+                if (last) umma::commit(&bars.x_empty);  // the last reader of X and Y
             };
             int g = 0, it = 0;
             for (int u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
@@ -295,28 +321,28 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                     tile_range<KV>(e == 0 ? ta : tb, nt, causal, first, count);
                     wait(&bars.x_full, it & 1);
                     issue_a1(g);
-                    issue_a2(g);
+                    issue_a2(g, count == 1);
                     for (int j = 0; j < count && wait.ok; ++j, ++g) {
-                        const int st = g % STAGES;
-                        wait(&bars.p_full, g & 1);
+                        const int us = g % US, ws = g % WS;
+                        if (j + 1 < count) issue_a1(g + 1);
                         // the first products of an item overwrite the sums
                         if (j == 0 && it > 0) wait(&bars.acc_empty, (it - 1) & 1);
-                        if (!wait.ok) break;
                         if (KV) {
+                            wait(&bars.p_full, g & 1);
+                            if (!wait.ok) break;
                             umma::fence_after_sync();
-                            accumulate(kAcc2, kA1, smem_addr(smem + L::kW + st * L::kTile), j > 0);
-                            umma::commit(&bars.pw_done);
+                            accumulate(kAcc2, kP, smem_addr(smem + L::kW + ws * L::kTile), j > 0);
+                            umma::commit(&bars.w_empty[ws]);
                         }
-                        if (j + 1 < count) issue_a1(g + 1);
                         wait(&bars.ds_full, g & 1);
                         if (!wait.ok) break;
                         umma::fence_after_sync();
-                        accumulate(kAcc1, kA2, smem_addr(smem + L::kU + st * L::kTile), j > 0);
-                        umma::commit(&bars.acc_done);
-                        umma::commit(&bars.uw_empty[st]);
-                        if (j + 1 < count) issue_a2(g + 1);
+                        accumulate(kAcc1, KV ? kDs : kDs2 + 32 * (g & 1),
+                                   smem_addr(smem + L::kU + us * L::kTile), j > 0);
+                        umma::commit(&bars.acc_done[g & 1]);
+                        umma::commit(&bars.u_empty[us]);
+                        if (j + 1 < count) issue_a2(g + 1, j + 2 == count);
                     }
-                    if (wait.ok) umma::commit(&bars.x_empty);
                 }
             }
             // no product may be in flight when tensor memory is given back
@@ -341,9 +367,9 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int q = base + lane + 32 * i;
-                            lv[i] = q < n ? lrow[q] * kLog2e : INFINITY;
-                            dv[i] = q < n ? drow[q] : 0.f;
-                            if (lv[i] == -INFINITY) lv[i] = INFINITY;
+                            lv[i] = q < n ? -lrow[q] * kLog2e : -INFINITY;
+                            dv[i] = q < n ? -drow[q] : 0.f;
+                            if (lv[i] == INFINITY) lv[i] = -INFINITY;
                         }
                         // buffer g & 1 was last read for tile g - 2
                         if (g >= 2) wait(&bars.stat_empty[g & 1], ((g - 2) >> 1) & 1);
@@ -374,24 +400,25 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                 int first, count;
                 tile_range<KV>(tile, nt, causal, first, count);
                 const int row = tile * kRows + r;
-                float row_l = INFINITY, row_delta = 0.f;
+                float row_l = -INFINITY, row_delta = 0.f;  // negated
                 if (!KV && row < n) {
-                    row_l = lse[int64_t(bh) * n + row] * kLog2e;
-                    if (row_l == -INFINITY) row_l = INFINITY;
-                    row_delta = delta[int64_t(bh) * n + row];
+                    row_l = -lse[int64_t(bh) * n + row] * kLog2e;
+                    if (row_l == INFINITY) row_l = -INFINITY;
+                    row_delta = -delta[int64_t(bh) * n + row];
                 }
                 for (int j = 0; j < count; ++j, ++g) {
                     const int col0 = (first + j) * kRows + 64 * half;
                     const float* stat =
                         reinterpret_cast<const float*>(smem + L::kStat) + (g & 1) * 2 * kRows + 64 * half;
                     float p[64];
-                    uint32_t pk[32];
                     wait(&bars.a1_full, g & 1);
                     umma::fence_after_sync();
                     umma::tmem_ld32(a1, p);
                     umma::tmem_ld32(a1 + 32, p + 32);
                     if (KV) wait(&bars.stat_full[g & 1], (g >> 1) & 1);
                     umma::tmem_wait_ld();
+                    umma::fence_before_sync();
+                    umma::mbar_arrive(&bars.a1_free);
                     // columns [lo, hi) of this half take part: keys up to the
                     // end and the query (KV = false), queries from the key on
                     // (KV = true; queries past the end have L = +inf)
@@ -407,41 +434,62 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                         float4 l4;
                         if (KV) l4 = *reinterpret_cast<const float4*>(stat + c);
                         else l4 = make_float4(row_l, row_l, row_l, row_l);
-                        p[c] = ex2_sfu(fmaf(p[c], scale_log2, -l4.x));
-                        p[c + 1] = ex2_sfu(fmaf(p[c + 1], scale_log2, -l4.y));
-                        p[c + 2] = ex2_sfu(fmaf(p[c + 2], scale_log2, -l4.z));
-                        p[c + 3] = ex2_sfu(fmaf(p[c + 3], scale_log2, -l4.w));
+                        const float2 za = fma2(make_float2(p[c], p[c + 1]), splat2(scale_log2),
+                                               make_float2(l4.x, l4.y));
+                        const float2 zb = fma2(make_float2(p[c + 2], p[c + 3]), splat2(scale_log2),
+                                               make_float2(l4.z, l4.w));
+                        p[c] = ex2_sfu(za.x);
+                        p[c + 1] = ex2_sfu(za.y);
+                        p[c + 2] = ex2_sfu(zb.x);
+                        p[c + 3] = ex2_sfu(zb.y);
                     }
                     if (lo > 0 || hi < 64) {
 #pragma unroll
                         for (int c = 0; c < 64; ++c)
                             if (c < lo || c >= hi) p[c] = 0.f;
                     }
-                    if (KV) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-                        umma::tmem_st32(a1, reinterpret_cast<const float*>(pk));
-                        umma::tmem_wait_st();
-                    }
-                    umma::fence_before_sync();
-                    umma::mbar_arrive(&bars.p_full);
 
-                    float dp[64];
+                    // A2 in two parts; P goes over the first, dS over the second
+                    uint32_t ds[32];
+                    float dp[32];
+                    auto part = [&](int c0) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            float4 d4;
+                            if (KV) d4 = *reinterpret_cast<const float4*>(stat + kRows + c0 + c);
+                            else d4 = make_float4(row_delta, row_delta, row_delta, row_delta);
+                            const float2 a = mul2(make_float2(p[c0 + c], p[c0 + c + 1]),
+                                                  add2(make_float2(dp[c], dp[c + 1]),
+                                                       make_float2(d4.x, d4.y)));
+                            const float2 b = mul2(make_float2(p[c0 + c + 2], p[c0 + c + 3]),
+                                                  add2(make_float2(dp[c + 2], dp[c + 3]),
+                                                       make_float2(d4.z, d4.w)));
+                            ds[(c0 + c) / 2] = pack_bf16x2(a.x, a.y);
+                            ds[(c0 + c) / 2 + 1] = pack_bf16x2(b.x, b.y);
+                        }
+                    };
                     wait(&bars.a2_full, g & 1);
                     umma::fence_after_sync();
                     umma::tmem_ld32(a2, dp);
-                    umma::tmem_ld32(a2 + 32, dp + 32);
                     umma::tmem_wait_ld();
+                    if (KV) {
+                        uint32_t pk[32];
 #pragma unroll
-                    for (int c = 0; c < 64; c += 4) {
-                        float4 d4;
-                        if (KV) d4 = *reinterpret_cast<const float4*>(stat + kRows + c);
-                        else d4 = make_float4(row_delta, row_delta, row_delta, row_delta);
-                        pk[c / 2] = pack_bf16x2(p[c] * (dp[c] - d4.x), p[c + 1] * (dp[c + 1] - d4.y));
-                        pk[c / 2 + 1] =
-                            pack_bf16x2(p[c + 2] * (dp[c + 2] - d4.z), p[c + 3] * (dp[c + 3] - d4.w));
+                        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+                        umma::tmem_st32(lane_addr + kP + 64 * half, reinterpret_cast<const float*>(pk));
+                        umma::tmem_wait_st();
+                        umma::fence_before_sync();
+                        umma::mbar_arrive(&bars.p_full);
                     }
-                    umma::tmem_st32(a2, reinterpret_cast<const float*>(pk));
+                    part(0);
+                    umma::tmem_ld32(a2 + 32, dp);
+                    umma::tmem_wait_ld();
+                    part(32);
+                    // without KV: the buffer was last read by the sum of tile g - 2
+                    if (!KV && g >= 2) wait(&bars.acc_done[g & 1], ((g - 2) >> 1) & 1);
+                    umma::fence_after_sync();
+                    umma::tmem_st32(lane_addr + (KV ? kDs : kDs2 + 32 * (g & 1)) + 64 * half,
+                                    reinterpret_cast<const float*>(ds));
                     umma::tmem_wait_st();
                     umma::fence_before_sync();
                     umma::mbar_arrive(&bars.ds_full);
@@ -450,9 +498,8 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                         if (lane == 0) umma::mbar_arrive(&bars.stat_empty[g & 1]);
                     }
                 }
-                // the item's sums: acc1 is complete after its last product, and
-                // acc2's last product was seen before that one was issued
-                wait(&bars.acc_done, (g - 1) & 1);
+                // the item's sums: complete with the last tile's
+                wait(&bars.acc_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
                 umma::fence_after_sync();
                 constexpr int H = D / 2;  // columns per thread
                 float o1[H], o2[KV ? H : 1];
