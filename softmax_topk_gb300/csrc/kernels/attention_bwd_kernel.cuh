@@ -24,9 +24,13 @@
 // GB300 mapping (persistent CTAs, one per SM, warp-specialised):
 //   * load warp: TMA tiled loads of the resident pair once per item and of the
 //     streamed pairs through a ring of stages;
-//   * MMA warp (one lane): the products, accumulators in tensor memory.  A
-//     product that overwrites what an earlier one reads is issued after that
-//     one's completion was seen;
+//   * issuing warps (one lane each): the products, accumulators in tensor
+//     memory.  One warp issues A1 and A2, another the sums (without KV A1, A2
+//     and the sum have a warp each): an issuer needs some 300 cycles between
+//     two products for its waits and commits, which one alone left the tensor
+//     pipe idle for (57 % busy), and the other's product fills.  A product that
+//     overwrites what an earlier one reads is issued after that one's
+//     completion was seen;
 //   * stat warp (KV only): the streamed rows' -L log2e and -delta into shared
 //     memory, L = +inf for rows past the end so that their P is 0;
 //   * eight compute warps: thread (r, h) owns tile row r (one tensor-memory
@@ -36,14 +40,11 @@
 //     The two roundings to bf16 are the price of the bf16 tensor cores, as P's
 //     is in the forward; sums are fp32.
 //
-// Tensor memory (512 columns): A1, A2 and, with KV and D = 128, two sums of
-// 128 columns each leave no room for P and dS of their own.  A1 is read into
-// registers at once and so is free for the next tile's scores while this
-// tile's exponentials run; P and dS are written over A2, half by half, after
-// the thread has read its part.  So only A2 of the next tile has to wait for
-// this tile's two sums, and that wait passes under the next exponentials.
-// Without KV dS alternates between two buffers where the second sum would be,
-// and A2 waits for its readers only.
+// Tensor memory (512 columns).  With KV and D = 128 the two sums take 256
+// columns, so A1 and A2 take turns in one buffer of 128, and P and dS share
+// another.  A1 and A2 are read into registers as soon as they are complete, and
+// the sums run between them: A1(g), dS(g-1) U, A2(g), P(g) W, A1(g+1), ...
+// Without KV A1, A2 and two buffers for dS have room of their own.
 #pragma once
 
 #include <cuda.h>
@@ -63,18 +64,23 @@ constexpr int kRows = 128;          // rows of a tile, resident or streamed
 constexpr int kComputeWarps = 8;
 constexpr int kCompute = kComputeWarps * 32;
 constexpr int kLoadWarp = 8;
-constexpr int kMmaWarp = 9;
-constexpr int kStatWarp = 10;
-constexpr int kThreads = 352;
+constexpr int kMmaWarp = 9;    // A1; with KV A2 too
+constexpr int kSumWarp = 10;   // the sums
+constexpr int kStatWarp = 11;  // KV: the statistics; else A2
+constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kA1 = 0;         // A1 (fp32, 128 columns)
-constexpr uint32_t kA2 = 128;       // A2 (fp32, 128 columns)
-constexpr uint32_t kAcc1 = 256;     // dK or dQ, D columns
-constexpr uint32_t kAcc2 = 384;     // dV, D columns
-// bf16 operands, 32 columns for tile columns 0-63 and 32 for 64-127, 64 apart
-constexpr uint32_t kP = kA2;        // KV: over A2
-constexpr uint32_t kDs = kA2 + 32;  // KV: over A2
-constexpr uint32_t kDs2 = 384;      // without KV: tile g at kDs2 + 32 (g & 1)
+// Tensor memory columns.  bf16 operands (P, dS) take 32 columns for tile
+// columns 0-63 and 32 for 64-127, 64 apart.
+template <bool KV>
+struct Tmem {
+    static constexpr uint32_t kA1 = 0;                // fp32, 128 columns
+    static constexpr uint32_t kA2 = KV ? 0 : 128;     // fp32, 128 columns
+    static constexpr uint32_t kP = 128;               // KV
+    static constexpr uint32_t kDs = KV ? 160 : 384;   // tile g at kDs + 32 (g % kDsBuffers)
+    static constexpr int kDsBuffers = KV ? 1 : 2;
+    static constexpr uint32_t kAcc1 = 256;            // dK or dQ, D columns
+    static constexpr uint32_t kAcc2 = 384;            // dV, D columns (KV)
+};
 constexpr float kLog2e = 1.442695041f;
 
 // One stage more for U than for W: U of a tile is read twice, by its first and
@@ -102,9 +108,10 @@ struct Barriers {
     uint64_t u_full[L::kUStages], u_empty[L::kUStages];  // streamed tile landed / read
     uint64_t w_full[L::kWStages], w_empty[L::kWStages];
     uint64_t a1_full, a2_full;                     // A1 / A2 of a tile in tensor memory
-    uint64_t a1_free;                              // A1 is in registers (all compute threads)
+    uint64_t a1_free, a2_free;                     // they are in registers (all compute threads)
     uint64_t p_full, ds_full;                      // P / dS in tensor memory (all compute threads)
-    uint64_t acc_done[2];                          // sums of tile g (at g & 1) completed
+    uint64_t pw_done;                              // acc2 += P W completed
+    uint64_t acc_done[2];                          // acc1 += dS U of tile g (at g & 1) completed
     uint64_t acc_empty;                            // an item's sums are in registers
     uint64_t stat_full[2], stat_empty[2];          // the streamed rows' statistics there / read
     uint64_t drain;
@@ -165,6 +172,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                      __nv_bfloat16* __restrict__ out2, int n, int nt, int units, float scale,
                      int causal_flag, KernelCtl ctl) {
     using L = Layout<D>;
+    using TM = Tmem<KV>;
     constexpr int US = L::kUStages, WS = L::kWStages;
     static_assert(sizeof(Barriers<D>) <= L::kBytes - L::kBars, "barriers");
     // no static shared memory: the dynamic part starts on a 1024-byte boundary
@@ -175,7 +183,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
 
     if (tid == 0) {
         mbar_init(&bars.x_full, 1);
-        mbar_init(&bars.x_empty, 1);
+        mbar_init(&bars.x_empty, KV ? 1 : 2);  // the issuers of A1 and A2
         for (int s = 0; s < US; ++s) {
             mbar_init(&bars.u_full[s], 1);
             mbar_init(&bars.u_empty[s], 1);
@@ -189,6 +197,8 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
         mbar_init(&bars.p_full, kCompute);
         mbar_init(&bars.ds_full, kCompute);
         mbar_init(&bars.a1_free, kCompute);
+        mbar_init(&bars.a2_free, kCompute);
+        mbar_init(&bars.pw_done, 1);
         mbar_init(&bars.acc_done[0], 1);
         mbar_init(&bars.acc_done[1], 1);
         mbar_init(&bars.acc_empty, kCompute);
@@ -196,7 +206,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
             mbar_init(&bars.stat_full[s], 32);
             mbar_init(&bars.stat_empty[s], kComputeWarps);
         }
-        mbar_init(&bars.drain, 1);
+        mbar_init(&bars.drain, KV ? 2 : 3);  // every issuer
         mbar_init_fence();
     }
     if (warp == 0) umma::tmem_alloc(&bars.tmem, kTmemCols);
@@ -266,51 +276,78 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
             for (int k = g > WS ? g - WS : 0; k < g; ++k)
                 mbar_wait_bounded_ns(&bars.w_full[k % WS], (k / WS) & 1, kDrainTimeoutNs, ctl.err);
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || warp == kSumWarp || (!KV && warp == kStatWarp)) {
         if (lane == 0) {
             constexpr uint32_t id_a = umma::idesc_bf16(kRows, kRows, false);
             constexpr uint32_t id_acc = umma::idesc_bf16(kRows, D, true);
-            const uint32_t x_addr = smem_addr(smem + L::kX), y_addr = smem_addr(smem + L::kY);
+            // descriptors of the buffers' starts; an offset adds to the address field
+            const uint64_t x_desc = umma::desc_sw128(smem_addr(smem + L::kX), 16, 1024);
+            const uint64_t y_desc = umma::desc_sw128(smem_addr(smem + L::kY), 16, 1024);
+            const uint64_t u_desc = umma::desc_sw128(smem_addr(smem + L::kU), 16, 1024);
+            const uint64_t w_desc = umma::desc_sw128(smem_addr(smem + L::kW), 16, 1024);
+            const uint64_t u_sum = umma::desc_sw128(smem_addr(smem + L::kU), L::kBlock, 1024);
+            const uint64_t w_sum = umma::desc_sw128(smem_addr(smem + L::kW), L::kBlock, 1024);
             Waiter wait(ctl);
             // A (128 x 128 fp32) = resident tile times streamed tile transposed
-            auto product = [&](uint32_t dst, uint32_t a_addr, uint32_t b_addr) {
+            auto product = [&](uint32_t dst, uint64_t a, uint64_t b) {
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t koff = (s >> 2) * L::kBlock + (s & 3) * 32;
-                    umma::mma_bf16(tmem + dst, umma::desc_sw128(a_addr + koff, 16, 1024),
-                                   umma::desc_sw128(b_addr + koff, 16, 1024), id_a, s > 0);
+                    const uint32_t off = ((s >> 2) * L::kBlock + (s & 3) * 32) >> 4;
+                    umma::mma_bf16(tmem + dst, a + off, b + off, id_a, s > 0);
                 }
             };
             // acc (128 x D) += P or dS (tensor memory, tile columns 0-63 at
             // `src`, 64-127 at src + 64) times a streamed tile
-            auto accumulate = [&](uint32_t dst, uint32_t src, uint32_t b_addr, bool keep) {
+            auto accumulate = [&](uint32_t dst, uint32_t src, uint64_t b, bool keep) {
 #pragma unroll
                 for (int s = 0; s < kRows / 16; ++s)
                     umma::mma_bf16_tmem_a(tmem + dst, tmem + src + (s < 4 ? 8 * s : 32 + 8 * s),
-                                          umma::desc_sw128(b_addr + s * 2048, L::kBlock, 1024),
-                                          id_acc, keep || s > 0);
+                                          b + ((s * 2048) >> 4), id_acc, keep || s > 0);
             };
-            auto issue_a1 = [&](int g) {
+            auto tile_at = [](uint64_t desc, int stage) {
+                return desc + uint64_t(stage) * (L::kTile >> 4);
+            };
+            auto issue_a1 = [&](int g, bool last) {
                 const int us = g % US;
                 wait(&bars.u_full[us], (g / US) & 1);
-                if (g > 0) wait(&bars.a1_free, (g - 1) & 1);
+                if (g > 0) wait(KV ? &bars.a2_free : &bars.a1_free, (g - 1) & 1);
                 if (!wait.ok) return;
                 umma::fence_after_sync();
-                product(kA1, x_addr, smem_addr(smem + L::kU + us * L::kTile));
+                product(TM::kA1, x_desc, tile_at(u_desc, us));
                 umma::commit(&bars.a1_full);
+                if (!KV && last) umma::commit(&bars.x_empty);
             };
             auto issue_a2 = [&](int g, bool last) {
                 const int ws = g % WS;
                 wait(&bars.w_full[ws], (g / WS) & 1);
-                // over P and dS of tile g - 1 (without KV its readers are done:
-                // they have arrived on ds_full)
-                if (KV && g > 0) wait(&bars.acc_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+                if (KV) wait(&bars.a1_free, g & 1);
+                else if (g > 0) wait(&bars.a2_free, (g - 1) & 1);
                 if (!wait.ok) return;
                 umma::fence_after_sync();
-                product(kA2, y_addr, smem_addr(smem + L::kW + ws * L::kTile));
+                product(TM::kA2, y_desc, tile_at(w_desc, ws));
                 umma::commit(&bars.a2_full);
                 if (!KV) umma::commit(&bars.w_empty[ws]);
                 if (last) umma::commit(&bars.x_empty);  // the last reader of X and Y
+            };
+            // the item's first products (j == 0) overwrite the sums, which the
+            // compute warps must have read
+            auto issue_sums = [&](int g, int j, int it) {
+                const int us = g % US, ws = g % WS;
+                if (j == 0 && it > 0) wait(&bars.acc_empty, (it - 1) & 1);
+                if (KV) {
+                    wait(&bars.p_full, g & 1);
+                    if (!wait.ok) return;
+                    umma::fence_after_sync();
+                    accumulate(TM::kAcc2, TM::kP, tile_at(w_sum, ws), j > 0);
+                    umma::commit(&bars.pw_done);
+                    umma::commit(&bars.w_empty[ws]);
+                }
+                wait(&bars.ds_full, g & 1);
+                if (!wait.ok) return;
+                umma::fence_after_sync();
+                accumulate(TM::kAcc1, TM::kDs + 32 * (g % TM::kDsBuffers), tile_at(u_sum, us), j > 0);
+                umma::commit(&bars.acc_done[g & 1]);
+                umma::commit(&bars.u_empty[us]);
             };
             int g = 0, it = 0;
             for (int u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
@@ -319,29 +356,12 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                 for (int e = 0; e < cnt && wait.ok; ++e, ++it) {
                     int first, count;
                     tile_range<KV>(e == 0 ? ta : tb, nt, causal, first, count);
-                    wait(&bars.x_full, it & 1);
-                    issue_a1(g);
-                    issue_a2(g, count == 1);
+                    if (warp != kSumWarp) wait(&bars.x_full, it & 1);
                     for (int j = 0; j < count && wait.ok; ++j, ++g) {
-                        const int us = g % US, ws = g % WS;
-                        if (j + 1 < count) issue_a1(g + 1);
-                        // the first products of an item overwrite the sums
-                        if (j == 0 && it > 0) wait(&bars.acc_empty, (it - 1) & 1);
-                        if (KV) {
-                            wait(&bars.p_full, g & 1);
-                            if (!wait.ok) break;
-                            umma::fence_after_sync();
-                            accumulate(kAcc2, kP, smem_addr(smem + L::kW + ws * L::kTile), j > 0);
-                            umma::commit(&bars.w_empty[ws]);
-                        }
-                        wait(&bars.ds_full, g & 1);
-                        if (!wait.ok) break;
-                        umma::fence_after_sync();
-                        accumulate(kAcc1, KV ? kDs : kDs2 + 32 * (g & 1),
-                                   smem_addr(smem + L::kU + us * L::kTile), j > 0);
-                        umma::commit(&bars.acc_done[g & 1]);
-                        umma::commit(&bars.u_empty[us]);
-                        if (j + 1 < count) issue_a2(g + 1, j + 2 == count);
+                        const bool last = j + 1 == count;
+                        if (warp == kSumWarp) issue_sums(g, j, it);
+                        else if (warp == kMmaWarp) issue_a1(g, last);
+                        if (KV ? warp == kMmaWarp : warp == kStatWarp) issue_a2(g, last);
                     }
                 }
             }
@@ -388,7 +408,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
         // ---------------------------------------------------------------- compute
         const int r = tid & 127, half = tid >> 7;  // tile row, column half
         const uint32_t lane_addr = tmem + (uint32_t((warp & 3) * 32) << 16);
-        const uint32_t a1 = lane_addr + kA1 + 64 * half, a2 = lane_addr + kA2 + 64 * half;
+        const uint32_t a1 = lane_addr + TM::kA1 + 64 * half, a2 = lane_addr + TM::kA2 + 64 * half;
         const float scale_log2 = scale * kLog2e;
         Waiter wait(ctl);
         int g = 0;
@@ -449,46 +469,53 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                             if (c < lo || c >= hi) p[c] = 0.f;
                     }
 
-                    // A2 in two parts; P goes over the first, dS over the second
-                    uint32_t ds[32];
-                    float dp[32];
-                    auto part = [&](int c0) {
-#pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            float4 d4;
-                            if (KV) d4 = *reinterpret_cast<const float4*>(stat + kRows + c0 + c);
-                            else d4 = make_float4(row_delta, row_delta, row_delta, row_delta);
-                            const float2 a = mul2(make_float2(p[c0 + c], p[c0 + c + 1]),
-                                                  add2(make_float2(dp[c], dp[c + 1]),
-                                                       make_float2(d4.x, d4.y)));
-                            const float2 b = mul2(make_float2(p[c0 + c + 2], p[c0 + c + 3]),
-                                                  add2(make_float2(dp[c + 2], dp[c + 3]),
-                                                       make_float2(d4.z, d4.w)));
-                            ds[(c0 + c) / 2] = pack_bf16x2(a.x, a.y);
-                            ds[(c0 + c) / 2 + 1] = pack_bf16x2(b.x, b.y);
-                        }
-                    };
-                    wait(&bars.a2_full, g & 1);
-                    umma::fence_after_sync();
-                    umma::tmem_ld32(a2, dp);
-                    umma::tmem_wait_ld();
                     if (KV) {
                         uint32_t pk[32];
 #pragma unroll
                         for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-                        umma::tmem_st32(lane_addr + kP + 64 * half, reinterpret_cast<const float*>(pk));
+                        if (g > 0) wait(&bars.pw_done, (g - 1) & 1);
+                        umma::fence_after_sync();
+                        umma::tmem_st32(lane_addr + TM::kP + 64 * half,
+                                        reinterpret_cast<const float*>(pk));
                         umma::tmem_wait_st();
                         umma::fence_before_sync();
                         umma::mbar_arrive(&bars.p_full);
                     }
-                    part(0);
-                    umma::tmem_ld32(a2 + 32, dp);
-                    umma::tmem_wait_ld();
-                    part(32);
-                    // without KV: the buffer was last read by the sum of tile g - 2
-                    if (!KV && g >= 2) wait(&bars.acc_done[g & 1], ((g - 2) >> 1) & 1);
+
+                    float dp[64];
+                    wait(&bars.a2_full, g & 1);
                     umma::fence_after_sync();
-                    umma::tmem_st32(lane_addr + (KV ? kDs : kDs2 + 32 * (g & 1)) + 64 * half,
+                    umma::tmem_ld32(a2, dp);
+                    umma::tmem_ld32(a2 + 32, dp + 32);
+                    umma::tmem_wait_ld();
+                    umma::fence_before_sync();
+                    umma::mbar_arrive(&bars.a2_free);
+                    uint32_t ds[32];
+#pragma unroll
+                    for (int c0 = 0; c0 < 64; c0 += 16) {
+                        float4 d4[4];  // four loads ahead of their use
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            d4[i] = KV ? *reinterpret_cast<const float4*>(stat + kRows + c0 + 4 * i)
+                                       : make_float4(row_delta, row_delta, row_delta, row_delta);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = c0 + 4 * i;
+                            const float2 a = mul2(make_float2(p[c], p[c + 1]),
+                                                  add2(make_float2(dp[c], dp[c + 1]),
+                                                       make_float2(d4[i].x, d4[i].y)));
+                            const float2 b = mul2(make_float2(p[c + 2], p[c + 3]),
+                                                  add2(make_float2(dp[c + 2], dp[c + 3]),
+                                                       make_float2(d4[i].z, d4[i].w)));
+                            ds[c / 2] = pack_bf16x2(a.x, a.y);
+                            ds[c / 2 + 1] = pack_bf16x2(b.x, b.y);
+                        }
+                    }
+                    // the buffer's last reader: the sum of tile g - kDsBuffers
+                    constexpr int lag = TM::kDsBuffers;
+                    if (g >= lag) wait(&bars.acc_done[(g - lag) & 1], ((g - lag) >> 1) & 1);
+                    umma::fence_after_sync();
+                    umma::tmem_st32(lane_addr + TM::kDs + 32 * (g % lag) + 64 * half,
                                     reinterpret_cast<const float*>(ds));
                     umma::tmem_wait_st();
                     umma::fence_before_sync();
@@ -505,9 +532,9 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                 float o1[H], o2[KV ? H : 1];
 #pragma unroll
                 for (int c = 0; c < H / 32; ++c) {
-                    umma::tmem_ld32(lane_addr + kAcc1 + half * H + 32 * c, o1 + 32 * c);
+                    umma::tmem_ld32(lane_addr + TM::kAcc1 + half * H + 32 * c, o1 + 32 * c);
                     if constexpr (KV)
-                        umma::tmem_ld32(lane_addr + kAcc2 + half * H + 32 * c, o2 + 32 * c);
+                        umma::tmem_ld32(lane_addr + TM::kAcc2 + half * H + 32 * c, o2 + 32 * c);
                 }
                 umma::tmem_wait_ld();
                 umma::fence_before_sync();
