@@ -35,7 +35,7 @@
 namespace os {
 namespace route {
 
-constexpr int kWarps = 4;      // tokens per CTA at a time
+constexpr int kWarps = 4;      // warps per CTA
 constexpr int kMaxK = 32;      // one lane per chosen expert
 constexpr int kMaxExperts = 1024;
 
@@ -44,6 +44,8 @@ struct Shape {
     int lanes;     // lanes per group (a power of two)
     int per_lane;  // experts per lane
     int index_mask;  // experts up to a power of two, less one
+    int slots;       // K up to a power of two: lanes per token after the choice
+    int tokens;      // rows that a warp takes at a time, at most 32 / slots
     int sigmoid, renorm;
     float scale;
 };
@@ -228,19 +230,24 @@ __device__ __forceinline__ void group_top2(const Shape& sh, float& a, float& b) 
 // values at the border are closer than `slack` + |value| 2^-21.
 __device__ __forceinline__ bool group_keep(const Shape& sh, int group, float value, float slack,
                                            bool exact, bool& near) {
-    const uint32_t gkey = group < sh.groups ? order_key(value + 0.f) : 0u;
-    int rank = 0;
-    for (int g = 0; g < sh.groups; ++g) {
-        const uint32_t o = __shfl_sync(kFullMask, gkey, g * sh.lanes);
-        rank += o > gkey || (o == gkey && g < group);
+    // round by round the best group that is left, ties to the lowest lane
+    uint32_t left = group < sh.groups ? order_key(value + 0.f) : 0u;
+    uint32_t low = 0;
+    bool keep = false;
+    for (int r = 0; r < sh.topk_groups; ++r) {
+        low = warp_max(left);
+        const int first = __ffs(__ballot_sync(kFullMask, left == low)) - 1;
+        if (group == first / sh.lanes) {
+            keep = true;
+            left = 0u;
+        }
     }
-    const bool keep = group < sh.groups && rank < sh.topk_groups;
     if (!exact) {
-        const float low = key_value(warp_min(keep ? gkey : 0xffffffffu));
-        const uint32_t out = warp_max(keep ? 0u : gkey);
+        const uint32_t out = warp_max(left);
         if (out != 0u) {
-            const float high = key_value(out);
-            if (high != -INFINITY && !(low - high > slack + fabsf(low) * 0x1p-21f)) near = true;
+            const float worst = key_value(low), best_out = key_value(out);
+            if (best_out != -INFINITY && !(worst - best_out > slack + fabsf(worst) * 0x1p-21f))
+                near = true;
         }
     }
     return keep;
@@ -383,13 +390,27 @@ __device__ __forceinline__ float signed_value(int k) {
 constexpr int kNone = INT_MIN;             // takes no part; below every key
 constexpr int kMissing = int(0x80800000u);  // keys of -inf are below this
 
+// Sum and maximum over the `width` lanes (a power of two) of this lane's slots.
+__device__ __forceinline__ float slot_sum(float v, int width) {
+    for (int o = width / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
+}
+__device__ __forceinline__ float slot_max(float v, int width) {
+    for (int o = width / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
+    return v;
+}
+
 // N: experts per lane, rounded up to a power of two.
+//
+// A warp chooses for `tokens` rows one after the other and then does what is
+// left, slot by slot, for all of them at once: lane t * slots + k has slot k of
+// token t (slots: K up to a power of two).
 template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32)
 route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __restrict__ weights,
              int* __restrict__ idx, int64_t rows, const Shape sh) {
     const int lane = threadIdx.x & 31;
-    const int E = sh.experts;
+    const int E = sh.experts, K = sh.K;
     const Place at(sh);
     const int base = at.base, count = at.count;
     const bool by_score = bias != nullptr;  // else logits give the order
@@ -398,106 +419,124 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
     const bool need_scores = by_score || pair_sum;
     const bool need_sum = !sh.sigmoid && (need_scores || !sh.renorm);
     const int low_bits = sh.index_mask;  // of a key: the expert, counted down
+    const int my_token = lane / sh.slots, my_slot = lane % sh.slots;
     float be[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) be[i] = by_score && i < count ? bias[base + i] : 0.f;
 
-    for (int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < rows;
-         row += int64_t(gridDim.x) * kWarps) {
-        const T* xrow = x + row * E;
+    const int64_t step = int64_t(gridDim.x) * kWarps * sh.tokens;
+    for (int64_t row0 = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * sh.tokens; row0 < rows;
+         row0 += step) {
+        const int tokens = int(min(int64_t(sh.tokens), rows - row0));
+        int mine = kNone, after = kNone;     // this lane's slot and the next best
+        float m_slot = 0.f, inv_slot = 1.f;  // its row's maximum and 1 / sum
+        uint32_t unsure = 0;                 // one bit per token
         float v[N];
-        load_run<T, N, VEC>(xrow + base, count, v);
-        float m = 0.f, inv_d = 1.f;
-        if (!sh.sigmoid) {
-            m = v[0];
+        load_run<T, N, VEC>(x + row0 * E + base, count, v);
+        for (int t = 0; t < tokens; ++t) {
+            float ahead[N];  // the next token's logits
+            if (t + 1 < tokens) load_run<T, N, VEC>(x + (row0 + t + 1) * E + base, count, ahead);
+            float m = 0.f, inv_d = 1.f;
+            if (!sh.sigmoid) {
+                m = v[0];
 #pragma unroll
-            for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
-            m = key_value(warp_max(order_key(m + 0.f)));
-        }
-        float s[N];  // scores, where they are compared
-        if (need_sum) {
-            const float ref = m == -INFINITY ? 0.f : m;
-            float d = 0.f;
-#pragma unroll
-            for (int i = 0; i < N; i += 2) {
-                const float2 e = exp_pair<false>(
-                    make_float2(v[i] - ref, i + 1 < N ? v[i + 1] - ref : -INFINITY));
-                s[i] = e.x;
-                if (i + 1 < N) s[i + 1] = e.y;
-                d += e.x + e.y;
+                for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+                m = key_value(warp_max(order_key(m + 0.f)));
             }
-            d = warp_sum(d);
-            inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
+            float s[N];  // scores, where they are compared
+            if (need_sum) {
+                const float ref = m == -INFINITY ? 0.f : m;
+                float d = 0.f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) s[i] *= inv_d;
-        } else if (need_scores) {
+                for (int i = 0; i < N; i += 2) {
+                    const float2 e = exp_pair<false>(
+                        make_float2(v[i] - ref, i + 1 < N ? v[i + 1] - ref : -INFINITY));
+                    s[i] = e.x;
+                    if (i + 1 < N) s[i + 1] = e.y;
+                    d += e.x + e.y;
+                }
+                d = warp_sum(d);
+                inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) s[i] *= inv_d;
+            } else if (need_scores) {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    s[i] = rcp_sfu(1.f + ex2_sfu(-expc::kLog2e * v[i]));
+            }
+            if (my_token == t) {
+                m_slot = m;
+                inv_slot = inv_d;
+            }
+            float c[N];
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                s[i] = rcp_sfu(1.f + ex2_sfu(-expc::kLog2e * v[i]));
-        }
-        const float err = (sh.sigmoid ? 1.f : inv_d) * 0x1p-19f;  // twice the bound of a score
-
-        float c[N];
+                c[i] = by_score && v[i] != -INFINITY ? s[i] + be[i] : v[i];
+            bool keep = true;
+            if (sh.groups > 1) {
+                float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            c[i] = by_score && v[i] != -INFINITY ? s[i] + be[i] : v[i];
-        bool unsure = false, keep = true;
-        if (sh.groups > 1) {
-            float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (i < count) {
-                    const float g = pair_sum && !by_score && v[i] != -INFINITY ? s[i] : c[i];
-                    b = fmaxf(b, fminf(a, g));
-                    a = fmaxf(a, g);
+                for (int i = 0; i < N; ++i) {
+                    if (i < count) {
+                        const float g = pair_sum && !by_score && v[i] != -INFINITY ? s[i] : c[i];
+                        b = fmaxf(b, fminf(a, g));
+                        a = fmaxf(a, g);
+                    }
                 }
+                group_top2(sh, a, b);
+                bool near = false;
+                keep = group_keep(sh, at.group, pair_sum ? a + b : a,
+                                  (sh.sigmoid ? 1.f : inv_d) * 0x1p-18f, !need_scores, near);
+                if (near) unsure |= 1u << t;
             }
-            group_top2(sh, a, b);
-            keep = group_keep(sh, at.group, pair_sum ? a + b : a, 2.f * err, !need_scores, unsure);
-        }
-        int key[N];
+            int key[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            key[i] = keep && i < count
-                         ? ((signed_key(c[i] + 0.f) & ~low_bits) | (low_bits - (base + i)))
-                         : kNone;
+            for (int i = 0; i < N; ++i)
+                key[i] = keep && i < count
+                             ? ((signed_key(c[i] + 0.f) & ~low_bits) | (low_bits - (base + i)))
+                             : kNone;
 
-        // ---- K rounds: lane k takes slot k's key; `next` is the best left out
-        if constexpr (N <= 8) sort_run<N>(key);
-        auto lane_best = [&]() {
-            int best = key[0];
-            if constexpr (N > 8) {
+            // K rounds, and one for the best that is left out
+            if constexpr (N <= 8) sort_run<N>(key);
+            auto lane_best = [&]() {
+                int best = key[0];
+                if constexpr (N > 8) {
 #pragma unroll
-                for (int i = 1; i < N; ++i) best = max(best, key[i]);
-            }
-            return best;
-        };
-        int mine = kNone;
-        for (int k = 0; k < sh.K; ++k) {
-            const int best = lane_best();
-            const int top = __reduce_max_sync(kFullMask, best);
-            if (lane == k) mine = top;
-            if (best == top) {  // one lane: keys differ in their experts
+                    for (int i = 1; i < N; ++i) best = max(best, key[i]);
+                }
+                return best;
+            };
+            const int slot_here = my_token == t ? my_slot : -1;
+            for (int k = 0; k < K; ++k) {
+                const int best = lane_best();
+                const int top = __reduce_max_sync(kFullMask, best);
+                if (slot_here == k) mine = top;
+                const bool taken = best == top;  // one lane: keys differ in their experts
                 if constexpr (N <= 8) {
 #pragma unroll
-                    for (int i = 0; i + 1 < N; ++i) key[i] = key[i + 1];
-                    key[N - 1] = kNone;
-                } else {
+                    for (int i = 0; i + 1 < N; ++i) key[i] = taken ? key[i + 1] : key[i];
+                    key[N - 1] = taken ? kNone : key[N - 1];
+                } else if (taken) {
 #pragma unroll
                     for (int i = 0; i < N; ++i)
                         if (key[i] == top) key[i] = kNone;
                 }
             }
+            const int next = __reduce_max_sync(kFullMask, lane_best());
+            if (slot_here == K - 1) after = next;
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = ahead[i];
         }
-        const int next = __reduce_max_sync(kFullMask, lane_best());
 
-        // ---- is the order certain?  lane k compares slots k and k + 1, lane
-        // K - 1 its slot with what is left out
+        // ---- slot by slot: is the order certain?
+        const bool real = my_token < tokens && my_slot < K;
+        const T* xrow = x + (row0 + my_token) * E;
         int e = min(low_bits - (mine & low_bits), E - 1);
-        float xm = lane < sh.K ? widen(xrow[e]) : -INFINITY;
+        float xm = real ? widen(xrow[e]) : -INFINITY;
+        const float err = (sh.sigmoid ? 1.f : inv_slot) * 0x1p-19f;  // twice the bound of a score
         if (by_score || sizeof(T) == 4) {
-            int after = __shfl_down_sync(kFullMask, mine, 1);
-            if (lane == sh.K - 1) after = next;
+            const int below = __shfl_down_sync(kFullMask, mine, 1);
+            if (my_slot != K - 1) after = below;
             bool near;
             if (by_score) {
                 const float va = signed_value(mine & ~low_bits), vb = signed_value(after & ~low_bits);
@@ -505,29 +544,35 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
             } else {
                 near = (mine & ~low_bits) == (after & ~low_bits);
             }
-            near = near && lane < sh.K && after >= kMissing;
+            near = near && real && after >= kMissing;
             if (__any_sync(kFullMask, near)) {
                 // equal logits of equal bias stand in the order of their experts
                 const float b = by_score ? bias[e] : 0.f;
                 const float xa = __shfl_down_sync(kFullMask, xm, 1);
                 const float ba = __shfl_down_sync(kFullMask, b, 1);
-                if (near && (lane == sh.K - 1 || xa != xm || ba != b)) unsure = true;
+                if (near && (my_slot == K - 1 || xa != xm || ba != b)) unsure |= 1u << my_token;
             }
         }
-        if (__any_sync(kFullMask, unsure)) {
-            e = choose_exact<T, N>(xrow, bias, sh);
-            xm = lane < sh.K ? widen(xrow[e]) : -INFINITY;
+        unsure = __reduce_or_sync(kFullMask, unsure);
+        for (; unsure; unsure &= unsure - 1) {
+            const int t = __ffs(unsure) - 1;
+            const int chosen = choose_exact<T, N>(x + (row0 + t) * E, bias, sh);
+            const int here = __shfl_sync(kFullMask, chosen, my_slot);
+            if (my_token == t) {
+                e = here;
+                xm = real ? widen(xrow[e]) : -INFINITY;
+            }
         }
 
         // ---- weights
-        const bool live = lane < sh.K && xm != -INFINITY;
+        const bool live = real && xm != -INFINITY;
         float w;
         if (!sh.renorm) {
-            w = sh.sigmoid ? sigmoid(xm) : exp1(xm - m) * inv_d;
+            w = sh.sigmoid ? sigmoid(xm) : exp1(xm - m_slot) * inv_slot;
             if (!live) w = 0.f;
         } else {
             // relative to the largest chosen logit, so that no sum underflows
-            float top = key_value(warp_max(order_key((live ? xm : -INFINITY) + 0.f)));
+            float top = slot_max(live ? xm : -INFINITY, sh.slots);
             if (sh.sigmoid) top = fminf(top, 0.f);
             if (sh.sigmoid && xm > 0.f) {
                 w = sigmoid(xm);
@@ -536,12 +581,12 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
                 if (sh.sigmoid) w = __fdiv_rn(w, 1.f + exp1(xm));
             }
             if (!live) w = 0.f;
-            const float sum = warp_sum(w);
+            const float sum = slot_sum(w, sh.slots);
             w = sum > 0.f ? __fdiv_rn(w, sum) : 0.f;
         }
-        if (lane < sh.K) {
-            weights[row * sh.K + lane] = w * sh.scale;
-            idx[row * sh.K + lane] = e;
+        if (real) {
+            weights[(row0 + my_token) * K + my_slot] = w * sh.scale;
+            idx[(row0 + my_token) * K + my_slot] = e;
         }
     }
 }

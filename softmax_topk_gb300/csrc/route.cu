@@ -22,6 +22,8 @@ Shape make_shape(const RouteArgs& a, int groups) {
     while (s.lanes * 2 * groups <= 32) s.lanes *= 2;
     s.per_lane = (a.experts / groups + s.lanes - 1) / s.lanes;
     s.index_mask = pow2_at_least(a.experts) - 1;
+    s.slots = pow2_at_least(a.K);
+    s.tokens = 1;
     s.sigmoid = a.score == OS_SCORE_SIGMOID;
     s.renorm = a.renorm;
     s.scale = a.scale;
@@ -36,15 +38,23 @@ bool whole_runs(const Shape& s, int N, int size, const void* p, const void* q) {
            reinterpret_cast<uintptr_t>(p) % bytes == 0 && reinterpret_cast<uintptr_t>(q) % bytes == 0;
 }
 
-int64_t grid_for(int64_t rows) { return min64(ceil_div(rows, route::kWarps), int64_t(1) << 22); }
+int64_t grid_for(int64_t rows, int tokens) {
+    return min64(ceil_div(rows, int64_t(route::kWarps) * tokens), int64_t(1) << 22);
+}
 
 template <typename T, int N>
-cudaError_t launch_fwd(const RouteArgs& a, const Shape& s, float* weights, int32_t* idx,
+cudaError_t launch_fwd(const RouteArgs& a, Shape s, float* weights, int32_t* idx,
                        cudaStream_t stream) {
+    // one row per warp while the GPU has warps to spare (the latency of one
+    // row), else several, which share the work after the choice
+    const DeviceInfo* dev = device_info();
+    if (!dev) return cudaErrorInvalidDevice;
+    while (s.tokens * 2 * s.slots <= 32 && a.rows >= int64_t(dev->sms) * 32 * s.tokens * 2)
+        s.tokens *= 2;
     auto k = route::route_kernel<T, N, false>;
     if constexpr (N <= 32)  // groups of 33 to 64 experts to a lane never fill it
         if (whole_runs(s, N, sizeof(T), a.x, a.x)) k = route::route_kernel<T, N, true>;
-    return launch_kernel(k, grid_for(a.rows), route::kWarps * 32, 1, 0, stream,
+    return launch_kernel(k, grid_for(a.rows, s.tokens), route::kWarps * 32, 1, 0, stream,
                          static_cast<const T*>(a.x), a.bias, weights, reinterpret_cast<int*>(idx),
                          a.rows, s);
 }
@@ -54,7 +64,7 @@ cudaError_t launch_bwd(const RouteArgs& a, const Shape& s, const int32_t* idx,
                        const float* dweights, void* dx, cudaStream_t stream) {
     auto k = whole_runs(s, N, sizeof(T), a.x, dx) ? route::route_bwd_kernel<T, N, true>
                                                   : route::route_bwd_kernel<T, N, false>;
-    return launch_kernel(k, grid_for(a.rows), route::kWarps * 32, 1, 0, stream,
+    return launch_kernel(k, grid_for(a.rows, 1), route::kWarps * 32, 1, 0, stream,
                          static_cast<const T*>(a.x), reinterpret_cast<const int*>(idx), dweights,
                          static_cast<T*>(dx), a.rows, s);
 }
