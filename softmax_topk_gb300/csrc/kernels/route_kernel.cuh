@@ -122,89 +122,6 @@ __device__ __forceinline__ void load_run(const T* p, int count, float (&v)[N]) {
     }
 }
 
-// The choice of one token with s and c in 64 bits (bias given or sums of two
-// scores): rare, so written for size.  Every lane returns the expert of slot
-// `lane` (lane < K); m is the row's maximum.  Lane l looks after experts l,
-// l + 32, ...
-template <typename T>
-__device__ __noinline__ int choose_wide(const T* xrow, const float* bias, const Shape sh, float mf) {
-    const int lane = threadIdx.x & 31, E = sh.experts, gsize = E / sh.groups;
-    const double m = mf;
-    double d = 1.0;
-    if (!sh.sigmoid) {
-        d = 0.0;
-        for (int e = lane; e < E; e += 32) {
-            const float x = widen(xrow[e]);
-            if (x > -INFINITY) d += exp(double(x) - m);
-        }
-        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFullMask, d, o);
-    }
-    double c[kMaxExperts / 32];
-    for (int e = lane; e < E; e += 32) {
-        const float x = widen(xrow[e]);
-        double v = -INFINITY;
-        if (x > -INFINITY) {
-            v = sh.sigmoid ? 1.0 / (1.0 + exp(-double(x))) : exp(double(x) - m) / d;
-            if (bias) v += double(bias[e]);
-        }
-        c[e >> 5] = v;
-    }
-    // the groups that take part, one bit each
-    uint32_t kept = 0xffffffffu;
-    if (sh.groups > 1) {
-        double score = -INFINITY;  // lane g: group g's value
-        for (int g = 0; g < sh.groups; ++g) {
-            double a = -INFINITY, b = -INFINITY;
-            for (int e = lane; e < (g + 1) * gsize; e += 32)
-                if (e >= g * gsize) {
-                    b = fmax(b, fmin(a, c[e >> 5]));
-                    a = fmax(a, c[e >> 5]);
-                }
-            for (int o = 16; o > 0; o >>= 1) {
-                const double oa = __shfl_xor_sync(kFullMask, a, o);
-                const double ob = __shfl_xor_sync(kFullMask, b, o);
-                b = fmax(fmin(a, oa), fmax(b, ob));
-                a = fmax(a, oa);
-            }
-            if (lane == g) score = sh.group_top == 2 ? a + b : a;
-        }
-        int rank = 0;
-        for (int g = 0; g < sh.groups; ++g) {
-            const double o = __shfl_sync(kFullMask, score, g);
-            rank += o > score || (o == score && g < lane);
-        }
-        kept = __ballot_sync(kFullMask, lane < sh.groups && rank < sh.topk_groups);
-    }
-    // slot by slot: the best expert after the previous slot's in (c, expert) order
-    int mine = 0, last = -1;
-    double bound = INFINITY;
-    for (int k = 0; k < sh.K; ++k) {
-        double best = -INFINITY;
-        int at = kMaxExperts;
-        for (int e = lane; e < E; e += 32) {
-            if (!((kept >> (e / gsize)) & 1)) continue;
-            const double v = bias ? c[e >> 5] : double(widen(xrow[e]));  // s rises with x
-            const bool after = last < 0 || v < bound || (v == bound && e > last);
-            if (after && (at == kMaxExperts || v > best)) {
-                best = v;
-                at = e;
-            }
-        }
-        for (int o = 16; o > 0; o >>= 1) {
-            const double ob = __shfl_xor_sync(kFullMask, best, o);
-            const int oa = __shfl_xor_sync(kFullMask, at, o);
-            if (oa < kMaxExperts && (at == kMaxExperts || ob > best || (ob == best && oa < at))) {
-                best = ob;
-                at = oa;
-            }
-        }
-        last = at;
-        bound = best;
-        if (lane == k) mine = min(at, E - 1);  // in range whatever the inputs (NaN)
-    }
-    return mine;
-}
-
 // A lane's place: its group, its experts base .. base + count - 1.
 struct Place {
     int group, base, count;
@@ -253,7 +170,110 @@ __device__ __forceinline__ bool group_keep(const Shape& sh, int group, float val
     return keep;
 }
 
-// The choice with c in fp32; returns and arguments as choose_wide.
+// 64-bit order key of a double, and back.
+__device__ __forceinline__ long long wide_key(double v) {
+    const long long b = __double_as_longlong(v + 0.0);
+    return b ^ ((b >> 63) & 0x7fffffffffffffffll);
+}
+__device__ __forceinline__ double wide_value(long long k) {
+    return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffll));
+}
+constexpr long long kNoneWide = LLONG_MIN;
+// Largest key over the warp: the high halves, then the low ones among equals.
+__device__ __forceinline__ long long warp_max_wide(long long v) {
+    const int hi = __reduce_max_sync(kFullMask, int(v >> 32));
+    const uint32_t lo = __reduce_max_sync(kFullMask, int(v >> 32) == hi ? uint32_t(v) : 0u);
+    return (static_cast<long long>(hi) << 32) | lo;
+}
+
+// The choice with c in 64 bits, one run per lane as in the kernel.  64-bit
+// exponentials are slow (two lanes a clock per SM), so only the values that
+// can matter are formed so: all of them where the choice of groups was too
+// near (`all`), else those of at least `from`; the others are far from every
+// border, and their fp32 values (c32) keep them in their places.
+template <typename T, int N>
+__device__ __noinline__ int choose_wide(const T* xrow, const float* bias, const Shape sh, float mf,
+                                        const float* c32, float from, bool all) {
+    const int lane = threadIdx.x & 31, E = sh.experts;
+    const Place at_(sh);
+    const int base = at_.base, count = at_.count;
+    const bool by_score = bias != nullptr;
+    const bool pair_sum = sh.groups > 1 && sh.group_top == 2;
+    double d = 1.0;
+    if (!sh.sigmoid && by_score) {  // without a bias it is a common factor
+        d = 0.0;
+        for (int i = 0; i < count; ++i) {
+            const float x = widen(xrow[base + i]);
+            if (x > -INFINITY) d += exp(double(x) - double(mf));
+        }
+        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFullMask, d, o);
+    }
+    long long g[N];  // c, or for groups without a bias s
+    for (int i = 0; i < N; ++i) {
+        g[i] = kNoneWide;
+        if (i >= count) continue;
+        const float x = widen(xrow[base + i]);
+        double v = -INFINITY;
+        if (x > -INFINITY) {
+            if (all || c32[i] >= from) {
+                v = sh.sigmoid ? 1.0 / (1.0 + exp(-double(x))) : exp(double(x) - double(mf)) / d;
+                if (by_score) v += double(bias[base + i]);
+            } else {
+                v = c32[i];
+            }
+        }
+        g[i] = wide_key(v);
+    }
+    bool keep = true;
+    if (sh.groups > 1) {
+        long long a = kNoneWide, b = kNoneWide;
+        for (int i = 0; i < N; ++i) {
+            const long long lesser = min(a, g[i]);
+            a = max(a, g[i]);
+            b = max(b, lesser);
+        }
+        for (int o = sh.lanes / 2; o > 0; o >>= 1) {
+            const long long oa = __shfl_xor_sync(kFullMask, a, o);
+            const long long ob = __shfl_xor_sync(kFullMask, b, o);
+            b = max(min(a, oa), max(b, ob));
+            a = max(a, oa);
+        }
+        long long left = kNoneWide;
+        if (at_.group < sh.groups) left = pair_sum ? wide_key(wide_value(a) + wide_value(b)) : a;
+        keep = false;
+        for (int r = 0; r < sh.topk_groups; ++r) {
+            const long long top = warp_max_wide(left);
+            const int first = __ffs(__ballot_sync(kFullMask, left == top)) - 1;
+            if (at_.group == first / sh.lanes) {
+                keep = true;
+                left = kNoneWide;
+            }
+        }
+    }
+    for (int i = 0; i < N; ++i) {
+        if (i < count && !by_score) g[i] = wide_key(widen(xrow[base + i]));  // s rises with x
+        if (!keep) g[i] = kNoneWide;
+    }
+    int mine = 0;
+    for (int k = 0; k < sh.K; ++k) {
+        long long best = kNoneWide;
+        int at = 0;
+        for (int i = 0; i < N; ++i)
+            if (g[i] > best) {
+                best = g[i];
+                at = i;
+            }
+        const long long top = warp_max_wide(best);
+        const int src = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
+        const int e = min(__shfl_sync(kFullMask, base + at, src), E - 1);
+        if (lane == k) mine = e;
+        if (lane == src) g[at] = kNoneWide;
+    }
+    return mine;
+}
+
+// The choice with c in fp32 and experts beside it; every lane returns the
+// expert of slot `lane` (lane < K).
 template <typename T, int N>
 __device__ __noinline__ int choose_exact(const T* xrow, const float* bias, const Shape sh) {
     const int lane = threadIdx.x & 31, E = sh.experts;
@@ -280,30 +300,62 @@ __device__ __noinline__ int choose_exact(const T* xrow, const float* bias, const
         if (xv == -INFINITY) return 0.f;
         return sh.sigmoid ? sigmoid(xv) : exp1(xv - m) * inv_d;
     };
-    const float err = (sh.sigmoid ? 1.f : inv_d) * 0x1p-19f;  // twice the bound of a score
+    // twice the bound of a score: without the SFU's error 2^-21 (2^-22 s_max
+    // for a sigmoid's exponential, sum and quotient; a softmax's rounded
+    // difference makes it as large again)
+    const float err = (sh.sigmoid ? 1.f : inv_d) * (sh.sigmoid ? 0x1p-21f : 0x1p-20f);
 
     // the value that is compared, as an order key; 0 = takes no part
     uint32_t key[N];
+    float c32[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         float c = v[i];
         if (by_score && v[i] != -INFINITY) c = score(v[i]) + bias[i < count ? base + i : 0];
+        c32[i] = c;
         key[i] = i < count ? order_key(c + 0.f) : 0u;
     }
-    bool wide = false;
+    bool groups_near = false, near = false;
     if (sh.groups > 1) {
-        float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (i < count) {
-                float c = key_value(key[i]);
-                if (pair_sum && !by_score) c = v[i] == -INFINITY ? -INFINITY : score(v[i]);
-                b = fmaxf(b, fminf(a, c));
-                a = fmaxf(a, c);
+        // the two best with their places, to tell equal sums from near ones
+        float a = -INFINITY, b = -INFINITY, ax = 0.f, bx = 0.f, ab = 0.f, bb = 0.f;
+        auto take = [&](float c, float x, float bi) {
+            if (c > a) {
+                b = a, bx = ax, bb = ab;
+                a = c, ax = x, ab = bi;
+            } else if (c > b) {
+                b = c, bx = x, bb = bi;
             }
+        };
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < count && v[i] != -INFINITY)
+                take(pair_sum && !by_score ? score(v[i]) : c32[i], v[i],
+                     by_score ? bias[base + i] : 0.f);
+        for (int o = sh.lanes / 2; o > 0; o >>= 1) {
+            const float oa = __shfl_xor_sync(kFullMask, a, o), ob = __shfl_xor_sync(kFullMask, b, o);
+            const float oax = __shfl_xor_sync(kFullMask, ax, o), obx = __shfl_xor_sync(kFullMask, bx, o);
+            const float oab = __shfl_xor_sync(kFullMask, ab, o), obb = __shfl_xor_sync(kFullMask, bb, o);
+            take(oa, oax, oab);
+            take(ob, obx, obb);
         }
-        group_top2(sh, a, b);
-        if (!group_keep(sh, at_.group, pair_sum ? a + b : a, 2.f * err, !(by_score || pair_sum), wide)) {
+        if (!pair_sum) b = 0.f, bx = 0.f, bb = 0.f;
+        const float value = a + b, slack = 2.f * err;
+        bool border = false;
+        const bool keep = group_keep(sh, at_.group, value, slack, !(by_score || pair_sum), border);
+        if (__any_sync(kFullMask, border)) {
+            // groups within the slack of the last one taken must all be made
+            // of the same logits and biases: then the lower ones are right
+            const uint32_t low = warp_min(keep ? order_key(value + 0.f) : 0xffffffffu);
+            const float edge = key_value(low);
+            const bool in = at_.group < sh.groups &&
+                            fabsf(value - edge) <= 2.f * (slack + fabsf(edge) * 0x1p-21f);
+            const int src = __ffs(__ballot_sync(kFullMask, keep && order_key(value + 0.f) == low)) - 1;
+            auto same = [&](float t) { return t == __shfl_sync(kFullMask, t, src); };
+            const bool equal = same(a) & same(ax) & same(ab) & same(b) & same(bx) & same(bb);
+            groups_near = __any_sync(kFullMask, in && !equal) || edge != edge;
+        }
+        if (!keep) {
 #pragma unroll
             for (int i = 0; i < N; ++i) key[i] = 0u;
         }
@@ -324,7 +376,7 @@ __device__ __noinline__ int choose_exact(const T* xrow, const float* bias, const
     };
     local_best();
     int mine = 0;
-    float prev_c = 0.f, prev_x = 0.f, prev_b = 0.f;
+    float prev_c = 0.f, prev_x = 0.f, prev_b = 0.f, slack = 0.f;
     for (int k = 0; k < sh.K; ++k) {
         const uint32_t top = warp_max(best);
         const int src = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
@@ -332,12 +384,12 @@ __device__ __noinline__ int choose_exact(const T* xrow, const float* bias, const
         if (lane == k) mine = e;
         if (by_score) {
             const float c = key_value(top), be = bias[e], xv = widen(xrow[e]);
-            if (k > 0 && c != -INFINITY && !(prev_c - c > err + fabsf(prev_c) * 0x1p-22f) &&
-                !(xv == prev_x && be == prev_b))
-                wide = true;
+            if (k > 0 && c != -INFINITY && !(prev_c - c > slack) && !(xv == prev_x && be == prev_b))
+                near = true;
             prev_c = c;
             prev_x = xv;
             prev_b = be;
+            slack = err + fabsf(c) * 0x1p-22f;
         }
         if (lane == src) {
 #pragma unroll
@@ -346,20 +398,18 @@ __device__ __noinline__ int choose_exact(const T* xrow, const float* bias, const
             local_best();
         }
     }
-    if (by_score && prev_c != -INFINITY) {
+    if (by_score && prev_c != -INFINITY && best != 0u && !(key_value(best) < prev_c - slack)) {
         // experts left out that are too near the last one taken
-        const float border = prev_c - (err + fabsf(prev_c) * 0x1p-22f);
-        bool near = false;
-        if (best != 0u && !(key_value(best) < border)) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (key[i] != 0u && !(key_value(key[i]) < border) &&
-                    !(v[i] == prev_x && bias[base + i] == prev_b))
-                    near = true;
-        }
-        wide = wide || __any_sync(kFullMask, near);
+        for (int i = 0; i < N; ++i)
+            if (key[i] != 0u && !(key_value(key[i]) < prev_c - slack) &&
+                !(v[i] == prev_x && bias[base + i] == prev_b))
+                near = true;
     }
-    return wide ? choose_wide<T>(xrow, bias, sh, m) : mine;
+    near = __any_sync(kFullMask, near);
+    if (groups_near || near)
+        mine = choose_wide<T, N>(xrow, bias, sh, m, c32, prev_c - 2.f * slack, groups_near);
+    return mine;
 }
 
 // Descending order of N (a power of two, at most 8) values by a network.
