@@ -41,9 +41,8 @@ constexpr int kMaxExperts = 1024;
 
 struct Shape {
     int experts, K, groups, topk_groups, group_top;
-    int lanes;     // lanes per group (a power of two)
+    int lanes, lanes_log2;  // lanes per group (a power of two)
     int per_lane;  // experts per lane
-    int index_mask;  // experts up to a power of two, less one
     int slots;       // K up to a power of two: lanes per token after the choice
     int tokens;      // rows that a warp takes at a time, at most 32 / slots
     int sigmoid, renorm;
@@ -127,8 +126,8 @@ struct Place {
     int group, base, count;
     __device__ __forceinline__ explicit Place(const Shape& sh) {
         const int lane = threadIdx.x & 31, gsize = sh.experts / sh.groups;
-        group = lane / sh.lanes;
-        const int first = (lane % sh.lanes) * sh.per_lane;  // within the group
+        group = lane >> sh.lanes_log2;
+        const int first = (lane & (sh.lanes - 1)) * sh.per_lane;  // within the group
         base = group * gsize + first;
         count = group < sh.groups ? max(0, min(sh.per_lane, gsize - first)) : 0;
     }
@@ -154,7 +153,7 @@ __device__ __forceinline__ bool group_keep(const Shape& sh, int group, float val
     for (int r = 0; r < sh.topk_groups; ++r) {
         low = warp_max(left);
         const int first = __ffs(__ballot_sync(kFullMask, left == low)) - 1;
-        if (group == first / sh.lanes) {
+        if (group == first >> sh.lanes_log2) {
             keep = true;
             left = 0u;
         }
@@ -168,6 +167,42 @@ __device__ __forceinline__ bool group_keep(const Shape& sh, int group, float val
         }
     }
     return keep;
+}
+
+// The same run written.
+template <typename T, int N, bool VEC>
+__device__ __forceinline__ void store_run(T* p, int count, const float (&v)[N]) {
+    if constexpr (VEC) {
+        if (count == 0) return;
+        constexpr int bytes = N * int(sizeof(T));
+        uint32_t w[(bytes + 3) / 4];
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) w[i / 2] = pack_bf16x2(v[i], i + 1 < N ? v[i + 1] : 0.f);
+        }
+        if constexpr (bytes >= 16) {
+#pragma unroll
+            for (int i = 0; i < bytes / 16; ++i)
+                reinterpret_cast<uint4*>(p)[i] =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else if constexpr (bytes == 8) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        } else if constexpr (bytes == 4) {
+            *reinterpret_cast<uint32_t*>(p) = w[0];
+        } else {
+            *reinterpret_cast<uint16_t*>(p) = uint16_t(w[0]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < count) {
+                if constexpr (sizeof(T) == 4) p[i] = v[i];
+                else p[i] = __float2bfloat16_rn(v[i]);
+            }
+    }
 }
 
 // 64-bit order key of a double, and back.
@@ -244,7 +279,7 @@ __device__ __noinline__ int choose_wide(const T* xrow, const float* bias, const 
         for (int r = 0; r < sh.topk_groups; ++r) {
             const long long top = warp_max_wide(left);
             const int first = __ffs(__ballot_sync(kFullMask, left == top)) - 1;
-            if (at_.group == first / sh.lanes) {
+            if (at_.group == first >> sh.lanes_log2) {
                 keep = true;
                 left = kNoneWide;
             }
@@ -456,7 +491,7 @@ __device__ __forceinline__ float slot_max(float v, int width) {
 // left, slot by slot, for all of them at once: lane t * slots + k has slot k of
 // token t (slots: K up to a power of two).
 template <typename T, int N, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, N <= 8 ? 6 : 3)
 route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __restrict__ weights,
              int* __restrict__ idx, int64_t rows, const Shape sh) {
     const int lane = threadIdx.x & 31;
@@ -468,7 +503,9 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
     const bool pair_sum = sh.groups > 1 && sh.group_top == 2;
     const bool need_scores = by_score || pair_sum;
     const bool need_sum = !sh.sigmoid && (need_scores || !sh.renorm);
-    const int low_bits = sh.index_mask;  // of a key: the expert, counted down
+    constexpr int low_bits = N - 1;  // of a key: the place in the run, counted down
+    __shared__ int chosen_at[kWarps][32];
+    int* const chosen = chosen_at[threadIdx.x >> 5];  // experts, slot by slot
     const int my_token = lane / sh.slots, my_slot = lane % sh.slots;
     float be[N];
 #pragma unroll
@@ -543,7 +580,7 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 key[i] = keep && i < count
-                             ? ((signed_key(c[i] + 0.f) & ~low_bits) | (low_bits - (base + i)))
+                             ? ((signed_key(c[i] + 0.f) & ~low_bits) | (low_bits - i))
                              : kNone;
 
             // K rounds, and one for the best that is left out
@@ -559,9 +596,12 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
             const int slot_here = my_token == t ? my_slot : -1;
             for (int k = 0; k < K; ++k) {
                 const int best = lane_best();
-                const int top = __reduce_max_sync(kFullMask, best);
+                const int top = __reduce_max_sync(kFullMask, best & ~low_bits);
                 if (slot_here == k) mine = top;
-                const bool taken = best == top;  // one lane: keys differ in their experts
+                // the lowest lane among equals has the lowest expert
+                const int src = __ffs(__ballot_sync(kFullMask, (best & ~low_bits) == top)) - 1;
+                const bool taken = lane == src;
+                if (taken) chosen[t * sh.slots + k] = base + low_bits - (best & low_bits);
                 if constexpr (N <= 8) {
 #pragma unroll
                     for (int i = 0; i + 1 < N; ++i) key[i] = taken ? key[i + 1] : key[i];
@@ -569,10 +609,10 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
                 } else if (taken) {
 #pragma unroll
                     for (int i = 0; i < N; ++i)
-                        if (key[i] == top) key[i] = kNone;
+                        if (key[i] == best) key[i] = kNone;
                 }
             }
-            const int next = __reduce_max_sync(kFullMask, lane_best());
+            const int next = __reduce_max_sync(kFullMask, lane_best() & ~low_bits);
             if (slot_here == K - 1) after = next;
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] = ahead[i];
@@ -581,7 +621,9 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
         // ---- slot by slot: is the order certain?
         const bool real = my_token < tokens && my_slot < K;
         const T* xrow = x + (row0 + my_token) * E;
-        int e = min(low_bits - (mine & low_bits), E - 1);
+        __syncwarp();
+        int e = real ? min(chosen[lane], E - 1) : 0;
+        __syncwarp();
         float xm = real ? widen(xrow[e]) : -INFINITY;
         const float err = (sh.sigmoid ? 1.f : inv_slot) * 0x1p-19f;  // twice the bound of a score
         if (by_score || sizeof(T) == 4) {
@@ -589,10 +631,10 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
             if (my_slot != K - 1) after = below;
             bool near;
             if (by_score) {
-                const float va = signed_value(mine & ~low_bits), vb = signed_value(after & ~low_bits);
+                const float va = signed_value(mine), vb = signed_value(after);
                 near = !(va - vb > err + (fabsf(va) + fabsf(vb)) * float(low_bits + 2) * 0x1p-23f);
             } else {
-                near = (mine & ~low_bits) == (after & ~low_bits);
+                near = mine == after;
             }
             near = near && real && after >= kMissing;
             if (__any_sync(kFullMask, near)) {
@@ -650,59 +692,97 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
 // Only the plain softmax gives every logit a gradient; the others are zero
 // outside the chosen experts, whose logits alone are read.  One read of what
 // is needed and one write of the dense row: memory bound.
+//
+// A warp takes `tokens` rows at a time, lane t * slots + k slot k of row t, as
+// in the choice: what the slots add is worked out for all of them at once,
+// the rows are written in whole vectors without it, and then each slot's lane
+// writes its expert's value over the row's.  Slots that name one expert twice
+// are summed in slot order by the first of them, which alone writes.
 template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32)
 route_bwd_kernel(const T* __restrict__ x, const int* __restrict__ idx,
                  const float* __restrict__ dweights, T* __restrict__ dx, int64_t rows,
                  const Shape sh) {
-    __shared__ alignas(16) float buffer[N <= 2 ? 1 : kWarps][N <= 2 ? 1 : 32 * N];
     const int lane = threadIdx.x & 31;
-    const int E = sh.experts;
+    const int E = sh.experts, K = sh.K;
     const int base = lane * sh.per_lane;
     const int count = max(0, min(sh.per_lane, E - base));
     const bool all = !sh.sigmoid && !sh.renorm;
-    for (int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < rows;
-         row += int64_t(gridDim.x) * kWarps) {
-        const T* xrow = x + row * E;
-        // lane k: slot k's expert, logit and gradient; an expert outside the
-        // row takes no part
+    const int my_token = lane / sh.slots, my_slot = lane % sh.slots;
+    const int64_t step = int64_t(gridDim.x) * kWarps * sh.tokens;
+    for (int64_t row0 = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * sh.tokens; row0 < rows;
+         row0 += step) {
+        const int tokens = int(min(int64_t(sh.tokens), rows - row0));
+        const int64_t my_row = row0 + my_token;
+        // this slot's expert, logit and gradient; an expert outside the row
+        // takes no part
         int e = -1;
         float xk = -INFINITY, g = 0.f;
-        if (lane < sh.K) {
-            e = idx[row * sh.K + lane];
+        if (my_token < tokens && my_slot < K) {
+            e = idx[my_row * K + my_slot];
             if (e < 0 || e >= E) e = -1;
             if (e >= 0) {
-                xk = widen(xrow[e]);
-                g = dweights[row * sh.K + lane] * sh.scale;
+                xk = widen(x[my_row * E + e]);
+                g = dweights[my_row * K + my_slot] * sh.scale;
             }
         }
         const bool live = xk != -INFINITY;
+        // lanes of one token that name one expert
+        const uint32_t same = __match_any_sync(kFullMask, e >= 0 ? my_token * kMaxExperts + e : -1 - lane);
+        float slot = 0.f;  // what this slot adds to its expert's logit
+        float m_row = 0.f, inv_row = 0.f;
         float v[N];
-        float slot;  // what slot k adds to its expert's logit
         if (all) {
-            load_run<T, N, VEC>(xrow + base, count, v);
-            float m = v[0];
+            // every row's maximum and sum, kept by its slots' lanes
+            for (int t = 0; t < tokens; ++t) {
+                load_run<T, N, VEC>(x + (row0 + t) * E + base, count, v);
+                float m = v[0];
 #pragma unroll
-            for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
-            m = key_value(warp_max(order_key(m + 0.f)));
-            const float ref = m == -INFINITY ? 0.f : m;
-            float d = 0.f;
+                for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+                m = key_value(warp_max(order_key(m + 0.f)));
+                if (m == -INFINITY) m = 0.f;
+                float d = 0.f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                v[i] = v[i] == -INFINITY ? 0.f : exp1(v[i] - ref);
-                d += v[i];
+                for (int i = 0; i < N; i += 2) {
+                    const float2 p = exp_pair<false>(
+                        make_float2(v[i] - m, i + 1 < N ? v[i + 1] - m : -INFINITY));
+                    d += p.x + p.y;
+                    v[i] = p.x;
+                    if (i + 1 < N) v[i + 1] = p.y;
+                }
+                d = warp_sum(d);
+                const float inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
+                // D of this row from its slots
+                float part = 0.f;
+                if (my_token == t) {
+                    m_row = m;
+                    inv_row = inv_d;
+                    if (live) part = g * (exp1(xk - m) * inv_d);
+                }
+                const float D = warp_sum(part);
+                if (my_token == t) slot = D;
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] *= -inv_d * D;
+                store_run<T, N, VEC>(dx + (row0 + t) * E + base, count, v);
             }
-            d = warp_sum(d);
-            const float inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
-            const float sk = live ? exp1(xk - ref) * inv_d : 0.f;
-            const float D = warp_sum(g * sk);
-            slot = live ? g * sk : 0.f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] *= -inv_d * D;
+            // the slot's own value: s (g - D), with D taken off once below
+            const float s = live ? exp1(xk - m_row) * inv_row : 0.f;
+            const float D = slot;
+            float sum = 0.f;
+            if (__any_sync(kFullMask, __popc(same) > 1)) {
+#pragma unroll 1
+                for (int k = 0; k < 32; ++k) {
+                    const float gk = __shfl_sync(kFullMask, g, k);
+                    if ((same >> k) & 1) sum += gk;
+                }
+            } else {
+                sum = g;
+            }
+            slot = s * (sum - D);
         } else {
             float top = 0.f, w;
             if (sh.renorm) {
-                top = key_value(warp_max(order_key((live ? xk : -INFINITY) + 0.f)));
+                top = slot_max(live ? xk : -INFINITY, sh.slots);
                 if (sh.sigmoid) top = fminf(top, 0.f);
             }
             const float s = sh.sigmoid ? sigmoid(xk) : 0.f;
@@ -715,94 +795,34 @@ route_bwd_kernel(const T* __restrict__ x, const int* __restrict__ idx,
             if (!live) w = 0.f;
             float D = 0.f;
             if (sh.renorm) {
-                const float sum = warp_sum(w);
+                const float sum = slot_sum(w, sh.slots);
                 w = sum > 0.f ? __fdiv_rn(w, sum) : 0.f;
-                D = warp_sum(g * w);
+                D = slot_sum(g * w, sh.slots);
             }
             slot = w * (g - D);
             if (sh.sigmoid) slot *= sigmoid(-xk);
             if (!live) slot = 0.f;
+            if (__any_sync(kFullMask, __popc(same) > 1)) {
+                float sum = 0.f;
+#pragma unroll 1
+                for (int k = 0; k < 32; ++k) {
+                    const float a = __shfl_sync(kFullMask, slot, k);
+                    if ((same >> k) & 1) sum += a;
+                }
+                slot = sum;
+            }
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] = 0.f;
+            for (int t = 0; t < tokens; ++t)
+                store_run<T, N, VEC>(dx + (row0 + t) * E + base, count, v);
         }
-        if constexpr (N <= 2) {
-            for (int k = 0; k < sh.K; ++k) {
-                const int ek = __shfl_sync(kFullMask, e, k) - base;
-                const float add = __shfl_sync(kFullMask, slot, k);
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (i == ek) v[i] += add;
-            }
-        } else {
-            // every lane's run into shared memory, the slots' parts added there
-            // (one by one where an expert is named twice, so that the order of
-            // the sum is fixed), and the runs back
-            float* mine = buffer[threadIdx.x >> 5];
-            if constexpr (VEC) {
-#pragma unroll
-                for (int i = 0; i < N; i += 4)
-                    *reinterpret_cast<float4*>(mine + base + i) =
-                        make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (i < count) mine[base + i] = v[i];
-            }
-            __syncwarp();
-            const uint32_t same = __match_any_sync(kFullMask, e >= 0 ? e : -1 - lane);
-            if (!__any_sync(kFullMask, __popc(same) > 1)) {
-                if (e >= 0) mine[e] += slot;
-            } else {
-                for (int k = 0; k < sh.K; ++k) {
-                    if (lane == k && e >= 0) mine[e] += slot;
-                    __syncwarp();
-                }
-            }
-            __syncwarp();
-            if constexpr (VEC) {
-#pragma unroll
-                for (int i = 0; i < N; i += 4) {
-                    const float4 t = *reinterpret_cast<const float4*>(mine + base + i);
-                    v[i] = t.x, v[i + 1] = t.y, v[i + 2] = t.z, v[i + 3] = t.w;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (i < count) v[i] = mine[base + i];
-            }
-            __syncwarp();
+        __syncwarp();  // orders the rows' stores before the slots'
+        if (e >= 0 && (__ffs(same) - 1) == lane) {
+            T* at = dx + my_row * E + e;
+            if constexpr (sizeof(T) == 4) *at = slot;
+            else *at = __float2bfloat16_rn(slot);
         }
-        T* drow = dx + row * E + base;
-        if constexpr (VEC) {
-            constexpr int bytes = N * int(sizeof(T));
-            uint32_t w[(bytes + 3) / 4];
-            if constexpr (sizeof(T) == 4) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) w[i] = __float_as_uint(v[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; i += 2) w[i / 2] = pack_bf16x2(v[i], i + 1 < N ? v[i + 1] : 0.f);
-            }
-            if constexpr (bytes >= 16) {
-#pragma unroll
-                for (int i = 0; i < bytes / 16; ++i)
-                    __stcs(reinterpret_cast<uint4*>(drow) + i,
-                           make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
-            } else if constexpr (bytes == 8) {
-                *reinterpret_cast<uint2*>(drow) = make_uint2(w[0], w[1]);
-            } else if constexpr (bytes == 4) {
-                *reinterpret_cast<uint32_t*>(drow) = w[0];
-            } else {
-                *reinterpret_cast<uint16_t*>(drow) = uint16_t(w[0]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i < count) {
-                    if constexpr (sizeof(T) == 4) drow[i] = v[i];
-                    else drow[i] = __float2bfloat16_rn(v[i]);
-                }
-        }
+        __syncwarp();
     }
 }
 

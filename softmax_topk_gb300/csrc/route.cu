@@ -19,9 +19,11 @@ Shape make_shape(const RouteArgs& a, int groups) {
     s.topk_groups = a.topk_groups;
     s.group_top = a.group_top;
     s.lanes = 1;
-    while (s.lanes * 2 * groups <= 32) s.lanes *= 2;
+    while (s.lanes * 2 * groups <= 32) {
+        s.lanes *= 2;
+        ++s.lanes_log2;
+    }
     s.per_lane = (a.experts / groups + s.lanes - 1) / s.lanes;
-    s.index_mask = pow2_at_least(a.experts) - 1;
     s.slots = pow2_at_least(a.K);
     s.tokens = 1;
     s.sigmoid = a.score == OS_SCORE_SIGMOID;
@@ -42,15 +44,20 @@ int64_t grid_for(int64_t rows, int tokens) {
     return min64(ceil_div(rows, int64_t(route::kWarps) * tokens), int64_t(1) << 22);
 }
 
+// Rows per warp: one while the GPU has warps to spare (the latency of one
+// row), else several, which share the work after the choice.
+bool share_rows(const RouteArgs& a, Shape& s) {
+    const DeviceInfo* dev = device_info();
+    if (!dev) return false;
+    while (s.tokens * 2 * s.slots <= 32 && a.rows >= int64_t(dev->sms) * 32 * s.tokens * 2)
+        s.tokens *= 2;
+    return true;
+}
+
 template <typename T, int N>
 cudaError_t launch_fwd(const RouteArgs& a, Shape s, float* weights, int32_t* idx,
                        cudaStream_t stream) {
-    // one row per warp while the GPU has warps to spare (the latency of one
-    // row), else several, which share the work after the choice
-    const DeviceInfo* dev = device_info();
-    if (!dev) return cudaErrorInvalidDevice;
-    while (s.tokens * 2 * s.slots <= 32 && a.rows >= int64_t(dev->sms) * 32 * s.tokens * 2)
-        s.tokens *= 2;
+    if (!share_rows(a, s)) return cudaErrorInvalidDevice;
     auto k = route::route_kernel<T, N, false>;
     if constexpr (N <= 32)  // groups of 33 to 64 experts to a lane never fill it
         if (whole_runs(s, N, sizeof(T), a.x, a.x)) k = route::route_kernel<T, N, true>;
@@ -60,11 +67,12 @@ cudaError_t launch_fwd(const RouteArgs& a, Shape s, float* weights, int32_t* idx
 }
 
 template <typename T, int N>
-cudaError_t launch_bwd(const RouteArgs& a, const Shape& s, const int32_t* idx,
+cudaError_t launch_bwd(const RouteArgs& a, Shape s, const int32_t* idx,
                        const float* dweights, void* dx, cudaStream_t stream) {
+    if (!share_rows(a, s)) return cudaErrorInvalidDevice;
     auto k = whole_runs(s, N, sizeof(T), a.x, dx) ? route::route_bwd_kernel<T, N, true>
                                                   : route::route_bwd_kernel<T, N, false>;
-    return launch_kernel(k, grid_for(a.rows, 1), route::kWarps * 32, 1, 0, stream,
+    return launch_kernel(k, grid_for(a.rows, s.tokens), route::kWarps * 32, 1, 0, stream,
                          static_cast<const T*>(a.x), reinterpret_cast<const int*>(idx), dweights,
                          static_cast<T*>(dx), a.rows, s);
 }
