@@ -95,32 +95,68 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 constexpr uint32_t kKeyNegInf = 0x007fffffu;  // order_key(-inf)
 
-// A row's weight function: w(x) = e^((x - m) / T) as a multiple of 2^-bits.
+// p 2^64 as an integer, p in [0, 1).
+__device__ __forceinline__ u64 fraction64(float p) {
+    const uint32_t b = __float_as_uint(p);
+    const int shift = int(b >> 23) - 127 + 41;  // p = mantissa 2^(shift - 64)
+    const u64 mantissa = (b & 0x7fffffu) | 0x800000u;
+    if (shift < -23) return 0;  // also 0 and subnormal numbers
+    return shift >= 0 ? mantissa << shift : mantissa >> -shift;
+}
+
+// A row's weight function: w(x) = e^((x - m) / T) up to a constant factor of the
+// row, as a multiple of 2^-bits.
 //
-// (x - m) 32 log2 e / T = 32 n + j + g, |g| <= 1/2 and 2^(g/32) = e^y with
-// y = g ln 2 / 32; w = 2^n 2^(j/32) (1 + (e^y - 1)).  Every product whose
-// rounding would show at 2^-38 carries its residual, and the two parts of w are
-// turned into integers by adding a constant whose last bit is their unit (all
-// on the FMA and integer pipes: the conversion instructions run at an eighth
-// of their rate, 256 rows of 128256 columns took 141 us with them).
+// With c = 32 log2 e / T in two fp32 parts, the exponent is 32 n + j + g, |g| <=
+// 1/2, and 2^(g/32) = e^y with y = g ln 2 / 32; w = 2^n 2^(j/32) (1 + (e^y -
+// 1)).  Every product whose rounding would show at 2^-38 carries its residual,
+// and the two parts of w are turned into integers by adding a constant whose
+// last bit is their unit (on the FMA and integer pipes: the conversion
+// instructions run at an eighth of their rate).  Two ways:
+//   plain rows (nearly all): the exponent is x c - base with an integer base >
+//     m c, two values at a time on packed pairs, 32 FMA-pipe operations per
+//     column, which bound the sums' passes;
+//   any row: the exponent is (x - m) c, x - m in two parts; w(m) = 1.
 struct Weight {
-    float m, c_hi, c_lo;  // maximum; 32 log2 e / T in two parts
+    float m, c_hi, c_lo;  // maximum; c
     float unit;           // 1.5 * 2^(23 - bits): its last bit is 2^-bits
+    float origin;         // plain rows: the rounding constant less the base
+    float clamp;          // plain rows: a lower x may stand in for any lower one
     int bits;             // 31..44
+    bool plain;
     const float* table;   // kPow2 in shared memory
 
-    __device__ __forceinline__ void set(float m_, double temperature, int bits_, const float* t) {
+    __device__ __forceinline__ void set(float m_, float temperature, int bits_, const float* t) {
+        constexpr float kHi = 0x1.715476p+5f, kLo = 0x1.4ae0cp-21f;  // 32 log2 e
         m = m_;
-        const double c = fmin(46.166241308446829036 / temperature, 1e30);
-        c_hi = float(c);
-        c_lo = float(c - double(c_hi));
+        c_hi = fminf(__fdiv_rn(kHi, temperature), 1e30f);
+        c_lo = c_hi < 1e30f && c_hi > 1e-30f
+                   ? __fdiv_rn(fmaf(-c_hi, temperature, kHi) + kLo, temperature) : 0.f;
         bits = bits_;
         unit = 1.5f * __int_as_float((23 - bits + 127) << 23);
         table = t;
+        clamp = m - __fdiv_rn(1920.f, c_hi);  // 2^-60
+        // the clamp, as rounded, still far below every weight that counts, and
+        // exponents small enough for their residuals
+        plain = c_hi > 1e-30f && fabsf(m) * c_hi < 12000.f && fabsf(clamp) * c_hi < 14000.f &&
+                (m - clamp) * c_hi > 1600.f;
+        origin = expc::kRound - (ceilf(m * c_hi) + 1.f);
     }
 
-    // w = hi 2^-22 + lo 2^-bits
-    __device__ __forceinline__ void parts(float x, uint32_t& hi, int& lo) const {
+    // 2^g/32 times the table's value: t (1 + (e^y - 1)) = wh + wl
+    static __device__ __forceinline__ void scale(float g, float gl, float t, float t_lo, float& wh,
+                                                 float& wl) {
+        constexpr float kL = 0x1.62e43p-6f, kLLo = -0x1.05c61p-34f;  // ln 2 / 32
+        const float yh = __fmul_rn(g, kL);
+        const float yl = fmaf(g, kL, -yh) + fmaf(gl, kL, g * kLLo);
+        const float poly = fmaf(yh, fmaf(yh, 0x1.555556p-5f, 0x1.555556p-3f), 0.5f);
+        const float q = __fmul_rn(yh * yh, poly);
+        const float eh = yh + q, el = (q - (eh - yh)) + yl;  // e^y - 1
+        wh = fmaf(t, eh, t);
+        wl = fmaf(t, el, fmaf(t, eh, t - wh) + fmaf(t_lo, eh, t_lo));
+    }
+    // e^((x - m) / T) = (wh + wl) 2^n by the second way; n below -60 is -200
+    __device__ __forceinline__ void relative(float x, float& wh, float& wl, int& n) const {
         const float dh = x - m;
         const float bb = dh - x;
         const float dl = (x - (dh - bb)) + (-m - bb);  // x - m = dh + dl exactly
@@ -129,25 +165,69 @@ struct Weight {
         const float uf = th + expc::kRound;
         const float gh = th - (uf - expc::kRound);
         const float g = gh + tl;
-        const float gl = tl - (g - gh);
-        constexpr float kL = 0x1.62e43p-6f, kLLo = -0x1.05c61p-34f;  // ln 2 / 32
-        const float yh = __fmul_rn(g, kL);
-        const float yl = fmaf(g, kL, -yh) + fmaf(gl, kL, g * kLLo);
-        const float poly = fmaf(yh, fmaf(yh, 0x1.555556p-5f, 0x1.555556p-3f), 0.5f);
-        const float q = __fmul_rn(yh * yh, poly);
-        const float eh = yh + q, el = (q - (eh - yh)) + yl;  // e^y - 1
         const int i = __float_as_int(uf);  // the constant's bits are a multiple of 32
-        const float t = table[i & 31], t_lo = table[32 + (i & 31)];
-        const float wh = fmaf(t, eh, t);
-        const float wl = fmaf(t, el, fmaf(t, eh, t - wh) + fmaf(t_lo, eh, t_lo));
-        // 2^n: n is the constant's distance, moved to the exponent field
-        const float s = __int_as_float(((i & ~31) << 18) + 0x3f800000);
+        scale(g, tl - (g - gh), table[i & 31], table[32 + (i & 31)], wh, wl);
+        n = (i - __float_as_int(expc::kRound)) >> 5;
+        if (!(th > -4000.f)) n = -200;                // below 2^-125, -inf
+        if (x == m) wh = 1.f, wl = 0.f, n = 0;        // also m = +inf
+    }
+    // (wh + wl) 2^n = hi 2^-22 + lo 2^-bits
+    __device__ __forceinline__ void fix(float wh, float wl, int n, uint32_t& hi, int& lo) const {
+        const float s = __int_as_float((max(n, -100) + 127) << 23);
         const float big = fmaf(wh, s, 3.f);  // last bit 2^-22
         const float rest = fmaf(wl, s, fmaf(wh, s, -(big - 3.f)));
         hi = __float_as_uint(big) - __float_as_uint(3.f);
         lo = __float_as_int(rest + unit) - __float_as_int(unit);
-        if (!(th > -1920.f)) hi = 0, lo = 0;           // below 2^-60, -inf
-        if (x == m) hi = 1u << 22, lo = 0;             // also m = +inf
+    }
+    // The first way, two values at a time, for x in [clamp, m].  Negated values
+    // save the sign changes that the packed forms lack.
+    __device__ __forceinline__ void parts2(float2 x, uint32_t (&hi)[2], int (&lo)[2]) const {
+        const float2 minus = splat2(-1.f), K = splat2(origin);
+        const float2 np = mul2(x, splat2(-c_hi));
+        const float2 pl = fma2(x, splat2(c_lo), fma2(x, splat2(c_hi), np));
+        const float2 uf = fma2(np, minus, K);
+        const float2 gh = fma2(np, minus, fma2(uf, minus, K));
+        const float2 g = add2(gh, pl);
+        const float2 gl = fma2(fma2(gh, minus, g), minus, pl);
+        constexpr float kL = 0x1.62e43p-6f, kLLo = -0x1.05c61p-34f;  // ln 2 / 32
+        const float2 yh = mul2(g, splat2(kL));
+        const float2 nyl = fma2(g, splat2(-kL), yh);
+        const float2 yl = fma2(nyl, minus, fma2(g, splat2(kLLo), mul2(gl, splat2(kL))));
+        const float2 poly = fma2(yh, fma2(yh, splat2(0x1.555556p-5f), splat2(0x1.555556p-3f)),
+                                 splat2(0.5f));
+        const float2 yy = mul2(yh, yh);
+        const float2 eh = fma2(yy, poly, yh);  // e^y - 1
+        const float2 el = add2(fma2(yy, poly, fma2(eh, minus, yh)), yl);
+        const int i0 = __float_as_int(uf.x), i1 = __float_as_int(uf.y);
+        const float2 t = make_float2(table[i0 & 31], table[i1 & 31]);
+        const float2 t_lo = make_float2(table[32 + (i0 & 31)], table[32 + (i1 & 31)]);
+        const float2 wh = fma2(t, eh, t);
+        const float2 wl = fma2(t, el, add2(fma2(t, eh, fma2(wh, minus, t)), fma2(t_lo, eh, t_lo)));
+        // 2^n: n is the rounding constant's distance, moved to the exponent field
+        const float2 s = make_float2(__int_as_float(((i0 & ~31) << 18) + 0x3f800000),
+                                     __int_as_float(((i1 & ~31) << 18) + 0x3f800000));
+        const float2 big = fma2(wh, s, splat2(3.f));
+        const float2 rest = fma2(wl, s, fma2(wh, s, fma2(big, minus, splat2(3.f))));
+        const float2 end = add2(rest, splat2(unit));
+        hi[0] = __float_as_uint(big.x) - __float_as_uint(3.f);
+        hi[1] = __float_as_uint(big.y) - __float_as_uint(3.f);
+        lo[0] = __float_as_int(end.x) - __float_as_int(unit);
+        lo[1] = __float_as_int(end.y) - __float_as_int(unit);
+    }
+    __device__ __forceinline__ void parts(float x, uint32_t& hi, int& lo) const {
+        if (plain) {  // the same operations as a pair's, so that sums agree to the bit
+            uint32_t h[2];
+            int l[2];
+            const float y = fmaxf(x, clamp);
+            parts2(make_float2(y, y), h, l);
+            hi = h[0], lo = l[0];
+        } else {
+            float wh, wl;
+            int n;
+            relative(x, wh, wl, n);
+            fix(wh, wl, n, hi, lo);
+            if (n < -60) hi = 0, lo = 0;
+        }
     }
     __device__ __forceinline__ u64 join(uint32_t hi, int lo) const {
         const long long w = static_cast<long long>(u64(hi) << (bits - 22)) + lo;
@@ -159,71 +239,31 @@ struct Weight {
         parts(x, hi, lo);
         return join(hi, lo);
     }
-    // Whether parts2 holds: the row's values clamped at least() are finite and
-    // the clamp, as rounded, is still far below every weight that counts.
-    __device__ __forceinline__ bool plain() const {
-        return c_hi > 1e-30f && fabsf(m) < 1e30f && fabsf(least()) < 1e30f &&
-               (m - least()) * c_hi > 1600.f;
-    }
-    // weights below this are 0 (2^-60); a lower x may stand in for any lower one
-    __device__ __forceinline__ float least() const { return m - 1920.f / c_hi; }
-
-    // parts() of two values at a time on packed fp32 pairs, for x in [least(), m]
-    // and plain() rows; negated values save the sign changes that the packed
-    // forms lack.
-    __device__ __forceinline__ void parts2(float2 x, uint32_t (&hi)[2], int (&lo)[2]) const {
-        const float2 minus = splat2(-1.f), nm = splat2(-m), ch = splat2(c_hi), K = splat2(expc::kRound);
-        const float2 dh = add2(x, nm);
-        const float2 bb = fma2(x, minus, dh);
-        const float2 d1 = fma2(bb, minus, dh);
-        const float2 d2 = fma2(d1, minus, x);
-        const float2 dl = add2(d2, fma2(bb, minus, nm));
-        const float2 nth = mul2(dh, splat2(-c_hi));
-        const float2 tl = add2(fma2(dh, ch, nth), fma2(dh, splat2(c_lo), mul2(dl, ch)));
-        const float2 uf = fma2(nth, minus, K);
-        const float2 ngh = add2(nth, fma2(K, minus, uf));
-        const float2 g = fma2(ngh, minus, tl);
-        const float2 gl = fma2(add2(g, ngh), minus, tl);
-        constexpr float kL = 0x1.62e43p-6f, kLLo = -0x1.05c61p-34f;  // ln 2 / 32
-        const float2 nyh = mul2(g, splat2(-kL));
-        const float2 yl = add2(fma2(g, splat2(kL), nyh), fma2(gl, splat2(kL), mul2(g, splat2(kLLo))));
-        float2 poly = fma2(nyh, splat2(-0x1.555556p-5f), splat2(0x1.555556p-3f));
-        poly = fma2(nyh, mul2(poly, minus), splat2(0.5f));
-        const float2 q = mul2(mul2(nyh, nyh), poly);
-        const float2 eh = fma2(nyh, minus, q);
-        const float2 el = add2(fma2(add2(eh, nyh), minus, q), yl);
-        const int i0 = __float_as_int(uf.x), i1 = __float_as_int(uf.y);
-        const float2 t = make_float2(table[i0 & 31], table[i1 & 31]);
-        const float2 t_lo = make_float2(table[32 + (i0 & 31)], table[32 + (i1 & 31)]);
-        const float2 wh = fma2(t, eh, t);
-        const float2 wl = fma2(t, el, add2(fma2(t, eh, fma2(wh, minus, t)), fma2(t_lo, eh, t_lo)));
-        const float2 s = make_float2(__int_as_float(((i0 & ~31) << 18) + 0x3f800000),
-                                     __int_as_float(((i1 & ~31) << 18) + 0x3f800000));
-        const float2 big = fma2(wh, s, splat2(3.f));
-        const float2 rest = fma2(wl, s, fma2(wh, s, fma2(big, minus, splat2(3.f))));
-        const float2 end = add2(rest, splat2(unit));
-        hi[0] = __float_as_uint(big.x) - __float_as_uint(3.f);
-        hi[1] = __float_as_uint(big.y) - __float_as_uint(3.f);
-        lo[0] = __float_as_int(end.x) - __float_as_int(unit);
-        lo[1] = __float_as_int(end.y) - __float_as_int(unit);
+    // The share of x in a sum of weights, rounded once; a weight below the
+    // sums' last bit keeps its digits.
+    __device__ __forceinline__ float share(float x, u64 total) const {
+        float wh, wl;
+        int n;
+        relative(x, wh, wl, n);
+        const float e = n < -126 ? 0.f : (wh + wl) * __int_as_float((n + 127) << 23);
+        return float(double(e) * double((*this)(m)) / double(total));
     }
 
     // add(v, weight) for each of N values of at least `least_in`, and the summed
     // weights of the others.
     template <int N, typename Add>
-    __device__ __forceinline__ u64 hist(const float (&v)[N], float least_in, bool fast, Add add) const {
+    __device__ __forceinline__ u64 hist(const float (&v)[N], float least_in, Add add) const {
         uint32_t hi = 0;
         int lo = 0;
-        const float clamp = fast ? least() : -INFINITY;
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
             uint32_t h[2];
             int l[2];
-            if (fast) {
+            if (plain) {
                 parts2(make_float2(fmaxf(v[i], clamp), fmaxf(v[i + 1], clamp)), h, l);
             } else {
-                parts(fmaxf(v[i], clamp), h[0], l[0]);
-                parts(fmaxf(v[i + 1], clamp), h[1], l[1]);
+                parts(fmaxf(v[i], -INFINITY), h[0], l[0]);
+                parts(fmaxf(v[i + 1], -INFINITY), h[1], l[1]);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -234,14 +274,12 @@ struct Weight {
         return static_cast<u64>(static_cast<long long>(u64(hi) << (bits - 22)) + lo);
     }
 
-    // The summed weights of N values of at least `from` (finite); `fast` rows
-    // are plain() ones.
+    // The summed weights of N values of at least `from` (finite).
     template <int N>
-    __device__ __forceinline__ u64 sum_from(const float (&v)[N], float from, bool fast) const {
+    __device__ __forceinline__ u64 sum_from(const float (&v)[N], float from) const {
         uint32_t hi = 0;
         int lo = 0;
-        if (fast) {
-            const float clamp = least();
+        if (plain) {
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
                 uint32_t h[2];
@@ -297,6 +335,7 @@ struct Shared {
     u64 sum[kWarps];     // weights of a warp's run outside the histogram
     u64 draw[kWarps];   // kept weights of a warp's run
     u64 piece[kWarps];  // kept weights of a piece of the border's run
+    float floor_p;
     // rank 0's findings, read by the others
     uint32_t listed;    // columns put on the list (it may be more than fit)
     uint32_t bin;       // the border's step of the histogram
@@ -415,7 +454,7 @@ __device__ __forceinline__ u64 cta_sum(Shared& sh, u64 v) {
 // p (in [0, 1]) times `total`, rounded up: the least integer that is at least
 // the product.
 __device__ __forceinline__ u64 share_of(float p, u64 total) {
-    const u64 frac = __double2ull_rz(double(p) * 18446744073709551616.0);  // p < 1
+    const u64 frac = fraction64(p);  // p < 1
     const u64 want = __umul64hi(frac, total) + (frac * total != 0);
     return want > 0 ? want : 1;
 }
@@ -690,23 +729,28 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
 
         Weight w;
         const bool greedy = !(t_row > 0.f);
-        w.set(key_value(top_key), greedy ? 1.0 : double(t_row), bits, sh.table);
-        const bool fast = w.plain();
+        w.set(key_value(top_key), greedy ? 1.f : t_row, bits, sh.table);
         // the lowest logit that min-p keeps; compared in fp32 it decides as in
         // real arithmetic, since it is rounded up
         float floor_p = -FLT_MAX;
         if (mp > 0.f && !greedy) {
             const float q = fminf(mp, 1.f);
-            floor_p = q < 1.f ? __double2float_ru(double(w.m) + double(t_row) * log(double(q))) : w.m;
+            floor_p = w.m;
+            if (q < 1.f) {  // 64-bit arithmetic, slow here: one warp does it
+                if (warp == 0) {
+                    const float f = __double2float_ru(double(w.m) + double(t_row) * log(double(q)));
+                    if (lane == 0) sh.floor_p = f;
+                }
+                __syncthreads();
+                floor_p = sh.floor_p;
+            }
         }
         auto write = [&](int64_t c, float v, u64 total) {
             out[row] = int(c);
-            // the weight itself, not its integer: a small one keeps its digits
-            const double e = v == w.m ? 1.0 : exp((double(v) - double(w.m)) / double(t_row));
-            if (prob) prob[row] = greedy ? 1.f : float(ldexp(e, bits) / double(total));
+            if (prob) prob[row] = greedy ? 1.f : w.share(v, total);
         };
         auto target_of = [&](u64 total) {
-            return __umul64hi(__double2ull_rz(double(uu) * 18446744073709551616.0), total);
+            return __umul64hi(fraction64(uu), total);
         };
 
         bool done = false;
@@ -812,10 +856,10 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) near += __shfl_xor_sync(kFullMask, near, o);
                 const float pc = fmaxf(tp, 0.f);
-                const double small = (1.0 - double(pc)) * double(near) * 0.999 / double(cols);
-                double low = double(w.m) + double(t_row) * log(small);
-                low -= 1e-6 * (fabs(low) + fabs(double(w.m)) + double(t_row));
-                const float least = fmaxf(float(low), -FLT_MAX);
+                const float log_small = 0.6931472f * __log2f((1.f - pc) * near * 0.999f / float(cols));
+                const float low = w.m + t_row * log_small;
+                const float least = fmaxf(
+                    low - 1e-5f * (fabsf(w.m) + t_row * (1.f + fabsf(log_small))), -FLT_MAX);
                 const float steps = float(kBins) / (w.m - least);
                 if (w.m < INFINITY && steps > 0.f && steps < INFINITY) {
                     auto step_of = [&](float v) { return min(kBins - 1, int((w.m - v) * steps)); };
@@ -823,7 +867,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                     for (int64_t b = lo + lane; b < hi; b += 32) {
                         float v[EPV];
                         blocks.load(b, v);
-                        rest += w.hist(v, least, fast, [&](float y, u64 a) {
+                        rest += w.hist(v, least, [&](float y, u64 a) {
                             atomicAdd(&sh.mass[step_of(y)], a);
                         });
                     }
@@ -858,12 +902,17 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                     }
                     row_sync<S>();
                     const int bin = int(remote<S>(&sh.bin, 0));
+                    // step_of(v) == bin without a conversion
+                    auto in_step = [&](float v) {
+                        const float at = (w.m - v) * steps;
+                        return at >= float(bin) && (bin == kBins - 1 || at < float(bin + 1));
+                    };
                     for (int64_t b = bin < kBins ? lo + lane : hi; b < hi; b += 32) {
                         float v[EPV];
                         blocks.load(b, v);
 #pragma unroll
                         for (int i = 0; i < EPV; ++i)
-                            if (v[i] >= least && step_of(v[i]) == bin)
+                            if (v[i] >= least && in_step(v[i]))
                                 list_push<S>(sh, v[i], uint32_t(blocks.col(b) + i));
                     }
                     row_sync<S>();
@@ -924,7 +973,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                 blocks.load(b, v);
                 u64 a = 0;
                 if (!by_column) {
-                    a = w.sum_from(v, cut.value, fast);
+                    a = w.sum_from(v, cut.value);
                     if (cut.last != INT_MAX) {
 #pragma unroll
                         for (int i = 0; i < EPV; ++i)
