@@ -26,10 +26,11 @@
 //   top-k (<= 1024):   the columns at or above a bound that k of them reach
 //                      are listed in shared memory (a few times k), sorted,
 //                      and everything else happens on the list;
-//   top-p alone:       total weight; a histogram of weight over 2048 equal
-//                      steps of the logit down to where the rest could not
-//                      matter; the columns of the border's step are listed and
-//                      sorted, which gives the cut; then as without a filter;
+//   top-p alone:       a histogram of weight in fp32, over 2048 equal steps of
+//                      the logit down to where the rest could not matter, says
+//                      within what few steps the border lies; one pass sums the
+//                      weights above and below them per warp and lists their
+//                      columns, which are sorted and complete the sums;
 //   else (k larger, too many equal logits for the lists): the cut is found
 //                      digit by digit of the logits' order keys over the row.
 //
@@ -249,31 +250,20 @@ struct Weight {
         return float(double(e) * double((*this)(m)) / double(total));
     }
 
-    // add(v, weight) for each of N values of at least `least_in`, and the summed
-    // weights of the others.
-    template <int N, typename Add>
-    __device__ __forceinline__ u64 hist(const float (&v)[N], float least_in, Add add) const {
-        uint32_t hi = 0;
-        int lo = 0;
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            uint32_t h[2];
-            int l[2];
-            if (plain) {
-                parts2(make_float2(fmaxf(v[i], clamp), fmaxf(v[i + 1], clamp)), h, l);
-            } else {
-                parts(fmaxf(v[i], -INFINITY), h[0], l[0]);
-                parts(fmaxf(v[i + 1], -INFINITY), h[1], l[1]);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (v[i + j] >= least_in) add(v[i + j], join(h[j], l[j]));
-                else hi += h[j], lo += l[j];
-            }
+    // parts() of two values, in whichever way the row takes.
+    __device__ __forceinline__ void pair(float x, float y, uint32_t (&hi)[2], int (&lo)[2]) const {
+        if (plain) {
+            parts2(make_float2(fmaxf(x, clamp), fmaxf(y, clamp)), hi, lo);
+        } else {
+            parts(fmaxf(x, -INFINITY), hi[0], lo[0]);
+            parts(fmaxf(y, -INFINITY), hi[1], lo[1]);
         }
-        return static_cast<u64>(static_cast<long long>(u64(hi) << (bits - 22)) + lo);
     }
 
+    // What sums of parts amount to.
+    __device__ __forceinline__ u64 sum_of(uint32_t hi, int lo) const {
+        return static_cast<u64>(static_cast<long long>(u64(hi) << (bits - 22)) + lo);
+    }
     // The summed weights of N values of at least `from` (finite).
     template <int N>
     __device__ __forceinline__ u64 sum_from(const float (&v)[N], float from) const {
@@ -300,7 +290,7 @@ struct Weight {
                 if (x >= from) hi += h, lo += l;
             }
         }
-        return static_cast<u64>(static_cast<long long>(u64(hi) << (bits - 22)) + lo);
+        return sum_of(hi, lo);
     }
 };
 
@@ -331,16 +321,20 @@ struct Shared {
     float table[64];
     // exchanged over the cluster, one value per warp
     uint32_t top[kWarps], bound[kWarps];
-    float near[kWarps];  // weights of a warp's run, in fp32
-    u64 sum[kWarps];     // weights of a warp's run outside the histogram
-    u64 draw[kWarps];   // kept weights of a warp's run
+    float near[kWarps];  // weights of a warp's run, in fp32, to its own maximum
+    u64 sum[kWarps];     // weights of a warp's run outside the list
+    u64 draw[kWarps];    // kept weights of a warp's run (top-p: those above the list)
+    uint32_t slice;      // histogram's weight in this CTA's steps
+    uint32_t bin_lo, bin_hi;  // first and last step that may hold the border
     u64 piece[kWarps];  // kept weights of a piece of the border's run
     float floor_p;
     // rank 0's findings, read by the others
     uint32_t listed;    // columns put on the list (it may be more than fit)
-    uint32_t bin;       // the border's step of the histogram
     Cut cut;
-    u64 above, want;
+    uint32_t fine;      // the border's step when the listed ones are divided again
+    u64 fine_above;     // weight above it
+    u64 want;           // weight that the border reaches
+    u64 extra[kMaxCluster * kWarps];  // kept weights of a run's listed columns
     // scratch of one CTA
     u64 warp[kWarps];
     u64 result[2];
@@ -349,6 +343,7 @@ struct Shared {
     u64 list[kList];    // (order key << 32) | ~column
     union {
         u64 mass[kBins];
+        uint32_t steps[kBins];
         u64 sorted[kList];
     };
 };
@@ -662,6 +657,32 @@ struct Blocks {
         }
         return top;
     }
+    // The same with the sum d of 2^((x - maximum) c) in fp32.
+    __device__ __forceinline__ float maximum_and_sum(int64_t b, int64_t end, float c, float& d) const {
+        float top = -INFINITY;
+        d = 0.f;
+#pragma unroll 2
+        for (; b < end; b += 32) {
+            float v[EPV];
+            load(b, v);
+            float best = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < EPV; ++i) {
+                v[i] = fmaxf(v[i], -INFINITY);  // a NaN counts for nothing
+                best = fmaxf(best, v[i]);
+            }
+            if (best == -INFINITY) continue;
+            if (best > top) {
+                d *= ex2_sfu((top - best) * c);  // 0 at first
+                top = best;
+            }
+            float part = 0.f;
+#pragma unroll
+            for (int i = 0; i < EPV; ++i) part += ex2_sfu((v[i] - top) * c);
+            d += part;
+        }
+        return top;
+    }
 };
 
 template <typename T, int S>
@@ -689,9 +710,23 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
         const int full = int(blocks.count / per_warp);
         const bool list_k = by_k && k <= kTopK && k <= 32 * full;
 
-        // ---- the only pass over memory: maxima per thread
-        uint32_t key = order_key(blocks.maximum(lo + lane, hi));
+        // ---- the only pass over memory: maxima per thread, for top-p the weight
+        const bool by_p = !by_k && tp < 1.f && t_row > 0.f;
+        const float c_near = __fdiv_rn(1.442695041f, t_row);
+        float near = 0.f;
+        const float thread_top = by_p ? blocks.maximum_and_sum(lo + lane, hi, c_near, near)
+                                      : blocks.maximum(lo + lane, hi);
+        uint32_t key = order_key(thread_top);
         const uint32_t warp_top = __reduce_max_sync(kFullMask, key);
+        if (by_p) {
+            const float t = key_value(warp_top);
+            near = near > 0.f ? near * ex2_sfu((thread_top - t) * c_near) : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) near += __shfl_xor_sync(kFullMask, near, o);
+            if (lane == 0) sh.near[warp] = near;
+            for (int i = tid; i < kBins; i += kThreads) sh.steps[i] = 0;
+            if (tid < S * kWarps) sh.extra[tid] = 0;
+        }
         uint32_t bound = 0xffffffffu;
         if (list_k && rank * kWarps + warp < full) {
             // every such warp's j-th best thread maximum, j = ceil(k / warps):
@@ -714,7 +749,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
         }
         if (tid == 0) {
             sh.listed = 0;
-            sh.bin = kBins;  // none
+            sh.bin_lo = sh.bin_hi = kBins;  // none
             sh.cut = {NAN, 0};
         }
         row_sync<S>();
@@ -753,7 +788,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
             return __umul64hi(fraction64(uu), total);
         };
 
-        bool done = false;
+        bool done = false, have_runs = false;
         Cut cut = {-FLT_MAX, INT_MAX};
         if (top_key <= kKeyNegInf) {
             if (rank == 0 && tid == 0) {
@@ -826,33 +861,16 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                         }
                     }
                 }
-            } else if (!by_k && tp < 1.f) {
-                // ---- top-p: the border by a histogram of weight.  A total in
-                // fp32 (to 1e-4, the slack below) says how far down it may lie:
-                // columns of at most (1 - p) total / cols cannot reach it even
-                // together.
-                float near = 0.f;
-                {
-                    const float c = w.c_hi * 0.03125f;
-#pragma unroll 2
-                    for (int64_t b = lo + lane; b < hi; b += 32) {
-                        float v[EPV];
-                        blocks.load(b, v);
-                        float part = 0.f;
-#pragma unroll
-                        for (int i = 0; i < EPV; ++i)
-                            part += v[i] >= -FLT_MAX ? ex2_sfu((v[i] - w.m) * c) : 0.f;
-                        near += part;
-                    }
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) near += __shfl_xor_sync(kFullMask, near, o);
-                if (lane == 0) sh.near[warp] = near;
-                for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0;
-                row_sync<S>();
+            } else if (by_p) {
+                // ---- top-p.  The fp32 total says how far down the border may
+                // lie: columns of at most (1 - p) total / cols cannot reach it
+                // even together.
                 near = 0.f;
-                for (int i = lane; i < S * kWarps; i += 32)
-                    near += remote<S>(&sh.near[i % kWarps], i / kWarps);
+                for (int i = lane; i < S * kWarps; i += 32) {
+                    const float part = remote<S>(&sh.near[i % kWarps], i / kWarps);
+                    const float t = key_value(remote<S>(&sh.top[i % kWarps], i / kWarps));
+                    near += part > 0.f ? part * ex2_sfu((t - w.m) * c_near) : 0.f;
+                }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) near += __shfl_xor_sync(kFullMask, near, o);
                 const float pc = fmaxf(tp, 0.f);
@@ -861,86 +879,232 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                 const float least = fmaxf(
                     low - 1e-5f * (fabsf(w.m) + t_row * (1.f + fabsf(log_small))), -FLT_MAX);
                 const float steps = float(kBins) / (w.m - least);
-                if (w.m < INFINITY && steps > 0.f && steps < INFINITY) {
-                    auto step_of = [&](float v) { return min(kBins - 1, int((w.m - v) * steps)); };
-                    u64 rest = 0;
+                if (w.m < INFINITY && steps > 0.f && steps < INFINITY && near < INFINITY) {
+                    // weights in units of total 2^-31
+                    const float scale = 0x1p31f / near;
                     for (int64_t b = lo + lane; b < hi; b += 32) {
-                        float v[EPV];
-                        blocks.load(b, v);
-                        rest += w.hist(v, least, [&](float y, u64 a) {
-                            atomicAdd(&sh.mass[step_of(y)], a);
-                        });
-                    }
-                    rest = warp_sum64(rest);
-                    if (lane == 0) sh.sum[warp] = rest;
-                    row_sync<S>();
-                    if (rank == 0) {
-                        u64 total = 0;
-                        for (int i = lane; i < S * kWarps; i += 32)
-                            total += remote<S>(&sh.sum[i % kWarps], i / kWarps);
-                        total = warp_sum64(total);
-                        u64 part[kBins / kThreads], own = 0;
-#pragma unroll
-                        for (int i = 0; i < kBins / kThreads; ++i) {
-                            part[i] = 0;
-                            for (int r = 0; r < S; ++r)
-                                part[i] += remote<S>(&sh.mass[kBins / kThreads * tid + i], r);
-                            own += part[i];
-                        }
-                        const u64 upto = cta_prefix(sh, own);
-                        if (tid == kThreads - 1) sh.result[0] = upto;
-                        __syncthreads();
-                        const u64 want = share_of(pc, total + sh.result[0]);
-                        u64 run = upto - own;
-                        if (run < want && want <= upto) {
-                            int i = 0;
-                            while (i < kBins / kThreads - 1 && run + part[i] < want) run += part[i++];
-                            sh.bin = kBins / kThreads * tid + i;
-                            sh.above = run;
-                        }
-                        if (tid == 0) sh.want = want;
-                    }
-                    row_sync<S>();
-                    const int bin = int(remote<S>(&sh.bin, 0));
-                    // step_of(v) == bin without a conversion
-                    auto in_step = [&](float v) {
-                        const float at = (w.m - v) * steps;
-                        return at >= float(bin) && (bin == kBins - 1 || at < float(bin + 1));
-                    };
-                    for (int64_t b = bin < kBins ? lo + lane : hi; b < hi; b += 32) {
                         float v[EPV];
                         blocks.load(b, v);
 #pragma unroll
                         for (int i = 0; i < EPV; ++i)
-                            if (v[i] >= least && in_step(v[i]))
-                                list_push<S>(sh, v[i], uint32_t(blocks.col(b) + i));
+                            if (v[i] >= least)
+                                atomicAdd(&sh.steps[min(kBins - 1, int((w.m - v[i]) * steps))],
+                                          __float2uint_rn(ex2_sfu((v[i] - w.m) * c_near) * scale));
+                    }
+                    row_sync<S>();
+                    // every CTA adds up a share of the steps over the cluster;
+                    // the border lies where the running weight comes within
+                    // `slack` of p: every weight and the total are good to 1e-5
+                    // (a difference rounded, at most 60 octaves, and the SFU's
+                    // error), and half a unit per column is rounded away
+                    constexpr int kShare = kBins / S;
+                    constexpr int B = kShare > kThreads ? kShare / kThreads : 1;
+                    uint32_t part[B], own = 0;
+#pragma unroll
+                    for (int i = 0; i < B; ++i) {
+                        part[i] = 0;
+                        if (B * tid + i < kShare)
+#pragma unroll
+                            for (int r = 0; r < S; ++r)
+                                part[i] += remote<S>(&sh.steps[kShare * rank + B * tid + i], r);
+                        own += part[i];
+                    }
+                    const u64 upto = cta_prefix(sh, own);
+                    if (tid == kThreads - 1) sh.slice = uint32_t(upto);
+                    row_sync<S>();
+                    u64 run = upto - own;
+                    for (int r = 0; r < rank; ++r) run += remote<S>(&sh.slice, r);
+                    const float slack = 3e-5f + float(cols) * 0x1p-31f;
+                    const float from = (pc - slack) * 0x1p31f, to = (pc + slack) * 0x1p31f;
+#pragma unroll
+                    for (int i = 0; i < B; ++i) {
+                        const float before = float(run), after = float(run + part[i]);
+                        // steps whose end reaches `from`, and the first that reaches `to`
+                        if (B * tid + i < kShare) {
+                            const uint32_t step = kShare * rank + B * tid + i;
+                            if (after >= from && (before < from || step == 0)) sh.bin_lo = step;
+                            if (after >= to && before < to) sh.bin_hi = step;
+                        }
+                        run += part[i];
+                    }
+                    row_sync<S>();
+                    int bin_lo = kBins, bin_hi = kBins;
+                    for (int r = 0; r < S; ++r) {
+                        bin_lo = min(bin_lo, int(remote<S>(&sh.bin_lo, r)));
+                        bin_hi = min(bin_hi, int(remote<S>(&sh.bin_hi, r)));
+                    }
+                    // weights above those steps, below them, and the columns in them
+                    const float from_step = float(bin_lo);
+                    const float to_step = bin_hi >= kBins - 1 ? INFINITY : float(bin_hi + 1);
+                    u64 above = 0, rest = 0;
+                    for (int64_t b = lo + lane; b < hi; b += 32) {
+                        float v[EPV];
+                        blocks.load(b, v);
+                        uint32_t hi_a = 0, hi_r = 0;
+                        int lo_a = 0, lo_r = 0;
+#pragma unroll
+                        for (int i = 0; i < EPV; i += 2) {
+                            uint32_t h[2];
+                            int l[2];
+                            w.pair(v[i], v[i + 1], h, l);
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float at = (w.m - v[i + j]) * steps;
+                                if (v[i + j] >= least && at < to_step) {
+                                    if (at < from_step) hi_a += h[j], lo_a += l[j];
+                                    else list_push<S>(sh, v[i + j], uint32_t(blocks.col(b) + i + j));
+                                } else {
+                                    hi_r += h[j], lo_r += l[j];
+                                }
+                            }
+                        }
+                        above += w.sum_of(hi_a, lo_a);
+                        rest += w.sum_of(hi_r, lo_r);
+                    }
+                    above = warp_sum64(above);
+                    rest = warp_sum64(rest);
+                    if (lane == 0) {
+                        sh.draw[warp] = above;
+                        sh.sum[warp] = above + rest;
                     }
                     row_sync<S>();
                     const uint32_t n = remote<S>(&sh.listed, 0);
                     if (n > 0 && n <= kList) {
                         if (rank == 0) {
+                            u64 total = 0, top_sum = 0;
+                            for (int i = lane; i < S * kWarps; i += 32) {
+                                total += remote<S>(&sh.sum[i % kWarps], i / kWarps);
+                                top_sum += remote<S>(&sh.draw[i % kWarps], i / kWarps);
+                            }
+                            total = warp_sum64(total);
+                            top_sum = warp_sum64(top_sum);
                             sort_list(sh, int(n));
                             constexpr int P = kList / kThreads;
-                            u64 a[P], own = 0;
+                            u64 a[P], mine = 0;
 #pragma unroll
                             for (int i = 0; i < P; ++i) {
                                 const int at = P * tid + i;
                                 a[i] = at < int(n) ? w(key_value(uint32_t(sh.sorted[at] >> 32))) : 0;
-                                own += a[i];
+                                mine += a[i];
                             }
-                            const u64 upto = cta_prefix(sh, own) + sh.above, want = sh.want;
-                            u64 run = upto - own;
-                            if (run < want && want <= upto) {
-                                int i = 0;
-                                while (i < P - 1 && run + a[i] < want) run += a[i++];
+                            const u64 upto = cta_prefix(sh, mine);
+                            if (tid == kThreads - 1) sh.result[0] = upto;
+                            __syncthreads();
+                            const u64 want = share_of(pc, total + sh.result[0]);
+                            u64 run = top_sum + upto - mine;
+#pragma unroll
+                            for (int i = 0; i < P; ++i) {
+                                if (a[i] == 0 && P * tid + i >= int(n)) break;
                                 const u64 e = sh.sorted[P * tid + i];
-                                sh.cut = {key_value(uint32_t(e >> 32)),
-                                          int(0xffffffffu - uint32_t(e))};
+                                const uint32_t col = 0xffffffffu - uint32_t(e);
+                                if (run < want) {  // stays
+                                    const uint32_t block = (col + uint32_t(blocks.head)) / EPV;
+                                    atomicAdd(&sh.extra[block / uint32_t(per_warp)], a[i]);
+                                    if (want <= run + a[i] && top_sum < want)
+                                        sh.cut = {key_value(uint32_t(e >> 32)), int(col)};
+                                }
+                                run += a[i];
                             }
                         }
                         row_sync<S>();
                         cut = remote<S>(&sh.cut, 0);
                         settled = cut.value == cut.value;  // found
+                        have_runs = settled && uu != 0.f;
+                    } else if (n > kList) {
+                        // many small weights at the border (p close to 1):
+                        // divide those steps into 2048 again, by exact weights
+                        const float first = from_step;
+                        const float range = fminf(to_step, (w.m - least) * steps) - first;
+                        const float fine = float(kBins) / range;
+                        auto fine_of = [&](float v) {
+                            return min(kBins - 1, int(((w.m - v) * steps - first) * fine));
+                        };
+                        auto each_listed = [&](auto f) {
+                            for (int64_t b = lo + lane; b < hi; b += 32) {
+                                float v[EPV];
+                                blocks.load(b, v);
+#pragma unroll 1
+                                for (int i = 0; i < EPV; ++i) {
+                                    float y = v[0];
+#pragma unroll
+                                    for (int j = 1; j < EPV; ++j) y = j == i ? v[j] : y;
+                                    const float at = (w.m - y) * steps;
+                                    if (y >= least && at < to_step && at >= from_step)
+                                        f(y, blocks.col(b) + i);
+                                }
+                            }
+                        };
+                        for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0;
+                        if (tid == 0) {
+                            sh.listed = 0;
+                            sh.fine = kBins;  // none
+                        }
+                        row_sync<S>();
+                        each_listed([&](float v, int64_t) { atomicAdd(&sh.mass[fine_of(v)], w(v)); });
+                        row_sync<S>();
+                        if (rank == 0) {
+                            u64 total = 0, top_sum = 0;
+                            for (int i = lane; i < S * kWarps; i += 32) {
+                                total += remote<S>(&sh.sum[i % kWarps], i / kWarps);
+                                top_sum += remote<S>(&sh.draw[i % kWarps], i / kWarps);
+                            }
+                            total = warp_sum64(total);
+                            top_sum = warp_sum64(top_sum);
+                            constexpr int F = kBins / kThreads;
+                            u64 part[F], mine = 0;
+#pragma unroll
+                            for (int i = 0; i < F; ++i) {
+                                part[i] = 0;
+                                for (int r = 0; r < S; ++r)
+                                    part[i] += remote<S>(&sh.mass[F * tid + i], r);
+                                mine += part[i];
+                            }
+                            const u64 upto = cta_prefix(sh, mine);
+                            if (tid == kThreads - 1) sh.result[0] = upto;
+                            __syncthreads();
+                            const u64 want = share_of(pc, total + sh.result[0]);
+                            u64 run = top_sum + upto - mine;
+                            if (run < want && want <= run + mine && top_sum < want) {
+                                int i = 0;
+                                while (i < F - 1 && run + part[i] < want) run += part[i++];
+                                sh.fine = F * tid + i;
+                                sh.fine_above = run;
+                                sh.want = want;
+                            }
+                        }
+                        row_sync<S>();
+                        const int step = int(remote<S>(&sh.fine, 0));
+                        if (step < kBins)
+                            each_listed([&](float v, int64_t c) {
+                                if (fine_of(v) == step) list_push<S>(sh, v, uint32_t(c));
+                            });
+                        row_sync<S>();
+                        const uint32_t n_fine = remote<S>(&sh.listed, 0);
+                        if (n_fine > 0 && n_fine <= kList) {
+                            if (rank == 0) {
+                                sort_list(sh, int(n_fine));
+                                constexpr int P = kList / kThreads;
+                                u64 a[P], mine = 0;
+#pragma unroll
+                                for (int i = 0; i < P; ++i) {
+                                    const int at = P * tid + i;
+                                    a[i] = at < int(n_fine) ? w(key_value(uint32_t(sh.sorted[at] >> 32))) : 0;
+                                    mine += a[i];
+                                }
+                                const u64 upto = cta_prefix(sh, mine) + sh.fine_above, want = sh.want;
+                                u64 run = upto - mine;
+                                if (run < want && want <= upto) {
+                                    int i = 0;
+                                    while (i < P - 1 && run + a[i] < want) run += a[i++];
+                                    const u64 e = sh.sorted[P * tid + i];
+                                    sh.cut = {key_value(uint32_t(e >> 32)),
+                                              int(0xffffffffu - uint32_t(e))};
+                                }
+                            }
+                            row_sync<S>();
+                            cut = remote<S>(&sh.cut, 0);
+                            settled = cut.value == cut.value;  // found
+                        }
                     }
                 }
             }
@@ -954,7 +1118,10 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                 row_sync<S>();
                 cut = remote<S>(&sh.cut, 0);
             }
-            if (floor_p > cut.value) cut = {floor_p, INT_MAX};
+            if (floor_p > cut.value) {
+                cut = {floor_p, INT_MAX};
+                have_runs = false;
+            }
         }
 
         if (!done) {
@@ -995,12 +1162,14 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                 }
                 return a;
             };
-            u64 mine = 0;
+            if (!have_runs) {
+                u64 mine = 0;
 #pragma unroll 2
-            for (int64_t b = lo + lane; b < hi; b += 32) mine += block_weight(b);
-            mine = warp_sum64(mine);
-            if (lane == 0) sh.draw[warp] = mine;
-            row_sync<S>();
+                for (int64_t b = lo + lane; b < hi; b += 32) mine += block_weight(b);
+                mine = warp_sum64(mine);
+                if (lane == 0) sh.draw[warp] = mine;
+                row_sync<S>();
+            }
             // the run that holds the border: before <= target < before + its sum
             constexpr int R = (S * kWarps + 31) / 32;  // runs per lane, in order
             u64 part[R], own = 0;
@@ -1008,6 +1177,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
             for (int i = 0; i < R; ++i) {
                 const int g = R * lane + i;
                 part[i] = g < S * kWarps ? remote<S>(&sh.draw[g % kWarps], g / kWarps) : 0;
+                if (have_runs && g < S * kWarps) part[i] += remote<S>(&sh.extra[g], 0);
                 own += part[i];
             }
             const u64 upto = warp_prefix64(own, lane);
@@ -1041,26 +1211,16 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                         const u64 end = before + warp_prefix64(a, lane);
                         const uint32_t hit = __ballot_sync(kFullMask, end > target);
                         if (hit) {
-                            if (lane == __ffs(hit) - 1) {
-                                float v[EPV];
-                                blocks.load(b0 + lane, v);
-                                u64 run = end - a;
-                                int64_t pick = 0;
-                                float x_pick = w.m;
-                                bool open = true;
-#pragma unroll
-                                for (int i = 0; i < EPV; ++i) {
-                                    const int64_t c = blocks.col(b0 + lane) + i;
-                                    const u64 a_i = kept_weight(v[i], c);
-                                    if (open && a_i > 0) {
-                                        pick = c;
-                                        x_pick = v[i];
-                                        run += a_i;
-                                        open = run <= target;
-                                    }
-                                }
-                                write(pick, x_pick, total);
-                            }
+                            // the block that holds the border: a lane per column
+                            const int at = __ffs(hit) - 1;
+                            const u64 start = __shfl_sync(kFullMask, end - a, at);
+                            const int64_t c = blocks.col(b0 + at) + lane;
+                            const bool in = lane < EPV && c >= 0 && c < cols;
+                            const float v = in ? widen(x[row * cols + c]) : -INFINITY;
+                            const u64 a_c = in ? kept_weight(v, c) : 0;
+                            const u64 upto_c = start + warp_prefix64(a_c, lane);
+                            uint32_t found = __ballot_sync(kFullMask, a_c > 0 && upto_c > target);
+                            if (lane == __ffs(found) - 1) write(c, v, total);
                             break;
                         }
                         before = __shfl_sync(kFullMask, end, 31);
