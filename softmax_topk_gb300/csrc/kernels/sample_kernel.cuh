@@ -368,10 +368,18 @@ __device__ __forceinline__ V remote(const V* local, int rank) {
         return v;
     }
 }
+// Barrier over the CTAs of a row.  Threads of a warp come to it from loops that
+// they left at different times, so the cluster's barrier is the form that
+// counts threads, not the .aligned one, which takes a warp for converged.
 template <int S>
 __device__ __forceinline__ void row_sync() {
-    if constexpr (S == 1) __syncthreads();
-    else cluster_sync();
+    if constexpr (S == 1) {
+        __syncthreads();
+    } else {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release;\n\t"
+                     "barrier.cluster.wait.acquire;" ::: "memory");
+    }
 }
 
 // Puts (x, col) on rank 0's list.
@@ -685,6 +693,52 @@ struct Blocks {
     }
 };
 
+// The weights that stay of a row, in column order.  Columns at the cut and past
+// its last one are summed with the rest and taken off again; column by column
+// where every kept column counts (u = 0).
+template <typename T>
+struct Kept {
+    static constexpr int EPV = Blocks<T>::EPV;
+    Blocks<T> blocks;
+    Weight w;
+    Cut cut;
+    u64 w_cut;  // w(cut.value) where the cut goes through equal logits
+    bool by_column;
+
+    __device__ __forceinline__ u64 column(float v, int64_t c) const {
+        if (!cut.keeps(v, c)) return 0;
+        const u64 a = w(v);
+        return by_column && a == 0 ? 1ull : a;  // u = 0: the first column, however small
+    }
+    __device__ __forceinline__ u64 block(int64_t b) const {
+        float v[EPV];
+        blocks.load(b, v);
+        u64 a = 0;
+        if (!by_column) {
+            a = w.sum_from(v, cut.value);
+            if (cut.last != INT_MAX) {
+#pragma unroll
+                for (int i = 0; i < EPV; ++i)
+                    if (v[i] == cut.value && blocks.col(b) + i > cut.last) a -= w_cut;
+            }
+            return a;
+        }
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < EPV; ++i) any |= v[i] >= cut.value;
+        if (any) {
+#pragma unroll 1
+            for (int j = 0; j < EPV; ++j) {
+                float y = v[0];
+#pragma unroll
+                for (int i = 1; i < EPV; ++i) y = i == j ? v[i] : y;
+                a += column(y, blocks.col(b) + j);
+            }
+        }
+        return a;
+    }
+};
+
 template <typename T, int S>
 __global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restrict__ out,
@@ -933,11 +987,13 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                         bin_lo = min(bin_lo, int(remote<S>(&sh.bin_lo, r)));
                         bin_hi = min(bin_hi, int(remote<S>(&sh.bin_hi, r)));
                     }
-                    // weights above those steps, below them, and the columns in them
+                    // weights above those steps, below them, and the columns in
+                    // them; not needed where min-p cuts above them
                     const float from_step = float(bin_lo);
                     const float to_step = bin_hi >= kBins - 1 ? INFINITY : float(bin_hi + 1);
+                    if (bin_lo < kBins && (w.m - floor_p) * steps < from_step) settled = true;
                     u64 above = 0, rest = 0;
-                    for (int64_t b = lo + lane; b < hi; b += 32) {
+                    for (int64_t b = settled ? hi : lo + lane; b < hi; b += 32) {
                         float v[EPV];
                         blocks.load(b, v);
                         uint32_t hi_a = 0, hi_r = 0;
@@ -1125,47 +1181,12 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
         }
 
         if (!done) {
-            // ---- the draw, in column order; column by column where every kept
-            // column counts (u = 0).  Columns at the cut and past its last one
-            // are summed with the rest and taken off again.
-            const bool by_column = uu == 0.f;
-            const u64 w_cut = cut.last != INT_MAX ? w(cut.value) : 0;
-            auto kept_weight = [&](float v, int64_t c) -> u64 {
-                if (!cut.keeps(v, c)) return 0;
-                const u64 a = w(v);
-                return uu == 0.f && a == 0 ? 1ull : a;  // u = 0: the first column, however small
-            };
-            auto block_weight = [&](int64_t b) {
-                float v[EPV];
-                blocks.load(b, v);
-                u64 a = 0;
-                if (!by_column) {
-                    a = w.sum_from(v, cut.value);
-                    if (cut.last != INT_MAX) {
-#pragma unroll
-                        for (int i = 0; i < EPV; ++i)
-                            if (v[i] == cut.value && blocks.col(b) + i > cut.last) a -= w_cut;
-                    }
-                    return a;
-                }
-                bool any = false;
-#pragma unroll
-                for (int i = 0; i < EPV; ++i) any |= v[i] >= cut.value;
-                if (any) {
-#pragma unroll 1
-                    for (int j = 0; j < EPV; ++j) {
-                        float y = v[0];
-#pragma unroll
-                        for (int i = 1; i < EPV; ++i) y = i == j ? v[i] : y;
-                        a += kept_weight(y, blocks.col(b) + j);
-                    }
-                }
-                return a;
-            };
+            // ---- the draw, in column order
+            const Kept<T> kept = {blocks, w, cut, cut.last != INT_MAX ? w(cut.value) : 0, uu == 0.f};
             if (!have_runs) {
                 u64 mine = 0;
 #pragma unroll 2
-                for (int64_t b = lo + lane; b < hi; b += 32) mine += block_weight(b);
+                for (int64_t b = lo + lane; b < hi; b += 32) mine += kept.block(b);
                 mine = warp_sum64(mine);
                 if (lane == 0) sh.draw[warp] = mine;
                 row_sync<S>();
@@ -1200,14 +1221,14 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                 const int64_t per_piece = (per_warp / 32 + kWarps - 1) / kWarps * 32;
                 const int64_t plo = min(to, from + warp * per_piece), phi = min(to, plo + per_piece);
                 u64 piece = 0;
-                for (int64_t b = plo + lane; b < phi; b += 32) piece += block_weight(b);
+                for (int64_t b = plo + lane; b < phi; b += 32) piece += kept.block(b);
                 piece = warp_sum64(piece);
                 if (lane == 0) sh.piece[warp] = piece;
                 __syncthreads();
                 for (int i = 0; i < warp; ++i) before += sh.piece[i];
                 if (before <= target && target < before + piece) {
                     for (int64_t b0 = plo; b0 < phi; b0 += 32) {
-                        const u64 a = b0 + lane < phi ? block_weight(b0 + lane) : 0;
+                        const u64 a = b0 + lane < phi ? kept.block(b0 + lane) : 0;
                         const u64 end = before + warp_prefix64(a, lane);
                         const uint32_t hit = __ballot_sync(kFullMask, end > target);
                         if (hit) {
@@ -1217,7 +1238,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                             const int64_t c = blocks.col(b0 + at) + lane;
                             const bool in = lane < EPV && c >= 0 && c < cols;
                             const float v = in ? widen(x[row * cols + c]) : -INFINITY;
-                            const u64 a_c = in ? kept_weight(v, c) : 0;
+                            const u64 a_c = in ? kept.column(v, c) : 0;
                             const u64 upto_c = start + warp_prefix64(a_c, lane);
                             uint32_t found = __ballot_sync(kFullMask, a_c > 0 && upto_c > target);
                             if (lane == __ffs(found) - 1) write(c, v, total);

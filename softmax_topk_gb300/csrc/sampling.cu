@@ -1,5 +1,4 @@
 // Sampling from rows of logits: the launch.
-#include <cstdlib>
 #include "host_common.h"
 #include "internal.h"
 #include "kernels/sample_kernel.cuh"
@@ -31,7 +30,6 @@ cudaError_t launch_t(const void* x, const float* u, int32_t* out, float* prob, i
     const int64_t useful = ceil_div(int64_t(cols) * int64_t(sizeof(T)), 16 * sample::kThreads);
     int S = 1;
     while (S < sample::kMaxCluster && 2 * S * rows <= slots && 2 * S <= useful) S *= 2;
-    if (getenv("SAMPLE_S")) S = atoi(getenv("SAMPLE_S"));
     if (S == 8) return launch_s<T, 8>(x, u, out, prob, rows, cols, s, bits, stream);
     if (S == 4) return launch_s<T, 4>(x, u, out, prob, rows, cols, s, bits, stream);
     if (S == 2) return launch_s<T, 2>(x, u, out, prob, rows, cols, s, bits, stream);
