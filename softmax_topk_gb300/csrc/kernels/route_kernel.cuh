@@ -43,6 +43,7 @@ struct Shape {
     int experts, K, groups, topk_groups, group_top;
     int lanes, lanes_log2;  // lanes per group (a power of two)
     int per_lane;  // experts per lane
+    int index_mask;  // experts up to a power of two, less one
     int slots;       // K up to a power of two: lanes per token after the choice
     int tokens;      // rows that a warp takes at a time, at most 32 / slots
     int sigmoid, renorm;
@@ -679,6 +680,382 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
         if (real) {
             weights[(row0 + my_token) * K + my_slot] = w * sh.scale;
             idx[(row0 + my_token) * K + my_slot] = e;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ large batches
+// Four threads per token.  What crosses lanes in the kernel above (redux, votes,
+// shuffles, four fifths of its instructions) mostly happens in a thread's
+// registers here, 8 tokens to an instruction, at the price of the rows' stay in
+// shared memory and of latency, so it takes large batches only (see route.cu).
+//
+// A warp copies 8 rows in 16-byte chunks, placed so that the four threads of a
+// row, reading one chunk each of neighbouring places or of different groups,
+// and the next row's four hit different banks.  Every thread keeps the best P
+// (K up to a power of two, at least 4) of its chunks as a sorted list of keys in
+// registers, the value with its low bits replaced by the expert; four new ones
+// are sorted and merged into it at once, and the best key that fell out is
+// kept too.  The four lists are merged over shuffles.  Then the listed experts'
+// full values settle the order that the cut-off bits hide; where a value is
+// too near the next, or a key that fell out may hide a better one, the token
+// goes to choose_exact (the whole warp).
+constexpr int kListWarps = 4;
+constexpr int kListRows = 8;       // rows per warp
+constexpr int kListExperts = 1024;
+constexpr int kListPerLane = 32;   // of choose_exact
+
+// a >= b after it.
+__device__ __forceinline__ void order(int& a, int& b) {
+    const int t = max(a, b);
+    b = min(a, b);
+    a = t;
+}
+// A bitonic list into falling order.
+template <int P>
+__device__ __forceinline__ void order_bitonic(int (&list)[P]) {
+#pragma unroll
+    for (int step = P / 2; step > 0; step /= 2)
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if ((i & step) == 0) order(list[i], list[i + step]);
+}
+// Merges four keys into the sorted list; `out`: the best key that has fallen out.
+template <int P>
+__device__ __forceinline__ void merge4(int (&list)[P], int (&k)[4], int& out) {
+    order(k[0], k[1]);
+    order(k[2], k[3]);
+    order(k[0], k[2]);
+    order(k[1], k[3]);
+    order(k[1], k[2]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int& tail = list[P - 1 - i];
+        out = max(out, min(tail, k[i]));
+        tail = max(tail, k[i]);
+    }
+    order_bitonic<P>(list);  // P - 4 falling, then 4 rising
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_addr(dst)), "l"(src)
+                 : "memory");
+}
+
+// Sum, maximum, minimum over the four threads of a row.
+__device__ __forceinline__ float row_sum(float v) {
+    v += __shfl_xor_sync(kFullMask, v, 1);
+    return v + __shfl_xor_sync(kFullMask, v, 2);
+}
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(kFullMask, v, 1));
+    return fmaxf(v, __shfl_xor_sync(kFullMask, v, 2));
+}
+
+template <typename T, int P>
+__global__ void __launch_bounds__(kListWarps * 32, P <= 8 ? 5 : 4)
+route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
+                  float* __restrict__ weights, int* __restrict__ idx, int64_t rows, const Shape sh) {
+    constexpr int EPV = 16 / int(sizeof(T));
+    extern __shared__ __align__(16) unsigned char list_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sub = lane & 3, my = lane >> 2;  // thread of the row, row of the tile
+    const int E = sh.experts, K = sh.K, G = sh.groups, gsize = E / G;
+    const int chunks = E / EPV, group_chunks = gsize / EPV;
+    const bool by_score = bias != nullptr;
+    const bool pair_sum = G > 1 && sh.group_top == 2;
+    const bool need_scores = by_score || pair_sum;
+    const bool need_sum = !sh.sigmoid && (need_scores || !sh.renorm);
+    const int mask = sh.index_mask;
+    // bias, its groups 4 floats apart so that threads in different groups meet
+    // different banks; the groups' values of every row; the warps' tiles
+    float* const b_sm = reinterpret_cast<float*>(list_smem);
+    float* const value = b_sm + E + 4 * G + (warp * kListRows + my) * G;  // where G > 1
+    unsigned char* const tile = list_smem + (E + 4 * G + (G > 1 ? kListWarps * kListRows * G : 0)) * 4 +
+                                warp * kListRows * E * int(sizeof(T));
+    for (int e = threadIdx.x; e < E; e += kListWarps * 32)
+        b_sm[e + 4 * (e / gsize)] = by_score ? bias[e] : 0.f;
+    __syncthreads();
+    auto place = [&](int r, int c) {
+        return (r * chunks + (c ^ (((c >> 3) ^ ((r & 1) << 2)) & 7))) * 16;
+    };
+
+    const int64_t tiles = (rows + kListRows - 1) / kListRows;
+    for (int64_t t = int64_t(blockIdx.x) * kListWarps + warp; t < tiles;
+         t += int64_t(gridDim.x) * kListWarps) {
+        const int64_t row0 = t * kListRows;
+        const int here = int(min(int64_t(kListRows), rows - row0));
+        __syncwarp();  // the last tile has been read
+        for (int r = 0; r < here; ++r)
+            for (int c = lane; c < chunks; c += 32)
+                cp_async16(tile + place(r, c), x + (row0 + r) * E + c * EPV);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        // threads past the last row work on row 0 and write nothing
+        const int r = my < here ? my : 0;
+        auto load = [&](int c, float (&v)[EPV]) {
+            const uint4 w = *reinterpret_cast<const uint4*>(tile + place(r, c));
+            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    v[i] = __uint_as_float(a[i]);
+                } else {
+                    const float2 f = unpack_bf16x2(a[i]);
+                    v[2 * i] = f.x;
+                    v[2 * i + 1] = f.y;
+                }
+            }
+        };
+        auto logit = [&](int e) {
+            return widen(reinterpret_cast<const T*>(tile + place(r, e / EPV))[e % EPV]);
+        };
+
+        float m = 0.f, inv_d = 1.f;
+        if (!sh.sigmoid) {
+            m = -INFINITY;
+            for (int c = sub; c < chunks; c += 4) {
+                float v[EPV];
+                load(c, v);
+#pragma unroll
+                for (int i = 0; i < EPV; ++i) m = fmaxf(m, v[i]);
+            }
+            m = row_max(m);
+            if (need_sum) {
+                const float ref = m == -INFINITY ? 0.f : m;
+                float d = 0.f;
+                for (int c = sub; c < chunks; c += 4) {
+                    float v[EPV];
+                    load(c, v);
+                    float part = 0.f;
+#pragma unroll
+                    for (int i = 0; i < EPV; i += 2) {
+                        const float2 e = exp_pair<false>(make_float2(v[i] - ref, v[i + 1] - ref));
+                        part += e.x + e.y;
+                    }
+                    d += part;
+                }
+                d = row_sum(d);
+                inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
+            }
+        }
+        const float err = (sh.sigmoid ? 1.f : inv_d) * 0x1p-19f;  // twice the bound of a score
+        auto score = [&](float v) {  // the SFU's; 0 for -inf
+            return sh.sigmoid ? rcp_sfu(1.f + ex2_sfu(-expc::kLog2e * v))
+                              : exp_pair<false>(make_float2(v - m, v - m)).x * inv_d;
+        };
+
+        // ---- groups that take part, one bit each; thread `sub` values every
+        // fourth group and ranks it
+        uint32_t kept = 0xffffffffu;
+        bool unsure = false;
+        if (G > 1) {
+            for (int g = sub; g < G; g += 4) {
+                float a = -INFINITY, b = -INFINITY;
+                const float* gb = b_sm + g * (gsize + 4);
+                for (int c = 0; c < group_chunks; ++c, gb += EPV) {
+                    float v[EPV];
+                    load(g * group_chunks + c, v);
+#pragma unroll
+                    for (int i = 0; i < EPV; ++i) {
+                        float y = v[i];
+                        if (need_scores) {
+                            y = score(v[i]) + gb[i];
+                            if (v[i] == -INFINITY) y = -INFINITY;
+                        }
+                        b = fmaxf(b, fminf(a, y));
+                        a = fmaxf(a, y);
+                    }
+                }
+                value[g] = pair_sum ? a + b : a;
+            }
+            __syncwarp();
+            kept = 0;
+            float low = INFINITY, high = -INFINITY;
+            for (int g = sub; g < G; g += 4) {
+                const float y = value[g];
+                int rank = 0;
+                for (int h = 0; h < G; ++h) {
+                    const float o = value[h];
+                    rank += o > y || (o == y && h < g);
+                }
+                if (rank < sh.topk_groups) {
+                    kept |= 1u << g;
+                    low = fminf(low, y);
+                } else {
+                    high = fmaxf(high, y);
+                }
+            }
+            kept |= __shfl_xor_sync(kFullMask, kept, 1);
+            kept |= __shfl_xor_sync(kFullMask, kept, 2);
+            low = -row_max(-low);
+            high = row_max(high);
+            // (fewer or more than topk_groups only where values are NaN)
+            if (need_scores && high != -INFINITY &&
+                !(low - high > 2.f * err + fabsf(low) * 0x1p-21f))
+                unsure = true;
+        }
+
+        // ---- the P best of this thread's chunks: every fourth of those that
+        // take part
+        int list[P], out = kNone;
+#pragma unroll
+        for (int i = 0; i < P; ++i) list[i] = kNone;
+        {
+            uint32_t left = G > 1 ? kept : 1u;
+            int c0 = sub;
+            while (left) {
+                while (left && c0 >= group_chunks) {
+                    c0 -= group_chunks;
+                    left &= left - 1;
+                }
+                if (!left) break;
+                const int g = __ffs(left) - 1;
+                float v[EPV];
+                load(g * group_chunks + c0, v);
+                const float* gb = b_sm + g * (gsize + 4) + c0 * EPV;
+                const int first = mask - (g * gsize + c0 * EPV);
+#pragma unroll
+                for (int i = 0; i < EPV; i += 4) {
+                    int k[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float y = v[i + j];
+                        if (by_score) {
+                            y = score(v[i + j]) + gb[i + j];
+                            if (v[i + j] == -INFINITY) y = -INFINITY;
+                        }
+                        k[j] = (signed_key(y + 0.f) & ~mask) | (first - i - j);
+                    }
+                    merge4<P>(list, k, out);
+                }
+                c0 += 4;
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int step = 1; step <= 2; step *= 2) {
+            int other[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) other[i] = __shfl_xor_sync(kFullMask, list[i], step);
+            out = max(out, __shfl_xor_sync(kFullMask, out, step));
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                out = max(out, min(list[i], other[P - 1 - i]));
+                list[i] = max(list[i], other[P - 1 - i]);
+            }
+            order_bitonic<P>(list);
+            out = max(out, __shfl_xor_sync(kFullMask, out, step));
+        }
+
+        // ---- the listed experts' full values, in order
+        float c[P];
+        int e[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            e[i] = list[i] == kNone ? E - 1 : mask - (list[i] & mask);
+            const float y = logit(e[i]);
+            c[i] = list[i] == kNone ? -INFINITY : y;
+            if (by_score && c[i] != -INFINITY) c[i] = score(y) + b_sm[e[i] + 4 * (e[i] / gsize)];
+        }
+        // neighbours whose cut-off bits hid their order change places
+        const bool exact_keys = !by_score && sizeof(T) == 2;  // no bits were cut off
+        bool wrong = false;
+#pragma unroll
+        for (int i = 0; i + 1 < P; ++i) wrong = wrong || c[i + 1] > c[i];
+        if (__any_sync(kFullMask, wrong)) {
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass)
+#pragma unroll
+                for (int i = 0; i + 1 < P; ++i)
+                    if (c[i + 1] > c[i]) {
+                        const float tc = c[i];
+                        c[i] = c[i + 1];
+                        c[i + 1] = tc;
+                        const int te = e[i];
+                        e[i] = e[i + 1];
+                        e[i + 1] = te;
+                    }
+        }
+        // the most that is left out: the slots past K - 1, and what a key
+        // outside the list can stand for
+        float rest = out < kMissing ? -INFINITY : signed_value(out | mask);
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (i >= K) rest = fmaxf(rest, c[i]);
+        bool near = false;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float next = i + 1 < P && i + 1 < K ? c[i + 1 < P ? i + 1 : i] : rest;
+            const float slack = by_score ? err + fabsf(c[i]) * 0x1p-22f : 0.f;
+            near = near || (i < K && next != -INFINITY && !(c[i] - next > slack));
+        }
+        if (__any_sync(kFullMask, near && !exact_keys)) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                if (i < K && c[i] != -INFINITY && !exact_keys) {
+                    const float next = i + 1 < P && i + 1 < K ? c[i + 1 < P ? i + 1 : i] : rest;
+                    const float slack = by_score ? err + fabsf(c[i]) * 0x1p-22f : 0.f;
+                    bool bad = next != -INFINITY && !(c[i] - next > slack);
+                    if (bad && i + 1 < P && i + 1 < K) {
+                        // equal logits of equal bias stand in the order of
+                        // their experts
+                        const int p = e[i], n = e[i + 1 < P ? i + 1 : i];
+                        bad = !(p < n && logit(p) == logit(n) &&
+                                b_sm[p + 4 * (p / gsize)] == b_sm[n + 4 * (n / gsize)]);
+                    }
+                    unsure = unsure || bad;
+                }
+            }
+        }
+        for (uint32_t todo = __ballot_sync(kFullMask, unsure && my < here && sub == 0); todo;
+             todo &= todo - 1) {
+            const int src = __ffs(todo) - 1;
+            const int chosen = choose_exact<T, kListPerLane>(x + (row0 + (src >> 2)) * E, bias, sh);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int got = __shfl_sync(kFullMask, chosen, i);
+                if (my == src >> 2 && i < K) e[i] = got;
+            }
+        }
+
+        // ---- weights: thread `sub` has the slots sub, sub + 4, ...
+        constexpr int Q = P / 4;
+        float z[Q], w[Q], sum = 0.f, top = -INFINITY;
+        int ez[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            ez[q] = sub == 0 ? e[4 * q] : sub == 1 ? e[4 * q + 1] : sub == 2 ? e[4 * q + 2] : e[4 * q + 3];
+            z[q] = 4 * q + sub < K ? logit(ez[q]) : -INFINITY;
+            top = fmaxf(top, z[q]);
+        }
+        top = row_max(top);
+        if (sh.sigmoid) top = fminf(top, 0.f);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if (!sh.renorm) {
+                w[q] = sh.sigmoid ? sigmoid(z[q]) : exp1(z[q] - m) * inv_d;
+            } else if (sh.sigmoid && z[q] > 0.f) {
+                w[q] = sigmoid(z[q]);
+            } else {
+                w[q] = exp1(z[q] - top);
+                if (sh.sigmoid) w[q] = __fdiv_rn(w[q], 1.f + exp1(z[q]));
+            }
+            if (z[q] == -INFINITY) w[q] = 0.f;
+            sum += w[q];
+        }
+        sum = row_sum(sum);
+        if (my < here) {
+            const int64_t at = (row0 + my) * K;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                if (4 * q + sub < K) {
+                    float y = w[q];
+                    if (sh.renorm) y = sum > 0.f ? __fdiv_rn(y, sum) : 0.f;
+                    weights[at + 4 * q + sub] = y * sh.scale;
+                    idx[at + 4 * q + sub] = ez[q];
+                }
+            }
         }
     }
 }

@@ -9,6 +9,8 @@ namespace {
 
 using route::Shape;
 
+constexpr int64_t kListRowsPerSm = 16;
+
 // Lanes per group: the largest power of two that still gives every group its
 // own lanes; experts per lane follow.
 Shape make_shape(const RouteArgs& a, int groups) {
@@ -24,6 +26,7 @@ Shape make_shape(const RouteArgs& a, int groups) {
         ++s.lanes_log2;
     }
     s.per_lane = (a.experts / groups + s.lanes - 1) / s.lanes;
+    s.index_mask = pow2_at_least(a.experts) - 1;
     s.slots = pow2_at_least(a.K);
     s.tokens = 1;
     s.sigmoid = a.score == OS_SCORE_SIGMOID;
@@ -77,9 +80,41 @@ cudaError_t launch_bwd(const RouteArgs& a, Shape s, const int32_t* idx,
                          static_cast<T*>(dx), a.rows, s);
 }
 
+// The kernel of four threads per row: rows and groups of whole 16-byte chunks
+// (rows of eight of them, for the copy's placement), lists and choose_exact's
+// runs that fit, and enough rows.
+template <typename T>
+bool list_fits(const RouteArgs& a, const Shape& s, int sms) {
+    const int bytes = a.experts * int(sizeof(T));
+    return a.K <= 16 && a.experts <= route::kListExperts && bytes % 128 == 0 &&
+           a.experts / a.groups * int(sizeof(T)) % 16 == 0 && s.per_lane <= route::kListPerLane &&
+           reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.rows >= int64_t(sms) * kListRowsPerSm;
+}
+
+template <typename T, int P>
+cudaError_t launch_list(const RouteArgs& a, const Shape& s, float* w, int32_t* idx, int sms,
+                        cudaStream_t stream) {
+    auto k = route::route_list_kernel<T, P>;
+    constexpr int kRows = route::kListWarps * route::kListRows;
+    const int smem = (a.experts + 4 * a.groups + (a.groups > 1 ? kRows * a.groups : 0)) * 4 +
+                     kRows * a.experts * int(sizeof(T));
+    const int per_sm = blocks_per_sm(k, route::kListWarps * 32, smem);
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    const int64_t grid = min64(ceil_div(a.rows, kRows), int64_t(sms) * per_sm);
+    return launch_kernel(k, grid, route::kListWarps * 32, 1, smem, stream,
+                         static_cast<const T*>(a.x), a.bias, w, reinterpret_cast<int*>(idx), a.rows, s);
+}
+
 template <typename T>
 cudaError_t fwd(const RouteArgs& a, float* w, int32_t* idx, cudaStream_t stream) {
     const Shape s = make_shape(a, a.groups);
+    const DeviceInfo* dev = device_info();
+    if (!dev) return cudaErrorInvalidDevice;
+    if (list_fits<T>(a, s, dev->sms)) {
+        if (a.K <= 4) return launch_list<T, 4>(a, s, w, idx, dev->sms, stream);
+        if (a.K <= 8) return launch_list<T, 8>(a, s, w, idx, dev->sms, stream);
+        return launch_list<T, 16>(a, s, w, idx, dev->sms, stream);
+    }
     if (s.per_lane <= 1) return launch_fwd<T, 1>(a, s, w, idx, stream);
     if (s.per_lane <= 2) return launch_fwd<T, 2>(a, s, w, idx, stream);
     if (s.per_lane <= 4) return launch_fwd<T, 4>(a, s, w, idx, stream);
