@@ -381,7 +381,8 @@ os_status os_route_topk(const void* x, const float* bias, float* weights, int32_
         return OS_ERR_ALIAS;
     os::RouteArgs a = {x, in, bias, rows, static_cast<int>(experts), K, groups, topk_groups,
                        group_top, score, renorm != 0, scale};
-    const cudaError_t e = os::launch_route(a, weights, idx, reinterpret_cast<cudaStream_t>(stream));
+    const auto launch = in == OS_F32 ? os::route_fwd_f32 : os::route_fwd_bf16;
+    const cudaError_t e = launch(a, weights, idx, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? OS_OK : OS_ERR_CUDA;
 }
 
@@ -401,8 +402,8 @@ os_status os_route_bwd(const void* x, const int32_t* idx, const float* dweights,
         return OS_ERR_ALIAS;
     os::RouteArgs a = {x, in, nullptr, rows, static_cast<int>(experts), K, 1, 1, 1, score,
                        renorm != 0, scale};
-    const cudaError_t e = os::launch_route_bwd(a, idx, dweights, dx,
-                                               reinterpret_cast<cudaStream_t>(stream));
+    const auto launch = in == OS_F32 ? os::route_bwd_f32 : os::route_bwd_bf16;
+    const cudaError_t e = launch(a, idx, dweights, dx, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? OS_OK : OS_ERR_CUDA;
 }
 

@@ -70,9 +70,14 @@ struct RouteArgs {
     bool renorm;
     float scale;
 };
-cudaError_t launch_route(const RouteArgs& a, float* weights, int32_t* idx, cudaStream_t stream);
-cudaError_t launch_route_bwd(const RouteArgs& a, const int32_t* idx, const float* dweights,
-                             void* dx, cudaStream_t stream);
+#define OS_DECLARE_ROUTE(NAME)                                                                \
+    cudaError_t route_fwd_##NAME(const RouteArgs& a, float* weights, int32_t* idx,            \
+                                 cudaStream_t stream);                                        \
+    cudaError_t route_bwd_##NAME(const RouteArgs& a, const int32_t* idx,                      \
+                                 const float* dweights, void* dx, cudaStream_t stream);
+
+OS_DECLARE_ROUTE(f32)
+OS_DECLARE_ROUTE(bf16)
 
 // one column per row under the sampling settings (see os_sample)
 cudaError_t launch_sample(const void* x, os_dtype in, const float* u, int32_t* out, float* prob,

@@ -703,7 +703,6 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
 constexpr int kListWarps = 4;
 constexpr int kListRows = 8;       // rows per warp
 constexpr int kListExperts = 1024;
-constexpr int kListPerLane = 32;   // of choose_exact
 
 // a >= b after it.
 __device__ __forceinline__ void order(int& a, int& b) {
@@ -720,9 +719,17 @@ __device__ __forceinline__ void order_bitonic(int (&list)[P]) {
         for (int i = 0; i < P; ++i)
             if ((i & step) == 0) order(list[i], list[i + step]);
 }
-// Merges four keys into the sorted list; `out`: the best key that has fallen out.
+// The best two keys that have fallen out of a list.
+struct Fallen {
+    int first = kNone, second = kNone;
+    __device__ __forceinline__ void take(int k) {
+        second = max(second, min(first, k));
+        first = max(first, k);
+    }
+};
+// Merges four keys into the sorted list.
 template <int P>
-__device__ __forceinline__ void merge4(int (&list)[P], int (&k)[4], int& out) {
+__device__ __forceinline__ void merge4(int (&list)[P], int (&k)[4], Fallen& out) {
     order(k[0], k[1]);
     order(k[2], k[3]);
     order(k[0], k[2]);
@@ -731,7 +738,7 @@ __device__ __forceinline__ void merge4(int (&list)[P], int (&k)[4], int& out) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         int& tail = list[P - 1 - i];
-        out = max(out, min(tail, k[i]));
+        out.take(min(tail, k[i]));
         tail = max(tail, k[i]);
     }
     order_bitonic<P>(list);  // P - 4 falling, then 4 rising
@@ -752,7 +759,13 @@ __device__ __forceinline__ float row_max(float v) {
     return fmaxf(v, __shfl_xor_sync(kFullMask, v, 2));
 }
 
-template <typename T, int P>
+// A sigmoid's choice value in 64 bits.
+static __device__ __noinline__ double wide_choice(float x, float bias) {
+    return 1.0 / (1.0 + exp(-double(x))) + double(bias);
+}
+
+// P: list length; N: experts per lane in choose_exact.
+template <typename T, int P, int N>
 __global__ void __launch_bounds__(kListWarps * 32, P <= 8 ? 5 : 4)
 route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
                   float* __restrict__ weights, int* __restrict__ idx, int64_t rows, const Shape sh) {
@@ -898,7 +911,8 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
 
         // ---- the P best of this thread's chunks: every fourth of those that
         // take part
-        int list[P], out = kNone;
+        int list[P];
+        Fallen out;
 #pragma unroll
         for (int i = 0; i < P; ++i) list[i] = kNone;
         {
@@ -938,80 +952,102 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
             int other[P];
 #pragma unroll
             for (int i = 0; i < P; ++i) other[i] = __shfl_xor_sync(kFullMask, list[i], step);
-            out = max(out, __shfl_xor_sync(kFullMask, out, step));
+            const int first = __shfl_xor_sync(kFullMask, out.first, step);
+            const int second = __shfl_xor_sync(kFullMask, out.second, step);
+            out.take(first);
+            out.take(second);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                out = max(out, min(list[i], other[P - 1 - i]));
+                out.take(min(list[i], other[P - 1 - i]));
                 list[i] = max(list[i], other[P - 1 - i]);
             }
             order_bitonic<P>(list);
-            out = max(out, __shfl_xor_sync(kFullMask, out, step));
+            // both threads of the pair saw the same keys fall, in another order
         }
 
-        // ---- the listed experts' full values, in order
-        float c[P];
-        int e[P];
+        // ---- the listed experts' full values, and the best fallen one's, in
+        // order
+        constexpr int C = P + 1;
+        float c[C];
+        int e[C];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            e[i] = list[i] == kNone ? E - 1 : mask - (list[i] & mask);
+        for (int i = 0; i < C; ++i) {
+            const int k = i < P ? list[i < P ? i : 0] : out.first;
+            e[i] = k == kNone ? E - 1 : mask - (k & mask);
             const float y = logit(e[i]);
-            c[i] = list[i] == kNone ? -INFINITY : y;
+            c[i] = k == kNone ? -INFINITY : y;
             if (by_score && c[i] != -INFINITY) c[i] = score(y) + b_sm[e[i] + 4 * (e[i] / gsize)];
         }
+        auto swap_at = [&](int i) {
+            const float tc = c[i];
+            c[i] = c[i + 1];
+            c[i + 1] = tc;
+            const int te = e[i];
+            e[i] = e[i + 1];
+            e[i + 1] = te;
+        };
         // neighbours whose cut-off bits hid their order change places
         const bool exact_keys = !by_score && sizeof(T) == 2;  // no bits were cut off
         bool wrong = false;
 #pragma unroll
-        for (int i = 0; i + 1 < P; ++i) wrong = wrong || c[i + 1] > c[i];
+        for (int i = 0; i + 1 < C; ++i) wrong = wrong || c[i + 1] > c[i];
         if (__any_sync(kFullMask, wrong)) {
 #pragma unroll
             for (int pass = 0; pass < 2; ++pass)
 #pragma unroll
-                for (int i = 0; i + 1 < P; ++i)
-                    if (c[i + 1] > c[i]) {
-                        const float tc = c[i];
-                        c[i] = c[i + 1];
-                        c[i + 1] = tc;
-                        const int te = e[i];
-                        e[i] = e[i + 1];
-                        e[i + 1] = te;
-                    }
+                for (int i = 0; i + 1 < C; ++i)
+                    if (c[i + 1] > c[i]) swap_at(i);
         }
-        // the most that is left out: the slots past K - 1, and what a key
-        // outside the list can stand for
-        float rest = out < kMissing ? -INFINITY : signed_value(out | mask);
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-            if (i >= K) rest = fmaxf(rest, c[i]);
+        // values too near to their successors for this arithmetic
         bool near = false;
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float next = i + 1 < P && i + 1 < K ? c[i + 1 < P ? i + 1 : i] : rest;
+        for (int i = 0; i + 1 < C; ++i) {
             const float slack = by_score ? err + fabsf(c[i]) * 0x1p-22f : 0.f;
-            near = near || (i < K && next != -INFINITY && !(c[i] - next > slack));
+            near = near || (i < K && c[i + 1] != -INFINITY && !(c[i] - c[i + 1] > slack));
         }
         if (__any_sync(kFullMask, near && !exact_keys)) {
+            // pairs in 64 bits: a sigmoid's needs nothing of the row (a
+            // softmax's sum would); twice over for three in a row
+            auto wide = [&](int i) {
+                return wide_choice(logit(e[i]), b_sm[e[i] + 4 * (e[i] / gsize)]);
+            };
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                if (i < K && c[i] != -INFINITY && !exact_keys) {
-                    const float next = i + 1 < P && i + 1 < K ? c[i + 1 < P ? i + 1 : i] : rest;
+                for (int i = 0; i + 1 < C; ++i) {
                     const float slack = by_score ? err + fabsf(c[i]) * 0x1p-22f : 0.f;
-                    bool bad = next != -INFINITY && !(c[i] - next > slack);
-                    if (bad && i + 1 < P && i + 1 < K) {
+                    bool bad = i < K && c[i + 1] != -INFINITY && !exact_keys && !(c[i] - c[i + 1] > slack);
+                    if (bad) {
                         // equal logits of equal bias stand in the order of
                         // their experts
-                        const int p = e[i], n = e[i + 1 < P ? i + 1 : i];
-                        bad = !(p < n && logit(p) == logit(n) &&
-                                b_sm[p + 4 * (p / gsize)] == b_sm[n + 4 * (n / gsize)]);
+                        const int p = e[i], n = e[i + 1];
+                        const bool same = logit(p) == logit(n) &&
+                                          b_sm[p + 4 * (p / gsize)] == b_sm[n + 4 * (n / gsize)];
+                        if (same) {
+                            if (n < p) swap_at(i);
+                        } else if (by_score && sh.sigmoid) {
+                            const double a = wide(i), b = wide(i + 1);
+                            if (b > a || (b == a && n < p)) swap_at(i);
+                        } else {
+                            unsure = true;
+                        }
                     }
-                    unsure = unsure || bad;
                 }
+            }
+        }
+        // what the second fallen key, and those below it, can stand for
+        if (!exact_keys && out.second >= kMissing) {
+            const float rest = signed_value(out.second | mask);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float slack = by_score ? err + fabsf(c[i]) * 0x1p-22f : 0.f;
+                if (i == K - 1 && !(c[i] - rest > slack)) unsure = true;
             }
         }
         for (uint32_t todo = __ballot_sync(kFullMask, unsure && my < here && sub == 0); todo;
              todo &= todo - 1) {
             const int src = __ffs(todo) - 1;
-            const int chosen = choose_exact<T, kListPerLane>(x + (row0 + (src >> 2)) * E, bias, sh);
+            const int chosen = choose_exact<T, N>(x + (row0 + (src >> 2)) * E, bias, sh);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int got = __shfl_sync(kFullMask, chosen, i);

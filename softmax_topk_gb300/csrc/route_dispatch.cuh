@@ -1,10 +1,12 @@
-// Router over experts: the choice of kernel variant and the launches.
+// route_dispatch.cuh -- router over experts: the choice of kernel variant and the
+// launches, per dtype (route_f32.cu, route_bf16.cu).
+#pragma once
+
 #include "host_common.h"
 #include "internal.h"
 #include "kernels/route_kernel.cuh"
 
 namespace os {
-
 namespace {
 
 using route::Shape;
@@ -13,7 +15,7 @@ constexpr int64_t kListRowsPerSm = 16;
 
 // Lanes per group: the largest power of two that still gives every group its
 // own lanes; experts per lane follow.
-Shape make_shape(const RouteArgs& a, int groups) {
+inline Shape make_shape(const RouteArgs& a, int groups) {
     Shape s = {};
     s.experts = a.experts;
     s.K = a.K;
@@ -37,19 +39,19 @@ Shape make_shape(const RouteArgs& a, int groups) {
 
 // Whole vectors: every lane that has experts has a full run, which starts on a
 // boundary of its own size (at most 16 bytes).
-bool whole_runs(const Shape& s, int N, int size, const void* p, const void* q) {
+inline bool whole_runs(const Shape& s, int N, int size, const void* p, const void* q) {
     const int bytes = N * size < 16 ? N * size : 16;
     return s.per_lane == N && s.experts == s.groups * s.lanes * N &&
            reinterpret_cast<uintptr_t>(p) % bytes == 0 && reinterpret_cast<uintptr_t>(q) % bytes == 0;
 }
 
-int64_t grid_for(int64_t rows, int tokens) {
+inline int64_t grid_for(int64_t rows, int tokens) {
     return min64(ceil_div(rows, int64_t(route::kWarps) * tokens), int64_t(1) << 22);
 }
 
 // Rows per warp: one while the GPU has warps to spare (the latency of one
 // row), else several, which share the work after the choice.
-bool share_rows(const RouteArgs& a, Shape& s) {
+inline bool share_rows(const RouteArgs& a, Shape& s) {
     const DeviceInfo* dev = device_info();
     if (!dev) return false;
     while (s.tokens * 2 * s.slots <= 32 && a.rows >= int64_t(dev->sms) * 32 * s.tokens * 2)
@@ -82,19 +84,21 @@ cudaError_t launch_bwd(const RouteArgs& a, Shape s, const int32_t* idx,
 
 // The kernel of four threads per row: rows and groups of whole 16-byte chunks
 // (rows of eight of them, for the copy's placement), lists and choose_exact's
-// runs that fit, and enough rows.
+// runs that fit, enough rows, and enough experts for the lists to pay (65536
+// rows, us, one warp / four threads per row: 64 experts 15.5 / 19.2, 128 with
+// a bias 27 / 29, 256 with a bias and groups 76 / 52, 512 with a bias 160 / 127).
 template <typename T>
 bool list_fits(const RouteArgs& a, const Shape& s, int sms) {
     const int bytes = a.experts * int(sizeof(T));
-    return a.K <= 16 && a.experts <= route::kListExperts && bytes % 128 == 0 &&
-           a.experts / a.groups * int(sizeof(T)) % 16 == 0 && s.per_lane <= route::kListPerLane &&
+    return a.K <= 16 && a.experts >= 256 && a.experts <= route::kListExperts && bytes % 128 == 0 &&
+           a.experts / a.groups * int(sizeof(T)) % 16 == 0 && s.per_lane <= 32 &&
            reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.rows >= int64_t(sms) * kListRowsPerSm;
 }
 
 template <typename T, int P>
 cudaError_t launch_list(const RouteArgs& a, const Shape& s, float* w, int32_t* idx, int sms,
                         cudaStream_t stream) {
-    auto k = route::route_list_kernel<T, P>;
+    auto k = s.per_lane <= 8 ? route::route_list_kernel<T, P, 8> : route::route_list_kernel<T, P, 32>;
     constexpr int kRows = route::kListWarps * route::kListRows;
     const int smem = (a.experts + 4 * a.groups + (a.groups > 1 ? kRows * a.groups : 0)) * 4 +
                      kRows * a.experts * int(sizeof(T));
@@ -137,16 +141,4 @@ cudaError_t bwd(const RouteArgs& a, const int32_t* idx, const float* dw, void* d
 }
 
 }  // namespace
-
-cudaError_t launch_route(const RouteArgs& a, float* weights, int32_t* idx, cudaStream_t stream) {
-    return a.in == OS_F32 ? fwd<float>(a, weights, idx, stream)
-                          : fwd<__nv_bfloat16>(a, weights, idx, stream);
-}
-
-cudaError_t launch_route_bwd(const RouteArgs& a, const int32_t* idx, const float* dweights,
-                             void* dx, cudaStream_t stream) {
-    return a.in == OS_F32 ? bwd<float>(a, idx, dweights, dx, stream)
-                          : bwd<__nv_bfloat16>(a, idx, dweights, dx, stream);
-}
-
 }  // namespace os

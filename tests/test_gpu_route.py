@@ -88,7 +88,8 @@ def test_groups(st, experts, K, groups, topk_groups, group_top, dtype, score):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("experts,K,groups,topk_groups,group_top", [
     (64, 1, 1, 1, 1), (64, 4, 8, 3, 2), (128, 3, 1, 1, 1), (128, 8, 4, 2, 2), (256, 8, 1, 1, 1),
-    (256, 6, 8, 4, 2), (320, 5, 5, 2, 1), (384, 9, 3, 2, 2), (512, 16, 1, 1, 1), (512, 10, 16, 7, 2)])
+    (256, 6, 8, 4, 2), (320, 5, 5, 2, 1), (384, 9, 3, 2, 2), (512, 16, 1, 1, 1), (512, 10, 16, 7, 2),
+    (256, 1, 1, 1, 1), (256, 4, 32, 9, 2), (1024, 8, 1, 1, 1), (960, 12, 15, 4, 1)])
 def test_batches_of_a_thread_per_row(st, experts, K, groups, topk_groups, group_top, dtype, score):
     """Rows enough for the kernel with a thread per row, the last tile ragged; with and without
     a bias, missing experts and empty rows among them."""
@@ -107,8 +108,8 @@ def test_near_ties_in_a_large_batch(st, score):
     g = torch.Generator(device="cuda")
     g.manual_seed(19)
     base = torch.randn(2500, 1, generator=g, device="cuda")
-    x = base + torch.randint(-3, 4, (2500, 64), generator=g, device="cuda") * 2.0 ** -24 * base.abs()
-    bias = torch.randint(-2, 3, (64,), generator=g, device="cuda").float() * 2.0 ** -25
+    x = base + torch.randint(-3, 4, (2500, 256), generator=g, device="cuda") * 2.0 ** -24 * base.abs()
+    bias = torch.randint(-2, 3, (256,), generator=g, device="cuda").float() * 2.0 ** -25
     for b in (None, bias, bias + 1.0, bias * 0):
         check(st, x, 7, score=score, bias=b)
 
