@@ -190,7 +190,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
         }
         for (int s = 0; s < WS; ++s) {
             mbar_init(&bars.w_full[s], 1);
-            mbar_init(&bars.w_empty[s], 1);
+            mbar_init(&bars.w_empty[s], KV ? 2 : 1);  // A2, and with KV P W
         }
         mbar_init(&bars.a1_full, 1);
         mbar_init(&bars.a2_full, 1);
@@ -326,7 +326,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                 umma::fence_after_sync();
                 product(TM::kA2, y_desc, tile_at(w_desc, ws));
                 umma::commit(&bars.a2_full);
-                if (!KV) umma::commit(&bars.w_empty[ws]);
+                umma::commit(&bars.w_empty[ws]);
                 if (last) umma::commit(&bars.x_empty);  // the last reader of X and Y
             };
             // the item's first products (j == 0) overwrite the sums, which the
@@ -335,6 +335,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                 const int us = g % US, ws = g % WS;
                 if (j == 0 && it > 0) wait(&bars.acc_empty, (it - 1) & 1);
                 if (KV) {
+                    wait(&bars.w_full[ws], (g / WS) & 1);  // P does not depend on W
                     wait(&bars.p_full, g & 1);
                     if (!wait.ok) return;
                     umma::fence_after_sync();
@@ -342,7 +343,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                     umma::commit(&bars.pw_done);
                     umma::commit(&bars.w_empty[ws]);
                 }
-                wait(&bars.ds_full, g & 1);
+                wait(&bars.ds_full, g & 1);  // U(g): dS was made from its product
                 if (!wait.ok) return;
                 umma::fence_after_sync();
                 accumulate(TM::kAcc1, TM::kDs + 32 * (g % TM::kDsBuffers), tile_at(u_sum, us), j > 0);
