@@ -400,14 +400,24 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, out=Non
 
 
 def _like(name, t, shape, dtype, device):
-    """An output or optional input: `t` when it fits, a new tensor when it is None."""
-    if t is None:
-        import torch
-        return torch.empty(shape, dtype=dtype, device=device)
+    """`t`, when it is a contiguous tensor of this shape, dtype and device."""
     if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
                          f"on {device}")
     return t
+
+
+def _call(device, name, fn, *args):
+    """fn(*args, torch's current stream on `device`), with that device current."""
+    import torch
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with _OnDevice(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _check(status, name)
 
 
 def attention_backward(q, k, v, out, lse, dout, causal: bool = False, scale: float | None = None,
@@ -417,30 +427,30 @@ def attention_backward(q, k, v, out, lse, dout, causal: bool = False, scale: flo
     or None).  ``causal`` and ``scale`` as in the forward call.  ``delta`` is an fp32
     workspace of lse's shape (allocated when not given)."""
     import torch
-    if not q.is_cuda or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.dim() < 2:
+    bf16, f32 = torch.bfloat16, torch.float32
+    if not q.is_cuda or q.dtype != bf16 or not q.is_contiguous() or q.dim() < 2:
         raise ValueError("q must be a contiguous bf16 CUDA tensor [..., n, head_dim]")
-    shape, dev, bf16 = q.shape, q.device, torch.bfloat16
-    for name, t in (("k", k), ("v", v), ("out", out), ("dout", dout)):
-        if t is None:
-            raise ValueError(f"{name} is required")
-        _like(name, t, shape, bf16, dev)
     if lse is None:
         raise ValueError("lse is required: call attention with want_lse=True")
-    _like("lse", lse, shape[:-1], torch.float32, dev)
-    if dlse is not None:
-        _like("dlse", dlse, shape[:-1], torch.float32, dev)
+    shape, dev = q.shape, q.device
+    rows = shape[:-1]
     n, hd = shape[-2], shape[-1]
-    bh = q.numel() // max(n * hd, 1)
-    dq = _like("dq", dq, shape, bf16, dev)
-    dk = _like("dk", dk, shape, bf16, dev)
-    dv = _like("dv", dv, shape, bf16, dev)
-    delta = _like("delta", delta, shape[:-1], torch.float32, dev)
-    s = (1.0 / hd ** 0.5) if scale is None else float(scale)
-    with _OnDevice(dev):
-        os_attention_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                         dout.data_ptr(), dlse.data_ptr() if dlse is not None else None,
-                         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), delta.data_ptr(), bh, n, hd,
-                         s, int(causal), _stream_handle(q))
+    _like("k", k, shape, bf16, dev)
+    _like("v", v, shape, bf16, dev)
+    _like("out", out, shape, bf16, dev)
+    _like("dout", dout, shape, bf16, dev)
+    _like("lse", lse, rows, f32, dev)
+    if dlse is not None:
+        _like("dlse", dlse, rows, f32, dev)
+    dq = torch.empty_like(q) if dq is None else _like("dq", dq, shape, bf16, dev)
+    dk = torch.empty_like(q) if dk is None else _like("dk", dk, shape, bf16, dev)
+    dv = torch.empty_like(q) if dv is None else _like("dv", dv, shape, bf16, dev)
+    delta = torch.empty_like(lse) if delta is None else _like("delta", delta, rows, f32, dev)
+    _call(dev, "os_attention_bwd", _lib.os_attention_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+          None if dlse is None else dlse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+          delta.data_ptr(), q.numel() // max(n * hd, 1), n, hd,
+          1.0 / hd ** 0.5 if scale is None else float(scale), int(causal))
     return dq, dk, dv
 
 
@@ -455,17 +465,23 @@ def route(x, K: int, score: str | int = "softmax", bias=None, groups: int = 1,
     import torch
     if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D CUDA tensor")
+    code = _dtype_code(x.dtype)
     rows, experts = x.shape
+    dev, shape = x.device, (rows, K)
     if bias is not None:
-        _like("bias", bias, (experts,), torch.float32, x.device)
-    weights = _like("weights", weights, (rows, K), torch.float32, x.device)
-    idx = _like("idx", idx, (rows, K), torch.int32, x.device)
-    code = SCORES[score] if isinstance(score, str) else int(score)
-    with _OnDevice(x.device):
-        os_route_topk(x.data_ptr(), bias.data_ptr() if bias is not None else None,
-                      weights.data_ptr(), idx.data_ptr(), rows, experts, K, groups,
-                      groups if topk_groups is None else topk_groups, group_top, code,
-                      int(renorm), scale, _dtype_code(x.dtype), _stream_handle(x))
+        _like("bias", bias, (experts,), torch.float32, dev)
+    if weights is None:
+        weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _like("weights", weights, shape, torch.float32, dev)
+    if idx is None:
+        idx = torch.empty(shape, dtype=torch.int32, device=dev)
+    else:
+        _like("idx", idx, shape, torch.int32, dev)
+    _call(dev, "os_route_topk", _lib.os_route_topk, x.data_ptr(),
+          None if bias is None else bias.data_ptr(), weights.data_ptr(), idx.data_ptr(), rows,
+          experts, K, groups, groups if topk_groups is None else topk_groups, group_top,
+          SCORES[score] if isinstance(score, str) else int(score), int(renorm), scale, code)
     return weights, idx
 
 
@@ -479,17 +495,26 @@ def route_backward(x, idx, dweights, score: str | int = "softmax", renorm: bool 
         raise ValueError("x must be a contiguous 2-D CUDA tensor")
     if idx.dim() != 2:
         raise ValueError("idx must be int32 [rows, K]")
+    code = _dtype_code(x.dtype)
     rows, experts = x.shape
     K = idx.shape[1]
-    _like("idx", idx, (rows, K), torch.int32, x.device)
-    _like("dweights", dweights, (rows, K), torch.float32, x.device)
-    dx = _like("dx", dx, x.shape, x.dtype, x.device)
-    code = SCORES[score] if isinstance(score, str) else int(score)
-    with _OnDevice(x.device):
-        os_route_bwd(x.data_ptr(), idx.data_ptr(), dweights.data_ptr(), dx.data_ptr(), rows,
-                     experts, K, code, int(renorm), scale, _dtype_code(x.dtype),
-                     _stream_handle(x))
+    dev, shape = x.device, (rows, K)
+    _like("idx", idx, shape, torch.int32, dev)
+    _like("dweights", dweights, shape, torch.float32, dev)
+    dx = torch.empty_like(x) if dx is None else _like("dx", dx, x.shape, x.dtype, dev)
+    _call(dev, "os_route_bwd", _lib.os_route_bwd, x.data_ptr(), idx.data_ptr(),
+          dweights.data_ptr(), dx.data_ptr(), rows, experts, K,
+          SCORES[score] if isinstance(score, str) else int(score), int(renorm), scale, code)
     return dx
+
+
+def _setting(settings, name, value, rows, dtype, device):
+    """One of os_sample's settings: a tensor of a value per row, or one for all."""
+    import torch
+    if isinstance(value, torch.Tensor):
+        setattr(settings, name, _like(name, value, (rows,), dtype, device).data_ptr())
+    else:
+        setattr(settings, name + "_all", value)
 
 
 def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, prob=None):
@@ -501,23 +526,27 @@ def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, prob=
     import torch
     if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D CUDA tensor")
-    rows = x.shape[0]
-    settings = Sampling()
-    for name, value, dtype in (("temperature", temperature, torch.float32),
-                               ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32),
-                               ("min_p", min_p, torch.float32)):
-        if isinstance(value, torch.Tensor):
-            setattr(settings, name, _like(name, value, (rows,), dtype, x.device).data_ptr())
-        else:
-            setattr(settings, name + "_all", value)
     if u is None:
         raise ValueError("u is required: one uniform number per row")
-    _like("u", u, (rows,), torch.float32, x.device)
-    out = _like("out", out, (rows,), torch.int32, x.device)
-    prob = _like("prob", prob, (rows,), torch.float32, x.device)
-    with _OnDevice(x.device):
-        os_sample(x.data_ptr(), u.data_ptr(), settings, out.data_ptr(), prob.data_ptr(), rows,
-                  x.shape[1], _dtype_code(x.dtype), _stream_handle(x))
+    code = _dtype_code(x.dtype)
+    rows, cols = x.shape
+    dev, f32, i32 = x.device, torch.float32, torch.int32
+    settings = Sampling()
+    _setting(settings, "temperature", temperature, rows, f32, dev)
+    _setting(settings, "top_k", top_k, rows, i32, dev)
+    _setting(settings, "top_p", top_p, rows, f32, dev)
+    _setting(settings, "min_p", min_p, rows, f32, dev)
+    _like("u", u, (rows,), f32, dev)
+    if out is None:
+        out = torch.empty(rows, dtype=i32, device=dev)
+    else:
+        _like("out", out, (rows,), i32, dev)
+    if prob is None:
+        prob = torch.empty(rows, dtype=f32, device=dev)
+    else:
+        _like("prob", prob, (rows,), f32, dev)
+    _call(dev, "os_sample", _lib.os_sample, x.data_ptr(), u.data_ptr(), ctypes.byref(settings),
+          out.data_ptr(), prob.data_ptr(), rows, cols, code)
     return out, prob
 
 

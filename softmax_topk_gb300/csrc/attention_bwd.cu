@@ -11,40 +11,52 @@ namespace os {
 
 namespace {
 
+using attn_bwd::Side;
+
 template <int D, bool KV>
-cudaError_t launch_side(const CUtensorMap& mx, const CUtensorMap& my, const CUtensorMap& mu,
-                        const CUtensorMap& mw, const float* lse, const float* delta, void* out1,
-                        void* out2, int64_t bh, int n, float scale, bool causal,
+cudaError_t launch_side(const Side& side, const AttentionBwdArgs& a, int nt, int64_t units, int sms,
                         const KernelCtl& ctl, cudaStream_t stream) {
     auto k = attn_bwd::attention_bwd_kernel<D, KV>;
     constexpr int smem = attn_bwd::Layout<D>::kBytes;
     if (!prepare_kernel(k, 1, smem)) return cudaErrorInvalidConfiguration;
-    const DeviceInfo* dev = device_info();
-    if (!dev) return cudaErrorInvalidDevice;
-    const int nt = (n + attn_bwd::kRows - 1) / attn_bwd::kRows;
-    const int64_t units = causal ? bh * ((nt + 1) / 2) : bh * nt;
-    return launch_kernel(k, min64(units, dev->sms), attn_bwd::kThreads, 1, smem, stream, mx, my, mu,
-                         mw, lse, delta, static_cast<__nv_bfloat16*>(out1),
-                         static_cast<__nv_bfloat16*>(out2), n, nt, static_cast<int>(units), scale,
-                         causal ? 1 : 0, ctl);
+    return launch_kernel(k, min64(units, sms), attn_bwd::kThreads, 1, smem, stream, side, a.lse,
+                         static_cast<const float*>(a.delta), a.n, nt, static_cast<int>(units),
+                         a.scale, a.causal ? 1 : 0, ctl);
 }
 
 template <int D>
 cudaError_t launch_d(const AttentionBwdArgs& a, const KernelCtl& ctl, cudaStream_t stream) {
-    CUtensorMap mq, mk, mv, mdo;
-    if (!make_tile_map(&mq, a.q, a.bh, a.n, D) || !make_tile_map(&mk, a.k, a.bh, a.n, D) ||
-        !make_tile_map(&mv, a.v, a.bh, a.n, D) || !make_tile_map(&mdo, a.dout, a.bh, a.n, D))
+    const DeviceInfo* dev = device_info();
+    if (!dev) return cudaErrorInvalidDevice;
+    Side kv = {}, q = {};
+    if (!make_tile_map(&kv.x, a.k, a.bh, a.n, D) || !make_tile_map(&kv.y, a.v, a.bh, a.n, D) ||
+        !make_tile_map(&kv.u, a.q, a.bh, a.n, D) || !make_tile_map(&kv.w, a.dout, a.bh, a.n, D))
         return cudaErrorInvalidValue;
+    kv.out1 = static_cast<__nv_bfloat16*>(a.dk);
+    kv.out2 = static_cast<__nv_bfloat16*>(a.dv);
+    q.x = kv.u;
+    q.y = kv.w;
+    q.u = kv.x;
+    q.w = kv.y;
+    q.out1 = static_cast<__nv_bfloat16*>(a.dq);
     const int64_t rows = a.bh * a.n;
     cudaError_t e = launch_kernel(attn_bwd::delta_kernel<D>, ceil_div(rows * (D / 8), 256), 256, 1,
                                   0, stream, static_cast<const __nv_bfloat16*>(a.o),
                                   static_cast<const __nv_bfloat16*>(a.dout), a.dlse, a.delta, rows);
     if (e != cudaSuccess) return e;
-    e = launch_side<D, true>(mk, mv, mq, mdo, a.lse, a.delta, a.dk, a.dv, a.bh, a.n, a.scale,
-                             a.causal, ctl, stream);
+    const int nt = (a.n + attn_bwd::kRows - 1) / attn_bwd::kRows;
+    const int64_t units = a.causal ? a.bh * ((nt + 1) / 2) : a.bh * nt;
+    if (2 * units <= dev->sms) {
+        auto k = attn_bwd::attention_bwd_both_kernel<D>;
+        constexpr int smem = attn_bwd::Layout<D>::kBytes;
+        if (!prepare_kernel(k, 1, smem)) return cudaErrorInvalidConfiguration;
+        return launch_kernel(k, 2 * units, attn_bwd::kThreads, 1, smem, stream, kv, q, a.lse,
+                             static_cast<const float*>(a.delta), a.n, nt, static_cast<int>(units),
+                             a.scale, a.causal ? 1 : 0, ctl);
+    }
+    e = launch_side<D, true>(kv, a, nt, units, dev->sms, ctl, stream);
     if (e != cudaSuccess) return e;
-    return launch_side<D, false>(mq, mdo, mk, mv, a.lse, a.delta, a.dq, nullptr, a.bh, a.n, a.scale,
-                                 a.causal, ctl, stream);
+    return launch_side<D, false>(q, a, nt, units, dev->sms, ctl, stream);
 }
 
 }  // namespace

@@ -162,15 +162,22 @@ delta_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restric
     if (row < rows && part == 0) delta[row] = s - (dlse ? dlse[row] : 0.f);
 }
 
+// One side's arguments.
+struct Side {
+    CUtensorMap x, y, u, w;
+    __nv_bfloat16 *out1, *out2;
+};
+
+// The program of one CTA: number `cta` of `ctas` that walk the side's units.
 template <int D, bool KV>
-__global__ void __launch_bounds__(kThreads, 1)
-attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
-                     const __grid_constant__ CUtensorMap map_y,
-                     const __grid_constant__ CUtensorMap map_u,
-                     const __grid_constant__ CUtensorMap map_w, const float* __restrict__ lse,
-                     const float* __restrict__ delta, __nv_bfloat16* __restrict__ out1,
-                     __nv_bfloat16* __restrict__ out2, int n, int nt, int units, float scale,
-                     int causal_flag, KernelCtl ctl) {
+__device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensorMap& map_y,
+                                        const CUtensorMap& map_u, const CUtensorMap& map_w,
+                                        const float* __restrict__ lse,
+                                        const float* __restrict__ delta,
+                                        __nv_bfloat16* __restrict__ out1,
+                                        __nv_bfloat16* __restrict__ out2, int n, int nt, int units,
+                                        float scale, int causal_flag, const KernelCtl& ctl, int cta,
+                                        int ctas) {
     using L = Layout<D>;
     using TM = Tmem<KV>;
     constexpr int US = L::kUStages, WS = L::kWStages;
@@ -227,7 +234,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
             umma::prefetch_tensormap(&map_w);
             Waiter wait(ctl);
             int g = 0, nu = 0, it = 0;  // tiles of W and of U, items so far
-            for (int u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
+            for (int u = cta; u < units && wait.ok; u += ctas) {
                 int bh, ta, tb;
                 const int cnt = attn::work_unit(u, nt, causal, bh, ta, tb);
                 for (int e = 0; e < cnt && wait.ok; ++e) {
@@ -351,7 +358,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
                 umma::commit(&bars.u_empty[us]);
             };
             int g = 0, it = 0;
-            for (int u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
+            for (int u = cta; u < units && wait.ok; u += ctas) {
                 int bh, ta, tb;
                 const int cnt = attn::work_unit(u, nt, causal, bh, ta, tb);
                 for (int e = 0; e < cnt && wait.ok; ++e, ++it) {
@@ -374,7 +381,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
         if (KV) {
             Waiter wait(ctl);
             int g = 0;
-            for (int u = blockIdx.x; u < units; u += gridDim.x) {
+            for (int u = cta; u < units; u += ctas) {
                 int bh, ta, tb;
                 const int cnt = attn::work_unit(u, nt, causal, bh, ta, tb);
                 for (int e = 0; e < cnt; ++e) {
@@ -413,7 +420,7 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
         const float scale_log2 = scale * kLog2e;
         Waiter wait(ctl);
         int g = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        for (int u = cta; u < units; u += ctas) {
             int bh, ta, tb;
             const int cnt = attn::work_unit(u, nt, causal, bh, ta, tb);
             for (int e = 0; e < cnt; ++e) {
@@ -569,6 +576,31 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
         umma::fence_after_sync();
         umma::tmem_dealloc(tmem, kTmemCols);
     }
+}
+
+// One side per launch.
+template <int D, bool KV>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_bwd_kernel(const __grid_constant__ Side side, const float* __restrict__ lse,
+                     const float* __restrict__ delta, int n, int nt, int units, float scale,
+                     int causal, KernelCtl ctl) {
+    bwd_cta<D, KV>(side.x, side.y, side.u, side.w, lse, delta, side.out1, side.out2, n, nt, units,
+                   scale, causal, ctl, blockIdx.x, gridDim.x);
+}
+
+// Both sides at once, a CTA per unit of each: for sizes at which that many CTAs
+// fit the SMs (2 x 300, d = 64: 28 us a call with two launches after delta's).
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_bwd_both_kernel(const __grid_constant__ Side kv, const __grid_constant__ Side q,
+                          const float* __restrict__ lse, const float* __restrict__ delta, int n,
+                          int nt, int units, float scale, int causal, KernelCtl ctl) {
+    if (int(blockIdx.x) < units)
+        bwd_cta<D, true>(kv.x, kv.y, kv.u, kv.w, lse, delta, kv.out1, kv.out2, n, nt, units, scale,
+                         causal, ctl, blockIdx.x, units);
+    else
+        bwd_cta<D, false>(q.x, q.y, q.u, q.w, lse, delta, q.out1, q.out2, n, nt, units, scale,
+                          causal, ctl, blockIdx.x - units, units);
 }
 
 }  // namespace attn_bwd

@@ -802,6 +802,14 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
         for (int r = 0; r < here; ++r)
             for (int c = lane; c < chunks; c += 32)
                 cp_async16(tile + place(r, c), x + (row0 + r) * E + c * EPV);
+        // the next tile on its way into L2 while this one is worked on
+        const int64_t ahead = t + int64_t(gridDim.x) * kListWarps;
+        if (ahead < tiles) {
+            const unsigned char* p = reinterpret_cast<const unsigned char*>(x + ahead * kListRows * E);
+            const int bytes = int(min(int64_t(kListRows), rows - ahead * kListRows)) * E * int(sizeof(T));
+            for (int i = lane * 128; i < bytes; i += 32 * 128)
+                asm volatile("prefetch.global.L2 [%0];" :: "l"(p + i));
+        }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
         // threads past the last row work on row 0 and write nothing
