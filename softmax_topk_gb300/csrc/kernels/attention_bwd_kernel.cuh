@@ -44,7 +44,8 @@
 // columns, so A1 and A2 take turns in one buffer of 128, and P and dS share
 // another.  A1 and A2 are read into registers as soon as they are complete, and
 // the sums run between them: A1(g), dS(g-1) U, A2(g), P(g) W, A1(g+1), ...
-// Without KV A1, A2 and two buffers for dS have room of their own.
+// Otherwise A1 and A2 have buffers of their own (d = 64, 16 x 16384 causal: 1851
+// us with a shared one), and without KV dS has two.
 #pragma once
 
 #include <cuda.h>
@@ -71,15 +72,16 @@ constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 // Tensor memory columns.  bf16 operands (P, dS) take 32 columns for tile
 // columns 0-63 and 32 for 64-127, 64 apart.
-template <bool KV>
+template <int D, bool KV>
 struct Tmem {
+    static constexpr bool kShared = KV && D == 128;   // A1 and A2 in one buffer
     static constexpr uint32_t kA1 = 0;                // fp32, 128 columns
-    static constexpr uint32_t kA2 = KV ? 0 : 128;     // fp32, 128 columns
-    static constexpr uint32_t kP = 128;               // KV
-    static constexpr uint32_t kDs = KV ? 160 : 384;   // tile g at kDs + 32 (g % kDsBuffers)
+    static constexpr uint32_t kA2 = kShared ? 0 : 128;
+    static constexpr uint32_t kP = kShared ? 128 : 256;   // KV
+    static constexpr uint32_t kDs = KV ? kP + 32 : 384;   // tile g at kDs + 32 (g % kDsBuffers)
     static constexpr int kDsBuffers = KV ? 1 : 2;
-    static constexpr uint32_t kAcc1 = 256;            // dK or dQ, D columns
-    static constexpr uint32_t kAcc2 = 384;            // dV, D columns (KV)
+    static constexpr uint32_t kAcc1 = kShared || !KV ? 256 : 384;  // dK or dQ, D columns
+    static constexpr uint32_t kAcc2 = kShared ? 384 : 448;         // dV, D columns (KV)
 };
 constexpr float kLog2e = 1.442695041f;
 
@@ -111,7 +113,7 @@ struct Barriers {
     uint64_t a1_free, a2_free;                     // they are in registers (all compute threads)
     uint64_t p_full, ds_full;                      // P / dS in tensor memory (all compute threads)
     uint64_t pw_done;                              // acc2 += P W completed
-    uint64_t acc_done[2];                          // acc1 += dS U of tile g (at g & 1) completed
+    uint64_t acc_done[2];                          // both sums of tile g (at g & 1) completed
     uint64_t acc_empty;                            // an item's sums are in registers
     uint64_t stat_full[2], stat_empty[2];          // the streamed rows' statistics there / read
     uint64_t drain;
@@ -179,7 +181,7 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
                                         float scale, int causal_flag, const KernelCtl& ctl, int cta,
                                         int ctas) {
     using L = Layout<D>;
-    using TM = Tmem<KV>;
+    using TM = Tmem<D, KV>;
     constexpr int US = L::kUStages, WS = L::kWStages;
     static_assert(sizeof(Barriers<D>) <= L::kBytes - L::kBars, "barriers");
     // no static shared memory: the dynamic part starts on a 1024-byte boundary
@@ -317,7 +319,7 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
             auto issue_a1 = [&](int g, bool last) {
                 const int us = g % US;
                 wait(&bars.u_full[us], (g / US) & 1);
-                if (g > 0) wait(KV ? &bars.a2_free : &bars.a1_free, (g - 1) & 1);
+                if (g > 0) wait(TM::kShared ? &bars.a2_free : &bars.a1_free, (g - 1) & 1);
                 if (!wait.ok) return;
                 umma::fence_after_sync();
                 product(TM::kA1, x_desc, tile_at(u_desc, us));
@@ -327,7 +329,7 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
             auto issue_a2 = [&](int g, bool last) {
                 const int ws = g % WS;
                 wait(&bars.w_full[ws], (g / WS) & 1);
-                if (KV) wait(&bars.a1_free, g & 1);
+                if (TM::kShared) wait(&bars.a1_free, g & 1);
                 else if (g > 0) wait(&bars.a2_free, (g - 1) & 1);
                 if (!wait.ok) return;
                 umma::fence_after_sync();
@@ -347,7 +349,7 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
                     if (!wait.ok) return;
                     umma::fence_after_sync();
                     accumulate(TM::kAcc2, TM::kP, tile_at(w_sum, ws), j > 0);
-                    umma::commit(&bars.pw_done);
+                    if (D == 128) umma::commit(&bars.pw_done);
                     umma::commit(&bars.w_empty[ws]);
                 }
                 wait(&bars.ds_full, g & 1);  // U(g): dS was made from its product
@@ -447,6 +449,16 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
                     umma::tmem_wait_ld();
                     umma::fence_before_sync();
                     umma::mbar_arrive(&bars.a1_free);
+                    float dp[64];
+                    constexpr bool kEarly = !KV && D == 64;
+                    if (kEarly) {
+                        // A2 is there by now, and its load passes under the
+                        // exponentials
+                        wait(&bars.a2_full, g & 1);
+                        umma::fence_after_sync();
+                        umma::tmem_ld32(a2, dp);
+                        umma::tmem_ld32(a2 + 32, dp + 32);
+                    }
                     // columns [lo, hi) of this half take part: keys up to the
                     // end and the query (KV = false), queries from the key on
                     // (KV = true; queries past the end have L = +inf)
@@ -481,7 +493,13 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
                         uint32_t pk[32];
 #pragma unroll
                         for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-                        if (g > 0) wait(&bars.pw_done, (g - 1) & 1);
+                        // P's last reader: P W of tile g - 1.  At d = 64 dS U of
+                        // that tile is done by now too and its barrier serves
+                        // both; at d = 128 it would hold P up (1195 -> 1303 us)
+                        if (g > 0) {
+                            if (D == 128) wait(&bars.pw_done, (g - 1) & 1);
+                            else wait(&bars.acc_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+                        }
                         umma::fence_after_sync();
                         umma::tmem_st32(lane_addr + TM::kP + 64 * half,
                                         reinterpret_cast<const float*>(pk));
@@ -490,12 +508,16 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
                         umma::mbar_arrive(&bars.p_full);
                     }
 
-                    float dp[64];
-                    wait(&bars.a2_full, g & 1);
-                    umma::fence_after_sync();
-                    umma::tmem_ld32(a2, dp);
-                    umma::tmem_ld32(a2 + 32, dp + 32);
+                    if (!kEarly) {
+                        wait(&bars.a2_full, g & 1);
+                        umma::fence_after_sync();
+                        umma::tmem_ld32(a2, dp);
+                        umma::tmem_ld32(a2 + 32, dp + 32);
+                    }
                     umma::tmem_wait_ld();
+                    // (nothing that uses dp moves above the wait)
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(dp[c]));
                     umma::fence_before_sync();
                     umma::mbar_arrive(&bars.a2_free);
                     uint32_t ds[32];
@@ -521,8 +543,10 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
                     }
                     // the buffer's last reader: the sum of tile g - kDsBuffers
                     constexpr int lag = TM::kDsBuffers;
-                    if (g >= lag) wait(&bars.acc_done[(g - lag) & 1], ((g - lag) >> 1) & 1);
-                    umma::fence_after_sync();
+                    if ((!KV || D == 128) && g >= lag) {
+                        wait(&bars.acc_done[(g - lag) & 1], ((g - lag) >> 1) & 1);
+                        umma::fence_after_sync();
+                    }
                     umma::tmem_st32(lane_addr + TM::kDs + 32 * (g % lag) + 64 * half,
                                     reinterpret_cast<const float*>(ds));
                     umma::tmem_wait_st();
