@@ -44,7 +44,7 @@ cudaError_t launch_d(const AttentionBwdArgs& a, const KernelCtl& ctl, cudaStream
                                   0, stream, static_cast<const __nv_bfloat16*>(a.o),
                                   static_cast<const __nv_bfloat16*>(a.dout), a.dlse, a.delta, rows);
     if (e != cudaSuccess) return e;
-    const int nt = (a.n + attn_bwd::kRows - 1) / attn_bwd::kRows;
+    const int nt = static_cast<int>(ceil_div(a.n, attn_bwd::kRows));
     const int64_t units = a.causal ? a.bh * ((nt + 1) / 2) : a.bh * nt;
     if (2 * units <= dev->sms) {
         auto k = attn_bwd::attention_bwd_both_kernel<D>;

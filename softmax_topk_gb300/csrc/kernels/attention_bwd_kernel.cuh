@@ -111,7 +111,9 @@ struct Barriers {
     uint64_t w_full[L::kWStages], w_empty[L::kWStages];
     uint64_t a1_full, a2_full;                     // A1 / A2 of a tile in tensor memory
     uint64_t a1_free, a2_free;                     // they are in registers (all compute threads)
-    uint64_t p_full, ds_full;                      // P / dS in tensor memory (all compute threads)
+    uint64_t p_full;                               // P in tensor memory (all compute threads)
+    uint64_t ds_full[2];                           // dS likewise, one per buffer: a buffer is
+                                                   // filled again only once its sum was issued
     uint64_t pw_done;                              // acc2 += P W completed
     uint64_t acc_done[2];                          // both sums of tile g (at g & 1) completed
     uint64_t acc_empty;                            // an item's sums are in registers
@@ -204,7 +206,8 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
         mbar_init(&bars.a1_full, 1);
         mbar_init(&bars.a2_full, 1);
         mbar_init(&bars.p_full, kCompute);
-        mbar_init(&bars.ds_full, kCompute);
+        mbar_init(&bars.ds_full[0], kCompute);
+        mbar_init(&bars.ds_full[1], kCompute);
         mbar_init(&bars.a1_free, kCompute);
         mbar_init(&bars.a2_free, kCompute);
         mbar_init(&bars.pw_done, 1);
@@ -352,10 +355,11 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
                     if (D == 128) umma::commit(&bars.pw_done);
                     umma::commit(&bars.w_empty[ws]);
                 }
-                wait(&bars.ds_full, g & 1);  // U(g): dS was made from its product
+                constexpr int B = TM::kDsBuffers;
+                wait(&bars.ds_full[g % B], (g / B) & 1);  // U(g): dS was made from its product
                 if (!wait.ok) return;
                 umma::fence_after_sync();
-                accumulate(TM::kAcc1, TM::kDs + 32 * (g % TM::kDsBuffers), tile_at(u_sum, us), j > 0);
+                accumulate(TM::kAcc1, TM::kDs + 32 * (g % B), tile_at(u_sum, us), j > 0);
                 umma::commit(&bars.acc_done[g & 1]);
                 umma::commit(&bars.u_empty[us]);
             };
@@ -551,7 +555,7 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
                                     reinterpret_cast<const float*>(ds));
                     umma::tmem_wait_st();
                     umma::fence_before_sync();
-                    umma::mbar_arrive(&bars.ds_full);
+                    umma::mbar_arrive(&bars.ds_full[g % lag]);
                     if (KV) {
                         __syncwarp();
                         if (lane == 0) umma::mbar_arrive(&bars.stat_empty[g & 1]);
