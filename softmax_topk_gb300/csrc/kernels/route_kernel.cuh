@@ -18,11 +18,12 @@
 //
 // Exact choices.  Without a bias s rises with x, so logits are compared and
 // the choice is exact.  With a bias (and for sums of two scores) c is computed
-// s carries at most (|x - m| + 12) 2^-24 relative, which is at most
-// 2^-20 s_max absolute (|z| e^-|z| is small where s is), and the sum one
-// rounding.  A token in which two compared values lie closer than the bounds
-// allow (about 1 in 500 for 256 experts and 8 choices), and are not of equal
-// logit and bias, is chosen again with s and c in 64 bits.
+// in fp32 with bounds: s carries at most (|x - m| + 12) 2^-24 relative, which is
+// at most 2^-20 s_max absolute (|z| e^-|z| is small where s is), and the sum one
+// rounding.  Three steps, each for the tokens that the one before could not
+// settle: choices by 32-bit keys, a value with its low bits replaced by its
+// place; by full fp32 values of exact functions (choose_exact); and in 64 bits
+// (choose_wide).  Values of equal logit and bias need no more digits.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -1005,6 +1006,9 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
 #pragma unroll
                 for (int i = 0; i + 1 < C; ++i)
                     if (c[i + 1] > c[i]) swap_at(i);
+            // (an expert more than two places down may have farther to go)
+#pragma unroll
+            for (int i = 0; i + 1 < C; ++i) unsure = unsure || c[i + 1] > c[i];
         }
         // values too near to their successors for this arithmetic
         bool near = false;
@@ -1015,29 +1019,37 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
         }
         if (__any_sync(kFullMask, near && !exact_keys)) {
             // pairs in 64 bits: a sigmoid's needs nothing of the row (a
-            // softmax's sum would); twice over for three in a row
+            // softmax's sum would); twice over for three in a row, and where
+            // the second time still finds a pair to exchange there are more.
+            // A run of near values that goes past slot K - 1 is ordered to its
+            // end, for any of them may belong there
             auto wide = [&](int i) {
                 return wide_choice(logit(e[i]), b_sm[e[i] + 4 * (e[i] / gsize)]);
             };
 #pragma unroll 1
             for (int pass = 0; pass < 2; ++pass) {
+                bool bad = false;
 #pragma unroll
                 for (int i = 0; i + 1 < C; ++i) {
                     const float slack = by_score ? err + fabsf(c[i]) * 0x1p-22f : 0.f;
-                    bool bad = i < K && c[i + 1] != -INFINITY && !exact_keys && !(c[i] - c[i + 1] > slack);
+                    bad = (i < K || bad) && c[i + 1] != -INFINITY && !exact_keys &&
+                          !(c[i] - c[i + 1] > slack);
                     if (bad) {
                         // equal logits of equal bias stand in the order of
                         // their experts
                         const int p = e[i], n = e[i + 1];
                         const bool same = logit(p) == logit(n) &&
                                           b_sm[p + 4 * (p / gsize)] == b_sm[n + 4 * (n / gsize)];
-                        if (same) {
-                            if (n < p) swap_at(i);
-                        } else if (by_score && sh.sigmoid) {
+                        bool change = same && n < p;
+                        if (!same && by_score && sh.sigmoid) {
                             const double a = wide(i), b = wide(i + 1);
-                            if (b > a || (b == a && n < p)) swap_at(i);
-                        } else {
+                            change = b > a || (b == a && n < p);
+                        } else if (!same) {
                             unsure = true;
+                        }
+                        if (change) {
+                            swap_at(i);
+                            unsure = unsure || pass == 1;
                         }
                     }
                 }

@@ -114,6 +114,56 @@ def test_near_ties_in_a_large_batch(st, score):
         check(st, x, 7, score=score, bias=b)
 
 
+def near_runs(rows, experts, g, values):
+    """Normal logits, in row r 2 + r % 19 of them at random places replaced by values(n)."""
+    x = torch.randn(rows, experts, generator=g)
+    for r in range(rows):
+        n = 2 + r % 19
+        x[r, torch.randperm(experts, generator=g)[:n]] = values(n)
+    return x
+
+
+def check_some(st, x, K, rows=2500, **kw):
+    """x, and rows of it again up to `rows` in all (a large batch), against the oracle of x."""
+    big = x.repeat((rows + len(x) - 1) // len(x), 1)[:rows]
+    w, idx = st.route(big, K, **kw)
+    idx = idx.cpu().numpy()
+    okw = dict(kw)
+    if okw.get("bias") is not None:
+        okw["bias"] = okw["bias"].cpu().numpy().astype(np.float64)
+    _, want = ref.route(x, K, **okw)
+    tied = okw.get("groups", 1) > 1 and okw["group_top"] == 2
+    for r in range(len(x)):
+        if (idx[r::len(x)] != want[r]).any() and not (tied and _border_below_64_bits(x[r], okw)):
+            raise AssertionError(f"row {r}: {idx[r]} for {want[r]}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("experts,K,groups", [(256, 2, 1), (256, 4, 1), (256, 6, 1), (256, 8, 1),
+                                              (512, 12, 1), (512, 16, 1), (256, 8, 8), (1024, 8, 4)])
+def test_runs_of_near_choices(st, experts, K, groups, dtype):
+    """Runs of 2 to 20 saturated scores (1 - e^-x, x from 14 to 22: hardly two apart in fp32, all
+    in 64 bits) in orders of every kind, below and across the border of the choice, with one bias
+    for all and with biases that differ in the last bits."""
+    g = torch.Generator().manual_seed(experts + K + groups)
+    x = near_runs(190, experts, g, lambda n: 14 + 8 * torch.rand(n, generator=g)).to("cuda", DT[dtype])
+    fine = (torch.randint(-3, 4, (experts,), generator=g).float() * 2.0 ** -24).cuda()
+    coarse = (torch.randint(0, 3, (experts,), generator=g).float() * 2.0 ** -12).cuda()
+    for b in (fine * 0, fine, fine + 0.5, coarse):
+        check_some(st, x, K, score="sigmoid", bias=b, groups=groups, topk_groups=max(1, groups // 2),
+                   group_top=2 if groups > 1 else 1)
+
+
+@pytest.mark.parametrize("K", [4, 5, 8, 16])
+def test_runs_of_near_logits(st, K):
+    """Logits that differ in their last bits only, in random order of the experts."""
+    g = torch.Generator().manual_seed(K)
+    x = near_runs(190, 1024, g, lambda n: 5 + torch.arange(n) * 2.0 ** -21).cuda()
+    for score in ("softmax", "sigmoid"):
+        check_some(st, x, K, score=score)
+        check_some(st, x, K, score=score, bias=torch.zeros(1024, device="cuda"))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_large_batches(st, score):
     """Many rows: choices that turn on the last bits of fp32 come up and are settled in 64 bits."""
