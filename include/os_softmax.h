@@ -337,12 +337,13 @@ os_status os_route_bwd(const void *x, const int32_t *idx, const float *dweights,
  *          finite, temperature >= 0, top_k >= 0, top_p and min_p in [0, 1]
  *          (OS_ERR_VALUE); per-row values outside are taken as the nearest
  *          inside, a NaN as 0 (temperature) or as off, and top_k past the
- *          row's length is off.  Temperatures below 1.5e-30 act as that.
+ *          row's length is off.  Temperatures below 5e-29 act as that.
  * Entries of -inf are never drawn, NaN entries count as -inf, and a row
- * without any other entry gives column -1 and probability 0.  Cuts and draws
- * fall where real arithmetic has them, up to 2^-38 relative in the sums: the
- * weights are summed as integers, so a result depends on the row and the
- * settings alone.
+ * without any other entry gives column -1 and probability 0.  Weights are
+ * summed as integers, so a result depends on the row and the settings alone:
+ * each is good to 2^-38 of itself and half a unit of 2^-B of the largest, with
+ * B = 44 for rows of up to 2^18 columns and 62 - log2(columns) beyond, and cuts
+ * and draws fall where real arithmetic has them up to that.
  */
 typedef struct {
     const float *temperature;

@@ -55,6 +55,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kList = 2048;   // columns that a list holds
 constexpr int kBins = 2048;   // steps of the top-p histogram
 constexpr int kTopK = 1024;   // top-k up to here is settled on a list
+constexpr float kColdest = 5e-29f;  // colder rows would leave fp32's range with 32 log2 e / T
 using u64 = unsigned long long;
 
 // 2^(j/32) in two fp32 parts, j = 0..31: the high parts, then the low ones
@@ -130,8 +131,8 @@ struct Weight {
     __device__ __forceinline__ void set(float m_, float temperature, int bits_, const float* t) {
         constexpr float kHi = 0x1.715476p+5f, kLo = 0x1.4ae0cp-21f;  // 32 log2 e
         m = m_;
-        c_hi = fminf(__fdiv_rn(kHi, temperature), 1e30f);
-        c_lo = c_hi < 1e30f && c_hi > 1e-30f
+        c_hi = __fdiv_rn(kHi, temperature);
+        c_lo = c_hi > 1e-30f
                    ? __fdiv_rn(fmaf(-c_hi, temperature, kHi) + kLo, temperature) : 0.f;
         bits = bits_;
         unit = 1.5f * __int_as_float((23 - bits + 127) << 23);
@@ -397,6 +398,13 @@ __device__ __forceinline__ void list_push(Shared& sh, float x, uint32_t col) {
             asm volatile("st.shared::cluster.u64 [%0], %1;"
                          :: "r"(map_to_rank(&sh.list[at], 0)), "l"(e) : "memory");
     }
+}
+
+// How many are on it while others are being put there.
+template <int S>
+__device__ __forceinline__ uint32_t listed_now(Shared& sh) {
+    if constexpr (S == 1) return *static_cast<volatile uint32_t*>(&sh.listed);
+    else return remote<S>(&sh.listed, 0);
 }
 
 // Sorts list[0, n) into sorted[0, n), best (key, lower column) first.  Up to
@@ -754,7 +762,8 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
         const int64_t per_warp = (blocks.count + S * kThreads - 1) / (S * kThreads) * 32;
         const int64_t lo = min(blocks.count, (rank * kWarps + warp) * per_warp);
         const int64_t hi = min(blocks.count, lo + per_warp);
-        const float t_row = s.temperature ? s.temperature[row] : s.temperature_all;
+        float t_row = s.temperature ? s.temperature[row] : s.temperature_all;
+        if (t_row > 0.f) t_row = fmaxf(t_row, kColdest);
         const int k = s.top_k ? s.top_k[row] : s.top_k_all;
         const float tp = s.top_p ? s.top_p[row] : s.top_p_all;
         const float mp = s.min_p ? s.min_p[row] : s.min_p_all;
@@ -774,7 +783,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
         const uint32_t warp_top = __reduce_max_sync(kFullMask, key);
         if (by_p) {
             const float t = key_value(warp_top);
-            near = near > 0.f ? near * ex2_sfu((thread_top - t) * c_near) : 0.f;
+            near = near == 0.f ? 0.f : near * ex2_sfu((thread_top - t) * c_near);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) near += __shfl_xor_sync(kFullMask, near, o);
             if (lane == 0) sh.near[warp] = near;
@@ -855,11 +864,16 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
             uu = 0.f;  // the first kept column
         } else {
             bool settled = !by_k && !(tp < 1.f);
-            if (list_k && bound > kKeyNegInf) {
-                // ---- top-k on a list
-                const float least = key_value(bound);
+            if (list_k) {
+                // ---- top-k on a list.  Where a mask leaves a warp too few
+                // columns for a bound, all that are there, while they fit
+                // (256 x 50257 with 100 columns left, top-k 50: 2105 us by the
+                // general cut, 29 so)
+                const bool all = bound <= kKeyNegInf;
+                const float least = all ? -FLT_MAX : key_value(bound);
 #pragma unroll 2
                 for (int64_t b = lo + lane; b < hi; b += 32) {
+                    if (all && listed_now<S>(sh) > kList) break;
                     float v[EPV];
                     blocks.load(b, v);
 #pragma unroll
@@ -869,6 +883,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                 row_sync<S>();
                 const uint32_t n = remote<S>(&sh.listed, 0);
                 if (n <= kList) {
+                    const int stay = min(k, int(n));
                     settled = done = true;
                     if (rank == 0) {
                         sort_list(sh, int(n));
@@ -877,7 +892,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                         float v[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            e[i] = 2 * tid + i < k ? sh.sorted[2 * tid + i] : 0;
+                            e[i] = 2 * tid + i < stay ? sh.sorted[2 * tid + i] : 0;
                             v[i] = e[i] ? key_value(uint32_t(e[i] >> 32)) : -INFINITY;
                             a[i] = e[i] ? w(v[i]) : 0;
                         }
@@ -909,7 +924,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                             if (a[i] == 0) continue;
                             const u64 col = 0xffffffffu - uint32_t(e[i]);
                             u64 before = 0;
-                            for (int j = 0; j < k; ++j) before += sh.list[j] < col ? sh.sorted[j] : 0;
+                            for (int j = 0; j < stay; ++j) before += sh.list[j] < col ? sh.sorted[j] : 0;
                             if (before <= target && target < before + a[i])
                                 write(int64_t(col), v[i], total);
                         }
@@ -923,10 +938,11 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                 for (int i = lane; i < S * kWarps; i += 32) {
                     const float part = remote<S>(&sh.near[i % kWarps], i / kWarps);
                     const float t = key_value(remote<S>(&sh.top[i % kWarps], i / kWarps));
-                    near += part > 0.f ? part * ex2_sfu((t - w.m) * c_near) : 0.f;
+                    near += part == 0.f ? 0.f : part * ex2_sfu((t - w.m) * c_near);
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) near += __shfl_xor_sync(kFullMask, near, o);
+                // (infinite logits or temperatures make it NaN: the general cut)
                 const float pc = fmaxf(tp, 0.f);
                 const float log_small = 0.6931472f * __log2f((1.f - pc) * near * 0.999f / float(cols));
                 const float low = w.m + t_row * log_small;

@@ -162,6 +162,34 @@ def test_peaked_logits(st):
         check(st, x, u, **kw)
 
 
+@pytest.mark.parametrize("rows", [3, 40, 150])
+@pytest.mark.parametrize("left", [1, 7, 100, 1500, 2500, 9000])
+def test_masks_that_leave_few_columns(st, left, rows):
+    """Fewer columns than top-k keeps, or too few in some part of the row, in rows that one to
+    eight CTAs share; scattered, and all at the row's end."""
+    x, u = logits(rows, 50257, "f32", seed=left, holes=0)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(left + 1)
+    order = torch.rand(x.shape, generator=g, device="cuda")
+    order[::2] += torch.arange(50257, device="cuda") * 1e-5
+    kept = torch.zeros_like(x, dtype=torch.bool).scatter_(1, order.topk(left, 1)[1], True)
+    x.masked_fill_(~kept, -INF)
+    for kw in ({"top_k": 50}, {"top_k": 1000, "top_p": 0.9}, {"top_k": 3, "min_p": 0.2},
+               {"top_p": 0.8}, {"temperature": 0.5}):
+        check(st, x, u, **kw)
+
+
+def test_ends_of_the_temperature(st):
+    """Infinite, large and tiny temperatures under every filter, with masked columns; those below
+    5e-29 act as that, which between logits of this size leaves the largest alone."""
+    x, u = logits(6, 9001, "f32", seed=13, holes=0.3)
+    for value in (INF, 3e38, 1e30, 5e-29, 1e-30, 1e-45):
+        t = torch.full((6,), value, device="cuda")
+        for kw in ({}, {"top_p": 0.5}, {"top_p": 0.999, "min_p": 0.5}, {"top_k": 40},
+                   {"top_k": 2000, "top_p": 0.7}, {"min_p": 0.5}):
+            check(st, x, u, temperature=t, **kw)
+
+
 def test_draws_follow_the_distribution(st):
     """Evenly spaced u: every column comes as often as its probability says, within one draw."""
     x, _ = logits(1, 40, "f32", seed=10)
