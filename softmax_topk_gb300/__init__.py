@@ -533,6 +533,8 @@ def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, prob=
     dev, f32, i32 = x.device, torch.float32, torch.int32
     settings = Sampling()
     _setting(settings, "temperature", temperature, rows, f32, dev)
+    if not isinstance(top_k, torch.Tensor):
+        top_k = min(top_k, 2 ** 31 - 1)  # past the row's length: off
     _setting(settings, "top_k", top_k, rows, i32, dev)
     _setting(settings, "top_p", top_p, rows, f32, dev)
     _setting(settings, "min_p", min_p, rows, f32, dev)

@@ -242,5 +242,6 @@ def test_refusals(st):
         st.sample(x, u, top_k=torch.ones(4, device="cuda"))
     with pytest.raises(TypeError):
         st.sample(x.half(), u)
+    assert torch.equal(st.sample(x, u, top_k=2 ** 32 + 1)[0], st.sample(x, u)[0])  # off, not 1
     out, prob = st.sample(x[:0], u[:0])
     assert out.shape == (0,) and prob.shape == (0,)
