@@ -13,17 +13,6 @@ namespace {
 
 using attn_bwd::Side;
 
-template <int D, bool KV>
-cudaError_t launch_side(const Side& side, const AttentionBwdArgs& a, int nt, int64_t units, int sms,
-                        const KernelCtl& ctl, cudaStream_t stream) {
-    auto k = attn_bwd::attention_bwd_kernel<D, KV>;
-    constexpr int smem = attn_bwd::Layout<D>::kBytes;
-    if (!prepare_kernel(k, 1, smem)) return cudaErrorInvalidConfiguration;
-    return launch_kernel(k, min64(units, sms), attn_bwd::kThreads, 1, smem, stream, side, a.lse,
-                         static_cast<const float*>(a.delta), a.n, nt, static_cast<int>(units),
-                         a.scale, a.causal ? 1 : 0, ctl);
-}
-
 template <int D>
 cudaError_t launch_d(const AttentionBwdArgs& a, const KernelCtl& ctl, cudaStream_t stream) {
     const DeviceInfo* dev = device_info();
@@ -46,17 +35,15 @@ cudaError_t launch_d(const AttentionBwdArgs& a, const KernelCtl& ctl, cudaStream
     if (e != cudaSuccess) return e;
     const int nt = static_cast<int>(ceil_div(a.n, attn_bwd::kRows));
     const int64_t units = a.causal ? a.bh * ((nt + 1) / 2) : a.bh * nt;
-    if (2 * units <= dev->sms) {
-        auto k = attn_bwd::attention_bwd_both_kernel<D>;
-        constexpr int smem = attn_bwd::Layout<D>::kBytes;
-        if (!prepare_kernel(k, 1, smem)) return cudaErrorInvalidConfiguration;
-        return launch_kernel(k, 2 * units, attn_bwd::kThreads, 1, smem, stream, kv, q, a.lse,
-                             static_cast<const float*>(a.delta), a.n, nt, static_cast<int>(units),
-                             a.scale, a.causal ? 1 : 0, ctl);
-    }
-    e = launch_side<D, true>(kv, a, nt, units, dev->sms, ctl, stream);
-    if (e != cudaSuccess) return e;
-    return launch_side<D, false>(q, a, nt, units, dev->sms, ctl, stream);
+    // both sides in one launch, each by as many CTAs as it has units or the GPU
+    // SMs; those of the second side start as the first side's leave
+    const int ctas = static_cast<int>(min64(units, dev->sms));
+    auto k = attn_bwd::attention_bwd_kernel<D>;
+    constexpr int smem = attn_bwd::Layout<D>::kBytes;
+    if (!prepare_kernel(k, 1, smem)) return cudaErrorInvalidConfiguration;
+    return launch_kernel(k, 2 * ctas, attn_bwd::kThreads, 1, smem, stream, kv, q, a.lse,
+                         static_cast<const float*>(a.delta), a.n, nt, static_cast<int>(units),
+                         a.scale, a.causal ? 1 : 0, ctl);
 }
 
 }  // namespace

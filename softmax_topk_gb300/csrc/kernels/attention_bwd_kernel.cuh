@@ -606,29 +606,22 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
     }
 }
 
-// One side per launch.
-template <int D, bool KV>
-__global__ void __launch_bounds__(kThreads, 1)
-attention_bwd_kernel(const __grid_constant__ Side side, const float* __restrict__ lse,
-                     const float* __restrict__ delta, int n, int nt, int units, float scale,
-                     int causal, KernelCtl ctl) {
-    bwd_cta<D, KV>(side.x, side.y, side.u, side.w, lse, delta, side.out1, side.out2, n, nt, units,
-                   scale, causal, ctl, blockIdx.x, gridDim.x);
-}
-
-// Both sides at once, a CTA per unit of each: for sizes at which that many CTAs
-// fit the SMs (2 x 300, d = 64: 28 us a call with two launches after delta's).
+// Both sides in one launch: the first half of the CTAs takes keys, the second
+// queries.  They need nothing of each other, and no more than one CTA fits an SM, so
+// a CTA of the second half starts where one of the first has ended, or at once on
+// an SM that the first half leaves free.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-attention_bwd_both_kernel(const __grid_constant__ Side kv, const __grid_constant__ Side q,
-                          const float* __restrict__ lse, const float* __restrict__ delta, int n,
-                          int nt, int units, float scale, int causal, KernelCtl ctl) {
-    if (int(blockIdx.x) < units)
+attention_bwd_kernel(const __grid_constant__ Side kv, const __grid_constant__ Side q,
+                     const float* __restrict__ lse, const float* __restrict__ delta, int n, int nt,
+                     int units, float scale, int causal, KernelCtl ctl) {
+    const int ctas = gridDim.x / 2, cta = blockIdx.x;
+    if (cta < ctas)
         bwd_cta<D, true>(kv.x, kv.y, kv.u, kv.w, lse, delta, kv.out1, kv.out2, n, nt, units, scale,
-                         causal, ctl, blockIdx.x, units);
+                         causal, ctl, cta, ctas);
     else
         bwd_cta<D, false>(q.x, q.y, q.u, q.w, lse, delta, q.out1, q.out2, n, nt, units, scale,
-                          causal, ctl, blockIdx.x - units, units);
+                          causal, ctl, cta - ctas, ctas);
 }
 
 }  // namespace attn_bwd
