@@ -689,7 +689,7 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
 // Four threads per token.  What crosses lanes in the kernel above (redux, votes,
 // shuffles, four fifths of its instructions) mostly happens in a thread's
 // registers here, 8 tokens to an instruction, at the price of the rows' stay in
-// shared memory and of latency, so it takes large batches only (see route.cu).
+// shared memory and of latency, so it takes large batches only (rule and times: route_dispatch.cuh).
 //
 // A warp copies 8 rows in 16-byte chunks, placed so that the four threads of a
 // row, reading one chunk each of neighbouring places or of different groups,
@@ -752,8 +752,8 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 
 // Sum, maximum, minimum over the four threads of a row.
 __device__ __forceinline__ float row_sum(float v) {
-    v += __shfl_xor_sync(kFullMask, v, 1);
-    return v + __shfl_xor_sync(kFullMask, v, 2);
+    v += __shfl_xor_sync(kFullMask, v, 2);
+    return v + __shfl_xor_sync(kFullMask, v, 1);
 }
 __device__ __forceinline__ float row_max(float v) {
     v = fmaxf(v, __shfl_xor_sync(kFullMask, v, 1));
@@ -1077,7 +1077,7 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
 
         // ---- weights: thread `sub` has the slots sub, sub + 4, ...
         constexpr int Q = P / 4;
-        float z[Q], w[Q], sum = 0.f, top = -INFINITY;
+        float z[Q], w[Q], top = -INFINITY;
         int ez[Q];
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
@@ -1098,9 +1098,17 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
                 if (sh.sigmoid) w[q] = __fdiv_rn(w[q], 1.f + exp1(z[q]));
             }
             if (z[q] == -INFINITY) w[q] = 0.f;
-            sum += w[q];
         }
-        sum = row_sum(sum);
+        // added in the other kernel's order, so that renormalised weights do not
+        // depend on the number of rows
+        float part[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) part[q] = w[q];
+#pragma unroll
+        for (int step = Q / 2; step > 0; step /= 2)
+#pragma unroll
+            for (int q = 0; q < step; ++q) part[q] += part[q + step];
+        const float sum = row_sum(part[0]);
         if (my < here) {
             const int64_t at = (row0 + my) * K;
 #pragma unroll
