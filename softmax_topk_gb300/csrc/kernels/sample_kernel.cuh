@@ -184,6 +184,15 @@ struct Weight {
     // The first way, two values at a time, for x in [clamp, m].  Negated values
     // save the sign changes that the packed forms lack.
     __device__ __forceinline__ void parts2(float2 x, uint32_t (&hi)[2], int (&lo)[2]) const {
+        raw2(x, hi, lo);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            hi[i] -= __float_as_uint(3.f);
+            lo[i] -= __float_as_int(unit);
+        }
+    }
+    // The same with the constants that the parts were added to still in them.
+    __device__ __forceinline__ void raw2(float2 x, uint32_t (&hi)[2], int (&lo)[2]) const {
         const float2 minus = splat2(-1.f), K = splat2(origin);
         const float2 np = mul2(x, splat2(-c_hi));
         const float2 pl = fma2(x, splat2(c_lo), fma2(x, splat2(c_hi), np));
@@ -211,10 +220,10 @@ struct Weight {
         const float2 big = fma2(wh, s, splat2(3.f));
         const float2 rest = fma2(wl, s, fma2(wh, s, fma2(big, minus, splat2(3.f))));
         const float2 end = add2(rest, splat2(unit));
-        hi[0] = __float_as_uint(big.x) - __float_as_uint(3.f);
-        hi[1] = __float_as_uint(big.y) - __float_as_uint(3.f);
-        lo[0] = __float_as_int(end.x) - __float_as_int(unit);
-        lo[1] = __float_as_int(end.y) - __float_as_int(unit);
+        hi[0] = __float_as_uint(big.x);
+        hi[1] = __float_as_uint(big.y);
+        lo[0] = __float_as_int(end.x);
+        lo[1] = __float_as_int(end.y);
     }
     __device__ __forceinline__ void parts(float x, uint32_t& hi, int& lo) const {
         if (plain) {  // the same operations as a pair's, so that sums agree to the bit
@@ -271,14 +280,21 @@ struct Weight {
         uint32_t hi = 0;
         int lo = 0;
         if (plain) {
+            // values that do not count become the clamp, whose parts are 0;
+            // sums of the parts' bits wrap, and the constants come off at once
+            const float least = fmaxf(from, clamp);
+            uint32_t lo_bits = 0;
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
                 uint32_t h[2];
                 int l[2];
-                parts2(make_float2(fmaxf(v[i], clamp), fmaxf(v[i + 1], clamp)), h, l);
-                if (v[i] >= from) hi += h[0], lo += l[0];
-                if (v[i + 1] >= from) hi += h[1], lo += l[1];
+                raw2(make_float2(v[i] >= least ? v[i] : clamp, v[i + 1] >= least ? v[i + 1] : clamp),
+                     h, l);
+                hi += h[0] + h[1];
+                lo_bits += uint32_t(l[0]) + uint32_t(l[1]);
             }
+            hi -= uint32_t(N) * __float_as_uint(3.f);
+            lo = int(lo_bits - uint32_t(N) * __float_as_uint(unit));
         } else {
 #pragma unroll 1
             for (int i = 0; i < N; ++i) {
