@@ -1123,11 +1123,11 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                             }
                         };
                         for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0;
-                        if (tid == 0) {
-                            sh.listed = 0;
-                            sh.fine = kBins;  // none
-                        }
+                        if (tid == 0) sh.fine = kBins;  // none
                         row_sync<S>();
+                        // only now has every thread of the row read the first list's
+                        // length; the barrier before the next columns orders this
+                        if (tid == 0) sh.listed = 0;
                         each_listed([&](float v, int64_t) { atomicAdd(&sh.mass[fine_of(v)], w(v)); });
                         row_sync<S>();
                         if (rank == 0) {

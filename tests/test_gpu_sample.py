@@ -190,6 +190,21 @@ def test_ends_of_the_temperature(st):
             check(st, x, u, temperature=t, **kw)
 
 
+@pytest.mark.parametrize("rows", [1, 30, 100, 400])
+def test_many_columns_at_the_border(st, rows):
+    """Top-p whose border lies among thousands of small weights, which are divided again: rows of
+    one to eight CTAs, many of them."""
+    for cols, spread, p in ((128256, 2.5, 0.999), (50257, 0.3, 0.97), (20011, 0.01, 0.5)):
+        x, u = logits(min(rows, 20), cols, "f32", seed=rows, spread=spread, holes=0)
+        want, want_p = check(st, x, u, top_p=p)
+        x = x.repeat((rows + 19) // 20, 1)[:rows].contiguous()
+        u = u.repeat((rows + 19) // 20)[:rows].contiguous()
+        for _ in range(20):
+            out, prob = st.sample(x, u, top_p=p)
+            at = torch.arange(rows, device="cuda") % 20
+            assert torch.equal(out, want[at]) and torch.equal(prob, want_p[at])
+
+
 def test_draws_follow_the_distribution(st):
     """Evenly spaced u: every column comes as often as its probability says, within one draw."""
     x, _ = logits(1, 40, "f32", seed=10)
