@@ -52,6 +52,7 @@ namespace sample {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kRuns = kMaxCluster * kWarps;  // runs of columns of a row, one per warp
 constexpr int kList = 2048;   // columns that a list holds
 constexpr int kBins = 2048;   // steps of the top-p histogram
 constexpr int kTopK = 1024;   // top-k up to here is settled on a list
@@ -336,11 +337,11 @@ struct alignas(8) Cut {
 
 struct Shared {
     float table[64];
-    // exchanged over the cluster, one value per warp
-    uint32_t top[kWarps], bound[kWarps];
-    float near[kWarps];  // weights of a warp's run, in fp32, to its own maximum
-    u64 sum[kWarps];     // weights of a warp's run outside the list
-    u64 draw[kWarps];    // kept weights of a warp's run (top-p: those above the list)
+    // one value per warp of the row, every CTA's in each of them
+    uint32_t top[kRuns], bound[kRuns];
+    float near[kRuns];  // weights of a warp's run, in fp32, to its own maximum
+    u64 sum[kRuns];     // weights of a warp's run outside the list
+    u64 draw[kRuns];    // kept weights of a warp's run (top-p: those above the list)
     uint32_t slice;      // histogram's weight in this CTA's steps
     uint32_t bin_lo, bin_hi;  // first and last step that may hold the border
     u64 piece[kWarps];  // kept weights of a piece of the border's run
@@ -351,7 +352,7 @@ struct Shared {
     uint32_t fine;      // the border's step when the listed ones are divided again
     u64 fine_above;     // weight above it
     u64 want;           // weight that the border reaches
-    u64 extra[kMaxCluster * kWarps];  // kept weights of a run's listed columns
+    u64 extra[kRuns];   // kept weights of a run's listed columns
     // scratch of one CTA
     u64 warp[kWarps];
     u64 result[2];
@@ -385,6 +386,24 @@ __device__ __forceinline__ V remote(const V* local, int rank) {
         return v;
     }
 }
+// Stores a warp's value in every CTA of the row (lane r in rank r): written
+// before a barrier it is read after it as shared memory of one's own, where each
+// read of another CTA's takes ~700 cycles.
+template <int S, typename V>
+__device__ __forceinline__ void publish(V* local, V v, int lane) {
+    if constexpr (S == 1) {
+        if (lane == 0) *local = v;
+    } else if (lane < S) {
+        const uint32_t a = map_to_rank(local, lane);
+        if constexpr (sizeof(V) == 8) {
+            asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(a), "l"(v) : "memory");
+        } else {
+            uint32_t t;
+            memcpy(&t, &v, 4);
+            asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(a), "r"(t) : "memory");
+        }
+    }
+}
 // Barrier over the CTAs of a row.  Threads of a warp come to it from loops that
 // they left at different times, so the cluster's barrier is the form that
 // counts threads, not the .aligned one, which takes a warp for converged.
@@ -416,6 +435,21 @@ __device__ __forceinline__ void list_push(Shared& sh, float x, uint32_t col) {
     }
 }
 
+// Puts those of a block's columns on it that `which` names: few, so one after
+// the other (code for all of them side by side costs more time to fetch).
+template <int S, int N>
+__device__ __forceinline__ void list_push_all(Shared& sh, const float (&v)[N], uint32_t which,
+                                              uint32_t col) {
+#pragma unroll 1
+    for (; which; which &= which - 1) {
+        const int i = __ffs(which) - 1;
+        float y = v[0];
+#pragma unroll
+        for (int j = 1; j < N; ++j) y = j == i ? v[j] : y;
+        list_push<S>(sh, y, col + i);
+    }
+}
+
 // How many are on it while others are being put there.
 template <int S>
 __device__ __forceinline__ uint32_t listed_now(Shared& sh) {
@@ -432,6 +466,7 @@ __device__ __forceinline__ void sort_list(Shared& sh, int n) {
         if (tid < n) {
             const u64 mine = sh.list[tid];
             int rank = 0;
+#pragma unroll 8
             for (int i = 0; i < n; ++i) rank += sh.list[i] > mine;
             sh.sorted[rank] = mine;  // entries differ: each has a column of its own
         }
@@ -772,6 +807,14 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = S == 1 ? 0 : int(cluster_rank());
     if (tid < 64) sh.table[tid] = kPow2[tid];
+    // the row's other CTAs have to be there before anything is stored in them:
+    // asked for here, waited for after the first pass
+    if constexpr (S > 1) {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    }
+    bool first_row = true;
+    const int own_run = rank * kWarps + warp;  // this warp's run of columns
     for (int64_t row = blockIdx.x / S; row < rows; row += gridDim.x / S) {
         const Blocks<T> blocks(x + row * cols, cols);
         // runs of blocks, in column order: CTA by CTA, warp by warp
@@ -802,7 +845,6 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
             near = near == 0.f ? 0.f : near * ex2_sfu((thread_top - t) * c_near);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) near += __shfl_xor_sync(kFullMask, near, o);
-            if (lane == 0) sh.near[warp] = near;
             for (int i = tid; i < kBins; i += kThreads) sh.steps[i] = 0;
             if (tid < S * kWarps) sh.extra[tid] = 0;
         }
@@ -822,10 +864,16 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                 }
             bound = __shfl_sync(kFullMask, key, j - 1);
         }
-        if (lane == 0) {
-            sh.top[warp] = warp_top;
-            sh.bound[warp] = bound;
+        if constexpr (S > 1) {
+            if (first_row) {
+                __syncwarp();
+                asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+            }
+            first_row = false;
         }
+        publish<S>(&sh.top[own_run], warp_top, lane);
+        if (list_k) publish<S>(&sh.bound[own_run], bound, lane);
+        if (by_p) publish<S>(&sh.near[own_run], near, lane);
         if (tid == 0) {
             sh.listed = 0;
             sh.bin_lo = sh.bin_hi = kBins;  // none
@@ -835,8 +883,8 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
         uint32_t top_key = 0;
         bound = 0xffffffffu;
         for (int i = lane; i < S * kWarps; i += 32) {
-            top_key = max(top_key, remote<S>(&sh.top[i % kWarps], i / kWarps));
-            bound = min(bound, remote<S>(&sh.bound[i % kWarps], i / kWarps));
+            top_key = max(top_key, sh.top[i]);
+            if (list_k) bound = min(bound, sh.bound[i]);
         }
         top_key = __reduce_max_sync(kFullMask, top_key);
         bound = __reduce_min_sync(kFullMask, bound);
@@ -892,9 +940,11 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                     if (all && listed_now<S>(sh) > kList) break;
                     float v[EPV];
                     blocks.load(b, v);
+                    uint32_t for_list = 0;
 #pragma unroll
                     for (int i = 0; i < EPV; ++i)
-                        if (v[i] >= least) list_push<S>(sh, v[i], uint32_t(blocks.col(b) + i));
+                        if (v[i] >= least) for_list |= 1u << i;
+                    list_push_all<S>(sh, v, for_list, uint32_t(blocks.col(b)));
                 }
                 row_sync<S>();
                 const uint32_t n = remote<S>(&sh.listed, 0);
@@ -952,8 +1002,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                 // even together.
                 near = 0.f;
                 for (int i = lane; i < S * kWarps; i += 32) {
-                    const float part = remote<S>(&sh.near[i % kWarps], i / kWarps);
-                    const float t = key_value(remote<S>(&sh.top[i % kWarps], i / kWarps));
+                    const float part = sh.near[i], t = key_value(sh.top[i]);
                     near += part == 0.f ? 0.f : part * ex2_sfu((t - w.m) * c_near);
                 }
 #pragma unroll
@@ -1028,7 +1077,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                     for (int64_t b = settled ? hi : lo + lane; b < hi; b += 32) {
                         float v[EPV];
                         blocks.load(b, v);
-                        uint32_t hi_a = 0, hi_r = 0;
+                        uint32_t hi_a = 0, hi_r = 0, for_list = 0;
                         int lo_a = 0, lo_r = 0;
 #pragma unroll
                         for (int i = 0; i < EPV; i += 2) {
@@ -1040,7 +1089,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                                 const float at = (w.m - v[i + j]) * steps;
                                 if (v[i + j] >= least && at < to_step) {
                                     if (at < from_step) hi_a += h[j], lo_a += l[j];
-                                    else list_push<S>(sh, v[i + j], uint32_t(blocks.col(b) + i + j));
+                                    else for_list |= 1u << (i + j);
                                 } else {
                                     hi_r += h[j], lo_r += l[j];
                                 }
@@ -1048,50 +1097,51 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                         }
                         above += w.sum_of(hi_a, lo_a);
                         rest += w.sum_of(hi_r, lo_r);
+                        list_push_all<S>(sh, v, for_list, uint32_t(blocks.col(b)));
                     }
                     above = warp_sum64(above);
                     rest = warp_sum64(rest);
-                    if (lane == 0) {
-                        sh.draw[warp] = above;
-                        sh.sum[warp] = above + rest;
-                    }
+                    publish<S>(&sh.draw[own_run], above, lane);
+                    publish<S>(&sh.sum[own_run], above + rest, lane);
                     row_sync<S>();
                     const uint32_t n = remote<S>(&sh.listed, 0);
                     if (n > 0 && n <= kList) {
                         if (rank == 0) {
                             u64 total = 0, top_sum = 0;
                             for (int i = lane; i < S * kWarps; i += 32) {
-                                total += remote<S>(&sh.sum[i % kWarps], i / kWarps);
-                                top_sum += remote<S>(&sh.draw[i % kWarps], i / kWarps);
+                                total += sh.sum[i];
+                                top_sum += sh.draw[i];
                             }
                             total = warp_sum64(total);
                             top_sum = warp_sum64(top_sum);
                             sort_list(sh, int(n));
-                            constexpr int P = kList / kThreads;
-                            u64 a[P], mine = 0;
-#pragma unroll
-                            for (int i = 0; i < P; ++i) {
-                                const int at = P * tid + i;
-                                a[i] = at < int(n) ? w(key_value(uint32_t(sh.sorted[at] >> 32))) : 0;
-                                mine += a[i];
+                            // weights beside the sorted entries, in the list's place
+                            u64 mine = 0;
+#pragma unroll 1
+                            for (int at = tid; at < int(n); at += kThreads) {
+                                const u64 a = w(key_value(uint32_t(sh.sorted[at] >> 32)));
+                                sh.list[at] = a;
+                                mine += a;
                             }
-                            const u64 upto = cta_prefix(sh, mine);
-                            if (tid == kThreads - 1) sh.result[0] = upto;
-                            __syncthreads();
-                            const u64 want = share_of(pc, total + sh.result[0]);
-                            u64 run = top_sum + upto - mine;
-#pragma unroll
-                            for (int i = 0; i < P; ++i) {
-                                if (a[i] == 0 && P * tid + i >= int(n)) break;
-                                const u64 e = sh.sorted[P * tid + i];
-                                const uint32_t col = 0xffffffffu - uint32_t(e);
-                                if (run < want) {  // stays
+                            const u64 want = share_of(pc, total + cta_sum(sh, mine));
+                            u64 run_sum = top_sum;  // before this chunk of entries
+#pragma unroll 1
+                            for (int base = 0; base < int(n); base += kThreads) {
+                                const int at = base + tid;
+                                const u64 a = at < int(n) ? sh.list[at] : 0;
+                                const u64 upto = run_sum + cta_prefix(sh, a);
+                                if (at < int(n) && upto - a < want) {  // stays
+                                    const u64 e = sh.sorted[at];
+                                    const uint32_t col = 0xffffffffu - uint32_t(e);
                                     const uint32_t block = (col + uint32_t(blocks.head)) / EPV;
-                                    atomicAdd(&sh.extra[block / uint32_t(per_warp)], a[i]);
-                                    if (want <= run + a[i] && top_sum < want)
+                                    atomicAdd(&sh.extra[block / uint32_t(per_warp)], a);
+                                    if (want <= upto && top_sum < want)
                                         sh.cut = {key_value(uint32_t(e >> 32)), int(col)};
                                 }
-                                run += a[i];
+                                __syncthreads();
+                                if (tid == kThreads - 1) sh.result[0] = upto;
+                                __syncthreads();
+                                run_sum = sh.result[0];
                             }
                         }
                         row_sync<S>();
@@ -1133,8 +1183,8 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                         if (rank == 0) {
                             u64 total = 0, top_sum = 0;
                             for (int i = lane; i < S * kWarps; i += 32) {
-                                total += remote<S>(&sh.sum[i % kWarps], i / kWarps);
-                                top_sum += remote<S>(&sh.draw[i % kWarps], i / kWarps);
+                                total += sh.sum[i];
+                                top_sum += sh.draw[i];
                             }
                             total = warp_sum64(total);
                             top_sum = warp_sum64(top_sum);
@@ -1220,7 +1270,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
 #pragma unroll 2
                 for (int64_t b = lo + lane; b < hi; b += 32) mine += kept.block(b);
                 mine = warp_sum64(mine);
-                if (lane == 0) sh.draw[warp] = mine;
+                publish<S>(&sh.draw[own_run], mine, lane);
                 row_sync<S>();
             }
             // the run that holds the border: before <= target < before + its sum
@@ -1229,7 +1279,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int g = R * lane + i;
-                part[i] = g < S * kWarps ? remote<S>(&sh.draw[g % kWarps], g / kWarps) : 0;
+                part[i] = g < S * kWarps ? sh.draw[g] : 0;
                 if (have_runs && g < S * kWarps) part[i] += remote<S>(&sh.extra[g], 0);
                 own += part[i];
             }
@@ -1247,36 +1297,86 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
             run_id = __shfl_sync(kFullMask, run_id, src);
             before = __shfl_sync(kFullMask, before, src);
             if (run_id / kWarps == rank) {
-                // its columns again, a piece per warp
-                const int64_t from = run_id * per_warp;
-                const int64_t to = min(blocks.count, from + per_warp);
-                const int64_t per_piece = (per_warp / 32 + kWarps - 1) / kWarps * 32;
-                const int64_t plo = min(to, from + warp * per_piece), phi = min(to, plo + per_piece);
-                u64 piece = 0;
-                for (int64_t b = plo + lane; b < phi; b += 32) piece += kept.block(b);
-                piece = warp_sum64(piece);
-                if (lane == 0) sh.piece[warp] = piece;
-                __syncthreads();
-                for (int i = 0; i < warp; ++i) before += sh.piece[i];
-                if (before <= target && target < before + piece) {
-                    for (int64_t b0 = plo; b0 < phi; b0 += 32) {
-                        const u64 a = b0 + lane < phi ? kept.block(b0 + lane) : 0;
-                        const u64 end = before + warp_prefix64(a, lane);
-                        const uint32_t hit = __ballot_sync(kFullMask, end > target);
-                        if (hit) {
-                            // the block that holds the border: a lane per column
-                            const int at = __ffs(hit) - 1;
-                            const u64 start = __shfl_sync(kFullMask, end - a, at);
-                            const int64_t c = blocks.col(b0 + at) + lane;
-                            const bool in = lane < EPV && c >= 0 && c < cols;
-                            const float v = in ? widen(x[row * cols + c]) : -INFINITY;
-                            const u64 a_c = in ? kept.column(v, c) : 0;
-                            const u64 upto_c = start + warp_prefix64(a_c, lane);
-                            uint32_t found = __ballot_sync(kFullMask, a_c > 0 && upto_c > target);
-                            if (lane == __ffs(found) - 1) write(c, v, total);
-                            break;
+                // its columns again
+                if constexpr (S > 1) {
+                    // few rows: a piece per warp, then that piece's, until a warp can
+                    // walk the rest, column by column, the same few instructions
+                    // throughout (their fetch is what a row of its own waits for:
+                    // 1 x 128256, top-p, 44 us with the blocks' code below, 38 so)
+                    int64_t from = max(int64_t(0), blocks.col(run_id * per_warp));
+                    int64_t to = min(int64_t(cols), blocks.col((run_id + 1) * per_warp));
+                    for (;;) {
+                        const int64_t per = (to - from + kThreads - 1) / kThreads * 32;
+                        const int64_t end = min(to, from + (warp + 1) * per);
+                        u64 mine = 0;
+                        for (int64_t c = from + warp * per + lane; c < end; c += 128) {
+                            float v[4];  // four loads at a time
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                v[j] = c + 32 * j < end ? widen(x[row * cols + c + 32 * j]) : -INFINITY;
+#pragma unroll 1
+                            for (int j = 0; j < 4; ++j) {
+                                mine += kept.column(v[0], c + 32 * j);
+                                v[0] = v[1], v[1] = v[2], v[2] = v[3];
+                            }
                         }
-                        before = __shfl_sync(kFullMask, end, 31);
+                        mine = warp_sum64(mine);
+                        __syncthreads();  // the last round's have been read
+                        if (lane == 0) sh.piece[warp] = mine;
+                        __syncthreads();
+                        int p = 0;  // the last one takes what is left
+                        for (; p < kWarps - 1 && before + sh.piece[p] <= target; ++p) before += sh.piece[p];
+                        from += p * per;
+                        to = min(to, from + per);
+                        if (per <= 128) break;
+                    }
+                    if (warp == 0) {
+                        for (int64_t c0 = from; c0 < to; c0 += 32) {
+                            const int64_t c = c0 + lane;
+                            const float v = c < to ? widen(x[row * cols + c]) : -INFINITY;
+                            const u64 a = kept.column(v, c);
+                            const u64 upto = before + warp_prefix64(a, lane);
+                            const uint32_t found = __ballot_sync(kFullMask, a > 0 && upto > target);
+                            if (found) {
+                                if (lane == __ffs(found) - 1) write(c, v, total);
+                                break;
+                            }
+                            before = __shfl_sync(kFullMask, upto, 31);
+                        }
+                    }
+                } else {
+                    // many rows: a piece per warp, block by block (256 x 128256, one
+                    // temperature: 91 us, column by column 97)
+                    const int64_t from = run_id * per_warp;
+                    const int64_t to = min(blocks.count, from + per_warp);
+                    const int64_t per_piece = (per_warp / 32 + kWarps - 1) / kWarps * 32;
+                    const int64_t plo = min(to, from + warp * per_piece), phi = min(to, plo + per_piece);
+                    u64 piece = 0;
+                    for (int64_t b = plo + lane; b < phi; b += 32) piece += kept.block(b);
+                    piece = warp_sum64(piece);
+                    if (lane == 0) sh.piece[warp] = piece;
+                    __syncthreads();
+                    for (int i = 0; i < warp; ++i) before += sh.piece[i];
+                    if (before <= target && target < before + piece) {
+                        for (int64_t b0 = plo; b0 < phi; b0 += 32) {
+                            const u64 a = b0 + lane < phi ? kept.block(b0 + lane) : 0;
+                            const u64 end = before + warp_prefix64(a, lane);
+                            const uint32_t hit = __ballot_sync(kFullMask, end > target);
+                            if (hit) {
+                                // the block that holds the border: a lane per column
+                                const int at = __ffs(hit) - 1;
+                                const u64 start = __shfl_sync(kFullMask, end - a, at);
+                                const int64_t c = blocks.col(b0 + at) + lane;
+                                const bool in = lane < EPV && c >= 0 && c < cols;
+                                const float v = in ? widen(x[row * cols + c]) : -INFINITY;
+                                const u64 a_c = in ? kept.column(v, c) : 0;
+                                const u64 upto_c = start + warp_prefix64(a_c, lane);
+                                uint32_t found = __ballot_sync(kFullMask, a_c > 0 && upto_c > target);
+                                if (lane == __ffs(found) - 1) write(c, v, total);
+                                break;
+                            }
+                            before = __shfl_sync(kFullMask, end, 31);
+                        }
                     }
                 }
             }
