@@ -342,7 +342,7 @@ struct Shared {
     float near[kRuns];  // weights of a warp's run, in fp32, to its own maximum
     u64 sum[kRuns];     // weights of a warp's run outside the list
     u64 draw[kRuns];    // kept weights of a warp's run (top-p: those above the list)
-    uint32_t slice;      // histogram's weight in this CTA's steps
+    uint32_t slice[kMaxCluster];  // histogram's weight in each CTA's steps
     uint32_t bin_lo, bin_hi;  // first and last step that may hold the border
     u64 piece[kWarps];  // kept weights of a piece of the border's run
     float floor_p;
@@ -386,17 +386,20 @@ __device__ __forceinline__ V remote(const V* local, int rank) {
         return v;
     }
 }
-// Stores a warp's value in every CTA of the row (lane r in rank r): written
-// before a barrier it is read after it as shared memory of one's own, where each
-// read of another CTA's takes ~700 cycles.
+// Stores a value in the row's CTA `to` (nowhere where there is none); called by a
+// warp's lanes with their own numbers it stores in every CTA.  Written before a
+// barrier, the value is read after it as shared memory of one's own: reads of
+// other CTAs' by all their warps queue up for thousands of cycles.
 template <int S, typename V>
-__device__ __forceinline__ void publish(V* local, V v, int lane) {
+__device__ __forceinline__ void publish(V* local, V v, int to) {
     if constexpr (S == 1) {
-        if (lane == 0) *local = v;
-    } else if (lane < S) {
-        const uint32_t a = map_to_rank(local, lane);
+        if (to == 0) *local = v;
+    } else if (to < S) {
+        const uint32_t a = map_to_rank(local, to);
         if constexpr (sizeof(V) == 8) {
-            asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(a), "l"(v) : "memory");
+            u64 t;
+            memcpy(&t, &v, 8);
+            asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(a), "l"(t) : "memory");
         } else {
             uint32_t t;
             memcpy(&t, &v, 4);
@@ -1045,10 +1048,11 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                         own += part[i];
                     }
                     const u64 upto = cta_prefix(sh, own);
-                    if (tid == kThreads - 1) sh.slice = uint32_t(upto);
+                    if (warp == kWarps - 1)
+                        publish<S>(&sh.slice[rank], uint32_t(__shfl_sync(kFullMask, upto, 31)), lane);
                     row_sync<S>();
                     u64 run = upto - own;
-                    for (int r = 0; r < rank; ++r) run += remote<S>(&sh.slice, r);
+                    for (int r = 0; r < rank; ++r) run += sh.slice[r];
                     const float slack = 3e-5f + float(cols) * 0x1p-31f;
                     const float from = (pc - slack) * 0x1p31f, to = (pc + slack) * 0x1p31f;
 #pragma unroll
@@ -1057,17 +1061,15 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                         // steps whose end reaches `from`, and the first that reaches `to`
                         if (B * tid + i < kShare) {
                             const uint32_t step = kShare * rank + B * tid + i;
-                            if (after >= from && (before < from || step == 0)) sh.bin_lo = step;
-                            if (after >= to && before < to) sh.bin_hi = step;
+                            if (after >= from && (before < from || step == 0))
+                                for (int r = 0; r < S; ++r) publish<S>(&sh.bin_lo, step, r);
+                            if (after >= to && before < to)
+                                for (int r = 0; r < S; ++r) publish<S>(&sh.bin_hi, step, r);
                         }
                         run += part[i];
                     }
                     row_sync<S>();
-                    int bin_lo = kBins, bin_hi = kBins;
-                    for (int r = 0; r < S; ++r) {
-                        bin_lo = min(bin_lo, int(remote<S>(&sh.bin_lo, r)));
-                        bin_hi = min(bin_hi, int(remote<S>(&sh.bin_hi, r)));
-                    }
+                    const int bin_lo = int(sh.bin_lo), bin_hi = int(sh.bin_hi);
                     // weights above those steps, below them, and the columns in
                     // them; not needed where min-p cuts above them
                     const float from_step = float(bin_lo);
@@ -1143,9 +1145,14 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                                 __syncthreads();
                                 run_sum = sh.result[0];
                             }
+                            if (S > 1 && warp < S) {  // for the others' copies
+                                for (int i = lane; i < S * kWarps; i += 32)
+                                    publish<S>(&sh.extra[i], sh.extra[i], warp);
+                                if (lane == 0) publish<S>(&sh.cut, sh.cut, warp);
+                            }
                         }
                         row_sync<S>();
-                        cut = remote<S>(&sh.cut, 0);
+                        cut = sh.cut;
                         settled = cut.value == cut.value;  // found
                         have_runs = settled && uu != 0.f;
                     } else if (n > kList) {
@@ -1280,7 +1287,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
             for (int i = 0; i < R; ++i) {
                 const int g = R * lane + i;
                 part[i] = g < S * kWarps ? sh.draw[g] : 0;
-                if (have_runs && g < S * kWarps) part[i] += remote<S>(&sh.extra[g], 0);
+                if (have_runs && g < S * kWarps) part[i] += sh.extra[g];
                 own += part[i];
             }
             const u64 upto = warp_prefix64(own, lane);
