@@ -50,7 +50,9 @@ inline int64_t grid_for(int64_t rows, int tokens) {
 }
 
 // Rows per warp: one while the GPU has warps to spare (the latency of one
-// row), else several, which share the work after the choice.
+// row), else several, which share the work after the choice (65536 rows, us with
+// one / by this rule: 64 experts 43 / 23, 128 experts 47 / 29, their gradients
+// 25 / 9 and 24 / 11).
 inline bool share_rows(const RouteArgs& a, Shape& s) {
     const DeviceInfo* dev = device_info();
     if (!dev) return false;

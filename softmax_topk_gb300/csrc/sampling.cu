@@ -24,12 +24,21 @@ cudaError_t launch_t(const void* x, const float* u, int32_t* out, float* prob, i
     int log2_cols = 0;
     while ((int64_t(1) << log2_cols) < cols) ++log2_cols;
     const int bits = 62 - log2_cols < 44 ? 62 - log2_cols : 44;
-    // CTAs per row: as many as fit beside each other (two per SM), while each
-    // keeps 32 blocks of 16 bytes per warp or more
-    const int64_t slots = 2 * int64_t(dev->sms);
+    // CTAs per row: as many as the SMs take, while each keeps 32 blocks of 16
+    // bytes per warp or more: 8 up to one per SM, 4 up to one and a half, 2 up to
+    // two (more of the larger clusters do not all find their place at once).
+    // 128256 bf16 columns, us with no filter / top-p 0.9 / top-k 50:
+    //   12 rows:  8 13.7/27/21   4 19.1/37/21   2 29.8/58/23   1 46/92/26
+    //   38 rows:  8 28.4/57/40   4 27.9/50/23   2 30.1/61/23   1 47/94/27
+    //   60 rows:                 4 28.5/52/26   2 30.2/60/24   1 47/93/27
+    //   76 rows:                 4 39.6/78/37   2 30.7/60/24   1 47/93/27
+    //   152 rows:                               2 53.6/91/34   1 57/106/38
     const int64_t useful = ceil_div(int64_t(cols) * int64_t(sizeof(T)), 16 * sample::kThreads);
+    const int64_t half_sms = dev->sms / 2;
     int S = 1;
-    while (S < sample::kMaxCluster && 2 * S * rows <= slots && 2 * S <= useful) S *= 2;
+    if (rows <= 2 * half_sms && useful >= 2) S = 2;
+    if (4 * rows <= 3 * half_sms && useful >= 4) S = 4;
+    if (8 * rows <= 2 * half_sms && useful >= 8) S = sample::kMaxCluster;
     if (S == 8) return launch_s<T, 8>(x, u, out, prob, rows, cols, s, bits, stream);
     if (S == 4) return launch_s<T, 4>(x, u, out, prob, rows, cols, s, bits, stream);
     if (S == 2) return launch_s<T, 2>(x, u, out, prob, rows, cols, s, bits, stream);
