@@ -39,8 +39,8 @@
 //
 // What bounds it: 256 rows of 128256 bf16 columns with one temperature take 91 us
 // (0.75 TB/s of the one read; 10 us at the rate of memory) and are bound by
-// instructions, 43 per column, half of them packed pairs on the FMA pipe; top-p
-// 0.9 150 us, a histogram more.  256 x 50257 fp32: 45 us, top-p 78, top-k 50 29.
+// instructions, 43 per column, 16 of them packed pairs that take the FMA pipe two
+// cycles; top-p 0.9 150 us, a histogram more.  256 x 50257 fp32: 45 us, top-p 78, top-k 50 29.
 // One row: 13 us, top-p 26, the latency of its steps over eight CTAs.
 #pragma once
 
@@ -431,13 +431,20 @@ __device__ __forceinline__ void row_sync() {
 template <int S>
 __device__ __forceinline__ void list_push(Shared& sh, float x, uint32_t col) {
     const u64 e = (u64(order_key(x)) << 32) | (0xffffffffu - col);
+    // the lanes that are here together take their places with one addition
+    const uint32_t here = __activemask();
+    const int lane = threadIdx.x & 31, leader = __ffs(here) - 1;
+    const uint32_t mine = __popc(here & ((1u << lane) - 1)), all = __popc(here);
+    uint32_t at = 0;
     if constexpr (S == 1) {
-        const uint32_t at = atomicAdd(&sh.listed, 1u);
+        if (lane == leader) at = atomicAdd(&sh.listed, all);
+        at = __shfl_sync(here, at, leader) + mine;
         if (at < kList) sh.list[at] = e;
     } else {
-        uint32_t at;
-        asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;"
-                     : "=r"(at) : "r"(map_to_rank(&sh.listed, 0)) : "memory");
+        if (lane == leader)
+            asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
+                         : "=r"(at) : "r"(map_to_rank(&sh.listed, 0)), "r"(all) : "memory");
+        at = __shfl_sync(here, at, leader) + mine;
         if (at < kList)
             asm volatile("st.shared::cluster.u64 [%0], %1;"
                          :: "r"(map_to_rank(&sh.list[at], 0)), "l"(e) : "memory");
@@ -500,6 +507,16 @@ __device__ __forceinline__ void sort_list(Shared& sh, int n) {
     __syncthreads();
 }
 
+// Adds to a 64-bit sum in shared memory by 32-bit additions, the carry handed on
+// by whoever caused it (with 64-bit atomics, which try again whenever another
+// thread was there first, 256 x 50257 with top-k 1025 takes 820 us, so 134).
+__device__ __forceinline__ void add64(u64* sum, u64 v) {
+    uint32_t* const word = reinterpret_cast<uint32_t*>(sum);
+    const uint32_t lo = uint32_t(v), old = atomicAdd(word, lo);
+    const uint32_t hi = uint32_t(v >> 32) + (old + lo < old);
+    if (hi) atomicAdd(word + 1, hi);
+}
+
 // Inclusive prefix sum of one value per thread over the CTA.
 __device__ __forceinline__ u64 cta_prefix(Shared& sh, u64 v) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -551,7 +568,7 @@ __device__ uint32_t select_key(Shared& sh, u64 want, Each each, Amount amount, u
         each([&](uint32_t key, uint32_t times) {
             if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) {
                 const int b = (key >> shift) & 255;
-                atomicAdd(&sh.mass[b], amount(key) * times);
+                add64(&sh.mass[b], amount(key) * times);
                 atomicAdd(&sh.count[b], times);
             }
         });
@@ -940,7 +957,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
             if (list_k) {
                 // ---- top-k on a list.  Where a mask leaves a warp too few
                 // columns for a bound, all that are there, while they fit
-                // (256 x 50257 with 100 columns left, top-k 50: 2105 us by the
+                // (256 x 50257 with 100 columns left, top-k 50: 157 us by the
                 // general cut, 29 so)
                 const bool all = bound <= kKeyNegInf;
                 const float least = all ? -FLT_MAX : key_value(bound);
@@ -1142,7 +1159,7 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                                     const u64 e = sh.sorted[at];
                                     const uint32_t col = 0xffffffffu - uint32_t(e);
                                     const uint32_t block = (col + uint32_t(blocks.head)) / EPV;
-                                    atomicAdd(&sh.extra[block / uint32_t(per_warp)], a);
+                                    add64(&sh.extra[block / uint32_t(per_warp)], a);
                                     if (want <= upto && top_sum < want)
                                         sh.cut = {key_value(uint32_t(e >> 32)), int(col)};
                                 }
@@ -1170,20 +1187,9 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                         auto fine_of = [&](float v) {
                             return min(kBins - 1, int(((w.m - v) * steps - first) * fine));
                         };
-                        auto each_listed = [&](auto f) {
-                            for (int64_t b = lo + lane; b < hi; b += 32) {
-                                float v[EPV];
-                                blocks.load(b, v);
-#pragma unroll 1
-                                for (int i = 0; i < EPV; ++i) {
-                                    float y = v[0];
-#pragma unroll
-                                    for (int j = 1; j < EPV; ++j) y = j == i ? v[j] : y;
-                                    const float at = (w.m - y) * steps;
-                                    if (y >= least && at < to_step && at >= from_step)
-                                        f(y, blocks.col(b) + i);
-                                }
-                            }
+                        auto in_border = [&](float v) {
+                            const float at = (w.m - v) * steps;
+                            return v >= least && at < to_step && at >= from_step;
                         };
                         for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0;
                         if (tid == 0) sh.fine = kBins;  // none
@@ -1191,7 +1197,20 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                         // only now has every thread of the row read the first list's
                         // length; the barrier before the next columns orders this
                         if (tid == 0) sh.listed = 0;
-                        each_listed([&](float v, int64_t) { atomicAdd(&sh.mass[fine_of(v)], w(v)); });
+                        for (int64_t b = lo + lane; b < hi; b += 32) {
+                            float v[EPV];
+                            blocks.load(b, v);
+#pragma unroll
+                            for (int i = 0; i < EPV; i += 2) {
+                                uint32_t h[2];
+                                int l[2];
+                                w.pair(v[i], v[i + 1], h, l);
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    if (in_border(v[i + j]))
+                                        add64(&sh.mass[fine_of(v[i + j])], w.join(h[j], l[j]));
+                            }
+                        }
                         row_sync<S>();
                         if (rank == 0) {
                             u64 total = 0, top_sum = 0;
@@ -1226,9 +1245,15 @@ sample_kernel(const T* __restrict__ x, const float* __restrict__ u, int* __restr
                         row_sync<S>();
                         const int step = int(remote<S>(&sh.fine, 0));
                         if (step < kBins)
-                            each_listed([&](float v, int64_t c) {
-                                if (fine_of(v) == step) list_push<S>(sh, v, uint32_t(c));
-                            });
+                            for (int64_t b = lo + lane; b < hi; b += 32) {
+                                float v[EPV];
+                                blocks.load(b, v);
+                                uint32_t for_list = 0;
+#pragma unroll
+                                for (int i = 0; i < EPV; ++i)
+                                    if (in_border(v[i]) && fine_of(v[i]) == step) for_list |= 1u << i;
+                                list_push_all<S>(sh, v, for_list, uint32_t(blocks.col(b)));
+                            }
                         row_sync<S>();
                         const uint32_t n_fine = remote<S>(&sh.listed, 0);
                         if (n_fine > 0 && n_fine <= kList) {
