@@ -6,7 +6,7 @@
 // delta_i = dO_i . O_i - dL_i:
 //   dV = P^T dO,   dP = dO V^T,   dS = P o (dP - delta),
 //   dQ = scale dS K,   dK = scale dS^T Q.
-// Two kernels, one per side that a sum runs over, so that every output row is
+// Two walks, one per side that a sum runs over, so that every output row is
 // summed by one CTA in a fixed order (no atomics, results do not depend on
 // scheduling):
 //   KV = true:  one item is a tile of 128 keys; it keeps K and V of those rows
@@ -46,6 +46,13 @@
 // the sums run between them: A1(g), dS(g-1) U, A2(g), P(g) W, A1(g+1), ...
 // Otherwise A1 and A2 have buffers of their own (d = 64, 16 x 16384 causal: 1851
 // us with a shared one), and without KV dS has two.
+//
+// What bounds it (64 x 4096, 1.37 TFLOP of the five products): d = 128 1177 us,
+// 1168 TFLOP/s, or 1632 with the two products that are formed twice, 0.84 of the
+// measured bf16 rate: the tensor pipe, which is busy 2048 of ~2700 cycles of a key
+// tile and 1536 of ~1740 of a query tile.  d = 64 (0.69 TFLOP) 899 us: the compute
+// warps' chain per tile, for a product takes half as long for as many scores.
+// Under the mask 690 us at d = 128, and 16 x 16384 at d = 64 1768 us.
 #pragma once
 
 #include <cuda.h>
@@ -609,7 +616,8 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
 // Both sides in one launch: the first half of the CTAs takes keys, the second
 // queries.  They need nothing of each other, and no more than one CTA fits an SM, so
 // a CTA of the second half starts where one of the first has ended, or at once on
-// an SM that the first half leaves free.
+// an SM that the first half leaves free (64 x 4096, d = 128: 1196 us with a launch
+// per side, d = 64 938; one launch less counts at 2 x 300 too, 28 -> 24 us a call).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_bwd_kernel(const __grid_constant__ Side kv, const __grid_constant__ Side q,
