@@ -147,29 +147,44 @@ __device__ __forceinline__ void group_top2(const Shape& sh, float& a, float& b) 
     }
 }
 
-// Whether this lane's group, of the given value, takes part; `near` is set when
-// values at the border are closer than `slack` + |value| 2^-21.
-__device__ __forceinline__ bool group_keep(const Shape& sh, int group, float value, float slack,
-                                           bool exact, bool& near) {
+// What a group's value may be off by, the sum a + b of two choice values (or a
+// alone, b = 0): their scores' bounds, `err` for two, and the roundings of a, b
+// and the sum, each |a| + |b| of 2^-24 however small the sum is (biases of
+// opposite sign), and as much again for taking this bound off.
+__device__ __forceinline__ float value_bound(float err, float a, float b) {
+    return err + (fabsf(a) + fabsf(b)) * 0x1p-22f;
+}
+
+// The border between the groups that take part and the others: the least that
+// one of the former can be worth and the most that one of the latter can.
+struct Border {
+    float low, high;
+    bool near;  // they overlap
+};
+
+// Whether this lane's group takes part, of the given value, which is off by less
+// than `bound` (`exact`: not at all).
+__device__ __forceinline__ bool group_keep(const Shape& sh, int group, float value, float bound,
+                                           bool exact, Border& border) {
     // round by round the best group that is left, ties to the lowest lane
     uint32_t left = group < sh.groups ? order_key(value + 0.f) : 0u;
-    uint32_t low = 0;
     bool keep = false;
     for (int r = 0; r < sh.topk_groups; ++r) {
-        low = warp_max(left);
-        const int first = __ffs(__ballot_sync(kFullMask, left == low)) - 1;
+        const uint32_t top = warp_max(left);
+        const int first = __ffs(__ballot_sync(kFullMask, left == top)) - 1;
         if (group == first >> sh.lanes_log2) {
             keep = true;
             left = 0u;
         }
     }
+    border.near = false;
     if (!exact) {
-        const uint32_t out = warp_max(left);
-        if (out != 0u) {
-            const float worst = key_value(low), best_out = key_value(out);
-            if (best_out != -INFINITY && !(worst - best_out > slack + fabsf(worst) * 0x1p-21f))
-                near = true;
-        }
+        const bool out = left != 0u && value != -INFINITY;  // a group of nothing is last for certain
+        const uint32_t low = warp_min(keep ? order_key(value - bound + 0.f) : 0xffffffffu);
+        const uint32_t high = warp_max(out ? order_key(value + bound + 0.f) : 0u);
+        border.low = key_value(low);
+        border.high = key_value(high);
+        border.near = high != 0u && !(border.low > border.high);
     }
     return keep;
 }
@@ -380,20 +395,19 @@ __device__ __noinline__ int choose_exact(const T* xrow, const float* bias, const
             take(ob, obx, obb);
         }
         if (!pair_sum) b = 0.f, bx = 0.f, bb = 0.f;
-        const float value = a + b, slack = 2.f * err;
-        bool border = false;
-        const bool keep = group_keep(sh, at_.group, value, slack, !(by_score || pair_sum), border);
-        if (__any_sync(kFullMask, border)) {
-            // groups within the slack of the last one taken must all be made
-            // of the same logits and biases: then the lower ones are right
-            const uint32_t low = warp_min(keep ? order_key(value + 0.f) : 0xffffffffu);
-            const float edge = key_value(low);
+        const float value = a + b, bound = value_bound(err, a, b);
+        Border border;
+        const bool keep = group_keep(sh, at_.group, value, bound, !(by_score || pair_sum), border);
+        if (border.near) {
+            // groups that may stand on either side of the border must all be
+            // made of the same logits and biases: then the lower ones are right
             const bool in = at_.group < sh.groups &&
-                            fabsf(value - edge) <= 2.f * (slack + fabsf(edge) * 0x1p-21f);
-            const int src = __ffs(__ballot_sync(kFullMask, keep && order_key(value + 0.f) == low)) - 1;
+                            (keep ? !(value - bound > border.high)
+                                  : value != -INFINITY && !(value + bound < border.low));
+            const int src = max(__ffs(__ballot_sync(kFullMask, in)) - 1, 0);
             auto same = [&](float t) { return t == __shfl_sync(kFullMask, t, src); };
             const bool equal = same(a) & same(ax) & same(ab) & same(b) & same(bx) & same(bb);
-            groups_near = __any_sync(kFullMask, in && !equal) || edge != edge;
+            groups_near = __any_sync(kFullMask, in && !equal);
         }
         if (!keep) {
 #pragma unroll
@@ -576,10 +590,12 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
                     }
                 }
                 group_top2(sh, a, b);
-                bool near = false;
-                keep = group_keep(sh, at.group, pair_sum ? a + b : a,
-                                  (sh.sigmoid ? 1.f : inv_d) * 0x1p-18f, !need_scores, near);
-                if (near) unsure |= 1u << t;
+                if (!pair_sum) b = 0.f;
+                Border border;
+                keep = group_keep(sh, at.group, a + b,
+                                  value_bound((sh.sigmoid ? 1.f : inv_d) * 0x1p-19f, a, b),
+                                  !need_scores, border);
+                if (border.near) unsure |= 1u << t;
             }
             int key[N];
 #pragma unroll
@@ -707,6 +723,11 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
 constexpr int kListWarps = 4;
 constexpr int kListRows = 8;       // rows per warp
 constexpr int kListExperts = 1024;
+// Bytes of shared memory before the rows: the bias, with groups their values and
+// bounds too.
+__host__ __device__ constexpr int list_head(int experts, int groups) {
+    return (experts + 4 * groups + (groups > 1 ? 2 * kListWarps * kListRows * groups : 0)) * 4;
+}
 
 // a >= b after it.
 __device__ __forceinline__ void order(int& a, int& b) {
@@ -785,11 +806,12 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
     const bool need_sum = !sh.sigmoid && (need_scores || !sh.renorm);
     const int mask = sh.index_mask;
     // bias, its groups 4 floats apart so that threads in different groups meet
-    // different banks; the groups' values of every row; the warps' tiles
+    // different banks; the groups' values of every row and what they may be off
+    // by; the warps' tiles
     float* const b_sm = reinterpret_cast<float*>(list_smem);
     float* const value = b_sm + E + 4 * G + (warp * kListRows + my) * G;  // where G > 1
-    unsigned char* const tile = list_smem + (E + 4 * G + (G > 1 ? kListWarps * kListRows * G : 0)) * 4 +
-                                warp * kListRows * E * int(sizeof(T));
+    float* const bound = value + kListWarps * kListRows * G;
+    unsigned char* const tile = list_smem + list_head(E, G) + warp * kListRows * E * int(sizeof(T));
     for (int e = threadIdx.x; e < E; e += kListWarps * 32)
         b_sm[e + 4 * (e / gsize)] = by_score ? bias[e] : 0.f;
     __syncthreads();
@@ -892,7 +914,9 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
                         a = fmaxf(a, y);
                     }
                 }
-                value[g] = pair_sum ? a + b : a;
+                if (!pair_sum) b = 0.f;
+                value[g] = a + b;
+                bound[g] = value_bound(err, a, b);
             }
             __syncwarp();
             kept = 0;
@@ -906,9 +930,9 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
                 }
                 if (rank < sh.topk_groups) {
                     kept |= 1u << g;
-                    low = fminf(low, y);
-                } else {
-                    high = fmaxf(high, y);
+                    low = fminf(low, y - bound[g]);
+                } else if (y != -INFINITY) {
+                    high = fmaxf(high, y + bound[g]);
                 }
             }
             kept |= __shfl_xor_sync(kFullMask, kept, 1);
@@ -916,9 +940,7 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
             low = -row_max(-low);
             high = row_max(high);
             // (fewer or more than topk_groups only where values are NaN)
-            if (need_scores && high != -INFINITY &&
-                !(low - high > 2.f * err + fabsf(low) * 0x1p-21f))
-                unsure = true;
+            if (need_scores && high != -INFINITY && !(low > high)) unsure = true;
         }
 
         // ---- the P best of this thread's chunks: every fourth of those that

@@ -102,8 +102,7 @@ cudaError_t launch_list(const RouteArgs& a, const Shape& s, float* w, int32_t* i
                         cudaStream_t stream) {
     auto k = s.per_lane <= 8 ? route::route_list_kernel<T, P, 8> : route::route_list_kernel<T, P, 32>;
     constexpr int kRows = route::kListWarps * route::kListRows;
-    const int smem = (a.experts + 4 * a.groups + (a.groups > 1 ? kRows * a.groups : 0)) * 4 +
-                     kRows * a.experts * int(sizeof(T));
+    const int smem = route::list_head(a.experts, a.groups) + kRows * a.experts * int(sizeof(T));
     const int per_sm = blocks_per_sm(k, route::kListWarps * 32, smem);
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     const int64_t grid = min64(ceil_div(a.rows, kRows), int64_t(sms) * per_sm);
