@@ -85,6 +85,52 @@ __device__ __forceinline__ float sigmoid(float x) {
     return __fdiv_rn(x < 0.f ? e : 1.f, 1.f + e);
 }
 
+// Sum of up to 1024 exponentials in [0, 1], of any order and split: each is a
+// multiple of 2^-21 and a rest, the rest rounded to a multiple of 2^-42, and both
+// are added as integers.  So the softmax's denominator has the same bits whichever
+// kernel formed it (a token's weights do not depend on its batch), and its error
+// is 2^-33 at most before the one rounding to fp32, where fp32 additions one after
+// the other each lose up to 2^-24 of the sum.  The two parts come out of additions
+// whose last bit is the unit wanted, two at a time, and carry the constants added
+// along until the end of a run.
+struct UnitSum {
+    static constexpr float kHi = 4.f, kLo = 0x1.8p-19f;  // last bits 2^-21 and 2^-42
+    uint32_t hi = 0, lo = 0;
+    template <int N>
+    __device__ __forceinline__ void add(const float (&e)[N]) {
+        uint32_t h = 0, l = 0;
+        constexpr int M = (N + 1) & ~1;
+#pragma unroll
+        for (int i = 0; i < M; i += 2) {
+            // (a NaN counts for nothing)
+            const float2 v = make_float2(fmaxf(e[i], 0.f), i + 1 < N ? fmaxf(e[i + 1], 0.f) : 0.f);
+            const float2 t = add2(v, splat2(kHi));
+            const float2 rest = fma2(add2(t, splat2(-kHi)), splat2(-1.f), v);  // exact
+            const float2 r = add2(rest, splat2(kLo));
+            h += __float_as_uint(t.x) + __float_as_uint(t.y);
+            l += __float_as_uint(r.x) + __float_as_uint(r.y);
+        }
+        hi += h - uint32_t(M) * 0x40800000u;  // kHi
+        lo += l - uint32_t(M) * 0x36400000u;  // kLo
+    }
+    // Over the warp's lanes.
+    __device__ __forceinline__ void warp() {
+        hi = __reduce_add_sync(kFullMask, hi);
+        lo = __reduce_add_sync(kFullMask, lo);
+    }
+    // Over the four threads of a row (lanes that differ in their last two bits).
+    __device__ __forceinline__ void four() {
+#pragma unroll
+        for (int o = 1; o <= 2; o *= 2) {
+            hi += __shfl_xor_sync(kFullMask, hi, o);
+            lo += __shfl_xor_sync(kFullMask, lo, o);
+        }
+    }
+    __device__ __forceinline__ float value() const {
+        return __ll2float_rn((static_cast<long long>(hi) << 21) + int(lo)) * 0x1p-42f;
+    }
+};
+
 // This lane's run of a row: N consecutive values from p, `count` of them real
 // (the rest -inf).  VEC: count is N or (a lane without experts) 0, and p
 // aligned to min(16, N * sizeof(T)).
@@ -552,16 +598,17 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
             float s[N];  // scores, where they are compared
             if (need_sum) {
                 const float ref = m == -INFINITY ? 0.f : m;
-                float d = 0.f;
 #pragma unroll
                 for (int i = 0; i < N; i += 2) {
                     const float2 e = exp_pair<false>(
                         make_float2(v[i] - ref, i + 1 < N ? v[i + 1] - ref : -INFINITY));
                     s[i] = e.x;
                     if (i + 1 < N) s[i + 1] = e.y;
-                    d += e.x + e.y;
                 }
-                d = warp_sum(d);
+                UnitSum sum;
+                sum.add(s);
+                sum.warp();
+                const float d = sum.value();
                 inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
 #pragma unroll
                 for (int i = 0; i < N; ++i) s[i] *= inv_d;
@@ -870,19 +917,20 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
             m = row_max(m);
             if (need_sum) {
                 const float ref = m == -INFINITY ? 0.f : m;
-                float d = 0.f;
+                UnitSum sum;
                 for (int c = sub; c < chunks; c += 4) {
                     float v[EPV];
                     load(c, v);
-                    float part = 0.f;
 #pragma unroll
                     for (int i = 0; i < EPV; i += 2) {
                         const float2 e = exp_pair<false>(make_float2(v[i] - ref, v[i + 1] - ref));
-                        part += e.x + e.y;
+                        v[i] = e.x;
+                        v[i + 1] = e.y;
                     }
-                    d += part;
+                    sum.add(v);
                 }
-                d = row_sum(d);
+                sum.four();
+                const float d = sum.value();
                 inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
             }
         }
