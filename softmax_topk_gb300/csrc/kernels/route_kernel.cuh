@@ -22,12 +22,11 @@
 //
 // Exact choices.  Without a bias s rises with x, so logits are compared and
 // the choice is exact.  With a bias (and for sums of two scores) c is computed
-// in fp32 with bounds: s carries at most (|x - m| + 12) 2^-24 relative, which is
-// at most 2^-20 s_max absolute (|z| e^-|z| is small where s is), and the sum one
-// rounding.  Three steps, each for the tokens that the one before could not
-// settle: choices by 32-bit keys, a value with its low bits replaced by its
-// place; by full fp32 values of exact functions (choose_exact); and in 64 bits
-// (choose_wide).  Values of equal logit and bias need no more digits.
+// in fp32 with bounds (score_bounds), and the addition of the bias rounds once.
+// Three steps, each for the tokens that the one before could not settle: choices
+// by 32-bit keys, a value with its low bits replaced by its place; by full fp32
+// values of exact functions (choose_exact); and in 64 bits (choose_wide).  Values
+// of equal logit and bias need no more digits.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -191,6 +190,23 @@ __device__ __forceinline__ void group_top2(const Shape& sh, float& a, float& b) 
         b = fmaxf(fminf(a, oa), fmaxf(b, ob));
         a = fmaxf(a, oa);
     }
+}
+
+// Twice what a score may be off by, so what the difference of two may be: with the
+// SFU's functions, or in choose_exact with exp1 (`fine`).  In units of 2^-24:
+//   softmax: e^z, z = x - m <= 0, is off by 2 |z| + 4 of itself (z rounded, its
+//     product with log2 e rounded, ex2 to 2^-22), fine |z| + 2 (exp1 to one ulp).
+//     The denominator's terms are off by that, weighted by their size: the mean of
+//     |z| under the weights e^z is at most 4.5 (N equal terms beside one of z = 0
+//     have z - 1 = N e^-z where it is largest: 4.45 for N = 1023), so 13, fine 6.5,
+//     and its sum (UnitSum), its reciprocal and the product round once each.
+//     Together e^-|z| (20 + 2 |z|), fine e^-|z| (11.5 + |z|), of s_max = 1 / d:
+//     at most 20 and 11.5 (at z = 0), 21 and 12 are taken.
+//   sigmoid: 1 / (1 + e^-x) is off by s (1 - s) (1.3 |x| + 4) + 3 s < 4, fine < 3
+//     (a quotient exact to its rounding): 16 and 4 are taken.
+__device__ __forceinline__ float score_bounds(const Shape& sh, float inv_d, bool fine) {
+    if (sh.sigmoid) return fine ? 0x1p-21f : 0x1p-19f;
+    return inv_d * (fine ? 0x1.8p-20f : 0x1.5p-19f);
 }
 
 // What a group's value may be off by, the sum a + b of two choice values (or a
@@ -391,20 +407,20 @@ __device__ __noinline__ int choose_exact(const T* xrow, const float* bias, const
         for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
         m = key_value(warp_max(order_key(m + 0.f)));
         const float ref = m == -INFINITY ? 0.f : m;
-        float d = 0.f;
+        float e[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) d += v[i] == -INFINITY ? 0.f : exp1(v[i] - ref);
-        d = warp_sum(d);
+        for (int i = 0; i < N; ++i) e[i] = v[i] == -INFINITY ? 0.f : exp1(v[i] - ref);
+        UnitSum sum;
+        sum.add(e);
+        sum.warp();
+        const float d = sum.value();
         inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
     }
     auto score = [&](float xv) {
         if (xv == -INFINITY) return 0.f;
         return sh.sigmoid ? sigmoid(xv) : exp1(xv - m) * inv_d;
     };
-    // twice the bound of a score: without the SFU's error 2^-21 (2^-22 s_max
-    // for a sigmoid's exponential, sum and quotient; a softmax's rounded
-    // difference makes it as large again)
-    const float err = (sh.sigmoid ? 1.f : inv_d) * (sh.sigmoid ? 0x1p-21f : 0x1p-20f);
+    const float err = score_bounds(sh, inv_d, true);
 
     // the value that is compared, as an order key; 0 = takes no part
     uint32_t key[N];
@@ -640,7 +656,7 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
                 if (!pair_sum) b = 0.f;
                 Border border;
                 keep = group_keep(sh, at.group, a + b,
-                                  value_bound((sh.sigmoid ? 1.f : inv_d) * 0x1p-19f, a, b),
+                                  value_bound(score_bounds(sh, inv_d, false), a, b),
                                   !need_scores, border);
                 if (border.near) unsure |= 1u << t;
             }
@@ -693,7 +709,7 @@ route_kernel(const T* __restrict__ x, const float* __restrict__ bias, float* __r
         int e = real ? min(chosen[lane], E - 1) : 0;
         __syncwarp();
         float xm = real ? widen(xrow[e]) : -INFINITY;
-        const float err = (sh.sigmoid ? 1.f : inv_slot) * 0x1p-19f;  // twice the bound of a score
+        const float err = score_bounds(sh, inv_slot, false);
         if (by_score || sizeof(T) == 4) {
             const int below = __shfl_down_sync(kFullMask, mine, 1);
             if (my_slot != K - 1) after = below;
@@ -934,7 +950,7 @@ route_list_kernel(const T* __restrict__ x, const float* __restrict__ bias,
                 inv_d = d > 0.f ? __frcp_rn(d) : 0.f;
             }
         }
-        const float err = (sh.sigmoid ? 1.f : inv_d) * 0x1p-19f;  // twice the bound of a score
+        const float err = score_bounds(sh, inv_d, false);
         auto score = [&](float v) {  // the SFU's; 0 for -inf
             return sh.sigmoid ? rcp_sfu(1.f + ex2_sfu(-expc::kLog2e * v))
                               : exp_pair<false>(make_float2(v - m, v - m)).x * inv_d;
