@@ -242,7 +242,8 @@ os_status os_attention_fwd(const void *q, const void *k, const void *v, void *o,
  *   q, k, v, o, dout  [bh][n][head_dim] bf16, 16-byte aligned: the forward's
  *              inputs, its output and the gradient that reaches that output.
  *   lse        [bh][n] fp32: the forward's logsumexp L.  A row with L = -inf
- *              has no keys and takes no part.
+ *              has no keys and takes no part, whatever its o and dlse hold
+ *              (its dout is finite, as everywhere).
  *   dlse       [bh][n] fp32: the gradient that reaches L, or NULL (none).
  *   dq, dk, dv [bh][n][head_dim] bf16 outputs, 16-byte aligned.
  *   delta      [bh][n] fp32 workspace, overwritten.

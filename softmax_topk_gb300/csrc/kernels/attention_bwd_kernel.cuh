@@ -410,7 +410,9 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
                             const int q = base + lane + 32 * i;
                             lv[i] = q < n ? -lrow[q] * kLog2e : -INFINITY;
                             dv[i] = q < n ? -drow[q] : 0.f;
-                            if (lv[i] == INFINITY) lv[i] = -INFINITY;
+                            // L = -inf, a row without keys: P is 0, and so is
+                            // delta, which may be NaN or infinite there
+                            if (lv[i] == INFINITY) lv[i] = -INFINITY, dv[i] = 0.f;
                         }
                         // buffer g & 1 was last read for tile g - 2
                         if (g >= 2) wait(&bars.stat_empty[g & 1], ((g - 2) >> 1) & 1);
@@ -444,8 +446,8 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& map_x, const CUtensor
                 float row_l = -INFINITY, row_delta = 0.f;  // negated
                 if (!KV && row < n) {
                     row_l = -lse[int64_t(bh) * n + row] * kLog2e;
-                    if (row_l == INFINITY) row_l = -INFINITY;
                     row_delta = -delta[int64_t(bh) * n + row];
+                    if (row_l == INFINITY) row_l = -INFINITY, row_delta = 0.f;
                 }
                 for (int j = 0; j < count; ++j, ++g) {
                     const int col0 = (first + j) * kRows + 64 * half;
