@@ -166,11 +166,14 @@ struct Weight {
     }
     // e^((x - m) / T) = (wh + wl) 2^n by the second way; n below -60 is -200
     __device__ __forceinline__ void relative(float x, float& wh, float& wl, int& n) const {
-        const float dh = x - m;
-        const float bb = dh - x;
-        const float dl = (x - (dh - bb)) + (-m - bb);  // x - m = dh + dl exactly
-        const float th = __fmul_rn(dh, c_hi);  // its residual is added below
-        const float tl = fmaf(dh, c_hi, -th) + fmaf(dh, c_lo, dl * c_hi);
+        // halves, since x - m may be past the largest number (and still be a small
+        // multiple of the temperature)
+        const float xh = 0.5f * x, mh = 0.5f * m, ch = 2.f * c_hi;
+        const float dh = xh - mh;
+        const float bb = dh - xh;
+        const float dl = (xh - (dh - bb)) + (-mh - bb);  // x / 2 - m / 2 = dh + dl exactly
+        const float th = __fmul_rn(dh, ch);  // its residual is added below
+        const float tl = fmaf(dh, ch, -th) + fmaf(dh, 2.f * c_lo, dl * ch);
         const float uf = th + expc::kRound;
         const float gh = th - (uf - expc::kRound);
         const float g = gh + tl;
