@@ -407,6 +407,12 @@ def _like(name, t, shape, dtype, device):
     return t
 
 
+def _int32(v):
+    """v, or where 32 bits do not hold it -1, which the C functions refuse (ctypes would hand
+    them its low bits)."""
+    return v if -2 ** 31 <= v < 2 ** 31 else -1
+
+
 def _call(device, name, fn, *args):
     """fn(*args, torch's current stream on `device`), with that device current."""
     import torch
@@ -480,8 +486,9 @@ def route(x, K: int, score: str | int = "softmax", bias=None, groups: int = 1,
         _like("idx", idx, shape, torch.int32, dev)
     _call(dev, "os_route_topk", _lib.os_route_topk, x.data_ptr(),
           None if bias is None else bias.data_ptr(), weights.data_ptr(), idx.data_ptr(), rows,
-          experts, K, groups, groups if topk_groups is None else topk_groups, group_top,
-          SCORES[score] if isinstance(score, str) else int(score), int(renorm), scale, code)
+          experts, _int32(K), _int32(groups),
+          _int32(groups if topk_groups is None else topk_groups), _int32(group_top),
+          SCORES[score] if isinstance(score, str) else _int32(int(score)), int(renorm), scale, code)
     return weights, idx
 
 
@@ -504,7 +511,7 @@ def route_backward(x, idx, dweights, score: str | int = "softmax", renorm: bool 
     dx = torch.empty_like(x) if dx is None else _like("dx", dx, x.shape, x.dtype, dev)
     _call(dev, "os_route_bwd", _lib.os_route_bwd, x.data_ptr(), idx.data_ptr(),
           dweights.data_ptr(), dx.data_ptr(), rows, experts, K,
-          SCORES[score] if isinstance(score, str) else int(score), int(renorm), scale, code)
+          SCORES[score] if isinstance(score, str) else _int32(int(score)), int(renorm), scale, code)
     return dx
 
 
@@ -534,7 +541,7 @@ def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, prob=
     settings = Sampling()
     _setting(settings, "temperature", temperature, rows, f32, dev)
     if not isinstance(top_k, torch.Tensor):
-        top_k = min(top_k, 2 ** 31 - 1)  # past the row's length: off
+        top_k = _int32(min(top_k, 2 ** 31 - 1))  # past the row's length: off
     _setting(settings, "top_k", top_k, rows, i32, dev)
     _setting(settings, "top_p", top_p, rows, f32, dev)
     _setting(settings, "min_p", min_p, rows, f32, dev)
