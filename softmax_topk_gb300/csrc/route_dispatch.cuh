@@ -11,8 +11,6 @@ namespace {
 
 using route::Shape;
 
-constexpr int64_t kListRowsPerSm = 16;
-
 // Lanes per group: the largest power of two that still gives every group its
 // own lanes; experts per lane follow.
 inline Shape make_shape(const RouteArgs& a, int groups) {
@@ -50,9 +48,15 @@ inline int64_t grid_for(int64_t rows, int tokens) {
 }
 
 // Rows per warp: one while the GPU has warps to spare (the latency of one
-// row), else several, which share the work after the choice (65536 rows, us with
-// one / by this rule: 64 experts 43 / 23, 128 experts 47 / 29, their gradients
-// 25 / 9 and 24 / 11).
+// row), else several, which share the work after the choice.  fp32, softmax, us
+// with one / by this rule, choice and gradient (inputs past L2 at 65536 rows; at
+// most 4864 rows have one either way):
+//   rows          9728               19456              65536
+//   64, K 6       7.7/6.4  6.0/3.9   14.1/9.2  9.3/4.1  45.6/24.1 27.3/10.0
+//   128, K 8      8.4/7.6  6.5/4.9   14.7/11.7 10.1/7.4 46.6/31.2 27.1/17.5
+//   512, K 16     32.1/29.7 9.4/8.3  59/52.2   15.7/14.2  185/159   48/40
+// (From a quarter as many rows on, 64 experts take 5.3 us instead of 6.4 at 9728
+// rows, and 60 of bf16 7.5 instead of 5.9.)
 inline bool share_rows(const RouteArgs& a, Shape& s) {
     const DeviceInfo* dev = device_info();
     if (!dev) return false;
@@ -84,17 +88,47 @@ cudaError_t launch_bwd(const RouteArgs& a, Shape s, const int32_t* idx,
                          static_cast<T*>(dx), a.rows, s);
 }
 
-// The kernel of four threads per row: rows and groups of whole 16-byte chunks
-// (rows of eight of them, for the copy's placement), lists and choose_exact's
-// runs that fit, enough rows, and enough experts for the lists to pay (65536
-// rows, us, one warp / four threads per row: 64 experts 15.5 / 19.2, 128 with
-// a bias 27 / 29, 256 with a bias and groups 76 / 52, 512 with a bias 160 / 127).
+// Rows per SM from which the kernel of four threads per row is faster than the
+// warps' (INT64_MAX: never).  Sigmoid scores take the most instructions and near
+// ones are settled in the thread, the orders of logits least; a softmax's near
+// scores go to choose_exact, a row of the tile after the other, and rows of 4 KB
+// leave room for one CTA per SM.  Us, one warp / four threads per row, K = 8:
+//   rows                           2432       4864       9728       19456      65536
+//   sigmoid, bias       256 fp32   12.1/13.5  15.9/14.5  22.1/15.6  27.3/22.3  55.7/50.2
+//                       512 fp32   20.3/17.6  27.2/17.8  34.7/21.6  48.2/35.8  115/86
+//                      1024 fp32   41.1/26.0  59.7/29.5  75.7/53.9  105/97     281/257
+//   and 8 groups        256 fp32   13.9/12.8  19.5/16.8  25.3/15.7  33.0/28.2  73.8/68.6
+//   logits (softmax)    256 fp32    4.9/7.7    7.2/7.8   10.6/9.1   15.7/14.3  41.8/41.7
+//                       512 fp32    8.9/10.8  12.0/10.9  19.5/17.3  31.4/31.4  91.8/69.6
+//                       768 bf16   10.8/12.2  17.7/12.4  30.8/17.2  54.3/28.7  169/86
+//                      1024 fp32   14.8/16.5  24.2/21.1  37.2/33.9  62.6/69.7  173/211
+//   softmax, bias       256 fp32    9.0/13.5  12.3/14.6  19.7/22.9  32.0/41.0  62.8/75.1
+//                       512 fp32   15.7/19.2  22.7/26.4  34.2/47.3  44.7/65.8  123/153
+//                       640 fp32   24.4/23.2  35.5/27.9  64.2/59.4  85/87      217/188
+//                       768 bf16   20.3/16.6  35.5/29.8  50.7/41.2  83/73      220/177
+//                      1024 fp32   46.0/44.2  64.2/55.8  86/108     124/161    276/377
+//   sigmoid, bias       128 fp32   10.2/12.5  11.6/12.6  14.0/13.8  17.7/16.6  36.8/37.1
+//                       192 fp32   12.0/12.7  16.5/14.3  20.4/14.8  26.4/19.3  55.2/44.9
+//   logits (softmax)    128 fp32    3.3/6.4    5.3/6.6    7.0/7.1   11.4/9.8   29.4/28.6
+//                       192 fp32    4.9/7.4    7.2/7.5   10.2/8.4   15.9/12.3  43.3/35.8
+// so up to 128 experts the warps' kernel stays.
+inline int64_t list_rows_per_sm(const RouteArgs& a, int row_bytes) {
+    if (a.score == OS_SCORE_SIGMOID && (a.bias || (a.groups > 1 && a.group_top == 2))) return 16;
+    if (row_bytes >= 4096 || (a.bias && a.score == OS_SCORE_SOFTMAX && a.experts <= 512))
+        return INT64_MAX;
+    return 32;
+}
+
+// That kernel fits: rows and groups of whole 16-byte chunks (rows of eight of
+// them, for the copy's placement), lists and choose_exact's runs that fit, and
+// enough rows and experts.
 template <typename T>
 bool list_fits(const RouteArgs& a, const Shape& s, int sms) {
     const int bytes = a.experts * int(sizeof(T));
-    return a.K <= 16 && a.experts >= 256 && a.experts <= route::kListExperts && bytes % 128 == 0 &&
+    return a.K <= 16 && a.experts > 128 && a.experts <= route::kListExperts && bytes % 128 == 0 &&
            a.experts / a.groups * int(sizeof(T)) % 16 == 0 && s.per_lane <= 32 &&
-           reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.rows >= int64_t(sms) * kListRowsPerSm;
+           reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
+           a.rows / sms >= list_rows_per_sm(a, bytes);
 }
 
 template <typename T, int P>

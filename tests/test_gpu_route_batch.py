@@ -13,8 +13,9 @@ def st():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("experts,K,groups", [(64, 4, 1), (256, 8, 1), (256, 8, 8), (320, 6, 5),
-                                              (384, 12, 3), (512, 4, 1), (1024, 16, 1), (1024, 8, 32)])
+@pytest.mark.parametrize("experts,K,groups", [(64, 4, 1), (192, 6, 4), (256, 8, 1), (256, 8, 8),
+                                              (320, 6, 5), (384, 12, 3), (512, 4, 1), (1024, 16, 1),
+                                              (1024, 8, 32)])
 def test_weights_do_not_depend_on_the_batch(st, experts, K, groups, dtype):
     """The same bits for a token alone, among a few and among thousands."""
     g = torch.Generator(device="cuda").manual_seed(experts + K)

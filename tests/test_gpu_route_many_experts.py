@@ -8,7 +8,7 @@ from oracle import operators as ref
 
 pytestmark = pytest.mark.gpu
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
-LARGE = 2500  # rows of a large batch
+LARGE = 5000  # rows of a large batch
 
 
 @pytest.fixture(scope="module")
