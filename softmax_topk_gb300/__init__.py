@@ -16,6 +16,8 @@ are the tensor-level conveniences: they take
 torch CUDA tensors, allocate outputs with torch, pass the current torch
 stream, and call the same C entry points.  PyTorch only provides memory and
 streams; every step of the computation runs in the library's CUDA kernels.
+Autograd records nothing of these calls: gradients come from ``attention_backward``
+and ``route_backward``, called by the training step itself.
 There is no fallback: if the library is not built, importing this package
 raises.
 """
@@ -378,7 +380,8 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, out=Non
     """Attention forward on the tensor cores: (O, L) for bf16 CUDA tensors q, k, v
     of one shape [..., n, head_dim] (leading dims are the batch x head slices),
     head_dim 64 or 128.  O has q's shape (bf16); L is fp32 [..., n], or None
-    when ``want_lse`` is false.  ``scale`` defaults to 1/sqrt(head_dim)."""
+    when ``want_lse`` is false.  ``scale`` defaults to 1/sqrt(head_dim).
+    Autograd records nothing; the gradient is ``attention_backward``."""
     import torch
     for t_ in (q, k, v):
         if not t_.is_cuda or t_.dtype != torch.bfloat16 or not t_.is_contiguous():
@@ -467,7 +470,9 @@ def route(x, K: int, score: str | int = "softmax", bias=None, groups: int = 1,
     K experts of largest score (plus ``bias``, fp32 [experts], for the choice only), best first.
     ``score`` is "softmax" or "sigmoid" of the logits x (fp32 or bf16 [rows, experts]).  With
     ``groups`` the experts are that many runs of equal length, of which the ``topk_groups`` of
-    largest value (the sum of a group's ``group_top`` largest) take part."""
+    largest value (the sum of a group's ``group_top`` largest) take part.  A token's result
+    does not depend on the others in the batch.  Autograd records nothing; the gradient is
+    ``route_backward``."""
     import torch
     if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D CUDA tensor")

@@ -52,7 +52,7 @@
 // measured bf16 rate: the tensor pipe, which is busy 2048 of ~2700 cycles of a key
 // tile and 1536 of ~1740 of a query tile.  d = 64 (0.69 TFLOP) 899 us: the compute
 // warps' chain per tile, for a product takes half as long for as many scores.
-// Under the mask 690 us at d = 128, and 16 x 16384 at d = 64 1768 us.
+// Under the mask 700 us at d = 128, and 16 x 16384 at d = 64 1768 us.
 #pragma once
 
 #include <cuda.h>

@@ -14,11 +14,11 @@
 // ones.  A token's row lives in the registers of one warp: lane l holds a run
 // of consecutive experts, runs in lane order inside a group and groups in lane
 // order, so the lowest expert among ties is the lowest lane's lowest element
-// and a maximum over the warp is one redux instruction.  65536 rows: 64 experts,
-// K = 6, softmax 23 us, 128 experts, K = 8, 29 us; 256 experts, sigmoid, bias and
-// groups 68 us by the kernel for large batches below (64 instructions per logit,
-// the ALU pipe 57 % busy; 10.5 us is what the bytes take).  The gradient of the
-// last: 21 us for 73 MB.
+// and a maximum over the warp is one redux instruction.  65536 rows, inputs past
+// L2: 64 experts, K = 6, softmax 24 us, 128 experts, K = 8, 31 us; 256 experts,
+// sigmoid, bias and groups 68 us by the kernel for large batches below (64
+// instructions per logit, the ALU pipe 56 % busy; 10.5 us is what the bytes take).
+// The gradient of the last: 21 us for 73 MB.
 //
 // Exact choices.  Without a bias s rises with x, so logits are compared and
 // the choice is exact.  With a bias (and for sums of two scores) c is computed
@@ -26,7 +26,9 @@
 // Three steps, each for the tokens that the one before could not settle: choices
 // by 32-bit keys, a value with its low bits replaced by its place; by full fp32
 // values of exact functions (choose_exact); and in 64 bits (choose_wide).  Values
-// of equal logit and bias need no more digits.
+// of equal logit and bias need no more digits.  The weights themselves are of
+// fp32 functions (the denominator's exponentials the SFU's), 6e-8 relative from
+// the true ones as measured: a rounding or two of the result's.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -41,7 +41,9 @@
 // (0.75 TB/s of the one read; 10 us at the rate of memory) and are bound by
 // instructions, 43 per column, 16 of them packed pairs that take the FMA pipe two
 // cycles; top-p 0.9 150 us, a histogram more.  256 x 50257 fp32: 45 us, top-p 78, top-k 50 29.
-// One row: 13 us, top-p 26, the latency of its steps over eight CTAs.
+// One row: 13 us, top-p 27, the latency of its steps over eight CTAs.  Temperature
+// 0: 42 us, 24 and 10.  Rows of one value throughout, where the general cut meets
+// all its atomics on one word: 256 x 50257 top-k 50 310 us, top-p 0.9 760.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -118,14 +120,16 @@ __device__ __forceinline__ u64 fraction64(float p) {
 //
 // With c = 32 log2 e / T in two fp32 parts, the exponent is 32 n + j + g, |g| <=
 // 1/2, and 2^(g/32) = e^y with y = g ln 2 / 32; w = 2^n 2^(j/32) (1 + (e^y -
-// 1)).  Every product whose rounding would show at 2^-38 carries its residual,
-// and the two parts of w are turned into integers by adding a constant whose
-// last bit is their unit (on the FMA and integer pipes: the conversion
-// instructions run at an eighth of their rate).  Two ways:
+// 1)): the table-driven exponential, reduced to 1/32 of an octave.  Every product
+// whose rounding would show at 2^-38 carries its residual, and the two parts of w
+// are turned into integers by adding a constant whose last bit is their unit (on
+// the FMA and integer pipes: the conversion instructions run at an eighth of their
+// rate).  Two ways:
 //   plain rows (nearly all): the exponent is x c - base with an integer base >
 //     m c, two values at a time on packed pairs, 32 FMA-pipe operations per
 //     column, which bound the sums' passes;
-//   any row: the exponent is (x - m) c, x - m in two parts; w(m) = 1.
+//   any row: the exponent is (x / 2 - m / 2) 2 c, the difference in two parts;
+//     w(m) = 1.
 struct Weight {
     float m, c_hi, c_lo;  // maximum; c
     float unit;           // 1.5 * 2^(23 - bits): its last bit is 2^-bits
