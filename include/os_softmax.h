@@ -3,8 +3,10 @@
  * softmax and fused softmax+TopK on one NVIDIA GB300 GPU (sm_103a), with the
  * attention forward that the same (m, d) recurrence carries onto the tensor
  * cores (os_attention_fwd) and its gradient (os_attention_bwd), the router
- * over experts (os_route_topk, os_route_bwd) and the sampler over whole rows
- * of logits (os_sample).
+ * over experts (os_route_topk, os_route_bwd), the sampler over whole rows
+ * of logits (os_sample), and the decode loop's operators: a paged key-value
+ * cache (os_paged_append, os_paged_attention, os_paged_reorder) and beam
+ * search's selection (os_beam_select).
  *
  * Operations (statement of the problem):
  *   softmax : for each row r of x[rows, cols], y[r, i] = e^(x[r,i] - m_r) / d_r
@@ -360,6 +362,152 @@ typedef struct {
 os_status os_sample(const void *x, const float *u, const os_sampling *s, int32_t *out,
                     float *prob, int64_t rows, int64_t cols, os_dtype in_dtype,
                     os_stream_t stream);
+
+/*
+ * A paged key-value cache: keys and values of many sequences in pages of one
+ * pool, found through a table.  Position p of sequence b is slot p % page_size
+ * of page table[b][p / page_size].
+ *   k, v      [pages][kv_heads][page_size][head_dim] bf16, 16-byte aligned.
+ *   table     [seqs][width] int32: pages of the pool.  Entries behind a
+ *             sequence's length are not used and may hold anything; an entry
+ *             outside [0, pages) is a page that is not there (see each call).
+ *             Sequences may share pages.
+ *   lengths   [seqs] int32: tokens that each sequence holds, those of this
+ *             step's append among them (one tensor serves the append and the
+ *             attention behind it).  Below 0 counts as 0, above width *
+ *             page_size as that.
+ *   pages >= 1, seqs >= 0, width >= 1, kv_heads >= 1, page_size >= 1, head_dim
+ *   64 or 128; pages * kv_heads * page_size, width * page_size and seqs *
+ *   (query or key heads) at most 2^31 - 1 (OS_ERR_SHAPE).
+ * The struct itself is read on the host during the call.
+ */
+typedef struct {
+    void *k, *v;
+    const int32_t *table, *lengths;
+    int64_t pages, seqs, width;
+    int32_t kv_heads, page_size, head_dim;
+} os_paged_cache;
+
+/*
+ * Store new tokens' keys and values in the cache, keys (and queries) rotated by
+ * their positions on the way.  Sequence b's n_b new tokens are rows starts[b] to
+ * starts[b + 1] - 1 of q, k and v; the i-th has position p = lengths[b] - n_b + i.
+ * With angles a_f = p inv_freq[f], f < rot / 2, the pairs (x_f, x_{f + rot/2})
+ * of a head, or with interleaved 1 (x_{2f}, x_{2f+1}), become
+ *   (x cos a - y sin a,  y cos a + x sin a);
+ * dimensions from rot on and v are copied.
+ *   k, v      [tokens] rows of kv_heads x head_dim bf16, k_stride and v_stride
+ *             elements apart (multiples of 8, at least the row); 16-byte
+ *             aligned.  They may be slices of one projection's result.
+ *   q, q_out  [tokens] rows of q_heads x head_dim bf16, q_stride apart, and the
+ *             rotated queries, dense; or both NULL (q_heads and q_stride are
+ *             then not looked at).
+ *   starts    [seqs + 1] int32, not falling; or NULL: one new token per sequence
+ *             (tokens == seqs, OS_ERR_SHAPE otherwise).
+ *   inv_freq  [rot / 2] fp32, finite; or NULL: no rotation (rot is then not
+ *             looked at).  rot: a multiple of 16, 16 to head_dim (OS_ERR_SHAPE).
+ *   tokens    0 to 2^31 - 1; 0: no-op.
+ * A row before starts[0] or from starts[seqs] on, or whose position is below 0
+ * (an idle place: length 0), takes no part: nothing is stored and its row of
+ * q_out is left as it was.  A position beyond the table, or whose page is not
+ * there, is not stored; its query is rotated all the same.  The places of the
+ * new tokens have to be different ones (sequences that share a page end before
+ * it): of two tokens for one place any piece may stay.
+ * q_out may not overlap the inputs or the cache, nor the cache any input
+ * (OS_ERR_ALIAS).  Angles are reduced in 64 bits (an error below 2^-22 turns
+ * at any position, 2^-30 below 2^24); products and sums in fp32, rounded once.
+ */
+os_status os_paged_append(const os_paged_cache *cache, const void *k, int64_t k_stride,
+                          const void *v, int64_t v_stride, const void *q, int64_t q_stride,
+                          void *q_out, const int32_t *starts, const float *inv_freq,
+                          int64_t tokens, int32_t q_heads, int32_t rot, int32_t interleaved,
+                          os_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over the cache: for query head h of
+ * sequence b, with its key head h / (q_heads / kv_heads),
+ *   O = sum_j softmax_j(scale q . k_j) v_j,  L = ln sum_j e^(scale q . k_j)
+ * over the keys j < lengths[b] whose page is there.  A sequence without keys gets
+ * O = 0 and L = -inf.
+ *   q         [seqs] rows of q_heads x head_dim bf16, q_stride elements apart (a
+ *             multiple of 8, at least the row); 16-byte aligned.  q_heads is a
+ *             multiple of kv_heads (OS_ERR_SHAPE).
+ *   out       [seqs][q_heads][head_dim] bf16, 16-byte aligned.
+ *   lse       [seqs][q_heads] fp32, or NULL (not written).
+ *   workspace os_paged_attention_workspace bytes, 16-byte aligned, overwritten.
+ *             Calls that can run at the same time need one each.
+ *   scale     finite and > 0 (OS_ERR_VALUE).
+ * Outputs and workspace may not overlap the inputs or each other (OS_ERR_ALIAS).
+ * What the cache holds behind the lengths is not used, whatever its bits.
+ * Arithmetic: products on the tensor cores from bf16 operands with fp32 sums;
+ * weights in fp32, as the sum of two bf16 numbers (2^-17) in the second product;
+ * O rounded once to bf16.  A sequence's keys may be split over the
+ * GPU's SMs and are joined in their order: the same call gives the same bits.
+ */
+os_status os_paged_attention(const os_paged_cache *cache, const void *q, int64_t q_stride,
+                             void *out, float *lse, void *workspace, int32_t q_heads,
+                             float scale, os_stream_t stream);
+
+/* Bytes of workspace that os_paged_attention wants, for any sizes, on the
+ * current device. */
+os_status os_paged_attention_workspace(int64_t *bytes);
+
+/*
+ * States after a beam search's choice: sequence j = group * beams + i goes on as
+ * its parent p = group * beams + parents[j].  Its row of out_table takes p's
+ * entries for p's full pages (which nothing writes any more, so sequences share
+ * them); of a page that p has filled in part, the filled rows are copied, in all
+ * layers, to the page that out_table names at that place.  Other entries of
+ * out_table stay.
+ *   cache     k, v are [layers][pages][kv_heads][page_size][head_dim] here;
+ *             table and lengths are those before the choice.  layers >= 1, and
+ *             layers * kv_heads * seqs at most 2^31 - 1 (OS_ERR_SHAPE).
+ *   parents   [seqs] int32, 0 to beams - 1.  Outside: the sequence has no parent,
+ *             its row stays and its length becomes 0.
+ *   out_table [seqs][width] int32.  At each sequence's next place it names a page
+ *             of the sequence's own, which no row of table uses (keep two tables
+ *             and let them take turns).  A page that is not there, or the parent's
+ *             own one, is not copied to.
+ *   out_lengths [seqs] int32: the parents' lengths; or NULL (not written).
+ *   beams     1 or more, a divisor of seqs (OS_ERR_SHAPE).
+ * Outputs may not overlap the inputs or each other (OS_ERR_ALIAS).
+ */
+os_status os_paged_reorder(const os_paged_cache *cache, const int32_t *parents,
+                           int32_t *out_table, int32_t *out_lengths, int32_t beams,
+                           int32_t layers, os_stream_t stream);
+
+/*
+ * Beam search's selection: of each group of `beams` rows of logits the K
+ * continuations (beam i, column v) of largest
+ *   c = scores_i + x_iv - ln sum_w e^(x_iw),
+ * best first, ties to the lower beam, then the lower column.
+ *   x        [groups * beams][cols] of in_dtype, read only.
+ *   scores   [groups][beams] fp32: the beams' summed log-probabilities.  A beam
+ *            of -inf (or NaN) is not there; its logits are not read.
+ *   ended    [groups][beams] bytes, not 0 where a beam has ended: it goes on as
+ *            (i, pad) with c = scores_i alone, and its logits are not read.  Or
+ *            NULL (none).
+ *   out      [groups][K] fp32: c;  parents, tokens  [groups][K] int32: i and v.
+ *            Where there are fewer than K continuations the places behind them
+ *            get -inf, -1 and -1.
+ *   workspace os_beam_select_workspace bytes, 16-byte aligned, overwritten.  Calls
+ *            that can run at the same time need one each.
+ *   beams, K 1 to 64 (OS_ERR_SHAPE, OS_ERR_K); pad 0 to cols - 1 (OS_ERR_VALUE);
+ *            groups >= 0, groups * beams at most 2^26.
+ * Logits of -inf and NaN are no continuations; +inf ones share their row's
+ * probability evenly.  Choices are those of real arithmetic: beams whose sums in
+ * fp32 leave the order open are summed again to 2^-38.  Outputs and workspace may
+ * not overlap the inputs or each other (OS_ERR_ALIAS).
+ */
+os_status os_beam_select(const void *x, const float *scores, const uint8_t *ended, float *out,
+                         int32_t *parents, int32_t *tokens, void *workspace, int64_t groups,
+                         int32_t beams, int64_t cols, int32_t K, int32_t pad,
+                         os_dtype in_dtype, os_stream_t stream);
+
+/* Bytes of workspace that os_beam_select wants for these sizes on the current
+ * device. */
+os_status os_beam_select_workspace(int64_t groups, int32_t beams, int64_t cols, int32_t K,
+                                   os_dtype in_dtype, int64_t *bytes);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *os_status_string(os_status status);

@@ -3,7 +3,9 @@
 The C ABI (include/os_softmax.h) is wrapped with ctypes under the same names:
 ``os_softmax_fwd``, ``os_softmax_topk``, ``os_topk``, ``os_softmax_causal_fwd``,
 ``os_softmax_stats``, ``os_topk_sample``, ``os_attention_fwd``, ``os_attention_bwd``,
-``os_route_topk``, ``os_route_bwd``, ``os_sample``, ``os_softmax_fwd_path``,
+``os_route_topk``, ``os_route_bwd``, ``os_sample``, ``os_paged_append``,
+``os_paged_attention``, ``os_paged_attention_workspace``, ``os_paged_reorder``,
+``os_beam_select``, ``os_beam_select_workspace``, ``os_softmax_fwd_path``,
 ``os_softmax_plan``, ``os_topk_plan``, ``os_exp_f32``, ``os_exp_pairs_f32``,
 ``os_exp_pairs_coarse_f32``, ``os_device_status``,
 ``os_set_wait_timeout_ns``, ``os_set_fault_injection``, ``os_status_string``.  They take raw
@@ -11,7 +13,8 @@ device pointers (ints) and a raw stream handle, exactly like the C functions,
 and raise ``OsError`` on a non-OK status.
 
 ``softmax``, ``softmax_topk``, ``topk``, ``softmax_causal``, ``softmax_stats``,
-``attention``, ``attention_backward``, ``route``, ``route_backward`` and ``sample``
+``attention``, ``attention_backward``, ``route``, ``route_backward``, ``sample``,
+``paged_append``, ``paged_attention``, ``paged_reorder`` and ``beam_select``
 are the tensor-level conveniences: they take
 torch CUDA tensors, allocate outputs with torch, pass the current torch
 stream, and call the same C entry points.  PyTorch only provides memory and
@@ -24,6 +27,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -69,6 +73,14 @@ class Sampling(ctypes.Structure):
                 ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float)]
 
 
+class PagedCache(ctypes.Structure):
+    """os_paged_cache: device pointers of the pool, the table and the lengths, and the sizes."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("pages", ctypes.c_int64), ("seqs", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -90,6 +102,14 @@ def _load() -> ctypes.CDLL:
                                   ctypes.c_float, st, vp]
     lib.os_route_bwd.argtypes = [vp, vp, vp, vp, i64, i64, i32, st, i32, ctypes.c_float, st, vp]
     lib.os_sample.argtypes = [vp, vp, ctypes.POINTER(Sampling), vp, vp, i64, i64, st, vp]
+    cache, p64 = ctypes.POINTER(PagedCache), ctypes.POINTER(ctypes.c_int64)
+    lib.os_paged_append.argtypes = [cache, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, i32, i32,
+                                    i32, vp]
+    lib.os_paged_attention.argtypes = [cache, vp, i64, vp, vp, vp, i32, ctypes.c_float, vp]
+    lib.os_paged_attention_workspace.argtypes = [p64]
+    lib.os_paged_reorder.argtypes = [cache, vp, vp, vp, i32, i32, vp]
+    lib.os_beam_select.argtypes = [vp] * 7 + [i64, i32, i64, i32, i32, st, vp]
+    lib.os_beam_select_workspace.argtypes = [i64, i32, i64, i32, st, p64]
     lib.os_softmax_plan.argtypes = [i64, i64, st, st, st, ctypes.POINTER(Plan)]
     lib.os_topk_plan.argtypes = [i64, i64, i32, ctypes.POINTER(Plan)]
     lib.os_exp_f32.argtypes = [vp, vp, i64, vp]
@@ -103,6 +123,8 @@ def _load() -> ctypes.CDLL:
     for name in ("os_softmax_fwd", "os_softmax_fwd_path", "os_softmax_topk", "os_topk",
                  "os_softmax_causal_fwd", "os_softmax_stats", "os_topk_sample", "os_attention_fwd",
                  "os_attention_bwd", "os_route_topk", "os_route_bwd", "os_sample",
+                 "os_paged_append", "os_paged_attention", "os_paged_attention_workspace",
+                 "os_paged_reorder", "os_beam_select", "os_beam_select_workspace",
                  "os_softmax_plan",
                  "os_topk_plan", "os_exp_f32", "os_exp_pairs_f32", "os_exp_pairs_coarse_f32",
                  "os_device_status",
@@ -193,6 +215,47 @@ def os_sample(x: int, u: int, settings: Sampling, out: int, prob: int | None, ro
               cols: int, in_dtype: int, stream: int | None) -> None:
     _check(_lib.os_sample(x, u, ctypes.byref(settings), out, prob, rows, cols, in_dtype, stream),
            "os_sample")
+
+
+def os_paged_append(cache: PagedCache, k: int, k_stride: int, v: int, v_stride: int,
+                    q: int | None, q_stride: int, q_out: int | None, starts: int | None,
+                    inv_freq: int | None, tokens: int, q_heads: int, rot: int, interleaved: int,
+                    stream: int | None) -> None:
+    _check(_lib.os_paged_append(ctypes.byref(cache), k, k_stride, v, v_stride, q, q_stride, q_out,
+                                starts, inv_freq, tokens, q_heads, rot, interleaved, stream),
+           "os_paged_append")
+
+
+def os_paged_attention(cache: PagedCache, q: int, q_stride: int, out: int, lse: int | None,
+                       workspace: int, q_heads: int, scale: float, stream: int | None) -> None:
+    _check(_lib.os_paged_attention(ctypes.byref(cache), q, q_stride, out, lse, workspace, q_heads,
+                                   scale, stream), "os_paged_attention")
+
+
+def os_paged_attention_workspace() -> int:
+    n = ctypes.c_int64()
+    _check(_lib.os_paged_attention_workspace(ctypes.byref(n)), "os_paged_attention_workspace")
+    return n.value
+
+
+def os_paged_reorder(cache: PagedCache, parents: int, out_table: int, out_lengths: int | None,
+                     beams: int, layers: int, stream: int | None) -> None:
+    _check(_lib.os_paged_reorder(ctypes.byref(cache), parents, out_table, out_lengths, beams,
+                                 layers, stream), "os_paged_reorder")
+
+
+def os_beam_select(x: int, scores: int, ended: int | None, out: int, parents: int, tokens: int,
+                   workspace: int, groups: int, beams: int, cols: int, K: int, pad: int,
+                   in_dtype: int, stream: int | None) -> None:
+    _check(_lib.os_beam_select(x, scores, ended, out, parents, tokens, workspace, groups, beams,
+                               cols, K, pad, in_dtype, stream), "os_beam_select")
+
+
+def os_beam_select_workspace(groups: int, beams: int, cols: int, K: int, in_dtype: int) -> int:
+    n = ctypes.c_int64()
+    _check(_lib.os_beam_select_workspace(groups, beams, cols, K, in_dtype, ctypes.byref(n)),
+           "os_beam_select_workspace")
+    return n.value
 
 
 def os_exp_f32(z: int, out: int, n: int, stream: int | None) -> None:
@@ -562,6 +625,210 @@ def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, prob=
     _call(dev, "os_sample", _lib.os_sample, x.data_ptr(), u.data_ptr(), ctypes.byref(settings),
           out.data_ptr(), prob.data_ptr(), rows, cols, code)
     return out, prob
+
+
+def _paged_cache(k_cache, v_cache, table, lengths, dims=4):
+    """The os_paged_cache of these tensors, whose kinds and shapes it checks."""
+    import torch
+    bf16, i32 = torch.bfloat16, torch.int32
+    if not k_cache.is_cuda or k_cache.dtype != bf16 or not k_cache.is_contiguous() or \
+            k_cache.dim() != dims:
+        raise ValueError("k_cache must be a contiguous bf16 CUDA tensor "
+                         f"{'[layers, ' if dims == 5 else '['}pages, kv_heads, page_size, head_dim]")
+    if table.dim() != 2:
+        raise ValueError("table must be int32 [seqs, width]")
+    pages, kv_heads, page_size, head_dim = k_cache.shape[-4:]
+    seqs, width = table.shape
+    dev = k_cache.device
+    _like("v_cache", v_cache, k_cache.shape, bf16, dev)
+    _like("table", table, (seqs, width), i32, dev)
+    _like("lengths", lengths, (seqs,), i32, dev)
+    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(),
+                      pages, seqs, width, _int32(kv_heads), _int32(page_size), _int32(head_dim))
+
+
+def _heads(name, t, rows, heads, head_dim, device):
+    """The distance between the rows of `t` [rows, heads, head_dim], bf16, each row contiguous."""
+    import torch
+    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != device or t.shape[0] != rows or \
+            t.shape[1] != heads or t.shape[2] != head_dim:
+        raise ValueError(f"{name} must be a bf16 tensor of shape {(rows, heads, head_dim)} "
+                         f"on {device}")
+    row, step, one = t.stride()
+    if t.numel() and ((one != 1) or (heads > 1 and step != head_dim)):
+        raise ValueError(f"{name}'s rows must be contiguous")
+    # (a single row has no distance)
+    return row if rows > 1 and t.numel() else heads * head_dim
+
+
+def paged_append(k_cache, v_cache, table, lengths, k, v, q=None, starts=None, inv_freq=None,
+                 interleaved: bool = False, q_out=None):
+    """Store new tokens' keys and values in a paged cache, keys and queries rotated by their
+    positions on the way; returns the rotated queries (bf16 [tokens, q_heads, head_dim], None
+    without q).
+
+    The cache is bf16 [pages, kv_heads, page_size, head_dim], ``table`` int32 [seqs, width] names
+    each sequence's pages, and ``lengths`` int32 [seqs] counts each sequence's tokens, the new
+    ones among them.  k, v [tokens, kv_heads, head_dim] and q may be slices of one tensor (rows
+    any multiple of 8 elements apart).  Sequence b's new tokens are rows starts[b] to
+    starts[b + 1] of them (int32 [seqs + 1]), its last; without ``starts`` each sequence has one.
+    ``inv_freq`` (fp32 [rot / 2]) are the angles per position of the first rot dimensions, in
+    pairs (f, f + rot / 2), or neighbours with ``interleaved``; without it nothing is rotated.
+    A sequence of length 0 takes no part, nor do rows outside ``starts``."""
+    import torch
+    cache = _paged_cache(k_cache, v_cache, table, lengths)
+    dev, tokens = k_cache.device, k.shape[0]
+    k_stride = _heads("k", k, tokens, cache.kv_heads, cache.head_dim, dev)
+    v_stride = _heads("v", v, tokens, cache.kv_heads, cache.head_dim, dev)
+    q_heads = q_stride = 0
+    if q is not None:
+        q_heads = q.shape[1] if q.dim() == 3 else 0
+        q_stride = _heads("q", q, tokens, q_heads, cache.head_dim, dev)
+        shape = (tokens, q_heads, cache.head_dim)
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _like("q_out", q_out, shape, torch.bfloat16, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = 0
+    if starts is not None:
+        _like("starts", starts, (cache.seqs + 1,), torch.int32, dev)
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _like("inv_freq", inv_freq, (rot // 2,), torch.float32, dev)
+    _call(dev, "os_paged_append", _lib.os_paged_append, ctypes.byref(cache), k.data_ptr(), k_stride,
+          v.data_ptr(), v_stride, None if q is None else q.data_ptr(), q_stride,
+          None if q is None else q_out.data_ptr(), None if starts is None else starts.data_ptr(),
+          None if inv_freq is None else inv_freq.data_ptr(), tokens, _int32(q_heads), _int32(rot),
+          int(interleaved))
+    return q_out
+
+
+_attention_workspace = {}  # bytes per device
+
+
+def paged_attention(q, k_cache, v_cache, table, lengths, scale: float | None = None, out=None,
+                    lse=None, workspace=None, want_lse: bool = True):
+    """Attention of one new token per sequence over a paged cache (see ``paged_append``):
+    (O bf16 [seqs, q_heads, head_dim], L fp32 [seqs, q_heads]) for q bf16 of O's shape, whose
+    rows may be apart; q_heads is a multiple of the cache's heads.  ``scale`` defaults to
+    1/sqrt(head_dim).  Keys behind a sequence's length, or of pages outside the pool, take no part;
+    a sequence without keys gets 0 and -inf.  L is None when ``want_lse`` is false.  ``workspace`` is a buffer of
+    ``os_paged_attention_workspace`` bytes (allocated when not given)."""
+    import torch
+    cache = _paged_cache(k_cache, v_cache, table, lengths)
+    dev = k_cache.device
+    seqs, head_dim = cache.seqs, cache.head_dim
+    q_heads = q.shape[1] if q.dim() == 3 else 0
+    q_stride = _heads("q", q, seqs, q_heads, head_dim, dev)
+    shape = (seqs, q_heads, head_dim)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _like("out", out, shape, torch.bfloat16, dev)
+    if lse is not None:
+        _like("lse", lse, shape[:2], torch.float32, dev)
+    elif want_lse:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    need = _attention_workspace.get(dev.index)
+    if need is None:
+        with _OnDevice(dev):
+            need = _attention_workspace[dev.index] = os_paged_attention_workspace()
+    workspace = _workspace(workspace, need, dev)
+    _call(dev, "os_paged_attention", _lib.os_paged_attention, ctypes.byref(cache), q.data_ptr(),
+          q_stride, out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+          _int32(q_heads),
+          1.0 / head_dim ** 0.5 if scale is None else float(scale))
+    return out, lse
+
+
+def _workspace(t, need, device):
+    """`t`, when it is a large enough byte buffer; a new one without it."""
+    import torch
+    if t is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if t.dtype != torch.uint8 or t.device != device or not t.is_contiguous() or t.numel() < need:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes "
+                         f"on {device}")
+    return t
+
+
+def paged_reorder(k_cache, v_cache, table, lengths, parents, out_table, out_lengths=None):
+    """States after a beam search's choice: sequence (group, i) goes on as the group's beam
+    parents[group, i] (int32 [groups, beams], as ``beam_select`` gives them; groups * beams are
+    the sequences).  Its row of ``out_table`` takes the parent's full pages, shared from then on;
+    the filled rows of the parent's last page are copied to the page that ``out_table`` names
+    there, one of the sequence's own that no row of ``table`` uses.  The caches may have a leading
+    dimension of layers.  Returns (out_table, out_lengths), the latter the parents' lengths.  A
+    parent outside the group leaves a sequence's row as it is, with length 0."""
+    import torch
+    cache = _paged_cache(k_cache, v_cache, table, lengths, 5 if k_cache.dim() == 5 else 4)
+    dev, i32 = k_cache.device, torch.int32
+    if parents.dim() != 2:
+        raise ValueError("parents must be int32 [groups, beams]")
+    groups, beams = parents.shape
+    if groups * beams != cache.seqs:
+        raise ValueError("groups * beams must be the table's sequences")
+    _like("parents", parents, (groups, beams), i32, dev)
+    _like("out_table", out_table, (cache.seqs, cache.width), i32, dev)
+    if out_lengths is None:
+        out_lengths = torch.empty(cache.seqs, dtype=i32, device=dev)
+    else:
+        _like("out_lengths", out_lengths, (cache.seqs,), i32, dev)
+    _call(dev, "os_paged_reorder", _lib.os_paged_reorder, ctypes.byref(cache), parents.data_ptr(),
+          out_table.data_ptr(), out_lengths.data_ptr(), _int32(max(beams, 1)),
+          _int32(k_cache.shape[0]) if k_cache.dim() == 5 else 1)
+    return out_table, out_lengths
+
+
+@functools.lru_cache(maxsize=256)
+def _beam_workspace(device_index, groups, beams, cols, K, code):
+    return os_beam_select_workspace(groups, beams, cols, K, code)
+
+
+def beam_select(x, scores, K: int | None = None, ended=None, pad: int = 0, out=None, parents=None,
+                tokens=None, workspace=None):
+    """Beam search's selection: of each group's beams the K continuations (beam i, column v) of
+    largest scores[g, i] + log_softmax(x[g, i])[v], best first, ties to the lower beam, then the
+    lower column: (their values fp32, beams int32, columns int32), each [groups, K].  x: logits
+    fp32 or bf16 [groups * beams, cols]; scores fp32 [groups, beams], -inf where there is no beam;
+    K defaults to the number of beams.  A beam that has ``ended`` (bool [groups, beams]) goes on
+    as (i, pad) with its score alone.  Places behind the last continuation get -inf, -1 and -1."""
+    import torch
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous 2-D CUDA tensor")
+    if scores.dim() != 2:
+        raise ValueError("scores must be float32 [groups, beams]")
+    code = _dtype_code(x.dtype)
+    groups, beams = scores.shape
+    cols, dev, f32, i32 = x.shape[1], x.device, torch.float32, torch.int32
+    if x.shape[0] != groups * beams:
+        raise ValueError("x must have a row for each of the scores")
+    _like("scores", scores, (groups, beams), f32, dev)
+    if ended is not None:
+        _like("ended", ended, (groups, beams), torch.bool, dev)
+    K = beams if K is None else K
+    need = _beam_workspace(dev.index, groups, beams, cols, _int32(K), code) \
+        if torch.cuda.current_device() == dev.index else _on(dev, os_beam_select_workspace, groups,
+                                                             beams, cols, _int32(K), code)
+    shape = (groups, K)
+    out = torch.empty(shape, dtype=f32, device=dev) if out is None else \
+        _like("out", out, shape, f32, dev)
+    parents = torch.empty(shape, dtype=i32, device=dev) if parents is None else \
+        _like("parents", parents, shape, i32, dev)
+    tokens = torch.empty(shape, dtype=i32, device=dev) if tokens is None else \
+        _like("tokens", tokens, shape, i32, dev)
+    workspace = _workspace(workspace, need, dev)
+    _call(dev, "os_beam_select", _lib.os_beam_select, x.data_ptr(), scores.data_ptr(),
+          None if ended is None else ended.data_ptr(), out.data_ptr(), parents.data_ptr(),
+          tokens.data_ptr(), workspace.data_ptr(), groups, beams, cols, K, _int32(pad), code)
+    return out, parents, tokens
+
+
+def _on(device, fn, *args):
+    with _OnDevice(device):
+        return fn(*args)
 
 
 def exp(z, pairs: bool = False, coarse: bool = False):

@@ -79,6 +79,27 @@ bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
     return pa < pb + uintptr_t(nb) && pb < pa + uintptr_t(na);
 }
 
+// A buffer of a call; those that are NULL are passed over.
+struct Buffer {
+    const void* p;
+    int64_t bytes;
+};
+
+// No written buffer overlaps a read one or another written one.
+template <int W, int R>
+bool apart(const Buffer (&written)[W], const Buffer (&read)[R]) {
+    for (int i = 0; i < W; ++i) {
+        if (!written[i].p) continue;
+        for (const Buffer& r : read)
+            if (r.p && overlaps(written[i].p, written[i].bytes, r.p, r.bytes)) return false;
+        for (int j = 0; j < i; ++j)
+            if (written[j].p &&
+                overlaps(written[i].p, written[i].bytes, written[j].p, written[j].bytes))
+                return false;
+    }
+    return true;
+}
+
 // rows >= 0, 1 <= cols <= 2^31-1, and rows*cols*8 representable.
 bool shape_ok(int64_t rows, int64_t cols) {
     if (rows < 0 || cols < 1 || cols > INT32_MAX) return false;
@@ -435,6 +456,210 @@ os_status os_sample(const void* x, const float* u, const os_sampling* s, int32_t
     }
     const cudaError_t e = os::launch_sample(x, in, u, out, prob, rows, static_cast<int>(cols), *s,
                                             reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? OS_OK : OS_ERR_CUDA;
+}
+
+// Sizes of a paged cache, with `heads` query or key heads and `layers` copies of the pool.
+static os_status paged_checks(const os_paged_cache* c, int64_t heads, int64_t layers) {
+    if (!c) return OS_ERR_NULL;
+    if (c->pages < 1 || c->seqs < 0 || c->width < 1 || c->kv_heads < 1 || c->page_size < 1 ||
+        (c->head_dim != 64 && c->head_dim != 128) || heads < c->kv_heads || layers < 1)
+        return OS_ERR_SHAPE;
+    if (c->pages > INT32_MAX / c->kv_heads / c->page_size || c->width > INT32_MAX / c->page_size ||
+        c->seqs > INT32_MAX / heads || c->seqs > INT32_MAX / c->kv_heads / layers ||
+        c->width > INT64_MAX / 8 / (c->seqs + 1))
+        return OS_ERR_SHAPE;
+    return OS_OK;
+}
+
+static os_status paged_pointers(const os_paged_cache* c) {
+    if (!c->k || !c->v || !c->table || !c->lengths) return OS_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(c->k) % 16 || reinterpret_cast<uintptr_t>(c->v) % 16 ||
+        reinterpret_cast<uintptr_t>(c->table) % 4 || reinterpret_cast<uintptr_t>(c->lengths) % 4)
+        return OS_ERR_ALIGN;
+    return OS_OK;
+}
+
+static int64_t pool_bytes(const os_paged_cache* c) {
+    return c->pages * c->kv_heads * c->page_size * c->head_dim * 2;
+}
+
+// Rows of `row` elements `stride` apart: dense 16-byte pieces, no row over the next.
+static bool rows_ok(int64_t rows, int64_t stride, int64_t row) {
+    return stride >= row && stride % 8 == 0 && stride <= INT64_MAX / 4 / (rows + 1);
+}
+
+static int64_t rows_bytes(int64_t rows, int64_t stride, int64_t row) {
+    return ((rows - 1) * stride + row) * 2;
+}
+
+os_status os_paged_append(const os_paged_cache* cache, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const void* q, int64_t q_stride,
+                          void* q_out, const int32_t* starts, const float* inv_freq,
+                          int64_t tokens, int32_t q_heads, int32_t rot, int32_t interleaved,
+                          os_stream_t stream) {
+    const os_status st = paged_checks(cache, q ? q_heads : cache ? cache->kv_heads : 1, 1);
+    if (st != OS_OK) return st;
+    const int64_t d = cache->head_dim, kv_row = cache->kv_heads * d, q_row = q ? q_heads * d : 0;
+    if (tokens < 0 || tokens > INT32_MAX || (!starts && tokens != cache->seqs)) return OS_ERR_SHAPE;
+    if (!rows_ok(tokens, k_stride, kv_row) || !rows_ok(tokens, v_stride, kv_row) ||
+        (q && !rows_ok(tokens, q_stride, q_row)) || (q && q_heads > INT32_MAX / 2 / d) ||
+        (inv_freq && (rot < 16 || rot > d || rot % 16)))
+        return OS_ERR_SHAPE;
+    if (interleaved != 0 && interleaved != 1) return OS_ERR_VALUE;
+    if (tokens == 0 || cache->seqs == 0) return OS_OK;
+    const os_status ps = paged_pointers(cache);
+    if (ps != OS_OK) return ps;
+    if (!k || !v || (q && !q_out) || (!q && q_out)) return OS_ERR_NULL;
+    for (const void* p : {k, v, q, static_cast<const void*>(q_out)})
+        if (reinterpret_cast<uintptr_t>(p) % 16) return OS_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(starts) % 4 || reinterpret_cast<uintptr_t>(inv_freq) % 4)
+        return OS_ERR_ALIGN;
+    const Buffer written[] = {{cache->k, pool_bytes(cache)},
+                              {cache->v, pool_bytes(cache)},
+                              {q_out, tokens * q_row * 2}};
+    const Buffer read[] = {{cache->table, cache->seqs * cache->width * 4},
+                           {cache->lengths, cache->seqs * 4},
+                           {k, rows_bytes(tokens, k_stride, kv_row)},
+                           {v, rows_bytes(tokens, v_stride, kv_row)},
+                           {q, rows_bytes(tokens, q_stride, q_row)},
+                           {starts, (cache->seqs + 1) * 4},
+                           {inv_freq, rot * 2}};
+    if (!apart(written, read)) return OS_ERR_ALIAS;
+    const os::PagedAppendArgs a = {q,        k,      v,       q_stride, k_stride, v_stride,        q_out,
+                                   starts,   inv_freq, tokens, q_heads,  rot,      interleaved != 0};
+    const cudaError_t e =
+        os::launch_paged_append(*cache, a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? OS_OK : OS_ERR_CUDA;
+}
+
+os_status os_paged_attention_workspace(int64_t* bytes) {
+    if (!bytes) return OS_ERR_NULL;
+    const os::DeviceInfo* dev = os::device_info();
+    if (!dev) return OS_ERR_CUDA;
+    *bytes = os::paged_attention_workspace(dev->sms);
+    return OS_OK;
+}
+
+os_status os_paged_attention(const os_paged_cache* cache, const void* q, int64_t q_stride,
+                             void* out, float* lse, void* workspace, int32_t q_heads, float scale,
+                             os_stream_t stream) {
+    const os_status st = paged_checks(cache, q_heads, 1);
+    if (st != OS_OK) return st;
+    const int64_t row = int64_t(q_heads) * cache->head_dim;
+    if (q_heads % cache->kv_heads || q_heads > INT32_MAX / 2 / cache->head_dim ||
+        !rows_ok(cache->seqs, q_stride, row))
+        return OS_ERR_SHAPE;
+    if (!(scale > 0.f) || !(scale < INFINITY)) return OS_ERR_VALUE;
+    if (cache->seqs == 0) return OS_OK;
+    const os_status ps = paged_pointers(cache);
+    if (ps != OS_OK) return ps;
+    if (!q || !out || !workspace) return OS_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(out) % 16 ||
+        reinterpret_cast<uintptr_t>(workspace) % 16 || reinterpret_cast<uintptr_t>(lse) % 4)
+        return OS_ERR_ALIGN;
+    const Buffer written[] = {{out, cache->seqs * row * 2}, {lse, cache->seqs * q_heads * 4}};
+    const Buffer read[] = {{cache->k, pool_bytes(cache)},
+                           {cache->v, pool_bytes(cache)},
+                           {cache->table, cache->seqs * cache->width * 4},
+                           {cache->lengths, cache->seqs * 4},
+                           {q, rows_bytes(cache->seqs, q_stride, row)}};
+    if (!apart(written, read)) return OS_ERR_ALIAS;
+    int64_t wb = 0;
+    const os_status ws = os_paged_attention_workspace(&wb);
+    if (ws != OS_OK) return ws;
+    const Buffer scratch[] = {{workspace, wb}};
+    if (!apart(scratch, read) || !apart(scratch, written)) return OS_ERR_ALIAS;
+    const cudaError_t e =
+        os::launch_paged_attention(*cache, q, q_stride, out, lse, workspace, q_heads, scale,
+                                   reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? OS_OK : OS_ERR_CUDA;
+}
+
+os_status os_paged_reorder(const os_paged_cache* cache, const int32_t* parents, int32_t* out_table,
+                           int32_t* out_lengths, int32_t beams, int32_t layers,
+                           os_stream_t stream) {
+    const os_status st = paged_checks(cache, cache ? cache->kv_heads : 1, layers);
+    if (st != OS_OK) return st;
+    if (beams < 1 || cache->seqs % beams) return OS_ERR_SHAPE;
+    if (pool_bytes(cache) > INT64_MAX / 4 / layers) return OS_ERR_SHAPE;
+    if (cache->seqs == 0) return OS_OK;
+    const os_status ps = paged_pointers(cache);
+    if (ps != OS_OK) return ps;
+    if (!parents || !out_table) return OS_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(parents) % 4 || reinterpret_cast<uintptr_t>(out_table) % 4 ||
+        reinterpret_cast<uintptr_t>(out_lengths) % 4)
+        return OS_ERR_ALIGN;
+    const int64_t tb = cache->seqs * cache->width * 4, lb = cache->seqs * 4;
+    const Buffer written[] = {{cache->k, pool_bytes(cache) * layers},
+                              {cache->v, pool_bytes(cache) * layers},
+                              {out_table, tb},
+                              {out_lengths, lb}};
+    const Buffer read[] = {{cache->table, tb}, {cache->lengths, lb}, {parents, lb}};
+    if (!apart(written, read)) return OS_ERR_ALIAS;
+    const cudaError_t e =
+        os::launch_paged_reorder(*cache, parents, beams, layers, out_table, out_lengths,
+                                 reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? OS_OK : OS_ERR_CUDA;
+}
+
+static os_status beam_checks(int64_t groups, int32_t beams, int64_t cols, int32_t K, os_dtype in) {
+    if (!valid_dtype(in)) return OS_ERR_DTYPE;
+    if (beams < 1 || beams > 64 || groups < 0 || groups > (1 << 26) / beams ||
+        !shape_ok(groups * beams, cols))
+        return OS_ERR_SHAPE;
+    if (K < 1 || K > 64) return OS_ERR_K;
+    return OS_OK;
+}
+
+os_status os_beam_select_workspace(int64_t groups, int32_t beams, int64_t cols, int32_t K,
+                                   os_dtype in, int64_t* bytes) {
+    const os_status st = beam_checks(groups, beams, cols, K, in);
+    if (st != OS_OK) return st;
+    if (!bytes) return OS_ERR_NULL;
+    const os::DeviceInfo* dev = os::device_info();
+    if (!dev) return OS_ERR_CUDA;
+    *bytes = groups == 0 ? 0 : os::beam_select_workspace(groups, beams, cols, K, in, dev->sms);
+    return OS_OK;
+}
+
+os_status os_beam_select(const void* x, const float* scores, const uint8_t* ended, float* out,
+                         int32_t* parents, int32_t* tokens, void* workspace, int64_t groups,
+                         int32_t beams, int64_t cols, int32_t K, int32_t pad, os_dtype in,
+                         os_stream_t stream) {
+    const os_status st = beam_checks(groups, beams, cols, K, in);
+    if (st != OS_OK) return st;
+    if (pad < 0 || pad >= cols) return OS_ERR_VALUE;
+    if (groups == 0) return OS_OK;
+    if (!x || !scores || !out || !parents || !tokens || !workspace) return OS_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(x) % elem_bytes(in) || reinterpret_cast<uintptr_t>(scores) % 4 ||
+        reinterpret_cast<uintptr_t>(out) % 4 || reinterpret_cast<uintptr_t>(parents) % 4 ||
+        reinterpret_cast<uintptr_t>(tokens) % 4 || reinterpret_cast<uintptr_t>(workspace) % 16)
+        return OS_ERR_ALIGN;
+    const int64_t rows = groups * beams, kb = groups * int64_t(K) * 4;
+    const Buffer written[] = {{out, kb}, {parents, kb}, {tokens, kb}};
+    const Buffer read[] = {{x, rows * cols * elem_bytes(in)}, {scores, rows * 4}, {ended, rows}};
+    if (!apart(written, read)) return OS_ERR_ALIAS;
+    int64_t wb = 0;
+    const os_status ws = os_beam_select_workspace(groups, beams, cols, K, in, &wb);
+    if (ws != OS_OK) return ws;
+    const Buffer scratch[] = {{workspace, wb}};
+    if (!apart(scratch, read) || !apart(scratch, written)) return OS_ERR_ALIAS;
+    os::BeamSelectArgs a = {};
+    a.x = x;
+    a.in = in;
+    a.scores = scores;
+    a.ended = ended;
+    a.out = out;
+    a.parents = parents;
+    a.tokens = tokens;
+    a.workspace = workspace;
+    a.groups = groups;
+    a.cols = cols;
+    a.beams = beams;
+    a.K = K;
+    a.pad = pad;
+    const cudaError_t e = os::launch_beam_select(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? OS_OK : OS_ERR_CUDA;
 }
 

@@ -1,0 +1,75 @@
+// Beam search's selection: the rows' runs, then the groups.
+#include "host_common.h"
+#include "internal.h"
+#include "kernels/beam_kernel.cuh"
+
+namespace os {
+
+namespace {
+
+constexpr int kMaxRuns = 32;
+
+// Runs per row: as many as fill the GPU a few times over.
+struct Split {
+    int runs;
+    int64_t run_tiles;
+};
+
+Split split_rows(int64_t rows, int64_t cols, os_dtype in, int sms) {
+    const int64_t tiles = ceil_div(cols + (in == OS_F32 ? 3 : 7), beam::kTile);
+    const int64_t want = min64(min64(tiles, kMaxRuns), ceil_div(int64_t(sms) * 8, rows));
+    Split s;
+    s.run_tiles = ceil_div(tiles, want);
+    s.runs = static_cast<int>(ceil_div(tiles, s.run_tiles));
+    return s;
+}
+
+template <typename T, int KP>
+cudaError_t launch(const beam::BeamArgs& a, int64_t groups, cudaStream_t stream) {
+    const cudaError_t e = launch_kernel(beam::beam_runs_kernel<T, KP>, groups * a.beams * a.runs,
+                                        beam::kThreads, 1, 0, stream, a);
+    if (e != cudaSuccess) return e;
+    return launch_behind(beam::beam_merge_kernel<T, KP>, dim3(static_cast<unsigned>(groups)),
+                         beam::kMergeThreads, stream, a);
+}
+
+template <typename T>
+cudaError_t launch_k(const beam::BeamArgs& a, int64_t groups, cudaStream_t stream) {
+    if (a.K <= 8) return launch<T, 8>(a, groups, stream);
+    if (a.K <= 16) return launch<T, 16>(a, groups, stream);
+    if (a.K <= 32) return launch<T, 32>(a, groups, stream);
+    return launch<T, 64>(a, groups, stream);
+}
+
+}  // namespace
+
+int64_t beam_select_workspace(int64_t groups, int beams, int64_t cols, int K, os_dtype in, int sms) {
+    const Split s = split_rows(groups * beams, cols, in, sms);
+    return groups * beams * s.runs * (K + 1) * 8;
+}
+
+cudaError_t launch_beam_select(const BeamSelectArgs& p, cudaStream_t stream) {
+    const DeviceInfo* dev = device_info();
+    if (!dev) return cudaErrorInvalidDevice;
+    const Split s = split_rows(p.groups * p.beams, p.cols, p.in, dev->sms);
+    beam::BeamArgs a = {};
+    a.x = p.x;
+    a.scores = p.scores;
+    a.ended = p.ended;
+    a.out = p.out;
+    a.parents = p.parents;
+    a.tokens = p.tokens;
+    a.states = static_cast<float2*>(p.workspace);
+    a.lists = reinterpret_cast<beam::u64*>(a.states + p.groups * p.beams * s.runs);
+    a.cols = p.cols;
+    a.beams = p.beams;
+    a.K = p.K;
+    a.runs = s.runs;
+    a.run_tiles = s.run_tiles;
+    a.pad = p.pad;
+    a.eps = static_cast<float>(40 + 2 * s.run_tiles) * 0x1p-23f;
+    return p.in == OS_F32 ? launch_k<float>(a, p.groups, stream)
+                          : launch_k<__nv_bfloat16>(a, p.groups, stream);
+}
+
+}  // namespace os

@@ -58,6 +58,24 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), int64_t grid, int threads, i
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// Launch `kernel` behind the one before it on `stream`, which lets it start early
+// (griddepcontrol.launch_dependents); it waits for that one's end itself
+// (griddepcontrol.wait) before it touches what that one wrote.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_behind(void (*kernel)(KArgs...), dim3 grid, int threads, cudaStream_t stream,
+                          Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 // Opt `kernel` into `smem` bytes of dynamic shared memory and, for cluster
 // sizes above 8, into non-portable cluster sizes.  Returns false on failure.
 // Done once per (device, kernel): later calls are a table lookup, so launches

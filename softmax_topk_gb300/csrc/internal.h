@@ -83,6 +83,42 @@ OS_DECLARE_ROUTE(bf16)
 cudaError_t launch_sample(const void* x, os_dtype in, const float* u, int32_t* out, float* prob,
                           int64_t rows, int cols, const os_sampling& s, cudaStream_t stream);
 
+// paged key-value cache (see os_paged_append, os_paged_attention, os_paged_reorder)
+struct PagedAppendArgs {
+    const void *q, *k, *v;  // q may be NULL
+    int64_t q_stride, k_stride, v_stride;
+    void* q_out;
+    const int32_t* starts;  // or NULL
+    const float* inv_freq;  // or NULL
+    int64_t tokens;
+    int q_heads, rot;
+    bool interleaved;
+};
+cudaError_t launch_paged_append(const os_paged_cache& c, const PagedAppendArgs& p,
+                                cudaStream_t stream);
+cudaError_t launch_paged_reorder(const os_paged_cache& c, const int32_t* parents, int beams,
+                                 int layers, int32_t* out_table, int32_t* out_lengths,
+                                 cudaStream_t stream);
+int64_t paged_attention_workspace(int sms);
+cudaError_t launch_paged_attention(const os_paged_cache& c, const void* q, int64_t q_stride,
+                                   void* out, float* lse, void* workspace, int q_heads, float scale,
+                                   cudaStream_t stream);
+
+// beam search's selection (see os_beam_select)
+struct BeamSelectArgs {
+    const void* x;
+    os_dtype in;
+    const float* scores;
+    const uint8_t* ended;  // or NULL
+    float* out;
+    int32_t *parents, *tokens;
+    void* workspace;
+    int64_t groups, cols;
+    int beams, K, pad;
+};
+int64_t beam_select_workspace(int64_t groups, int beams, int64_t cols, int K, os_dtype in, int sms);
+cudaError_t launch_beam_select(const BeamSelectArgs& p, cudaStream_t stream);
+
 // (m, d, lse) of every row; any output may be NULL
 cudaError_t launch_stats(const void* x, os_dtype in, float* m, float* d, float* lse, int64_t rows,
                          int cols, bool aligned, cudaStream_t stream);

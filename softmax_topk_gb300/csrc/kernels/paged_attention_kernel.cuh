@@ -1,0 +1,559 @@
+// paged_attention_kernel.cuh -- attention of one new token per sequence over a
+// paged key-value cache, split over the cache's length and joined.
+//
+// Per sequence b, key head h and query head of its group:
+//   s_j = scale q . k_j,  O = sum_j e^(s_j - m) v_j / l,  l = sum_j e^(s_j - m),
+//   L = m + ln l,  over the keys j < lengths[b] whose page is in the pool.
+//
+// A (b, h, up to 8 NT query heads) is a unit, 16 keys of it a block.  The blocks
+// of all units, laid end to end, are shared out evenly: every CTA gets a run of
+// them and every warp a run of the CTA's, whatever the sequences' lengths, so a
+// long sequence is split as far as the GPU is wide.  A unit that lies in one
+// warp's run is written by it; the pieces of one that does not are joined by
+// the CTA after its last block, and those of one that spans CTAs by the second
+// kernel, from the workspace, in the order of the keys: the same bits from call
+// to call.
+//
+// The products run on the tensor cores as S^T = K Q^T (16 keys x 8 heads) and
+// O^T = V^T P^T (D x 8 heads): eight query heads fill the narrow side, where
+// one query per sequence would leave 15 of 16 rows of the usual form empty.
+// Keys and values go from memory to the fragments' registers without a stop in
+// shared memory: the contraction's order is free, so a thread's 16 bytes of a
+// key row are its share of two steps, and of V the pairs of keys are put
+// together by byte permutes.  The next block's loads are issued as soon as the
+// registers are free.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "paged_common.cuh"
+
+namespace os {
+namespace paged {
+
+constexpr int kBlock = 16;  // keys per block
+// The running maximum is raised only when a score passes it by this much (in
+// bits), so weights stay below 2^8 and nearly every block skips the rescaling.
+constexpr float kSlack = 8.f;
+constexpr float kLn2f = 0.693147182f;
+
+struct AttnArgs {
+    const __nv_bfloat16* q;  // [seqs][q_stride], heads of D
+    const __nv_bfloat16* k;  // [pages][kv_heads][page_size][D]
+    const __nv_bfloat16* v;
+    const int* table;        // [seqs][width]
+    const int* lengths;      // [seqs]
+    __nv_bfloat16* out;      // [seqs][heads][D]
+    float* lse;              // [seqs][heads] or NULL
+    float* parts;            // workspace: two pieces per CTA
+    int4* tails;             // per CTA: unit that goes on behind it (or -1), CTAs that it goes on in
+    int64_t q_stride;
+    PageSplit split;
+    int seqs, width, pages, kv_heads;
+    int group, chunks, units;  // query heads per key head; their chunks; kv_heads * chunks
+    float scale_log2;          // scale * log2 e
+};
+
+template <int D, int NT>
+struct AttnShape {
+    static constexpr int kHeads = 8 * NT;  // query heads of a unit
+    // registers: 2 x 16 keys in flight, O^T and Q fragments
+    static constexpr int kWarps = D == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 16 : 12);
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kPiece = kHeads * D + 2 * kHeads;  // floats: O, m, l
+};
+
+template <int D, int NT>
+struct AttnShared {
+    using S = AttnShape<D, NT>;
+    float piece[S::kWarps][2][S::kPiece];
+    long long scan[S::kThreads];
+    long long warp_total[S::kWarps];
+    int unit[S::kWarps][2];  // unit of each piece or -1: [0] begun before the warp, [1] begun in it
+    long long end[S::kWarps];  // where the unit of piece [1] ends
+};
+
+__device__ __forceinline__ uint4 load_stream(const __nv_bfloat16* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+__device__ __forceinline__ float ex2f(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ int used_length(const AttnArgs& a, int b) {
+    const int len = __ldg(a.lengths + b);
+    return max(0, min(len, a.width * a.split.size));
+}
+
+// A place in the line of blocks: block j of unit u of sequence b.
+struct Cursor {
+    int b, u, j, blocks, len;
+    __device__ __forceinline__ void sequence(const AttnArgs& a) {
+        len = used_length(a, b);
+        blocks = (len + kBlock - 1) / kBlock;
+    }
+    __device__ __forceinline__ void next(const AttnArgs& a) {
+        if (++j < blocks) return;
+        j = 0;
+        if (++u < a.units) return;
+        u = 0;
+        do {
+            if (++b >= a.seqs) return;
+            sequence(a);
+        } while (blocks == 0);
+    }
+};
+
+// The pool's row of key 16 j + (lane mod 16), or -1: behind the length, or its
+// page is not in the pool.
+__device__ __forceinline__ int pool_row(const AttnArgs& a, const Cursor& c, int lane) {
+    const int key = c.j * kBlock + (lane & 15);
+    if (key >= c.len) return -1;
+    const int at = a.split.page(key);
+    const int page = __ldg(a.table + static_cast<int64_t>(c.b) * a.width + at);
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.pages)) return -1;
+    return (page * a.kv_heads + c.u / a.chunks) * a.split.size + key - at * a.split.size;
+}
+
+// One head's row of O, m and l: the result, rounded once.
+template <int D>
+__device__ __forceinline__ void store_lse(const AttnArgs& a, int64_t row, float m, float l) {
+    if (a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2f : -INFINITY;
+}
+
+// A piece's weight beside the joined maximum; a piece without keys has none.
+__device__ __forceinline__ float piece_weight(float m, float joined) {
+    return m == -INFINITY ? 0.f : ex2f(m - joined);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
+    paged_attention_kernel(const __grid_constant__ AttnArgs a) {
+    using S = AttnShape<D, NT>;
+    constexpr int kSteps = D / 32;   // pairs of contraction steps of Q K^T
+    constexpr int kTiles = D / 16;   // 16-row tiles of O^T
+    constexpr int kHalves = D / 64;  // 16-byte pieces of a V row per thread
+    extern __shared__ __align__(16) unsigned char raw[];
+    auto& sh = *reinterpret_cast<AttnShared<D, NT>*>(raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    // the join may be put in place while this grid works; it waits for its end
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    // ---- this warp's run of blocks
+    const int per_thread = (a.seqs + S::kThreads - 1) / S::kThreads;
+    const int first = tid * per_thread, last = min(a.seqs, first + per_thread);
+    long long mine = 0;
+    for (int b = first; b < last; ++b) mine += (used_length(a, b) + kBlock - 1) / kBlock;
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(kFullMask, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sh.warp_total[warp] = upto;
+    if (lane < 2) sh.unit[warp][lane] = -1;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < S::kWarps; ++w) {
+        if (w < warp) upto += sh.warp_total[w];
+        total += sh.warp_total[w];
+    }
+    sh.scan[tid] = upto;
+    __syncthreads();
+    total *= a.units;
+    // CTAs, then warps, take equal runs; the last ones may have none
+    const long long per_cta = (total + gridDim.x - 1) / gridDim.x;
+    const long long cta_begin = min(total, per_cta * blockIdx.x);
+    const long long cta_end = min(total, cta_begin + per_cta);
+    const long long per_warp = (cta_end - cta_begin + S::kWarps - 1) / S::kWarps;
+    const long long begin = min(cta_end, cta_begin + per_warp * warp);
+    const int n = static_cast<int>(min(cta_end, begin + per_warp) - begin);
+
+    // ---- sequences without keys
+    const int heads = a.kv_heads * a.group;
+    for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
+        if (used_length(a, b) > 0) continue;
+        for (int i = tid; i < heads * (D / 8); i += S::kThreads)
+            reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * heads * (D / 8) + i] =
+                make_uint4(0, 0, 0, 0);
+        for (int i = tid; a.lse && i < heads; i += S::kThreads)
+            a.lse[static_cast<int64_t>(b) * heads + i] = -INFINITY;
+    }
+
+    if (n > 0) {
+        Cursor cur;
+        long long unit_end;  // of the current unit, in the line
+        {
+            // the thread whose share of the sequences holds `begin`, then the sequence
+            int lo = 0, hi = S::kThreads - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                if (sh.scan[mid] * a.units > begin) hi = mid;
+                else lo = mid + 1;
+            }
+            long long before = lo > 0 ? sh.scan[lo - 1] * a.units : 0;
+            cur.b = lo * per_thread;
+            cur.sequence(a);
+            while (before + static_cast<long long>(cur.blocks) * a.units <= begin) {
+                before += static_cast<long long>(cur.blocks) * a.units;
+                ++cur.b;
+                cur.sequence(a);
+            }
+            const long long in = begin - before;
+            cur.u = static_cast<int>(in / cur.blocks);
+            cur.j = static_cast<int>(in % cur.blocks);
+            unit_end = begin - cur.j + cur.blocks;
+        }
+        Cursor ahead = cur;
+        uint4 kr[2][kSteps], vr[4][kHalves], q[NT][kSteps];
+        float o[NT][kTiles][4], m[NT][2], l[NT][2];
+
+        auto load_k = [&](int rows) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = __shfl_sync(kFullMask, rows, g + 8 * i);
+                if (row >= 0) {
+                    const __nv_bfloat16* p = a.k + static_cast<int64_t>(row) * D + 8 * t;
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) kr[i][s] = load_stream(p + 32 * s);
+                }
+            }
+        };
+        // values behind the length, or of no page, count as 0 (their weight is 0, and what
+        // memory holds there may be infinite or no number)
+        auto load_v = [&](int rows) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = __shfl_sync(kFullMask, rows, 2 * t + (i & 1) + 8 * (i >> 1));
+                const __nv_bfloat16* p = a.v + static_cast<int64_t>(row) * D + 8 * g;
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                    vr[i][h] = make_uint4(0, 0, 0, 0);
+                    if (row >= 0) vr[i][h] = load_stream(p + 64 * h);
+                }
+            }
+        };
+
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) kr[i][s] = make_uint4(0, 0, 0, 0);
+        int rows = pool_row(a, ahead, lane);
+        load_k(rows);
+        load_v(rows);
+        int rows_next = -1;
+        if (n > 1) {
+            ahead.next(a);
+            rows_next = pool_row(a, ahead, lane);
+        }
+        bool fresh = true;       // the block begins a unit, or the run
+        bool begun_here = cur.j == 0;
+        for (int i = 0; i < n; ++i) {
+            int rows_after = -1;
+            if (i + 2 < n) {
+                ahead.next(a);
+                rows_after = pool_row(a, ahead, lane);
+            }
+            if (fresh) {
+                const int h = cur.u / a.chunks, c = cur.u % a.chunks;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int head = c * S::kHeads + nt * 8 + g;
+                    const __nv_bfloat16* p =
+                        a.q + cur.b * a.q_stride + (h * a.group + head) * D + 8 * t;
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s)
+                        q[nt][s] = head < a.group ? *reinterpret_cast<const uint4*>(p + 32 * s)
+                                                  : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
+                    m[nt][0] = m[nt][1] = -INFINITY;
+                    l[nt][0] = l[nt][1] = 0.f;
+                }
+            }
+            // ---- scores, and the next block's keys asked for
+            float s[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st) {
+                    mma16816(s[nt], kr[0][st].x, kr[1][st].x, kr[0][st].y, kr[1][st].y,
+                             q[nt][st].x, q[nt][st].y);
+                    mma16816(s[nt], kr[0][st].z, kr[1][st].z, kr[0][st].w, kr[1][st].w,
+                             q[nt][st].z, q[nt][st].w);
+                }
+            }
+            const bool seen0 = __shfl_sync(kFullMask, rows, g) >= 0;
+            const bool seen1 = __shfl_sync(kFullMask, rows, g + 8) >= 0;
+            if (i + 1 < n) load_k(rows_next);
+            // ---- weights: s[nt] holds (key g, heads 2t, 2t+1), (key g + 8, the same)
+            bool raise = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[nt][e] = (e < 2 ? seen0 : seen1) ? s[nt][e] * a.scale_log2 : -INFINITY;
+                    raise |= s[nt][e] > m[nt][e & 1] + kSlack;
+                }
+            }
+            if (__any_sync(kFullMask, raise)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(s[nt][e], s[nt][e + 2]);
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1)
+                            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
+                        top = fmaxf(top, m[nt][e]);
+                        const float f = piece_weight(m[nt][e], top);
+                        m[nt][e] = top;
+                        l[nt][e] *= f;
+#pragma unroll
+                        for (int j = 0; j < kTiles; ++j) {
+                            o[nt][j][e] *= f;
+                            o[nt][j][e + 2] *= f;
+                        }
+                    }
+                }
+            }
+            // Weights as the sum of two bf16 numbers, one product each: 2^-17 of a
+            // weight, where one number would leave 2^-9 in every sum.
+            uint32_t p[NT][2], p_lo[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                // (nothing seen so far: the scores are -inf, the weights 0)
+                const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+                const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+                for (int i2 = 0; i2 < 2; ++i2) {
+                    const float w0 = ex2f(s[nt][2 * i2] - m0), w1 = ex2f(s[nt][2 * i2 + 1] - m1);
+                    l[nt][0] += w0;
+                    l[nt][1] += w1;
+                    const uint32_t w = pack_bf16(w0, w1);
+                    p[nt][i2] = transpose8x8(w);
+                    p_lo[nt][i2] = transpose8x8(pack_bf16(w0 - __uint_as_float(w << 16),
+                                                          w1 - __uint_as_float(w & 0xffff0000u)));
+                }
+            }
+            // ---- O^T += V^T P^T
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+                const int sel = j & 1 ? 0x7632 : 0x5410, w = j >> 1;
+                uint32_t av[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int key = (x >> 1) * 2;
+                    const int half = D == 128 ? x & 1 : 0, at = D == 128 ? w : w + 2 * (x & 1);
+                    av[x] = __byte_perm(word(vr[key][half], at), word(vr[key + 1][half], at), sel);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma16816(o[nt][j], av[0], av[1], av[2], av[3], p[nt][0], p[nt][1]);
+                    mma16816(o[nt][j], av[0], av[1], av[2], av[3], p_lo[nt][0], p_lo[nt][1]);
+                }
+            }
+            if (i + 1 < n) load_v(rows_next);
+            rows = rows_next;
+            rows_next = rows_after;
+            fresh = cur.j + 1 == cur.blocks;
+            if (fresh || i + 1 == n) {
+                // ---- the unit's last block, or the run's
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1)
+                            l[nt][e] += __shfl_xor_sync(kFullMask, l[nt][e], x);
+                const bool whole = fresh && begun_here;
+                const int slot = begun_here ? 1 : 0;
+                const int unit = cur.b * a.units + cur.u;
+                const int head0 = (cur.u % a.chunks) * S::kHeads;
+                const int64_t row0 = static_cast<int64_t>(cur.b) * heads +
+                                     (cur.u / a.chunks) * a.group + head0;
+                float* piece = sh.piece[warp][slot];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int head = nt * 8 + 2 * t + e;
+                        if (head0 + head >= a.group) continue;
+                        const float f = !whole ? 1.f : l[nt][e] > 0.f ? 1.f / l[nt][e] : 0.f;
+                        if (whole && g == 0) store_lse<D>(a, row0 + head, m[nt][e], l[nt][e]);
+                        if (!whole && g == 0) {
+                            piece[S::kHeads * D + head] = m[nt][e];
+                            piece[S::kHeads * D + S::kHeads + head] = l[nt][e];
+                        }
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h) {
+                            float v[8];
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                v[x] = f * (D == 128 ? o[nt][x % kTiles][2 * h + e]
+                                                     : o[nt][x & 3][2 * (x >> 2) + e]);
+                            const int d = 64 * h + 8 * g;
+                            if (whole) {
+                                *reinterpret_cast<uint4*>(a.out + (row0 + head) * D + d) =
+                                    make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                               pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+                            } else {
+                                float4* to = reinterpret_cast<float4*>(piece + head * D + d);
+                                to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                                to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                            }
+                        }
+                    }
+                }
+                if (!whole && lane == 0) {
+                    sh.unit[warp][slot] = unit;
+                    if (slot == 1) sh.end[warp] = unit_end;
+                }
+                begun_here = true;
+            }
+            if (i + 1 < n) {
+                cur.next(a);
+                if (fresh) unit_end = begin + i + 1 + cur.blocks;
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- pieces of units that warps share: the warp that began one joins it
+    bool tail = false;
+#pragma unroll 1
+    for (int slot = warp == 0 ? 0 : 1; slot < 2; ++slot) {
+        const int unit = sh.unit[warp][slot];
+        if (unit < 0) continue;
+        int parts = 1;  // this one and the next warps' first ones
+        while (warp + parts < S::kWarps && sh.unit[warp + parts][0] == unit) ++parts;
+        const bool open = slot == 0 || sh.end[warp] > cta_end;  // other CTAs have pieces too
+        tail |= slot == 1 && open;
+        float* to = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + slot) * S::kPiece;
+        const int b = unit / a.units, u = unit % a.units;
+        const int head0 = (u % a.chunks) * S::kHeads;
+        const int64_t row0 = static_cast<int64_t>(b) * heads + (u / a.chunks) * a.group + head0;
+#pragma unroll 1
+        for (int head = 0; head < min(S::kHeads, a.group - head0); ++head) {
+            float top = -INFINITY;
+            for (int i = 0; i < parts; ++i)
+                top = fmaxf(top, sh.piece[warp + i][i ? 0 : slot][S::kHeads * D + head]);
+            float sum = 0.f, acc[D / 32] = {};
+            for (int i = 0; i < parts; ++i) {
+                const float* from = sh.piece[warp + i][i ? 0 : slot];
+                const float f = piece_weight(from[S::kHeads * D + head], top);
+                sum += f * from[S::kHeads * D + S::kHeads + head];
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x)
+                    acc[x] += f * from[head * D + lane * (D / 32) + x];
+            }
+            if (open) {
+                for (int x = 0; x < D / 32; ++x) to[head * D + lane * (D / 32) + x] = acc[x];
+                if (lane == 0) {
+                    to[S::kHeads * D + head] = top;
+                    to[S::kHeads * D + S::kHeads + head] = sum;
+                }
+            } else {
+                const float f = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+                for (int x = 0; x < D / 32; x += 2)
+                    *reinterpret_cast<uint32_t*>(a.out + (row0 + head) * D + lane * (D / 32) + x) =
+                        pack_bf16(f * acc[x], f * acc[x + 1]);
+                if (lane == 0) store_lse<D>(a, row0 + head, top, sum);
+            }
+        }
+        if (tail && lane == 0)
+            a.tails[blockIdx.x] =
+                make_int4(unit, static_cast<int>((sh.end[warp] - 1) / per_cta) - blockIdx.x, 0, 0);
+    }
+    if (__syncthreads_or(tail) == 0 && tid == 0) a.tails[blockIdx.x] = make_int4(-1, 0, 0, 0);
+}
+
+// The units that span CTAs, one (CTA that began one, query head) per CTA here: the
+// pieces' sum weighted by their maxima, the warps taking every kJoinWarps-th.
+constexpr int kJoinWarps = 8;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    paged_join_kernel(const __grid_constant__ AttnArgs a) {
+    using S = AttnShape<D, NT>;
+    __shared__ float acc_sh[kJoinWarps][D], top_sh[kJoinWarps], sum_sh[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, head = blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 tail = a.tails[blockIdx.x];
+    if (tail.x < 0) return;
+    const int b = tail.x / a.units, u = tail.x % a.units;
+    const int head0 = (u % a.chunks) * S::kHeads;
+    if (head0 + head >= a.group) return;
+    const int parts = tail.y + 1;
+    float top = -INFINITY, sum = 0.f, acc[D / 32] = {};
+    for (int i = warp; i < parts; i += kJoinWarps) {
+        // the first is the second piece of the CTA that began it
+        const float* from = a.parts + (2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0)) * S::kPiece;
+        const float m = from[S::kHeads * D + head], l = from[S::kHeads * D + S::kHeads + head];
+        const float to = fmaxf(top, m);
+        const float f0 = piece_weight(top, to), f1 = piece_weight(m, to);
+        top = to;
+        sum = sum * f0 + l * f1;
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x)
+            acc[x] = acc[x] * f0 + from[head * D + lane * (D / 32) + x] * f1;
+    }
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) acc_sh[warp][lane * (D / 32) + x] = acc[x];
+    if (lane == 0) top_sh[warp] = top, sum_sh[warp] = sum;
+    __syncthreads();
+    const int d = threadIdx.x;
+    if (d >= D) return;
+    top = -INFINITY;
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, top_sh[w]);
+    float all = 0.f, value = 0.f;
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = piece_weight(top_sh[w], top);
+        all += f * sum_sh[w];
+        value += f * acc_sh[w][d];
+    }
+    const int64_t row = static_cast<int64_t>(b) * a.kv_heads * a.group +
+                        (u / a.chunks) * a.group + head0 + head;
+    a.out[row * D + d] = __float2bfloat16(all > 0.f ? value / all : 0.f);
+    if (d == 0) store_lse<D>(a, row, top, all);
+}
+
+}  // namespace paged
+}  // namespace os

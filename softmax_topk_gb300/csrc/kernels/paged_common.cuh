@@ -1,0 +1,31 @@
+// paged_common.cuh -- where a position of a sequence lies in a paged cache.
+#pragma once
+
+#include "ops.cuh"
+
+namespace os {
+namespace paged {
+
+// Position -> page of a sequence, slot in it.  Pages of 2^shift slots by a shift,
+// others (shift < 0) by the high half of a product with floor(2^64 / size) + 1,
+// exact for positions of 32 bits.
+struct PageSplit {
+    int size, shift;
+    unsigned long long magic;
+    __device__ __forceinline__ int page(int pos) const {
+        return shift >= 0 ? pos >> shift
+                          : static_cast<int>(
+                                __umul64hi(magic, static_cast<unsigned long long>(pos)));
+    }
+};
+
+inline PageSplit page_split(int size) {
+    PageSplit s = {size, -1, 0};
+    for (int i = 0; i < 31; ++i)
+        if (size == (1 << i)) s.shift = i;
+    if (s.shift < 0) s.magic = ~0ull / static_cast<unsigned>(size) + 1;
+    return s;
+}
+
+}  // namespace paged
+}  // namespace os
