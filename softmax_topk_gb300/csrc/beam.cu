@@ -1,4 +1,6 @@
 // Beam search's selection: the rows' runs, then the groups.
+#include <algorithm>
+
 #include "host_common.h"
 #include "internal.h"
 #include "kernels/beam_kernel.cuh"
@@ -17,7 +19,7 @@ struct Split {
 
 Split split_rows(int64_t rows, int64_t cols, os_dtype in, int sms) {
     const int64_t tiles = ceil_div(cols + (in == OS_F32 ? 3 : 7), beam::kTile);
-    const int64_t want = min64(min64(tiles, kMaxRuns), ceil_div(int64_t(sms) * 8, rows));
+    const int64_t want = min64(min64(tiles, kMaxRuns), std::max<int64_t>(1, int64_t(sms) * 6 / rows));
     Split s;
     s.run_tiles = ceil_div(tiles, want);
     s.runs = static_cast<int>(ceil_div(tiles, s.run_tiles));

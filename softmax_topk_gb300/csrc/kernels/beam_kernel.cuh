@@ -11,7 +11,8 @@
 // A run's K best: a bound that at least K of the tile's values reach is the least
 // of the maxima of K (or a few more) equal parts of the tile; the values that
 // reach it (some K ln K) go to a list in shared memory and are ranked by counting.
-// From then on a value has to pass the K-th of the list, which few do.
+// From then on a value has to pass the K-th of the list, which few do; every few
+// tiles the list is ranked again.
 //
 // Exact choices.  Values of different beams compare through their lse, which the
 // first kernel's fp32 sums give within eps (below).  Where two values of different
@@ -34,6 +35,7 @@ using u64 = unsigned long long;
 constexpr int kThreads = 256;   // of a run's CTA
 constexpr int kPer = 16;        // columns per thread and tile
 constexpr int kTile = kThreads * kPer;
+constexpr int kChunk = 4;       // tiles between two looks at the list
 constexpr int kList = 512;      // values that reach the bound; more go another way
 constexpr int kMergeThreads = 512;
 constexpr int kCandidates = 1024;
@@ -138,8 +140,7 @@ struct Tile {
     __device__ __forceinline__ int64_t col(int i) const {
         return base + (static_cast<int64_t>(i / kVec) * kThreads + threadIdx.x) * kVec + i % kVec;
     }
-    __device__ __forceinline__ void load(float (&v)[kPer]) const {
-        uint4 w[kBlocks];
+    __device__ __forceinline__ void fetch(uint4 (&w)[kBlocks]) const {
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
             const int64_t c = base + (static_cast<int64_t>(b) * kThreads + threadIdx.x) * kVec;
@@ -155,12 +156,66 @@ struct Tile {
                 w[b] = *reinterpret_cast<const uint4*>(e);
             }
         }
+    }
+    static __device__ __forceinline__ void values(const uint4 (&w)[kBlocks], float (&v)[kPer]) {
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
             const T* e = reinterpret_cast<const T*>(&w[b]);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) v[b * kVec + i] = widen(e[i]);
+            for (int i = 0; i < kVec; ++i) v[b * kVec + i] = static_cast<float>(e[i]);
         }
+    }
+};
+
+// NaN counts as -inf.
+__device__ __forceinline__ void clean(float (&v)[kPer]) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) v[e] = fmaxf(v[e], -INFINITY);
+}
+
+// A tile's share of the row's normalizer state, in the thread: m, and d + lost.  Values
+// that are no numbers are cleaned out of v.  Returns the values' maximum.
+struct State {
+    float m = -INFINITY, d = 0.f, lost = 0.f;
+
+    static __device__ __forceinline__ float weights(const float (&v)[kPer], float up) {
+        float part[4] = {};
+        if (fabsf(up) < 1e30f) {
+            // base-2 exponents with one rounding each, below the rounded maximum; the
+            // factor between it and the maximum comes at once
+            const float c = up * kLog2e;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) part[e & 3] += ex2f(fmaf(v[e], kLog2e, -c));
+            return ((part[0] + part[1]) + (part[2] + part[3])) * ex2f(fmaf(up, -kLog2e, c));
+        }
+        // a maximum of +-inf or near the largest number
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            part[e & 3] += v[e] == up ? 1.f : ex2f((v[e] - up) * kLog2e);
+        return (part[0] + part[1]) + (part[2] + part[3]);
+    }
+    __device__ __forceinline__ float add(float (&v)[kPer]) {
+        float top = fmaxf(v[0], -INFINITY);
+#pragma unroll
+        for (int e = 1; e < kPer; ++e) top = fmaxf(top, v[e]);
+        const float up = fmaxf(m, top);
+        if (up == -INFINITY) return top;
+        if (up > m) {
+            const float f = factor(m, up);
+            d *= f;
+            lost *= f;
+            m = up;
+        }
+        float sum = weights(v, up);
+        if (!(sum == sum)) {
+            clean(v);
+            sum = weights(v, up);
+        }
+        // the running sum keeps what its rounding loses
+        const float s = d + sum;
+        lost += d >= sum ? (d - s) + sum : (sum - s) + d;
+        d = s;
+        return top;
     }
 };
 
@@ -179,8 +234,48 @@ __device__ __forceinline__ int rank_list(RunShared& sh, int n, int K) {
     return left;
 }
 
+// The same for any number of values (many may be equal): the best in turn, of the sorted
+// list's `held` keys and a tile.
+template <typename T>
+__device__ __noinline__ int best_in_turn(RunShared& sh, const Tile<T> tile, int held, int K) {
+    const int tid = threadIdx.x;
+    uint4 w[Tile<T>::kBlocks];
+    float v[kPer];
+    tile.fetch(w);
+    Tile<T>::values(w, v);
+    clean(v);
+    const u64 before = tid < held ? sh.sorted[tid] : 0;
+    u64 below = ~0ull;
+    int k = 0;
+    __syncthreads();
+    for (; k < K; ++k) {
+        u64 best = before < below ? before : 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const u64 key = make_key(v[e], tile.col(e));
+            if (v[e] > -INFINITY && key < below && key > best) best = key;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const u64 other = __shfl_xor_sync(kFullMask, best, o);
+            best = other > best ? other : best;
+        }
+        if (tid % 32 == 0) sh.best[tid / 32] = best;
+        __syncthreads();
+        for (int i = 0; i < kThreads / 32; ++i) best = max(best, sh.best[i]);
+        __syncthreads();
+        if (best == 0) break;
+        if (tid == 0) sh.sorted[k] = best;
+        below = best;
+    }
+    __syncthreads();
+    if (tid < k) sh.list[tid] = sh.sorted[tid];
+    return k;
+}
+
 template <typename T, int KP>
-__global__ void __launch_bounds__(kThreads) beam_runs_kernel(const __grid_constant__ BeamArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+    beam_runs_kernel(const __grid_constant__ BeamArgs a) {
     __shared__ RunShared sh;
     const int64_t row = blockIdx.x / a.runs;
     const int run = static_cast<int>(blockIdx.x % a.runs);
@@ -191,105 +286,71 @@ __global__ void __launch_bounds__(kThreads) beam_runs_kernel(const __grid_consta
     tile.row = static_cast<const T*>(a.x) + row * a.cols;
     tile.cols = a.cols;
     const int head = static_cast<int>(reinterpret_cast<uintptr_t>(tile.row) % 16 / sizeof(T));
-    float m = -INFINITY, d = 0.f, lost = 0.f;
+    State state;
     int held = 0;  // keys in the list, best first
     const int64_t tiles = (a.cols + head + kTile - 1) / kTile;
     const int64_t first = run * a.run_tiles, last = min(tiles, first + a.run_tiles);
-#pragma unroll 1
-    for (int64_t i = first; i < last; ++i) {
-        tile.base = i * kTile - head;
-        float v[kPer];
-        tile.load(v);
-        if (tid == 0) sh.count = held;
-        float top = v[0];
-#pragma unroll
-        for (int e = 1; e < kPer; ++e) top = fmaxf(top, v[e]);
-        // ---- (m, d): weights below the thread's running maximum
-        const float up = fmaxf(m, top);
-        if (up > -INFINITY) {
-            float sum;
-            if (fabsf(up) < 1e30f) {
-                // base-2 exponents with one rounding each, below the rounded
-                // maximum; the factor between it and the maximum comes at once
-                const float c = up * kLog2e;
-                float part[4] = {};
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) part[e & 3] += ex2f(fmaf(v[e], kLog2e, -c));
-                sum = ((part[0] + part[1]) + (part[2] + part[3])) * ex2f(fmaf(up, -kLog2e, c));
-            } else {
-                // a maximum of +-inf or near the largest number
-                sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e)
-                    sum += v[e] == up ? 1.f : ex2f((v[e] - up) * kLog2e);
-            }
-            const float f = factor(m, up);
-            d *= f;
-            lost *= f;
-            m = up;
-            // the running sum keeps what its rounding loses
-            const float s = d + sum;
-            lost += d >= sum ? (d - s) + sum : (sum - s) + d;
-            d = s;
+    uint4 w[Tile<T>::kBlocks];
+    float v[kPer];
+    auto place = [&](int64_t i) { tile.base = i * kTile - head; };
+    // the next tile's values are asked for before this one's are worked on
+    auto step = [&](int64_t i) {
+        Tile<T>::values(w, v);
+        if (i + 1 < last) {
+            place(i + 1);
+            tile.fetch(w);
         }
-        // ---- the K best so far
-        uint32_t bound;
-        if (held < a.K)
-            bound = parts_bound<KP, kThreads>(order_key(top), sh.bound,
-                                              [](uint32_t x, uint32_t y) { return max(x, y); });
-        else
-            bound = static_cast<uint32_t>(sh.list[a.K - 1] >> 32) + 1;
-        bound = max(bound, sample::kKeyNegInf + 1);
-        const bool any = order_key(top) >= bound;
-        if (!__syncthreads_or(any)) continue;
-        if (any) {
+        place(i);
+        return order_key(state.add(v));
+    };
+    auto push = [&](uint32_t bound) {
 #pragma unroll
-            for (int e = 0; e < kPer; ++e)
-                if (order_key(v[e]) >= bound) {
-                    const int at = atomicAdd(&sh.count, 1);
-                    if (at < kList) sh.list[at] = make_key(v[e], tile.col(e));
-                }
+        for (int e = 0; e < kPer; ++e)
+            if (order_key(v[e]) >= bound) {
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < kList) sh.list[at] = make_key(v[e], tile.col(e));
+            }
+    };
+    if (tid == 0) sh.count = 0;
+    if (first < last) {
+        place(first);
+        tile.fetch(w);
+    }
+#pragma unroll 1
+    for (int64_t i = first; i < last;) {
+        // until the list is full a tile's own bound, from then on the K-th of the list
+        const bool full = held == a.K;
+        const int64_t end = full ? min(last, i + kChunk) : i + 1;
+        uint32_t bound = full ? static_cast<uint32_t>(sh.list[a.K - 1] >> 32) + 1 : 0;
+#pragma unroll 1
+        for (int64_t j = i; j < end; ++j) {
+            const uint32_t top = step(j);
+            if (!full)
+                bound = max(parts_bound<KP, kThreads>(
+                                top, sh.bound, [](uint32_t x, uint32_t y) { return max(x, y); }),
+                            sample::kKeyNegInf + 1);
+            if (top >= bound) push(bound);
         }
         __syncthreads();
         const int n = sh.count;
-        if (n <= kList) {
-            held = rank_list(sh, n, a.K);
-        } else {
-            // many equal values: the best in turn, from the tile and the old list
-            u64 mine_before = tid < held ? sh.sorted[tid] : 0, below = ~0ull;
-            int k = 0;
-            __syncthreads();
-            for (; k < a.K; ++k) {
-                u64 best = mine_before < below ? mine_before : 0;
+        if (n > held) {
+            if (n <= kList) {
+                held = rank_list(sh, n, a.K);
+            } else {
 #pragma unroll 1
-                for (int e = 0; e < kPer; ++e) {
-                    float x = v[0];
-#pragma unroll
-                    for (int j = 1; j < kPer; ++j) x = j == e ? v[j] : x;
-                    const u64 key = make_key(x, tile.col(e));
-                    if (x > -INFINITY && key < below && key > best) best = key;
+                for (int64_t j = i; j < end; ++j) {
+                    place(j);
+                    held = best_in_turn(sh, tile, held, a.K);
                 }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const u64 other = __shfl_xor_sync(kFullMask, best, o);
-                    best = other > best ? other : best;
-                }
-                if (lane == 0) sh.best[warp] = best;
-                __syncthreads();
-                for (int w = 0; w < kThreads / 32; ++w) best = max(best, sh.best[w]);
-                __syncthreads();
-                if (best == 0) break;
-                if (tid == 0) sh.sorted[k] = best;
-                below = best;
             }
-            __syncthreads();
-            held = k;
-            if (tid < held) sh.list[tid] = sh.sorted[tid];
         }
         __syncthreads();
+        if (tid == 0) sh.count = held;
+        __syncthreads();
+        i = end;
     }
+    float m = state.m, d = state.d + state.lost;
     // ---- the run's state
-    d += lost;
     float top = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
@@ -314,25 +375,35 @@ __global__ void __launch_bounds__(kThreads) beam_runs_kernel(const __grid_consta
 
 // ------------------------------------------------------------------ the groups
 struct MergeShared {
-    double value[kCandidates];
-    uint32_t beam[kCandidates], col[kCandidates];
-    double best[kMaxK];             // the chosen, in order
-    uint32_t best_beam[kMaxK], best_col[kMaxK];
-    double offset[kMaxBeams];       // score - lse + m
+    u64 order[kCandidates], at[kCandidates];  // of a value; beam and column
+    u64 best[kMaxK], best_at[kMaxK];          // the chosen, in order
+    double offset[kMaxBeams];       // score - lse, to add to x - m
+    double lse[kMaxBeams];          // ln of the summed weights
+    double m64[kMaxBeams];
     double score[kMaxBeams];
     float m[kMaxBeams];
     unsigned char kind[kMaxBeams];  // 0 no candidates, 1 a row, 2 ended
     unsigned char again[kMaxBeams]; // its sum is wanted in 38 bits
-    double bound[128];
-    double warp_value[kMergeThreads / 32];
-    u64 warp_at[kMergeThreads / 32];
+    u64 bound[128];
+    u64 warp_order[kMergeThreads / 32], warp_at[kMergeThreads / 32];
     u64 sum[kMergeThreads / 32];
     float pow2[64];
     int count;
 };
 
-// (value, place) pairs: larger value first, then the lower place
-__device__ __forceinline__ bool better(double c, u64 at, double c2, u64 at2) {
+// Doubles as integers of their order: 64-bit comparisons on the integer pipe (the
+// FP64 pipe takes one per SM and cycle or so).  No NaN comes here.
+__device__ __forceinline__ u64 order64(double v) {
+    const u64 b = static_cast<u64>(__double_as_longlong(v + 0.0));
+    return b >> 63 ? ~b : b | (1ull << 63);
+}
+__device__ __forceinline__ double value64(u64 o) {
+    return __longlong_as_double(static_cast<long long>(o >> 63 ? o & ~(1ull << 63) : ~o));
+}
+constexpr u64 kNone = 0x000fffffffffffffull;  // order64(-inf)
+
+// (order, place) pairs: larger value first, then the lower place
+__device__ __forceinline__ bool better(u64 c, u64 at, u64 c2, u64 at2) {
     return c > c2 || (c == c2 && at < at2);
 }
 
@@ -390,18 +461,13 @@ __global__ void __launch_bounds__(kMergeThreads)
             // ln d by parts: the power of two's share is exact in 64 bits
             const int e = d > 0.f ? ilogbf(d) : 0;
             const double ln_d = static_cast<double>(logf(scalbnf(d, -e))) + e * 0.6931471805599453;
-            sh.offset[i] = sh.score[i] - ln_d;
+            sh.lse[i] = ln_d;
+            sh.m64[i] = top;
         }
     }
     const int lists = a.beams * a.runs;
     const double eps = a.eps;
-    // candidate e of list j: its value, or -inf where there is none
-    auto value = [&](u64 key, int beam) -> double {
-        if (sh.kind[beam] == 2) return key ? sh.score[beam] : -INFINITY;
-        if (key == 0) return -INFINITY;
-        const float x = key_value(static_cast<uint32_t>(key >> 32)), m = sh.m[beam];
-        return sh.offset[beam] + (x == m ? 0.0 : static_cast<double>(x) - static_cast<double>(m));
-    };
+    // entry e of list j (a beam's run): its key, 0 where there is none
     auto key_of = [&](int list, int e) -> u64 {
         const int beam = list / a.runs;
         if (sh.kind[beam] == 1) return a.lists[((row0 + beam) * a.runs + list % a.runs) * a.K + e];
@@ -409,86 +475,91 @@ __global__ void __launch_bounds__(kMergeThreads)
         return sh.kind[beam] == 2 && list % a.runs == 0 && e == 0
                    ? (1ull << 63) | (0xffffffffu - static_cast<uint32_t>(a.pad)) : 0;
     };
+    auto order_of = [&](u64 key, int beam) -> u64 {
+        if (key == 0) return kNone;
+        if (sh.kind[beam] == 2) return order64(sh.score[beam]);
+        const float x = key_value(static_cast<uint32_t>(key >> 32));
+        if (sh.m[beam] == INFINITY) return x == INFINITY ? order64(sh.offset[beam]) : kNone;
+        return order64(sh.offset[beam] + (static_cast<double>(x) - sh.m64[beam]));
+    };
+    auto at_of = [](u64 key, int beam) {
+        return (static_cast<u64>(beam) << 32) | (0xffffffffu - static_cast<uint32_t>(key));
+    };
     int found = 0;
     for (int round = 0; round < 2; ++round) {
         __syncthreads();
         if (tid == 0) sh.count = 0;
-        // ---- a bound that K of the lists' first values reach
-        double top = -INFINITY;
-        for (int j = tid; j < lists; j += kMergeThreads) {
-            const double c = value(key_of(j, 0), j / a.runs);
-            top = c > top ? c : top;
-        }
-        double bound = parts_bound<KP, kMergeThreads>(
-            top, sh.bound, [](double x, double y) { return x > y ? x : y; });
-        // (one that the errors may have put below another is not lost)
-        if (round == 0) bound -= 4 * eps;
+        for (int i = tid; i < a.beams; i += kMergeThreads)
+            if (sh.kind[i] == 1)
+                sh.offset[i] = sh.score[i] - sh.lse[i];
         __syncthreads();
+        // ---- a bound that K of the lists' first entries reach, dealt out to the parts in turn
+        u64 top = kNone;
+        {
+            constexpr int kPart = kMergeThreads / KP;
+            const int all = max(lists, min(kMergeThreads, lists * a.K));
+            for (int i = tid / kPart + KP * (tid % kPart); i < all; i += kMergeThreads) {
+                const u64 c = order_of(key_of(i % lists, i / lists), i % lists / a.runs);
+                top = c > top ? c : top;
+            }
+        }
+        u64 bound = parts_bound<KP, kMergeThreads>(top, sh.bound,
+                                                   [](u64 x, u64 y) { return x > y ? x : y; });
+        // (one that the errors may have put below another is not lost)
+        if (round == 0 && bound > kNone) bound = order64(value64(bound) - 4 * eps);
+        if (bound == kNone) ++bound;
         for (int i = tid; i < lists * a.K; i += kMergeThreads) {
             const int list = i / a.K, beam = list / a.runs;
             const u64 key = key_of(list, i % a.K);
-            const double c = value(key, beam);
-            if (c > -INFINITY && c >= bound) {
+            const u64 c = order_of(key, beam);
+            if (c >= bound) {
                 const int at = atomicAdd(&sh.count, 1);
                 if (at < kCandidates) {
-                    sh.value[at] = c;
-                    sh.beam[at] = beam;
-                    sh.col[at] = 0xffffffffu - static_cast<uint32_t>(key);
+                    sh.order[at] = c;
+                    sh.at[at] = at_of(key, beam);
                 }
             }
         }
         __syncthreads();
-        const int n = sh.count, want = a.K;
+        const int n = sh.count;
         if (n <= kCandidates) {
             for (int i = tid; i < n; i += kMergeThreads) {
-                const double c = sh.value[i];
-                const u64 at = (static_cast<u64>(sh.beam[i]) << 32) | sh.col[i];
+                const u64 c = sh.order[i], at = sh.at[i];
                 int rank = 0;
-                for (int j = 0; j < n; ++j)
-                    rank += better(sh.value[j], (static_cast<u64>(sh.beam[j]) << 32) | sh.col[j],
-                                   c, at);
-                if (rank < want) {
+                for (int j = 0; j < n; ++j) rank += better(sh.order[j], sh.at[j], c, at);
+                if (rank < a.K) {
                     sh.best[rank] = c;
-                    sh.best_beam[rank] = sh.beam[i];
-                    sh.best_col[rank] = sh.col[i];
+                    sh.best_at[rank] = at;
                 }
             }
-            found = min(n, want);
+            found = min(n, a.K);
         } else {
             // many equal values: the best of what is left in turn
-            double c0 = INFINITY;
-            u64 at0 = 0;
-            for (found = 0; found < want; ++found) {
-                double c1 = -INFINITY;
-                u64 at1 = ~0ull;
+            u64 c0 = ~0ull, at0 = 0;
+            for (found = 0; found < a.K; ++found) {
+                u64 c1 = kNone, at1 = ~0ull;
                 for (int i = tid; i < lists * a.K; i += kMergeThreads) {
                     const int beam = i / a.K / a.runs;
                     const u64 key = key_of(i / a.K, i % a.K);
-                    const double c = value(key, beam);
-                    const u64 at = (static_cast<u64>(beam) << 32) |
-                                   (0xffffffffu - static_cast<uint32_t>(key));
-                    if (c > -INFINITY && (found == 0 || better(c0, at0, c, at)) &&
+                    const u64 c = order_of(key, beam), at = at_of(key, beam);
+                    if (c > kNone && (found == 0 || better(c0, at0, c, at)) &&
                         better(c, at, c1, at1))
                         c1 = c, at1 = at;
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) {
-                    const double c = __shfl_xor_sync(kFullMask, c1, o);
+                    const u64 c = __shfl_xor_sync(kFullMask, c1, o);
                     const u64 at = __shfl_xor_sync(kFullMask, at1, o);
                     if (better(c, at, c1, at1)) c1 = c, at1 = at;
                 }
-                if (lane == 0) sh.warp_value[warp] = c1, sh.warp_at[warp] = at1;
+                if (lane == 0) sh.warp_order[warp] = c1, sh.warp_at[warp] = at1;
                 __syncthreads();
                 for (int w = 0; w < kMergeThreads / 32; ++w)
-                    if (better(sh.warp_value[w], sh.warp_at[w], c1, at1))
-                        c1 = sh.warp_value[w], at1 = sh.warp_at[w];
+                    if (better(sh.warp_order[w], sh.warp_at[w], c1, at1))
+                        c1 = sh.warp_order[w], at1 = sh.warp_at[w];
                 __syncthreads();
-                if (!(c1 > -INFINITY)) break;
-                if (tid == 0) {
-                    sh.best[found] = c1;
-                    sh.best_beam[found] = static_cast<uint32_t>(at1 >> 32);
-                    sh.best_col[found] = static_cast<uint32_t>(at1);
-                }
+                if (c1 == kNone) break;
+                if (tid == 0) sh.best[found] = c1, sh.best_at[found] = at1;
                 c0 = c1, at0 = at1;
             }
         }
@@ -497,43 +568,42 @@ __global__ void __launch_bounds__(kMergeThreads)
         // ---- values of different beams that the sums cannot tell apart: neighbours in the
         // order, and of what is not chosen all that come near the last chosen
         bool near = false;
-        auto mark = [&](uint32_t b0, uint32_t b1) {
+        auto mark = [&](u64 at0, u64 at1) {
+            const uint32_t b0 = at0 >> 32, b1 = at1 >> 32;
             if (b0 == b1) return;
             near = true;
             sh.again[b0] = sh.again[b1] = 1;
         };
         for (int i = tid; i + 1 < found; i += kMergeThreads)
-            if (sh.best[i] - sh.best[i + 1] <= 2 * eps) mark(sh.best_beam[i], sh.best_beam[i + 1]);
-        const uint32_t last_beam = sh.best_beam[found - 1];
-        const u64 last_at = (static_cast<u64>(last_beam) << 32) | sh.best_col[found - 1];
-        const double last = sh.best[found - 1];
-        auto behind = [&](double c, uint32_t beam, uint32_t col) {
-            if (c >= last - 2 * eps && better(last, last_at, c, (static_cast<u64>(beam) << 32) | col))
-                mark(last_beam, beam);
+            if (value64(sh.best[i]) - value64(sh.best[i + 1]) <= 2 * eps)
+                mark(sh.best_at[i], sh.best_at[i + 1]);
+        const u64 last = sh.best[found - 1], last_at = sh.best_at[found - 1];
+        const u64 low = order64(value64(last) - 2 * eps);
+        auto behind = [&](u64 c, u64 at) {
+            if (c >= low && better(last, last_at, c, at)) mark(last_at, at);
         };
         if (n <= kCandidates)
-            for (int i = tid; i < n; i += kMergeThreads) behind(sh.value[i], sh.beam[i], sh.col[i]);
+            for (int i = tid; i < n; i += kMergeThreads) behind(sh.order[i], sh.at[i]);
         else
             for (int i = tid; i < lists * a.K; i += kMergeThreads) {
-                const u64 key = key_of(i / a.K, i % a.K);
                 const int beam = i / a.K / a.runs;
-                const double c = value(key, beam);
-                if (c > -INFINITY) behind(c, beam, 0xffffffffu - static_cast<uint32_t>(key));
+                const u64 key = key_of(i / a.K, i % a.K);
+                if (key) behind(order_of(key, beam), at_of(key, beam));
             }
         if (!__syncthreads_or(near)) break;
         for (int b = 0; b < a.beams; ++b) {
             if (!sh.again[b] || sh.kind[b] != 1 || sh.m[b] == INFINITY) continue;
             const double log_sum = exact_log_sum(
                 sh, static_cast<const T*>(a.x) + (row0 + b) * a.cols, a.cols, sh.m[b]);
-            if (tid == 0) sh.offset[b] = sh.score[b] - log_sum;
+            if (tid == 0) sh.lse[b] = log_sum;
         }
     }
     if (tid < a.K) {
         const bool is = tid < found;
         const int64_t at = static_cast<int64_t>(blockIdx.x) * a.K + tid;
-        a.out[at] = is ? static_cast<float>(sh.best[tid]) : -INFINITY;
-        a.parents[at] = is ? static_cast<int>(sh.best_beam[tid]) : -1;
-        a.tokens[at] = is ? static_cast<int>(sh.best_col[tid]) : -1;
+        a.out[at] = is ? static_cast<float>(value64(sh.best[tid])) : -INFINITY;
+        a.parents[at] = is ? static_cast<int>(sh.best_at[tid] >> 32) : -1;
+        a.tokens[at] = is ? static_cast<int>(sh.best_at[tid] & 0xffffffffu) : -1;
     }
 }
 

@@ -17,11 +17,10 @@
 // The products run on the tensor cores as S^T = K Q^T (16 keys x 8 heads) and
 // O^T = V^T P^T (D x 8 heads): eight query heads fill the narrow side, where
 // one query per sequence would leave 15 of 16 rows of the usual form empty.
-// Keys and values go from memory to the fragments' registers without a stop in
-// shared memory: the contraction's order is free, so a thread's 16 bytes of a
-// key row are its share of two steps, and of V the pairs of keys are put
-// together by byte permutes.  The next block's loads are issued as soon as the
-// registers are free.
+//
+// Every warp has a ring of its own in shared memory, filled by asynchronous copies
+// of 16 bytes, K and V of two blocks ahead of the one it works on: the rows of a
+// block may lie in 16 different pages, and no warp waits for another.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -59,45 +58,65 @@ struct AttnArgs {
 template <int D, int NT>
 struct AttnShape {
     static constexpr int kHeads = 8 * NT;  // query heads of a unit
-    // registers: 2 x 16 keys in flight, O^T and Q fragments
-    static constexpr int kWarps = D == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 16 : 12);
+    static constexpr int kWarps = 8;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kPiece = kHeads * D + 2 * kHeads;  // floats: O, m, l
+    static constexpr int kRow = D * 2;               // bytes of a key
+    static constexpr int kSide = kBlock * kRow;      // K or V of a block
+    static constexpr int kAhead = 2;                 // blocks asked for ahead
+    static constexpr int kHeadStride = D + 4;        // of a piece: spreads the heads over the banks
+    static constexpr int kPiece = kHeads * kHeadStride + 2 * kHeads;  // floats: O, m, l
+    static constexpr int kM = kHeads * kHeadStride, kL = kM + kHeads;
 };
 
 template <int D, int NT>
 struct AttnShared {
     using S = AttnShape<D, NT>;
-    float piece[S::kWarps][2][S::kPiece];
+    unsigned char ring[S::kWarps][S::kAhead][2][S::kSide];  // K, V of a block
+    float head[S::kWarps][S::kPiece];  // the piece of a unit begun before the warp
     long long scan[S::kThreads];
     long long warp_total[S::kWarps];
     int unit[S::kWarps][2];  // unit of each piece or -1: [0] begun before the warp, [1] begun in it
     long long end[S::kWarps];  // where the unit of piece [1] ends
+    // The piece that the warp began lies in its ring, which is empty when it is written.
+    __device__ __forceinline__ float* piece(int warp, int which) {
+        static_assert(S::kPiece * sizeof(float) <= sizeof(ring[0]), "a piece fits the ring");
+        return which ? reinterpret_cast<float*>(ring[warp]) : head[warp];
+    }
 };
 
-__device__ __forceinline__ uint4 load_stream(const __nv_bfloat16* p) {
-    uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-    return r;
+// 16 bytes to shared memory; zeros where `there` is false (nothing is read then).
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool there) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;"
+                 :: "r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+template <bool TRANS>
+__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t at) {
+    if constexpr (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
-}
-
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
-    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -162,9 +181,10 @@ template <int D, int NT>
 __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ AttnArgs a) {
     using S = AttnShape<D, NT>;
-    constexpr int kSteps = D / 32;   // pairs of contraction steps of Q K^T
-    constexpr int kTiles = D / 16;   // 16-row tiles of O^T
-    constexpr int kHalves = D / 64;  // 16-byte pieces of a V row per thread
+    constexpr int kTiles = D / 16;    // contraction steps of K Q^T, 16-row tiles of O^T
+    constexpr int kChunks = D / 8;    // 16-byte pieces of a row
+    constexpr int kLanesRow = kChunks;             // lanes that copy one row
+    constexpr int kRowsAtOnce = 32 / kLanesRow;
     extern __shared__ __align__(16) unsigned char raw[];
     auto& sh = *reinterpret_cast<AttnShared<D, NT>*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -238,52 +258,47 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
             unit_end = begin - cur.j + cur.blocks;
         }
         Cursor ahead = cur;
-        uint4 kr[2][kSteps], vr[4][kHalves], q[NT][kSteps];
+        uint32_t q[NT][kTiles][2];
         float o[NT][kTiles][4], m[NT][2], l[NT][2];
-
-        auto load_k = [&](int rows) {
+        const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(sh.ring[warp]));
+        uint32_t place = ring;  // of the current block
+        // K or V of 16 rows; a row's 16-byte pieces change places with its low bits, so that
+        // the same piece of eight rows lies in different banks.  Rows that are not there are
+        // zeros: their weights are 0, and what memory holds there may be no number.
+        auto fetch = [&](const __nv_bfloat16* pool, uint32_t to, int rows) {
+            const int chunk = lane % kLanesRow, r0 = lane / kLanesRow;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int row = __shfl_sync(kFullMask, rows, g + 8 * i);
-                if (row >= 0) {
-                    const __nv_bfloat16* p = a.k + static_cast<int64_t>(row) * D + 8 * t;
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) kr[i][s] = load_stream(p + 32 * s);
-                }
-            }
-        };
-        // values behind the length, or of no page, count as 0 (their weight is 0, and what
-        // memory holds there may be infinite or no number)
-        auto load_v = [&](int rows) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = __shfl_sync(kFullMask, rows, 2 * t + (i & 1) + 8 * (i >> 1));
-                const __nv_bfloat16* p = a.v + static_cast<int64_t>(row) * D + 8 * g;
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                    vr[i][h] = make_uint4(0, 0, 0, 0);
-                    if (row >= 0) vr[i][h] = load_stream(p + 64 * h);
-                }
+            for (int i = 0; i < kBlock / kRowsAtOnce; ++i) {
+                const int r = r0 + i * kRowsAtOnce;
+                const int row = __shfl_sync(kFullMask, rows, r);
+                copy_async(to + r * S::kRow + ((chunk ^ (r & 7)) * 16),
+                           pool + static_cast<int64_t>(max(row, 0)) * D + chunk * 8, row >= 0);
             }
         };
 
+        // rows of the blocks up to kAhead behind the current one
+        int rows[S::kAhead + 1];
+        rows[0] = pool_row(a, ahead, lane);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 1; i <= S::kAhead; ++i) {
+            rows[i] = -1;
+            if (i < n) {
+                ahead.next(a);
+                rows[i] = pool_row(a, ahead, lane);
+            }
+        }
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) kr[i][s] = make_uint4(0, 0, 0, 0);
-        int rows = pool_row(a, ahead, lane);
-        load_k(rows);
-        load_v(rows);
-        int rows_next = -1;
-        if (n > 1) {
-            ahead.next(a);
-            rows_next = pool_row(a, ahead, lane);
+        for (int i = 0; i < S::kAhead; ++i) {
+            if (i < n) fetch(a.k, ring + 2 * i * S::kSide, rows[i]);
+            copy_commit();
+            if (i < n) fetch(a.v, ring + (2 * i + 1) * S::kSide, rows[i]);
+            copy_commit();
         }
         bool fresh = true;       // the block begins a unit, or the run
         bool begun_here = cur.j == 0;
         for (int i = 0; i < n; ++i) {
             int rows_after = -1;
-            if (i + 2 < n) {
+            if (i + S::kAhead + 1 < n) {
                 ahead.next(a);
                 rows_after = pool_row(a, ahead, lane);
             }
@@ -293,35 +308,51 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
                 for (int nt = 0; nt < NT; ++nt) {
                     const int head = c * S::kHeads + nt * 8 + g;
                     const __nv_bfloat16* p =
-                        a.q + cur.b * a.q_stride + (h * a.group + head) * D + 8 * t;
+                        a.q + cur.b * a.q_stride + (h * a.group + head) * D + 2 * t;
 #pragma unroll
-                    for (int s = 0; s < kSteps; ++s)
-                        q[nt][s] = head < a.group ? *reinterpret_cast<const uint4*>(p + 32 * s)
-                                                  : make_uint4(0, 0, 0, 0);
+                    for (int j = 0; j < kTiles; ++j) {
 #pragma unroll
-                    for (int j = 0; j < kTiles; ++j)
+                        for (int e = 0; e < 2; ++e)
+                            q[nt][j][e] = head < a.group ? *reinterpret_cast<const uint32_t*>(
+                                                               p + 16 * j + 8 * e)
+                                                         : 0u;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
+                    }
                     m[nt][0] = m[nt][1] = -INFINITY;
                     l[nt][0] = l[nt][1] = 0.f;
                 }
             }
-            // ---- scores, and the next block's keys asked for
-            float s[NT][4];
+            // ---- scores (two sums that take turns: half the wait for each other)
+            copy_wait<2 * S::kAhead - 1>();
+            __syncwarp();
+            float s[NT][4], s_odd[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int st = 0; st < kSteps; ++st) {
-                    mma16816(s[nt], kr[0][st].x, kr[1][st].x, kr[0][st].y, kr[1][st].y,
-                             q[nt][st].x, q[nt][st].y);
-                    mma16816(s[nt], kr[0][st].z, kr[1][st].z, kr[0][st].w, kr[1][st].w,
-                             q[nt][st].z, q[nt][st].w);
+                for (int e = 0; e < 4; ++e) s[nt][e] = s_odd[nt][e] = 0.f;
+            {
+                const int r = lane & 15;
+                const uint32_t at = place + r * S::kRow;
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) {
+                    uint32_t kf[4];
+                    load_matrices<false>(kf, at + (((2 * j + (lane >> 4)) ^ (r & 7)) * 16));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816(j & 1 ? s_odd[nt] : s[nt], kf, q[nt][j][0], q[nt][j][1]);
                 }
             }
-            const bool seen0 = __shfl_sync(kFullMask, rows, g) >= 0;
-            const bool seen1 = __shfl_sync(kFullMask, rows, g + 8) >= 0;
-            if (i + 1 < n) load_k(rows_next);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[nt][e] += s_odd[nt][e];
+            // K of a later block into this one's place
+            __syncwarp();
+            if (i + S::kAhead < n) fetch(a.k, place, rows[S::kAhead]);
+            copy_commit();
+            const bool seen0 = __shfl_sync(kFullMask, rows[0], g) >= 0;
+            const bool seen1 = __shfl_sync(kFullMask, rows[0], g + 8) >= 0;
             // ---- weights: s[nt] holds (key g, heads 2t, 2t+1), (key g + 8, the same)
             bool raise = false;
 #pragma unroll
@@ -372,26 +403,31 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
                                                           w1 - __uint_as_float(w & 0xffff0000u)));
                 }
             }
-            // ---- O^T += V^T P^T
+            // ---- O^T += V^T P^T, and V of a later block
+            copy_wait<2 * S::kAhead - 1>();
+            __syncwarp();
+            {
+                const int r = (lane & 7) + 8 * (lane >> 4);
+                const uint32_t at = place + S::kSide + r * S::kRow;
 #pragma unroll
-            for (int j = 0; j < kTiles; ++j) {
-                const int sel = j & 1 ? 0x7632 : 0x5410, w = j >> 1;
-                uint32_t av[4];
+                for (int j = 0; j < kTiles; ++j) {
+                    uint32_t vf[4];
+                    load_matrices<true>(vf, at + (((2 * j + ((lane >> 3) & 1)) ^ (r & 7)) * 16));
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int key = (x >> 1) * 2;
-                    const int half = D == 128 ? x & 1 : 0, at = D == 128 ? w : w + 2 * (x & 1);
-                    av[x] = __byte_perm(word(vr[key][half], at), word(vr[key + 1][half], at), sel);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma16816(o[nt][j], av[0], av[1], av[2], av[3], p[nt][0], p[nt][1]);
-                    mma16816(o[nt][j], av[0], av[1], av[2], av[3], p_lo[nt][0], p_lo[nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma16816(o[nt][j], vf, p[nt][0], p[nt][1]);
+                        mma16816(o[nt][j], vf, p_lo[nt][0], p_lo[nt][1]);
+                    }
                 }
             }
-            if (i + 1 < n) load_v(rows_next);
-            rows = rows_next;
-            rows_next = rows_after;
+            __syncwarp();
+            if (i + S::kAhead < n) fetch(a.v, place + S::kSide, rows[S::kAhead]);
+            copy_commit();
+            place += 2 * S::kSide;
+            if (place == ring + 2 * S::kAhead * S::kSide) place = ring;
+#pragma unroll
+            for (int x = 0; x < S::kAhead; ++x) rows[x] = rows[x + 1];
+            rows[S::kAhead] = rows_after;
             fresh = cur.j + 1 == cur.blocks;
             if (fresh || i + 1 == n) {
                 // ---- the unit's last block, or the run's
@@ -403,12 +439,12 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
                         for (int x = 4; x < 32; x <<= 1)
                             l[nt][e] += __shfl_xor_sync(kFullMask, l[nt][e], x);
                 const bool whole = fresh && begun_here;
-                const int slot = begun_here ? 1 : 0;
+                const int which = begun_here ? 1 : 0;
                 const int unit = cur.b * a.units + cur.u;
                 const int head0 = (cur.u % a.chunks) * S::kHeads;
                 const int64_t row0 = static_cast<int64_t>(cur.b) * heads +
                                      (cur.u / a.chunks) * a.group + head0;
-                float* piece = sh.piece[warp][slot];
+                float* piece = sh.piece(warp, which);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -418,32 +454,23 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
                         const float f = !whole ? 1.f : l[nt][e] > 0.f ? 1.f / l[nt][e] : 0.f;
                         if (whole && g == 0) store_lse<D>(a, row0 + head, m[nt][e], l[nt][e]);
                         if (!whole && g == 0) {
-                            piece[S::kHeads * D + head] = m[nt][e];
-                            piece[S::kHeads * D + S::kHeads + head] = l[nt][e];
+                            piece[S::kM + head] = m[nt][e];
+                            piece[S::kL + head] = l[nt][e];
                         }
 #pragma unroll
-                        for (int h = 0; h < kHalves; ++h) {
-                            float v[8];
+                        for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                v[x] = f * (D == 128 ? o[nt][x % kTiles][2 * h + e]
-                                                     : o[nt][x & 3][2 * (x >> 2) + e]);
-                            const int d = 64 * h + 8 * g;
-                            if (whole) {
-                                *reinterpret_cast<uint4*>(a.out + (row0 + head) * D + d) =
-                                    make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                               pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-                            } else {
-                                float4* to = reinterpret_cast<float4*>(piece + head * D + d);
-                                to[0] = make_float4(v[0], v[1], v[2], v[3]);
-                                to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                            for (int x = 0; x < 2; ++x) {
+                                const int d = 16 * j + 8 * x + g;
+                                const float v = f * o[nt][j][2 * x + e];
+                                if (whole) a.out[(row0 + head) * D + d] = __float2bfloat16(v);
+                                else piece[head * S::kHeadStride + d] = v;
                             }
-                        }
                     }
                 }
                 if (!whole && lane == 0) {
-                    sh.unit[warp][slot] = unit;
-                    if (slot == 1) sh.end[warp] = unit_end;
+                    sh.unit[warp][which] = unit;
+                    if (which == 1) sh.end[warp] = unit_end;
                 }
                 begun_here = true;
             }
@@ -473,21 +500,21 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
         for (int head = 0; head < min(S::kHeads, a.group - head0); ++head) {
             float top = -INFINITY;
             for (int i = 0; i < parts; ++i)
-                top = fmaxf(top, sh.piece[warp + i][i ? 0 : slot][S::kHeads * D + head]);
+                top = fmaxf(top, sh.piece(warp + i, i ? 0 : slot)[S::kM + head]);
             float sum = 0.f, acc[D / 32] = {};
             for (int i = 0; i < parts; ++i) {
-                const float* from = sh.piece[warp + i][i ? 0 : slot];
-                const float f = piece_weight(from[S::kHeads * D + head], top);
-                sum += f * from[S::kHeads * D + S::kHeads + head];
+                const float* from = sh.piece(warp + i, i ? 0 : slot);
+                const float f = piece_weight(from[S::kM + head], top);
+                sum += f * from[S::kL + head];
 #pragma unroll
                 for (int x = 0; x < D / 32; ++x)
-                    acc[x] += f * from[head * D + lane * (D / 32) + x];
+                    acc[x] += f * from[head * S::kHeadStride + lane * (D / 32) + x];
             }
             if (open) {
-                for (int x = 0; x < D / 32; ++x) to[head * D + lane * (D / 32) + x] = acc[x];
+                for (int x = 0; x < D / 32; ++x) to[head * S::kHeadStride + lane * (D / 32) + x] = acc[x];
                 if (lane == 0) {
-                    to[S::kHeads * D + head] = top;
-                    to[S::kHeads * D + S::kHeads + head] = sum;
+                    to[S::kM + head] = top;
+                    to[S::kL + head] = sum;
                 }
             } else {
                 const float f = sum > 0.f ? 1.f / sum : 0.f;
@@ -522,18 +549,33 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     const int head0 = (u % a.chunks) * S::kHeads;
     if (head0 + head >= a.group) return;
     const int parts = tail.y + 1;
+    // the first piece is the second one of the CTA that began the unit
+    auto piece = [&](int i) {
+        return a.parts + (2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0)) * S::kPiece;
+    };
     float top = -INFINITY, sum = 0.f, acc[D / 32] = {};
-    for (int i = warp; i < parts; i += kJoinWarps) {
-        // the first is the second piece of the CTA that began it
-        const float* from = a.parts + (2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0)) * S::kPiece;
-        const float m = from[S::kHeads * D + head], l = from[S::kHeads * D + S::kHeads + head];
-        const float to = fmaxf(top, m);
-        const float f0 = piece_weight(top, to), f1 = piece_weight(m, to);
-        top = to;
-        sum = sum * f0 + l * f1;
+    for (int i0 = warp; i0 < parts; i0 += 32 * kJoinWarps) {
+        // a lane's maximum and weight each, then the rows
+        const int mine = i0 + lane * kJoinWarps;
+        const float m = mine < parts ? piece(mine)[S::kM + head] : -INFINITY;
+        const float l = mine < parts ? piece(mine)[S::kL + head] : 0.f;
+        float to = fmaxf(top, m);
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x)
-            acc[x] = acc[x] * f0 + from[head * D + lane * (D / 32) + x] * f1;
+        for (int o = 16; o > 0; o >>= 1) to = fmaxf(to, __shfl_xor_sync(kFullMask, to, o));
+        const float f0 = piece_weight(top, to), f = piece_weight(m, to);
+        top = to;
+        sum *= f0;
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) acc[x] *= f0;
+        const int here = min(32, (parts - i0 + kJoinWarps - 1) / kJoinWarps);
+#pragma unroll 4
+        for (int i = 0; i < here; ++i) {
+            const float w = __shfl_sync(kFullMask, f, i);
+            sum += w * __shfl_sync(kFullMask, l, i);
+            const float* from = piece(i0 + i * kJoinWarps) + head * S::kHeadStride + lane * (D / 32);
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) acc[x] += w * from[x];
+        }
     }
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) acc_sh[warp][lane * (D / 32) + x] = acc[x];
