@@ -29,6 +29,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libos_softmax.so")
@@ -102,7 +103,7 @@ def _load() -> ctypes.CDLL:
                                   ctypes.c_float, st, vp]
     lib.os_route_bwd.argtypes = [vp, vp, vp, vp, i64, i64, i32, st, i32, ctypes.c_float, st, vp]
     lib.os_sample.argtypes = [vp, vp, ctypes.POINTER(Sampling), vp, vp, i64, i64, st, vp]
-    cache, p64 = ctypes.POINTER(PagedCache), ctypes.POINTER(ctypes.c_int64)
+    cache, p64 = vp, ctypes.POINTER(ctypes.c_int64)  # cache: a PagedCache or its bytes
     lib.os_paged_append.argtypes = [cache, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, i32, i32,
                                     i32, vp]
     lib.os_paged_attention.argtypes = [cache, vp, i64, vp, vp, vp, i32, ctypes.c_float, vp]
@@ -627,38 +628,61 @@ def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, prob=
     return out, prob
 
 
+_POOL = struct.Struct("4P3q3i4x")  # os_paged_cache, as bytes (a third of the Structure's time)
+
+
 def _paged_cache(k_cache, v_cache, table, lengths, dims=4):
-    """The os_paged_cache of these tensors, whose kinds and shapes it checks."""
+    """The os_paged_cache of these tensors, whose kinds and shapes it checks: (its bytes, the
+    device's index, seqs, kv_heads, head_dim)."""
     import torch
     bf16, i32 = torch.bfloat16, torch.int32
-    if not k_cache.is_cuda or k_cache.dtype != bf16 or not k_cache.is_contiguous() or \
-            k_cache.dim() != dims:
+    shape, dev = k_cache.shape, k_cache.get_device()
+    if dev < 0 or k_cache.dtype is not bf16 or len(shape) != dims or not k_cache.is_contiguous():
         raise ValueError("k_cache must be a contiguous bf16 CUDA tensor "
                          f"{'[layers, ' if dims == 5 else '['}pages, kv_heads, page_size, head_dim]")
     if table.dim() != 2:
         raise ValueError("table must be int32 [seqs, width]")
-    pages, kv_heads, page_size, head_dim = k_cache.shape[-4:]
     seqs, width = table.shape
-    dev = k_cache.device
-    _like("v_cache", v_cache, k_cache.shape, bf16, dev)
-    _like("table", table, (seqs, width), i32, dev)
-    _like("lengths", lengths, (seqs,), i32, dev)
-    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(),
-                      pages, seqs, width, _int32(kv_heads), _int32(page_size), _int32(head_dim))
+    # one condition for what is nearly always so; then, which it was
+    if v_cache.shape != shape or v_cache.dtype is not bf16 or v_cache.get_device() != dev or \
+            not v_cache.is_contiguous() or table.dtype is not i32 or table.get_device() != dev or \
+            not table.is_contiguous() or lengths.dtype is not i32 or lengths.dim() != 1 or \
+            lengths.get_device() != dev or lengths.numel() != seqs or not lengths.is_contiguous():
+        device = k_cache.device
+        _like("v_cache", v_cache, shape, bf16, device)
+        _like("table", table, (seqs, width), i32, device)
+        _like("lengths", lengths, (seqs,), i32, device)
+    kv_heads, page_size, head_dim = shape[-3:]
+    return _POOL.pack(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(),
+                      shape[-4], seqs, width, _int32(kv_heads), _int32(page_size),
+                      _int32(head_dim)), dev, seqs, kv_heads, head_dim
 
 
-def _heads(name, t, rows, heads, head_dim, device):
-    """The distance between the rows of `t` [rows, heads, head_dim], bf16, each row contiguous."""
-    import torch
-    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != device or t.shape[0] != rows or \
-            t.shape[1] != heads or t.shape[2] != head_dim:
-        raise ValueError(f"{name} must be a bf16 tensor of shape {(rows, heads, head_dim)} "
-                         f"on {device}")
+def _heads(name, t, shape, dtype, dev):
+    """The distance between the rows of `t`, bf16 [rows, heads, head_dim], each row contiguous."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on the cache's "
+                         "device")
     row, step, one = t.stride()
-    if t.numel() and ((one != 1) or (heads > 1 and step != head_dim)):
+    rows, heads, head_dim = shape
+    if step == head_dim and one == 1 and rows > 1:
+        return row
+    if t.numel() and (one != 1 or (heads > 1 and step != head_dim)):
         raise ValueError(f"{name}'s rows must be contiguous")
-    # (a single row has no distance)
+    # (a single row has no distance, nor has an empty tensor)
     return row if rows > 1 and t.numel() else heads * head_dim
+
+
+def _call_on(index, name, fn, *args):
+    """fn(*args, torch's current stream on device `index`), with that device current."""
+    import torch
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with _OnDevice(torch.device("cuda", index)):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _check(status, name)
 
 
 def paged_append(k_cache, v_cache, table, lengths, k, v, q=None, starts=None, inv_freq=None,
@@ -676,32 +700,32 @@ def paged_append(k_cache, v_cache, table, lengths, k, v, q=None, starts=None, in
     pairs (f, f + rot / 2), or neighbours with ``interleaved``; without it nothing is rotated.
     A sequence of length 0 takes no part, nor do rows outside ``starts``."""
     import torch
-    cache = _paged_cache(k_cache, v_cache, table, lengths)
-    dev, tokens = k_cache.device, k.shape[0]
-    k_stride = _heads("k", k, tokens, cache.kv_heads, cache.head_dim, dev)
-    v_stride = _heads("v", v, tokens, cache.kv_heads, cache.head_dim, dev)
-    q_heads = q_stride = 0
+    bf16 = torch.bfloat16
+    cache, dev, seqs, kv_heads, head_dim = _paged_cache(k_cache, v_cache, table, lengths)
+    shape = (k.shape[0], kv_heads, head_dim)
+    k_stride, v_stride = _heads("k", k, shape, bf16, dev), _heads("v", v, shape, bf16, dev)
+    q_at = q_out_at = starts_at = freq_at = None
+    q_heads = q_stride = rot = 0
     if q is not None:
         q_heads = q.shape[1] if q.dim() == 3 else 0
-        q_stride = _heads("q", q, tokens, q_heads, cache.head_dim, dev)
-        shape = (tokens, q_heads, cache.head_dim)
+        shape = (shape[0], q_heads, head_dim)
+        q_stride = _heads("q", q, shape, bf16, dev)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            q_out = torch.empty(shape, dtype=bf16, device=k_cache.device)
         else:
-            _like("q_out", q_out, shape, torch.bfloat16, dev)
+            _like("q_out", q_out, shape, bf16, k_cache.device)
+        q_at, q_out_at = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rot = 0
     if starts is not None:
-        _like("starts", starts, (cache.seqs + 1,), torch.int32, dev)
+        starts_at = _like("starts", starts, (seqs + 1,), torch.int32, k_cache.device).data_ptr()
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        _like("inv_freq", inv_freq, (rot // 2,), torch.float32, dev)
-    _call(dev, "os_paged_append", _lib.os_paged_append, ctypes.byref(cache), k.data_ptr(), k_stride,
-          v.data_ptr(), v_stride, None if q is None else q.data_ptr(), q_stride,
-          None if q is None else q_out.data_ptr(), None if starts is None else starts.data_ptr(),
-          None if inv_freq is None else inv_freq.data_ptr(), tokens, _int32(q_heads), _int32(rot),
-          int(interleaved))
+        freq_at = _like("inv_freq", inv_freq, (rot // 2,), torch.float32,
+                        k_cache.device).data_ptr()
+    _call_on(dev, "os_paged_append", _lib.os_paged_append, cache, k.data_ptr(), k_stride,
+             v.data_ptr(), v_stride, q_at, q_stride, q_out_at, starts_at, freq_at, shape[0],
+             _int32(q_heads), _int32(rot), 1 if interleaved else 0)
     return q_out
 
 
@@ -717,29 +741,27 @@ def paged_attention(q, k_cache, v_cache, table, lengths, scale: float | None = N
     a sequence without keys gets 0 and -inf.  L is None when ``want_lse`` is false.  ``workspace`` is a buffer of
     ``os_paged_attention_workspace`` bytes (allocated when not given)."""
     import torch
-    cache = _paged_cache(k_cache, v_cache, table, lengths)
-    dev = k_cache.device
-    seqs, head_dim = cache.seqs, cache.head_dim
-    q_heads = q.shape[1] if q.dim() == 3 else 0
-    q_stride = _heads("q", q, seqs, q_heads, head_dim, dev)
-    shape = (seqs, q_heads, head_dim)
+    bf16 = torch.bfloat16
+    cache, dev, seqs, _, head_dim = _paged_cache(k_cache, v_cache, table, lengths)
+    device = k_cache.device
+    shape = (seqs, q.shape[1] if q.dim() == 3 else 0, head_dim)
+    q_stride = _heads("q", q, shape, bf16, dev)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=bf16, device=device)
     else:
-        _like("out", out, shape, torch.bfloat16, dev)
+        _like("out", out, shape, bf16, device)
     if lse is not None:
-        _like("lse", lse, shape[:2], torch.float32, dev)
+        _like("lse", lse, shape[:2], torch.float32, device)
     elif want_lse:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
-    need = _attention_workspace.get(dev.index)
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=device)
+    need = _attention_workspace.get(dev)
     if need is None:
-        with _OnDevice(dev):
-            need = _attention_workspace[dev.index] = os_paged_attention_workspace()
-    workspace = _workspace(workspace, need, dev)
-    _call(dev, "os_paged_attention", _lib.os_paged_attention, ctypes.byref(cache), q.data_ptr(),
-          q_stride, out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-          _int32(q_heads),
-          1.0 / head_dim ** 0.5 if scale is None else float(scale))
+        with _OnDevice(device):
+            need = _attention_workspace[dev] = os_paged_attention_workspace()
+    workspace = _workspace(workspace, need, device)
+    _call_on(dev, "os_paged_attention", _lib.os_paged_attention, cache, q.data_ptr(), q_stride,
+             out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+             _int32(shape[1]), 1.0 / head_dim ** 0.5 if scale is None else float(scale))
     return out, lse
 
 
@@ -763,28 +785,33 @@ def paged_reorder(k_cache, v_cache, table, lengths, parents, out_table, out_leng
     dimension of layers.  Returns (out_table, out_lengths), the latter the parents' lengths.  A
     parent outside the group leaves a sequence's row as it is, with length 0."""
     import torch
-    cache = _paged_cache(k_cache, v_cache, table, lengths, 5 if k_cache.dim() == 5 else 4)
-    dev, i32 = k_cache.device, torch.int32
+    layers = k_cache.shape[0] if k_cache.dim() == 5 else None
+    cache, dev, seqs, _, _ = _paged_cache(k_cache, v_cache, table, lengths,
+                                          4 if layers is None else 5)
+    i32 = torch.int32
     if parents.dim() != 2:
         raise ValueError("parents must be int32 [groups, beams]")
     groups, beams = parents.shape
-    if groups * beams != cache.seqs:
+    if groups * beams != seqs:
         raise ValueError("groups * beams must be the table's sequences")
-    _like("parents", parents, (groups, beams), i32, dev)
-    _like("out_table", out_table, (cache.seqs, cache.width), i32, dev)
+    device = k_cache.device
+    _like("parents", parents, (groups, beams), i32, device)
+    _like("out_table", out_table, table.shape, i32, device)
     if out_lengths is None:
-        out_lengths = torch.empty(cache.seqs, dtype=i32, device=dev)
+        out_lengths = torch.empty(seqs, dtype=i32, device=device)
     else:
-        _like("out_lengths", out_lengths, (cache.seqs,), i32, dev)
-    _call(dev, "os_paged_reorder", _lib.os_paged_reorder, ctypes.byref(cache), parents.data_ptr(),
-          out_table.data_ptr(), out_lengths.data_ptr(), _int32(max(beams, 1)),
-          _int32(k_cache.shape[0]) if k_cache.dim() == 5 else 1)
+        _like("out_lengths", out_lengths, (seqs,), i32, device)
+    _call_on(dev, "os_paged_reorder", _lib.os_paged_reorder, cache, parents.data_ptr(),
+             out_table.data_ptr(), out_lengths.data_ptr(), _int32(max(beams, 1)),
+             1 if layers is None else _int32(layers))
     return out_table, out_lengths
 
 
 @functools.lru_cache(maxsize=256)
-def _beam_workspace(device_index, groups, beams, cols, K, code):
-    return os_beam_select_workspace(groups, beams, cols, K, code)
+def _beam_workspace(index, groups, beams, cols, K, code):
+    import torch
+    with _OnDevice(torch.device("cuda", index)):
+        return os_beam_select_workspace(groups, beams, cols, K, code)
 
 
 def beam_select(x, scores, K: int | None = None, ended=None, pad: int = 0, out=None, parents=None,
@@ -802,33 +829,27 @@ def beam_select(x, scores, K: int | None = None, ended=None, pad: int = 0, out=N
         raise ValueError("scores must be float32 [groups, beams]")
     code = _dtype_code(x.dtype)
     groups, beams = scores.shape
-    cols, dev, f32, i32 = x.shape[1], x.device, torch.float32, torch.int32
-    if x.shape[0] != groups * beams:
+    rows, cols = x.shape
+    device, dev, f32, i32 = x.device, x.get_device(), torch.float32, torch.int32
+    if rows != groups * beams:
         raise ValueError("x must have a row for each of the scores")
-    _like("scores", scores, (groups, beams), f32, dev)
+    _like("scores", scores, (groups, beams), f32, device)
     if ended is not None:
-        _like("ended", ended, (groups, beams), torch.bool, dev)
+        ended = _like("ended", ended, (groups, beams), torch.bool, device).data_ptr()
     K = beams if K is None else K
-    need = _beam_workspace(dev.index, groups, beams, cols, _int32(K), code) \
-        if torch.cuda.current_device() == dev.index else _on(dev, os_beam_select_workspace, groups,
-                                                             beams, cols, _int32(K), code)
+    need = _beam_workspace(dev, groups, beams, cols, _int32(K), code)
     shape = (groups, K)
-    out = torch.empty(shape, dtype=f32, device=dev) if out is None else \
-        _like("out", out, shape, f32, dev)
-    parents = torch.empty(shape, dtype=i32, device=dev) if parents is None else \
-        _like("parents", parents, shape, i32, dev)
-    tokens = torch.empty(shape, dtype=i32, device=dev) if tokens is None else \
-        _like("tokens", tokens, shape, i32, dev)
-    workspace = _workspace(workspace, need, dev)
-    _call(dev, "os_beam_select", _lib.os_beam_select, x.data_ptr(), scores.data_ptr(),
-          None if ended is None else ended.data_ptr(), out.data_ptr(), parents.data_ptr(),
-          tokens.data_ptr(), workspace.data_ptr(), groups, beams, cols, K, _int32(pad), code)
+    out = torch.empty(shape, dtype=f32, device=device) if out is None else \
+        _like("out", out, shape, f32, device)
+    parents = torch.empty(shape, dtype=i32, device=device) if parents is None else \
+        _like("parents", parents, shape, i32, device)
+    tokens = torch.empty(shape, dtype=i32, device=device) if tokens is None else \
+        _like("tokens", tokens, shape, i32, device)
+    workspace = _workspace(workspace, need, device)
+    _call_on(dev, "os_beam_select", _lib.os_beam_select, x.data_ptr(), scores.data_ptr(), ended,
+             out.data_ptr(), parents.data_ptr(), tokens.data_ptr(), workspace.data_ptr(), groups,
+             beams, cols, K, _int32(pad), code)
     return out, parents, tokens
-
-
-def _on(device, fn, *args):
-    with _OnDevice(device):
-        return fn(*args)
 
 
 def exp(z, pairs: bool = False, coarse: bool = False):

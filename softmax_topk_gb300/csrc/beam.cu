@@ -18,8 +18,9 @@ struct Split {
 };
 
 Split split_rows(int64_t rows, int64_t cols, os_dtype in, int sms) {
-    const int64_t tiles = ceil_div(cols + (in == OS_F32 ? 3 : 7), beam::kTile);
-    const int64_t want = min64(min64(tiles, kMaxRuns), std::max<int64_t>(1, int64_t(sms) * 6 / rows));
+    const int64_t tiles = in == OS_F32 ? ceil_div(cols + 3, beam::Tile<float>::kTile)
+                                       : ceil_div(cols + 7, beam::Tile<__nv_bfloat16>::kTile);
+    const int64_t want = min64(min64(tiles, kMaxRuns), std::max<int64_t>(1, (int64_t(sms) * 3 + rows / 2) / rows));
     Split s;
     s.run_tiles = ceil_div(tiles, want);
     s.runs = static_cast<int>(ceil_div(tiles, s.run_tiles));
@@ -28,11 +29,16 @@ Split split_rows(int64_t rows, int64_t cols, os_dtype in, int sms) {
 
 template <typename T, int KP>
 cudaError_t launch(const beam::BeamArgs& a, int64_t groups, cudaStream_t stream) {
-    const cudaError_t e = launch_kernel(beam::beam_runs_kernel<T, KP>, groups * a.beams * a.runs,
-                                        beam::kThreads, 1, 0, stream, a);
+    auto runs = beam::beam_runs_kernel<T, KP>;
+    constexpr int smem = sizeof(beam::RunShared<T>);
+    if (!prepare_kernel(runs, 1, smem)) return cudaErrorInvalidConfiguration;
+    const cudaError_t e =
+        launch_behind(runs, dim3(static_cast<unsigned>(groups * a.beams * a.runs)), beam::kThreads,
+                      1, smem, stream, a);
     if (e != cudaSuccess) return e;
-    return launch_behind(beam::beam_merge_kernel<T, KP>, dim3(static_cast<unsigned>(groups)),
-                         beam::kMergeThreads, stream, a);
+    return launch_behind(beam::beam_merge_kernel<T, KP>,
+                         dim3(static_cast<unsigned>(groups * a.helpers)), beam::kMergeThreads,
+                         a.helpers, 0, stream, a);
 }
 
 template <typename T>
@@ -67,9 +73,12 @@ cudaError_t launch_beam_select(const BeamSelectArgs& p, cudaStream_t stream) {
     a.beams = p.beams;
     a.K = p.K;
     a.runs = s.runs;
-    a.run_tiles = s.run_tiles;
+    a.run_tiles = static_cast<int>(s.run_tiles);
     a.pad = p.pad;
-    a.eps = static_cast<float>(40 + 2 * s.run_tiles) * 0x1p-23f;
+    // the CTAs of a group share the exact sums, where there are SMs for them
+    a.helpers = beam::kHelpers;
+    while (a.helpers > 1 && p.groups * a.helpers > 2 * dev->sms) a.helpers /= 2;
+    a.eps = 36 * 0x1p-23f;
     return p.in == OS_F32 ? launch_k<float>(a, p.groups, stream)
                           : launch_k<__nv_bfloat16>(a, p.groups, stream);
 }

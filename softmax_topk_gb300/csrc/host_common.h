@@ -62,17 +62,22 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), int64_t grid, int threads, i
 // (griddepcontrol.launch_dependents); it waits for that one's end itself
 // (griddepcontrol.wait) before it touches what that one wrote.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_behind(void (*kernel)(KArgs...), dim3 grid, int threads, cudaStream_t stream,
-                          Args... args) {
+cudaError_t launch_behind(void (*kernel)(KArgs...), dim3 grid, int threads, int cluster, int smem,
+                          cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 

@@ -8,20 +8,22 @@
 // are all that can matter.  The second, one CTA per group, joins the runs' states
 // into lse and ranks the runs' lists by c.
 //
-// A run's K best: a bound that at least K of the tile's values reach is the least
-// of the maxima of K (or a few more) equal parts of the tile; the values that
-// reach it (some K ln K) go to a list in shared memory and are ranked by counting.
-// From then on a value has to pass the K-th of the list, which few do; every few
-// tiles the list is ranked again.
+// A run's K best: every thread keeps the largest value of its columns of each tile
+// (64 bytes; one store).  At the end of the run a bound that at least K values reach is
+// the least of the largest values of K (or a few more) equal parts of the threads;
+// the shares that reach it (some K ln K) are read again, their values that reach it go
+// to a list in shared memory, and the list is ranked by counting.  So the pass over
+// memory has no branch, no barrier and no atomic for the selection.
 //
 // Exact choices.  Values of different beams compare through their lse, which the
-// first kernel's fp32 sums give within eps (below).  Where two values of different
+// first kernel's fp32 sums give within eps.  Where two values of different
 // beams next to one another in the order, up to the first that is not chosen,
 // are nearer than both errors, the rows of these beams are summed again with the
-// sampler's weights (38 bits, added as integers) and the order is taken from those
-// sums in 64 bits.
+// sampler's weights (38 bits, added as integers), by the CTAs of a cluster, and the
+// order is taken from those sums in 64 bits.
 #pragma once
 
+#include "paged_common.cuh"
 #include "sample_kernel.cuh"
 
 namespace os {
@@ -33,11 +35,12 @@ using sample::widen;
 using u64 = unsigned long long;
 
 constexpr int kThreads = 256;   // of a run's CTA
-constexpr int kPer = 16;        // columns per thread and tile
-constexpr int kTile = kThreads * kPer;
-constexpr int kChunk = 4;       // tiles between two looks at the list
+constexpr int kBlocks = 4;      // 16-byte blocks per thread and tile
+constexpr int kSegmentCols = 1 << 16;  // columns between two selections
 constexpr int kList = 512;      // values that reach the bound; more go another way
-constexpr int kMergeThreads = 512;
+constexpr int kGroups = 512;    // threads' shares of a tile that do
+constexpr int kMergeThreads = 256;
+constexpr int kHelpers = 8;     // CTAs of a group, at most
 constexpr int kCandidates = 1024;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxK = 64;
@@ -50,11 +53,12 @@ struct BeamArgs {
     float* out;                    // [groups][K]
     int* parents;
     int* tokens;
-    u64* lists;                    // [groups * beams][runs][K]: keys, best first, 0 behind them
+    u64* lists;                    // [groups][K][beams * runs]: the runs' keys, best first, then 0
     float2* states;                // [groups * beams][runs]: m, d
     int64_t cols;
     int beams, K, runs;
-    int64_t run_tiles;             // tiles of a run
+    int run_tiles;                 // tiles of a run
+    int helpers;                   // CTAs of a group
     int pad;
     float eps;                     // bound of lse's error
 };
@@ -65,8 +69,8 @@ __device__ __forceinline__ bool has_row(const BeamArgs& a, int64_t row) {
 }
 
 // value and column in one number: larger is better, no two alike, 0 is none
-__device__ __forceinline__ u64 make_key(float x, int64_t col) {
-    return (static_cast<u64>(order_key(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(col));
+__device__ __forceinline__ u64 make_key(float x, uint32_t col) {
+    return (static_cast<u64>(order_key(x)) << 32) | (0xffffffffu - col);
 }
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -117,115 +121,174 @@ __device__ __forceinline__ V parts_bound(V v, V* sh, Max larger) {
     return least;
 }
 
+// Tiles on their way to a CTA, what it keeps of them, and its list: 70 KB for fp32, 62 for
+// bf16, so that three CTAs fit an SM.
+template <typename T>
 struct RunShared {
+    static constexpr int kStages = 3;
+    static constexpr int kSegment = kSegmentCols / (kThreads * kBlocks * 16 / int(sizeof(T)));
+    uint4 tile[kStages][kBlocks][kThreads];
+    float top[kSegment][kThreads];  // the largest of a thread's columns of a tile
     u64 list[kList];
     u64 sorted[kMaxK];
     uint32_t bound[128];
     u64 best[kThreads / 32];
     float m[kThreads / 32], d[kThreads / 32];
-    int count;
+    uint16_t group[kGroups];
+    int count, groups;
 };
 
 // Columns of the tile's thread, as 16-byte blocks: value i of the thread belongs
 // to column col(i).  Rows start anywhere, so block 0 is the aligned one that the
 // row's first column lies in; a block that the row covers in part is read by elements.
+// Columns count modulo 2^32: what lies before the row is past its end.
 template <typename T>
 struct Tile {
     static constexpr int kVec = 16 / sizeof(T);
-    static constexpr int kBlocks = kPer / kVec;
+    static constexpr int kPer = kBlocks * kVec;  // columns per thread
+    static constexpr int kTile = kThreads * kPer;
     const T* row;
-    int64_t cols, base;  // base: first column of the tile's block 0 (may be below 0)
-    int head;            // columns between the row's start and the block boundary before it
+    uint32_t cols, base;  // base: column of the thread's first value
 
-    __device__ __forceinline__ int64_t col(int i) const {
-        return base + (static_cast<int64_t>(i / kVec) * kThreads + threadIdx.x) * kVec + i % kVec;
+    __device__ __forceinline__ uint32_t col(int i) const {
+        return base + (i / kVec) * (kThreads * kVec) + i % kVec;
     }
-    __device__ __forceinline__ void fetch(uint4 (&w)[kBlocks]) const {
+    __device__ __forceinline__ bool whole(uint32_t c) const { return c < cols && cols - c >= kVec; }
+    // The tile on its way to the thread's places in shared memory, which no other thread
+    // reads or writes; -inf where there is no column.  `inside`: the row covers it all.
+    __device__ __forceinline__ void fetch(uint4 (&to)[kBlocks][kThreads], bool inside) const {
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
-            const int64_t c = base + (static_cast<int64_t>(b) * kThreads + threadIdx.x) * kVec;
-            if (c >= 0 && c + kVec <= cols) {
-                asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(w[b].x), "=r"(w[b].y), "=r"(w[b].z), "=r"(w[b].w)
-                             : "l"(row + c));
+            const uint32_t c = base + b * (kThreads * kVec);
+            uint4* at = &to[b][threadIdx.x];
+            if (inside || whole(c)) {
+                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;"
+                             :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(at))),
+                                "l"(row + c) : "memory");
             } else {
-                T e[kVec];
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < kVec; ++i)
-                    e[i] = c + i >= 0 && c + i < cols ? row[c + i] : T(-INFINITY);
-                w[b] = *reinterpret_cast<const uint4*>(e);
+                    reinterpret_cast<T*>(at)[i] = c + i < cols ? row[c + i] : T(-INFINITY);
             }
         }
     }
-    static __device__ __forceinline__ void values(const uint4 (&w)[kBlocks], float (&v)[kPer]) {
+    // The block from column c on, read anew.
+    __device__ __forceinline__ uint4 block(uint32_t c) const {
+        if (whole(c)) return __ldg(reinterpret_cast<const uint4*>(row + c));
+        uint32_t words[4];
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            const T* e = reinterpret_cast<const T*>(&w[b]);
+        for (int j = 0; j < 4; ++j) {
+            constexpr int kEach = 4 / sizeof(T);
+            words[j] = 0;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) v[b * kVec + i] = static_cast<float>(e[i]);
+            for (int i = 0; i < kEach; ++i) {
+                const uint32_t at = c + j * kEach + i;
+                const T v = at < cols ? row[at] : T(-INFINITY);
+                if constexpr (sizeof(T) == 4) words[j] = __float_as_uint(v);
+                else words[j] |= static_cast<uint32_t>(__bfloat16_as_ushort(v)) << (16 * i);
+            }
         }
+        return make_uint4(words[0], words[1], words[2], words[3]);
+    }
+    static __device__ __forceinline__ void values(const uint4& w, float* v) {
+        const uint32_t bits[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            v[i] = __uint_as_float(sizeof(T) == 4 ? bits[i % 4]
+                                   : i & 1        ? bits[i / 2 % 4] & 0xffff0000u
+                                                  : bits[i / 2 % 4] << 16);
     }
 };
 
-// NaN counts as -inf.
-__device__ __forceinline__ void clean(float (&v)[kPer]) {
+// The largest of a thread's columns, NaN passed over.
+template <typename T>
+__device__ __forceinline__ float largest_of(const uint4 (&w)[kBlocks]) {
+    if constexpr (sizeof(T) == 4) {
+        float top = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) v[e] = fmaxf(v[e], -INFINITY);
+        for (int b = 0; b < kBlocks; ++b) {
+            top = max3(top, __uint_as_float(w[b].x), __uint_as_float(w[b].y));
+            top = max3(top, __uint_as_float(w[b].z), __uint_as_float(w[b].w));
+        }
+        return top;
+    } else {
+        // two at a time, as they lie
+        uint32_t top = 0xff80ff80u;  // -inf, -inf
+        auto larger = [&](uint32_t v) {
+            asm("max.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(v));
+        };
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) larger(w[b].x), larger(w[b].y), larger(w[b].z), larger(w[b].w);
+        return fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u));
+    }
 }
 
-// A tile's share of the row's normalizer state, in the thread: m, and d + lost.  Values
-// that are no numbers are cleaned out of v.  Returns the values' maximum.
+// A thread's share of the row's normalizer state: weights e^(x - m) summed as d + lost,
+// and the largest value so far.  m follows the largest only when that has passed it by
+// more than one, so the roundings of the change of m fade with it.
+template <typename T>
 struct State {
-    float m = -INFINITY, d = 0.f, lost = 0.f;
+    float m = -INFINITY, d = 0.f, lost = 0.f, largest = -INFINITY;
 
-    static __device__ __forceinline__ float weights(const float (&v)[kPer], float up) {
-        float part[4] = {};
-        if (fabsf(up) < 1e30f) {
-            // base-2 exponents with one rounding each, below the rounded maximum; the
-            // factor between it and the maximum comes at once
-            const float c = up * kLog2e;
+    __device__ __forceinline__ float weights(const uint4 (&w)[kBlocks]) const {
+        // base-2 exponents with one rounding each, below the rounded reference; the
+        // factor between it and the reference comes at once
+        const float c = m * kLog2e;
+        float2 part[2] = {};
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) part[e & 3] += ex2f(fmaf(v[e], kLog2e, -c));
-            return ((part[0] + part[1]) + (part[2] + part[3])) * ex2f(fmaf(up, -kLog2e, c));
+        for (int b = 0; b < kBlocks; ++b) {
+            float v[Tile<T>::kVec];
+            Tile<T>::values(w[b], v);
+#pragma unroll
+            for (int e = 0; e < Tile<T>::kVec; e += 2) {
+                const float2 t = fma2(make_float2(v[e], v[e + 1]), splat2(kLog2e), splat2(-c));
+                part[e/2&1] = add2(part[e/2&1], make_float2(ex2f(t.x), ex2f(t.y)));
+            }
         }
-        // a maximum of +-inf or near the largest number
-#pragma unroll
-        for (int e = 0; e < kPer; ++e)
-            part[e & 3] += v[e] == up ? 1.f : ex2f((v[e] - up) * kLog2e);
-        return (part[0] + part[1]) + (part[2] + part[3]);
+        return ((part[0].x + part[0].y) + (part[1].x + part[1].y)) * ex2f(fmaf(m, -kLog2e, c));
     }
-    __device__ __forceinline__ float add(float (&v)[kPer]) {
-        float top = fmaxf(v[0], -INFINITY);
-#pragma unroll
-        for (int e = 1; e < kPer; ++e) top = fmaxf(top, v[e]);
-        const float up = fmaxf(m, top);
-        if (up == -INFINITY) return top;
-        if (up > m) {
-            const float f = factor(m, up);
+    // Returns the tile's largest value.
+    __device__ __forceinline__ float add(const uint4 (&w)[kBlocks]) {
+        const float top = largest_of<T>(w);
+        if (top > m + 1.f) {
+            const float f = factor(m, top);
             d *= f;
             lost *= f;
-            m = up;
+            m = top;
         }
-        float sum = weights(v, up);
-        if (!(sum == sum)) {
-            clean(v);
-            sum = weights(v, up);
-        }
+        largest = fmaxf(largest, top);
+        const float sum = m > -INFINITY ? weights(w) : 0.f;
         // the running sum keeps what its rounding loses
         const float s = d + sum;
         lost += d >= sum ? (d - s) + sum : (sum - s) + d;
         d = s;
         return top;
     }
+    // Not so where a value was NaN, or the reference is infinite or so large that it and
+    // its product with log2 e are too far apart (the sum is then NaN, or this is asked).
+    __device__ __forceinline__ bool good() const {
+        return d < INFINITY && (m == -INFINITY || fabsf(m) < 0x1p28f);
+    }
+    // the sum below another reference of at least `largest`
+    __device__ __forceinline__ float below(float top) const {
+        return m > -INFINITY ? (d + lost) * (m == top ? 1.f : exp1(m - top)) : 0.f;
+    }
 };
 
 // The list's first n keys ranked by counting; the K best, in order, to sh.sorted and
 // back to the list.  Returns how many there are.
-__device__ __forceinline__ int rank_list(RunShared& sh, int n, int K) {
+template <typename T>
+__device__ __forceinline__ int rank_list(RunShared<T>& sh, int n, int K) {
+    const auto* pairs = reinterpret_cast<const ulonglong2*>(sh.list);
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const u64 mine = sh.list[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += sh.list[j] > mine;
+#pragma unroll 4
+        for (int j = 0; j < n / 2; ++j) {
+            const ulonglong2 p = pairs[j];
+            rank += (p.x > mine) + (p.y > mine);
+        }
+        if (n & 1) rank += sh.list[n - 1] > mine;
         if (rank < K) sh.sorted[rank] = mine;
     }
     __syncthreads();
@@ -237,13 +300,13 @@ __device__ __forceinline__ int rank_list(RunShared& sh, int n, int K) {
 // The same for any number of values (many may be equal): the best in turn, of the sorted
 // list's `held` keys and a tile.
 template <typename T>
-__device__ __noinline__ int best_in_turn(RunShared& sh, const Tile<T> tile, int held, int K) {
+__device__ __noinline__ int best_in_turn(RunShared<T>& sh, const Tile<T> tile, int held, int K) {
     const int tid = threadIdx.x;
-    uint4 w[Tile<T>::kBlocks];
+    constexpr int kPer = Tile<T>::kPer;
     float v[kPer];
-    tile.fetch(w);
-    Tile<T>::values(w, v);
-    clean(v);
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+        Tile<T>::values(tile.block(tile.col(b * Tile<T>::kVec)), v + b * Tile<T>::kVec);
     const u64 before = tid < held ? sh.sorted[tid] : 0;
     u64 below = ~0ull;
     int k = 0;
@@ -270,95 +333,143 @@ __device__ __noinline__ int best_in_turn(RunShared& sh, const Tile<T> tile, int 
     }
     __syncthreads();
     if (tid < k) sh.list[tid] = sh.sorted[tid];
+    __syncthreads();
     return k;
 }
 
+// A thread's weights of tiles [first, last) below their largest value `top`, one by one:
+// for the rows that State cannot sum.
+template <typename T>
+__device__ __noinline__ float careful_sum(Tile<T> tile, int first, int last, int head, float top) {
+    float d = 0.f, lost = 0.f;
+    for (int i = first; i < last; ++i) {
+        tile.base = static_cast<uint32_t>(i) * Tile<T>::kTile - head + threadIdx.x * Tile<T>::kVec;
+        for (int b = 0; b < kBlocks; ++b) {
+            float v[Tile<T>::kVec];
+            Tile<T>::values(tile.block(tile.col(b * Tile<T>::kVec)), v);
+#pragma unroll
+            for (int e = 0; e < Tile<T>::kVec; ++e) {
+                const float x = !(v[e] > -INFINITY) ? 0.f : v[e] == top ? 1.f : exp1(v[e] - top);
+                const float s = d + x;
+                lost += d >= x ? (d - s) + x : (x - s) + d;
+                d = s;
+            }
+        }
+    }
+    return d + lost;
+}
+
 template <typename T, int KP>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, 3)
     beam_runs_kernel(const __grid_constant__ BeamArgs a) {
-    __shared__ RunShared sh;
+    using Tiles = Tile<T>;
+    constexpr int kTile = Tiles::kTile, kSegment = RunShared<T>::kSegment;
+    constexpr int kStages = RunShared<T>::kStages, kVec = Tiles::kVec;
+    extern __shared__ __align__(16) unsigned char raw[];
+    auto& sh = *reinterpret_cast<RunShared<T>*>(raw);
     const int64_t row = blockIdx.x / a.runs;
     const int run = static_cast<int>(blockIdx.x % a.runs);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;");
+    wait_before();
+    let_next();
     if (!has_row(a, row)) return;
-    Tile<T> tile;
+    Tiles tile;
     tile.row = static_cast<const T*>(a.x) + row * a.cols;
-    tile.cols = a.cols;
+    tile.cols = static_cast<uint32_t>(a.cols);
     const int head = static_cast<int>(reinterpret_cast<uintptr_t>(tile.row) % 16 / sizeof(T));
-    State state;
-    int held = 0;  // keys in the list, best first
-    const int64_t tiles = (a.cols + head + kTile - 1) / kTile;
-    const int64_t first = run * a.run_tiles, last = min(tiles, first + a.run_tiles);
-    uint4 w[Tile<T>::kBlocks];
-    float v[kPer];
-    auto place = [&](int64_t i) { tile.base = i * kTile - head; };
-    // the next tile's values are asked for before this one's are worked on
-    auto step = [&](int64_t i) {
-        Tile<T>::values(w, v);
-        if (i + 1 < last) {
-            place(i + 1);
-            tile.fetch(w);
-        }
-        place(i);
-        return order_key(state.add(v));
+    const int tiles = static_cast<int>((a.cols + head + kTile - 1) / kTile);
+    const int first = run * a.run_tiles, last = min(tiles, first + a.run_tiles);
+    auto place = [&](int i, int thread) {
+        tile.base = static_cast<uint32_t>(i) * kTile - head + thread * kVec;
     };
-    auto push = [&](uint32_t bound) {
+    auto fetch = [&](int i, int stage) {
+        place(i, tid);
+        const uint32_t begin = static_cast<uint32_t>(i) * kTile - head;
+        if (i < last) tile.fetch(sh.tile[stage], begin < tile.cols && tile.cols - begin >= kTile);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-        for (int e = 0; e < kPer; ++e)
-            if (order_key(v[e]) >= bound) {
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < kList) sh.list[at] = make_key(v[e], tile.col(e));
-            }
-    };
-    if (tid == 0) sh.count = 0;
-    if (first < last) {
-        place(first);
-        tile.fetch(w);
-    }
+    for (int i = 0; i < kStages - 1; ++i) fetch(first + i, i);
+    State<T> state;
+    int held = 0;  // keys in the list, best first
+    bool many = false;  // more values reached a bound than the list holds: many are equal
+    int stage = 0;
 #pragma unroll 1
-    for (int64_t i = first; i < last;) {
-        // until the list is full a tile's own bound, from then on the K-th of the list
-        const bool full = held == a.K;
-        const int64_t end = full ? min(last, i + kChunk) : i + 1;
-        uint32_t bound = full ? static_cast<uint32_t>(sh.list[a.K - 1] >> 32) + 1 : 0;
+    for (int from = first; from < last; from += kSegment) {
+        const int to = min(last, from + kSegment);
+        float largest = -INFINITY;
 #pragma unroll 1
-        for (int64_t j = i; j < end; ++j) {
-            const uint32_t top = step(j);
-            if (!full)
-                bound = max(parts_bound<KP, kThreads>(
-                                top, sh.bound, [](uint32_t x, uint32_t y) { return max(x, y); }),
-                            sample::kKeyNegInf + 1);
-            if (top >= bound) push(bound);
+        for (int i = from; i < to; ++i) {
+            fetch(i + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+            asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
+            uint4 w[kBlocks];
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) w[b] = sh.tile[stage][b][tid];
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+            const float top = state.add(w);
+            sh.top[i - from][tid] = top;
+            largest = fmaxf(largest, top);
         }
-        __syncthreads();
-        const int n = sh.count;
-        if (n > held) {
-            if (n <= kList) {
-                held = rank_list(sh, n, a.K);
-            } else {
-#pragma unroll 1
-                for (int64_t j = i; j < end; ++j) {
-                    place(j);
-                    held = best_in_turn(sh, tile, held, a.K);
+        // ---- the K best so far: a bound that K values of the segment reach (-inf is no
+        // continuation); with a full list, one past its K-th (a later column has to be larger)
+        if (tid == 0) sh.count = held, sh.groups = 0;
+        uint32_t least = parts_bound<KP, kThreads>(order_key(largest), sh.bound,
+                                                   [](uint32_t x, uint32_t y) { return max(x, y); });
+        least = max(least, sample::kKeyNegInf + 1);
+        if (held == a.K) least = max(least, static_cast<uint32_t>(sh.list[a.K - 1] >> 32) + 1);
+        const float bound = key_value(least);
+        if (largest >= bound)
+            for (int i = 0; i < to - from; ++i)
+                if (sh.top[i][tid] >= bound) {
+                    const int at = atomicAdd(&sh.groups, 1);
+                    if (at < kGroups) sh.group[at] = static_cast<uint16_t>(i * kThreads + tid);
                 }
+        __syncthreads();
+        const int groups = sh.groups;
+        if (groups <= kGroups) {
+            for (int i = tid; i < groups * kBlocks; i += kThreads) {
+                const int group = sh.group[i / kBlocks];
+                place(from + group / kThreads, group % kThreads);
+                const uint32_t c = tile.col(i % kBlocks * kVec);
+                float v[kVec];
+                Tiles::values(tile.block(c), v);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    if (v[e] >= bound) {
+                        const int at = atomicAdd(&sh.count, 1);
+                        if (at < kList) sh.list[at] = make_key(v[e], c + e);
+                    }
             }
+            __syncthreads();
         }
-        __syncthreads();
-        if (tid == 0) sh.count = held;
-        __syncthreads();
-        i = end;
+        const int n = sh.count;
+        if (groups > kGroups || n > kList) {
+            many = true;
+            __syncthreads();
+        } else {
+            if (n > held) held = rank_list(sh, n, a.K);
+            __syncthreads();
+        }
     }
-    float m = state.m, d = state.d + state.lost;
+    if (many) {
+        held = 0;
+#pragma unroll 1
+        for (int i = first; i < last; ++i) {
+            place(i, tid);
+            held = best_in_turn(sh, tile, held, a.K);
+        }
+    }
+    float top = state.largest;
     // ---- the run's state
-    float top = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
     if (lane == 0) sh.m[warp] = top;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, sh.m[w]);
-    d = m > -INFINITY ? d * factor(m, top) : 0.f;
+    float d = state.below(top);
+    if (__syncthreads_or(!state.good()))
+        d = top > -INFINITY ? careful_sum(tile, first, last, head, top) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFullMask, d, o);
     if (lane == 0) sh.d[warp] = d;
@@ -370,7 +481,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
         for (int w = 0; w < kThreads / 32; ++w) all += sh.d[w];
         a.states[at] = make_float2(top, all);
     }
-    if (tid < a.K) a.lists[at * a.K + tid] = tid < held ? sh.sorted[tid] : 0;
+    const int64_t group = row / a.beams, list = at - group * a.beams * a.runs;
+    if (tid < a.K)
+        a.lists[(group * a.K + tid) * a.beams * a.runs + list] = tid < held ? sh.sorted[tid] : 0;
 }
 
 // ------------------------------------------------------------------ the groups
@@ -381,12 +494,13 @@ struct MergeShared {
     double lse[kMaxBeams];          // ln of the summed weights
     double m64[kMaxBeams];
     double score[kMaxBeams];
-    float m[kMaxBeams];
+    float m[kMaxBeams], near[kMaxBeams];  // near: the offset in fp32
     unsigned char kind[kMaxBeams];  // 0 no candidates, 1 a row, 2 ended
-    unsigned char again[kMaxBeams]; // its sum is wanted in 38 bits
-    u64 bound[128];
+    uint32_t bound[128];
     u64 warp_order[kMergeThreads / 32], warp_at[kMergeThreads / 32];
     u64 sum[kMergeThreads / 32];
+    u64 slice[kMaxBeams][kHelpers];  // a row's summed weights, from each CTA of the cluster
+    u64 todo;                        // rows to be summed again
     float pow2[64];
     int count;
 };
@@ -407,26 +521,45 @@ __device__ __forceinline__ bool better(u64 c, u64 at, u64 c2, u64 at2) {
     return c > c2 || (c == c2 && at < at2);
 }
 
-// ln of a row's summed weights e^(x - m), the weights added as integers; thread 0 has it.
-template <typename T>
-__device__ double exact_log_sum(MergeShared& sh, const T* row, int64_t cols, float m) {
+__device__ __forceinline__ sample::Weight row_weights(float m, int64_t cols, const float* pow2) {
     int bits = 62;
     while ((int64_t(1) << (62 - bits)) < cols) --bits;
     sample::Weight w;
-    w.set(m, 1.f, min(44, bits), sh.pow2);
+    w.set(m, 1.f, min(44, bits), pow2);
+    return w;
+}
+
+// The weights e^(x - m) of columns [from, to) of a row, summed as integers.
+template <typename T>
+__device__ u64 exact_sum(MergeShared& sh, const sample::Weight& w, const T* row, int64_t from,
+                         int64_t to) {
+    constexpr int kAtOnce = 8;
     u64 sum = 0;
-    for (int64_t c = threadIdx.x; c < cols; c += kMergeThreads) {
-        const float x = widen(row[c]);
-        if (x > -INFINITY) sum += w(x);
+#pragma unroll 1
+    for (int64_t c = from + threadIdx.x; c < to; c += kAtOnce * kMergeThreads) {
+        float x[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            x[i] = c + i * kMergeThreads < to ? static_cast<float>(row[c + i * kMergeThreads])
+                                              : -INFINITY;
+        sum += w.sum_from(x, -FLT_MAX);
     }
     sum = sample::warp_sum64(sum);
     __syncthreads();
     if (threadIdx.x % 32 == 0) sh.sum[threadIdx.x / 32] = sum;
     __syncthreads();
-    if (threadIdx.x != 0) return 0.0;
     sum = 0;
+#pragma unroll
     for (int i = 0; i < kMergeThreads / 32; ++i) sum += sh.sum[i];
-    return log(static_cast<double>(sum)) - log(static_cast<double>(w(m)));
+    return sum;
+}
+
+// All CTAs of a group (threads come from branches, so the form that counts them).
+__device__ __forceinline__ void group_sync(int helpers) {
+    if (helpers == 1) __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.release;\n\t"
+                     "barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 template <typename T, int KP>
@@ -434,16 +567,65 @@ __global__ void __launch_bounds__(kMergeThreads)
     beam_merge_kernel(const __grid_constant__ BeamArgs a) {
     __shared__ MergeShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.beams;
+    const int64_t group = blockIdx.x / a.helpers, row0 = group * a.beams;
+    const int rank = static_cast<int>(blockIdx.x % a.helpers);
+    // this CTA's share of the rows whose sums have to be exact, into the first CTA
+    auto sum_rows = [&](u64 todo) {
+        const int64_t each = (a.cols + a.helpers - 1) / a.helpers;
+        for (; todo; todo &= todo - 1) {
+            const int i = __ffsll(static_cast<long long>(todo)) - 1;
+            float m = sh.m[i];
+            if (rank) {
+                const uint32_t at = map_to_rank(&sh.m[i], 0);
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(m) : "r"(at) : "memory");
+            }
+            const sample::Weight w = row_weights(m, a.cols, sh.pow2);
+            const u64 sum =
+                exact_sum(sh, w, static_cast<const T*>(a.x) + (row0 + i) * a.cols, rank * each,
+                          min(a.cols, (rank + 1) * each));
+            if (tid) continue;
+            if (rank) {
+                const uint32_t at = map_to_rank(&sh.slice[i][rank], 0);
+                asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(at), "l"(sum) : "memory");
+            } else {
+                sh.slice[i][0] = sum;
+            }
+        }
+    };
+    // (a CTA's shared memory may be written from outside once it has started)
+    if (a.helpers > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    if (rank) {
+        if (tid < 64) sh.pow2[tid] = sample::kPow2[tid];
+        let_next();
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        group_sync(a.helpers);
+        if (sh.todo == 0) return;
+        sum_rows(sh.todo);
+        group_sync(a.helpers);
+        return;
+    }
     for (int i = tid; i < a.beams; i += kMergeThreads) {
         const float s = a.scores[row0 + i];
         sh.score[i] = s;
         sh.kind[i] = !(s > -INFINITY) ? 0 : a.ended && a.ended[row0 + i] ? 2 : 1;
-        sh.again[i] = 0;
     }
     if (tid < 64) sh.pow2[tid] = sample::kPow2[tid];
     __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_before();
+    let_next();
+    if (a.helpers > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    // ---- the lists' entries, entry by entry of all lists: a thread's first ones stay in
+    // registers.  Threads take them so that the parts of the bound get equal shares.
+    const int lists = a.beams * a.runs, entries = lists * a.K;
+    const u64* keys = a.lists + group * entries;
+    constexpr int kPart = kMergeThreads / KP, kHeld = 4;
+    const int turn = tid / kPart + KP * (tid % kPart);
+    u64 mine[kHeld];
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+        const int i = turn + j * kMergeThreads;
+        mine[j] = i < entries ? __ldcg(keys + i) : 0;
+    }
     for (int i = warp; i < a.beams; i += kMergeThreads / 32) {
         if (sh.kind[i] != 1) continue;
         const float2* st = a.states + (row0 + i) * a.runs;
@@ -465,61 +647,75 @@ __global__ void __launch_bounds__(kMergeThreads)
             sh.m64[i] = top;
         }
     }
-    const int lists = a.beams * a.runs;
     const double eps = a.eps;
-    // entry e of list j (a beam's run): its key, 0 where there is none
-    auto key_of = [&](int list, int e) -> u64 {
-        const int beam = list / a.runs;
-        if (sh.kind[beam] == 1) return a.lists[((row0 + beam) * a.runs + list % a.runs) * a.K + e];
-        // an ended beam goes on with `pad` alone
-        return sh.kind[beam] == 2 && list % a.runs == 0 && e == 0
-                   ? (1ull << 63) | (0xffffffffu - static_cast<uint32_t>(a.pad)) : 0;
-    };
+    // the order of an entry's value, kNone where there is none
     auto order_of = [&](u64 key, int beam) -> u64 {
         if (key == 0) return kNone;
-        if (sh.kind[beam] == 2) return order64(sh.score[beam]);
+        if (sh.kind[beam] == 2) return order64(sh.offset[beam]);
         const float x = key_value(static_cast<uint32_t>(key >> 32));
         if (sh.m[beam] == INFINITY) return x == INFINITY ? order64(sh.offset[beam]) : kNone;
         return order64(sh.offset[beam] + (static_cast<double>(x) - sh.m64[beam]));
     };
-    auto at_of = [](u64 key, int beam) {
+    // f(key, beam) of the thread's entries that are continuations
+    auto each = [&](auto f) {
+        auto one = [&](int i, u64 key) {
+            const int list = i % lists, beam = list / a.runs;
+            if (sh.kind[beam] != 1) {
+                // an ended beam goes on with `pad` alone
+                key = sh.kind[beam] == 2 && i == beam * a.runs
+                          ? (1ull << 63) | (0xffffffffu - static_cast<uint32_t>(a.pad)) : 0;
+            }
+            if (key) f(key, beam);
+        };
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+            if (turn + j * kMergeThreads < entries) one(turn + j * kMergeThreads, mine[j]);
+#pragma unroll 1
+        for (int i = turn + kHeld * kMergeThreads; i < entries; i += kMergeThreads)
+            one(i, __ldcg(keys + i));
+    };
+    auto place_of = [](u64 key, int beam) {
         return (static_cast<u64>(beam) << 32) | (0xffffffffu - static_cast<uint32_t>(key));
+    };
+    // a value in fp32, and how far it may be off (its own three roundings)
+    auto rough = [&](u64 key, int beam, float& slack) {
+        const float off = sh.near[beam];
+        float t = 0.f;
+        if (sh.kind[beam] == 1) {
+            const float x = key_value(static_cast<uint32_t>(key >> 32)), m = sh.m[beam];
+            t = x == m ? 0.f : x - m;
+        }
+        slack = (fabsf(off) + fabsf(t)) * 0x1p-22f;
+        return off + t;
     };
     int found = 0;
     for (int round = 0; round < 2; ++round) {
         __syncthreads();
-        if (tid == 0) sh.count = 0;
+        if (tid == 0) sh.count = 0, sh.todo = 0;
         for (int i = tid; i < a.beams; i += kMergeThreads)
-            if (sh.kind[i] == 1)
-                sh.offset[i] = sh.score[i] - sh.lse[i];
+            if (sh.kind[i]) {
+                sh.offset[i] = sh.kind[i] == 1 ? sh.score[i] - sh.lse[i] : sh.score[i];
+                sh.near[i] = static_cast<float>(sh.offset[i]);
+            }
         __syncthreads();
-        // ---- a bound that K of the lists' first entries reach, dealt out to the parts in turn
-        u64 top = kNone;
-        {
-            constexpr int kPart = kMergeThreads / KP;
-            const int all = max(lists, min(kMergeThreads, lists * a.K));
-            for (int i = tid / kPart + KP * (tid % kPart); i < all; i += kMergeThreads) {
-                const u64 c = order_of(key_of(i % lists, i / lists), i % lists / a.runs);
-                top = c > top ? c : top;
-            }
-        }
-        u64 bound = parts_bound<KP, kMergeThreads>(top, sh.bound,
-                                                   [](u64 x, u64 y) { return x > y ? x : y; });
-        // (one that the errors may have put below another is not lost)
-        if (round == 0 && bound > kNone) bound = order64(value64(bound) - 4 * eps);
-        if (bound == kNone) ++bound;
-        for (int i = tid; i < lists * a.K; i += kMergeThreads) {
-            const int list = i / a.K, beam = list / a.runs;
-            const u64 key = key_of(list, i % a.K);
-            const u64 c = order_of(key, beam);
-            if (c >= bound) {
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < kCandidates) {
-                    sh.order[at] = c;
-                    sh.at[at] = at_of(key, beam);
-                }
-            }
-        }
+        // ---- a bound that K entries reach, less what the roundings and (in the first
+        // round) the sums' errors may have taken from others
+        float top = -INFINITY, slack;
+        each([&](u64 key, int beam) {
+            const float c = rough(key, beam, slack) - slack;
+            top = fmaxf(top, c);
+        });
+        float bound = key_value(parts_bound<KP, kMergeThreads>(
+            order_key(top), sh.bound, [](uint32_t x, uint32_t y) { return max(x, y); }));
+        bound -= 4 * a.eps + fabsf(bound) * 0x1p-22f;
+        each([&](u64 key, int beam) {
+            const float c = rough(key, beam, slack) + slack;
+            if (c < bound) return;
+            const u64 order = order_of(key, beam);
+            if (order == kNone) return;
+            const int i = atomicAdd(&sh.count, 1);
+            if (i < kCandidates) sh.order[i] = order, sh.at[i] = place_of(key, beam);
+        });
         __syncthreads();
         const int n = sh.count;
         if (n <= kCandidates) {
@@ -538,14 +734,12 @@ __global__ void __launch_bounds__(kMergeThreads)
             u64 c0 = ~0ull, at0 = 0;
             for (found = 0; found < a.K; ++found) {
                 u64 c1 = kNone, at1 = ~0ull;
-                for (int i = tid; i < lists * a.K; i += kMergeThreads) {
-                    const int beam = i / a.K / a.runs;
-                    const u64 key = key_of(i / a.K, i % a.K);
-                    const u64 c = order_of(key, beam), at = at_of(key, beam);
+                each([&](u64 key, int beam) {
+                    const u64 c = order_of(key, beam), at = place_of(key, beam);
                     if (c > kNone && (found == 0 || better(c0, at0, c, at)) &&
                         better(c, at, c1, at1))
                         c1 = c, at1 = at;
-                }
+                });
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) {
                     const u64 c = __shfl_xor_sync(kFullMask, c1, o);
@@ -564,43 +758,57 @@ __global__ void __launch_bounds__(kMergeThreads)
             }
         }
         __syncthreads();
-        if (round || found == 0) break;
+        if (round) break;
         // ---- values of different beams that the sums cannot tell apart: neighbours in the
         // order, and of what is not chosen all that come near the last chosen
-        bool near = false;
         auto mark = [&](u64 at0, u64 at1) {
-            const uint32_t b0 = at0 >> 32, b1 = at1 >> 32;
-            if (b0 == b1) return;
-            near = true;
-            sh.again[b0] = sh.again[b1] = 1;
+            const int b0 = static_cast<int>(at0 >> 32), b1 = static_cast<int>(at1 >> 32);
+            if (b0 != b1) atomicOr(&sh.todo, (1ull << b0) | (1ull << b1));
         };
-        for (int i = tid; i + 1 < found; i += kMergeThreads)
-            if (value64(sh.best[i]) - value64(sh.best[i + 1]) <= 2 * eps)
-                mark(sh.best_at[i], sh.best_at[i + 1]);
-        const u64 last = sh.best[found - 1], last_at = sh.best_at[found - 1];
-        const u64 low = order64(value64(last) - 2 * eps);
-        auto behind = [&](u64 c, u64 at) {
-            if (c >= low && better(last, last_at, c, at)) mark(last_at, at);
-        };
-        if (n <= kCandidates)
-            for (int i = tid; i < n; i += kMergeThreads) behind(sh.order[i], sh.at[i]);
-        else
-            for (int i = tid; i < lists * a.K; i += kMergeThreads) {
-                const int beam = i / a.K / a.runs;
-                const u64 key = key_of(i / a.K, i % a.K);
-                if (key) behind(order_of(key, beam), at_of(key, beam));
+        if (found > 0) {
+            for (int i = tid; i + 1 < found; i += kMergeThreads)
+                if (value64(sh.best[i]) - value64(sh.best[i + 1]) <= 2 * eps)
+                    mark(sh.best_at[i], sh.best_at[i + 1]);
+            const u64 last = sh.best[found - 1], last_at = sh.best_at[found - 1];
+            const u64 low = order64(value64(last) - 2 * eps);
+            auto behind = [&](u64 c, u64 at) {
+                if (c >= low && better(last, last_at, c, at)) mark(last_at, at);
+            };
+            if (n <= kCandidates)
+                for (int i = tid; i < n; i += kMergeThreads) behind(sh.order[i], sh.at[i]);
+            else
+                each([&](u64 key, int beam) { behind(order_of(key, beam), place_of(key, beam)); });
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // what has a sum, for every CTA of the group
+            u64 todo = sh.todo;
+            for (u64 left = todo; left; left &= left - 1) {
+                const int i = __ffsll(static_cast<long long>(left)) - 1;
+                if (sh.kind[i] != 1 || sh.m[i] == INFINITY) todo &= ~(1ull << i);
             }
-        if (!__syncthreads_or(near)) break;
-        for (int b = 0; b < a.beams; ++b) {
-            if (!sh.again[b] || sh.kind[b] != 1 || sh.m[b] == INFINITY) continue;
-            const double log_sum = exact_log_sum(
-                sh, static_cast<const T*>(a.x) + (row0 + b) * a.cols, a.cols, sh.m[b]);
-            if (tid == 0) sh.lse[b] = log_sum;
+            __syncwarp();
+            if (lane == 0) sh.todo = todo;
+            else if (lane < a.helpers) {
+                const uint32_t at = map_to_rank(&sh.todo, lane);
+                asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(at), "l"(todo) : "memory");
+            }
+        }
+        group_sync(a.helpers);
+        const u64 todo = sh.todo;
+        if (todo == 0) break;
+        sum_rows(todo);
+        group_sync(a.helpers);
+        if (tid < a.beams && (todo >> tid & 1)) {
+            const sample::Weight w = row_weights(sh.m[tid], a.cols, sh.pow2);
+            u64 sum = 0;
+            for (int i = 0; i < a.helpers; ++i) sum += sh.slice[tid][i];
+            sh.lse[tid] = log(static_cast<double>(sum) / static_cast<double>(w(sh.m[tid])));
         }
     }
     if (tid < a.K) {
         const bool is = tid < found;
-        const int64_t at = static_cast<int64_t>(blockIdx.x) * a.K + tid;
+        const int64_t at = group * a.K + tid;
         a.out[at] = is ? static_cast<float>(value64(sh.best[tid])) : -INFINITY;
         a.parents[at] = is ? static_cast<int>(sh.best_at[tid] >> 32) : -1;
         a.tokens[at] = is ? static_cast<int>(sh.best_at[tid] & 0xffffffffu) : -1;

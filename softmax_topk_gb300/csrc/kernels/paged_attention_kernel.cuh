@@ -58,7 +58,7 @@ struct AttnArgs {
 template <int D, int NT>
 struct AttnShape {
     static constexpr int kHeads = 8 * NT;  // query heads of a unit
-    static constexpr int kWarps = 8;
+    static constexpr int kWarps = D == 128 ? 8 : 12;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRow = D * 2;               // bytes of a key
     static constexpr int kSide = kBlock * kRow;      // K or V of a block
@@ -73,8 +73,6 @@ struct AttnShared {
     using S = AttnShape<D, NT>;
     unsigned char ring[S::kWarps][S::kAhead][2][S::kSide];  // K, V of a block
     float head[S::kWarps][S::kPiece];  // the piece of a unit begun before the warp
-    long long scan[S::kThreads];
-    long long warp_total[S::kWarps];
     int unit[S::kWarps][2];  // unit of each piece or -1: [0] begun before the warp, [1] begun in it
     long long end[S::kWarps];  // where the unit of piece [1] ends
     // The piece that the warp began lies in its ring, which is empty when it is written.
@@ -189,31 +187,29 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
     auto& sh = *reinterpret_cast<AttnShared<D, NT>*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
-    // the join may be put in place while this grid works; it waits for its end
-    asm volatile("griddepcontrol.launch_dependents;");
+    wait_before();
+    let_next();  // the join: it waits for this grid's end itself
 
-    // ---- this warp's run of blocks
-    const int per_thread = (a.seqs + S::kThreads - 1) / S::kThreads;
-    const int first = tid * per_thread, last = min(a.seqs, first + per_thread);
-    long long mine = 0;
-    for (int b = first; b < last; ++b) mine += (used_length(a, b) + kBlock - 1) / kBlock;
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(kFullMask, upto, o);
-        if (lane >= o) upto += v;
-    }
-    if (lane == 31) sh.warp_total[warp] = upto;
+    // ---- this warp's run of blocks: every warp adds up the lengths itself, which for
+    // the usual numbers of sequences takes less time than waiting for others
     if (lane < 2) sh.unit[warp][lane] = -1;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < S::kWarps; ++w) {
-        if (w < warp) upto += sh.warp_total[w];
-        total += sh.warp_total[w];
-    }
-    sh.scan[tid] = upto;
-    __syncthreads();
-    total *= a.units;
+    auto blocks_of = [&](int b) {
+        return b < a.seqs ? (used_length(a, b) + kBlock - 1) / kBlock : 0;
+    };
+    auto scanned = [&](long long v) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long before = __shfl_up_sync(kFullMask, v, o);
+            if (lane >= o) v += before;
+        }
+        return v;
+    };
+    const int per_lane = (a.seqs + 31) / 32;
+    long long mine = 0;
+#pragma unroll 4
+    for (int i = 0; i < per_lane; ++i) mine += blocks_of(lane * per_lane + i);
+    const long long upto = scanned(mine);
+    const long long total = __shfl_sync(kFullMask, upto, 31) * a.units;
     // CTAs, then warps, take equal runs; the last ones may have none
     const long long per_cta = (total + gridDim.x - 1) / gridDim.x;
     const long long cta_begin = min(total, per_cta * blockIdx.x);
@@ -221,37 +217,26 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
     const long long per_warp = (cta_end - cta_begin + S::kWarps - 1) / S::kWarps;
     const long long begin = min(cta_end, cta_begin + per_warp * warp);
     const int n = static_cast<int>(min(cta_end, begin + per_warp) - begin);
-
-    // ---- sequences without keys
     const int heads = a.kv_heads * a.group;
-    for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
-        if (used_length(a, b) > 0) continue;
-        for (int i = tid; i < heads * (D / 8); i += S::kThreads)
-            reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * heads * (D / 8) + i] =
-                make_uint4(0, 0, 0, 0);
-        for (int i = tid; a.lse && i < heads; i += S::kThreads)
-            a.lse[static_cast<int64_t>(b) * heads + i] = -INFINITY;
-    }
 
     if (n > 0) {
         Cursor cur;
         long long unit_end;  // of the current unit, in the line
         {
-            // the thread whose share of the sequences holds `begin`, then the sequence
-            int lo = 0, hi = S::kThreads - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi) / 2;
-                if (sh.scan[mid] * a.units > begin) hi = mid;
-                else lo = mid + 1;
+            // the lane whose sequences hold `begin`, then the sequence
+            const int holder = __ffs(__ballot_sync(kFullMask, upto * a.units > begin)) - 1;
+            long long before = __shfl_sync(kFullMask, upto - mine, holder) * a.units;
+            cur.b = holder * per_lane;
+            while (true) {
+                const int b = cur.b + lane;
+                const long long here = scanned(blocks_of(b)) * a.units;
+                const unsigned past = __ballot_sync(kFullMask, before + here > begin);
+                const int skip = past ? __ffs(past) - 1 : 32;
+                if (skip > 0) before += __shfl_sync(kFullMask, here, skip - 1);
+                cur.b += skip;
+                if (past) break;
             }
-            long long before = lo > 0 ? sh.scan[lo - 1] * a.units : 0;
-            cur.b = lo * per_thread;
             cur.sequence(a);
-            while (before + static_cast<long long>(cur.blocks) * a.units <= begin) {
-                before += static_cast<long long>(cur.blocks) * a.units;
-                ++cur.b;
-                cur.sequence(a);
-            }
             const long long in = begin - before;
             cur.u = static_cast<int>(in / cur.blocks);
             cur.j = static_cast<int>(in % cur.blocks);
@@ -480,30 +465,39 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
             }
         }
     }
+    // ---- sequences without keys
+    for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
+        if (used_length(a, b) > 0) continue;
+        for (int i = tid; i < heads * (D / 8); i += S::kThreads)
+            reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * heads * (D / 8) + i] =
+                make_uint4(0, 0, 0, 0);
+        for (int i = tid; a.lse && i < heads; i += S::kThreads)
+            a.lse[static_cast<int64_t>(b) * heads + i] = -INFINITY;
+    }
     __syncthreads();
 
-    // ---- pieces of units that warps share: the warp that began one joins it
-    bool tail = false;
+    // ---- pieces of units that warps share: unit j begins before the CTA (0) or in warp
+    // j - 1; the warps share its heads out
 #pragma unroll 1
-    for (int slot = warp == 0 ? 0 : 1; slot < 2; ++slot) {
-        const int unit = sh.unit[warp][slot];
+    for (int j = 0; j <= S::kWarps; ++j) {
+        const int w0 = max(j - 1, 0), slot = j > 0;
+        const int unit = sh.unit[w0][slot];
         if (unit < 0) continue;
         int parts = 1;  // this one and the next warps' first ones
-        while (warp + parts < S::kWarps && sh.unit[warp + parts][0] == unit) ++parts;
-        const bool open = slot == 0 || sh.end[warp] > cta_end;  // other CTAs have pieces too
-        tail |= slot == 1 && open;
+        while (w0 + parts < S::kWarps && sh.unit[w0 + parts][0] == unit) ++parts;
+        const bool open = slot == 0 || sh.end[w0] > cta_end;  // other CTAs have pieces too
         float* to = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + slot) * S::kPiece;
         const int b = unit / a.units, u = unit % a.units;
         const int head0 = (u % a.chunks) * S::kHeads;
         const int64_t row0 = static_cast<int64_t>(b) * heads + (u / a.chunks) * a.group + head0;
 #pragma unroll 1
-        for (int head = 0; head < min(S::kHeads, a.group - head0); ++head) {
+        for (int head = warp; head < min(S::kHeads, a.group - head0); head += S::kWarps) {
             float top = -INFINITY;
             for (int i = 0; i < parts; ++i)
-                top = fmaxf(top, sh.piece(warp + i, i ? 0 : slot)[S::kM + head]);
+                top = fmaxf(top, sh.piece(w0 + i, i ? 0 : slot)[S::kM + head]);
             float sum = 0.f, acc[D / 32] = {};
             for (int i = 0; i < parts; ++i) {
-                const float* from = sh.piece(warp + i, i ? 0 : slot);
+                const float* from = sh.piece(w0 + i, i ? 0 : slot);
                 const float f = piece_weight(from[S::kM + head], top);
                 sum += f * from[S::kL + head];
 #pragma unroll
@@ -511,7 +505,9 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
                     acc[x] += f * from[head * S::kHeadStride + lane * (D / 32) + x];
             }
             if (open) {
-                for (int x = 0; x < D / 32; ++x) to[head * S::kHeadStride + lane * (D / 32) + x] = acc[x];
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x)
+                    to[head * S::kHeadStride + lane * (D / 32) + x] = acc[x];
                 if (lane == 0) {
                     to[S::kM + head] = top;
                     to[S::kL + head] = sum;
@@ -525,11 +521,17 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
                 if (lane == 0) store_lse<D>(a, row0 + head, top, sum);
             }
         }
-        if (tail && lane == 0)
-            a.tails[blockIdx.x] =
-                make_int4(unit, static_cast<int>((sh.end[warp] - 1) / per_cta) - blockIdx.x, 0, 0);
     }
-    if (__syncthreads_or(tail) == 0 && tid == 0) a.tails[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (warp == 0) {
+        // the unit that goes on behind the CTA, if one does, and in how many more CTAs
+        const bool goes_on =
+            lane < S::kWarps && sh.unit[lane][1] >= 0 && sh.end[lane] > cta_end;
+        if (goes_on)
+            a.tails[blockIdx.x] = make_int4(
+                sh.unit[lane][1], static_cast<int>((sh.end[lane] - 1) / per_cta) - blockIdx.x, 0, 0);
+        if (!__any_sync(kFullMask, goes_on) && lane == 0)
+            a.tails[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    }
 }
 
 // The units that span CTAs, one (CTA that began one, query head) per CTA here: the
@@ -542,7 +544,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     using S = AttnShape<D, NT>;
     __shared__ float acc_sh[kJoinWarps][D], top_sh[kJoinWarps], sum_sh[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, head = blockIdx.y;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_before();
+    let_next();
     const int4 tail = a.tails[blockIdx.x];
     if (tail.x < 0) return;
     const int b = tail.x / a.units, u = tail.x % a.units;

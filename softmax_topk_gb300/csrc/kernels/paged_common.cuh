@@ -4,6 +4,14 @@
 #include "ops.cuh"
 
 namespace os {
+
+// The kernels of a decode step follow one another on a stream.  Each is launched so that
+// it may be put in place while the one before it still runs (launch_behind): wait_before
+// holds it until that one has ended and its writes are seen, let_next lets the one behind
+// it come as soon as every CTA has called it.
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 namespace paged {
 
 // Position -> page of a sequence, slot in it.  Pages of 2^shift slots by a shift,

@@ -63,6 +63,8 @@ __global__ void __launch_bounds__(kAppendThreads)
     __shared__ int pos_sh[kAppendTokens], row_sh[kAppendTokens];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * per_cta;
+    wait_before();
+    let_next();
     if (warp < per_cta) {
         const int64_t t = t0 + warp;
         int pos = -1, row = -1;  // of the pool: page * kv_heads * page_size + slot
@@ -166,11 +168,20 @@ struct ReorderArgs {
 
 constexpr int kReorderThreads = 128;
 
+__device__ __forceinline__ uint4 load_once(const char* p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
+}
+
 __global__ void __launch_bounds__(kReorderThreads)
     reorder_kernel(const __grid_constant__ ReorderArgs a) {
     const int tid = threadIdx.x;
     const int j = blockIdx.x % a.seqs;
-    const int64_t part = blockIdx.x / a.seqs;  // (layer, head)
+    const int part = blockIdx.x / a.seqs;  // (layer, head)
+    wait_before();
+    let_next();
     const int parent = __ldg(a.parents + j);
     const bool alive = static_cast<unsigned>(parent) < static_cast<unsigned>(a.beams);
     const int p = alive ? j / a.beams * a.beams + parent : j;
@@ -190,11 +201,30 @@ __global__ void __launch_bounds__(kReorderThreads)
     const int head = static_cast<int>(part % a.kv_heads);
     const int64_t base = part / a.kv_heads * a.layer_bytes + head * a.head_bytes;
     const int pieces = static_cast<int>(rest * a.row_bytes / 16);
-    for (int side = 0; side < 2; ++side) {
-        char* cache = reinterpret_cast<char*>(side ? a.v_cache : a.k_cache) + base;
-        const uint4* src = reinterpret_cast<const uint4*>(cache + from * a.page_bytes);
-        uint4* dst = reinterpret_cast<uint4*>(cache + to * a.page_bytes);
-        for (int i = tid; i < pieces; i += kReorderThreads) dst[i] = src[i];
+    const char* k_from = reinterpret_cast<const char*>(a.k_cache) + base + from * a.page_bytes;
+    const char* v_from = reinterpret_cast<const char*>(a.v_cache) + base + from * a.page_bytes;
+    char* k_to = reinterpret_cast<char*>(a.k_cache) + base + to * a.page_bytes;
+    char* v_to = reinterpret_cast<char*>(a.v_cache) + base + to * a.page_bytes;
+    // eight loads on their way per thread before the first store
+    constexpr int kAtOnce = 4;
+    for (int i0 = tid; i0 < pieces; i0 += kAtOnce * kReorderThreads) {
+        uint4 k[kAtOnce], v[kAtOnce];
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x) {
+            const int i = i0 + x * kReorderThreads;
+            if (i < pieces) {
+                k[x] = load_once(k_from + 16 * static_cast<int64_t>(i));
+                v[x] = load_once(v_from + 16 * static_cast<int64_t>(i));
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x) {
+            const int i = i0 + x * kReorderThreads;
+            if (i < pieces) {
+                reinterpret_cast<uint4*>(k_to)[i] = k[x];
+                reinterpret_cast<uint4*>(v_to)[i] = v[x];
+            }
+        }
     }
 }
 

@@ -15,7 +15,8 @@ cudaError_t append(const paged::AppendArgs& a, cudaStream_t stream) {
     const DeviceInfo* dev = device_info();
     if (!dev) return cudaErrorInvalidDevice;
     const int per_cta = a.tokens >= 16 * int64_t(dev->sms) ? paged::kAppendTokens : 1;
-    return launch_kernel(paged::append_kernel<D, INTERLEAVED>, ceil_div(a.tokens, per_cta),
+    return launch_behind(paged::append_kernel<D, INTERLEAVED>,
+                         dim3(static_cast<unsigned>(ceil_div(a.tokens, per_cta))),
                          paged::kAppendThreads, 1, 0, stream, a, per_cta);
 }
 
@@ -72,7 +73,8 @@ cudaError_t launch_paged_reorder(const os_paged_cache& c, const int32_t* parents
     a.kv_heads = c.kv_heads;
     a.layers = layers;
     a.split = paged::page_split(c.page_size);
-    return launch_kernel(paged::reorder_kernel, c.seqs * layers * c.kv_heads,
+    return launch_behind(paged::reorder_kernel,
+                         dim3(static_cast<unsigned>(c.seqs * layers * c.kv_heads)),
                          paged::kReorderThreads, 1, 0, stream, a);
 }
 
