@@ -431,7 +431,8 @@ os_status os_paged_append(const os_paged_cache *cache, const void *k, int64_t k_
  * O = 0 and L = -inf.
  *   q         [seqs] rows of q_heads x head_dim bf16, q_stride elements apart (a
  *             multiple of 8, at least the row); 16-byte aligned.  q_heads is a
- *             multiple of kv_heads (OS_ERR_SHAPE).
+ *             multiple of kv_heads; seqs * kv_heads * ceil(q_heads / kv_heads / 8)
+ *             * ceil(width * page_size / 16) at most 2^30 (OS_ERR_SHAPE).
  *   out       [seqs][q_heads][head_dim] bf16, 16-byte aligned.
  *   lse       [seqs][q_heads] fp32, or NULL (not written).
  *   workspace os_paged_attention_workspace bytes, 16-byte aligned, overwritten.

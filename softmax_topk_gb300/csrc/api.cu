@@ -550,6 +550,10 @@ os_status os_paged_attention(const os_paged_cache* cache, const void* q, int64_t
     if (q_heads % cache->kv_heads || q_heads > INT32_MAX / 2 / cache->head_dim ||
         !rows_ok(cache->seqs, q_stride, row))
         return OS_ERR_SHAPE;
+    // blocks of 16 keys that there can be, for 8 query heads each
+    const int64_t units = int64_t(cache->kv_heads) * ((q_heads / cache->kv_heads + 7) / 8);
+    const int64_t blocks = (cache->width * cache->page_size + 15) / 16;
+    if (cache->seqs > 0 && units * blocks > (1 << 30) / cache->seqs) return OS_ERR_SHAPE;
     if (!(scale > 0.f) || !(scale < INFINITY)) return OS_ERR_VALUE;
     if (cache->seqs == 0) return OS_OK;
     const os_status ps = paged_pointers(cache);

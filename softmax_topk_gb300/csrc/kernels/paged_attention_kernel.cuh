@@ -47,7 +47,7 @@ struct AttnArgs {
     __nv_bfloat16* out;      // [seqs][heads][D]
     float* lse;              // [seqs][heads] or NULL
     float* parts;            // workspace: two pieces per CTA
-    int4* tails;             // per CTA: unit that goes on behind it (or -1), CTAs that it goes on in
+    int4* tails;             // per CTA: of the unit that goes on behind it, row of out (or -1), CTAs, heads
     int64_t q_stride;
     PageSplit split;
     int seqs, width, pages, kv_heads;
@@ -73,8 +73,10 @@ struct AttnShared {
     using S = AttnShape<D, NT>;
     unsigned char ring[S::kWarps][S::kAhead][2][S::kSide];  // K, V of a block
     float head[S::kWarps][S::kPiece];  // the piece of a unit begun before the warp
-    int unit[S::kWarps][2];  // unit of each piece or -1: [0] begun before the warp, [1] begun in it
-    long long end[S::kWarps];  // where the unit of piece [1] ends
+    // The warps' pieces: [0] of a unit begun before the warp, [1] of one begun in it; where
+    // the unit begins in the line (or -1), and of [1] where it ends and its first row of out
+    int unit[2][S::kWarps];
+    int end[S::kWarps], row[S::kWarps], head_row;  // head_row: of [0] of the first warp
     // The piece that the warp began lies in its ring, which is empty when it is written.
     __device__ __forceinline__ float* piece(int warp, int which) {
         static_assert(S::kPiece * sizeof(float) <= sizeof(ring[0]), "a piece fits the ring");
@@ -134,9 +136,10 @@ __device__ __forceinline__ int used_length(const AttnArgs& a, int b) {
     return max(0, min(len, a.width * a.split.size));
 }
 
-// A place in the line of blocks: block j of unit u of sequence b.
+// A place in the line of blocks: block j of query heads' chunk c of key head h of
+// sequence b.
 struct Cursor {
-    int b, u, j, blocks, len;
+    int b, h, c, j, blocks, len;
     __device__ __forceinline__ void sequence(const AttnArgs& a) {
         len = used_length(a, b);
         blocks = (len + kBlock - 1) / kBlock;
@@ -144,8 +147,10 @@ struct Cursor {
     __device__ __forceinline__ void next(const AttnArgs& a) {
         if (++j < blocks) return;
         j = 0;
-        if (++u < a.units) return;
-        u = 0;
+        if (++c < a.chunks) return;
+        c = 0;
+        if (++h < a.kv_heads) return;
+        h = 0;
         do {
             if (++b >= a.seqs) return;
             sequence(a);
@@ -153,20 +158,26 @@ struct Cursor {
     }
 };
 
-// The pool's row of key 16 j + (lane mod 16), or -1: behind the length, or its
-// page is not in the pool.
-__device__ __forceinline__ int pool_row(const AttnArgs& a, const Cursor& c, int lane) {
-    const int key = c.j * kBlock + (lane & 15);
-    if (key >= c.len) return -1;
-    const int at = a.split.page(key);
-    const int page = __ldg(a.table + static_cast<int64_t>(c.b) * a.width + at);
-    if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.pages)) return -1;
-    return (page * a.kv_heads + c.u / a.chunks) * a.split.size + key - at * a.split.size;
-}
+// Where key 16 j + (lane mod 16) lies: its page (asked for; -1 behind the length), and its
+// row in the page.
+struct Key {
+    int page, in;
+    __device__ __forceinline__ void ask(const AttnArgs& a, const Cursor& c, int lane) {
+        const int key = c.j * kBlock + (lane & 15);
+        const int at = a.split.page(key);
+        page = -1;
+        if (key < c.len) page = __ldg(a.table + static_cast<int64_t>(c.b) * a.width + at);
+        in = c.h * a.split.size + key - at * a.split.size;
+    }
+    // the pool's row, or -1: no such page
+    __device__ __forceinline__ int row(const AttnArgs& a) const {
+        return static_cast<unsigned>(page) < static_cast<unsigned>(a.pages)
+                   ? page * a.kv_heads * a.split.size + in : -1;
+    }
+};
 
 // One head's row of O, m and l: the result, rounded once.
-template <int D>
-__device__ __forceinline__ void store_lse(const AttnArgs& a, int64_t row, float m, float l) {
+__device__ __forceinline__ void store_lse(const AttnArgs& a, int row, float m, float l) {
     if (a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2f : -INFINITY;
 }
 
@@ -192,44 +203,54 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
 
     // ---- this warp's run of blocks: every warp adds up the lengths itself, which for
     // the usual numbers of sequences takes less time than waiting for others
-    if (lane < 2) sh.unit[warp][lane] = -1;
+    if (lane < 2) sh.unit[lane][warp] = -1;
     auto blocks_of = [&](int b) {
         return b < a.seqs ? (used_length(a, b) + kBlock - 1) / kBlock : 0;
     };
-    auto scanned = [&](long long v) {
+    auto scanned = [&](int v) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long before = __shfl_up_sync(kFullMask, v, o);
+            const int before = __shfl_up_sync(kFullMask, v, o);
             if (lane >= o) v += before;
         }
         return v;
     };
     const int per_lane = (a.seqs + 31) / 32;
-    long long mine = 0;
+    int mine = 0;
 #pragma unroll 4
     for (int i = 0; i < per_lane; ++i) mine += blocks_of(lane * per_lane + i);
-    const long long upto = scanned(mine);
-    const long long total = __shfl_sync(kFullMask, upto, 31) * a.units;
+    const int upto = scanned(mine) * a.units;
+    const int total = __shfl_sync(kFullMask, upto, 31);
     // CTAs, then warps, take equal runs; the last ones may have none
-    const long long per_cta = (total + gridDim.x - 1) / gridDim.x;
-    const long long cta_begin = min(total, per_cta * blockIdx.x);
-    const long long cta_end = min(total, cta_begin + per_cta);
-    const long long per_warp = (cta_end - cta_begin + S::kWarps - 1) / S::kWarps;
-    const long long begin = min(cta_end, cta_begin + per_warp * warp);
-    const int n = static_cast<int>(min(cta_end, begin + per_warp) - begin);
+    const int per_cta = (total + gridDim.x - 1) / gridDim.x;
+    const int cta_begin = static_cast<int>(
+        min(static_cast<int64_t>(total), static_cast<int64_t>(per_cta) * blockIdx.x));
+    const int cta_end = cta_begin + min(total - cta_begin, per_cta);
+    const int per_warp = (cta_end - cta_begin + S::kWarps - 1) / S::kWarps;
+    const int begin = min(cta_end, cta_begin + per_warp * warp);
+    const int n = min(cta_end - begin, per_warp);
     const int heads = a.kv_heads * a.group;
+
+    // ---- sequences without keys
+    for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
+        if (used_length(a, b) > 0) continue;
+        for (int i = tid; i < heads * (D / 8); i += S::kThreads)
+            reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * heads * (D / 8) + i] =
+                make_uint4(0, 0, 0, 0);
+        for (int i = tid; a.lse && i < heads; i += S::kThreads)
+            a.lse[static_cast<int64_t>(b) * heads + i] = -INFINITY;
+    }
 
     if (n > 0) {
         Cursor cur;
-        long long unit_end;  // of the current unit, in the line
+        int unit_end;  // of the current unit, in the line
         {
             // the lane whose sequences hold `begin`, then the sequence
-            const int holder = __ffs(__ballot_sync(kFullMask, upto * a.units > begin)) - 1;
-            long long before = __shfl_sync(kFullMask, upto - mine, holder) * a.units;
+            const int holder = __ffs(__ballot_sync(kFullMask, upto > begin)) - 1;
+            int before = __shfl_sync(kFullMask, upto - mine * a.units, holder);
             cur.b = holder * per_lane;
-            while (true) {
-                const int b = cur.b + lane;
-                const long long here = scanned(blocks_of(b)) * a.units;
+            while (per_lane > 1) {
+                const int here = scanned(blocks_of(cur.b + lane)) * a.units;
                 const unsigned past = __ballot_sync(kFullMask, before + here > begin);
                 const int skip = past ? __ffs(past) - 1 : 32;
                 if (skip > 0) before += __shfl_sync(kFullMask, here, skip - 1);
@@ -237,12 +258,12 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
                 if (past) break;
             }
             cur.sequence(a);
-            const long long in = begin - before;
-            cur.u = static_cast<int>(in / cur.blocks);
-            cur.j = static_cast<int>(in % cur.blocks);
+            const int unit = (begin - before) / cur.blocks;
+            cur.j = begin - before - unit * cur.blocks;
+            cur.h = a.chunks == 1 ? unit : unit / a.chunks;
+            cur.c = a.chunks == 1 ? 0 : unit % a.chunks;
             unit_end = begin - cur.j + cur.blocks;
         }
-        Cursor ahead = cur;
         uint32_t q[NT][kTiles][2];
         float o[NT][kTiles][4], m[NT][2], l[NT][2];
         const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(sh.ring[warp]));
@@ -261,17 +282,38 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
             }
         };
 
-        // rows of the blocks up to kAhead behind the current one
-        int rows[S::kAhead + 1];
-        rows[0] = pool_row(a, ahead, lane);
+        auto load_q = [&]() {
 #pragma unroll
-        for (int i = 1; i <= S::kAhead; ++i) {
-            rows[i] = -1;
+            for (int nt = 0; nt < NT; ++nt) {
+                const int head = cur.c * S::kHeads + nt * 8 + g;
+                const __nv_bfloat16* p =
+                    a.q + cur.b * a.q_stride + (cur.h * a.group + head) * D + 2 * t;
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        q[nt][j][e] = head < a.group
+                                          ? *reinterpret_cast<const uint32_t*>(p + 16 * j + 8 * e)
+                                          : 0u;
+            }
+        };
+        load_q();
+
+        // rows of the current block and of kAhead behind it; the one after those is asked
+        // for a block before it is used
+        int rows[S::kAhead + 1];
+        Cursor ahead = cur;
+        Key key[S::kAhead + 1];
+#pragma unroll
+        for (int i = 0; i <= S::kAhead; ++i) {
+            key[i].page = -1;
             if (i < n) {
-                ahead.next(a);
-                rows[i] = pool_row(a, ahead, lane);
+                if (i > 0) ahead.next(a);
+                key[i].ask(a, ahead, lane);
             }
         }
+#pragma unroll
+        for (int i = 0; i <= S::kAhead; ++i) rows[i] = key[i].row(a);
 #pragma unroll
         for (int i = 0; i < S::kAhead; ++i) {
             if (i < n) fetch(a.k, ring + 2 * i * S::kSide, rows[i]);
@@ -282,28 +324,20 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
         bool fresh = true;       // the block begins a unit, or the run
         bool begun_here = cur.j == 0;
         for (int i = 0; i < n; ++i) {
-            int rows_after = -1;
+            Key after;
+            after.page = -1;
             if (i + S::kAhead + 1 < n) {
                 ahead.next(a);
-                rows_after = pool_row(a, ahead, lane);
+                after.ask(a, ahead, lane);
             }
             if (fresh) {
-                const int h = cur.u / a.chunks, c = cur.u % a.chunks;
+                if (i > 0) load_q();
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const int head = c * S::kHeads + nt * 8 + g;
-                    const __nv_bfloat16* p =
-                        a.q + cur.b * a.q_stride + (h * a.group + head) * D + 2 * t;
 #pragma unroll
-                    for (int j = 0; j < kTiles; ++j) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            q[nt][j][e] = head < a.group ? *reinterpret_cast<const uint32_t*>(
-                                                               p + 16 * j + 8 * e)
-                                                         : 0u;
+                    for (int j = 0; j < kTiles; ++j)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
-                    }
                     m[nt][0] = m[nt][1] = -INFINITY;
                     l[nt][0] = l[nt][1] = 0.f;
                 }
@@ -412,7 +446,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
             if (place == ring + 2 * S::kAhead * S::kSide) place = ring;
 #pragma unroll
             for (int x = 0; x < S::kAhead; ++x) rows[x] = rows[x + 1];
-            rows[S::kAhead] = rows_after;
+            rows[S::kAhead] = after.row(a);
             fresh = cur.j + 1 == cur.blocks;
             if (fresh || i + 1 == n) {
                 // ---- the unit's last block, or the run's
@@ -423,79 +457,88 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1)
                             l[nt][e] += __shfl_xor_sync(kFullMask, l[nt][e], x);
-                const bool whole = fresh && begun_here;
-                const int which = begun_here ? 1 : 0;
-                const int unit = cur.b * a.units + cur.u;
-                const int head0 = (cur.u % a.chunks) * S::kHeads;
-                const int64_t row0 = static_cast<int64_t>(cur.b) * heads +
-                                     (cur.u / a.chunks) * a.group + head0;
-                float* piece = sh.piece(warp, which);
+                const int head0 = cur.c * S::kHeads;
+                const int row0 = cur.b * heads + cur.h * a.group + head0;
+                if (fresh && begun_here) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int head = nt * 8 + 2 * t + e;
-                        if (head0 + head >= a.group) continue;
-                        const float f = !whole ? 1.f : l[nt][e] > 0.f ? 1.f / l[nt][e] : 0.f;
-                        if (whole && g == 0) store_lse<D>(a, row0 + head, m[nt][e], l[nt][e]);
-                        if (!whole && g == 0) {
-                            piece[S::kM + head] = m[nt][e];
-                            piece[S::kL + head] = l[nt][e];
-                        }
+                        for (int e = 0; e < 2; ++e) {
+                            const int head = nt * 8 + 2 * t + e;
+                            if (head0 + head >= a.group) continue;
+                            const float f = l[nt][e] > 0.f ? 1.f / l[nt][e] : 0.f;
+                            if (g == 0) store_lse(a, row0 + head, m[nt][e], l[nt][e]);
+                            __nv_bfloat16* to =
+                                a.out + static_cast<int64_t>(row0 + head) * D + g;
 #pragma unroll
-                        for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const int d = 16 * j + 8 * x + g;
-                                const float v = f * o[nt][j][2 * x + e];
-                                if (whole) a.out[(row0 + head) * D + d] = __float2bfloat16(v);
-                                else piece[head * S::kHeadStride + d] = v;
+                            for (int j = 0; j < kTiles; ++j) {
+                                to[16 * j] = __float2bfloat16(f * o[nt][j][e]);
+                                to[16 * j + 8] = __float2bfloat16(f * o[nt][j][2 + e]);
                             }
+                        }
                     }
-                }
-                if (!whole && lane == 0) {
-                    sh.unit[warp][which] = unit;
-                    if (which == 1) sh.end[warp] = unit_end;
+                } else {
+                    const int which = begun_here ? 1 : 0;
+                    float* piece = sh.piece(warp, which);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int head = nt * 8 + 2 * t + e;
+                            if (g == 0) {
+                                piece[S::kM + head] = m[nt][e];
+                                piece[S::kL + head] = l[nt][e];
+                            }
+                            float* to = piece + head * S::kHeadStride + g;
+#pragma unroll
+                            for (int j = 0; j < kTiles; ++j) {
+                                to[16 * j] = o[nt][j][e];
+                                to[16 * j + 8] = o[nt][j][2 + e];
+                            }
+                        }
+                    }
+                    if (lane == 0) {
+                        sh.unit[which][warp] = unit_end - cur.blocks;  // (where it begins)
+                        if (which) sh.end[warp] = unit_end, sh.row[warp] = row0;
+                        else if (warp == 0) sh.head_row = row0;
+                    }
                 }
                 begun_here = true;
             }
             if (i + 1 < n) {
                 cur.next(a);
-                if (fresh) unit_end = begin + i + 1 + cur.blocks;
+                if (fresh) unit_end += cur.blocks;
             }
         }
-    }
-    // ---- sequences without keys
-    for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
-        if (used_length(a, b) > 0) continue;
-        for (int i = tid; i < heads * (D / 8); i += S::kThreads)
-            reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * heads * (D / 8) + i] =
-                make_uint4(0, 0, 0, 0);
-        for (int i = tid; a.lse && i < heads; i += S::kThreads)
-            a.lse[static_cast<int64_t>(b) * heads + i] = -INFINITY;
     }
     __syncthreads();
 
     // ---- pieces of units that warps share: unit j begins before the CTA (0) or in warp
     // j - 1; the warps share its heads out
+    const int first_of = lane < S::kWarps ? sh.unit[0][lane] : -1;
+    const int begun_by = lane < S::kWarps ? sh.unit[1][lane] : -1;
+    const bool goes_on = begun_by >= 0 && sh.end[min(lane, S::kWarps - 1)] > cta_end;
+    const unsigned open_ones = __ballot_sync(kFullMask, goes_on);
 #pragma unroll 1
     for (int j = 0; j <= S::kWarps; ++j) {
         const int w0 = max(j - 1, 0), slot = j > 0;
-        const int unit = sh.unit[w0][slot];
+        const int unit = __shfl_sync(kFullMask, slot ? begun_by : first_of, w0);
         if (unit < 0) continue;
-        int parts = 1;  // this one and the next warps' first ones
-        while (w0 + parts < S::kWarps && sh.unit[w0 + parts][0] == unit) ++parts;
-        const bool open = slot == 0 || sh.end[w0] > cta_end;  // other CTAs have pieces too
+        // this piece, and the first ones of the warps behind it that go on with the unit
+        const unsigned same = __ballot_sync(kFullMask, first_of == unit);
+        const int parts = __ffs(~(same >> (w0 + 1)));
+        const bool open = slot == 0 || (open_ones >> w0 & 1);  // other CTAs have pieces too
         float* to = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + slot) * S::kPiece;
-        const int b = unit / a.units, u = unit % a.units;
-        const int head0 = (u % a.chunks) * S::kHeads;
-        const int64_t row0 = static_cast<int64_t>(b) * heads + (u / a.chunks) * a.group + head0;
+        const int row0 = slot ? sh.row[w0] : sh.head_row;
+        const int left = a.group - row0 % a.group;  // heads of the unit's chunk
 #pragma unroll 1
-        for (int head = warp; head < min(S::kHeads, a.group - head0); head += S::kWarps) {
+        for (int head = warp; head < min(S::kHeads, left); head += S::kWarps) {
             float top = -INFINITY;
+#pragma unroll 4
             for (int i = 0; i < parts; ++i)
                 top = fmaxf(top, sh.piece(w0 + i, i ? 0 : slot)[S::kM + head]);
             float sum = 0.f, acc[D / 32] = {};
+#pragma unroll 4
             for (int i = 0; i < parts; ++i) {
                 const float* from = sh.piece(w0 + i, i ? 0 : slot);
                 const float f = piece_weight(from[S::kM + head], top);
@@ -516,21 +559,24 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
                 const float f = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
                 for (int x = 0; x < D / 32; x += 2)
-                    *reinterpret_cast<uint32_t*>(a.out + (row0 + head) * D + lane * (D / 32) + x) =
+                    *reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(row0 + head) * D +
+                                                 lane * (D / 32) + x) =
                         pack_bf16(f * acc[x], f * acc[x + 1]);
-                if (lane == 0) store_lse<D>(a, row0 + head, top, sum);
+                if (lane == 0) store_lse(a, row0 + head, top, sum);
             }
         }
     }
     if (warp == 0) {
-        // the unit that goes on behind the CTA, if one does, and in how many more CTAs
-        const bool goes_on =
-            lane < S::kWarps && sh.unit[lane][1] >= 0 && sh.end[lane] > cta_end;
-        if (goes_on)
+        // the unit that goes on behind the CTA, if one does: its first row of out, in how
+        // many CTAs it has pieces, and its heads
+        if (goes_on) {
+            const int row0 = sh.row[lane];
             a.tails[blockIdx.x] = make_int4(
-                sh.unit[lane][1], static_cast<int>((sh.end[lane] - 1) / per_cta) - blockIdx.x, 0, 0);
-        if (!__any_sync(kFullMask, goes_on) && lane == 0)
+                row0, (sh.end[lane] - 1) / per_cta - static_cast<int>(blockIdx.x) + 1,
+                min(S::kHeads, a.group - row0 % a.group), 0);
+        } else if (lane == 0 && open_ones == 0) {
             a.tails[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        }
     }
 }
 
@@ -546,22 +592,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, head = blockIdx.y;
     wait_before();
     let_next();
-    const int4 tail = a.tails[blockIdx.x];
-    if (tail.x < 0) return;
-    const int b = tail.x / a.units, u = tail.x % a.units;
-    const int head0 = (u % a.chunks) * S::kHeads;
-    if (head0 + head >= a.group) return;
-    const int parts = tail.y + 1;
     // the first piece is the second one of the CTA that began the unit
     auto piece = [&](int i) {
         return a.parts + (2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0)) * S::kPiece;
     };
+    // A lane has the maximum and the sum of one piece, asked for before it is known how many
+    // there are (what is no piece is not used).
+    const int most = min(32 * kJoinWarps, static_cast<int>(gridDim.x - blockIdx.x));
+    int mine = warp + lane * kJoinWarps;
+    float m = -INFINITY, l = 0.f;
+    if (mine < most) m = piece(mine)[S::kM + head], l = piece(mine)[S::kL + head];
+    const int4 tail = a.tails[blockIdx.x];  // (row of out, CTAs, heads)
+    if (tail.x < 0 || head >= tail.z) return;
+    const int parts = tail.y;
     float top = -INFINITY, sum = 0.f, acc[D / 32] = {};
-    for (int i0 = warp; i0 < parts; i0 += 32 * kJoinWarps) {
-        // a lane's maximum and weight each, then the rows
-        const int mine = i0 + lane * kJoinWarps;
-        const float m = mine < parts ? piece(mine)[S::kM + head] : -INFINITY;
-        const float l = mine < parts ? piece(mine)[S::kL + head] : 0.f;
+    for (int i0 = warp; i0 < parts; i0 += 32 * kJoinWarps, mine += 32 * kJoinWarps) {
+        if (i0 > warp && mine < parts) m = piece(mine)[S::kM + head], l = piece(mine)[S::kL + head];
+        if (mine >= parts) m = -INFINITY, l = 0.f;
         float to = fmaxf(top, m);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) to = fmaxf(to, __shfl_xor_sync(kFullMask, to, o));
@@ -594,10 +641,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
         all += f * sum_sh[w];
         value += f * acc_sh[w][d];
     }
-    const int64_t row = static_cast<int64_t>(b) * a.kv_heads * a.group +
-                        (u / a.chunks) * a.group + head0 + head;
-    a.out[row * D + d] = __float2bfloat16(all > 0.f ? value / all : 0.f);
-    if (d == 0) store_lse<D>(a, row, top, all);
+    const int row = tail.x + head;
+    a.out[static_cast<int64_t>(row) * D + d] = __float2bfloat16(all > 0.f ? value / all : 0.f);
+    if (d == 0) store_lse(a, row, top, all);
 }
 
 }  // namespace paged
