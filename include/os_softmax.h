@@ -484,9 +484,9 @@ os_status os_paged_reorder(const os_paged_cache *cache, const int32_t *parents,
  * best first, ties to the lower beam, then the lower column.
  *   x        [groups * beams][cols] of in_dtype, read only.
  *   scores   [groups][beams] fp32: the beams' summed log-probabilities.  A beam
- *            of -inf (or NaN) is not there; its logits are not read.
+ *            of -inf (or NaN) is not there; its logits take no part.
  *   ended    [groups][beams] bytes, not 0 where a beam has ended: it goes on as
- *            (i, pad) with c = scores_i alone, and its logits are not read.  Or
+ *            (i, pad) with c = scores_i alone, and its logits take no part.  Or
  *            NULL (none).
  *   out      [groups][K] fp32: c;  parents, tokens  [groups][K] int32: i and v.
  *            Where there are fewer than K continuations the places behind them

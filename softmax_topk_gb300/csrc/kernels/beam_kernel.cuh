@@ -63,11 +63,6 @@ struct BeamArgs {
     float eps;                     // bound of lse's error
 };
 
-// A live beam's candidates are its row's columns.
-__device__ __forceinline__ bool has_row(const BeamArgs& a, int64_t row) {
-    return a.scores[row] > -INFINITY && !(a.ended && a.ended[row]);
-}
-
 // value and column in one number: larger is better, no two alike, 0 is none
 __device__ __forceinline__ u64 make_key(float x, uint32_t col) {
     return (static_cast<u64>(order_key(x)) << 32) | (0xffffffffu - col);
@@ -372,7 +367,10 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     wait_before();
     let_next();
-    if (!has_row(a, row)) return;
+    // a beam that is not there or has ended has no continuations of its own (known only
+    // after the first tiles are asked for, so as not to wait twice)
+    const float score = a.scores[row];
+    const bool ended = a.ended && a.ended[row];
     Tiles tile;
     tile.row = static_cast<const T*>(a.x) + row * a.cols;
     tile.cols = static_cast<uint32_t>(a.cols);
@@ -390,6 +388,10 @@ __global__ void __launch_bounds__(kThreads, 3)
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(first + i, i);
+    if (!(score > -INFINITY) || ended) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+    }
     State<T> state;
     int held = 0;  // keys in the list, best first
     bool many = false;  // more values reached a bound than the list holds: many are equal
@@ -409,6 +411,16 @@ __global__ void __launch_bounds__(kThreads, 3)
             const float top = state.add(w);
             sh.top[i - from][tid] = top;
             largest = fmaxf(largest, top);
+        }
+        if (to == last) {
+            // the row's state, warp by warp (NaN where a thread could not sum)
+            float top = state.largest;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+            float d = state.good() ? state.below(top) : NAN;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFullMask, d, o);
+            if (lane == 0) sh.m[warp] = top, sh.d[warp] = d;
         }
         // ---- the K best so far: a bound that K values of the segment reach (-inf is no
         // continuation); with a full list, one past its K-th (a later column has to be larger)
@@ -459,27 +471,34 @@ __global__ void __launch_bounds__(kThreads, 3)
             held = best_in_turn(sh, tile, held, a.K);
         }
     }
-    float top = state.largest;
     // ---- the run's state
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-    if (lane == 0) sh.m[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, sh.m[w]);
-    float d = state.below(top);
-    if (__syncthreads_or(!state.good()))
-        d = top > -INFINITY ? careful_sum(tile, first, last, head, top) : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFullMask, d, o);
-    if (lane == 0) sh.d[warp] = d;
-    __syncthreads();
     const int64_t at = row * a.runs + run;
-    if (tid == 0) {
-        float all = 0.f;
+    if (first < last) {
+        constexpr int kWarps = kThreads / 32;
+        auto join = [&](float& top) {
+            float m = sh.m[lane % kWarps], d = sh.d[lane % kWarps];
+            top = m;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) all += sh.d[w];
-        a.states[at] = make_float2(top, all);
+            for (int o = kWarps / 2; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+            d = m > -INFINITY ? d * factor(m, top) : 0.f;
+#pragma unroll
+            for (int o = kWarps / 2; o > 0; o >>= 1) d += __shfl_xor_sync(kFullMask, d, o);
+            return d;
+        };
+        float top, d = join(top);
+        if (!(d == d)) {
+            __syncthreads();
+            float mine = careful_sum(tile, first, last, head, top);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(kFullMask, mine, o);
+            if (lane == 0) sh.m[warp] = top, sh.d[warp] = mine;
+            __syncthreads();
+            d = join(top);
+        }
+        if (tid == 0) a.states[at] = make_float2(top, d);
+    } else if (tid == 0) {
+        a.states[at] = make_float2(-INFINITY, 0.f);
     }
     const int64_t group = row / a.beams, list = at - group * a.beams * a.runs;
     if (tid < a.K)
@@ -488,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 
 // ------------------------------------------------------------------ the groups
 struct MergeShared {
-    u64 order[kCandidates], at[kCandidates];  // of a value; beam and column
+    ulonglong2 found[kCandidates];            // a value's order; its beam and column
     u64 best[kMaxK], best_at[kMaxK];          // the chosen, in order
     double offset[kMaxBeams];       // score - lse, to add to x - m
     double lse[kMaxBeams];          // ln of the summed weights
@@ -592,6 +611,7 @@ __global__ void __launch_bounds__(kMergeThreads)
             }
         }
     };
+    if (tid == 0) sh.todo = 0;
     // (a CTA's shared memory may be written from outside once it has started)
     if (a.helpers > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     if (rank) {
@@ -620,11 +640,18 @@ __global__ void __launch_bounds__(kMergeThreads)
     const u64* keys = a.lists + group * entries;
     constexpr int kPart = kMergeThreads / KP, kHeld = 4;
     const int turn = tid / kPart + KP * (tid % kPart);
+    // (entry e of the lists begins with list e, so that a part's entries are of many lists)
+    auto list_of = [&](int i) {
+        const int e = i / lists;
+        return (i - e * lists + e) % lists;
+    };
     u64 mine[kHeld];
+    int mine_of[kHeld];
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
         const int i = turn + j * kMergeThreads;
-        mine[j] = i < entries ? __ldcg(keys + i) : 0;
+        mine_of[j] = i < entries ? list_of(i) : -1;
+        mine[j] = i < entries ? __ldcg(keys + i / lists * lists + mine_of[j]) : 0;
     }
     for (int i = warp; i < a.beams; i += kMergeThreads / 32) {
         if (sh.kind[i] != 1) continue;
@@ -658,8 +685,8 @@ __global__ void __launch_bounds__(kMergeThreads)
     };
     // f(key, beam) of the thread's entries that are continuations
     auto each = [&](auto f) {
-        auto one = [&](int i, u64 key) {
-            const int list = i % lists, beam = list / a.runs;
+        auto one = [&](int i, int list, u64 key) {
+            const int beam = list / a.runs;
             if (sh.kind[beam] != 1) {
                 // an ended beam goes on with `pad` alone
                 key = sh.kind[beam] == 2 && i == beam * a.runs
@@ -669,10 +696,12 @@ __global__ void __launch_bounds__(kMergeThreads)
         };
 #pragma unroll
         for (int j = 0; j < kHeld; ++j)
-            if (turn + j * kMergeThreads < entries) one(turn + j * kMergeThreads, mine[j]);
+            if (mine_of[j] >= 0) one(turn + j * kMergeThreads, mine_of[j], mine[j]);
 #pragma unroll 1
-        for (int i = turn + kHeld * kMergeThreads; i < entries; i += kMergeThreads)
-            one(i, __ldcg(keys + i));
+        for (int i = turn + kHeld * kMergeThreads; i < entries; i += kMergeThreads) {
+            const int list = list_of(i);
+            one(i, list, __ldcg(keys + i / lists * lists + list));
+        }
     };
     auto place_of = [](u64 key, int beam) {
         return (static_cast<u64>(beam) << 32) | (0xffffffffu - static_cast<uint32_t>(key));
@@ -691,7 +720,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     int found = 0;
     for (int round = 0; round < 2; ++round) {
         __syncthreads();
-        if (tid == 0) sh.count = 0, sh.todo = 0;
+        if (tid == 0) sh.count = 0;
         for (int i = tid; i < a.beams; i += kMergeThreads)
             if (sh.kind[i]) {
                 sh.offset[i] = sh.kind[i] == 1 ? sh.score[i] - sh.lse[i] : sh.score[i];
@@ -714,18 +743,22 @@ __global__ void __launch_bounds__(kMergeThreads)
             const u64 order = order_of(key, beam);
             if (order == kNone) return;
             const int i = atomicAdd(&sh.count, 1);
-            if (i < kCandidates) sh.order[i] = order, sh.at[i] = place_of(key, beam);
+            if (i < kCandidates) sh.found[i] = make_ulonglong2(order, place_of(key, beam));
         });
         __syncthreads();
         const int n = sh.count;
         if (n <= kCandidates) {
             for (int i = tid; i < n; i += kMergeThreads) {
-                const u64 c = sh.order[i], at = sh.at[i];
+                const ulonglong2 c = sh.found[i];
                 int rank = 0;
-                for (int j = 0; j < n; ++j) rank += better(sh.order[j], sh.at[j], c, at);
+#pragma unroll 8
+                for (int j = 0; j < n; ++j) {
+                    const ulonglong2 other = sh.found[j];
+                    rank += better(other.x, other.y, c.x, c.y);
+                }
                 if (rank < a.K) {
-                    sh.best[rank] = c;
-                    sh.best_at[rank] = at;
+                    sh.best[rank] = c.x;
+                    sh.best_at[rank] = c.y;
                 }
             }
             found = min(n, a.K);
@@ -775,28 +808,27 @@ __global__ void __launch_bounds__(kMergeThreads)
                 if (c >= low && better(last, last_at, c, at)) mark(last_at, at);
             };
             if (n <= kCandidates)
-                for (int i = tid; i < n; i += kMergeThreads) behind(sh.order[i], sh.at[i]);
+                for (int i = tid; i < n; i += kMergeThreads) behind(sh.found[i].x, sh.found[i].y);
             else
                 each([&](u64 key, int beam) { behind(order_of(key, beam), place_of(key, beam)); });
         }
         __syncthreads();
-        if (warp == 0) {
-            // what has a sum, for every CTA of the group
-            u64 todo = sh.todo;
-            for (u64 left = todo; left; left &= left - 1) {
-                const int i = __ffsll(static_cast<long long>(left)) - 1;
-                if (sh.kind[i] != 1 || sh.m[i] == INFINITY) todo &= ~(1ull << i);
-            }
-            __syncwarp();
-            if (lane == 0) sh.todo = todo;
-            else if (lane < a.helpers) {
-                const uint32_t at = map_to_rank(&sh.todo, lane);
-                asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(at), "l"(todo) : "memory");
-            }
+        // what has a sum, for every CTA of the group
+        u64 todo = sh.todo;
+        for (u64 left = todo; left; left &= left - 1) {
+            const int i = __ffsll(static_cast<long long>(left)) - 1;
+            if (sh.kind[i] != 1 || sh.m[i] == INFINITY) todo &= ~(1ull << i);
+        }
+        if (todo == 0) {
+            // the others need not be waited for
+            if (a.helpers > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+            break;
+        }
+        if (tid > 0 && tid < a.helpers) {
+            const uint32_t at = map_to_rank(&sh.todo, tid);
+            asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(at), "l"(todo) : "memory");
         }
         group_sync(a.helpers);
-        const u64 todo = sh.todo;
-        if (todo == 0) break;
         sum_rows(todo);
         group_sync(a.helpers);
         if (tid < a.beams && (todo >> tid & 1)) {
