@@ -34,10 +34,9 @@ cudaError_t launch(const beam::BeamArgs& a, int64_t groups, cudaStream_t stream)
     if (!prepare_kernel(runs, 1, smem)) return cudaErrorInvalidConfiguration;
     const cudaError_t e =
         launch_behind(runs, dim3(static_cast<unsigned>(groups * a.beams * a.runs)), beam::kThreads,
-                      1, smem, stream, a);
+                      smem, stream, a);
     if (e != cudaSuccess) return e;
-    return launch_behind(beam::beam_merge_kernel<T, KP>,
-                         dim3(static_cast<unsigned>(groups * a.helpers)), beam::kMergeThreads,
+    return launch_kernel(beam::beam_merge_kernel<T, KP>, groups * a.helpers, beam::kMergeThreads,
                          a.helpers, 0, stream, a);
 }
 

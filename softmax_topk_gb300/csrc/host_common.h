@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <map>
 #include <mutex>
+#include <set>
 #include <utility>
 
 #include "../../include/os_softmax.h"
@@ -58,26 +59,37 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), int64_t grid, int threads, i
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// Launch `kernel` behind the one before it on `stream`, which lets it start early
-// (griddepcontrol.launch_dependents); it waits for that one's end itself
-// (griddepcontrol.wait) before it touches what that one wrote.
+// True from the second call for `kernel` on the current device on; the first one has
+// the kernel's code loaded.
+inline bool loaded_before(const void* kernel) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    static std::mutex mu;
+    static std::set<std::pair<int, const void*>> seen;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!seen.insert({dev, kernel}).second) return true;
+    cudaFuncAttributes attributes;
+    if (cudaFuncGetAttributes(&attributes, kernel) != cudaSuccess) cudaGetLastError();
+    return false;
+}
+
+// Launch `kernel` behind the one before it on `stream`, which may let it be put in place
+// before it has ended (griddepcontrol.launch_dependents); it waits for that one's end
+// itself (griddepcontrol.wait) before it touches memory.  The first launch of a kernel,
+// whose code has only just been loaded, waits as any other launch does.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_behind(void (*kernel)(KArgs...), dim3 grid, int threads, int cluster, int smem,
+cudaError_t launch_behind(void (*kernel)(KArgs...), dim3 grid, int threads, int smem,
                           cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.numAttrs = loaded_before(reinterpret_cast<const void*>(kernel)) ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 

@@ -366,7 +366,6 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int run = static_cast<int>(blockIdx.x % a.runs);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     wait_before();
-    let_next();
     // a beam that is not there or has ended has no continuations of its own (known only
     // after the first tiles are asked for, so as not to wait twice)
     const float score = a.scores[row];
@@ -616,7 +615,6 @@ __global__ void __launch_bounds__(kMergeThreads)
     if (a.helpers > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     if (rank) {
         if (tid < 64) sh.pow2[tid] = sample::kPow2[tid];
-        let_next();
         asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
         group_sync(a.helpers);
         if (sh.todo == 0) return;
@@ -631,8 +629,6 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
     if (tid < 64) sh.pow2[tid] = sample::kPow2[tid];
     __syncthreads();
-    wait_before();
-    let_next();
     if (a.helpers > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     // ---- the lists' entries, entry by entry of all lists: a thread's first ones stay in
     // registers.  Threads take them so that the parts of the bound get equal shares.
@@ -819,16 +815,12 @@ __global__ void __launch_bounds__(kMergeThreads)
             const int i = __ffsll(static_cast<long long>(left)) - 1;
             if (sh.kind[i] != 1 || sh.m[i] == INFINITY) todo &= ~(1ull << i);
         }
-        if (todo == 0) {
-            // the others need not be waited for
-            if (a.helpers > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-            break;
-        }
-        if (tid > 0 && tid < a.helpers) {
+        if (todo && tid > 0 && tid < a.helpers) {
             const uint32_t at = map_to_rank(&sh.todo, tid);
             asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(at), "l"(todo) : "memory");
         }
         group_sync(a.helpers);
+        if (todo == 0) break;
         sum_rows(todo);
         group_sync(a.helpers);
         if (tid < a.beams && (todo >> tid & 1)) {

@@ -17,7 +17,7 @@ cudaError_t append(const paged::AppendArgs& a, cudaStream_t stream) {
     const int per_cta = a.tokens >= 16 * int64_t(dev->sms) ? paged::kAppendTokens : 1;
     return launch_behind(paged::append_kernel<D, INTERLEAVED>,
                          dim3(static_cast<unsigned>(ceil_div(a.tokens, per_cta))),
-                         paged::kAppendThreads, 1, 0, stream, a, per_cta);
+                         paged::kAppendThreads, 0, stream, a, per_cta);
 }
 
 }  // namespace
@@ -75,7 +75,7 @@ cudaError_t launch_paged_reorder(const os_paged_cache& c, const int32_t* parents
     a.split = paged::page_split(c.page_size);
     return launch_behind(paged::reorder_kernel,
                          dim3(static_cast<unsigned>(c.seqs * layers * c.kv_heads)),
-                         paged::kReorderThreads, 1, 0, stream, a);
+                         paged::kReorderThreads, 0, stream, a);
 }
 
 }  // namespace os

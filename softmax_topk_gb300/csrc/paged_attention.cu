@@ -32,11 +32,11 @@ cudaError_t launch(paged::AttnArgs a, void* workspace, cudaStream_t stream) {
     auto k = paged::paged_attention_kernel<D, NT>;
     constexpr int smem = sizeof(paged::AttnShared<D, NT>);
     if (!prepare_kernel(k, 1, smem)) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_behind(k, dim3(ctas), S::kThreads, 1, smem, stream, a);
+    const cudaError_t e = launch_behind(k, dim3(ctas), S::kThreads, smem, stream, a);
     if (e != cudaSuccess || ctas == 1) return e;
     return launch_behind(paged::paged_join_kernel<D, NT>,
                          dim3(ctas, static_cast<unsigned>(min64(a.group, S::kHeads))),
-                         32 * paged::kJoinWarps, 1, 0, stream, a);
+                         32 * paged::kJoinWarps, 0, stream, a);
 }
 
 }  // namespace
