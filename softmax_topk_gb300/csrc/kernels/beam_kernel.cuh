@@ -37,9 +37,9 @@ using u64 = unsigned long long;
 constexpr int kThreads = 256;   // of a run's CTA
 constexpr int kBlocks = 4;      // 16-byte blocks per thread and tile
 constexpr int kSegmentCols = 1 << 16;  // columns between two selections
-constexpr int kList = 512;      // values that reach the bound; more go another way
+constexpr int kList = 1024;     // values that reach the bound; more go another way
 constexpr int kGroups = 512;    // threads' shares of a tile that do
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = kThreads;
 constexpr int kHelpers = 8;     // CTAs of a group, at most
 constexpr int kCandidates = 1024;
 constexpr int kMaxBeams = 64;
@@ -79,44 +79,33 @@ __device__ __forceinline__ float factor(float x, float m) {
     return x == m ? 1.f : exp1(x - m);
 }
 
-// The best KP parts' least maximum; every thread gets it.  KP is a power of two
-// of 8 to 64: the threads' maxima are joined in parts of kThreads / KP threads.
-template <int KP, int THREADS, typename V, typename Max>
-__device__ __forceinline__ V parts_bound(V v, V* sh, Max larger) {
-    constexpr int kPart = THREADS / KP;
-    static_assert(KP <= 64, "parts");
-    const int tid = threadIdx.x;
-    if constexpr (kPart <= 32) {
+// The least of the maxima of KP parts of the CTA's values (as order keys); every thread
+// gets it.  Thread t is of part t mod KP, so that neighbouring columns are of different
+// parts and a short row fills them all.  sh: a word per thread.
+template <int KP>
+__device__ __forceinline__ uint32_t parts_bound(uint32_t v, uint32_t* sh) {
+    constexpr int kLanes = KP < 32 ? KP : 32, kWarps = kThreads / 32;
+    const int lane = threadIdx.x % 32;
 #pragma unroll
-        for (int o = kPart / 2; o > 0; o >>= 1) v = larger(v, __shfl_xor_sync(kFullMask, v, o));
-        if (tid % kPart == 0) sh[tid / kPart] = v;
-    } else {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v = larger(v, __shfl_xor_sync(kFullMask, v, o));
-        if (tid % 32 == 0) sh[tid / 32] = v;
-        __syncthreads();
-        // parts of several warps: their first ones' places take the maximum
-        if (tid < KP)
-            for (int i = 1; i < kPart / 32; ++i)
-                sh[64 + tid] = i == 1 ? larger(sh[tid * (kPart / 32)], sh[tid * (kPart / 32) + 1])
-                                      : larger(sh[64 + tid], sh[tid * (kPart / 32) + i]);
-        sh += 64;
-    }
+    for (int o = 16; o >= kLanes; o >>= 1) v = max(v, __shfl_xor_sync(kFullMask, v, o));
+    sh[threadIdx.x] = v;
     __syncthreads();
-    V least = sh[(tid & 31) % KP];
-    if (KP > 32) {
-        const V other = sh[32 + (tid & 31) % (KP > 32 ? KP - 32 : 1)];
-        least = larger(least, other) == least ? other : least;
+    // 64 parts: the even warps have the first 32 of them, the odd ones the others
+    constexpr int kSets = KP > 32 ? 2 : 1;
+    uint32_t least = 0xffffffffu;
+#pragma unroll
+    for (int set = 0; set < kSets; ++set) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int w = set; w < kWarps; w += kSets) top = max(top, sh[w * 32 + lane]);
+        least = min(least, top);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const V other = __shfl_xor_sync(kFullMask, least, o);
-        least = larger(least, other) == least ? other : least;
-    }
+    for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(kFullMask, least, o));
     return least;
 }
 
-// Tiles on their way to a CTA, what it keeps of them, and its list: 70 KB for fp32, 62 for
+// Tiles on their way to a CTA, what it keeps of them, and its list: 75 KB for fp32, 67 for
 // bf16, so that three CTAs fit an SM.
 template <typename T>
 struct RunShared {
@@ -126,7 +115,7 @@ struct RunShared {
     float top[kSegment][kThreads];  // the largest of a thread's columns of a tile
     u64 list[kList];
     u64 sorted[kMaxK];
-    uint32_t bound[128];
+    uint32_t bound[kThreads];
     u64 best[kThreads / 32];
     float m[kThreads / 32], d[kThreads / 32];
     uint16_t group[kGroups];
@@ -424,8 +413,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         // ---- the K best so far: a bound that K values of the segment reach (-inf is no
         // continuation); with a full list, one past its K-th (a later column has to be larger)
         if (tid == 0) sh.count = held, sh.groups = 0;
-        uint32_t least = parts_bound<KP, kThreads>(order_key(largest), sh.bound,
-                                                   [](uint32_t x, uint32_t y) { return max(x, y); });
+        uint32_t least = parts_bound<KP>(order_key(largest), sh.bound);
         least = max(least, sample::kKeyNegInf + 1);
         if (held == a.K) least = max(least, static_cast<uint32_t>(sh.list[a.K - 1] >> 32) + 1);
         const float bound = key_value(least);
@@ -514,7 +502,7 @@ struct MergeShared {
     double score[kMaxBeams];
     float m[kMaxBeams], near[kMaxBeams];  // near: the offset in fp32
     unsigned char kind[kMaxBeams];  // 0 no candidates, 1 a row, 2 ended
-    uint32_t bound[128];
+    uint32_t bound[kMergeThreads];
     u64 warp_order[kMergeThreads / 32], warp_at[kMergeThreads / 32];
     u64 sum[kMergeThreads / 32];
     u64 slice[kMaxBeams][kHelpers];  // a row's summed weights, from each CTA of the cluster
@@ -631,11 +619,10 @@ __global__ void __launch_bounds__(kMergeThreads)
     __syncthreads();
     if (a.helpers > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     // ---- the lists' entries, entry by entry of all lists: a thread's first ones stay in
-    // registers.  Threads take them so that the parts of the bound get equal shares.
+    // registers.
     const int lists = a.beams * a.runs, entries = lists * a.K;
     const u64* keys = a.lists + group * entries;
-    constexpr int kPart = kMergeThreads / KP, kHeld = 4;
-    const int turn = tid / kPart + KP * (tid % kPart);
+    constexpr int kHeld = 4;
     // (entry e of the lists begins with list e, so that a part's entries are of many lists)
     auto list_of = [&](int i) {
         const int e = i / lists;
@@ -645,7 +632,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     int mine_of[kHeld];
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
-        const int i = turn + j * kMergeThreads;
+        const int i = tid + j * kMergeThreads;
         mine_of[j] = i < entries ? list_of(i) : -1;
         mine[j] = i < entries ? __ldcg(keys + i / lists * lists + mine_of[j]) : 0;
     }
@@ -692,9 +679,9 @@ __global__ void __launch_bounds__(kMergeThreads)
         };
 #pragma unroll
         for (int j = 0; j < kHeld; ++j)
-            if (mine_of[j] >= 0) one(turn + j * kMergeThreads, mine_of[j], mine[j]);
+            if (mine_of[j] >= 0) one(tid + j * kMergeThreads, mine_of[j], mine[j]);
 #pragma unroll 1
-        for (int i = turn + kHeld * kMergeThreads; i < entries; i += kMergeThreads) {
+        for (int i = tid + kHeld * kMergeThreads; i < entries; i += kMergeThreads) {
             const int list = list_of(i);
             one(i, list, __ldcg(keys + i / lists * lists + list));
         }
@@ -730,8 +717,7 @@ __global__ void __launch_bounds__(kMergeThreads)
             const float c = rough(key, beam, slack) - slack;
             top = fmaxf(top, c);
         });
-        float bound = key_value(parts_bound<KP, kMergeThreads>(
-            order_key(top), sh.bound, [](uint32_t x, uint32_t y) { return max(x, y); }));
+        float bound = key_value(parts_bound<KP>(order_key(top), sh.bound));
         bound -= 4 * a.eps + fabsf(bound) * 0x1p-22f;
         each([&](u64 key, int beam) {
             const float c = rough(key, beam, slack) + slack;

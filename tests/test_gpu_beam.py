@@ -179,3 +179,12 @@ def test_buffers_and_refusals(st):
             (st.OsError, (x, s, 2 ** 32 + 4), {})):
         with pytest.raises(error):
             st.beam_select(*args, **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cols", [511, 513, 600, 1105, 1793, 2000, 4095, 9297])
+@pytest.mark.parametrize("K", [1, 8, 17, 64])
+def test_rows_that_fill_a_tile_in_part(st, dtype, cols, K):
+    """A bound that K values reach, where only some threads have columns."""
+    x, s = logits(6, cols, seed=cols, dtype=dtype)
+    check(st, x, s.view(2, 3), K)
