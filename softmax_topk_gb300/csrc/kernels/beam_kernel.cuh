@@ -539,7 +539,7 @@ __device__ __forceinline__ sample::Weight row_weights(float m, int64_t cols, con
 template <typename T>
 __device__ u64 exact_sum(MergeShared& sh, const sample::Weight& w, const T* row, int64_t from,
                          int64_t to) {
-    constexpr int kAtOnce = 8;
+    constexpr int kAtOnce = 16;
     u64 sum = 0;
 #pragma unroll 1
     for (int64_t c = from + threadIdx.x; c < to; c += kAtOnce * kMergeThreads) {
