@@ -379,7 +379,8 @@ os_status os_sample(const void *x, const float *u, const os_sampling *s, int32_t
  *   pages >= 1, seqs >= 0, width >= 1, kv_heads >= 1, page_size >= 1, head_dim
  *   64 or 128; pages * kv_heads * page_size, width * page_size and seqs *
  *   (query or key heads) at most 2^31 - 1 (OS_ERR_SHAPE).
- * The struct itself is read on the host during the call.
+ * The struct itself is read on the host during the call; what it points to may
+ * not change while a call works on it.
  */
 typedef struct {
     void *k, *v;
@@ -400,8 +401,8 @@ typedef struct {
  *             elements apart (multiples of 8, at least the row); 16-byte
  *             aligned.  They may be slices of one projection's result.
  *   q, q_out  [tokens] rows of q_heads x head_dim bf16, q_stride apart, and the
- *             rotated queries, dense; or both NULL (q_heads and q_stride are
- *             then not looked at).
+ *             rotated queries, dense; q_heads at least kv_heads (OS_ERR_SHAPE).
+ *             Or both NULL (q_heads and q_stride are then not looked at).
  *   starts    [seqs + 1] int32, not falling; or NULL: one new token per sequence
  *             (tokens == seqs, OS_ERR_SHAPE otherwise).
  *   inv_freq  [rot / 2] fp32, finite; or NULL: no rotation (rot is then not
@@ -496,9 +497,11 @@ os_status os_paged_reorder(const os_paged_cache *cache, const int32_t *parents,
  *   beams, K 1 to 64 (OS_ERR_SHAPE, OS_ERR_K); pad 0 to cols - 1 (OS_ERR_VALUE);
  *            groups >= 0, groups * beams at most 2^26.
  * Logits of -inf and NaN are no continuations; +inf ones share their row's
- * probability evenly.  Choices are those of real arithmetic: beams whose sums in
- * fp32 leave the order open are summed again to 2^-38.  Outputs and workspace may
- * not overlap the inputs or each other (OS_ERR_ALIAS).
+ * probability evenly.  Choices are those of real arithmetic up to the sums'
+ * precision: beams whose sums in fp32 leave the order open are summed again,
+ * each weight to 2^-38 of itself and 2^-45 of the row's largest (2^-32 for the
+ * longest rows), as integers, so that equal rows have equal sums.  Outputs and
+ * workspace may not overlap the inputs or each other (OS_ERR_ALIAS).
  */
 os_status os_beam_select(const void *x, const float *scores, const uint8_t *ended, float *out,
                          int32_t *parents, int32_t *tokens, void *workspace, int64_t groups,

@@ -493,6 +493,17 @@ __global__ void __launch_bounds__(kThreads, 3)
 }
 
 // ------------------------------------------------------------------ the groups
+// A sum of integers of 64 bits: high * 2^32 + low, each the sum of the halves.
+struct Sum {
+    u64 high, low;
+    __device__ __forceinline__ void add(Sum s) { high += s.high, low += s.low; }
+    // (from the parts' only form with low below 2^32, so that equal sums are equal doubles)
+    __device__ __forceinline__ double value() const {
+        return static_cast<double>(high + (low >> 32)) * 4294967296.0 +
+               static_cast<double>(low & 0xffffffffu);
+    }
+};
+
 struct MergeShared {
     ulonglong2 found[kCandidates];            // a value's order; its beam and column
     u64 best[kMaxK], best_at[kMaxK];          // the chosen, in order
@@ -504,8 +515,8 @@ struct MergeShared {
     unsigned char kind[kMaxBeams];  // 0 no candidates, 1 a row, 2 ended
     uint32_t bound[kMergeThreads];
     u64 warp_order[kMergeThreads / 32], warp_at[kMergeThreads / 32];
-    u64 sum[kMergeThreads / 32];
-    u64 slice[kMaxBeams][kHelpers];  // a row's summed weights, from each CTA of the cluster
+    Sum sum[kMergeThreads / 32];
+    Sum slice[kMaxBeams][kHelpers];  // a row's summed weights, from each CTA of the cluster
     u64 todo;                        // rows to be summed again
     float pow2[64];
     int count;
@@ -527,20 +538,25 @@ __device__ __forceinline__ bool better(u64 c, u64 at, u64 c2, u64 at2) {
     return c > c2 || (c == c2 && at < at2);
 }
 
-__device__ __forceinline__ sample::Weight row_weights(float m, int64_t cols, const float* pow2) {
-    int bits = 62;
-    while ((int64_t(1) << (62 - bits)) < cols) --bits;
+// A row's weights as multiples of 2^-bits, so that a thread's sum of its share of the
+// columns stays below 2^62.
+__device__ __forceinline__ sample::Weight row_weights(float m, int64_t cols, int helpers,
+                                                      const float* pow2) {
+    const int64_t share = cols / (int64_t(kMergeThreads) * helpers) + 1;
+    int bits = 44;
+    while (bits > 31 && share >> (62 - bits)) --bits;
     sample::Weight w;
-    w.set(m, 1.f, min(44, bits), pow2);
+    w.set(m, 1.f, bits, pow2);
     return w;
 }
 
-// The weights e^(x - m) of columns [from, to) of a row, summed as integers.
+// The weights e^(x - m) of columns [from, to) of a row, summed as integers; thread 0 has
+// the result.
 template <typename T>
-__device__ u64 exact_sum(MergeShared& sh, const sample::Weight& w, const T* row, int64_t from,
+__device__ Sum exact_sum(MergeShared& sh, const sample::Weight& w, const T* row, int64_t from,
                          int64_t to) {
     constexpr int kAtOnce = 16;
-    u64 sum = 0;
+    u64 mine = 0;
 #pragma unroll 1
     for (int64_t c = from + threadIdx.x; c < to; c += kAtOnce * kMergeThreads) {
         float x[kAtOnce];
@@ -548,15 +564,13 @@ __device__ u64 exact_sum(MergeShared& sh, const sample::Weight& w, const T* row,
         for (int i = 0; i < kAtOnce; ++i)
             x[i] = c + i * kMergeThreads < to ? static_cast<float>(row[c + i * kMergeThreads])
                                               : -INFINITY;
-        sum += w.sum_from(x, -FLT_MAX);
+        mine += w.sum_from(x, -FLT_MAX);
     }
-    sum = sample::warp_sum64(sum);
+    Sum sum = {sample::warp_sum64(mine >> 32), sample::warp_sum64(mine & 0xffffffffu)};
     __syncthreads();
     if (threadIdx.x % 32 == 0) sh.sum[threadIdx.x / 32] = sum;
     __syncthreads();
-    sum = 0;
-#pragma unroll
-    for (int i = 0; i < kMergeThreads / 32; ++i) sum += sh.sum[i];
+    for (int i = 1; threadIdx.x == 0 && i < kMergeThreads / 32; ++i) sum.add(sh.sum[i]);
     return sum;
 }
 
@@ -585,14 +599,16 @@ __global__ void __launch_bounds__(kMergeThreads)
                 const uint32_t at = map_to_rank(&sh.m[i], 0);
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(m) : "r"(at) : "memory");
             }
-            const sample::Weight w = row_weights(m, a.cols, sh.pow2);
-            const u64 sum =
+            const sample::Weight w = row_weights(m, a.cols, a.helpers, sh.pow2);
+            const Sum sum =
                 exact_sum(sh, w, static_cast<const T*>(a.x) + (row0 + i) * a.cols, rank * each,
                           min(a.cols, (rank + 1) * each));
             if (tid) continue;
             if (rank) {
                 const uint32_t at = map_to_rank(&sh.slice[i][rank], 0);
-                asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(at), "l"(sum) : "memory");
+                asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(at), "l"(sum.high) : "memory");
+                asm volatile("st.shared::cluster.u64 [%0], %1;"
+                             :: "r"(at + 8), "l"(sum.low) : "memory");
             } else {
                 sh.slice[i][0] = sum;
             }
@@ -810,10 +826,10 @@ __global__ void __launch_bounds__(kMergeThreads)
         sum_rows(todo);
         group_sync(a.helpers);
         if (tid < a.beams && (todo >> tid & 1)) {
-            const sample::Weight w = row_weights(sh.m[tid], a.cols, sh.pow2);
-            u64 sum = 0;
-            for (int i = 0; i < a.helpers; ++i) sum += sh.slice[tid][i];
-            sh.lse[tid] = log(static_cast<double>(sum) / static_cast<double>(w(sh.m[tid])));
+            const sample::Weight w = row_weights(sh.m[tid], a.cols, a.helpers, sh.pow2);
+            Sum sum = {0, 0};
+            for (int i = 0; i < a.helpers; ++i) sum.add(sh.slice[tid][i]);
+            sh.lse[tid] = log(sum.value() / static_cast<double>(w(sh.m[tid])));
         }
     }
     if (tid < a.K) {

@@ -188,3 +188,18 @@ def test_rows_that_fill_a_tile_in_part(st, dtype, cols, K):
     """A bound that K values reach, where only some threads have columns."""
     x, s = logits(6, cols, seed=cols, dtype=dtype)
     check(st, x, s.view(2, 3), K)
+
+
+def test_long_rows(st):
+    """More than 2^22 columns: runs of many tiles, sums of many segments; equal rows tie."""
+    cols = 5_000_011
+    x, _ = logits(1, cols, seed=21, dtype=torch.bfloat16)
+    x = torch.cat([x, x.flip(1), x])
+    s = torch.tensor([[-3.0, -3.25, -3.0]], device="cuda")
+    got = st.beam_select(x, s, 9)
+    want = ref.beam_select(x[:2], s[:, :2], 9)[0]
+    # beams 0 and 2 are equal: each of beam 0's columns comes in both, the lower beam first
+    assert got[1][0, :2].tolist() == [0, 2] and got[2][0, 0] == got[2][0, 1]
+    assert abs(float(got[0][0, 0]) - want[0, 0]) <= 200 * 2.0 ** -23 + 2.0 ** -24 * abs(want[0, 0])
+    both = got[0][0][got[1][0] != 1]
+    assert torch.equal(both[0:2 * (len(both) // 2):2], both[1:2 * (len(both) // 2):2])

@@ -291,3 +291,45 @@ def test_graph_with_other_lengths(st):
         graph.replay()
         want = st.paged_attention(q, k, v, table, lengths)
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+COLD = """
+import torch
+import softmax_topk_gb300 as st
+g = torch.Generator(device="cuda")
+g.manual_seed(1)
+def randn(*shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+k, v = (randn(120, 2, 16, 64).bfloat16() for _ in range(2))
+table = torch.arange(60, device="cuda").int().view(2, 30).contiguous()
+lengths = torch.tensor([480, 33], device="cuda").int()
+q, kn = randn(2, 4, 64).bfloat16(), randn(2, 2, 64).bfloat16()
+inv = torch.ones(32, device="cuda")
+x, s = randn(2, 9000), torch.zeros(1, 2, device="cuda")
+new = table + 60  # pages of the sequences' own
+def step():
+    q2 = st.paged_append(k, v, table, lengths, kn, kn, q=q, inv_freq=inv)
+    out, lse = st.paged_attention(q2, k, v, table, lengths)
+    some = st.beam_select(x, s, 2)
+    return [q2, out, lse, *some, *st.paged_reorder(k, v, table, lengths, some[1], new)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+print("same")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first call of every operator is recorded into a graph."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", COLD], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stdout + r.stderr
