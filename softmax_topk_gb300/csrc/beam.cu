@@ -83,7 +83,13 @@ cudaError_t launch_beam_select(const BeamSelectArgs& p, cudaStream_t stream) {
     // the CTAs of a group share the exact sums, where there are SMs for them
     a.helpers = beam::kHelpers;
     while (a.helpers > 1 && p.groups * a.helpers > 2 * dev->sms) a.helpers /= 2;
-    a.eps = 36 * 0x1p-23f;
+    // What the first kernel's ln d can be off, in units u of 2^-23: an exponent's rounding
+    // (above 2^-32: half a step of 2^-19 times ln 2) 5.8, log2 e in one part 2.5, ex2.approx 2,
+    // the factor of the rounded reference 2.5; sums of a tile's 32 values 5, of tiles
+    // (compensated) 1, changes of the reference 2.4; threads to a warp 4.5, warps to a run 3,
+    // runs to a row 4, the logarithm 0.5: 33.2.  Smaller weights are below 2^-32 of the
+    // largest and add at most 4 in the longest rows.
+    a.eps = 40 * 0x1p-23f;
     return p.in == OS_F32 ? launch_k<float>(a, p.groups, stream)
                           : launch_k<__nv_bfloat16>(a, p.groups, stream);
 }

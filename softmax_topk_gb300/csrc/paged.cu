@@ -10,8 +10,9 @@ namespace {
 
 template <int D, bool INTERLEAVED>
 cudaError_t append(const paged::AppendArgs& a, cudaStream_t stream) {
-    // one token per CTA until the GPU is full of them, then four: angles and
-    // places are worked out for all at once
+    // One token per CTA until the GPU is full of them, then four: angles and places
+    // are worked out for all at once.  us with one / four: 512 tokens 3.6 / 4.1, 1000
+    // 5.3 / 5.6, 2400 8.7 / 7.7, 5000 16.3 / 13.0, 36000 92 / 69 (16 + 8 heads of 128).
     const DeviceInfo* dev = device_info();
     if (!dev) return cudaErrorInvalidDevice;
     const int per_cta = a.tokens >= 16 * int64_t(dev->sms) ? paged::kAppendTokens : 1;

@@ -8,7 +8,9 @@ namespace os {
 
 namespace {
 
-// Blocks that a CTA should have at least: fewer CTAs leave fewer pieces to join.
+// Blocks that a CTA should have at least: fewer CTAs leave fewer pieces to join.  us with
+// 2, 4, 8, 16 blocks, 2 key heads: 300 keys 6.5 / 6.2 / 7.0 / 7.6, 1000 keys 7.2 / 6.8 /
+// 7.4 / 8.3, 3000 keys 9.4 / 8.2 / 7.9 / 8.5.
 constexpr int kMinBlocks = 4;
 
 template <int D, int NT>

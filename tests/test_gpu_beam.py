@@ -2,8 +2,8 @@
 
 Beams and columns are those of real arithmetic, so they are compared exactly; the inputs are drawn
 so that distinct values of different beams differ by more than 2^-30, or are equal throughout.
-Values are good to their rounding (2^-24 of the value) and the sums' error of lse, which for rows
-of up to 40 tiles of 4096 columns is below (40 + 80) 2^-23."""
+Values are good to their rounding (2^-24 of the value) and the sums' error of lse, which is below
+40 units of 2^-23 (120 are allowed)."""
 import numpy as np
 import pytest
 import torch
