@@ -168,7 +168,7 @@ struct Tile {
     }
     // The block from column c on, read anew.
     __device__ __forceinline__ uint4 block(uint32_t c) const {
-        if (whole(c)) return __ldg(reinterpret_cast<const uint4*>(row + c));
+        if (whole(c)) return *reinterpret_cast<const uint4*>(row + c);
         uint32_t words[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

@@ -144,7 +144,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 __device__ __forceinline__ int used_length(const AttnArgs& a, int b) {
-    const int len = __ldg(a.lengths + b);
+    const int len = a.lengths[b];
     return max(0, min(len, a.width * a.split.size));
 }
 
@@ -178,7 +178,7 @@ struct Key {
         const int key = c.j * kBlock + (lane & 15);
         const int at = a.split.page(key);
         page = -1;
-        if (key < c.len) page = __ldg(a.table + static_cast<int64_t>(c.b) * a.width + at);
+        if (key < c.len) page = a.table[static_cast<int64_t>(c.b) * a.width + at];
         in = c.h * a.split.size + key - at * a.split.size;
     }
     // the pool's row, or -1: no such page

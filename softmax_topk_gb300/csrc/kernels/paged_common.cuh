@@ -8,7 +8,9 @@ namespace os {
 // The kernels of a decode step follow one another on a stream.  Each is launched so that
 // it may be put in place while the one before it still runs (launch_behind): wait_before
 // holds it until that one has ended and its writes are seen, let_next lets the one behind
-// it come as soon as every CTA has called it.
+// it come as soon as every CTA has called it.  What the one before may have written is read
+// by plain loads: for those of the read-only path the compiler may take it that nothing
+// writes there while the kernel runs, its wait included, and move them before the wait.
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;"); }
 

@@ -45,12 +45,12 @@ constexpr int kAppendTokens = 4;  // at most, per CTA
 // The last sequence that starts at or before token t (those without tokens end
 // before it), or -1 where t is behind the last sequence or before the first.
 __device__ __forceinline__ int sequence_of(const int* starts, int seqs, int64_t t, int lane) {
-    if (t < __ldg(starts) || t >= __ldg(starts + seqs)) return -1;
+    if (t < *starts || t >= starts[seqs]) return -1;
     int lo = 0, hi = seqs;  // starts[lo] <= t < starts[hi]
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
         const int at = lo + (lane + 1) * step;
-        const unsigned ok = __ballot_sync(kFullMask, at < hi && __ldg(starts + at) <= t);
+        const unsigned ok = __ballot_sync(kFullMask, at < hi && starts[at] <= t);
         const int below = __popc(ok);
         const int nlo = lo + below * step;
         hi = min(hi, nlo + step);
@@ -75,12 +75,12 @@ __global__ void __launch_bounds__(kAppendThreads)
         if (t < a.tokens) {
             const int b = a.starts ? sequence_of(a.starts, a.seqs, t, lane) : static_cast<int>(t);
             if (b >= 0) {
-                const int64_t p = a.starts ? t + __ldg(a.lengths + b) - __ldg(a.starts + b + 1)
-                                           : static_cast<int64_t>(__ldg(a.lengths + b)) - 1;
+                const int64_t p = a.starts ? t + a.lengths[b] - a.starts[b + 1]
+                                           : static_cast<int64_t>(a.lengths[b]) - 1;
                 pos = static_cast<int>(min(max(p, int64_t(-1)), int64_t(INT_MAX)));
                 if (pos >= 0 && pos < a.width * a.split.size) {
                     const int at = a.split.page(pos);
-                    const int page = __ldg(a.table + static_cast<int64_t>(b) * a.width + at);
+                    const int page = a.table[static_cast<int64_t>(b) * a.width + at];
                     if (static_cast<unsigned>(page) < static_cast<unsigned>(a.pages))
                         row = page * a.kv_heads * a.split.size + pos - at * a.split.size;
                 }
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     for (int i = tid; i < per_cta * half; i += kAppendThreads) {
         const int w = i / half, f = i % half;
         const double turns = static_cast<double>(max(pos_sh[w], 0)) *
-                             (static_cast<double>(__ldg(a.inv_freq + f)) * 0.15915494309189535);
+                             (static_cast<double>(a.inv_freq[f]) * 0.15915494309189535);
         const float part = static_cast<float>(turns - rint(turns));
         float s, c;
         sincospif(2.f * part, &s, &c);
@@ -190,19 +190,29 @@ __global__ void __launch_bounds__(kReorderThreads)
     const int part = blockIdx.x / a.seqs;  // (layer, head)
     wait_before();
     let_next();
-    const int parent = __ldg(a.parents + j);
+    const int parent = a.parents[j];
     const bool alive = static_cast<unsigned>(parent) < static_cast<unsigned>(a.beams);
     const int p = alive ? j / a.beams * a.beams + parent : j;
-    const int len = alive ? max(0, min(__ldg(a.lengths + p), a.width * a.split.size)) : 0;
+    const int len = alive ? max(0, min(a.lengths[p], a.width * a.split.size)) : 0;
     const int full = a.split.page(len), rest = len - full * a.split.size;
     const int* old_row = a.table + static_cast<int64_t>(p) * a.width;
     int* new_row = a.out_table + static_cast<int64_t>(j) * a.width;
     if (part == 0) {
-        for (int i = tid; i < full; i += kReorderThreads) new_row[i] = __ldg(old_row + i);
+        // (eight on their way at a time: the tables do not overlap)
+        constexpr int kEntries = 8;
+        for (int i0 = tid; i0 < full; i0 += kEntries * kReorderThreads) {
+            int page[kEntries];
+#pragma unroll
+            for (int x = 0; x < kEntries; ++x)
+                if (i0 + x * kReorderThreads < full) page[x] = old_row[i0 + x * kReorderThreads];
+#pragma unroll
+            for (int x = 0; x < kEntries; ++x)
+                if (i0 + x * kReorderThreads < full) new_row[i0 + x * kReorderThreads] = page[x];
+        }
         if (tid == 0 && a.out_lengths) a.out_lengths[j] = len;
     }
     if (rest == 0) return;
-    const int from = __ldg(old_row + full), to = new_row[full];
+    const int from = old_row[full], to = new_row[full];
     if (static_cast<unsigned>(from) >= static_cast<unsigned>(a.pages) ||
         static_cast<unsigned>(to) >= static_cast<unsigned>(a.pages) || from == to)
         return;

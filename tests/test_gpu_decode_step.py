@@ -293,6 +293,43 @@ def test_graph_with_other_lengths(st):
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+def test_what_the_kernel_before_wrote(st):
+    """Calls that may be put in place early still read what the kernels just before them write."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=g, device="cuda")
+
+    k, v = (randn(300, 2, 16, 64).bfloat16() for _ in range(2))
+    tables = [torch.randint(0, 200, (8, 20), generator=g, device="cuda").int() for _ in range(4)]
+    lengths = [torch.randint(0, 321, (8,), generator=g, device="cuda").int() for _ in range(4)]
+    own = torch.arange(200, 296, device="cuda").int().view(8, 12)
+    queries = [randn(8, 4, 64).bfloat16() for _ in range(4)]
+    parents = [torch.randint(0, 4, (2, 4), generator=g, device="cuda").int() for _ in range(4)]
+    table, length, q = (torch.zeros_like(x[0]) for x in (tables, lengths, queries))
+    parent, out_table = torch.zeros_like(parents[0]), torch.zeros_like(tables[0])
+
+    def run(wait):
+        got = []
+        for i in range(40):
+            q.copy_(queries[i % 4])
+            table.copy_(tables[i % 3])
+            length.copy_(lengths[i % 4])
+            wait()
+            got += [t.clone() for t in st.paged_attention(q, k, v, table, length)]
+            out_table.fill_(-1)
+            out_table[:, 8:] = own
+            parent.copy_(parents[i % 4])
+            wait()
+            got += [t.clone() for t in st.paged_reorder(k, v, table, length, parent, out_table)]
+            wait()
+        return got
+
+    want = run(torch.cuda.synchronize)
+    assert same(run(lambda: None), want)
+
+
 COLD = """
 import torch
 import softmax_topk_gb300 as st
