@@ -148,13 +148,18 @@ __device__ __forceinline__ int used_length(const AttnArgs& a, int b) {
     return max(0, min(len, a.width * a.split.size));
 }
 
+// (a length may be near 2^31)
+__device__ __forceinline__ int blocks_in(int len) {
+    return static_cast<int>((static_cast<unsigned>(len) + kBlock - 1) / kBlock);
+}
+
 // A place in the line of blocks: block j of query heads' chunk c of key head h of
 // sequence b.
 struct Cursor {
     int b, h, c, j, blocks, len;
     __device__ __forceinline__ void sequence(const AttnArgs& a) {
         len = used_length(a, b);
-        blocks = (len + kBlock - 1) / kBlock;
+        blocks = blocks_in(len);
     }
     __device__ __forceinline__ void next(const AttnArgs& a) {
         if (++j < blocks) return;
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
     // the usual numbers of sequences takes less time than waiting for others
     if (lane < 2) sh.unit[lane][warp] = -1;
     auto blocks_of = [&](int b) {
-        return b < a.seqs ? (used_length(a, b) + kBlock - 1) / kBlock : 0;
+        return b < a.seqs ? blocks_in(used_length(a, b)) : 0;
     };
     auto scanned = [&](int v) {
 #pragma unroll

@@ -123,6 +123,25 @@ def test_attention_lengths_past_the_table(st):
     check_attention(st, pool, pool.randn(2, 3, 64).bfloat16())
 
 
+def test_attention_longest(st):
+    """A length of 2^31 - 2, all pages but the first and the last not there: those two are the
+    same page, so that its keys count twice."""
+    page, width = 662, 3243933  # their product is 2^31 - 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    k, v = (torch.randn(1, 1, page, 64, generator=g, device="cuda").bfloat16() for _ in range(2))
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[0, 0] = table[0, -1] = 0
+    q = torch.randn(1, 2, 64, generator=g, device="cuda").bfloat16()
+    out, lse = st.paged_attention(q, k, v, table, torch.tensor([2 ** 31 - 1]).int().cuda())
+    s = k[0, 0].double() @ q[0].double().T / 8
+    w = s.softmax(0)
+    want, weighted = w.T @ v[0, 0].double(), w.T @ v[0, 0].double().abs()
+    err = (out[0].double() - want).abs()
+    assert bool((err <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * weighted).all()), float(err.max())
+    assert float((lse[0].double() - s.logsumexp(0) - np.log(2)).abs().max()) <= 2.0 ** -11
+
+
 def test_attention_of_large_scores(st):
     """Scores that rise and fall by hundreds: the running maximum is raised again and again."""
     pool = Pool([700, 700], 1, 16, 64)
