@@ -441,6 +441,9 @@ os_status os_paged_append(const os_paged_cache *cache, const void *k, int64_t k_
  *   scale     finite and > 0 (OS_ERR_VALUE).
  * Outputs and workspace may not overlap the inputs or each other (OS_ERR_ALIAS).
  * What the cache holds behind the lengths is not used, whatever its bits.
+ * A head with a score that is NaN or +inf gets NaN, in O and L; an infinity or NaN
+ * among the values used leaves its dimension of O without a finite value (an infinity
+ * or NaN), for all heads that use it.
  * Arithmetic: products on the tensor cores from bf16 operands with fp32 sums;
  * weights in fp32, as the sum of two bf16 numbers (2^-17) in the second product;
  * O rounded once to bf16.  A sequence's keys may be split over the

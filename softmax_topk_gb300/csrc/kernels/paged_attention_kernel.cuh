@@ -193,10 +193,13 @@ struct Key {
     }
 };
 
-// One head's row of O, m and l: the result, rounded once.
+// One head's L from m and l; without keys -inf, and NaN where a score was one.
 __device__ __forceinline__ void store_lse(const AttnArgs& a, int row, float m, float l) {
-    if (a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2f : -INFINITY;
+    if (a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2f;
 }
+
+// What O's sums are multiplied by.
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
 // A piece's weight beside the joined maximum; a piece without keys has none.
 __device__ __forceinline__ float piece_weight(float m, float joined) {
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
                         for (int e = 0; e < 2; ++e) {
                             const int head = nt * 8 + 2 * t + e;
                             if (head0 + head >= a.group) continue;
-                            const float f = l[nt][e] > 0.f ? 1.f / l[nt][e] : 0.f;
+                            const float f = inverse(l[nt][e]);
                             if (g == 0) store_lse(a, row0 + head, m[nt][e], l[nt][e]);
                             __nv_bfloat16* to =
                                 a.out + static_cast<int64_t>(row0 + head) * D + g;
@@ -576,7 +579,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
                     to[S::kL + head] = sum;
                 }
             } else {
-                const float f = sum > 0.f ? 1.f / sum : 0.f;
+                const float f = inverse(sum);
 #pragma unroll
                 for (int x = 0; x < D / 32; x += 2)
                     *reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(row0 + head) * D +
@@ -662,7 +665,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
         value += f * acc_sh[w][d];
     }
     const int row = tail.x + head;
-    a.out[static_cast<int64_t>(row) * D + d] = __float2bfloat16(all > 0.f ? value / all : 0.f);
+    a.out[static_cast<int64_t>(row) * D + d] = __float2bfloat16(all == 0.f ? 0.f : value / all);
     if (d == 0) store_lse(a, row, top, all);
 }
 

@@ -155,6 +155,30 @@ def test_attention_of_large_scores(st):
     check_attention(st, pool, q, scale=1.0)
 
 
+@pytest.mark.parametrize("length", [40, 20000])
+def test_attention_not_a_number(st, length):
+    """A head whose scores are NaN or +inf has NaN in O and in L, the others what they had;
+    a dimension with an infinite value is not finite (a weight's two parts times it are infinities
+    of either sign, or NaN for a part of 0)."""
+    pool = Pool([length, length], 2, 16, 64)
+    q = pool.randn(2, 8, 64).bfloat16()
+    args = (pool.k, pool.v, pool.table, pool.lengths)
+    want, want_lse = st.paged_attention(q, *args)
+    q[0, 1, 5] = NAN
+    q[1, 4] = 3e38
+    at = pool.table[1, (length - 1) // 16].long(), 1, (length - 1) % 16
+    pool.k[at] = 3e38  # a score of +inf for head 4 of sequence 1, whose key head is 1
+    out, lse = st.paged_attention(q, *args)
+    assert out[0, 1].isnan().all() and lse[0, 1].isnan()
+    assert out[1, 4].isnan().all() and lse[1, 4].isnan()
+    for b, h in [(0, 0), (0, 2), (0, 3), (0, 4), (0, 7), (1, 0), (1, 3)]:
+        assert torch.equal(out[b, h], want[b, h]) and lse[b, h] == want_lse[b, h], (b, h)
+    pool.v[pool.table[0, 0].long(), 1, 3, 17] = INF
+    out, lse = st.paged_attention(q, *args)
+    assert not out[0, 4:, 17].isfinite().any() and torch.equal(out[0, 4:, :17], want[0, 4:, :17])
+    assert torch.equal(out[0, 4:, 18:], want[0, 4:, 18:]) and torch.equal(lse[0, 4:], want_lse[0, 4:])
+
+
 def test_attention_shared_pages(st):
     """Sequences that share pages, as beams do."""
     pool = Pool([90] * 4, 2, 16, 128)
