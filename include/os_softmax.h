@@ -376,8 +376,8 @@ os_status os_sample(const void *x, const float *u, const os_sampling *s, int32_t
  *             step's append among them (one tensor serves the append and the
  *             attention behind it).  Below 0 counts as 0, above width *
  *             page_size as that.
- *   pages >= 1, seqs >= 0, width >= 1, kv_heads >= 1, page_size >= 1, head_dim
- *   64 or 128; pages * kv_heads * page_size, width * page_size and seqs *
+ *   pages >= 1, seqs >= 0, width >= 1, kv_heads 1 to 2^20, page_size 1 to 2^24,
+ *   head_dim 64 or 128; pages * kv_heads * page_size, width * page_size and seqs *
  *   (query or key heads) at most 2^31 - 1 (OS_ERR_SHAPE).
  * The struct itself is read on the host during the call; what it points to may
  * not change while a call works on it.
@@ -488,7 +488,8 @@ os_status os_paged_reorder(const os_paged_cache *cache, const int32_t *parents,
  * best first, ties to the lower beam, then the lower column.
  *   x        [groups * beams][cols] of in_dtype, read only.
  *   scores   [groups][beams] fp32: the beams' summed log-probabilities.  A beam
- *            of -inf (or NaN) is not there; its logits take no part.
+ *            of -inf (or NaN) is not there; its logits take no part.  +inf is no
+ *            score: which columns such a beam goes on with is not specified.
  *   ended    [groups][beams] bytes, not 0 where a beam has ended: it goes on as
  *            (i, pad) with c = scores_i alone, and its logits take no part.  Or
  *            NULL (none).

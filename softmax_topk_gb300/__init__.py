@@ -702,7 +702,7 @@ def paged_append(k_cache, v_cache, table, lengths, k, v, q=None, starts=None, in
     import torch
     bf16 = torch.bfloat16
     cache, dev, seqs, kv_heads, head_dim = _paged_cache(k_cache, v_cache, table, lengths)
-    shape = (k.shape[0], kv_heads, head_dim)
+    shape = (k.shape[0] if k.dim() else 0, kv_heads, head_dim)
     k_stride, v_stride = _heads("k", k, shape, bf16, dev), _heads("v", v, shape, bf16, dev)
     q_at = q_out_at = starts_at = freq_at = None
     q_heads = q_stride = rot = 0

@@ -465,6 +465,8 @@ static os_status paged_checks(const os_paged_cache* c, int64_t heads, int64_t la
     if (c->pages < 1 || c->seqs < 0 || c->width < 1 || c->kv_heads < 1 || c->page_size < 1 ||
         (c->head_dim != 64 && c->head_dim != 128) || heads < c->kv_heads || layers < 1)
         return OS_ERR_SHAPE;
+    // (the kernels count a token's and a page's 16-byte pieces in 32 bits)
+    if (c->kv_heads > (1 << 20) || c->page_size > (1 << 24)) return OS_ERR_SHAPE;
     if (c->pages > INT32_MAX / c->kv_heads / c->page_size || c->width > INT32_MAX / c->page_size ||
         c->seqs > INT32_MAX / heads || c->seqs > INT32_MAX / c->kv_heads / layers ||
         c->width > INT64_MAX / 8 / (c->seqs + 1))

@@ -48,6 +48,25 @@ def refuses_bad_caches(st, call):
         assert call(cache(st, **{name: CACHE[name] + step})) == ALIGN, name
 
 
+def test_heads_and_pages_that_32_bits_cannot_count(st):
+    """A token's heads and a page's rows are counted in 16-byte pieces of 32 bits."""
+    def append(rows, **kw):
+        return st._lib.os_paged_append(cache(st, pages=1, seqs=1, **kw), at(10), rows, at(11),
+                                       rows, None, 0, None, None, None, 1, 0, 0, 0, None)
+
+    def reorder(**kw):
+        return st._lib.os_paged_reorder(cache(st, pages=1, seqs=0, **kw), None, None, None, 1, 1,
+                                        None)
+
+    many = dict(page_size=1, head_dim=128)
+    assert append(2 ** 28, kv_heads=2 ** 20 + 1, **many) == SHAPE
+    assert reorder(kv_heads=2 ** 20 + 1, **many) == SHAPE and reorder(kv_heads=2 ** 20, **many) == OK
+    long = dict(kv_heads=1, width=1)
+    assert append(64, page_size=2 ** 24 + 1, **long) == SHAPE
+    assert reorder(page_size=2 ** 24 + 1, **long) == SHAPE
+    assert reorder(page_size=2 ** 24, **long) == OK
+
+
 def test_append_refusals(st):
     base = dict(k=at(10), k_stride=128, v=at(11), v_stride=128, q=at(12), q_stride=256,
                 q_out=at(13), starts=at(14), inv_freq=at(15), tokens=20, q_heads=4, rot=64,

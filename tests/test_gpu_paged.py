@@ -413,6 +413,7 @@ def test_tensor_refusals(st):
     refused(st.OsError, st.paged_attention, q, *good, scale=-1.0)
     refused(ValueError, st.paged_append, *good, k, k, q_out=q)
     refused(ValueError, st.paged_append, *good, k, k[:1])
+    refused(ValueError, st.paged_append, *good, k[0, 0, 0], k[0, 0, 0])
     refused(st.OsError, st.paged_append, *good, k[:1], k[:1])
     refused(ValueError, st.paged_append, *good, k, k, starts=torch.zeros(2).int().cuda())
     refused(st.OsError, st.paged_append, *good, k, k, inv_freq=torch.ones(12).cuda())
