@@ -27,8 +27,8 @@
 // What bounds it: memory, once there is enough to read.  64 sequences of 4096
 // keys, 16 heads of 128: 2.15 GB in 319 us, 6.7 TB/s, the measured copy's rate (four
 // schedulers issue in a quarter of their cycles).  128 sequences of up to 2000, 16
-// heads of 64: 95 us, 6.0 TB/s; one of 131072, 2 key heads: 32 us, 4.2 TB/s; one of
-// 1000: 7 us.  What is left is a constant of 6 to 12 us: three waits in a row for
+// heads of 64: 95 us, 6.0 TB/s; one of 131072, 2 key heads: 29 us, 4.6 TB/s; one of
+// 1000: 6.6 us.  What is left is a constant of 6 to 10 us: three waits in a row for
 // memory (lengths, table, first keys, 2.5 us), the last block, its pieces and the
 // second kernel (4 us), and two launches.
 #pragma once
@@ -62,6 +62,7 @@ struct AttnArgs {
     PageSplit split;
     int seqs, width, pages, kv_heads;
     int group, chunks, units;  // query heads per key head; their chunks; kv_heads * chunks
+    int ctas;                  // of the first kernel
     float scale_log2;          // scale * log2 e
 };
 
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
 
     // The join's CTAs, which wait for this grid's end themselves: not before the keys are
     // read (at the start 1 x 1000 took 7.2 us, 1 x 131072 31.7, the 61 ragged ones 51.2; here
-    // 7.0, 31.1, 50.8).
+    // 7.0, 31.0, 50.8).
     let_next();
     // ---- pieces of units that warps share: unit j begins before the CTA (0) or in warp
     // j - 1; the warps share its heads out
@@ -603,31 +604,71 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
     }
 }
 
-// The units that span CTAs, one (CTA that began one, query head) per CTA here: the
-// pieces' sum weighted by their maxima, the warps taking every kJoinWarps-th.
-constexpr int kJoinWarps = 8;
+// The units that span CTAs, a CTA per query head: the pieces' sum weighted by their
+// maxima, dealt out to the warps in turn.  BY_UNIT, where there are fewer
+// units than CTAs of the first kernel: blockIdx.x is a unit, whose CTAs are found from the
+// lengths while the first kernel's last CTAs still run.  Otherwise it is a CTA of the first
+// kernel, which has left a note of the unit that it began and did not end.  (1 x 131072,
+// two units of 76 CTAs: 31.0 us with the notes, 29.0 by unit.  Warps: by unit 29.2 with
+// eight, 1 x 1000 6.9 and 6.6; from notes the 61 ragged ones 50.8 with eight and 51.9 with
+// sixteen.  At most 64 registers: its CTAs fit beside the first kernel's: 51.9 -> 50.9.)
+constexpr int join_warps(bool by_unit) { return by_unit ? 16 : 8; }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+template <int D, int NT, bool BY_UNIT>
+__global__ void __launch_bounds__(32 * join_warps(BY_UNIT), BY_UNIT ? 1 : 4)
     paged_join_kernel(const __grid_constant__ AttnArgs a) {
     using S = AttnShape<D, NT>;
+    constexpr int kJoinWarps = join_warps(BY_UNIT);
     __shared__ float acc_sh[kJoinWarps][D], top_sh[kJoinWarps], sum_sh[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, head = blockIdx.y;
+    int first = blockIdx.x;  // CTA that began the unit
+    int row0 = -1, parts = 0, heads = 0;  // the unit's first row of out, its CTAs, its heads
+    if constexpr (BY_UNIT) {
+        // (no newer than this kernel: the first one had waited for what was before it when it
+        // let this one come)
+        auto blocks_of = [&](int i) {
+            return blocks_in(max(0, min(__ldcg(a.lengths + i), a.width * a.split.size)));
+        };
+        const int b = blockIdx.x / a.units, unit = blockIdx.x % a.units;
+        int total = 0, before = 0;
+        for (int i = lane; i < a.seqs; i += 32) {
+            const int blocks = blocks_of(i);
+            total += blocks;
+            before += i < b ? blocks : 0;
+        }
+        const int mine = blocks_of(b);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            total += __shfl_xor_sync(kFullMask, total, o);
+            before += __shfl_xor_sync(kFullMask, before, o);
+        }
+        const int per_cta = (total * a.units + a.ctas - 1) / a.ctas;
+        const int begin = before * a.units + unit * mine;
+        if (mine > 0) {
+            first = begin / per_cta;
+            parts = (begin + mine - 1) / per_cta - first + 1;
+        }
+        const int chunk = unit % a.chunks * S::kHeads;
+        heads = min(S::kHeads, a.group - chunk);
+        if (parts > 1) row0 = (b * a.kv_heads + unit / a.chunks) * a.group + chunk;
+    }
     wait_before();
     let_next();
     // the first piece is the second one of the CTA that began the unit
     auto piece = [&](int i) {
-        return a.parts + (2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0)) * S::kPiece;
+        return a.parts + (2 * (static_cast<int64_t>(first) + i) + (i == 0)) * S::kPiece;
     };
     // A lane has the maximum and the sum of one piece, asked for before it is known how many
     // there are (what is no piece is not used).
-    const int most = min(32 * kJoinWarps, static_cast<int>(gridDim.x - blockIdx.x));
+    const int most = BY_UNIT ? parts : min(32 * kJoinWarps, static_cast<int>(gridDim.x) - first);
     int mine = warp + lane * kJoinWarps;
     float m = -INFINITY, l = 0.f;
     if (mine < most) m = piece(mine)[S::kM + head], l = piece(mine)[S::kL + head];
-    const int4 tail = a.tails[blockIdx.x];  // (row of out, CTAs, heads)
-    if (tail.x < 0 || head >= tail.z) return;
-    const int parts = tail.y;
+    if constexpr (!BY_UNIT) {
+        const int4 tail = a.tails[blockIdx.x];  // (row of out, CTAs, heads)
+        row0 = tail.x, parts = tail.y, heads = tail.z;
+    }
+    if (row0 < 0 || head >= heads) return;
     float top = -INFINITY, sum = 0.f, acc[D / 32] = {};
     for (int i0 = warp; i0 < parts; i0 += 32 * kJoinWarps, mine += 32 * kJoinWarps) {
         if (i0 > warp && mine < parts) m = piece(mine)[S::kM + head], l = piece(mine)[S::kL + head];
@@ -641,7 +682,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) acc[x] *= f0;
         const int here = min(32, (parts - i0 + kJoinWarps - 1) / kJoinWarps);
-#pragma unroll 8
+#pragma unroll 4
         for (int i = 0; i < here; ++i) {
             const float w = __shfl_sync(kFullMask, f, i);
             sum += w * __shfl_sync(kFullMask, l, i);
@@ -664,7 +705,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
         all += f * sum_sh[w];
         value += f * acc_sh[w][d];
     }
-    const int row = tail.x + head;
+    const int row = row0 + head;
     a.out[static_cast<int64_t>(row) * D + d] = __float2bfloat16(all == 0.f ? 0.f : value / all);
     if (d == 0) store_lse(a, row, top, all);
 }

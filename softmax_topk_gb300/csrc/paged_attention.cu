@@ -29,6 +29,7 @@ cudaError_t launch(paged::AttnArgs a, void* workspace, cudaStream_t stream) {
     const int64_t most =
         ceil_div(int64_t(a.width) * a.split.size, paged::kBlock) * a.seqs * a.units;
     const int ctas = static_cast<int>(min64(dev->sms, ceil_div(most, kMinBlocks)));
+    a.ctas = ctas;
     a.tails = static_cast<int4*>(workspace);
     a.parts = reinterpret_cast<float*>(a.tails + ctas);
     auto k = paged::paged_attention_kernel<D, NT>;
@@ -36,9 +37,12 @@ cudaError_t launch(paged::AttnArgs a, void* workspace, cudaStream_t stream) {
     if (!prepare_kernel(k, 1, smem)) return cudaErrorInvalidConfiguration;
     const cudaError_t e = launch_behind(k, dim3(ctas), S::kThreads, smem, stream, a);
     if (e != cudaSuccess || ctas == 1) return e;
-    return launch_behind(paged::paged_join_kernel<D, NT>,
-                         dim3(ctas, static_cast<unsigned>(min64(a.group, S::kHeads))),
-                         32 * paged::kJoinWarps, 0, stream, a);
+    const unsigned heads = static_cast<unsigned>(min64(a.group, S::kHeads));
+    const bool by_unit = int64_t(a.seqs) * a.units < ctas;
+    return launch_behind(by_unit ? paged::paged_join_kernel<D, NT, true>
+                                 : paged::paged_join_kernel<D, NT, false>,
+                         dim3(by_unit ? static_cast<unsigned>(a.seqs * a.units) : ctas, heads),
+                         32 * paged::join_warps(by_unit), 0, stream, a);
 }
 
 }  // namespace

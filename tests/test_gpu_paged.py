@@ -94,6 +94,16 @@ def test_attention_split_over_the_gpu(st, d, lengths):
     check_attention(st, pool, 2 * pool.randn(len(lengths), 6, d).bfloat16())
 
 
+@pytest.mark.parametrize("seqs,kv_heads,group", [(75, 2, 2), (76, 2, 2), (151, 1, 16), (152, 1, 3),
+                                                 (40, 1, 24), (3, 1, 40)])
+def test_attention_about_as_many_units_as_ctas(st, seqs, kv_heads, group):
+    """The join goes by units below one per SM (152 of them), and by CTAs from there on."""
+    lengths = [(97 * i + 50) % 700 if i % 7 else 0 for i in range(seqs)]
+    lengths[-1] = 4000
+    pool = Pool(lengths, kv_heads, 16, 64, seed=seqs)
+    check_attention(st, pool, 2 * pool.randn(seqs, kv_heads * group, 64).bfloat16())
+
+
 def test_attention_more_sequences_than_threads(st):
     lengths = [(7 * i) % 40 for i in range(1500)]
     pool = Pool(lengths, 1, 8, 64)
