@@ -604,22 +604,20 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 1)
     }
 }
 
-// The units that span CTAs, a CTA per query head: the pieces' sum weighted by their
-// maxima, dealt out to the warps in turn.  BY_UNIT, where there are fewer
-// units than CTAs of the first kernel: blockIdx.x is a unit, whose CTAs are found from the
-// lengths while the first kernel's last CTAs still run.  Otherwise it is a CTA of the first
-// kernel, which has left a note of the unit that it began and did not end.  (1 x 131072,
-// two units of 76 CTAs: 31.0 us with the notes, 29.0 by unit.  Warps: by unit 29.2 with
-// eight, 1 x 1000 6.9 and 6.6; from notes the 61 ragged ones 50.8 with eight and 51.9 with
-// sixteen.  At most 64 registers: its CTAs fit beside the first kernel's: 51.9 -> 50.9.)
-constexpr int join_warps(bool by_unit) { return by_unit ? 16 : 8; }
+// The units that span CTAs, a CTA per query head: the pieces' sum weighted by their maxima,
+// dealt out to the warps in turn.  BY_UNIT, where there are fewer units than CTAs of the
+// first kernel: blockIdx.x is a unit, whose CTAs are found from the lengths while the first
+// kernel's last CTAs still run.  Otherwise it is a CTA of the first kernel, which has left a
+// note of the unit that it began and did not end.  (1 x 131072, two units of 76 CTAs: 31.0
+// us with the notes, 28.6 by unit.)
+constexpr int kJoinWarps = 16, kFewJoinWarps = 4;
 
-template <int D, int NT, bool BY_UNIT>
-__global__ void __launch_bounds__(32 * join_warps(BY_UNIT), BY_UNIT ? 1 : 4)
+template <int D, int NT, bool BY_UNIT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == kJoinWarps ? 1 : 8)
     paged_join_kernel(const __grid_constant__ AttnArgs a) {
     using S = AttnShape<D, NT>;
-    constexpr int kJoinWarps = join_warps(BY_UNIT);
-    __shared__ float acc_sh[kJoinWarps][D], top_sh[kJoinWarps], sum_sh[kJoinWarps];
+    static_assert(32 * WARPS >= D, "a thread per dimension");
+    __shared__ float acc_sh[WARPS][D], top_sh[WARPS], sum_sh[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, head = blockIdx.y;
     int first = blockIdx.x;  // CTA that began the unit
     int row0 = -1, parts = 0, heads = 0;  // the unit's first row of out, its CTAs, its heads
@@ -660,8 +658,8 @@ __global__ void __launch_bounds__(32 * join_warps(BY_UNIT), BY_UNIT ? 1 : 4)
     };
     // A lane has the maximum and the sum of one piece, asked for before it is known how many
     // there are (what is no piece is not used).
-    const int most = BY_UNIT ? parts : min(32 * kJoinWarps, static_cast<int>(gridDim.x) - first);
-    int mine = warp + lane * kJoinWarps;
+    const int most = BY_UNIT ? parts : min(32 * WARPS, static_cast<int>(gridDim.x) - first);
+    int mine = warp + lane * WARPS;
     float m = -INFINITY, l = 0.f;
     if (mine < most) m = piece(mine)[S::kM + head], l = piece(mine)[S::kL + head];
     if constexpr (!BY_UNIT) {
@@ -670,7 +668,7 @@ __global__ void __launch_bounds__(32 * join_warps(BY_UNIT), BY_UNIT ? 1 : 4)
     }
     if (row0 < 0 || head >= heads) return;
     float top = -INFINITY, sum = 0.f, acc[D / 32] = {};
-    for (int i0 = warp; i0 < parts; i0 += 32 * kJoinWarps, mine += 32 * kJoinWarps) {
+    for (int i0 = warp; i0 < parts; i0 += 32 * WARPS, mine += 32 * WARPS) {
         if (i0 > warp && mine < parts) m = piece(mine)[S::kM + head], l = piece(mine)[S::kL + head];
         if (mine >= parts) m = -INFINITY, l = 0.f;
         float to = fmaxf(top, m);
@@ -681,12 +679,12 @@ __global__ void __launch_bounds__(32 * join_warps(BY_UNIT), BY_UNIT ? 1 : 4)
         sum *= f0;
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) acc[x] *= f0;
-        const int here = min(32, (parts - i0 + kJoinWarps - 1) / kJoinWarps);
+        const int here = min(32, (parts - i0 + WARPS - 1) / WARPS);
 #pragma unroll 4
         for (int i = 0; i < here; ++i) {
             const float w = __shfl_sync(kFullMask, f, i);
             sum += w * __shfl_sync(kFullMask, l, i);
-            const float* from = piece(i0 + i * kJoinWarps) + head * S::kHeadStride + lane * (D / 32);
+            const float* from = piece(i0 + i * WARPS) + head * S::kHeadStride + lane * (D / 32);
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) acc[x] += w * from[x];
         }
@@ -698,9 +696,9 @@ __global__ void __launch_bounds__(32 * join_warps(BY_UNIT), BY_UNIT ? 1 : 4)
     const int d = threadIdx.x;
     if (d >= D) return;
     top = -INFINITY;
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, top_sh[w]);
+    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, top_sh[w]);
     float all = 0.f, value = 0.f;
-    for (int w = 0; w < kJoinWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
         const float f = piece_weight(top_sh[w], top);
         all += f * sum_sh[w];
         value += f * acc_sh[w][d];

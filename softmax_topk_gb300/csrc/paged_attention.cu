@@ -9,8 +9,8 @@ namespace os {
 namespace {
 
 // Blocks that a CTA should have at least: fewer CTAs leave fewer pieces to join.  us with
-// 2, 4, 8, 16 blocks, 2 key heads: 300 keys 6.5 / 6.2 / 7.0 / 7.6, 1000 keys 7.2 / 6.8 /
-// 7.4 / 8.3, 3000 keys 9.4 / 8.2 / 7.9 / 8.5.
+// 2, 4, 8 blocks, 2 key heads: 300 keys 6.1 / 6.1 / 6.9, 1000 keys 6.7 / 6.4 / 6.9, 3000
+// keys 6.9 / 7.1 / 7.2.
 constexpr int kMinBlocks = 4;
 
 template <int D, int NT>
@@ -37,12 +37,20 @@ cudaError_t launch(paged::AttnArgs a, void* workspace, cudaStream_t stream) {
     if (!prepare_kernel(k, 1, smem)) return cudaErrorInvalidConfiguration;
     const cudaError_t e = launch_behind(k, dim3(ctas), S::kThreads, smem, stream, a);
     if (e != cudaSuccess || ctas == 1) return e;
-    const unsigned heads = static_cast<unsigned>(min64(a.group, S::kHeads));
-    const bool by_unit = int64_t(a.seqs) * a.units < ctas;
-    return launch_behind(by_unit ? paged::paged_join_kernel<D, NT, true>
-                                 : paged::paged_join_kernel<D, NT, false>,
-                         dim3(by_unit ? static_cast<unsigned>(a.seqs * a.units) : ctas, heads),
-                         32 * paged::join_warps(by_unit), 0, stream, a);
+    // Sixteen warps a head where the join has an SM for each, else four.  us with sixteen,
+    // eight, four: 1 x 1000, 2 x 8 heads 6.5 / 6.8 / 6.7, 1 x 131072 28.6 / 30.0 / 32.4,
+    // 2 x 30000, 2 x 16 heads 18.4 / 19.1 / 20.4; 64 x 4096, 16 heads on one 43.5 / 35.9 /
+    // 31.9, 16 x 4096, 4 x 8 heads 32.2 / 28.8 / 27.7.
+    const int64_t units = int64_t(a.seqs) * a.units, heads = min64(a.group, S::kHeads);
+    const bool by_unit = units < ctas;
+    const bool many = by_unit && units * heads <= dev->sms;
+    constexpr int kMany = paged::kJoinWarps, kFew = paged::kFewJoinWarps;
+    return launch_behind(many      ? paged::paged_join_kernel<D, NT, true, kMany>
+                         : by_unit ? paged::paged_join_kernel<D, NT, true, kFew>
+                                   : paged::paged_join_kernel<D, NT, false, kFew>,
+                         dim3(static_cast<unsigned>(by_unit ? units : ctas),
+                              static_cast<unsigned>(heads)),
+                         32 * (many ? kMany : kFew), 0, stream, a);
 }
 
 }  // namespace
