@@ -1,6 +1,7 @@
 // Beam search's selection: the rows' runs, then the groups.
 #include <algorithm>
 
+#include "beam_error.h"
 #include "host_common.h"
 #include "internal.h"
 #include "kernels/beam_kernel.cuh"
@@ -83,13 +84,9 @@ cudaError_t launch_beam_select(const BeamSelectArgs& p, cudaStream_t stream) {
     // the CTAs of a group share the exact sums, where there are SMs for them
     a.helpers = beam::kHelpers;
     while (a.helpers > 1 && p.groups * a.helpers > 2 * dev->sms) a.helpers /= 2;
-    // What the first kernel's ln d can be off, in units u of 2^-23: an exponent's rounding
-    // (above 2^-32: half a step of 2^-19 times ln 2) 5.8, log2 e in one part 2.5, ex2.approx 2,
-    // the factor of the rounded reference 2.5; sums of a tile's 32 values 5, of tiles
-    // (compensated) 1, changes of the reference 2.4; threads to a warp 4.5, warps to a run 3,
-    // runs to a row 4, the logarithm 0.5: 33.2.  Smaller weights are below 2^-32 of the
-    // largest and add at most 4 in the longest rows.
-    a.eps = 40 * 0x1p-23f;
+    // (36 units of 2^-23 for 1000 columns, 38 for 50257 in runs of one tile, 43 for 128256 in one)
+    const int per_tile = p.in == OS_F32 ? beam::Tile<float>::kPer : beam::Tile<__nv_bfloat16>::kPer;
+    a.eps = static_cast<float>(beam_lse_error(p.cols, s.run_tiles * per_tile));
     return p.in == OS_F32 ? launch_k<float>(a, p.groups, stream)
                           : launch_k<__nv_bfloat16>(a, p.groups, stream);
 }

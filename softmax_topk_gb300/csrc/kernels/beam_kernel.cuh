@@ -219,7 +219,9 @@ __device__ __forceinline__ float largest_of(const uint4 (&w)[kBlocks]) {
 
 // A thread's share of the row's normalizer state: weights e^(x - m) summed as d + lost,
 // and the largest value so far.  m follows the largest only when that has passed it by
-// more than one, so the roundings of the change of m fade with it.
+// more than one, so what has been through many changes of m weighs little beside what
+// came later, and the changes' roundings add up to the logarithm of the share's columns
+// (beam_error.h).
 template <typename T>
 struct State {
     float m = -INFINITY, d = 0.f, lost = 0.f, largest = -INFINITY;
