@@ -46,17 +46,18 @@ constexpr int kAppendTokens = 4;  // at most, per CTA
 // before it), or -1 where t is behind the last sequence or before the first.
 __device__ __forceinline__ int sequence_of(const int* starts, int seqs, int64_t t, int lane) {
     if (t < *starts || t >= starts[seqs]) return -1;
-    int lo = 0, hi = seqs;  // starts[lo] <= t < starts[hi]
+    // (a lane may look up to 32 steps past lo: beyond 2^31 where there are nearly as many
+    // sequences, so the places are unsigned)
+    unsigned lo = 0, hi = seqs;  // starts[lo] <= t < starts[hi]
     while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int at = lo + (lane + 1) * step;
+        const unsigned step = (hi - lo + 31) / 32;
+        const unsigned at = lo + (lane + 1) * step;
         const unsigned ok = __ballot_sync(kFullMask, at < hi && starts[at] <= t);
-        const int below = __popc(ok);
-        const int nlo = lo + below * step;
+        const unsigned nlo = lo + __popc(ok) * step;
         hi = min(hi, nlo + step);
         lo = nlo;
     }
-    return lo;
+    return static_cast<int>(lo);
 }
 
 template <int D, bool INTERLEAVED>
