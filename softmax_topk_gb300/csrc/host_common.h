@@ -7,7 +7,6 @@
 #include <cstdint>
 #include <map>
 #include <mutex>
-#include <set>
 #include <utility>
 
 #include "../../include/os_softmax.h"
@@ -59,27 +58,86 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), int64_t grid, int threads, i
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// True from the second call for `kernel` on the current device on; the first one has
-// the kernel's code loaded.
-inline bool loaded_before(const void* kernel) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    static std::mutex mu;
-    static std::set<std::pair<int, const void*>> seen;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!seen.insert({dev, kernel}).second) return true;
-    cudaFuncAttributes attributes;
-    if (cudaFuncGetAttributes(&attributes, kernel) != cudaSuccess) cudaGetLastError();
-    return false;
-}
+// Whether kernels have run to their end before, per device.  A kernel whose code has only
+// just been loaded is not put in place early, and what counts is the order on the GPU: a
+// launch on another stream may come before the first one that was asked for, and one that was
+// captured runs when its graph does.  So the end of an ordinary launch is what is looked for.
+class RunBefore {
+  public:
+    static RunBefore& of_library() {
+        static RunBefore r;
+        return r;
+    }
+    // True once a launch of `kernel` on device `dev` is known to have ended.
+    bool operator()(int dev, const void* kernel) {
+        std::lock_guard<std::mutex> lock(mu_);
+        const auto found = kernels_.insert({{dev, kernel}, Kernel()});
+        Kernel& k = found.first->second;
+        if (k.ended) return true;
+        if (found.second) {  // loads its code
+            cudaFuncAttributes attributes;
+            if (cudaFuncGetAttributes(&attributes, kernel) != cudaSuccess) cudaGetLastError();
+        }
+        if (!k.end) return false;
+        const Relaxed relaxed;
+        if (cudaEventQuery(k.end) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        cudaEventDestroy(k.end);
+        k.end = nullptr;
+        return k.ended = true;
+    }
+    // `kernel` has been launched, as any other kernel is, on `stream` of device `dev`.
+    void launched(int dev, const void* kernel, cudaStream_t stream) {
+        std::lock_guard<std::mutex> lock(mu_);
+        Kernel& k = kernels_[{dev, kernel}];
+        if (k.ended || k.end) return;
+        const Relaxed relaxed;
+        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) {
+            cudaGetLastError();
+            return;
+        }
+        if (capture != cudaStreamCaptureStatusNone) return;
+        cudaEvent_t end = nullptr;
+        if (cudaEventCreateWithFlags(&end, cudaEventDisableTiming) == cudaSuccess) {
+            if (cudaEventRecord(end, stream) == cudaSuccess) {
+                k.end = end;
+                return;
+            }
+            cudaEventDestroy(end);
+        }
+        cudaGetLastError();
+    }
+
+  private:
+    struct Kernel {
+        cudaEvent_t end = nullptr;  // of the first ordinary launch, until it has come
+        bool ended = false;
+    };
+    // What is asked here has nothing to do with a capture that may go on, in any thread.
+    struct Relaxed {
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+        ~Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    };
+    std::mutex mu_;
+    std::map<std::pair<int, const void*>, Kernel> kernels_;
+};
 
 // Launch `kernel` behind the one before it on `stream`, which may let it be put in place
 // before it has ended (griddepcontrol.launch_dependents); it waits for that one's end
-// itself (griddepcontrol.wait) before it touches memory.  The first launch of a kernel,
-// whose code has only just been loaded, waits as any other launch does.
+// itself (griddepcontrol.wait) before it touches memory.  Until it has run once it waits as
+// any other kernel does; so it does for good in a graph that was captured before.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_behind(void (*kernel)(KArgs...), dim3 grid, int threads, int smem,
                           cudaStream_t stream, Args... args) {
+    const void* k = reinterpret_cast<const void*>(kernel);
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool early = RunBefore::of_library()(dev, k);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
@@ -89,8 +147,10 @@ cudaError_t launch_behind(void (*kernel)(KArgs...), dim3 grid, int threads, int 
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = loaded_before(reinterpret_cast<const void*>(kernel)) ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+    cfg.numAttrs = early ? 1 : 0;
+    const cudaError_t status = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+    if (status == cudaSuccess && !early) RunBefore::of_library().launched(dev, k, stream);
+    return status;
 }
 
 // Opt `kernel` into `smem` bytes of dynamic shared memory and, for cluster
