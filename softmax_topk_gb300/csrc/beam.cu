@@ -84,7 +84,7 @@ cudaError_t launch_beam_select(const BeamSelectArgs& p, cudaStream_t stream) {
     // the CTAs of a group share the exact sums, where there are SMs for them
     a.helpers = beam::kHelpers;
     while (a.helpers > 1 && p.groups * a.helpers > 2 * dev->sms) a.helpers /= 2;
-    // (36 units of 2^-23 for 1000 columns, 38 for 50257 in runs of one tile, 43 for 128256 in one)
+    // (31 units of 2^-23 for 1000 columns, 33 for 50257 in runs of one tile, 38 for 128256 in one)
     const int per_tile = p.in == OS_F32 ? beam::Tile<float>::kPer : beam::Tile<__nv_bfloat16>::kPer;
     a.eps = static_cast<float>(beam_lse_error(p.cols, s.run_tiles * per_tile));
     return p.in == OS_F32 ? launch_k<float>(a, p.groups, stream)

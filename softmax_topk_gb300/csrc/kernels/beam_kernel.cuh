@@ -31,6 +31,7 @@
 // instructions per column on eight SMs.  4 beams of 50257 fp32: 10 us.
 #pragma once
 
+#include "../beam_error.h"
 #include "paged_common.cuh"
 #include "sample_kernel.cuh"
 
@@ -70,7 +71,7 @@ struct BeamArgs {
     int run_tiles;                 // tiles of a run
     int helpers;                   // CTAs of a group
     int pad;
-    float eps;                     // bound of lse's error
+    float eps;                     // bound of lse's error (and kFarError)
 };
 
 // value and column in one number: larger is better, no two alike, 0 is none
@@ -531,7 +532,7 @@ struct MergeShared {
     Sum slice[kMaxBeams][kHelpers];  // a row's summed weights, from each CTA of the cluster
     u64 todo;                        // rows to be summed again
     float pow2[64];
-    int count;
+    int count, far;                  // far: a row's maximum is beyond 2^24
 };
 
 // Doubles as integers of their order: 64-bit comparisons on the integer pipe (the
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__(kMergeThreads)
             }
         }
     };
-    if (tid == 0) sh.todo = 0;
+    if (tid == 0) sh.todo = 0, sh.far = 0;
     // (a CTA's shared memory may be written from outside once it has started)
     if (a.helpers > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     if (rank) {
@@ -683,9 +684,9 @@ __global__ void __launch_bounds__(kMergeThreads)
             const double ln_d = static_cast<double>(logf(scalbnf(d, -e))) + e * 0.6931471805599453;
             sh.lse[i] = ln_d;
             sh.m64[i] = top;
+            if (fabsf(top) >= 0x1p24f && fabsf(top) < INFINITY) sh.far = 1;
         }
     }
-    const double eps = a.eps;
     // the order of an entry's value, kNone where there is none
     auto order_of = [&](u64 key, int beam) -> u64 {
         if (key == 0) return kNone;
@@ -738,6 +739,7 @@ __global__ void __launch_bounds__(kMergeThreads)
                 sh.near[i] = static_cast<float>(sh.offset[i]);
             }
         __syncthreads();
+        const float eps = sh.far ? a.eps + kFarError : a.eps;
         // ---- a bound that K entries reach, less what the roundings and (in the first
         // round) the sums' errors may have taken from others
         float top = -INFINITY, slack;
@@ -746,7 +748,7 @@ __global__ void __launch_bounds__(kMergeThreads)
             top = fmaxf(top, c);
         });
         float bound = key_value(parts_bound<KP>(order_key(top), sh.bound));
-        bound -= 4 * a.eps + fabsf(bound) * 0x1p-22f;
+        bound -= 4 * eps + fabsf(bound) * 0x1p-22f;
         each([&](u64 key, int beam) {
             const float c = rough(key, beam, slack) + slack;
             if (c < bound) return;

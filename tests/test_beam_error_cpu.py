@@ -39,16 +39,17 @@ SIZES = [(1, 16), (7, 16), (1000, 16), (50257, 32), (128256, 512), (5_000_011, 6
 def test_changes_of_the_reference(bound, cols, share):
     """`share` weights near the first reference, then values that each pass the reference by just
     over 1: what k changes of 1.25 units leave on the whole sum, for the worst k, beside the terms
-    that do not depend on the share.  (For rows of 20000 columns a thread the total is above 40.)"""
+    that do not depend on the share.  (No constant of 40 units is a bound for 20000 columns a
+    thread.)"""
     worst, later = 0.0, 0.0
     for k in range(1, 60):
         later += math.exp(1 - k)  # the values that came, beside the last
         mass = share * math.exp(-k)
         worst = max(worst, 1.25 * k * mass / (mass + later))
-    rest = 0.612 * (3 + math.log(cols)) + 5.5 + 2.5 + 2 + 5 + 10.75
+    rest = 0.612 * (3 + math.log(cols)) + 2.5 + 2 + 5 + 10.75
     assert bound(cols, share) >= rest + worst
     if share >= 20000:
-        assert rest + worst > 40
+        assert rest + worst + share ** 2 * 2.0 ** -26 > 40
 
 
 def test_mean_distance_and_mean_number_of_changes():
@@ -144,6 +145,7 @@ def rows():
     yield "normal", (rng.standard_normal(128256) * 2.5).astype(f32)
     yield "wide", (rng.standard_normal(128256) * 12).astype(f32)
     yield "far from 0", (rng.standard_normal(50257) * 3 + 9e4).astype(f32)
+    yield "far beyond 2^24", np.float64(2 ** 27) - 16 * rng.integers(0, 9, 50257)
     yield "all but equal", (rng.random(300000) * 1e-3).astype(f32)
     # nearly all the mass 17 below the maximum
     low = np.full(2 ** 20, -17.0, f32) + (rng.random(2 ** 20) * 0.1).astype(f32)
@@ -161,10 +163,12 @@ def rows():
 
 def test_replayed_sums_stay_within_the_bound(bound):
     for name, row in rows():
+        row = row.astype(f32)
+        far = 5.5 if np.abs(row).max() >= 2 ** 24 else 0
         top = float(row.max())
         want = math.log(math.fsum(np.exp(row.astype(np.float64) - top)))
         share = -(-len(row) // 4096) * 16
         for off in (-2, 0, 2):
             err = abs(replay(row, 16, off) - want) / U
             # (the last logarithm is not replayed)
-            assert err <= bound(len(row), share) - 0.5, (name, off, err)
+            assert err <= bound(len(row), share) + far - 0.5, (name, off, err)

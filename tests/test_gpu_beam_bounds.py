@@ -23,7 +23,7 @@ def st():
 
 
 def bound(cols, share):
-    return U * (0.612 * (3 + math.log(cols)) + 25.75 + 1.25 * (math.log(share) + 0.6) +
+    return U * (0.612 * (3 + math.log(cols)) + 20.25 + 1.25 * (math.log(share) + 0.6) +
                 share * share * 2.0 ** -26)
 
 
@@ -68,6 +68,32 @@ def test_choices_between_rising_and_falling_rows(st):
     assert top >= 2  # both places of a group are its better beam's
     want = (up == 2).int()
     assert torch.equal(parents[:, 0], want) and torch.equal(parents[:, 1], want)
+
+
+@pytest.mark.parametrize("base", [2.0 ** 24, -2.0 ** 26, 2.0 ** 27, 2.0 ** 29])
+def test_rows_far_from_zero(st, base):
+    """Maxima beyond 2^24, whose products with log2 e are rounded to whole numbers."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    gap = max(1.0, abs(base) * 2.0 ** -23)
+    x = base - gap * torch.randint(0, 12, (10, 30011), generator=g, device="cuda").double()
+    x = x.float()
+    s = -torch.rand(10, 1, generator=g, device="cuda")
+    got = st.beam_select(x, s, 20)
+    values, parents, tokens = ref.beam_select(x, s, 20)
+    assert np.array_equal(got[1].cpu().numpy(), parents)
+    assert np.array_equal(got[2].cpu().numpy(), tokens)
+    err = np.abs(got[0].cpu().double().numpy() - values)
+    assert np.all(err <= bound(30011, 128) + 5.5 * U + 2.0 ** -24 * np.abs(values))
+    # beams that differ by little, and equal rows
+    x[1], x[6] = x[0].flip(0), x[5]
+    s = torch.full((2, 5), -1.0, device="cuda")
+    s[0, 1] = torch.nextafter(s[0, 0], torch.zeros((), device="cuda"))
+    s[:, 2:] = -9.0
+    got = st.beam_select(x, s, 12)
+    values, parents, tokens = ref.beam_select(x, s, 12)
+    assert np.array_equal(got[1].cpu().numpy(), parents)
+    assert np.array_equal(got[2].cpu().numpy(), tokens)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
