@@ -438,10 +438,10 @@ os_status os_paged_append(const os_paged_cache *cache, const void *k, int64_t k_
  *   lse       [seqs][q_heads] fp32, or NULL (not written).
  *   workspace os_paged_attention_workspace bytes, 16-byte aligned, overwritten.
  *             Calls that can run at the same time need one each.
- *   scale     finite and > 0 (OS_ERR_VALUE).
+ *   scale     > 0, and finite as scale log2 e too: at most 2.35e38 (OS_ERR_VALUE).
  * Outputs and workspace may not overlap the inputs or each other (OS_ERR_ALIAS).
  * What the cache holds behind the lengths is not used, whatever its bits.
- * A head with a score that is NaN or +inf gets NaN, in O and L; an infinity or NaN
+ * A head with a score that is NaN or +inf (from 2.35e38 on) gets NaN, in O and L; an infinity or NaN
  * among the values used leaves its dimension of O without a finite value (an infinity
  * or NaN), for all heads that use it.
  * Arithmetic: products on the tensor cores from bf16 operands with fp32 sums;

@@ -556,7 +556,8 @@ os_status os_paged_attention(const os_paged_cache* cache, const void* q, int64_t
     const int64_t units = int64_t(cache->kv_heads) * ((q_heads / cache->kv_heads + 7) / 8);
     const int64_t blocks = (cache->width * cache->page_size + 15) / 16;
     if (cache->seqs > 0 && units * blocks > (1 << 30) / cache->seqs) return OS_ERR_SHAPE;
-    if (!(scale > 0.f) || !(scale < INFINITY)) return OS_ERR_VALUE;
+    // (scores are formed as powers of two: scale log2 e has to be a number too)
+    if (!(scale > 0.f) || !(scale * os::kScoreLog2e < INFINITY)) return OS_ERR_VALUE;
     if (cache->seqs == 0) return OS_OK;
     const os_status ps = paged_pointers(cache);
     if (ps != OS_OK) return ps;

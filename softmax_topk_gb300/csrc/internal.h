@@ -99,6 +99,7 @@ cudaError_t launch_paged_append(const os_paged_cache& c, const PagedAppendArgs& 
 cudaError_t launch_paged_reorder(const os_paged_cache& c, const int32_t* parents, int beams,
                                  int layers, int32_t* out_table, int32_t* out_lengths,
                                  cudaStream_t stream);
+constexpr float kScoreLog2e = 1.44269504f;
 int64_t paged_attention_workspace(int sms);
 cudaError_t launch_paged_attention(const os_paged_cache& c, const void* q, int64_t q_stride,
                                    void* out, float* lse, void* workspace, int q_heads, float scale,

@@ -74,7 +74,7 @@ cudaError_t launch_paged_attention(const os_paged_cache& c, const void* q, int64
     a.pages = static_cast<int>(c.pages);
     a.kv_heads = c.kv_heads;
     a.group = q_heads / c.kv_heads;
-    a.scale_log2 = scale * 1.44269504f;
+    a.scale_log2 = scale * kScoreLog2e;
     a.split = paged::page_split(c.page_size);
     if (c.head_dim == 64)
         return a.group <= 8 ? launch<64, 1>(a, workspace, stream) : launch<64, 2>(a, workspace, stream);
