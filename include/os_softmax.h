@@ -503,8 +503,8 @@ os_status os_paged_reorder(const os_paged_cache *cache, const int32_t *parents,
  * Logits of -inf and NaN are no continuations; +inf ones share their row's
  * probability evenly.  Choices are those of real arithmetic up to the sums'
  * precision: beams whose sums in fp32 leave the order open are summed again,
- * each weight to 2^-38 of itself and 2^-45 of the row's largest (2^-32 for the
- * longest rows), as integers, so that equal rows have equal sums.  Outputs and
+ * each weight to 2^-38 of itself and 2^-45 of the row's largest (up to 2^26 columns;
+ * 2^-39 for the longest rows), as integers, so that equal rows have equal sums.  Outputs and
  * workspace may not overlap the inputs or each other (OS_ERR_ALIAS).
  */
 os_status os_beam_select(const void *x, const float *scores, const uint8_t *ended, float *out,

@@ -552,12 +552,12 @@ __device__ __forceinline__ bool better(u64 c, u64 at, u64 c2, u64 at2) {
 }
 
 // A row's weights as multiples of 2^-bits, so that a thread's sum of its share of the
-// columns stays below 2^62.
+// columns stays below 2^62: 44 bits up to 2^26 columns, 38 for 2^31 - 1 without helpers.
 __device__ __forceinline__ sample::Weight row_weights(float m, int64_t cols, int helpers,
                                                       const float* pow2) {
     const int64_t share = cols / (int64_t(kMergeThreads) * helpers) + 1;
     int bits = 44;
-    while (bits > 31 && share >> (62 - bits)) --bits;
+    while (share >> (62 - bits)) --bits;
     sample::Weight w;
     w.set(m, 1.f, bits, pow2);
     return w;
