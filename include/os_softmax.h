@@ -374,8 +374,10 @@ os_status os_sample(const void *x, const float *u, const os_sampling *s, int32_t
  *             Sequences may share pages.
  *   lengths   [seqs] int32: tokens that each sequence holds, those of this
  *             step's append among them (one tensor serves the append and the
- *             attention behind it).  Below 0 counts as 0, above width *
- *             page_size as that.
+ *             attention behind it).  Below 0 counts as 0.  Above width *
+ *             page_size the attention and the reordering take it as that; the
+ *             append's positions follow from the length as it is, and those
+ *             beyond the table are not stored.
  *   pages >= 1, seqs >= 0, width >= 1, kv_heads 1 to 2^20, page_size 1 to 2^24,
  *   head_dim 64 or 128; pages * kv_heads * page_size, width * page_size and seqs *
  *   (query or key heads) at most 2^31 - 1 (OS_ERR_SHAPE).
@@ -415,8 +417,10 @@ typedef struct {
  * new tokens have to be different ones (sequences that share a page end before
  * it): of two tokens for one place any piece may stay.
  * q_out may not overlap the inputs or the cache, nor the cache any input
- * (OS_ERR_ALIAS).  Angles are reduced in 64 bits (an error below 2^-22 turns
- * at any position, 2^-30 below 2^24); products and sums in fp32, rounded once.
+ * (OS_ERR_ALIAS).  Angles are reduced in 64 bits: an error of at most 2^-51 of
+ * the number of turns, p |inv_freq| / 2 pi (for frequencies up to 1 that is 2^-22
+ * turns at any position, 2^-29 below 2^24), and 2^-25 turns; products and sums
+ * in fp32, rounded once.
  */
 os_status os_paged_append(const os_paged_cache *cache, const void *k, int64_t k_stride,
                           const void *v, int64_t v_stride, const void *q, int64_t q_stride,
@@ -467,8 +471,10 @@ os_status os_paged_attention_workspace(int64_t *bytes);
  *   cache     k, v are [layers][pages][kv_heads][page_size][head_dim] here;
  *             table and lengths are those before the choice.  layers >= 1, and
  *             layers * kv_heads * seqs at most 2^31 - 1 (OS_ERR_SHAPE).
- *   parents   [seqs] int32, 0 to beams - 1.  Outside: the sequence has no parent,
- *             its row stays and its length becomes 0.
+ *   parents   [seqs] int32, 0 to beams - 1.  Outside (-1 from os_beam_select): the
+ *             sequence has no parent, its row stays and its length becomes 0.  Leave
+ *             it 0, an idle place, until a later choice fills it: the row may name
+ *             pages that others share, and an append to it would write there.
  *   out_table [seqs][width] int32.  At each sequence's next place it names a page
  *             of the sequence's own, which no row of table uses (keep two tables
  *             and let them take turns).  A page that is not there, or the parent's
@@ -503,7 +509,7 @@ os_status os_paged_reorder(const os_paged_cache *cache, const int32_t *parents,
  * Logits of -inf and NaN are no continuations; +inf ones share their row's
  * probability evenly.  Choices are those of real arithmetic up to the sums'
  * precision: beams whose sums in fp32 leave the order open are summed again,
- * each weight to 2^-38 of itself and 2^-45 of the row's largest (up to 2^26 columns;
+ * each weight to 2^-38 of itself and 2^-45 of the row's largest (up to 2^25 columns;
  * 2^-39 for the longest rows), as integers, so that equal rows have equal sums.  Outputs and
  * workspace may not overlap the inputs or each other (OS_ERR_ALIAS).
  */

@@ -698,7 +698,8 @@ def paged_append(k_cache, v_cache, table, lengths, k, v, q=None, starts=None, in
     starts[b + 1] of them (int32 [seqs + 1]), its last; without ``starts`` each sequence has one.
     ``inv_freq`` (fp32 [rot / 2]) are the angles per position of the first rot dimensions, in
     pairs (f, f + rot / 2), or neighbours with ``interleaved``; without it nothing is rotated.
-    A sequence of length 0 takes no part, nor do rows outside ``starts``."""
+    A sequence of length 0 takes no part, nor do rows outside ``starts``: their rows of ``q_out``
+    are left as they were, which in one that is allocated here is anything."""
     import torch
     bf16 = torch.bfloat16
     cache, dev, seqs, kv_heads, head_dim = _paged_cache(k_cache, v_cache, table, lengths)
@@ -783,7 +784,9 @@ def paged_reorder(k_cache, v_cache, table, lengths, parents, out_table, out_leng
     the filled rows of the parent's last page are copied to the page that ``out_table`` names
     there, one of the sequence's own that no row of ``table`` uses.  The caches may have a leading
     dimension of layers.  Returns (out_table, out_lengths), the latter the parents' lengths.  A
-    parent outside the group leaves a sequence's row as it is, with length 0."""
+    parent outside the group (-1 where ``beam_select`` found no continuation) leaves a sequence's
+    row as it is, with length 0; it has to stay 0, not count up with the others, until a later choice
+    fills the place, for its row may name pages that others share."""
     import torch
     layers = k_cache.shape[0] if k_cache.dim() == 5 else None
     cache, dev, seqs, _, _ = _paged_cache(k_cache, v_cache, table, lengths,

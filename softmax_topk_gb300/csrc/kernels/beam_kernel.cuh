@@ -552,7 +552,7 @@ __device__ __forceinline__ bool better(u64 c, u64 at, u64 c2, u64 at2) {
 }
 
 // A row's weights as multiples of 2^-bits, so that a thread's sum of its share of the
-// columns stays below 2^62: 44 bits up to 2^26 columns, 38 for 2^31 - 1 without helpers.
+// columns stays below 2^62: 44 bits up to 2^25 columns, 38 for 2^31 - 1 without helpers.
 __device__ __forceinline__ sample::Weight row_weights(float m, int64_t cols, int helpers,
                                                       const float* pow2) {
     const int64_t share = cols / (int64_t(kMergeThreads) * helpers) + 1;
