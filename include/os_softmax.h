@@ -451,7 +451,9 @@ os_status os_paged_append(const os_paged_cache *cache, const void *k, int64_t k_
  * Arithmetic: products on the tensor cores from bf16 operands with fp32 sums;
  * weights in fp32, as the sum of two bf16 numbers (2^-17) in the second product;
  * O rounded once to bf16.  A sequence's keys may be split over the
- * GPU's SMs and are joined in their order: the same call gives the same bits.
+ * GPU's SMs and are joined in their order: the same call gives the same bits.  (The
+ * split follows all lengths and the table's width; among other sequences, or under a
+ * wider table, last bits may differ.)
  */
 os_status os_paged_attention(const os_paged_cache *cache, const void *q, int64_t q_stride,
                              void *out, float *lse, void *workspace, int32_t q_heads,

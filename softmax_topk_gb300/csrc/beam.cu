@@ -13,9 +13,15 @@ namespace {
 constexpr int kMaxRuns = 32;
 
 // Runs per row: as many as the GPU holds at once (three to an SM), for each run pays for a
-// selection of its own.  us with 1, 2, 3, 4 runs: 256 rows of 128256 bf16 29 / 32 / 31 / 34
-// (one row in eight ended: 30 / 27 / 31 / 31), of 32000 fp32 18 / 21 / 20 / 23, 160 rows of
-// 128256 bf16 25 / 21 / 23 / 24, 128 rows 23 / 19 / 19 / 23.
+// selection of its own.  us with 1, 2, 3 runs, where no beam has ended, one in eight, seven
+// in eight:
+//   128 rows of 128256 bf16   25.9 21.6 23.3   26.3 21.8 23.8   24.5 19.5 18.7   (3 are taken)
+//   160                       28.3 24.5 26.3   28.7 24.6 23.2   24.7 20.0 20.6   (2)
+//   256                       29.1 32.9 30.5   29.0 27.5 30.0   26.1 20.8 21.5   (1)
+//   512                       49.2 46.5 46.7   38.3 41.5 42.8   27.7 24.9 26.1   (1)
+//   256 rows of 32000 fp32    17.7 21.3 20.7   17.8 18.4 20.7   15.3 16.4 16.7   (1)
+// The host does not know which beams have ended.  The rule loses 2 to 3 us at 128 rows, and at
+// 512 where none has; 5 at 256 where most have.
 constexpr int kRunsPerSm = 3;
 
 struct Split {

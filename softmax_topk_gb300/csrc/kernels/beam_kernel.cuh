@@ -22,13 +22,15 @@
 // sampler's weights (38 bits, added as integers), by the CTAs of a cluster, and the
 // order is taken from those sums in 64 bits.
 //
-// What bounds it: 32 groups of 8 beams of 128256 bf16 columns, K = 16, take 29 us (the
-// one read at the rate of memory: 9.7).  The first kernel takes 18: 4 for starting and
-// the first tiles, 10 for the stream and its instructions (about 8 per column, of which
-// one on the SFU), 4 for the selection at its end, when every CTA's memory stands idle.
-// The second takes 8, the latency of its steps on one SM per group.  Where a group needs
-// exact sums (one call in six at these sizes) it takes 25 more: two rows of 43
-// instructions per column on eight SMs.  4 beams of 50257 fp32: 10 us.
+// What bounds it: 32 groups of 8 beams of 128256 bf16 columns, K = 16, take 29 us in a
+// graph, with one beam in eight ended too (the one read at the rate of memory: 9.7 and 8.5).
+// Alone and cold the first kernel takes 23, with memory at a third of its rate and schedulers
+// that issue in 42 % of their cycles: on SMs with one CTA or two, the start, the stream (about
+// 8 instructions per column, of which one on the SFU) and the selection at its end, when the
+// CTA's memory stands idle, follow one another.  The second takes 10, the latency of its
+// steps on one SM per group (issue 4 %).  Where a group needs exact sums (5 calls in 300 at
+// these sizes) it takes 18 more: two rows of 43 instructions per column on eight SMs.  4
+// beams of 50257 fp32: 11 us.
 #pragma once
 
 #include "../beam_error.h"
@@ -50,8 +52,8 @@ constexpr int kList = 1024;     // values that reach the bound; more go another 
 constexpr int kGroups = 512;    // threads' shares of a tile that do
 constexpr int kMergeThreads = kThreads;
 constexpr int kHelpers = 8;     // CTAs of a group, at most: four equal beams of 50257 columns
-                                // take 37 us with eight and 113 with one, beams that need no
-                                // exact sums 10.8 and 10.4
+                                // take 27 us with eight and 74 with one, beams that need no
+                                // exact sums 10.9 and 10.5
 constexpr int kCandidates = 1024;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxK = 64;

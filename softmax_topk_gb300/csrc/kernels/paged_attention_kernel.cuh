@@ -25,9 +25,9 @@
 // flight only half of the time, took 430 us where the ring takes 319.)
 //
 // What bounds it: memory, once there is enough to read.  64 sequences of 4096
-// keys, 16 heads of 128: 2.15 GB in 318 us, 6.8 TB/s, the measured copy's rate (four
+// keys, 16 heads of 128: 2.15 GB in 316 to 321 us, 6.7 TB/s, the measured copy's rate (four
 // schedulers issue in a quarter of their cycles).  128 sequences of up to 2000, 16
-// heads of 64: 95 us, 6.0 TB/s; one of 131072, 2 key heads: 29 us, 4.6 TB/s; one of
+// heads of 64: 96 us, 5.9 TB/s; one of 131072, 2 key heads: 29 us, 4.6 TB/s; one of
 // 1000: 6.6 us.  What is left is a constant of 6 to 10 us: three waits in a row for
 // memory (lengths, table, first keys, 2.5 us), the last block, its pieces and the
 // second kernel (4 us), and two launches.

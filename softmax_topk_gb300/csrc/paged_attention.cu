@@ -8,9 +8,14 @@ namespace os {
 
 namespace {
 
-// Blocks that a CTA should have at least: fewer CTAs leave fewer pieces to join.  us with
-// 2, 4, 8 blocks, 2 key heads: 300 keys 6.1 / 6.1 / 6.9, 1000 keys 6.7 / 6.4 / 6.9, 3000
-// keys 6.9 / 7.1 / 7.2.
+// Blocks of the table's room per CTA, at least: fewer CTAs leave fewer pieces to join.  us
+// with 2, 4, 8 blocks, 2 key heads and tables no wider than the sequence: 300 keys 6.1 / 6.1 /
+// 6.9, 1000 keys 6.7 / 6.4 / 6.9, 3000 keys 6.9 / 7.1 / 7.2.  The host knows the room alone.
+// Under a wide table there is a CTA per SM, whatever the lengths, down to a block each.  us
+// for a table of 131072 keys, in brackets for one that fits: 1 x 300, 2 x 8 heads 6.0 (6.1),
+// 1 x 1000 6.5 (6.5), 1 x 2000, 16 heads on one 8.7 (7.4), 4 x 200, 16 on one 6.7 (7.7),
+// 64 x 40, 2 x 4 heads 6.9 (7.0), 100 x 33, 8 heads of 64 on one 10.3 (7.1).  Four blocks at
+// least by the lengths, in both kernels, took 6.1, 6.5, 7.6, 7.6, 8.9 and 11.1 there.
 constexpr int kMinBlocks = 4;
 
 template <int D, int NT>
