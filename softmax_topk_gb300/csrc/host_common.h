@@ -129,7 +129,8 @@ class RunBefore {
 // Launch `kernel` behind the one before it on `stream`, which may let it be put in place
 // before it has ended (griddepcontrol.launch_dependents); it waits for that one's end
 // itself (griddepcontrol.wait) before it touches memory.  Until it has run once it waits as
-// any other kernel does; so it does for good in a graph that was captured before.
+// any other kernel does; so it does for good in a graph that was captured before (append and
+// attention of 1000 keys 10.0 us a layer there, 8.7 in one captured after a run).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_behind(void (*kernel)(KArgs...), dim3 grid, int threads, int smem,
                           cudaStream_t stream, Args... args) {
