@@ -8,7 +8,7 @@ namespace os {
 
 // A bound of the error of a row's ln d as beam_runs_kernel and beam_merge_kernel form it,
 // for rows of `cols` columns of which a thread sums `share` of one run.  In units u of
-// 2^-23 (half a rounding is u / 2; exp1 is within 0.75 of its value, ex2.approx within 2):
+// 2^-23 of the value (a rounding loses u / 2 at most, exp1 0.75, ex2.approx 2):
 //
 //   exponents and differences of maxima  A rounded difference loses u / 2 times its size.
 //       From a value by its thread's reference, the references behind it, the warp's, the
